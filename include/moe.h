@@ -63,6 +63,17 @@ typedef struct CUstream_st* moe_stream_t; /* the same handle type as cudaStream_
                                      activations, fp32 accumulation (TensorRT-LLM "DeepSeek R1 throughput on
                                      Blackwell", "Precision strategy": FP4 MoE weights). h and I must be
                                      multiples of 256 */
+#define MOE_DTYPE_MXFP4 3         /* MXFP4 expert weights (e2m1, a power-of-two e8m0 scale per 32): only with the
+                                     4-bit rows of moe_forward_fp4 and its steps; h and I multiples of 256 */
+
+/* element types of the 4-bit and balance-loss entry points */
+#define MOE_TYPE_F32 0
+#define MOE_TYPE_BF16 1
+#define MOE_TYPE_F16 2
+
+/* microscaled 4-bit formats */
+#define MOE_FP4_NV 0 /* NVFP4: e2m1 codes, an e4m3 scale for 16 elements, one fp32 scale g for the matrix */
+#define MOE_FP4_MX 1 /* MXFP4 (OCP microscaling): e2m1 codes, a power-of-two scale (e8m0 byte) for 32 elements */
 
 /* moe_route flags */
 #define MOE_LOGITS_GIVEN 1 /* `logits` is an input: skip the router GEMM */
@@ -97,7 +108,7 @@ typedef struct {
   int32_t score;        /* MOE_SCORE_SOFTMAX | MOE_SCORE_SIGMOID */
   int32_t renormalize;  /* 1: divide the selected weights by their sum */
   float routed_scale;   /* multiplies the routed weights (DeepSeek-V3: 2.5) */
-  int32_t dtype;        /* MOE_DTYPE_BF16 | MOE_DTYPE_FP8_BLOCK128 | MOE_DTYPE_NVFP4 */
+  int32_t dtype;        /* MOE_DTYPE_BF16 | MOE_DTYPE_FP8_BLOCK128 | MOE_DTYPE_NVFP4 | MOE_DTYPE_MXFP4 */
   float capacity_factor;/* 0: dropless. > 0: every expert keeps at most ceil(capacity_factor * T * k / E)
                            assignments, the earliest tokens first; the rest skip that expert (Ultralytics
                            "Load balancing and capacity": a capacity factor such as 1.25x the fair
@@ -323,6 +334,106 @@ typedef struct {
   int32_t reserved[3];
 } moe_balance_stats;
 int moe_balance(const moe_config* cfg, const void* ws, moe_balance_stats* stats, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Microscaled 4-bit rows and weights
+ * ------------------------------------------------------------------------------------------
+ * A 4-bit matrix [rows, cols] is two arrays, both row-major: codes [rows, cols/2] (element 2i in the low
+ * nibble of byte i) and scales [rows, cols/16] (MOE_FP4_NV) or [rows, cols/32] (MOE_FP4_MX) bytes; cols is
+ * a multiple of 32. Quantisation, with every rounding to nearest even and saturating:
+ *   MOE_FP4_NV  scale = e4m3(RN(amax / RN(6 g))), code = e2m1(RN(x / RN(scale * g))), 0 where that step is
+ *               0; value = code * scale * g. RN rounds to fp32; g > 0 and finite, 1 where its pointer is
+ *               NULL. The format of moe_quantize_weights_nvfp4, which chooses g from the weights; for
+ *               activations g is the caller's, usually (a calibrated) amax / 2688.
+ *   MOE_FP4_MX  scale = 2^(floor(log2 amax) - 2), at least 2^-127; code = e2m1(x / scale); value = code *
+ *               scale. g is not used and may be NULL.
+ * A block that holds an infinity or a NaN gets the NaN scale and zero codes: its values are NaN. */
+
+/* Rows to 4 bits. x [rows, cols] of x_type with ldx elements from row to row (rows 16-byte aligned); g [1]
+ * or NULL; q and s out. rows * cols / 8 < 2^32 - 256.
+ * Errors: MOE_ERR_INVALID, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA. */
+int moe_quantize_fp4(const void* x, int32_t x_type, int64_t rows, int64_t cols, int64_t ldx, int32_t format,
+                     const float* g, void* q, void* s, moe_stream_t stream);
+
+/* The values of 4-bit rows: y [rows, cols] of y_type, rounded once. Sizes and errors as moe_quantize_fp4. */
+int moe_dequantize_fp4(const void* q, const void* s, int64_t rows, int64_t cols, int32_t format, const float* g,
+                       int32_t y_type, void* y, moe_stream_t stream);
+
+/* y = A B^T of two 4-bit matrices on the block-scaled tensor cores, fp32 accumulation, rounded once.
+ *   aq, as   A [M, K];  bq, bs  B [N, K];  ga, gb  their matrix scales [1] or NULL (MOE_FP4_NV)
+ *   y        [M, N] out with ldy >= N elements from row to row, MOE_TYPE_BF16 or MOE_TYPE_F32
+ *   status   device int32 that MOE_STATUS_WAIT_TIMEOUT is added to if a wait gives up (y is then not
+ *            valid), or NULL
+ * M >= 0 and N >= 1 are any numbers below 2^31 - 256, K is a multiple of 32. Errors: MOE_ERR_INVALID, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA. */
+int moe_matmul_fp4(const void* aq, const void* as, const float* ga, const void* bq, const void* bs, const float* gb,
+                   int64_t M, int64_t N, int64_t K, int32_t format, int32_t y_type, void* y, int64_t ldy,
+                   int32_t* status, moe_stream_t stream);
+
+/* The layer with 4-bit rows as well as 4-bit weights: the tensor cores multiply the codes, nothing is
+ * expanded. cfg->dtype is MOE_DTYPE_NVFP4 (weights of moe_quantize_weights_nvfp4) or MOE_DTYPE_MXFP4 (weights
+ * of moe_quantize_fp4 on their rows: w_* codes, s_* e8m0 bytes [.., cols/32], g_* unused). Routing, combine,
+ * workspace and results otherwise as for moe_forward; the same workspace serves both.
+ *
+ * moe_fp4_activations: the NVFP4 scales of the rows that enter the gate/up product (g_x [1]) and of the
+ * SwiGLU product that enters the down product (g_h [1]), device pointers, NULL = 1. The struct may be NULL
+ * (both 1), and is not used with MOE_DTYPE_MXFP4. */
+typedef struct {
+  const float* g_x;
+  const float* g_h;
+} moe_fp4_activations;
+
+/* moe_dispatch with the rows quantised (each token once): xq [R_tot, h/2] codes, xs [R_tot, h/16] or
+ * [R_tot, h/32] scales. Other arguments and errors as moe_dispatch. */
+int moe_dispatch_fp4(const moe_config* cfg, const moe_fp4_activations* act, const void* x, const int32_t* topk_idx,
+                     const float* topk_w, int32_t* counts, int32_t* offsets, int32_t* inv_pos, int32_t* row_token,
+                     float* row_weight, void* xq, void* xs, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* moe_expert_ffn on 4-bit rows: H = silu(x W_gate^T) * (x W_up^T) in fp32, quantised with g_h straight from
+ * there; yd = (H W_down^T) * row_weight, bf16. H is kept in the workspace's hbuf. Other arguments and errors
+ * as moe_expert_ffn. */
+int moe_expert_ffn_fp4(const moe_config* cfg, const moe_weights* weights, const moe_fp4_activations* act, const void* xq,
+                       const void* xs, const int32_t* offsets, const float* row_weight, void* yd, void* ws,
+                       size_t ws_bytes, moe_stream_t stream);
+
+/* moe_forward with 4-bit rows: route, dispatch, experts, combine on `stream`. In the workspace the codes of
+ * the rows are at xd and their scales behind them, at xd + the codes' R_tot * h / 2 bytes rounded up to 256
+ * (hbuf likewise). Errors: as moe_forward. */
+int moe_forward_fp4(const moe_config* cfg, const void* x, const moe_weights* weights, const moe_fp4_activations* act,
+                    void* y, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * The router's load-balance loss
+ * ------------------------------------------------------------------------------------------
+ * For each sequence s, over its n unmasked tokens:
+ *   p[t, e]  the router's probabilities: softmax of logits[t] over the experts (MOE_SCORE_SOFTMAX), or
+ *            sigmoid(logits[t, e]) divided by its sum over the experts (MOE_SCORE_SIGMOID)
+ *   counts[s, e]     assignments of its tokens to expert e (topk_idx entries outside [0, E) are skipped)
+ *   mean_prob[s, e]  mean of p[t, e]
+ *   loss[s] = alpha * E / (k * n) * sum_e counts[s, e] * mean_prob[s, e]     (0 without tokens)
+ * An even load has loss alpha; counts are not differentiated. cfg gives T, E, k and score.
+ *   logits       [T, E] of logits_type (MOE_TYPE_F32 or MOE_TYPE_BF16); -inf masks an expert; a row of
+ *                nothing but -inf has p = 0
+ *   topk_idx     [T, k] int32 (from moe_route)
+ *   seq_offsets  [n_seq + 1] int32, ascending within [0, T]: sequence s is tokens [seq_offsets[s],
+ *                seq_offsets[s + 1]); tokens of no sequence are left out. NULL: one sequence of all tokens
+ *                (n_seq = 1)
+ *   token_mask   [T] bytes, 0 = padding, left out whatever its logits hold; NULL: no padding
+ *   loss [n_seq] fp32, counts [n_seq, E] int32, mean_prob [n_seq, E] fp32, tokens [n_seq] int32 (n) out
+ *   ws           moe_balance_loss_workspace_size() bytes; its contents do not matter
+ * Deterministic; at most two launches. Errors: MOE_ERR_INVALID, MOE_ERR_WORKSPACE, MOE_ERR_CUDA. */
+int moe_balance_loss_workspace_size(const moe_config* cfg, int32_t n_seq, size_t* bytes);
+int moe_balance_loss(const moe_config* cfg, const void* logits, int32_t logits_type, const int32_t* topk_idx,
+                     const int32_t* seq_offsets, int32_t n_seq, const uint8_t* token_mask, float alpha, float* loss,
+                     int32_t* counts, float* mean_prob, int32_t* tokens, void* ws, size_t ws_bytes,
+                     moe_stream_t stream);
+
+/* Its gradient: dlogits [T, E] of logits_type = sum_s dloss[s] * d loss[s] / d logits, from the counts and
+ * tokens that moe_balance_loss returned. dloss [n_seq] fp32. Rows of padding, and of tokens in no sequence, are
+ * 0. One launch. Errors: MOE_ERR_INVALID, MOE_ERR_CUDA. */
+int moe_balance_loss_backward(const moe_config* cfg, const void* logits, int32_t logits_type, const int32_t* counts,
+                              const int32_t* tokens, const int32_t* seq_offsets, int32_t n_seq,
+                              const uint8_t* token_mask, float alpha, const float* dloss, void* dlogits,
+                              moe_stream_t stream);
 
 /* Device status word of a workspace: waits for `stream`, then reads the MOE_STATUS_* bits that
  * kernels of earlier calls with this workspace set into *status, and clears them. moe_forward clears

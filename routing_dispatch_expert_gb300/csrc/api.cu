@@ -45,13 +45,16 @@ int check_config(const moe_config* c) {
   if ((int64_t)c->topk_group * (c->E / c->n_group) < c->k)
     return fail(MOE_ERR_INVALID, "the kept groups hold fewer than k experts");
   if (c->score != MOE_SCORE_SOFTMAX && c->score != MOE_SCORE_SIGMOID) return fail(MOE_ERR_INVALID, "unknown score");
-  if (c->dtype != MOE_DTYPE_BF16 && c->dtype != MOE_DTYPE_FP8_BLOCK128 && c->dtype != MOE_DTYPE_NVFP4)
+  if (c->dtype != MOE_DTYPE_BF16 && c->dtype != MOE_DTYPE_FP8_BLOCK128 && c->dtype != MOE_DTYPE_NVFP4 &&
+      c->dtype != MOE_DTYPE_MXFP4)
     return fail(MOE_ERR_INVALID, "unknown dtype");
   if (c->E > 1024) return fail(MOE_ERR_UNSUPPORTED, "E > 1024");
   if (c->h % 256 != 0) return fail(MOE_ERR_UNSUPPORTED, "h must be a multiple of 256");
   if (c->I % 128 != 0) return fail(MOE_ERR_UNSUPPORTED, "I must be a multiple of 128");
   if (c->dtype == MOE_DTYPE_NVFP4 && c->I % 256 != 0)
     return fail(MOE_ERR_UNSUPPORTED, "NVFP4 weights need I to be a multiple of 256");
+  if (c->dtype == MOE_DTYPE_MXFP4 && c->I % 256 != 0)
+    return fail(MOE_ERR_UNSUPPORTED, "MXFP4 weights need I to be a multiple of 256");
   if (c->I_shared != 0 && c->I_shared != c->I) return fail(MOE_ERR_UNSUPPORTED, "I_shared must be 0 or I");
   if ((int64_t)c->T * (c->k + 1) > INT32_MAX) return fail(MOE_ERR_UNSUPPORTED, "T * (k + 1) exceeds int32 rows");
   if (!(c->capacity_factor >= 0.f)) return fail(MOE_ERR_INVALID, "capacity_factor must be >= 0");
@@ -272,9 +275,19 @@ int capacity_of(const moe_config* c) {
   return cap >= (double)INT32_MAX ? 0 : (int)cap;
 }
 
+// The 4-bit rows of a layer: format, activation scales, and where the codes and scales of the rows are.
+struct Fp4Rows {
+  int format;
+  const float* g_x;
+  const float* g_h;
+  const void* xq;
+  const void* xs;
+};
+
 int do_dispatch(const moe_config* c, const void* x, const int32_t* topk_idx, const float* topk_w, int32_t* counts,
                 int32_t* offsets, int32_t* inv_pos, int32_t* row_token, float* row_weight, void* xd, float* xd_scales,
-                void* ws, const Layout& L, cudaStream_t stream, bool shared_rows = true) {
+                void* ws, const Layout& L, cudaStream_t stream, bool shared_rows = true,
+                const Fp4Rows* fp4 = nullptr) {
   moe::DispatchDesc d;
   d.x = x;
   d.topk_idx = topk_idx;
@@ -295,6 +308,12 @@ int do_dispatch(const moe_config* c, const void* x, const int32_t* topk_idx, con
   d.shared = c->I_shared > 0 && shared_rows;  // false: the shared expert reads x itself
   d.fp8 = c->dtype == MOE_DTYPE_FP8_BLOCK128;
   d.capacity = capacity_of(c);
+  if (fp4) {
+    d.xd = const_cast<void*>(fp4->xq);
+    d.fp4_scales = static_cast<uint8_t*>(const_cast<void*>(fp4->xs));
+    d.fp4_format = fp4->format;
+    d.fp4_g = fp4->g_x;
+  }
   set_placement(d, c, expert_counts_ptr(ws, L.l, c));
   cudaError_t e = moe::launch_dispatch(d, stream);
   if (e != cudaSuccess) return cuda_fail(e, "dispatch launch");
@@ -565,6 +584,83 @@ int do_shared_ffn_bf16(const moe_config* c, const moe_weights* w, const void* x,
   return MOE_OK;
 }
 
+// 4-bit rows and weights: the grouped GEMMs of gemm_a4.cu, H in the workspace as codes and scales.
+int do_expert_ffn_fp4(const moe_config* c, const moe_weights* w, const Fp4Rows& f, const int32_t* offsets,
+                      const float* row_weight, void* yd, void* ws, const Layout& L, cudaStream_t stream) {
+  if (c->T == 0) return MOE_OK;
+  const bool shared = c->I_shared > 0, nv = f.format == MOE_FP4_NV;
+  std::string err;
+  void* hq = at<void>(ws, L.l.hbuf);
+  void* hs = at<void>(ws, L.l.hbuf + align256((size_t)L.R_tot * c->I / 2));
+  moe::GemmA4Desc g;
+  g.format = f.format;
+  g.A = f.xq;
+  g.As = f.xs;
+  g.Ag = f.g_x;
+  g.a_rows = L.R_tot;
+  g.B = w->w_gu;
+  g.Bs = w->s_gu;
+  g.Bg = nv ? w->g_gu : nullptr;
+  g.B_shared = shared ? w->w_gu_shared : nullptr;
+  g.Bs_shared = shared ? w->s_gu_shared : nullptr;
+  g.Bg_shared = shared && nv ? w->g_gu_shared : nullptr;
+  g.b_rows = 2 * (int64_t)c->I;
+  g.offsets = offsets;
+  g.slot_expert = c->placement ? c->placement->slot_expert : nullptr;
+  g.n_experts = c->E;
+  g.E = (int)n_groups(c);
+  g.R = (int)L.R;
+  g.T = c->T;
+  g.K = c->h;
+  g.N = c->I;
+  g.I = c->I;
+  g.mode = 0;
+  g.out = hq;
+  g.out_scales = hs;
+  g.out_g = f.g_h;
+  g.ldo = c->I;
+  g.status = status_ptr(ws, L.l);
+  cudaError_t e = moe::launch_gemm_a4(g, stream, &err);
+  if (e != cudaSuccess) return err.empty() ? cuda_fail(e, "4-bit gate/up GEMM launch") : cuda_fail(e, err.c_str());
+  g.A = hq;
+  g.As = hs;
+  g.Ag = f.g_h;
+  g.B = w->w_d;
+  g.Bs = w->s_d;
+  g.Bg = nv ? w->g_d : nullptr;
+  g.B_shared = shared ? w->w_d_shared : nullptr;
+  g.Bs_shared = shared ? w->s_d_shared : nullptr;
+  g.Bg_shared = shared && nv ? w->g_d_shared : nullptr;
+  g.b_rows = c->h;
+  g.K = c->I;
+  g.N = c->h;
+  g.mode = 1;
+  g.out = yd;
+  g.out_scales = nullptr;
+  g.out_g = nullptr;
+  g.ldo = c->h;
+  g.row_weight = row_weight;
+  e = moe::launch_gemm_a4(g, stream, &err);
+  if (e != cudaSuccess) return err.empty() ? cuda_fail(e, "4-bit down GEMM launch") : cuda_fail(e, err.c_str());
+  counted(2);
+  return MOE_OK;
+}
+
+int check_fp4_layer(const moe_config* c, const moe_fp4_activations* act, Fp4Rows* f) {
+  if (c->dtype != MOE_DTYPE_NVFP4 && c->dtype != MOE_DTYPE_MXFP4)
+    return fail(MOE_ERR_UNSUPPORTED, "4-bit rows need MOE_DTYPE_NVFP4 or MOE_DTYPE_MXFP4 weights");
+  f->format = c->dtype == MOE_DTYPE_NVFP4 ? MOE_FP4_NV : MOE_FP4_MX;
+  f->g_x = act && f->format == MOE_FP4_NV ? act->g_x : nullptr;
+  f->g_h = act && f->format == MOE_FP4_NV ? act->g_h : nullptr;
+  return MOE_OK;
+}
+
+// MXFP4 weights have no path that expands them
+int refuse_mxfp4(const moe_config* c) {
+  if (c->dtype != MOE_DTYPE_MXFP4) return MOE_OK;
+  return fail(MOE_ERR_UNSUPPORTED, "MXFP4 weights take 4-bit rows: use the _fp4 entry points");
+}
+
 int check_expert_weights(const moe_config* c, const moe_weights* w) {
   if (!w) return fail(MOE_ERR_INVALID, "weights is NULL");
   REQUIRE_PTR(w->w_gu, "weights->w_gu");
@@ -573,7 +669,7 @@ int check_expert_weights(const moe_config* c, const moe_weights* w) {
     REQUIRE_PTR(w->w_gu_shared, "weights->w_gu_shared");
     REQUIRE_PTR(w->w_d_shared, "weights->w_d_shared");
   }
-  if (c->dtype == MOE_DTYPE_FP8_BLOCK128 || c->dtype == MOE_DTYPE_NVFP4) {
+  if (c->dtype != MOE_DTYPE_BF16) {
     REQUIRE_PTR(w->s_gu, "weights->s_gu");
     REQUIRE_PTR(w->s_d, "weights->s_d");
     if (c->I_shared > 0) {
@@ -666,6 +762,7 @@ MOE_EXPORT int moe_expert_ffn(const moe_config* cfg, const moe_weights* weights,
   Layout L = make_layout(cfg);
   if ((rc = check_ws(ws, ws_bytes, L))) return rc;
   if ((rc = check_expert_weights(cfg, weights))) return rc;
+  if ((rc = refuse_mxfp4(cfg))) return rc;
   REQUIRE_PTR(xd, "xd");
   REQUIRE_PTR(offsets, "offsets");
   REQUIRE_PTR(row_weight, "row_weight");
@@ -725,6 +822,7 @@ MOE_EXPORT int moe_forward(const moe_config* cfg, const void* x, const moe_weigh
   if (!weights) return fail(MOE_ERR_INVALID, "weights is NULL");
   REQUIRE_PTR(weights->w_router, "weights->w_router");
   if ((rc = check_expert_weights(cfg, weights))) return rc;
+  if ((rc = refuse_mxfp4(cfg))) return rc;
   cudaStream_t s = (cudaStream_t)stream;
   // the status word, the grouped GEMMs' tile counters and the fused kernel's barrier counter
   cudaError_t e = cudaMemsetAsync(status_ptr(ws, L.l), 0, kHeaderInts * sizeof(int), s);
@@ -779,6 +877,297 @@ MOE_EXPORT int moe_forward(const moe_config* cfg, const void* x, const moe_weigh
                           cfg->I_shared > 0, s);
   if (e != cudaSuccess) return cuda_fail(e, "combine launch");
   if (cfg->T > 0) counted(1);
+  return MOE_OK;
+}
+
+// ------------------------------------------------------------------------------------------
+// 4-bit rows
+// ------------------------------------------------------------------------------------------
+MOE_EXPORT int moe_dispatch_fp4(const moe_config* cfg, const moe_fp4_activations* act, const void* x,
+                                const int32_t* topk_idx, const float* topk_w, int32_t* counts, int32_t* offsets,
+                                int32_t* inv_pos, int32_t* row_token, float* row_weight, void* xq, void* xs, void* ws,
+                                size_t ws_bytes, moe_stream_t stream) {
+  int rc = check_config(cfg);
+  if (rc) return rc;
+  Fp4Rows f;
+  if ((rc = check_fp4_layer(cfg, act, &f))) return rc;
+  Layout L = make_layout(cfg);
+  if ((rc = check_ws(ws, ws_bytes, L))) return rc;
+  REQUIRE_PTR(x, "x");
+  REQUIRE_PTR(topk_idx, "topk_idx");
+  REQUIRE_PTR(topk_w, "topk_w");
+  REQUIRE_PTR(counts, "counts");
+  REQUIRE_PTR(offsets, "offsets");
+  REQUIRE_PTR(inv_pos, "inv_pos");
+  REQUIRE_PTR(row_token, "row_token");
+  REQUIRE_PTR(row_weight, "row_weight");
+  REQUIRE_PTR(xq, "xq");
+  REQUIRE_PTR(xs, "xs");
+  f.xq = xq;
+  f.xs = xs;
+  return do_dispatch(cfg, x, topk_idx, topk_w, counts, offsets, inv_pos, row_token, row_weight, nullptr, nullptr, ws, L,
+                     (cudaStream_t)stream, true, &f);
+}
+
+MOE_EXPORT int moe_expert_ffn_fp4(const moe_config* cfg, const moe_weights* weights, const moe_fp4_activations* act,
+                                  const void* xq, const void* xs, const int32_t* offsets, const float* row_weight,
+                                  void* yd, void* ws, size_t ws_bytes, moe_stream_t stream) {
+  int rc = check_config(cfg);
+  if (rc) return rc;
+  Fp4Rows f;
+  if ((rc = check_fp4_layer(cfg, act, &f))) return rc;
+  Layout L = make_layout(cfg);
+  if ((rc = check_ws(ws, ws_bytes, L))) return rc;
+  if ((rc = check_expert_weights(cfg, weights))) return rc;
+  REQUIRE_PTR(xq, "xq");
+  REQUIRE_PTR(xs, "xs");
+  REQUIRE_PTR(offsets, "offsets");
+  REQUIRE_PTR(row_weight, "row_weight");
+  REQUIRE_PTR(yd, "yd");
+  f.xq = xq;
+  f.xs = xs;
+  return do_expert_ffn_fp4(cfg, weights, f, offsets, row_weight, yd, ws, L, (cudaStream_t)stream);
+}
+
+MOE_EXPORT int moe_forward_fp4(const moe_config* cfg, const void* x, const moe_weights* weights,
+                               const moe_fp4_activations* act, void* y, void* ws, size_t ws_bytes,
+                               moe_stream_t stream) {
+  int rc = check_config(cfg);
+  if (rc) return rc;
+  Fp4Rows f;
+  if ((rc = check_fp4_layer(cfg, act, &f))) return rc;
+  Layout L = make_layout(cfg);
+  if ((rc = check_ws(ws, ws_bytes, L))) return rc;
+  REQUIRE_PTR(x, "x");
+  REQUIRE_PTR(y, "y");
+  if (!weights) return fail(MOE_ERR_INVALID, "weights is NULL");
+  REQUIRE_PTR(weights->w_router, "weights->w_router");
+  if ((rc = check_expert_weights(cfg, weights))) return rc;
+  cudaStream_t s = (cudaStream_t)stream;
+  const moe_ws_layout& l = L.l;
+  cudaError_t e = cudaMemsetAsync(status_ptr(ws, l), 0, kHeaderInts * sizeof(int), s);
+  if (e != cudaSuccess) return cuda_fail(e, "status reset");
+  f.xq = at<void>(ws, l.xd);
+  f.xs = at<void>(ws, l.xd + align256((size_t)L.R_tot * cfg->h / 2));
+  if ((rc = do_route(cfg, x, weights, at<float>(ws, l.logits), 0, at<int32_t>(ws, l.topk_idx), at<float>(ws, l.topk_w),
+                     ws, L, s)))
+    return rc;
+  if ((rc = do_dispatch(cfg, x, at<int32_t>(ws, l.topk_idx), at<float>(ws, l.topk_w), at<int32_t>(ws, l.counts),
+                        at<int32_t>(ws, l.offsets), at<int32_t>(ws, l.inv_pos), at<int32_t>(ws, l.row_token),
+                        at<float>(ws, l.row_weight), nullptr, nullptr, ws, L, s, true, &f)))
+    return rc;
+  if ((rc = do_expert_ffn_fp4(cfg, weights, f, at<int32_t>(ws, l.offsets), at<float>(ws, l.row_weight),
+                              at<void>(ws, l.yd), ws, L, s)))
+    return rc;
+  e = moe::launch_combine(at<void>(ws, l.yd), at<int32_t>(ws, l.inv_pos), y, cfg->T, cfg->h, cfg->k, cfg->I_shared > 0, s);
+  if (e != cudaSuccess) return cuda_fail(e, "combine launch");
+  if (cfg->T > 0) counted(1);
+  return MOE_OK;
+}
+
+namespace {
+
+int check_fp4_rows(int64_t rows, int64_t cols, int32_t format) {
+  if (rows < 0 || cols < 0) return fail(MOE_ERR_INVALID, "negative size");
+  if (format != MOE_FP4_NV && format != MOE_FP4_MX) return fail(MOE_ERR_INVALID, "unknown 4-bit format");
+  if (cols % 32) return fail(MOE_ERR_UNSUPPORTED, "cols must be a multiple of 32");
+  if (cols / 8 > 0 && rows > ((int64_t)UINT32_MAX - 256) / (cols / 8))
+    return fail(MOE_ERR_UNSUPPORTED, "rows * cols / 8 exceeds 2^32 - 256");
+  return MOE_OK;
+}
+
+}  // namespace
+
+MOE_EXPORT int moe_quantize_fp4(const void* x, int32_t x_type, int64_t rows, int64_t cols, int64_t ldx, int32_t format,
+                                const float* g, void* q, void* s, moe_stream_t stream) {
+  int rc = check_fp4_rows(rows, cols, format);
+  if (rc) return rc;
+  if (x_type != MOE_TYPE_F32 && x_type != MOE_TYPE_BF16 && x_type != MOE_TYPE_F16)
+    return fail(MOE_ERR_INVALID, "unknown element type");
+  if (rows == 0 || cols == 0) return MOE_OK;
+  if (rows > 1 && ldx < cols) return fail(MOE_ERR_INVALID, "ldx must be at least cols");
+  if (rows > 1 && ldx % (x_type == MOE_TYPE_F32 ? 4 : 8)) return fail(MOE_ERR_INVALID, "rows must be 16-byte aligned");
+  REQUIRE_PTR(x, "x");
+  REQUIRE_PTR(q, "q");
+  REQUIRE_PTR(s, "s");
+  cudaError_t e = moe::launch_quantize_fp4(x, x_type, rows, cols, ldx, format, g, q, s, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "4-bit quantisation launch");
+  counted(1);
+  return MOE_OK;
+}
+
+MOE_EXPORT int moe_dequantize_fp4(const void* q, const void* s, int64_t rows, int64_t cols, int32_t format,
+                                  const float* g, int32_t y_type, void* y, moe_stream_t stream) {
+  int rc = check_fp4_rows(rows, cols, format);
+  if (rc) return rc;
+  if (y_type != MOE_TYPE_F32 && y_type != MOE_TYPE_BF16 && y_type != MOE_TYPE_F16)
+    return fail(MOE_ERR_INVALID, "unknown element type");
+  if (rows == 0 || cols == 0) return MOE_OK;
+  REQUIRE_PTR(q, "q");
+  REQUIRE_PTR(s, "s");
+  REQUIRE_PTR(y, "y");
+  cudaError_t e = moe::launch_dequantize_fp4(q, s, g, rows, cols, format, y_type, y, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "4-bit expansion launch");
+  counted(1);
+  return MOE_OK;
+}
+
+MOE_EXPORT int moe_matmul_fp4(const void* aq, const void* as, const float* ga, const void* bq, const void* bs,
+                              const float* gb, int64_t M, int64_t N, int64_t K, int32_t format, int32_t y_type, void* y,
+                              int64_t ldy, int32_t* status, moe_stream_t stream) {
+  if (M < 0 || N < 1 || K < 1) return fail(MOE_ERR_INVALID, "M must be >= 0, N and K positive");
+  if (format != MOE_FP4_NV && format != MOE_FP4_MX) return fail(MOE_ERR_INVALID, "unknown 4-bit format");
+  if (y_type != MOE_TYPE_F32 && y_type != MOE_TYPE_BF16) return fail(MOE_ERR_INVALID, "y must be bf16 or fp32");
+  if (K % 32) return fail(MOE_ERR_UNSUPPORTED, "K must be a multiple of 32");
+  // row, column and tile numbers are 32-bit
+  if (M > INT32_MAX - 256 || N > INT32_MAX - 256 || K > INT32_MAX - 256 ||
+      moe::cdiv(M, 128) * moe::cdiv(N, 256) > INT32_MAX - 1024)
+    return fail(MOE_ERR_UNSUPPORTED, "M, N or K too large");
+  if (ldy < N) return fail(MOE_ERR_INVALID, "ldy must be at least N");
+  if (M == 0) return MOE_OK;
+  REQUIRE_PTR(aq, "aq");
+  REQUIRE_PTR(as, "as");
+  REQUIRE_PTR(bq, "bq");
+  REQUIRE_PTR(bs, "bs");
+  REQUIRE_PTR(y, "y");
+  const bool nv = format == MOE_FP4_NV;
+  moe::GemmA4Desc g;
+  g.format = format;
+  g.A = aq;
+  g.As = as;
+  g.Ag = nv ? ga : nullptr;
+  g.a_rows = M;
+  g.B = bq;
+  g.Bs = bs;
+  g.Bg = nv ? gb : nullptr;
+  g.b_rows = N;
+  g.offsets = nullptr;
+  g.E = 1;
+  g.R = 0;
+  g.T = (int)M;
+  g.K = (int)K;
+  g.N = (int)N;
+  g.I = 0;
+  g.mode = 2;
+  g.f32 = y_type == MOE_TYPE_F32;
+  g.out = y;
+  g.ldo = ldy;
+  g.status = status;
+  std::string err;
+  cudaError_t e = moe::launch_gemm_a4(g, (cudaStream_t)stream, &err);
+  if (e != cudaSuccess) return err.empty() ? cuda_fail(e, "4-bit GEMM launch") : cuda_fail(e, err.c_str());
+  counted(1);
+  return MOE_OK;
+}
+
+// ------------------------------------------------------------------------------------------
+// The router's balance loss
+// ------------------------------------------------------------------------------------------
+namespace {
+
+int check_balance_loss(const moe_config* cfg, int32_t logits_type, const int32_t* seq_offsets, int32_t n_seq) {
+  int rc = check_config(cfg);
+  if (rc) return rc;
+  if (logits_type != MOE_TYPE_F32 && logits_type != MOE_TYPE_BF16)
+    return fail(MOE_ERR_INVALID, "logits must be fp32 or bf16");
+  if (n_seq < 1) return fail(MOE_ERR_INVALID, "n_seq must be positive");
+  // blocks of a launch and entries of the workspace are 32-bit
+  if (n_seq > (1 << 24)) return fail(MOE_ERR_UNSUPPORTED, "n_seq > 2^24");
+  if (!seq_offsets && n_seq != 1) return fail(MOE_ERR_INVALID, "n_seq must be 1 without seq_offsets");
+  return MOE_OK;
+}
+
+size_t balance_loss_bytes(const moe_config* cfg, int32_t n_seq) {
+  return align256(sizeof(int32_t) * (size_t)moe::balance_loss_entries(cfg->T, cfg->E, n_seq) * (2 * (size_t)cfg->E + 1));
+}
+
+}  // namespace
+
+MOE_EXPORT int moe_balance_loss_workspace_size(const moe_config* cfg, int32_t n_seq, size_t* bytes) {
+  int rc = check_balance_loss(cfg, MOE_TYPE_F32, reinterpret_cast<const int32_t*>(16), n_seq);
+  if (rc) return rc;
+  if (!bytes) return fail(MOE_ERR_INVALID, "bytes is NULL");
+  *bytes = balance_loss_bytes(cfg, n_seq);
+  return MOE_OK;
+}
+
+MOE_EXPORT int moe_balance_loss(const moe_config* cfg, const void* logits, int32_t logits_type, const int32_t* topk_idx,
+                                const int32_t* seq_offsets, int32_t n_seq, const uint8_t* token_mask, float alpha,
+                                float* loss, int32_t* counts, float* mean_prob, int32_t* tokens, void* ws,
+                                size_t ws_bytes, moe_stream_t stream) {
+  int rc = check_balance_loss(cfg, logits_type, seq_offsets, n_seq);
+  if (rc) return rc;
+  REQUIRE_PTR(loss, "loss");
+  REQUIRE_PTR(counts, "counts");
+  REQUIRE_PTR(mean_prob, "mean_prob");
+  REQUIRE_PTR(tokens, "tokens");
+  cudaStream_t s = (cudaStream_t)stream;
+  if (cfg->T == 0) {
+    const size_t se = (size_t)n_seq * cfg->E;
+    cudaError_t e = cudaMemsetAsync(loss, 0, sizeof(float) * n_seq, s);
+    if (e == cudaSuccess) e = cudaMemsetAsync(tokens, 0, sizeof(int32_t) * n_seq, s);
+    if (e == cudaSuccess) e = cudaMemsetAsync(counts, 0, sizeof(int32_t) * se, s);
+    if (e == cudaSuccess) e = cudaMemsetAsync(mean_prob, 0, sizeof(float) * se, s);
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e, "clearing the results of no tokens");
+  }
+  REQUIRE_PTR(logits, "logits");
+  REQUIRE_PTR(topk_idx, "topk_idx");
+  REQUIRE_PTR(ws, "ws");
+  if (ws_bytes < balance_loss_bytes(cfg, n_seq)) return fail(MOE_ERR_WORKSPACE, "balance-loss workspace too small");
+  moe::BalanceLossDesc d;
+  d.logits = logits;
+  d.topk_idx = topk_idx;
+  d.offsets = seq_offsets;
+  d.mask = token_mask;
+  d.T = cfg->T;
+  d.E = cfg->E;
+  d.k = cfg->k;
+  d.S = n_seq;
+  d.sigmoid = cfg->score == MOE_SCORE_SIGMOID;
+  d.bf16 = logits_type == MOE_TYPE_BF16;
+  d.alpha = alpha;
+  d.scratch = ws;
+  d.loss = loss;
+  d.counts = counts;
+  d.mean = mean_prob;
+  d.tokens = tokens;
+  int launches = 0;
+  cudaError_t e = moe::launch_balance_loss(d, &launches, s);
+  if (e != cudaSuccess) return cuda_fail(e, "balance-loss launch");
+  counted(launches);
+  return MOE_OK;
+}
+
+MOE_EXPORT int moe_balance_loss_backward(const moe_config* cfg, const void* logits, int32_t logits_type,
+                                         const int32_t* counts, const int32_t* tokens, const int32_t* seq_offsets,
+                                         int32_t n_seq, const uint8_t* token_mask, float alpha, const float* dloss,
+                                         void* dlogits, moe_stream_t stream) {
+  int rc = check_balance_loss(cfg, logits_type, seq_offsets, n_seq);
+  if (rc) return rc;
+  if (cfg->T == 0) return MOE_OK;
+  REQUIRE_PTR(logits, "logits");
+  REQUIRE_PTR(counts, "counts");
+  REQUIRE_PTR(tokens, "tokens");
+  REQUIRE_PTR(dloss, "dloss");
+  REQUIRE_PTR(dlogits, "dlogits");
+  moe::BalanceLossBackwardDesc d;
+  d.logits = logits;
+  d.offsets = seq_offsets;
+  d.mask = token_mask;
+  d.counts = counts;
+  d.tokens = tokens;
+  d.dloss = dloss;
+  d.dlogits = dlogits;
+  d.T = cfg->T;
+  d.E = cfg->E;
+  d.k = cfg->k;
+  d.S = n_seq;
+  d.sigmoid = cfg->score == MOE_SCORE_SIGMOID;
+  d.bf16 = logits_type == MOE_TYPE_BF16;
+  d.alpha = alpha;
+  cudaError_t e = moe::launch_balance_loss_backward(d, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "balance-loss gradient launch");
+  counted(1);
   return MOE_OK;
 }
 

@@ -15,7 +15,8 @@
 //                  row_weight
 //   4. gather      one warp per item (a 1024-element piece of one token's row): the piece is read
 //                  once and written to the token's k rows (and to the shared expert's row), as bf16
-//                  or as e4m3 with 1x128 scales (dispatch_impl.cuh).
+//                  or as e4m3 with 1x128 scales, or as 4-bit codes with block scales
+//                  (dispatch_impl.cuh).
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -183,6 +184,19 @@ __global__ void __launch_bounds__(256) gather_fp8_kernel(const uint4* __restrict
     gather_fp8_item(x, inv_pos, xd, xs, h, k, R, shared, it, lane);
 }
 
+template <int FMT>
+__global__ void __launch_bounds__(256) gather_fp4_kernel(const uint4* __restrict__ x, const int32_t* __restrict__ inv_pos,
+                                                         uint32_t* __restrict__ xq, uint8_t* __restrict__ xs,
+                                                         const float* __restrict__ g, int T, int h, int k, int R,
+                                                         int shared) {
+  const int lane = threadIdx.x & 31;
+  const float gs = g ? *g : 1.0f;
+  const int64_t warps = (gridDim.x * blockDim.x) >> 5;
+  const int64_t items = (int64_t)T * fp8_items_per_row(h);
+  for (int64_t it = (blockIdx.x * blockDim.x + threadIdx.x) >> 5; it < items; it += warps)
+    gather_fp4_item<FMT>(x, inv_pos, xq, xs, gs, h, k, R, shared, it, lane);
+}
+
 // Load balance of one step from its counts (S <= 1024 experts or slots): the busiest expert's rows,
 // the experts with rows, the kept rows (offsets[S]) and the dropped assignments, and busiest / mean.
 __global__ void __launch_bounds__(1024) balance_kernel(const int32_t* __restrict__ counts,
@@ -254,11 +268,17 @@ cudaError_t launch_dispatch(const DispatchDesc& d, cudaStream_t stream) {
   dp::rank_kernel<<<nblk, dp::TPB, rank_smem, stream>>>(d.topk_idx, d.topk_w, d.scratch, d.offsets, d.T, d.k, d.E,
                                                          cap, d.inv_pos, d.row_token, d.row_weight, d.n_slots,
                                                          d.max_replicas, d.replicas, d.replica_slot);
-  const int64_t items = (int64_t)d.T * (d.fp8 ? dp::fp8_items_per_row(d.h) : dp::bf16_items_per_row(d.h));
+  const bool quantised = d.fp8 || d.fp4_scales;
+  const int64_t items = (int64_t)d.T * (quantised ? dp::fp8_items_per_row(d.h) : dp::bf16_items_per_row(d.h));
   int64_t blocks = cdiv(items, 8);
   if (blocks > (int64_t)num_sms() * 16) blocks = (int64_t)num_sms() * 16;
   const int R = d.T * d.k;
-  if (d.fp8)
+  if (d.fp4_scales) {
+    auto kernel = d.fp4_format == fp4::kNv ? dp::gather_fp4_kernel<fp4::kNv> : dp::gather_fp4_kernel<fp4::kMx>;
+    kernel<<<(unsigned)blocks, 256, 0, stream>>>(reinterpret_cast<const uint4*>(d.x), d.inv_pos,
+                                                 reinterpret_cast<uint32_t*>(d.xd), d.fp4_scales, d.fp4_g, d.T, d.h, d.k,
+                                                 R, d.shared);
+  } else if (d.fp8)
     dp::gather_fp8_kernel<<<(unsigned)blocks, 256, 0, stream>>>(reinterpret_cast<const uint4*>(d.x), d.inv_pos,
                                                                 reinterpret_cast<uint8_t*>(d.xd), d.xd_scales, d.T,
                                                                 d.h, d.k, R, d.shared);

@@ -12,6 +12,7 @@
 #include <cuda_fp8.h>
 
 #include "common.cuh"
+#include "fp4_impl.cuh"
 
 namespace moe {
 namespace dp {
@@ -104,6 +105,48 @@ __device__ __forceinline__ void gather_fp8_item(const uint4* __restrict__ x, con
       }
       *reinterpret_cast<uint2*>(xd + (int64_t)r * h + c * 8) = qv;
       if (scale_writer) xs[(int64_t)r * hb + blk] = scale;
+    }
+  }
+}
+
+// 4-bit item: 1024 elements of token t's row in passes of 256, a lane 8 consecutive elements; every block of
+// 16 (NVFP4) or 32 (MXFP4) is quantised once (fp4_impl.cuh), then its codes and its scale byte are written
+// to the token's k rows (and the shared expert's row).
+template <int FMT>
+__device__ __forceinline__ void gather_fp4_item(const uint4* __restrict__ x, const int32_t* __restrict__ inv_pos,
+                                                uint32_t* __restrict__ xq, uint8_t* __restrict__ xs, float g, int h,
+                                                int k, int R, int shared, int64_t it, int lane) {
+  const int per = fp8_items_per_row(h);
+  const int64_t t = it / per;
+  const int hv = h / 8;
+  constexpr int kLanes = fp4::kBlock<FMT> / 8;
+  const int c0 = (int)(it - t * per) * (kFp8ItemElems / 8);
+  const int my_row = lane < k ? inv_pos[t * k + lane] : -1;
+  const uint4* src = x + t * hv;
+  uint4 v[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    if (c0 + 32 * u < hv) v[u] = src[c0 + lane + 32 * u];  // h % 256 == 0: a pass is whole
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int c = c0 + lane + 32 * u;
+    if (c0 + 32 * u >= hv) break;
+    const float f[8] = {bf16_lo(v[u].x), bf16_hi(v[u].x), bf16_lo(v[u].y), bf16_hi(v[u].y),
+                        bf16_lo(v[u].z), bf16_hi(v[u].z), bf16_lo(v[u].w), bf16_hi(v[u].w)};
+    float by;
+    const uint32_t scale = fp4::block_scale<FMT>(fp4::block_amax<FMT>(fp4::amax8<FMT>(f)), g, by);
+    const uint32_t q = fp4::codes8<FMT>(f, by);
+    for (int j = 0; j <= k; ++j) {
+      int r;
+      if (j < k) {
+        r = __shfl_sync(0xffffffffu, my_row, j);
+        if (r < 0) continue;
+      } else {
+        if (!shared) break;
+        r = R + (int)t;
+      }
+      xq[(int64_t)r * hv + c] = q;
+      if (lane % kLanes == 0) xs[(int64_t)r * (hv / kLanes) + c / kLanes] = (uint8_t)scale;
     }
   }
 }

@@ -1,0 +1,538 @@
+// Products of 4-bit rows and 4-bit weights on the block-scaled tensor cores (tcgen05 kind::mxf4nvf4 and
+// kind::mxf4, TMEM, TMA): the expert FFN's grouped GEMMs and the product of two matrices.
+//
+//   mode 0  H = quantise(silu(A W_gate^T) * (A W_up^T)), codes and block scales, from the fp32 product
+//   mode 1  yd (bf16) = (A W_down^T) * row_weight
+//   mode 2  y (bf16 or fp32) = A B^T, one group
+//
+// A and B are e2m1 codes, two a byte, row-major along K, with a scale byte for 16 (NVFP4, e4m3) or 32
+// (MXFP4, e8m0) elements; the tensor core multiplies codes and scales itself and accumulates in fp32, so
+// nothing is expanded: a K block of 256 elements is one 128-byte swizzled row of shared memory.
+//
+//   * tiles of 128 rows x 256 columns (mode 0: 128 gate and the 128 matching up columns), persistent,
+//     one CTA per SM, a 4-stage ring of 54 KB: codes by TMA, scales by four warps (one a stage).
+//   * scales: `tcgen05.mma` reads them from TMEM, where row r of a 128-row operand has its 4 scale bytes
+//     of a step in lane r % 32 of column r / 32, repeated in the four lane quarters; `tcgen05.cp
+//     .32x128b.warpx4` copies 512 bytes of shared memory [32 lanes][4 columns][4 bytes] there. The scales
+//     stay row-major in HBM (the layout of the quantised weights, a plain copy of a checkpoint): a lane
+//     loads 16 (8) bytes of 4 rows and stores them transposed as one 16-byte line per step.
+//   * TMEM: two accumulators of 256 columns do not leave room for the scales, so they share 48: columns
+//     [0, 256) and [208, 464), scales in [464, 512). The epilogue reads the shared columns of a tile
+//     first and hands them over; the next tile's MMAs then run beside the rest of the epilogue.
+//   * eight epilogue warps, two per TMEM lane quarter, 32 columns at a time; in mode 0 a lane holds whole
+//     quantisation blocks of its row, so H is quantised in registers.
+//   * a tile of at most 96 rows loads only the 32-row boxes that hold rows (a few rows an expert: the
+//     weights are the traffic); the rest of the tile keeps stale codes, whose products are not stored.
+#include <cuda.h>
+
+#include "common.cuh"
+#include "fp4_impl.cuh"
+#include "gemm_common.cuh"
+#include "kernels.h"
+
+namespace moe {
+namespace a4 {
+
+constexpr int BM = 128;
+constexpr int BN = 256;
+constexpr int BK = 256;  // elements of a K block: 128 bytes of codes
+constexpr int STAGES = 4;
+constexpr int A_BYTES = BM * BK / 2;
+constexpr int B_BYTES = BN * BK / 2;
+constexpr int SFA_BYTES = BM * BK / 16;
+constexpr int SFB_BYTES = BN * BK / 16;
+constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SFA_BYTES + SFB_BYTES;
+constexpr int SCALE_WARP0 = 2;
+constexpr int EPI_WARP0 = SCALE_WARP0 + STAGES;
+constexpr int EPI_WARPS = 8;
+constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
+constexpr int ACC1 = 208;    // column of the second accumulator
+constexpr int SFA_COL = 464;
+constexpr int SFB_COL = 480;
+constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024;
+
+struct Args {
+  const int32_t* offsets;
+  const int32_t* slot_expert;
+  int E, shared, R, T, K, N, n_tiles, mode, I, f32;
+  int a_rows, b_rows;
+  const uint8_t* a_scales;
+  const uint8_t* b_scales;
+  const uint8_t* bs_scales;
+  const float* a_g;
+  const float* b_g;
+  const float* bs_g;
+  int64_t ldo;
+  int vec;  // bytes that every output row is aligned to: 32, 16 or less
+  void* out;
+  uint8_t* out_scales;
+  const float* out_g;
+  const float* row_weight;
+  int* status;
+  long long wait_limit;
+};
+
+struct Shared {
+  uint64_t full[STAGES];
+  uint64_t empty[STAGES];
+  uint64_t tfull[2];
+  uint64_t tfree;
+  uint64_t mma_done;
+  uint32_t tmem_slot;
+  volatile int abort_flag;
+  int unreported;
+  grp::Table tb;
+};
+
+using grp::wait_or_abort;
+
+// D (+)= A * B^T with block scales in TMEM; K = 64 elements.
+template <int FMT>
+__device__ __forceinline__ void umma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                         uint32_t accumulate) {
+  if (FMT == fp4::kNv)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+// 512 bytes of scales [32][16] from shared memory to 4 TMEM columns, once for each lane quarter.
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// Descriptor of 32 lines of 16 bytes, no swizzle: groups of 8 lines 128 bytes apart.
+__device__ __forceinline__ uint64_t scales_desc(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)(128u >> 4) << 16;
+  d |= (uint64_t)(128u >> 4) << 32;
+  d |= (uint64_t)1u << 46;
+  return d;
+}
+
+// Instruction descriptor: e2m1 operands, both K-major, fp32 accumulators; scales e4m3 (NVFP4) or e8m0.
+template <int FMT>
+__host__ __device__ constexpr uint32_t idesc_fp4(int M, int N) {
+  return (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (FMT == fp4::kNv ? 0u : 1u << 23) |
+         ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// The scale bytes of one row's K block as words of 4: 4 words (NVFP4) or 2 (MXFP4). `p`: the row's
+// scales of the block; `left`: how many of them there are (the rest of a short last block is 0).
+template <int FMT, bool VEC>
+__device__ __forceinline__ void load_scales(const uint8_t* p, int left, uint32_t (&w)[FMT == fp4::kNv ? 4 : 2]) {
+  constexpr int kWords = FMT == fp4::kNv ? 4 : 2;
+  if (VEC) {
+    if (FMT == fp4::kNv) {
+      const uint4 v = *reinterpret_cast<const uint4*>(p);
+      w[0] = v.x, w[1] = v.y, w[kWords - 2] = v.z, w[kWords - 1] = v.w;
+    } else {
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      w[0] = v.x, w[1] = v.y;
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < kWords; ++i) {
+    w[i] = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (4 * i + j < left) w[i] |= (uint32_t)p[4 * i + j] << (8 * j);
+  }
+}
+
+// 32 fp32 columns of a row to its output; `n`: how many of them exist.
+__device__ __forceinline__ void store_row(const Args& a, int64_t row, int col, int n, const float* v) {
+  if (a.f32) {
+    float* o = static_cast<float*>(a.out) + row * a.ldo + col;
+    if (n >= 32 && a.vec >= 16) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        reinterpret_cast<float4*>(o)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (i < n) o[i] = v[i];
+    }
+    return;
+  }
+  uint32_t w[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+  uint16_t* o = static_cast<uint16_t*>(a.out) + row * a.ldo + col;
+  if (n >= 32 && a.vec >= 32) {
+    st_global_v8(o, w);
+    st_global_v8(o + 16, w + 8);
+  } else if (n >= 32 && a.vec >= 16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      reinterpret_cast<uint4*>(o)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (i < n) o[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+  }
+}
+
+template <int FMT, bool VEC>
+__global__ void __launch_bounds__(THREADS, 1)
+    gemm_a4_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA32,
+                   const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmBs, const Args args) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Shared s;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = args.E + args.shared;
+  int* status = args.status ? args.status : &s.unreported;
+
+  if (warp == 0) {
+    grp::build_table(s.tb, args.offsets, args.E, args.shared, args.R, args.T, BM, lane);
+    if (lane == 0) {
+      for (int i = 0; i < STAGES; ++i) {
+        mbar_init(&s.full[i], 2);  // the TMA thread and the stage's scale warp
+        mbar_init(&s.empty[i], 1);
+      }
+      mbar_init(&s.tfull[0], 1);
+      mbar_init(&s.tfull[1], 1);
+      mbar_init(&s.tfree, EPI_WARPS);
+      mbar_init(&s.mma_done, 1);
+      s.abort_flag = 0;
+      fence_mbar_init();
+      tma_prefetch_desc(&tmA);
+      tma_prefetch_desc(&tmA32);
+      tma_prefetch_desc(&tmB);
+      tma_prefetch_desc(&tmBs);
+    }
+  }
+  if (warp == 1) {
+    tmem_alloc(&s.tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = s.tmem_slot;
+  const int total = s.tb.gtile[G] * args.n_tiles;
+  const int kblocks = (args.K + BK - 1) / BK;
+
+  if (warp == 0 && lane == 0) {
+    // ---------------- TMA producer
+    int stage = 0;
+    uint32_t phase = 0;
+    long long issued = 0;
+    bool ok = true;
+    for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
+      const grp::Tile t = grp::decode(s.tb, G, args.n_tiles, tile, BM);
+      const CUtensorMap* mb = t.g < args.E ? &tmB : &tmBs;
+      const int z = t.g < args.E ? (args.slot_expert ? args.slot_expert[t.g] : t.g) : 0;
+      const int n0 = args.mode == 0 ? t.n_tile * (BN / 2) : t.n_tile * BN;
+      const int n1 = args.mode == 0 ? args.I + n0 : n0 + BN / 2;
+      const int boxes = (t.rows + 31) / 32;
+      const uint32_t a_bytes = boxes == 4 ? A_BYTES : boxes * (A_BYTES / 4);
+      for (int kb = 0; kb < kblocks; ++kb) {
+        if (!wait_or_abort(&s.empty[stage], phase ^ 1, &s.abort_flag, status, args.wait_limit)) {
+          ok = false;
+          break;
+        }
+        uint8_t* a = smem + stage * STAGE_BYTES;
+        uint8_t* b = a + A_BYTES;
+        mbar_arrive_expect_tx(&s.full[stage], a_bytes + B_BYTES);
+        if (boxes == 4)
+          tma_load_2d(a, &tmA, &s.full[stage], kb * (BK / 2), t.a_row);
+        else
+          for (int i = 0; i < boxes; ++i)
+            tma_load_2d(a + i * (A_BYTES / 4), &tmA32, &s.full[stage], kb * (BK / 2), t.a_row + 32 * i);
+        tma_load_3d(b, mb, &s.full[stage], kb * (BK / 2), n0, z);
+        tma_load_3d(b + B_BYTES / 2, mb, &s.full[stage], kb * (BK / 2), n1, z);
+        ++issued;
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+    }
+    const long long first = issued > STAGES ? issued - STAGES : 0;
+    for (long long i = first; i < issued; ++i)
+      grp::drain_wait(&s.full[i % STAGES], (uint32_t)((i / STAGES) & 1), args.wait_limit);
+  } else if (warp == 1 && lane == 0) {
+    // ---------------- MMA issuer
+    constexpr uint32_t IDESC = idesc_fp4<FMT>(BM, BN);
+    int stage = 0, n = 0;  // n: tiles of this CTA so far
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x, ++n) {
+      // the columns shared with the tile before have been read (and all of the tile before that one)
+      if (n > 0 && !wait_or_abort(&s.tfree, (uint32_t)(n - 1) & 1, &s.abort_flag, status, args.wait_limit)) break;
+      const uint32_t d = tmem_base + (n & 1 ? ACC1 : 0);
+      for (int kb = 0; kb < kblocks; ++kb) {
+        if (!wait_or_abort(&s.full[stage], phase, &s.abort_flag, status, args.wait_limit)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t a = smem_u32(smem + stage * STAGE_BYTES);
+        const uint32_t b = a + A_BYTES, sfa = b + B_BYTES, sfb = sfa + SFA_BYTES;
+        // copies and MMAs of one thread run in order: the copies wait for the MMAs that read the columns
+        constexpr int kSteps = FMT == fp4::kNv ? 4 : 2;  // scale words of a K block
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+          copy_scales(tmem_base + SFA_COL + 4 * i, scales_desc(sfa + 512 * i));
+          copy_scales(tmem_base + SFB_COL + 8 * i, scales_desc(sfb + 1024 * i));
+          copy_scales(tmem_base + SFB_COL + 8 * i + 4, scales_desc(sfb + 1024 * i + 512));
+        }
+#pragma unroll
+        for (int kk = 0; kk < BK / 64; ++kk) {
+          const int w = FMT == fp4::kNv ? kk : kk / 2;             // word of the scales
+          const uint32_t id = FMT == fp4::kNv ? 0u : 2u * (kk & 1);  // bytes of it: all four, or a half
+          umma_fp4<FMT>(d, sw128_kmajor_desc(a + kk * 32), sw128_kmajor_desc(b + kk * 32),
+                        IDESC | id << 4 | id << 29, tmem_base + SFA_COL + 4 * w, tmem_base + SFB_COL + 8 * w,
+                        (kb | kk) != 0);
+        }
+        umma_commit(&s.empty[stage]);
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      if (ok) umma_commit(&s.tfull[n & 1]);
+    }
+    umma_commit(&s.mma_done);
+    grp::drain_wait(&s.mma_done, 0, args.wait_limit);
+  } else if (warp >= SCALE_WARP0 && warp < EPI_WARP0) {
+    // ---------------- scale producers: warp w fills stage w, every STAGES-th K block of this CTA
+    const int w = warp - SCALE_WARP0;
+    const int pitch = args.K / fp4::kBlock<FMT>;
+    constexpr int kPer = BK / fp4::kBlock<FMT>;  // scales of a row's K block
+    constexpr int kWords = kPer / 4;
+    const uint32_t sfa = smem_u32(smem + w * STAGE_BYTES) + A_BYTES + B_BYTES + 16 * lane, sfb = sfa + SFA_BYTES;
+    int c0 = 0;  // K blocks of this CTA before the tile
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x, c0 += kblocks) {
+      const grp::Tile t = grp::decode(s.tb, G, args.n_tiles, tile, BM);
+      const bool routed = t.g < args.E;
+      const int64_t z = routed ? (args.slot_expert ? args.slot_expert[t.g] : t.g) : 0;
+      const int n0 = args.mode == 0 ? t.n_tile * (BN / 2) : t.n_tile * BN;
+      const int n1 = args.mode == 0 ? args.I + n0 : n0 + BN / 2;
+      const uint8_t* bs = (routed ? args.b_scales : args.bs_scales) + z * args.b_rows * (int64_t)pitch;
+      const uint8_t* p[12];  // rows past the end take the last one's scales: they are not stored
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        p[i] = args.a_scales + min(t.a_row + lane + 32 * i, args.a_rows - 1) * (int64_t)pitch;
+        p[4 + i] = bs + min(n0 + lane + 32 * i, args.b_rows - 1) * (int64_t)pitch;
+        p[8 + i] = bs + min(n1 + lane + 32 * i, args.b_rows - 1) * (int64_t)pitch;
+      }
+      for (int kb = (w - c0) & (STAGES - 1); kb < kblocks; kb += STAGES) {
+        uint32_t v[12][kWords];
+#pragma unroll
+        for (int i = 0; i < 12; ++i) load_scales<FMT, VEC>(p[i] + kb * kPer, pitch - kb * kPer, v[i]);
+        const int got = wait_or_abort(&s.empty[w], phase ^ 1, &s.abort_flag, status, args.wait_limit);
+        if (__any_sync(0xffffffffu, !got)) {
+          ok = false;
+          break;
+        }
+        phase ^= 1;
+#pragma unroll
+        for (int j = 0; j < kWords; ++j) {
+          sts128(sfa + 512 * j, v[0][j], v[1][j], v[2][j], v[3][j]);
+          sts128(sfb + 1024 * j, v[4][j], v[5][j], v[6][j], v[7][j]);
+          sts128(sfb + 1024 * j + 512, v[8][j], v[9][j], v[10][j], v[11][j]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.full[w]);
+      }
+    }
+  } else if (warp >= EPI_WARP0) {
+    // ---------------- epilogue
+    const int quarter = warp & 3, half = (warp - EPI_WARP0) >> 2;
+    const int r = quarter * 32 + lane;
+    const uint32_t tq = tmem_base + ((uint32_t)(quarter * 32) << 16);
+    const float ag = args.a_g ? *args.a_g : 1.0f;
+    const float hg = args.out_g ? *args.out_g : 1.0f;
+    const int chunks = args.mode == 0 ? 4 : 8;  // of 32 output columns
+    int n = 0;
+    for (int tile = blockIdx.x; tile < total; tile += gridDim.x, ++n) {
+      const grp::Tile t = grp::decode(s.tb, G, args.n_tiles, tile, BM);
+      const bool routed = t.g < args.E;
+      const bool valid = r < t.rows;
+      const int64_t row = (int64_t)t.a_row + r;
+      const float* bg = routed ? args.b_g : args.bs_g;
+      float scale = bg ? ag * bg[routed ? (args.slot_expert ? args.slot_expert[t.g] : t.g) : 0] : ag;
+      if (args.mode == 1 && valid && routed) scale *= args.row_weight[row];
+      const int got = wait_or_abort(&s.tfull[n & 1], (uint32_t)(n >> 1) & 1, &s.abort_flag, status, args.wait_limit);
+      if (__any_sync(0xffffffffu, !got)) break;
+      __syncwarp();
+      tc_fence_after();
+      const uint32_t tacc = tq + (n & 1 ? ACC1 : 0);
+      const bool any = quarter * 32 < t.rows;  // this quarter has rows
+      // Positions 0 .. chunks - 1 in the order that frees the shared columns first (the last 48 columns of
+      // the first accumulator, the first 48 of the second): they lie in the chunks of positions 0 and 1.
+      // The two warps of a quarter take alternate positions.
+      for (int i = half; i < chunks; i += 2) {
+        const int c = 32 * (n & 1 ? i : chunks - 1 - i);
+        if (args.mode == 0) {
+          uint32_t gate[32], up[32];
+          if (any) {
+            tmem_ld32(tacc + c, gate);
+            tmem_ld32(tacc + BN / 2 + c, up);
+            tmem_ld_wait_regs(gate);
+            tmem_ld_wait_regs(up);
+          }
+          if (i < 2) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.tfree);
+          }
+          if (!any) continue;
+          float h[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            h[j] = grp::silu(__uint_as_float(gate[j]) * scale) * (__uint_as_float(up[j]) * scale);
+          uint32_t q[4], sc = 0;
+          constexpr int kBlk = fp4::kBlock<FMT>;
+#pragma unroll
+          for (int b = 0; b < 32 / kBlk; ++b) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int j = 0; j < kBlk; ++j) m = max(m, fp4::abs_bits(h[kBlk * b + j]));
+            float by;
+            sc |= fp4::block_scale<FMT>(m, hg, by) << (8 * b);
+#pragma unroll
+            for (int j = 0; j < kBlk / 8; ++j) q[kBlk / 8 * b + j] = fp4::codes8<FMT>(h + kBlk * b + 8 * j, by);
+          }
+          if (valid) {
+            const int col = t.n_tile * (BN / 2) + c;
+            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(args.out) + (row * args.ldo + col) / 2) =
+                make_uint4(q[0], q[1], q[2], q[3]);
+            uint8_t* so = args.out_scales + (row * args.ldo + col) / kBlk;
+            if (FMT == fp4::kNv)
+              *reinterpret_cast<uint16_t*>(so) = (uint16_t)sc;
+            else
+              *so = (uint8_t)sc;
+          }
+        } else {
+          uint32_t v[32];
+          if (any) {
+            tmem_ld32(tacc + c, v);
+            tmem_ld_wait_regs(v);
+          }
+          if (i < 2) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.tfree);
+          }
+          const int col = t.n_tile * BN + c;
+          if (valid && col < args.N) {
+            float f[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[j]) * scale;
+            store_row(args, row, col, args.N - col, f);
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem_base, 512);
+  }
+}
+
+}  // namespace a4
+
+cudaError_t launch_gemm_a4(const GemmA4Desc& d, cudaStream_t stream, std::string* err) {
+  cudaError_t e = tma_encoder_ready();
+  if (e != cudaSuccess) {
+    *err = "cuTensorMapEncodeTiled is not available from the driver";
+    return e;
+  }
+  using Kernel = decltype(&a4::gemm_a4_kernel<fp4::kNv, true>);
+  static const Kernel kernels[4] = {a4::gemm_a4_kernel<fp4::kNv, true>, a4::gemm_a4_kernel<fp4::kNv, false>,
+                                    a4::gemm_a4_kernel<fp4::kMx, true>, a4::gemm_a4_kernel<fp4::kMx, false>};
+  // the dynamic shared-memory opt-in is a per-device function attribute
+  static PerDevice<bool> attr;
+  bool attr_set = false;
+  e = per_device<bool>(
+      attr,
+      [](bool& v) {
+        cudaError_t r = cudaSuccess;
+        for (Kernel k : kernels)
+          if (r == cudaSuccess)
+            r = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, a4::SMEM_BYTES);
+        v = r == cudaSuccess;
+        return r;
+      },
+      &attr_set);
+  if (e != cudaSuccess) {
+    *err = "cudaFuncSetAttribute failed";
+    return e;
+  }
+  CUtensorMap tA, tA32, tB, tBs;
+  const CUtensorMapDataType U8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  const bool ok = tma_encode_2d(&tA, d.A, U8, 1, d.a_rows, d.K / 2, a4::BM) &&
+                  tma_encode_2d(&tA32, d.A, U8, 1, d.a_rows, d.K / 2, a4::BM / 4) &&
+                  tma_encode_3d(&tB, d.B, U8, 1, d.n_experts, d.b_rows, d.K / 2, a4::BN / 2) &&
+                  tma_encode_3d(&tBs, d.B_shared ? d.B_shared : d.B, U8, 1, 1, d.b_rows, d.K / 2, a4::BN / 2);
+  if (!ok) {
+    *err = "cuTensorMapEncodeTiled rejected a 4-bit GEMM operand";
+    return cudaErrorInvalidValue;
+  }
+  a4::Args a;
+  a.offsets = d.offsets;
+  a.slot_expert = d.slot_expert;
+  a.E = d.E;
+  a.shared = d.B_shared != nullptr;
+  a.R = d.R;
+  a.T = d.T;
+  a.K = d.K;
+  a.N = d.N;
+  a.mode = d.mode;
+  a.I = d.I;
+  a.f32 = d.f32;
+  a.n_tiles = d.mode == 0 ? d.I / (a4::BN / 2) : (int)cdiv(d.N, a4::BN);
+  a.a_rows = (int)d.a_rows;
+  a.b_rows = (int)d.b_rows;
+  a.a_scales = static_cast<const uint8_t*>(d.As);
+  a.b_scales = static_cast<const uint8_t*>(d.Bs);
+  a.bs_scales = static_cast<const uint8_t*>(d.Bs_shared);
+  a.a_g = d.Ag;
+  a.b_g = d.Bg;
+  a.bs_g = d.Bg_shared;
+  a.ldo = d.ldo;
+  const uintptr_t mis = reinterpret_cast<uintptr_t>(d.out) | (uintptr_t)(d.ldo * (d.f32 ? 4 : 2));
+  a.vec = mis % 32 == 0 ? 32 : mis % 16 == 0 ? 16 : 0;
+  a.out = d.out;
+  a.out_scales = static_cast<uint8_t*>(d.out_scales);
+  a.out_g = d.out_g;
+  a.row_weight = d.row_weight;
+  a.status = d.status;
+  a.wait_limit = 4000000000LL;  // about two seconds of SM clock
+  // a row's scales of a K block are one aligned load where rows of scales are whole numbers of them
+  const bool vec = d.K % a4::BK == 0;
+  kernels[(d.format == fp4::kNv ? 0 : 2) + (vec ? 0 : 1)]<<<num_sms(), a4::THREADS, a4::SMEM_BYTES, stream>>>(tA, tA32,
+                                                                                                             tB, tBs, a);
+  return cudaGetLastError();
+}
+
+}  // namespace moe

@@ -83,6 +83,10 @@ struct DispatchDesc {
   const int32_t* replicas = nullptr;
   const int32_t* replica_slot = nullptr;
   int32_t* expert_counts = nullptr;  // scratch [E]: kept rows per logical expert
+  // 4-bit rows (nullptr: not): xd takes the codes [R_tot, h/2], fp4_scales the block scales
+  uint8_t* fp4_scales = nullptr;
+  int fp4_format = 0;
+  const float* fp4_g = nullptr;  // [1] NVFP4 scale of the activations, nullptr: 1
 };
 cudaError_t launch_dispatch(const DispatchDesc& d, cudaStream_t stream);
 // Steps 1-3 of a small batch as one cooperative launch (fused.cu): the router GEMM on the CUDA cores
@@ -191,6 +195,74 @@ cudaError_t launch_grouped_gemm_nvfp4(const GroupedGemmFp4Desc& d, cudaStream_t 
 // gathered in g itself, the blocks are quantised, then g is turned into the matrix scales.
 cudaError_t launch_quantize_weights_nvfp4(const void* w, int64_t batch, int64_t rows, int64_t cols, void* q, void* s,
                                           float* g, cudaStream_t stream);
+
+// Rows to microscaled 4 bits and back (fp4_quant.cu); rows * cols / 8 < 2^32 - 256.
+cudaError_t launch_quantize_fp4(const void* x, int type, int64_t rows, int64_t cols, int64_t ldx, int format,
+                                const float* g, void* q, void* s, cudaStream_t stream);
+cudaError_t launch_dequantize_fp4(const void* q, const void* s, const float* g, int64_t rows, int64_t cols, int format,
+                                  int type, void* y, cudaStream_t stream);
+
+// The product of 4-bit rows and 4-bit weights on the block-scaled tensor cores (gemm_a4.cu).
+// mode 0: H codes and scales = quantise(silu(A W_gate^T) * (A W_up^T)); mode 1: yd (bf16) = (A W_down^T) *
+// row_weight; mode 2: y (bf16 or fp32) [T, N] = A B^T, one group.
+struct GemmA4Desc {
+  int format;  // MOE_FP4_*
+  const void* A;         // [a_rows, K/2] codes
+  const void* As;        // [a_rows, K/block] scales
+  const float* Ag;       // [1] activation scale or nullptr
+  int64_t a_rows;
+  const void* B;         // [E, b_rows, K/2]
+  const void* Bs;        // [E, b_rows, K/block]
+  const float* Bg;       // [E] matrix scales or nullptr
+  const void* B_shared = nullptr;  // [b_rows, K/2] shared expert or nullptr
+  const void* Bs_shared = nullptr;
+  const float* Bg_shared = nullptr;
+  int64_t b_rows;
+  const int32_t* offsets;  // nullptr: one group of rows [0, T)
+  const int32_t* slot_expert = nullptr;
+  int n_experts = 1;
+  int E, R, T, K, N, I;
+  int mode;
+  int f32 = 0;               // mode 2: fp32 output
+  void* out;                 // codes, or rows
+  void* out_scales = nullptr;  // mode 0
+  const float* out_g = nullptr;  // mode 0: [1] scale of H or nullptr
+  int64_t ldo;               // elements
+  const float* row_weight = nullptr;
+  int* status;               // nullptr: a wait that gives up is not recorded
+};
+cudaError_t launch_gemm_a4(const GemmA4Desc& d, cudaStream_t stream, std::string* err);
+
+// The router's balance loss (balance_loss.cu). scratch: balance_loss_entries() * (2 E + 1) words.
+int64_t balance_loss_entries(int T, int E, int S);
+struct BalanceLossDesc {
+  const void* logits;  // [T, E]
+  const int32_t* topk_idx;
+  const int32_t* offsets;  // [S + 1] or nullptr
+  const uint8_t* mask;     // [T] or nullptr
+  int T, E, k, S;
+  int sigmoid, bf16;
+  float alpha;
+  void* scratch;
+  float* loss;
+  int32_t* counts;
+  float* mean;
+  int32_t* tokens;
+};
+cudaError_t launch_balance_loss(const BalanceLossDesc& d, int* launches, cudaStream_t stream);
+struct BalanceLossBackwardDesc {
+  const void* logits;
+  const int32_t* offsets;
+  const uint8_t* mask;
+  const int32_t* counts;
+  const int32_t* tokens;
+  const float* dloss;
+  void* dlogits;
+  int T, E, k, S;
+  int sigmoid, bf16;
+  float alpha;
+};
+cudaError_t launch_balance_loss_backward(const BalanceLossBackwardDesc& d, cudaStream_t stream);
 
 // Step 4: combine.
 cudaError_t launch_combine(const void* yd, const int32_t* inv_pos, void* y, int T, int h, int k, int shared,

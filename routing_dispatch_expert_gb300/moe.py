@@ -17,8 +17,12 @@ SO_PATH = os.path.join(_PKG, "_build", "libmoe_gb300.so")
 
 MOE_OK, MOE_ERR_INVALID, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_CUDA, MOE_ERR_DEVICE = 0, -1, -2, -3, -4, -5
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
-DTYPES = {"bf16": 0, "fp8": 1, "nvfp4": 2}
-MOE_DTYPE_BF16, MOE_DTYPE_FP8_BLOCK128, MOE_DTYPE_NVFP4 = 0, 1, 2
+DTYPES = {"bf16": 0, "fp8": 1, "nvfp4": 2, "mxfp4": 3}
+MOE_DTYPE_BF16, MOE_DTYPE_FP8_BLOCK128, MOE_DTYPE_NVFP4, MOE_DTYPE_MXFP4 = 0, 1, 2, 3
+MOE_TYPE_F32, MOE_TYPE_BF16, MOE_TYPE_F16 = 0, 1, 2
+ELEMENT_TYPES = {torch.float32: MOE_TYPE_F32, torch.bfloat16: MOE_TYPE_BF16, torch.float16: MOE_TYPE_F16}
+FP4_FORMATS = {"nvfp4": 0, "mxfp4": 1}
+FP4_BLOCK = {"nvfp4": 16, "mxfp4": 32}
 MOE_LOGITS_GIVEN = 1
 MOE_STATUS_BAD_EXPERT_INDEX, MOE_STATUS_WAIT_TIMEOUT = 1, 2
 
@@ -54,6 +58,10 @@ class MoeWsLayout(ctypes.Structure):
                                                "router_w3", "scratch", "total")]
 
 
+class MoeFp4Activations(ctypes.Structure):
+    _fields_ = [("g_x", ctypes.c_void_p), ("g_h", ctypes.c_void_p)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -69,6 +77,7 @@ def load():
             vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
             cfgp = ctypes.POINTER(MoeConfig)
             wp = ctypes.POINTER(MoeWeightsStruct)
+            actp = ctypes.POINTER(MoeFp4Activations)
             sig = {
                 "moe_workspace_size": [cfgp, ctypes.POINTER(sz)],
                 "moe_workspace_layout": [cfgp, ctypes.POINTER(MoeWsLayout)],
@@ -87,6 +96,15 @@ def load():
                 "moe_graph_destroy": [vp],
                 "moe_eplb_plan": [vp, i32, i32, i32, vp, vp, vp, vp, vp],
                 "moe_balance": [cfgp, vp, vp, vp],
+                "moe_quantize_fp4": [vp, i32, i64, i64, i64, i32, vp, vp, vp, vp],
+                "moe_dequantize_fp4": [vp, vp, i64, i64, i32, vp, i32, vp, vp],
+                "moe_matmul_fp4": [vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, i32, vp, i64, vp, vp],
+                "moe_dispatch_fp4": [cfgp, actp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
+                "moe_expert_ffn_fp4": [cfgp, wp, actp, vp, vp, vp, vp, vp, vp, sz, vp],
+                "moe_forward_fp4": [cfgp, vp, wp, actp, vp, vp, sz, vp],
+                "moe_balance_loss_workspace_size": [cfgp, i32, ctypes.POINTER(sz)],
+                "moe_balance_loss": [cfgp, vp, i32, vp, vp, i32, vp, ctypes.c_float, vp, vp, vp, vp, vp, sz, vp],
+                "moe_balance_loss_backward": [cfgp, vp, i32, vp, vp, vp, i32, vp, ctypes.c_float, vp, vp, vp],
             }
             for name, args in sig.items():
                 f = getattr(L, name)
@@ -253,6 +271,181 @@ def quantize_weights_nvfp4(w: torch.Tensor):
     return q, s, g
 
 
+def _tensor(t, name, dtypes, shape=None, contiguous=True):
+    """t, if it is a CUDA tensor of one of these dtypes and of this shape (None: any size); ValueError otherwise."""
+    dtypes = dtypes if isinstance(dtypes, tuple) else (dtypes,)
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
+    if shape is not None and (t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape))):
+        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t
+
+
+def _fp4_format(fmt):
+    if fmt not in FP4_FORMATS:
+        raise ValueError(f"unknown 4-bit format {fmt!r}: 'nvfp4' or 'mxfp4'")
+    return FP4_FORMATS[fmt]
+
+
+def _fp4_matrix(q, s, fmt, name):
+    """(rows, cols) of a 4-bit matrix."""
+    _tensor(q, name + " codes", torch.uint8, (None, None))
+    rows, cols = q.shape[0], 2 * q.shape[1]
+    _tensor(s, name + " scales", torch.uint8, (rows, cols // FP4_BLOCK[fmt]))
+    return rows, cols
+
+
+def _fp4_scale(g, name):
+    return None if g is None else _tensor(g, name, torch.float32, (1,))
+
+
+def quantize_fp4(x: torch.Tensor, fmt: str = "nvfp4", g: torch.Tensor | None = None, q=None, s=None):
+    """Rows [rows, cols] (fp32, bf16 or fp16; cols a multiple of 32; the rows may be strided) to microscaled 4
+    bits: (codes uint8 [rows, cols/2], scales uint8 [rows, cols/16] for 'nvfp4', [rows, cols/32] for 'mxfp4').
+    g: fp32 [1], the NVFP4 scale of the matrix (moe_quantize_fp4 in include/moe.h), None = 1."""
+    f = _fp4_format(fmt)
+    _tensor(x, "x", tuple(ELEMENT_TYPES), (None, None), contiguous=False)
+    rows, cols = x.shape
+    if cols > 1 and x.stride(1) != 1:
+        raise ValueError("the elements of a row of x must be contiguous")
+    if q is None:
+        q = torch.empty(rows, cols // 2, dtype=torch.uint8, device=x.device)
+    if s is None:
+        s = torch.empty(rows, cols // FP4_BLOCK[fmt], dtype=torch.uint8, device=x.device)
+    if cols % 32 == 0 and _fp4_matrix(q, s, fmt, "quantised") != (rows, cols):
+        raise ValueError(f"q and s must be those of a matrix {(rows, cols)}")
+    ldx = x.stride(0) if rows > 1 else cols
+    _check(load().moe_quantize_fp4(_ptr(x), ELEMENT_TYPES[x.dtype], rows, cols, ldx, f, _ptr(_fp4_scale(g, "g")),
+                                   _ptr(q), _ptr(s), _stream()))
+    return q, s
+
+
+def dequantize_fp4(q: torch.Tensor, s: torch.Tensor, fmt: str = "nvfp4", g: torch.Tensor | None = None,
+                   dtype=torch.float32, y=None) -> torch.Tensor:
+    """The values [rows, cols] that 4-bit rows stand for, rounded once to dtype (or to y's)."""
+    f = _fp4_format(fmt)
+    rows, cols = _fp4_matrix(q, s, fmt, "4-bit")
+    if y is None:
+        y = torch.empty(rows, cols, dtype=dtype, device=q.device)
+    _tensor(y, "y", tuple(ELEMENT_TYPES), (rows, cols))
+    _check(load().moe_dequantize_fp4(_ptr(q), _ptr(s), rows, cols, f, _ptr(_fp4_scale(g, "g")),
+                                     ELEMENT_TYPES[y.dtype], _ptr(y), _stream()))
+    return y
+
+
+def matmul_fp4(aq, a_s, bq, b_s, fmt: str = "nvfp4", ga=None, gb=None, dtype=torch.bfloat16, y=None,
+               status=None) -> torch.Tensor:
+    """y [M, N] = A B^T of 4-bit matrices A [M, K] and B [N, K] (codes, scales, NVFP4 matrix scales fp32 [1] or
+    None = 1), fp32 accumulation, rounded once to bf16 or fp32. y may have strided rows. status: int32 [1] that
+    MOE_STATUS_WAIT_TIMEOUT is added to if a wait of the kernel gives up."""
+    f = _fp4_format(fmt)
+    M, K = _fp4_matrix(aq, a_s, fmt, "A")
+    N, kb = _fp4_matrix(bq, b_s, fmt, "B")
+    if K != kb:
+        raise ValueError(f"A has rows of {K} elements, B of {kb}")
+    if y is None:
+        y = torch.empty(M, N, dtype=dtype, device=aq.device)
+    _tensor(y, "y", (torch.bfloat16, torch.float32), (M, N), contiguous=False)
+    if N > 1 and y.stride(1) != 1:
+        raise ValueError("the elements of a row of y must be contiguous")
+    if status is not None:
+        _tensor(status, "status", torch.int32, (1,))
+    ldy = y.stride(0) if M > 1 else N
+    _check(load().moe_matmul_fp4(_ptr(aq), _ptr(a_s), _ptr(_fp4_scale(ga, "ga")), _ptr(bq), _ptr(b_s),
+                                 _ptr(_fp4_scale(gb, "gb")), M, N, K, f, ELEMENT_TYPES[y.dtype], _ptr(y), ldy,
+                                 _ptr(status), _stream()))
+    return y
+
+
+class Fp4Activations:
+    """Scales of a layer's 4-bit rows (fp32 [1] each, None = 1): g_x of the rows that enter the gate/up product,
+    g_h of the SwiGLU product; usually the largest magnitude seen in calibration / 2688. NVFP4 only."""
+
+    def __init__(self, g_x: torch.Tensor | None = None, g_h: torch.Tensor | None = None):
+        self.tensors = (_fp4_scale(g_x, "g_x"), _fp4_scale(g_h, "g_h"))
+        self.struct = MoeFp4Activations(*(None if t is None else t.data_ptr() for t in self.tensors))
+
+
+def _act(act: Fp4Activations | None):
+    return None if act is None else ctypes.byref(act.struct)
+
+
+def dispatch_fp4(cfg, act: Fp4Activations | None, x, topk_idx, topk_w, counts, offsets, inv_pos, row_token, row_weight,
+                 xq, xs, ws):
+    """moe_dispatch_fp4: dispatch with the rows quantised to the 4 bits of cfg's weights."""
+    _check(load().moe_dispatch_fp4(ctypes.byref(cfg), _act(act), _ptr(x), _ptr(topk_idx), _ptr(topk_w), _ptr(counts),
+                                   _ptr(offsets), _ptr(inv_pos), _ptr(row_token), _ptr(row_weight), _ptr(xq), _ptr(xs),
+                                   _ptr(ws), ws.numel(), _stream()))
+
+
+def expert_ffn_fp4(cfg, weights: Weights, act: Fp4Activations | None, xq, xs, offsets, row_weight, yd, ws):
+    """moe_expert_ffn_fp4: the experts on 4-bit rows."""
+    _check(load().moe_expert_ffn_fp4(ctypes.byref(cfg), ctypes.byref(weights.struct), _act(act), _ptr(xq), _ptr(xs),
+                                     _ptr(offsets), _ptr(row_weight), _ptr(yd), _ptr(ws), ws.numel(), _stream()))
+
+
+def forward_fp4(cfg, x, weights: Weights, act: Fp4Activations | None, y, ws):
+    """moe_forward_fp4: the whole layer with 4-bit rows and 4-bit weights (dtype 'nvfp4' or 'mxfp4')."""
+    _check(load().moe_forward_fp4(ctypes.byref(cfg), _ptr(x), ctypes.byref(weights.struct), _act(act), _ptr(y),
+                                  _ptr(ws), ws.numel(), _stream()))
+
+
+def balance_loss_workspace(cfg: MoeConfig, n_seq: int = 1, device="cuda") -> torch.Tensor:
+    n = ctypes.c_size_t()
+    _check(load().moe_balance_loss_workspace_size(ctypes.byref(cfg), n_seq, ctypes.byref(n)))
+    return torch.empty(n.value, dtype=torch.uint8, device=device)
+
+
+def _balance_inputs(cfg, logits, seq_offsets, token_mask):
+    """n_seq, after the checks that both directions share."""
+    _tensor(logits, "logits", (torch.float32, torch.bfloat16), (cfg.T, cfg.E))
+    if token_mask is not None:
+        _tensor(token_mask, "token_mask", (torch.uint8, torch.bool), (cfg.T,))
+    if seq_offsets is None:
+        return 1
+    _tensor(seq_offsets, "seq_offsets", torch.int32, (None,))
+    if seq_offsets.numel() < 2:
+        raise ValueError("seq_offsets must hold the begin of each sequence and the end of the last")
+    return seq_offsets.numel() - 1
+
+
+def balance_loss(cfg, logits, topk_idx, alpha: float, seq_offsets=None, token_mask=None, ws=None) -> dict:
+    """The router's load-balance loss (moe_balance_loss in include/moe.h) of logits [T, E] (fp32 or bf16) and the
+    chosen experts topk_idx [T, k]: loss [S], counts [S, E], mean_prob [S, E] and tokens [S] of S sequences
+    (seq_offsets int32 [S + 1]; None: one of all tokens). token_mask [T]: 0 = padding. ws: balance_loss_workspace."""
+    S = _balance_inputs(cfg, logits, seq_offsets, token_mask)
+    _tensor(topk_idx, "topk_idx", torch.int32, (cfg.T, cfg.k))
+    ws = balance_loss_workspace(cfg, S, logits.device) if ws is None else _tensor(ws, "ws", torch.uint8, (None,))
+    dev = logits.device
+    loss = torch.empty(S, dtype=torch.float32, device=dev)
+    counts = torch.empty(S, cfg.E, dtype=torch.int32, device=dev)
+    mean = torch.empty(S, cfg.E, dtype=torch.float32, device=dev)
+    tokens = torch.empty(S, dtype=torch.int32, device=dev)
+    _check(load().moe_balance_loss(ctypes.byref(cfg), _ptr(logits), ELEMENT_TYPES[logits.dtype], _ptr(topk_idx),
+                                   _ptr(seq_offsets), S, _ptr(token_mask), alpha, _ptr(loss), _ptr(counts), _ptr(mean),
+                                   _ptr(tokens), _ptr(ws), ws.numel(), _stream()))
+    return {"loss": loss, "counts": counts, "mean_prob": mean, "tokens": tokens}
+
+
+def balance_loss_backward(cfg, logits, counts, tokens, alpha: float, dloss, seq_offsets=None, token_mask=None,
+                          dlogits=None) -> torch.Tensor:
+    """Gradient of balance_loss with respect to logits (of their dtype), from its counts and tokens and the
+    gradients dloss [S] of its losses."""
+    S = _balance_inputs(cfg, logits, seq_offsets, token_mask)
+    _tensor(counts, "counts", torch.int32, (S, cfg.E))
+    _tensor(tokens, "tokens", torch.int32, (S,))
+    _tensor(dloss, "dloss", torch.float32, (S,))
+    dlogits = torch.empty_like(logits) if dlogits is None else _tensor(dlogits, "dlogits", logits.dtype, (cfg.T, cfg.E))
+    _check(load().moe_balance_loss_backward(ctypes.byref(cfg), _ptr(logits), ELEMENT_TYPES[logits.dtype], _ptr(counts),
+                                            _ptr(tokens), _ptr(seq_offsets), S, _ptr(token_mask), alpha, _ptr(dloss),
+                                            _ptr(dlogits), _stream()))
+    return dlogits
+
+
 def launch_count() -> int:
     """Kernels the library has launched in this process so far."""
     return int(load().moe_launch_count())
@@ -289,11 +482,13 @@ def balance(cfg, ws) -> dict:
 
 
 class MoeLayer:
-    """Convenience wrapper: a config, its weights and a workspace; ``layer(x)`` runs moe_forward."""
+    """Convenience wrapper: a config, its weights and a workspace; ``layer(x)`` runs moe_forward, or
+    moe_forward_fp4 (4-bit rows and weights) with fp4_activations."""
 
-    def __init__(self, cfg: MoeConfig, weights: Weights, device="cuda"):
+    def __init__(self, cfg: MoeConfig, weights: Weights, device="cuda", fp4_activations: Fp4Activations | None = None):
         self.cfg = cfg
         self.weights = weights
+        self.fp4_activations = fp4_activations
         self.ws = alloc_workspace(cfg, device)
         # a fresh workspace holds arbitrary bits in its status word; read-and-clear it once
         device_status(cfg, self.ws)
@@ -301,7 +496,10 @@ class MoeLayer:
     def __call__(self, x: torch.Tensor, y: torch.Tensor | None = None) -> torch.Tensor:
         if y is None:
             y = torch.empty_like(x)
-        forward(self.cfg, x, self.weights, y, self.ws)
+        if self.fp4_activations is not None:
+            forward_fp4(self.cfg, x, self.weights, self.fp4_activations, y, self.ws)
+        else:
+            forward(self.cfg, x, self.weights, y, self.ws)
         return y
 
 
