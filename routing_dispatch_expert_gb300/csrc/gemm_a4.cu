@@ -10,12 +10,12 @@
 // nothing is expanded: a K block of 256 elements is one 128-byte swizzled row of shared memory.
 //
 //   * tiles of 128 rows x 256 columns (mode 0: 128 gate and the 128 matching up columns), persistent,
-//     one CTA per SM, a 4-stage ring of 54 KB: codes by TMA, scales by four warps (one a stage).
+//     one CTA per SM: a 4-stage ring of 48 KB for the codes (TMA), a 2-slot ring of 12 KB for the scales.
 //   * scales: `tcgen05.mma` reads them from TMEM, where row r of a 128-row operand has its 4 scale bytes
 //     of a step in lane r % 32 of column r / 32, repeated in the four lane quarters; `tcgen05.cp
 //     .32x128b.warpx4` copies 512 bytes of shared memory [32 lanes][4 columns][4 bytes] there. The scales
-//     stay row-major in HBM (the layout of the quantised weights, a plain copy of a checkpoint): a lane
-//     loads 16 (8) bytes of 4 rows and stores them transposed as one 16-byte line per step.
+//     stay row-major in HBM (the layout of the quantised weights, a plain copy of a checkpoint): six
+//     warps load 32-byte sectors of the rows and store them transposed, a 16-byte line per step.
 //   * TMEM: two accumulators of 256 columns do not leave room for the scales, so they share 48: columns
 //     [0, 256) and [208, 464), scales in [464, 512). The epilogue reads the shared columns of a tile
 //     first and hands them over; the next tile's MMAs then run beside the rest of the epilogue.
@@ -39,17 +39,23 @@ constexpr int BK = 256;  // elements of a K block: 128 bytes of codes
 constexpr int STAGES = 4;
 constexpr int A_BYTES = BM * BK / 2;
 constexpr int B_BYTES = BN * BK / 2;
-constexpr int SFA_BYTES = BM * BK / 16;
-constexpr int SFB_BYTES = BN * BK / 16;
-constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SFA_BYTES + SFB_BYTES;
+constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int SLOTS = 2;                 // ring of scales
+constexpr int SLOT_WORDS = 8;            // 4-byte words of scales of a row in a slot: a 32-byte sector
+constexpr int SLOT_BYTES = SLOT_WORDS * (BM + BN) * 4;
 constexpr int SCALE_WARP0 = 2;
-constexpr int EPI_WARP0 = SCALE_WARP0 + STAGES;
+constexpr int SCALE_WARPS = 6;           // 3 blocks of 128 rows (A, two of B) x 2 halves
+constexpr int EPI_WARP0 = SCALE_WARP0 + SCALE_WARPS;
+template <int FMT>
+constexpr int kWords = BK / fp4::kBlock<FMT> / 4;  // words of a row's K block
+template <int FMT>
+constexpr int kSlotBlocks = SLOT_WORDS / kWords<FMT>;  // K blocks of a slot
 constexpr int EPI_WARPS = 8;
 constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
 constexpr int ACC1 = 208;    // column of the second accumulator
 constexpr int SFA_COL = 464;
 constexpr int SFB_COL = 480;
-constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024;
+constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + SLOTS * SLOT_BYTES + 1024;
 
 struct Args {
   const int32_t* offsets;
@@ -75,6 +81,8 @@ struct Args {
 struct Shared {
   uint64_t full[STAGES];
   uint64_t empty[STAGES];
+  uint64_t sfull[SLOTS];
+  uint64_t sempty[SLOTS];
   uint64_t tfull[2];
   uint64_t tfree;
   uint64_t mma_done;
@@ -85,6 +93,17 @@ struct Shared {
 };
 
 using grp::wait_or_abort;
+
+// One lane of a converged warp, the same one on every call.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, e;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
 
 // D (+)= A * B^T with block scales in TMEM; K = 64 elements.
 template <int FMT>
@@ -133,27 +152,17 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, ui
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-// The scale bytes of one row's K block as words of 4: 4 words (NVFP4) or 2 (MXFP4). `p`: the row's
-// scales of the block; `left`: how many of them there are (the rest of a short last block is 0).
-template <int FMT, bool VEC>
-__device__ __forceinline__ void load_scales(const uint8_t* p, int left, uint32_t (&w)[FMT == fp4::kNv ? 4 : 2]) {
-  constexpr int kWords = FMT == fp4::kNv ? 4 : 2;
-  if (VEC) {
-    if (FMT == fp4::kNv) {
-      const uint4 v = *reinterpret_cast<const uint4*>(p);
-      w[0] = v.x, w[1] = v.y, w[kWords - 2] = v.z, w[kWords - 1] = v.w;
-    } else {
-      const uint2 v = *reinterpret_cast<const uint2*>(p);
-      w[0] = v.x, w[1] = v.y;
-    }
-    return;
-  }
+// 16 scale bytes of a row at p, of which the row has `left` (more, fewer or none): the rest are 0.
+template <bool VEC>
+__device__ __forceinline__ uint4 load_scales(const uint8_t* p, int left) {
+  if constexpr (VEC) {
+    return left > 0 ? *reinterpret_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0);
+  } else {
+    uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-  for (int i = 0; i < kWords; ++i) {
-    w[i] = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (4 * i + j < left) w[i] |= (uint32_t)p[4 * i + j] << (8 * j);
+    for (int i = 0; i < 16; ++i)
+      if (i < left) w[i / 4] |= (uint32_t)p[i] << (8 * (i % 4));
+    return make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
@@ -197,7 +206,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared s;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // the same in all lanes, and known to be: the roles' addresses and counters stay in uniform registers
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int G = args.E + args.shared;
   int* status = args.status ? args.status : &s.unreported;
 
@@ -205,8 +215,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     grp::build_table(s.tb, args.offsets, args.E, args.shared, args.R, args.T, BM, lane);
     if (lane == 0) {
       for (int i = 0; i < STAGES; ++i) {
-        mbar_init(&s.full[i], 2);  // the TMA thread and the stage's scale warp
+        mbar_init(&s.full[i], 1);
         mbar_init(&s.empty[i], 1);
+      }
+      for (int i = 0; i < SLOTS; ++i) {
+        mbar_init(&s.sfull[i], SCALE_WARPS);
+        mbar_init(&s.sempty[i], 1);
       }
       mbar_init(&s.tfull[0], 1);
       mbar_init(&s.tfull[1], 1);
@@ -230,6 +244,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t tmem_base = s.tmem_slot;
   const int total = s.tb.gtile[G] * args.n_tiles;
   const int kblocks = (args.K + BK - 1) / BK;
+  const uint32_t slots = smem_u32(smem) + STAGES * STAGE_BYTES;
 
   if (warp == 0 && lane == 0) {
     // ---------------- TMA producer
@@ -270,94 +285,129 @@ __global__ void __launch_bounds__(THREADS, 1)
     const long long first = issued > STAGES ? issued - STAGES : 0;
     for (long long i = first; i < issued; ++i)
       grp::drain_wait(&s.full[i % STAGES], (uint32_t)((i / STAGES) & 1), args.wait_limit);
-  } else if (warp == 1 && lane == 0) {
-    // ---------------- MMA issuer
+  } else if (warp == 1) {
+    // ---------------- MMA issuer. The whole warp walks the loop and one lane issues: with operands in uniform
+    // registers an instruction takes a few cycles to issue; from a branch that one lane alone had taken, each
+    // descriptor went through vector registers first, about 48 cycles for each of the 16 of a K block.
     constexpr uint32_t IDESC = idesc_fp4<FMT>(BM, BN);
-    int stage = 0, n = 0;  // n: tiles of this CTA so far
-    uint32_t phase = 0;
+    const bool leader = elect_one();
+    int stage = 0, slot = 0, n = 0;  // n: tiles of this CTA so far
+    uint32_t phase = 0, sphase = 0;
     bool ok = true;
     for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x, ++n) {
       // the columns shared with the tile before have been read (and all of the tile before that one)
-      if (n > 0 && !wait_or_abort(&s.tfree, (uint32_t)(n - 1) & 1, &s.abort_flag, status, args.wait_limit)) break;
+      if (n > 0 && !__all_sync(0xffffffffu, wait_or_abort(&s.tfree, (uint32_t)(n - 1) & 1, &s.abort_flag, status,
+                                                          args.wait_limit)))
+        break;
       const uint32_t d = tmem_base + (n & 1 ? ACC1 : 0);
       for (int kb = 0; kb < kblocks; ++kb) {
-        if (!wait_or_abort(&s.full[stage], phase, &s.abort_flag, status, args.wait_limit)) {
+        const int in_slot = kb % kSlotBlocks<FMT>;
+        if (!__all_sync(0xffffffffu,
+                        (in_slot > 0 || wait_or_abort(&s.sfull[slot], sphase, &s.abort_flag, status, args.wait_limit)) &&
+                            wait_or_abort(&s.full[stage], phase, &s.abort_flag, status, args.wait_limit))) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t a = smem_u32(smem + stage * STAGE_BYTES);
-        const uint32_t b = a + A_BYTES, sfa = b + B_BYTES, sfb = sfa + SFA_BYTES;
-        // copies and MMAs of one thread run in order: the copies wait for the MMAs that read the columns
-        constexpr int kSteps = FMT == fp4::kNv ? 4 : 2;  // scale words of a K block
+        const uint32_t a = smem_u32(smem) + stage * STAGE_BYTES;
+        const uint32_t b = a + A_BYTES;
+        const uint32_t sf = slots + slot * SLOT_BYTES + in_slot * kWords<FMT> * 3 * 512;
+        const bool slot_done = in_slot == kSlotBlocks<FMT> - 1 || kb + 1 == kblocks;
+        if (leader) {
+          // copies and MMAs of one thread run in order: the copies wait for the MMAs that read the columns
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-          copy_scales(tmem_base + SFA_COL + 4 * i, scales_desc(sfa + 512 * i));
-          copy_scales(tmem_base + SFB_COL + 8 * i, scales_desc(sfb + 1024 * i));
-          copy_scales(tmem_base + SFB_COL + 8 * i + 4, scales_desc(sfb + 1024 * i + 512));
-        }
+          for (int i = 0; i < kWords<FMT>; ++i) {
+            copy_scales(tmem_base + SFA_COL + 4 * i, scales_desc(sf + 1536 * i));
+            copy_scales(tmem_base + SFB_COL + 8 * i, scales_desc(sf + 1536 * i + 512));
+            copy_scales(tmem_base + SFB_COL + 8 * i + 4, scales_desc(sf + 1536 * i + 1024));
+          }
 #pragma unroll
-        for (int kk = 0; kk < BK / 64; ++kk) {
-          const int w = FMT == fp4::kNv ? kk : kk / 2;             // word of the scales
-          const uint32_t id = FMT == fp4::kNv ? 0u : 2u * (kk & 1);  // bytes of it: all four, or a half
-          umma_fp4<FMT>(d, sw128_kmajor_desc(a + kk * 32), sw128_kmajor_desc(b + kk * 32),
-                        IDESC | id << 4 | id << 29, tmem_base + SFA_COL + 4 * w, tmem_base + SFB_COL + 8 * w,
-                        (kb | kk) != 0);
+          for (int kk = 0; kk < BK / 64; ++kk) {
+            const int w = FMT == fp4::kNv ? kk : kk / 2;             // word of the scales
+            const uint32_t id = FMT == fp4::kNv ? 0u : 2u * (kk & 1);  // bytes of it: all four, or a half
+            umma_fp4<FMT>(d, sw128_kmajor_desc(a + kk * 32), sw128_kmajor_desc(b + kk * 32),
+                          IDESC | id << 4 | id << 29, tmem_base + SFA_COL + 4 * w, tmem_base + SFB_COL + 8 * w,
+                          (kb | kk) != 0);
+          }
+          if (slot_done) umma_commit(&s.sempty[slot]);
+          umma_commit(&s.empty[stage]);
+          if (kb + 1 == kblocks) umma_commit(&s.tfull[n & 1]);
         }
-        umma_commit(&s.empty[stage]);
+        if (slot_done && ++slot == SLOTS) {
+          slot = 0;
+          sphase ^= 1;
+        }
         if (++stage == STAGES) {
           stage = 0;
           phase ^= 1;
         }
       }
-      if (ok) umma_commit(&s.tfull[n & 1]);
     }
-    umma_commit(&s.mma_done);
-    grp::drain_wait(&s.mma_done, 0, args.wait_limit);
+    if (leader) {
+      umma_commit(&s.mma_done);
+      grp::drain_wait(&s.mma_done, 0, args.wait_limit);
+    }
+    __syncwarp();
   } else if (warp >= SCALE_WARP0 && warp < EPI_WARP0) {
-    // ---------------- scale producers: warp w fills stage w, every STAGES-th K block of this CTA
-    const int w = warp - SCALE_WARP0;
+    // ---------------- scale producers: each warp half of the lines of one 128-row block (A, the first and the second of
+    // B). Lanes 2 i and 2 i + 1 hold the two 16-byte halves of the 32-byte sector of rows l, l + 32, l + 64, l + 96:
+    // whole sectors from L2, and one 16-byte line of shared memory for each word of the slot. Loads run two slots
+    // ahead of the stores, in registers.
+    const int unit = warp - SCALE_WARP0, block = unit >> 1;
+    const int line = (unit & 1) * 16 + (lane >> 1), part = lane & 1;
     const int pitch = args.K / fp4::kBlock<FMT>;
-    constexpr int kPer = BK / fp4::kBlock<FMT>;  // scales of a row's K block
-    constexpr int kWords = kPer / 4;
-    const uint32_t sfa = smem_u32(smem + w * STAGE_BYTES) + A_BYTES + B_BYTES + 16 * lane, sfb = sfa + SFA_BYTES;
-    int c0 = 0;  // K blocks of this CTA before the tile
+    const int per_tile = (kblocks + kSlotBlocks<FMT> - 1) / kSlotBlocks<FMT>;
+    const uint32_t dst = slots + (uint32_t)((4 * part * 3 + block) * 512 + 16 * line);
+    const uint8_t* p[4];
+    int load_tile = blockIdx.x, load_slot = 0;
+    auto fetch = [&](uint4 (&v)[4]) {
+      if (load_tile >= total) return;
+      if (load_slot == 0) {
+        const grp::Tile t = grp::decode(s.tb, G, args.n_tiles, load_tile, BM);
+        const bool routed = t.g < args.E;
+        const int64_t z = routed ? (args.slot_expert ? args.slot_expert[t.g] : t.g) : 0;
+        const int n0 = args.mode == 0 ? t.n_tile * (BN / 2) : t.n_tile * BN;
+        const int r0 = block == 0 ? t.a_row : block == 1 ? n0 : args.mode == 0 ? args.I + n0 : n0 + BN / 2;
+        const int rows = block == 0 ? args.a_rows : args.b_rows;
+        const uint8_t* base = block == 0 ? args.a_scales
+                                         : (routed ? args.b_scales : args.bs_scales) + z * args.b_rows * (int64_t)pitch;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)  // rows past the end take the last one's scales: they are not stored
+          p[i] = base + min(r0 + line + 32 * i, rows - 1) * (int64_t)pitch + 16 * part;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        v[i] = load_scales<VEC>(p[i] + load_slot * (4 * SLOT_WORDS), pitch - load_slot * (4 * SLOT_WORDS) - 16 * part);
+      if (++load_slot == per_tile) {
+        load_slot = 0;
+        load_tile += gridDim.x;
+      }
+    };
+    auto store = [&](const uint4 (&v)[4], int slot, uint32_t phase) {
+      const int got = wait_or_abort(&s.sempty[slot], phase ^ 1, &s.abort_flag, status, args.wait_limit);
+      if (!__all_sync(0xffffffffu, got)) return false;
+      const uint32_t at = dst + slot * SLOT_BYTES;
+      sts128(at, v[0].x, v[1].x, v[2].x, v[3].x);
+      sts128(at + 1536, v[0].y, v[1].y, v[2].y, v[3].y);
+      sts128(at + 2 * 1536, v[0].z, v[1].z, v[2].z, v[3].z);
+      sts128(at + 3 * 1536, v[0].w, v[1].w, v[2].w, v[3].w);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.sfull[slot]);
+      return true;
+    };
+    const int tiles = blockIdx.x < total ? (total - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
+    const int64_t fills = (int64_t)tiles * per_tile;
+    uint4 v0[4], v1[4];
+    fetch(v0);
+    fetch(v1);
     uint32_t phase = 0;
-    bool ok = true;
-    for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x, c0 += kblocks) {
-      const grp::Tile t = grp::decode(s.tb, G, args.n_tiles, tile, BM);
-      const bool routed = t.g < args.E;
-      const int64_t z = routed ? (args.slot_expert ? args.slot_expert[t.g] : t.g) : 0;
-      const int n0 = args.mode == 0 ? t.n_tile * (BN / 2) : t.n_tile * BN;
-      const int n1 = args.mode == 0 ? args.I + n0 : n0 + BN / 2;
-      const uint8_t* bs = (routed ? args.b_scales : args.bs_scales) + z * args.b_rows * (int64_t)pitch;
-      const uint8_t* p[12];  // rows past the end take the last one's scales: they are not stored
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        p[i] = args.a_scales + min(t.a_row + lane + 32 * i, args.a_rows - 1) * (int64_t)pitch;
-        p[4 + i] = bs + min(n0 + lane + 32 * i, args.b_rows - 1) * (int64_t)pitch;
-        p[8 + i] = bs + min(n1 + lane + 32 * i, args.b_rows - 1) * (int64_t)pitch;
-      }
-      for (int kb = (w - c0) & (STAGES - 1); kb < kblocks; kb += STAGES) {
-        uint32_t v[12][kWords];
-#pragma unroll
-        for (int i = 0; i < 12; ++i) load_scales<FMT, VEC>(p[i] + kb * kPer, pitch - kb * kPer, v[i]);
-        const int got = wait_or_abort(&s.empty[w], phase ^ 1, &s.abort_flag, status, args.wait_limit);
-        if (__any_sync(0xffffffffu, !got)) {
-          ok = false;
-          break;
-        }
-        phase ^= 1;
-#pragma unroll
-        for (int j = 0; j < kWords; ++j) {
-          sts128(sfa + 512 * j, v[0][j], v[1][j], v[2][j], v[3][j]);
-          sts128(sfb + 1024 * j, v[4][j], v[5][j], v[6][j], v[7][j]);
-          sts128(sfb + 1024 * j + 512, v[8][j], v[9][j], v[10][j], v[11][j]);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s.full[w]);
-      }
+    static_assert(SLOTS == 2, "the two register sets are the two slots");
+    for (int64_t i = 0; i < fills; i += 2, phase ^= 1) {
+      if (!store(v0, 0, phase)) break;
+      fetch(v0);
+      if (i + 1 == fills || !store(v1, 1, phase)) break;
+      fetch(v1);
     }
   } else if (warp >= EPI_WARP0) {
     // ---------------- epilogue
@@ -388,12 +438,19 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int i = half; i < chunks; i += 2) {
         const int c = 32 * (n & 1 ? i : chunks - 1 - i);
         if (args.mode == 0) {
-          uint32_t gate[32], up[32];
+          float h[32];
           if (any) {
-            tmem_ld32(tacc + c, gate);
-            tmem_ld32(tacc + BN / 2 + c, up);
-            tmem_ld_wait_regs(gate);
-            tmem_ld_wait_regs(up);
+#pragma unroll
+            for (int j0 = 0; j0 < 32; j0 += 16) {
+              uint32_t gate[16], up[16];
+              tmem_ld16(tacc + c + j0, gate);
+              tmem_ld16(tacc + BN / 2 + c + j0, up);
+              tmem_ld_wait_regs(gate);
+              tmem_ld_wait_regs(up);
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                h[j0 + j] = grp::silu(__uint_as_float(gate[j]) * scale) * (__uint_as_float(up[j]) * scale);
+            }
           }
           if (i < 2) {
             tc_fence_before();
@@ -401,10 +458,6 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (lane == 0) mbar_arrive(&s.tfree);
           }
           if (!any) continue;
-          float h[32];
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            h[j] = grp::silu(__uint_as_float(gate[j]) * scale) * (__uint_as_float(up[j]) * scale);
           uint32_t q[4], sc = 0;
           constexpr int kBlk = fp4::kBlock<FMT>;
 #pragma unroll
@@ -528,8 +581,8 @@ cudaError_t launch_gemm_a4(const GemmA4Desc& d, cudaStream_t stream, std::string
   a.row_weight = d.row_weight;
   a.status = d.status;
   a.wait_limit = 4000000000LL;  // about two seconds of SM clock
-  // a row's scales of a K block are one aligned load where rows of scales are whole numbers of them
-  const bool vec = d.K % a4::BK == 0;
+  // rows of scales that are whole 16-byte pieces are loaded as such, others byte by byte
+  const bool vec = d.K / (d.format == fp4::kNv ? fp4::kBlock<fp4::kNv> : fp4::kBlock<fp4::kMx>) % 16 == 0;
   kernels[(d.format == fp4::kNv ? 0 : 2) + (vec ? 0 : 1)]<<<num_sms(), a4::THREADS, a4::SMEM_BYTES, stream>>>(tA, tA32,
                                                                                                              tB, tBs, a);
   return cudaGetLastError();
