@@ -543,10 +543,13 @@ cudaError_t launch_gemm_a4(const GemmA4Desc& d, cudaStream_t stream, std::string
   }
   CUtensorMap tA, tA32, tB, tBs;
   const CUtensorMapDataType U8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-  const bool ok = tma_encode_2d(&tA, d.A, U8, 1, d.a_rows, d.K / 2, a4::BM) &&
-                  tma_encode_2d(&tA32, d.A, U8, 1, d.a_rows, d.K / 2, a4::BM / 4) &&
-                  tma_encode_3d(&tB, d.B, U8, 1, d.n_experts, d.b_rows, d.K / 2, a4::BN / 2) &&
-                  tma_encode_3d(&tBs, d.B_shared ? d.B_shared : d.B, U8, 1, 1, d.b_rows, d.K / 2, a4::BN / 2);
+  // an encode costs a small call about a microsecond: a map that no tile uses is a copy of another
+  bool ok = tma_encode_2d(&tA32, d.A, U8, 1, d.a_rows, d.K / 2, a4::BM / 4) &&
+            tma_encode_3d(&tB, d.B, U8, 1, d.n_experts, d.b_rows, d.K / 2, a4::BN / 2);
+  tA = tA32;
+  tBs = tB;
+  if (d.a_rows > a4::BM - 32) ok = ok && tma_encode_2d(&tA, d.A, U8, 1, d.a_rows, d.K / 2, a4::BM);
+  if (d.B_shared) ok = ok && tma_encode_3d(&tBs, d.B_shared, U8, 1, 1, d.b_rows, d.K / 2, a4::BN / 2);
   if (!ok) {
     *err = "cuTensorMapEncodeTiled rejected a 4-bit GEMM operand";
     return cudaErrorInvalidValue;

