@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(256) gather_fp4_kernel(const uint4* __restrict
                                                          const float* __restrict__ g, int T, int h, int k, int R,
                                                          int shared) {
   const int lane = threadIdx.x & 31;
-  const float gs = g ? *g : 1.0f;
+  const fp4::Scale gs(FMT == fp4::kNv ? g : nullptr);
   const int64_t warps = (gridDim.x * blockDim.x) >> 5;
   const int64_t items = (int64_t)T * fp8_items_per_row(h);
   for (int64_t it = (blockIdx.x * blockDim.x + threadIdx.x) >> 5; it < items; it += warps)

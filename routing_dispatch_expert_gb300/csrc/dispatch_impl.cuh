@@ -114,7 +114,7 @@ __device__ __forceinline__ void gather_fp8_item(const uint4* __restrict__ x, con
 // to the token's k rows (and the shared expert's row).
 template <int FMT>
 __device__ __forceinline__ void gather_fp4_item(const uint4* __restrict__ x, const int32_t* __restrict__ inv_pos,
-                                                uint32_t* __restrict__ xq, uint8_t* __restrict__ xs, float g, int h,
+                                                uint32_t* __restrict__ xq, uint8_t* __restrict__ xs, const fp4::Scale& g, int h,
                                                 int k, int R, int shared, int64_t it, int lane) {
   const int per = fp8_items_per_row(h);
   const int64_t t = it / per;
@@ -123,18 +123,17 @@ __device__ __forceinline__ void gather_fp4_item(const uint4* __restrict__ x, con
   const int c0 = (int)(it - t * per) * (kFp8ItemElems / 8);
   const int my_row = lane < k ? inv_pos[t * k + lane] : -1;
   const uint4* src = x + t * hv;
-  uint4 v[4];
+  fp4::Eight<MOE_TYPE_BF16> v[4];
 #pragma unroll
   for (int u = 0; u < 4; ++u)
-    if (c0 + 32 * u < hv) v[u] = src[c0 + lane + 32 * u];  // h % 256 == 0: a pass is whole
+    if (c0 + 32 * u < hv) v[u].w = src[c0 + lane + 32 * u];  // h % 256 == 0: a pass is whole
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const int c = c0 + lane + 32 * u;
     if (c0 + 32 * u >= hv) break;
-    const float f[8] = {bf16_lo(v[u].x), bf16_hi(v[u].x), bf16_lo(v[u].y), bf16_hi(v[u].y),
-                        bf16_lo(v[u].z), bf16_hi(v[u].z), bf16_lo(v[u].w), bf16_hi(v[u].w)};
-    float by;
-    const uint32_t scale = fp4::block_scale<FMT>(fp4::block_amax<FMT>(fp4::amax8<FMT>(f)), g, by);
+    float by, f[8];
+    v[u].values(f);
+    const uint32_t scale = fp4::block_scale<FMT>(fp4::block_amax<FMT>(v[u].amax()), g, by);
     const uint32_t q = fp4::codes8<FMT>(f, by);
     for (int j = 0; j <= k; ++j) {
       int r;

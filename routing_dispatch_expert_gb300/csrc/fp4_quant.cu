@@ -3,6 +3,8 @@
 // One pass over the rows: a lane holds 8 consecutive elements, so a warp's loads (16 or 32 bytes a lane)
 // and stores (4 bytes of codes a lane) are contiguous; a block of 16 or 32 elements is 2 or 4 lanes,
 // which share its largest magnitude by shuffles. HBM-bound.
+#include <type_traits>
+
 #include "common.cuh"
 #include "fp4_impl.cuh"
 #include "kernels.h"
@@ -12,78 +14,83 @@ namespace fp4 {
 
 constexpr int kThreads = 256;
 
-template <int TYPE>  // MOE_TYPE_*
-__device__ __forceinline__ void load8(const void* p, int64_t at, float* v) {
-  if (TYPE == MOE_TYPE_F32) {
-    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
-    const float4 a = q[0], b = q[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    return;
-  }
-  const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (TYPE == MOE_TYPE_BF16) {
-      v[2 * i] = bf16_lo(u[i]);
-      v[2 * i + 1] = bf16_hi(u[i]);
-    } else {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
-      v[2 * i] = f.x;
-      v[2 * i + 1] = f.y;
-    }
-  }
-}
+// A thread has kUnits units of 8 elements, kThreads apart: their loads are all in flight together.
+constexpr int kUnits = 4;
 
-// One thread per 8 elements; `per_row` of them a row (a multiple of 4: blocks never straddle a warp).
-template <int FMT, int TYPE>
+// `per_row` units a row (a multiple of 4: blocks never straddle a warp); PACKED: rows follow one another.
+template <int FMT, int TYPE, bool PACKED>
 __global__ void __launch_bounds__(kThreads) quantize_kernel(const void* __restrict__ x, int64_t ldx, uint32_t units,
                                                             uint32_t per_row, const float* __restrict__ g,
                                                             uint32_t* __restrict__ q, uint8_t* __restrict__ s) {
-  const uint32_t u = blockIdx.x * kThreads + threadIdx.x;
-  const bool in = u < units;
-  const float gs = g ? *g : 1.0f;
-  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (in) {
-    const uint32_t row = u / per_row;
-    load8<TYPE>(x, row * ldx + 8 * (int64_t)(u - row * per_row), v);
+  const uint32_t u0 = blockIdx.x * (kThreads * kUnits) + threadIdx.x;
+  const Scale gs(FMT == kNv ? g : nullptr);
+  Eight<TYPE> x8[kUnits];
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    const uint32_t u = u0 + i * kThreads;
+    if (u < units) {
+      const uint32_t row = PACKED ? 0 : u / per_row;
+      x8[i].load(x, row * ldx + 8 * (int64_t)(u - row * per_row));
+    } else {
+      x8[i].clear();
+    }
   }
-  const uint32_t m = block_amax<FMT>(amax8<FMT>(v));
-  if (!in) return;
-  float by;
-  const uint32_t code = block_scale<FMT>(m, gs, by);
-  q[u] = codes8<FMT>(v, by);
-  constexpr uint32_t kLanes = kBlock<FMT> / 8;
-  if (u % kLanes == 0) s[u / kLanes] = (uint8_t)code;
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    const uint32_t u = u0 + i * kThreads;
+    const uint32_t m = block_amax<FMT>(x8[i].amax());
+    if (u >= units) continue;
+    float by, v[8];
+    x8[i].values(v);
+    const uint32_t code = block_scale<FMT>(m, gs, by);
+    q[u] = codes8<FMT>(v, by);
+    constexpr uint32_t kLanes = kBlock<FMT> / 8;
+    if (u % kLanes == 0) s[u / kLanes] = (uint8_t)code;
+  }
 }
 
-template <int FMT, int TYPE>
+template <int FMT, int TYPE, bool WIDE>
 __global__ void __launch_bounds__(kThreads) dequantize_kernel(const uint32_t* __restrict__ q,
                                                               const uint8_t* __restrict__ s,
                                                               const float* __restrict__ g, uint32_t units,
                                                               void* __restrict__ y) {
-  const uint32_t u = blockIdx.x * kThreads + threadIdx.x;
-  if (u >= units) return;
-  const uint32_t b = s[u / (kBlock<FMT> / 8)];
-  float v[8];
-  values8(q[u], FMT == kNv ? e4m3_value(b) : e8m0_value(b), FMT == kNv && g ? *g : 1.0f, v);
-  if (TYPE == MOE_TYPE_F32) {
-    float4* o = reinterpret_cast<float4*>(static_cast<float*>(y) + 8 * (int64_t)u);
-    o[0] = make_float4(v[0], v[1], v[2], v[3]);
-    o[1] = make_float4(v[4], v[5], v[6], v[7]);
-    return;
-  }
-  uint32_t w[4];
+  const uint32_t u0 = blockIdx.x * (kThreads * kUnits) + threadIdx.x;
+  const float gs = FMT == kNv && g ? *g : 1.0f;
+  uint32_t c[kUnits], b[kUnits];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (TYPE == MOE_TYPE_BF16) {
-      w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-    } else {
-      const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
+  for (int i = 0; i < kUnits; ++i) {
+    const uint32_t u = u0 + i * kThreads;
+    c[i] = u < units ? q[u] : 0;
+    b[i] = u < units ? s[u / (kBlock<FMT> / 8)] : 0;
   }
-  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(y) + 8 * (int64_t)u) = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    const uint32_t u = u0 + i * kThreads;
+    if (u >= units) return;
+    float v[8];
+    values8(c[i], FMT == kNv ? e4m3_value(b[i]) : e8m0_value(b[i]), gs, v);
+    if (TYPE == MOE_TYPE_F32) {
+      float* o = static_cast<float*>(y) + 8 * (int64_t)u;
+      if (WIDE) {
+        st_global_v8(o, reinterpret_cast<const uint32_t*>(v));
+      } else {  // y is 16-byte but not 32-byte aligned
+        reinterpret_cast<float4*>(o)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4*>(o)[1] = make_float4(v[4], v[5], v[6], v[7]);
+      }
+      continue;
+    }
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (TYPE == MOE_TYPE_BF16) {
+        w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+      } else {
+        const __half2 h = __floats2half2_rn(v[2 * j], v[2 * j + 1]);
+        w[j] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(y) + 8 * (int64_t)u) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
 }
 
 }  // namespace fp4
@@ -92,40 +99,47 @@ cudaError_t launch_quantize_fp4(const void* x, int type, int64_t rows, int64_t c
                                 const float* g, void* q, void* s, cudaStream_t stream) {
   if (rows == 0 || cols == 0) return cudaSuccess;
   const uint32_t per_row = (uint32_t)(cols / 8), units = (uint32_t)(rows * (cols / 8));
-  const uint32_t blocks = (uint32_t)cdiv(units, fp4::kThreads);
+  const uint32_t blocks = (uint32_t)cdiv(units, fp4::kThreads * fp4::kUnits);
   auto go = [&](auto kernel) {
     kernel<<<blocks, fp4::kThreads, 0, stream>>>(x, ldx, units, per_row, g, static_cast<uint32_t*>(q),
                                                  static_cast<uint8_t*>(s));
     return cudaGetLastError();
   };
   using namespace fp4;
-  if (format == kNv)
-    return type == MOE_TYPE_F32    ? go(quantize_kernel<kNv, MOE_TYPE_F32>)
-           : type == MOE_TYPE_BF16 ? go(quantize_kernel<kNv, MOE_TYPE_BF16>)
-                                   : go(quantize_kernel<kNv, MOE_TYPE_F16>);
-  return type == MOE_TYPE_F32    ? go(quantize_kernel<kMx, MOE_TYPE_F32>)
-         : type == MOE_TYPE_BF16 ? go(quantize_kernel<kMx, MOE_TYPE_BF16>)
-                                 : go(quantize_kernel<kMx, MOE_TYPE_F16>);
+  auto pick = [&](auto format_c, auto type_c) {
+    constexpr int F = decltype(format_c)::value, T = decltype(type_c)::value;
+    return rows == 1 || ldx == cols ? go(quantize_kernel<F, T, true>) : go(quantize_kernel<F, T, false>);
+  };
+  using std::integral_constant;
+  auto with_type = [&](auto format_c) {
+    return type == MOE_TYPE_F32    ? pick(format_c, integral_constant<int, MOE_TYPE_F32>{})
+           : type == MOE_TYPE_BF16 ? pick(format_c, integral_constant<int, MOE_TYPE_BF16>{})
+                                   : pick(format_c, integral_constant<int, MOE_TYPE_F16>{});
+  };
+  return format == kNv ? with_type(integral_constant<int, kNv>{}) : with_type(integral_constant<int, kMx>{});
 }
 
 cudaError_t launch_dequantize_fp4(const void* q, const void* s, const float* g, int64_t rows, int64_t cols, int format,
                                   int type, void* y, cudaStream_t stream) {
   if (rows == 0 || cols == 0) return cudaSuccess;
   const uint32_t units = (uint32_t)(rows * (cols / 8));
-  const uint32_t blocks = (uint32_t)cdiv(units, fp4::kThreads);
+  const uint32_t blocks = (uint32_t)cdiv(units, fp4::kThreads * fp4::kUnits);
   auto go = [&](auto kernel) {
     kernel<<<blocks, fp4::kThreads, 0, stream>>>(static_cast<const uint32_t*>(q), static_cast<const uint8_t*>(s), g,
                                                  units, y);
     return cudaGetLastError();
   };
   using namespace fp4;
-  if (format == kNv)
-    return type == MOE_TYPE_F32    ? go(dequantize_kernel<kNv, MOE_TYPE_F32>)
-           : type == MOE_TYPE_BF16 ? go(dequantize_kernel<kNv, MOE_TYPE_BF16>)
-                                   : go(dequantize_kernel<kNv, MOE_TYPE_F16>);
-  return type == MOE_TYPE_F32    ? go(dequantize_kernel<kMx, MOE_TYPE_F32>)
-         : type == MOE_TYPE_BF16 ? go(dequantize_kernel<kMx, MOE_TYPE_BF16>)
-                                 : go(dequantize_kernel<kMx, MOE_TYPE_F16>);
+  using std::integral_constant;
+  auto with_type = [&](auto format_c) {
+    constexpr int F = decltype(format_c)::value;
+    if (type == MOE_TYPE_F32)
+      return reinterpret_cast<uintptr_t>(y) % 32 == 0 ? go(dequantize_kernel<F, MOE_TYPE_F32, true>)
+                                                      : go(dequantize_kernel<F, MOE_TYPE_F32, false>);
+    return type == MOE_TYPE_BF16 ? go(dequantize_kernel<F, MOE_TYPE_BF16, false>)
+                                 : go(dequantize_kernel<F, MOE_TYPE_F16, false>);
+  };
+  return format == kNv ? with_type(integral_constant<int, kNv>{}) : with_type(integral_constant<int, kMx>{});
 }
 
 }  // namespace moe

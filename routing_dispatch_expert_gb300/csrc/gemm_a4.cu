@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int r = quarter * 32 + lane;
     const uint32_t tq = tmem_base + ((uint32_t)(quarter * 32) << 16);
     const float ag = args.a_g ? *args.a_g : 1.0f;
-    const float hg = args.out_g ? *args.out_g : 1.0f;
+    const fp4::Scale hg(args.mode == 0 ? args.out_g : nullptr);
     const int chunks = args.mode == 0 ? 4 : 8;  // of 32 output columns
     int n = 0;
     for (int tile = blockIdx.x; tile < total; tile += gridDim.x, ++n) {
