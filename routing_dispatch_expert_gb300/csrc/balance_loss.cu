@@ -45,9 +45,16 @@ struct Args {
   int32_t* tokens; // [S]
 };
 
+// flushing to zero costs nothing here (what underflows is below 1e-38 of the row's largest) and saves the scaling
+// around either instruction
 __device__ __forceinline__ float ex2(float x) {
   float r;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float reciprocal(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 
@@ -118,37 +125,45 @@ __device__ __forceinline__ float lanes_sum(float v) {
   return v;
 }
 
-// l becomes the row's probabilities; with DERIV d becomes 1 - sigmoid(l). The exponent x = l - m is
-// rounded twice before ex2.approx (2 ulp): a relative error of at most |x| 2^-23 + 2^-22, 3e-6 down to
-// probabilities of 1e-8 of the largest. A row of nothing but -inf has z = 0: no shift, no probabilities;
-// a NaN makes the whole row NaN.
+// l becomes w, and 1 / sum w is returned: the probabilities are w times it. With DERIV d becomes 1 - sigmoid(l).
+// The exponent is one fused multiply-add, fma(l, log2 e, -c log2 e): its own rounding is |x| 2^-24 for an exponent
+// x, that of c log2 e is the same for the whole row and cancels; ex2.approx and rcp.approx add 2 ulp and 1. In all
+// below 2e-6 down to probabilities of 1e-8 of the largest. Rows near the type's lowest value, where c log2 e would
+// overflow, are shifted first. A row of nothing but -inf has a sum of 0 and no probabilities; a NaN makes its
+// whole row NaN.
 template <bool SIGMOID, bool DERIV, int L, int EPL>
-__device__ __forceinline__ void probabilities(float (&l)[EPL], float (&d)[DERIV ? EPL : 1]) {
+__device__ __forceinline__ float weights(float (&l)[EPL], float (&d)[DERIV ? EPL : 1]) {
   float m = l[0];
 #pragma unroll
   for (int i = 1; i < EPL; ++i) m = fmaxf(m, l[i]);
   m = lanes_max<L>(m);
   float c = m == -INFINITY ? 0.f : m;
   if (SIGMOID) c = fminf(c, 0.f);
-  const float ec = SIGMOID ? ex2(c * kLog2e) : 0.f;
+  float ec = 0.f;
+  if (fabsf(c) > 1e30f) {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) l[i] -= c;
+    c = 0.f;  // and e^c is 0
+  } else if (SIGMOID) {
+    ec = ex2(c * kLog2e);
+  }
+  const float c2 = c * kLog2e;
   float z = 0.f;
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
     if (SIGMOID) {
-      const float u = ex2((c - l[i]) * kLog2e);  // inf for l = -inf: w = 0
-      const float w = __fdividef(1.0f, ec + u);
+      const float u = ex2(fmaf(l[i], -kLog2e, c2));  // e^(c - l); inf for l = -inf: w = 0
+      const float w = reciprocal(ec + u);
       // 1 - sigmoid = e^-l / (1 + e^-l); 1 in fp32 once u > 2^25, where u * w could be inf * 0
       if (DERIV) d[i] = u < 1e30f ? u * w : 1.0f;
       l[i] = w;
     } else {
-      l[i] = ex2((l[i] - c) * kLog2e);
+      l[i] = ex2(fmaf(l[i], kLog2e, -c2));
     }
     z += l[i];
   }
   z = lanes_sum<L>(z);
-  const float r = z == 0.f ? 0.f : __fdiv_rn(1.0f, z);
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) l[i] *= r;
+  return z == 0.f ? 0.f : __fdividef(1.0f, z);
 }
 
 // loss, counts, mean and token count of sequence s from its sums: called by all threads of a block
@@ -191,6 +206,7 @@ __global__ void __launch_bounds__(kThreads, EPL > 8 ? 1 : 2) forward_kernel(cons
   __shared__ int n_seq_tokens;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % L;
   const int b0 = blockIdx.x * a.per_block, b1 = min(a.T, b0 + a.per_block);
+  if (!SINGLE) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   for (int s = SINGLE ? 0 : seq_of(a.offsets, a.S, a.T, b0); s < a.S; ++s) {
     const int begin = seq_begin(a.offsets, s, a.S, a.T);
     if (!SINGLE && begin >= b1) break;
@@ -199,6 +215,15 @@ __global__ void __launch_bounds__(kThreads, EPL > 8 ? 1 : 2) forward_kernel(cons
     float acc[EPL], cur[EPL], none[1];
 #pragma unroll
     for (int i = 0; i < EPL; ++i) acc[i] = 0.f;
+    // probabilities: the next token's logits are loaded before this one's are worked on (the first before the counts)
+    auto fetch = [&](int base, float (&l)[EPL]) {
+      const int t = base + lane / L;
+      const bool in = t < hi && (!a.mask || a.mask[t]);
+      if (in) load_row<BF16, L, EPL>(a.logits, t, a.E, sub, l);
+      return in;
+    };
+    int base = lo + warp * PER_WARP;
+    bool in = base < hi && fetch(base, cur);
     for (int e = threadIdx.x; e < a.E; e += kThreads) hist[e] = 0;
     if (threadIdx.x == 0) n_seq_tokens = 0;
     __syncthreads();
@@ -214,25 +239,17 @@ __global__ void __launch_bounds__(kThreads, EPL > 8 ? 1 : 2) forward_kernel(cons
     }
     n = __reduce_add_sync(0xffffffffu, n);
     if (lane == 0 && n) atomicAdd(&n_seq_tokens, n);
-    // probabilities: the next token's logits are loaded before this one's are worked on
-    auto fetch = [&](int base, float (&l)[EPL]) {
-      const int t = base + lane / L;
-      const bool in = t < hi && (!a.mask || a.mask[t]);
-      if (in) load_row<BF16, L, EPL>(a.logits, t, a.E, sub, l);
-      return in;
-    };
-    int base = lo + warp * PER_WARP;
-    bool in = base < hi && fetch(base, cur);
     for (; base < hi; base += STRIDE) {
       float l[EPL];
       const bool now = in;
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) l[i] = now ? cur[i] : -INFINITY;
+      for (int i = 0; i < EPL; ++i) l[i] = L == 32 || now ? cur[i] : -INFINITY;
       in = base + STRIDE < hi && fetch(base + STRIDE, cur);
-      probabilities<SIGMOID, false, L, EPL>(l, none);
-      if (now) {
+      if (L == 32 && !now) continue;  // the whole warp
+      const float r = weights<SIGMOID, false, L, EPL>(l, none);
+      if (L == 32 || now) {
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) acc[i] += l[i];
+        for (int i = 0; i < EPL; ++i) acc[i] = fmaf(l[i], r, acc[i]);
       }
     }
     // tokens of the warp, then warps w and w + 8, then warps 0 .. 7
@@ -272,49 +289,52 @@ __global__ void __launch_bounds__(kThreads, EPL > 8 ? 1 : 2) forward_kernel(cons
   }
 }
 
-// The results of one sequence from its blocks' sums: a cluster of blocks a sequence, each with a part of
-// the experts, and within a block 32 lanes of experts times 32 warps of entries (S = 1 has hundreds).
+// The results of one sequence from its blocks' sums: `ranks` blocks a sequence (a cluster), each with `per` of the
+// experts; a block's threads are experts times groups of entries. More blocks only where a sequence has many
+// entries (one of 65536 tokens has 304). The kernel is launched beside the first one's end and waits for its
+// results here.
 constexpr int kFinishThreads = 1024;
-__global__ void __launch_bounds__(kFinishThreads) finish_kernel(const Args a) {
-  __shared__ float sums[32][33];
-  __shared__ int cnts[32][33];
+__global__ void __launch_bounds__(kFinishThreads) finish_kernel(const Args a, int ranks, int per) {
+  __shared__ float sums[kFinishThreads];
+  __shared__ int cnts[kFinishThreads];
   __shared__ float red[32];
   __shared__ float dot_part;
   __shared__ int n_tokens;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rank = (int)cluster_ctarank(), ranks = (int)gridDim.x / a.S;
-  const int s = blockIdx.x / ranks;
+  const int s = blockIdx.x / ranks, rank = blockIdx.x - s * ranks;
   const int begin = seq_begin(a.offsets, s, a.S, a.T), end = seq_begin(a.offsets, s + 1, a.S, a.T);
   const int f = begin / a.per_block, l = end > begin ? (end - 1) / a.per_block : f - 1;  // first, last block
+  const int groups = kFinishThreads / per, group = threadIdx.x / per;
+  const int e = rank * per + threadIdx.x % per;
   if (threadIdx.x == 0) n_tokens = 0;
-  __syncthreads();
-  int n = 0;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  float sum = 0.f;
+  int cnt = 0, n = 0;
+  if (e < a.E) {
+#pragma unroll 4
+    for (int b = f + group; b <= l; b += groups) {
+      sum += a.psum[((int64_t)b + s) * a.E + e];
+      cnt += a.pcnt[((int64_t)b + s) * a.E + e];
+    }
+  }
   for (int b = f + threadIdx.x; b <= l; b += kFinishThreads) n += a.pn[b + s];
-  n = __reduce_add_sync(0xffffffffu, n);
-  if (lane == 0 && n) atomicAdd(&n_tokens, n);
+  sums[threadIdx.x] = sum;
+  cnts[threadIdx.x] = cnt;
+  __syncthreads();
+  if (n) atomicAdd(&n_tokens, n);
   __syncthreads();
   float dot = 0.f;
-  for (int e0 = 32 * rank; e0 < a.E; e0 += 32 * ranks) {
-    const int e = e0 + lane;
-    float sum = 0.f;
-    int cnt = 0;
-    if (e < a.E) {
-#pragma unroll 4
-      for (int b = f + warp; b <= l; b += 32) {
-        sum += a.psum[((int64_t)b + s) * a.E + e];
-        cnt += a.pcnt[((int64_t)b + s) * a.E + e];
-      }
+  if (group == 0 && e < a.E) {
+    for (int g = 1; g < groups; ++g) {
+      sum += sums[g * per + threadIdx.x];
+      cnt += cnts[g * per + threadIdx.x];
     }
-    sums[warp][lane] = sum;
-    cnts[warp][lane] = cnt;
-    __syncthreads();
-    // warp w joins the 32 entries' sums of expert e0 + w
-    sum = lanes_sum<32>(sums[lane][warp]);
-    cnt = __reduce_add_sync(0xffffffffu, cnts[lane][warp]);
-    if (lane == 0 && e0 + warp < a.E) dot += finish_expert(a, s, e0 + warp, sum, cnt, n_tokens);
-    __syncthreads();
+    dot = finish_expert(a, s, e, sum, cnt, n_tokens);
   }
   dot = block_sum<32>(dot, red);
+  if (ranks == 1) {
+    if (threadIdx.x == 0) finish_loss(a, s, dot, n_tokens);
+    return;
+  }
   if (threadIdx.x == 0) dot_part = dot;
   cluster_sync();
   if (rank == 0 && threadIdx.x == 0) {
@@ -373,13 +393,13 @@ __global__ void __launch_bounds__(kThreads, EPL > 8 ? 1 : 2) backward_kernel(con
     float l[EPL], d[SIGMOID ? EPL : 1];
     const bool now = in;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) l[i] = now ? cur[i] : -INFINITY;
+    for (int i = 0; i < EPL; ++i) l[i] = L == 32 || now ? cur[i] : -INFINITY;
     in = base + STRIDE < b1 && fetch(base + STRIDE, cur);
-    probabilities<SIGMOID, SIGMOID, L, EPL>(l, d);
+    const float r = weights<SIGMOID, SIGMOID, L, EPL>(l, d);
     float dot = 0.f;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) dot = fmaf(l[i], g[i], dot);
-    dot = lanes_sum<L>(dot);
+    dot = lanes_sum<L>(dot) * r;
     if (t >= b1) continue;
     const bool zero = !now || !covered;  // padding, or a token of no sequence: whatever its logits hold
 #pragma unroll
@@ -388,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, EPL > 8 ? 1 : 2) backward_kernel(con
       float o[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float v = l[4 * j + i] * (g[4 * j + i] - dot);
+        const float v = l[4 * j + i] * r * (g[4 * j + i] - dot);
         o[i] = zero ? 0.f : SIGMOID ? v * d[SIGMOID ? 4 * j + i : 0] : v;
       }
       const int64_t at = (int64_t)t * a.E + e;
@@ -480,21 +500,26 @@ cudaError_t launch_balance_loss(const BalanceLossDesc& d, int* launches, cudaStr
   });
   *launches = 1;
   if (e != cudaSuccess || single) return e;
-  unsigned ranks = 1;
-  while (ranks < 8 && (int)(32 * ranks) < d.E) ranks *= 2;
+  int wide = 32;  // experts rounded up to a power of two, and those of a block
+  while (wide < d.E) wide *= 2;
+  const int64_t each = cdiv(blocks, d.S) + 1;  // entries of a sequence
+  int ranks = 1;
+  while (ranks < 8 && wide / ranks > 32 && each > 8 * (bl::kFinishThreads / (wide / ranks))) ranks *= 2;
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ranks;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3((unsigned)d.S * ranks);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)ranks;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)d.S * (unsigned)ranks);
   cfg.blockDim = dim3(bl::kFinishThreads);
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = ranks > 1 ? 2 : 1;
   *launches = 2;
-  return cudaLaunchKernelEx(&cfg, bl::finish_kernel, a);
+  return cudaLaunchKernelEx(&cfg, bl::finish_kernel, a, ranks, wide / ranks);
 }
 
 cudaError_t launch_balance_loss_backward(const BalanceLossBackwardDesc& d, cudaStream_t stream) {
