@@ -84,36 +84,53 @@ __device__ __forceinline__ int seq_of(const int32_t* offsets, int S, int T, int 
   return lo;
 }
 
-template <bool BF16>
-__device__ __forceinline__ float load1(const void* p, int64_t i) {
-  if (BF16) return __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i] << 16);
-  return static_cast<const float*>(p)[i];
-}
-
-// This lane's experts of a token: 4 (sub + L j) + i, j < EPL / 4, i < 4. Past E: -inf.
+// This lane's experts of a token, 4 (sub + L j) + i (j < EPL / 4, i < 4), as they lie in memory: nothing is done
+// with them until values(), so that the loads of a token are in flight while another one is worked on.
 template <bool BF16, int L, int EPL>
-__device__ __forceinline__ void load_row(const void* logits, int64_t row, int E, int sub, float (&l)[EPL]) {
-  const bool vec = (E & 3) == 0;
+struct Row {
+  uint32_t w[BF16 ? EPL / 2 : EPL];
+  __device__ __forceinline__ void load(const void* logits, int64_t row, int E, int sub) {
+    const bool vec = (E & 3) == 0;
 #pragma unroll
-  for (int j = 0; j < EPL / 4; ++j) {
-    const int e = 4 * (sub + L * j);
-    if (vec && e < E) {
+    for (int j = 0; j < EPL / 4; ++j) {
+      const int e = 4 * (sub + L * j);
+      const int64_t at = row * E + e;
       if (BF16) {
-        const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(logits) + row * E + e);
-        l[4 * j] = bf16_lo(v.x), l[4 * j + 1] = bf16_hi(v.x), l[4 * j + 2] = bf16_lo(v.y), l[4 * j + 3] = bf16_hi(v.y);
-      } else {
-        const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(logits) + row * E + e);
-        l[4 * j] = v.x, l[4 * j + 1] = v.y, l[4 * j + 2] = v.z, l[4 * j + 3] = v.w;
-      }
-    } else {
+        const uint16_t* p = static_cast<const uint16_t*>(logits) + at;
+        if (vec && e < E) {
+          const uint2 v = *reinterpret_cast<const uint2*>(p);
+          w[2 * j] = v.x, w[2 * j + 1] = v.y;
+        } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) l[4 * j + i] = e + i < E ? load1<BF16>(logits, row * E + e + i) : -INFINITY;
+          for (int i = 0; i < 2; ++i)  // 0xFF80: -inf
+            w[2 * j + i] = (e + 2 * i < E ? p[2 * i] : 0xFF80u) | (e + 2 * i + 1 < E ? p[2 * i + 1] : 0xFF80u) << 16;
+        }
+      } else {
+        const uint32_t* p = static_cast<const uint32_t*>(logits) + at;
+        if (vec && e < E) {
+          const uint4 v = *reinterpret_cast<const uint4*>(p);
+          w[4 * j] = v.x, w[4 * j + 1] = v.y, w[4 * j + 2] = v.z, w[4 * j + 3] = v.w;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[4 * j + i] = e + i < E ? p[i] : 0xFF800000u;
+        }
+      }
     }
   }
-}
+  __device__ __forceinline__ void values(float (&l)[EPL]) const {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      l[i] = !BF16 ? __uint_as_float(w[i]) : i & 1 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
+  }
+};
 
 template <int L>
 __device__ __forceinline__ float lanes_max(float v) {
+  if (L == 32) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+  }
 #pragma unroll
   for (int o = L / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
@@ -212,18 +229,19 @@ __global__ void __launch_bounds__(kThreads, EPL > 8 ? 1 : 2) forward_kernel(cons
     if (!SINGLE && begin >= b1) break;
     const int lo = max(begin, b0), hi = min(seq_begin(a.offsets, s + 1, a.S, a.T), b1);
     if (!SINGLE && lo >= hi) continue;
-    float acc[EPL], cur[EPL], none[1];
+    float acc[EPL], none[1];
+    Row<BF16, L, EPL> cur;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) acc[i] = 0.f;
     // probabilities: the next token's logits are loaded before this one's are worked on (the first before the counts)
-    auto fetch = [&](int base, float (&l)[EPL]) {
+    auto fetch = [&](int base) {
       const int t = base + lane / L;
       const bool in = t < hi && (!a.mask || a.mask[t]);
-      if (in) load_row<BF16, L, EPL>(a.logits, t, a.E, sub, l);
+      if (in) cur.load(a.logits, t, a.E, sub);
       return in;
     };
     int base = lo + warp * PER_WARP;
-    bool in = base < hi && fetch(base, cur);
+    bool in = base < hi && fetch(base);
     for (int e = threadIdx.x; e < a.E; e += kThreads) hist[e] = 0;
     if (threadIdx.x == 0) n_seq_tokens = 0;
     __syncthreads();
@@ -242,9 +260,12 @@ __global__ void __launch_bounds__(kThreads, EPL > 8 ? 1 : 2) forward_kernel(cons
     for (; base < hi; base += STRIDE) {
       float l[EPL];
       const bool now = in;
+      cur.values(l);
+      if (L < 32 && !now) {
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) l[i] = L == 32 || now ? cur[i] : -INFINITY;
-      in = base + STRIDE < hi && fetch(base + STRIDE, cur);
+        for (int i = 0; i < EPL; ++i) l[i] = -INFINITY;
+      }
+      in = base + STRIDE < hi && fetch(base + STRIDE);
       if (L == 32 && !now) continue;  // the whole warp
       const float r = weights<SIGMOID, false, L, EPL>(l, none);
       if (L == 32 || now) {
@@ -364,17 +385,18 @@ __global__ void __launch_bounds__(kThreads, EPL > 8 ? 1 : 2) backward_kernel(con
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % L;
   const int b0 = blockIdx.x * a.per_block, b1 = min(a.T, b0 + a.per_block);
   const bool vec = (a.E & 3) == 0;
-  float g[EPL], cur[EPL];
+  float g[EPL];
+  Row<BF16, L, EPL> cur;
   int until = -1;  // g is that of the sequence of the tokens before this one
   bool covered = false;
-  auto fetch = [&](int base, float (&l)[EPL]) {
+  auto fetch = [&](int base) {
     const int t = base + lane / L;
     const bool in = t < b1 && (!a.mask || a.mask[t]);
-    if (in) load_row<BF16, L, EPL>(a.logits, t, a.E, sub, l);
+    if (in) cur.load(a.logits, t, a.E, sub);
     return in;
   };
   int base = b0 + warp * PER_WARP;
-  bool in = base < b1 && fetch(base, cur);
+  bool in = base < b1 && fetch(base);
   for (; base < b1; base += STRIDE) {
     const int t = base + lane / L;
     if (t < b1 && t >= until) {
@@ -392,25 +414,30 @@ __global__ void __launch_bounds__(kThreads, EPL > 8 ? 1 : 2) backward_kernel(con
     }
     float l[EPL], d[SIGMOID ? EPL : 1];
     const bool now = in;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) l[i] = L == 32 || now ? cur[i] : -INFINITY;
-    in = base + STRIDE < b1 && fetch(base + STRIDE, cur);
-    const float r = weights<SIGMOID, SIGMOID, L, EPL>(l, d);
-    float dot = 0.f;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) dot = fmaf(l[i], g[i], dot);
-    dot = lanes_sum<L>(dot) * r;
-    if (t >= b1) continue;
+    cur.values(l);
+    in = base + STRIDE < b1 && fetch(base + STRIDE);
     const bool zero = !now || !covered;  // padding, or a token of no sequence: whatever its logits hold
+    if (L < 32 || !zero) {               // with L = 32 the whole warp has one token
+      const float r = weights<SIGMOID, SIGMOID, L, EPL>(l, d);
+      float dot = 0.f;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        l[i] *= r;
+        dot = fmaf(l[i], g[i], dot);
+      }
+      dot = lanes_sum<L>(dot);
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) l[i] *= SIGMOID ? (g[i] - dot) * d[SIGMOID ? i : 0] : g[i] - dot;
+    }
+    if (zero) {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) l[i] = 0.f;
+    }
+    if (t >= b1) continue;
 #pragma unroll
     for (int j = 0; j < EPL / 4; ++j) {
       const int e = 4 * (sub + L * j);
-      float o[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float v = l[4 * j + i] * r * (g[4 * j + i] - dot);
-        o[i] = zero ? 0.f : SIGMOID ? v * d[SIGMOID ? 4 * j + i : 0] : v;
-      }
+      const float* o = l + 4 * j;
       const int64_t at = (int64_t)t * a.E + e;
       if (vec && e < a.E) {
         if (BF16)
