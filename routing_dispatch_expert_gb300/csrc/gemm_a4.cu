@@ -44,7 +44,7 @@ constexpr int SLOTS = 2;                 // ring of scales
 constexpr int SLOT_WORDS = 8;            // 4-byte words of scales of a row in a slot: a 32-byte sector
 constexpr int SLOT_BYTES = SLOT_WORDS * (BM + BN) * 4;
 constexpr int SCALE_WARP0 = 2;
-constexpr int SCALE_WARPS = 6;           // 3 blocks of 128 rows (A, two of B) x 2 halves
+constexpr int SCALE_WARPS = 6;           // 3 blocks of 128 rows (A, two of B) x 2 slots
 constexpr int EPI_WARP0 = SCALE_WARP0 + SCALE_WARPS;
 template <int FMT>
 constexpr int kWords = BK / fp4::kBlock<FMT> / 4;  // words of a row's K block
@@ -55,6 +55,7 @@ constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
 constexpr int ACC1 = 208;    // column of the second accumulator
 constexpr int SFA_COL = 464;
 constexpr int SFB_COL = 480;
+
 constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + SLOTS * SLOT_BYTES + 1024;
 
 struct Args {
@@ -166,36 +167,193 @@ __device__ __forceinline__ uint4 load_scales(const uint8_t* p, int left) {
   }
 }
 
-// 32 fp32 columns of a row to its output; `n`: how many of them exist.
-__device__ __forceinline__ void store_row(const Args& a, int64_t row, int col, int n, const float* v) {
-  if (a.f32) {
-    float* o = static_cast<float*>(a.out) + row * a.ldo + col;
-    if (n >= 32 && a.vec >= 16) {
+// The scales' copies and the MMAs of one K block: codes at a (A) and b (B), scales of its words at sf. Copies and
+// MMAs of one thread run in order: the copies wait for the MMAs that read the columns they write.
+template <int FMT>
+__device__ __forceinline__ void issue_k_block(uint32_t tmem, uint32_t d, uint32_t a, uint32_t b, uint32_t sf, bool first) {
+  constexpr uint32_t IDESC = idesc_fp4<FMT>(BM, BN);
+#pragma unroll
+  for (int i = 0; i < kWords<FMT>; ++i) {
+    copy_scales(tmem + SFA_COL + 4 * i, scales_desc(sf + 1536 * i));
+    copy_scales(tmem + SFB_COL + 8 * i, scales_desc(sf + 1536 * i + 512));
+    copy_scales(tmem + SFB_COL + 8 * i + 4, scales_desc(sf + 1536 * i + 1024));
+  }
+#pragma unroll
+  for (int kk = 0; kk < BK / 64; ++kk) {
+    const int w = FMT == fp4::kNv ? kk : kk / 2;               // word of the scales
+    const uint32_t id = FMT == fp4::kNv ? 0u : 2u * (kk & 1);  // bytes of it: all four, or a half
+    umma_fp4<FMT>(d, sw128_kmajor_desc(a + kk * 32), sw128_kmajor_desc(b + kk * 32), IDESC | id << 4 | id << 29,
+                        tmem + SFA_COL + 4 * w, tmem + SFB_COL + 8 * w, !(first && kk == 0));
+  }
+}
+
+// Scale producers: three warps a slot, one for each 128-row block (A, the first and the second of B), and two such
+// groups in turn. Lanes 2 i and 2 i + 1 hold the two 16-byte halves of the 32-byte sector of rows l, l + 32, l + 64,
+// l + 96: whole sectors from L2, and one 16-byte line of shared memory for each word of the slot. A group issues the
+// loads of its next slot as soon as it has stored this one, and they land while the other group's slot is used.
+// Tiles first, first + step, ...
+template <int FMT, bool VEC>
+__device__ __forceinline__ void scale_producer(const Args& args, const grp::Table& tb, int warp, int lane, uint32_t slots,
+                                               int first, int step, uint64_t* sempty,
+                                               uint64_t* sfull, volatile int* abort_flag, int* status) {
+  static_assert(SLOTS == 2 && SCALE_WARPS == 6, "a group of three warps for each slot");
+  const int G = args.E + args.shared;
+  const int total = tb.gtile[G] * args.n_tiles;
+  const int kblocks = (args.K + BK - 1) / BK;
+  const int slot = (warp - SCALE_WARP0) / 3, block = (warp - SCALE_WARP0) % 3;
+  const int line = lane >> 1, part = lane & 1;  // and line + 16
+  const int pitch = args.K / fp4::kBlock<FMT>;
+  const int per_tile = (kblocks + kSlotBlocks<FMT> - 1) / kSlotBlocks<FMT>;
+  const uint32_t dst = slots + slot * SLOT_BYTES + (uint32_t)((4 * part * 3 + block) * 512 + 16 * line);
+  uint32_t phase = 0;
+  // fill number i of this CTA is slot i % 2: this group's fills are those of its parity
+  int fill = 0;
+  for (int tile = first; tile < total; tile += step) {
+    const grp::Tile t = grp::decode(tb, G, args.n_tiles, tile, BM);
+    const bool routed = t.g < args.E;
+    const int64_t z = routed ? (args.slot_expert ? args.slot_expert[t.g] : t.g) : 0;
+    const int n0 = args.mode == 0 ? t.n_tile * (BN / 2) : t.n_tile * BN;
+    const int r0 = block == 0 ? t.a_row : block == 1 ? n0 : args.mode == 0 ? args.I + n0 : n0 + BN / 2;
+    const int rows = block == 0 ? args.a_rows : args.b_rows;
+    const uint8_t* base = block == 0 ? args.a_scales
+                      : (routed ? args.b_scales : args.bs_scales) + z * args.b_rows * (int64_t)pitch;
+    const uint8_t* p[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)  // rows past the end take the last one's scales: they are not stored
+      p[i] = base + min(r0 + line + 16 * (i & 1) + 32 * (i >> 1), rows - 1) * (int64_t)pitch + 16 * part;
+    for (int j = 0; j < per_tile; ++j, ++fill) {
+      if ((fill & 1) != slot) continue;
+      uint4 v[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        reinterpret_cast<float4*>(o)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-    } else {
+        v[i] = load_scales<VEC>(p[i] + j * (4 * SLOT_WORDS), pitch - j * (4 * SLOT_WORDS) - 16 * part);
+      const int got = wait_or_abort(&sempty[slot], phase ^ 1, abort_flag, status, args.wait_limit);
+      if (!__all_sync(0xffffffffu, got)) return;
+      phase ^= 1;
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (i < n) o[i] = v[i];
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t at = dst + 256 * h;
+        sts128(at, v[h].x, v[2 + h].x, v[4 + h].x, v[6 + h].x);
+        sts128(at + 1536, v[h].y, v[2 + h].y, v[4 + h].y, v[6 + h].y);
+        sts128(at + 2 * 1536, v[h].z, v[2 + h].z, v[4 + h].z, v[6 + h].z);
+        sts128(at + 3 * 1536, v[h].w, v[2 + h].w, v[4 + h].w, v[6 + h].w);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sfull[slot]);
+    }
+  }
+}
+
+// H in fp32 of 32 gate columns (TMEM address g) and the matching 32 up columns (u) of this lane's row.
+__device__ __forceinline__ void swiglu(uint32_t g, uint32_t u, float scale, float (&h)[32]) {
+#pragma unroll
+  for (int j0 = 0; j0 < 32; j0 += 16) {
+    uint32_t gate[16], up[16];
+    tmem_ld16(g + j0, gate);
+    tmem_ld16(u + j0, up);
+    tmem_ld_wait_regs(gate);
+    tmem_ld_wait_regs(up);
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      h[j0 + j] = grp::silu(__uint_as_float(gate[j]) * scale) * (__uint_as_float(up[j]) * scale);
+  }
+}
+// H of a row quantised and stored: 16 bytes of codes and the scale bytes of their blocks.
+template <int FMT>
+__device__ __forceinline__ void store_codes(const Args& args, int64_t row, int col, const float (&h)[32],
+                                            const fp4::Scale& hg) {
+  uint32_t q[4], sc = 0;
+  constexpr int kBlk = fp4::kBlock<FMT>;
+#pragma unroll
+  for (int b = 0; b < 32 / kBlk; ++b) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < kBlk; ++j) m = max(m, fp4::abs_bits(h[kBlk * b + j]));
+    float by;
+    sc |= fp4::block_scale<FMT>(m, hg, by) << (8 * b);
+#pragma unroll
+    for (int j = 0; j < kBlk / 8; ++j) q[kBlk / 8 * b + j] = fp4::codes8<FMT>(h + kBlk * b + 8 * j, by);
+  }
+  *reinterpret_cast<uint4*>(static_cast<uint8_t*>(args.out) + (row * args.ldo + col) / 2) =
+      make_uint4(q[0], q[1], q[2], q[3]);
+  uint8_t* so = args.out_scales + (row * args.ldo + col) / kBlk;
+  if (FMT == fp4::kNv)
+    *reinterpret_cast<uint16_t*>(so) = (uint16_t)sc;
+  else
+    *so = (uint8_t)sc;
+}
+
+// rows of scales that are whole 16-byte pieces are loaded as such, others byte by byte
+inline bool scales_vec(const GemmA4Desc& d) {
+  return d.K / (d.format == fp4::kNv ? fp4::kBlock<fp4::kNv> : fp4::kBlock<fp4::kMx>) % 16 == 0;
+}
+
+// One 128-byte run (64 bf16 or 32 fp32 columns) of each of a warp's 32 rows to the output: lane = row, w = its run. A
+// lane that stored its own row would touch 32 lines an instruction, and the stores would hold up the scales' way
+// through the same unit. So four lanes exchange their rows' 32-byte quarters first, and an instruction stores 8
+// whole lines; rows that are not 16-byte aligned are exchanged over all 32 lanes and stored element by element, one
+// line an instruction. `rows`, `cols`: how many of them exist.
+__device__ __forceinline__ void store_run(const Args& a, int lane, uint32_t (&w)[32], int64_t row0, int rows, int col,
+                                          int cols) {
+  const int elem = a.f32 ? 4 : 2;
+  char* out = static_cast<char*>(a.out) + (row0 * a.ldo + col) * elem;
+  const int64_t pitch = a.ldo * elem;
+  const int n = cols * elem;  // bytes of the run
+  if (a.vec >= 16 && n >= 128) {
+    // after the step over lanes that differ in bit b, words 8 p .. hold quarter (p with that bit the lane's) of the
+    // row with that bit p's
+#pragma unroll
+    for (int b = 1; b < 4; b *= 2) {
+      const bool up = lane & b;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        if ((i >> 3) & b) continue;
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? w[i] : w[i + 8 * b], b);
+        if (up)
+          w[i] = got;
+        else
+          w[i + 8 * b] = got;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int r = (lane & ~3) + j;
+      if (r >= rows) continue;
+      char* o = out + r * pitch + 32 * (lane & 3);
+      if (a.vec >= 32) {
+        st_global_v8(o, w + 8 * j);
+      } else {
+        reinterpret_cast<uint4*>(o)[0] = make_uint4(w[8 * j], w[8 * j + 1], w[8 * j + 2], w[8 * j + 3]);
+        reinterpret_cast<uint4*>(o)[1] = make_uint4(w[8 * j + 4], w[8 * j + 5], w[8 * j + 6], w[8 * j + 7]);
+      }
     }
     return;
   }
-  uint32_t w[16];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-  uint16_t* o = static_cast<uint16_t*>(a.out) + row * a.ldo + col;
-  if (n >= 32 && a.vec >= 32) {
-    st_global_v8(o, w);
-    st_global_v8(o + 16, w + 8);
-  } else if (n >= 32 && a.vec >= 16) {
+  for (int b = 16; b > 0; b /= 2) {
+    const bool up = lane & b;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      reinterpret_cast<uint4*>(o)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-  } else {
+    for (int i = 0; i < 32; ++i) {
+      if (i & b) continue;
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? w[i] : w[i + b], b);
+      if (up)
+        w[i] = got;
+      else
+        w[i + b] = got;
+    }
+  }
+  const int at = 4 * lane;
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (i < n) o[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+  for (int r = 0; r < 32; ++r) {
+    if (r >= rows) continue;
+    char* o = out + r * pitch + at;
+    if (a.f32) {
+      if (at < n) *reinterpret_cast<uint32_t*>(o) = w[r];
+    } else {
+      if (at < n) reinterpret_cast<uint16_t*>(o)[0] = (uint16_t)w[r];
+      if (at + 2 < n) reinterpret_cast<uint16_t*>(o)[1] = (uint16_t)(w[r] >> 16);
+    }
   }
 }
 
@@ -219,7 +377,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         mbar_init(&s.empty[i], 1);
       }
       for (int i = 0; i < SLOTS; ++i) {
-        mbar_init(&s.sfull[i], SCALE_WARPS);
+        mbar_init(&s.sfull[i], SCALE_WARPS / 2);
         mbar_init(&s.sempty[i], 1);
       }
       mbar_init(&s.tfull[0], 1);
@@ -289,7 +447,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     // ---------------- MMA issuer. The whole warp walks the loop and one lane issues: with operands in uniform
     // registers an instruction takes a few cycles to issue; from a branch that one lane alone had taken, each
     // descriptor went through vector registers first, about 48 cycles for each of the 16 of a K block.
-    constexpr uint32_t IDESC = idesc_fp4<FMT>(BM, BN);
     const bool leader = elect_one();
     int stage = 0, slot = 0, n = 0;  // n: tiles of this CTA so far
     uint32_t phase = 0, sphase = 0;
@@ -314,21 +471,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t sf = slots + slot * SLOT_BYTES + in_slot * kWords<FMT> * 3 * 512;
         const bool slot_done = in_slot == kSlotBlocks<FMT> - 1 || kb + 1 == kblocks;
         if (leader) {
-          // copies and MMAs of one thread run in order: the copies wait for the MMAs that read the columns
-#pragma unroll
-          for (int i = 0; i < kWords<FMT>; ++i) {
-            copy_scales(tmem_base + SFA_COL + 4 * i, scales_desc(sf + 1536 * i));
-            copy_scales(tmem_base + SFB_COL + 8 * i, scales_desc(sf + 1536 * i + 512));
-            copy_scales(tmem_base + SFB_COL + 8 * i + 4, scales_desc(sf + 1536 * i + 1024));
-          }
-#pragma unroll
-          for (int kk = 0; kk < BK / 64; ++kk) {
-            const int w = FMT == fp4::kNv ? kk : kk / 2;             // word of the scales
-            const uint32_t id = FMT == fp4::kNv ? 0u : 2u * (kk & 1);  // bytes of it: all four, or a half
-            umma_fp4<FMT>(d, sw128_kmajor_desc(a + kk * 32), sw128_kmajor_desc(b + kk * 32),
-                          IDESC | id << 4 | id << 29, tmem_base + SFA_COL + 4 * w, tmem_base + SFB_COL + 8 * w,
-                          (kb | kk) != 0);
-          }
+          issue_k_block<FMT>(tmem_base, d, a, b, sf, kb == 0);
           if (slot_done) umma_commit(&s.sempty[slot]);
           umma_commit(&s.empty[stage]);
           if (kb + 1 == kblocks) umma_commit(&s.tfull[n & 1]);
@@ -349,66 +492,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     __syncwarp();
   } else if (warp >= SCALE_WARP0 && warp < EPI_WARP0) {
-    // ---------------- scale producers: each warp half of the lines of one 128-row block (A, the first and the second of
-    // B). Lanes 2 i and 2 i + 1 hold the two 16-byte halves of the 32-byte sector of rows l, l + 32, l + 64, l + 96:
-    // whole sectors from L2, and one 16-byte line of shared memory for each word of the slot. Loads run two slots
-    // ahead of the stores, in registers.
-    const int unit = warp - SCALE_WARP0, block = unit >> 1;
-    const int line = (unit & 1) * 16 + (lane >> 1), part = lane & 1;
-    const int pitch = args.K / fp4::kBlock<FMT>;
-    const int per_tile = (kblocks + kSlotBlocks<FMT> - 1) / kSlotBlocks<FMT>;
-    const uint32_t dst = slots + (uint32_t)((4 * part * 3 + block) * 512 + 16 * line);
-    const uint8_t* p[4];
-    int load_tile = blockIdx.x, load_slot = 0;
-    auto fetch = [&](uint4 (&v)[4]) {
-      if (load_tile >= total) return;
-      if (load_slot == 0) {
-        const grp::Tile t = grp::decode(s.tb, G, args.n_tiles, load_tile, BM);
-        const bool routed = t.g < args.E;
-        const int64_t z = routed ? (args.slot_expert ? args.slot_expert[t.g] : t.g) : 0;
-        const int n0 = args.mode == 0 ? t.n_tile * (BN / 2) : t.n_tile * BN;
-        const int r0 = block == 0 ? t.a_row : block == 1 ? n0 : args.mode == 0 ? args.I + n0 : n0 + BN / 2;
-        const int rows = block == 0 ? args.a_rows : args.b_rows;
-        const uint8_t* base = block == 0 ? args.a_scales
-                                         : (routed ? args.b_scales : args.bs_scales) + z * args.b_rows * (int64_t)pitch;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)  // rows past the end take the last one's scales: they are not stored
-          p[i] = base + min(r0 + line + 32 * i, rows - 1) * (int64_t)pitch + 16 * part;
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        v[i] = load_scales<VEC>(p[i] + load_slot * (4 * SLOT_WORDS), pitch - load_slot * (4 * SLOT_WORDS) - 16 * part);
-      if (++load_slot == per_tile) {
-        load_slot = 0;
-        load_tile += gridDim.x;
-      }
-    };
-    auto store = [&](const uint4 (&v)[4], int slot, uint32_t phase) {
-      const int got = wait_or_abort(&s.sempty[slot], phase ^ 1, &s.abort_flag, status, args.wait_limit);
-      if (!__all_sync(0xffffffffu, got)) return false;
-      const uint32_t at = dst + slot * SLOT_BYTES;
-      sts128(at, v[0].x, v[1].x, v[2].x, v[3].x);
-      sts128(at + 1536, v[0].y, v[1].y, v[2].y, v[3].y);
-      sts128(at + 2 * 1536, v[0].z, v[1].z, v[2].z, v[3].z);
-      sts128(at + 3 * 1536, v[0].w, v[1].w, v[2].w, v[3].w);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s.sfull[slot]);
-      return true;
-    };
-    const int tiles = blockIdx.x < total ? (total - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
-    const int64_t fills = (int64_t)tiles * per_tile;
-    uint4 v0[4], v1[4];
-    fetch(v0);
-    fetch(v1);
-    uint32_t phase = 0;
-    static_assert(SLOTS == 2, "the two register sets are the two slots");
-    for (int64_t i = 0; i < fills; i += 2, phase ^= 1) {
-      if (!store(v0, 0, phase)) break;
-      fetch(v0);
-      if (i + 1 == fills || !store(v1, 1, phase)) break;
-      fetch(v1);
-    }
+    scale_producer<FMT, VEC>(args, s.tb, warp, lane, slots, blockIdx.x, gridDim.x, s.sempty, s.sfull, &s.abort_flag,
+                             status);
   } else if (warp >= EPI_WARP0) {
     // ---------------- epilogue
     const int quarter = warp & 3, half = (warp - EPI_WARP0) >> 2;
@@ -416,7 +501,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t tq = tmem_base + ((uint32_t)(quarter * 32) << 16);
     const float ag = args.a_g ? *args.a_g : 1.0f;
     const fp4::Scale hg(args.mode == 0 ? args.out_g : nullptr);
-    const int chunks = args.mode == 0 ? 4 : 8;  // of 32 output columns
+    const int chunks = args.mode == 0 || !args.f32 ? 4 : 8;  // 32 columns of H, runs of 64 bf16 or 32 fp32 columns
     int n = 0;
     for (int tile = blockIdx.x; tile < total; tile += gridDim.x, ++n) {
       const grp::Tile t = grp::decode(s.tb, G, args.n_tiles, tile, BM);
@@ -432,72 +517,46 @@ __global__ void __launch_bounds__(THREADS, 1)
       tc_fence_after();
       const uint32_t tacc = tq + (n & 1 ? ACC1 : 0);
       const bool any = quarter * 32 < t.rows;  // this quarter has rows
-      // Positions 0 .. chunks - 1 in the order that frees the shared columns first (the last 48 columns of
-      // the first accumulator, the first 48 of the second): they lie in the chunks of positions 0 and 1.
-      // The two warps of a quarter take alternate positions.
+      // Positions in the order that frees the shared columns first (the last 48 of the first accumulator, the first
+      // 48 of the second), alternate ones for the two warps of a quarter: the shared columns lie in the first position
+      // (of 64 columns) or the first two (of 32). A warp that reads none of them still says here that it is done
+      // with the tile before.
       for (int i = half; i < chunks; i += 2) {
-        const int c = 32 * (n & 1 ? i : chunks - 1 - i);
-        if (args.mode == 0) {
-          float h[32];
-          if (any) {
+        const int at = n & 1 ? i : chunks - 1 - i;
+        float h[32];
+        uint32_t w[32];
+        if (any) {
+          if (args.mode == 0) {
+            swiglu(tacc + 32 * at, tacc + BN / 2 + 32 * at, scale, h);
+          } else if (args.f32) {
+            tmem_ld32(tacc + 32 * at, w);
+            tmem_ld_wait_regs(w);
 #pragma unroll
-            for (int j0 = 0; j0 < 32; j0 += 16) {
-              uint32_t gate[16], up[16];
-              tmem_ld16(tacc + c + j0, gate);
-              tmem_ld16(tacc + BN / 2 + c + j0, up);
-              tmem_ld_wait_regs(gate);
-              tmem_ld_wait_regs(up);
+            for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(__uint_as_float(w[j]) * scale);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 64; c += 32) {
+              uint32_t v[32];
+              tmem_ld32(tacc + 64 * at + c, v);
+              tmem_ld_wait_regs(v);
 #pragma unroll
               for (int j = 0; j < 16; ++j)
-                h[j0 + j] = grp::silu(__uint_as_float(gate[j]) * scale) * (__uint_as_float(up[j]) * scale);
+                w[c / 2 + j] = pack_bf16x2(__uint_as_float(v[2 * j]) * scale, __uint_as_float(v[2 * j + 1]) * scale);
             }
           }
-          if (i < 2) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s.tfree);
-          }
-          if (!any) continue;
-          uint32_t q[4], sc = 0;
-          constexpr int kBlk = fp4::kBlock<FMT>;
-#pragma unroll
-          for (int b = 0; b < 32 / kBlk; ++b) {
-            uint32_t m = 0;
-#pragma unroll
-            for (int j = 0; j < kBlk; ++j) m = max(m, fp4::abs_bits(h[kBlk * b + j]));
-            float by;
-            sc |= fp4::block_scale<FMT>(m, hg, by) << (8 * b);
-#pragma unroll
-            for (int j = 0; j < kBlk / 8; ++j) q[kBlk / 8 * b + j] = fp4::codes8<FMT>(h + kBlk * b + 8 * j, by);
-          }
-          if (valid) {
-            const int col = t.n_tile * (BN / 2) + c;
-            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(args.out) + (row * args.ldo + col) / 2) =
-                make_uint4(q[0], q[1], q[2], q[3]);
-            uint8_t* so = args.out_scales + (row * args.ldo + col) / kBlk;
-            if (FMT == fp4::kNv)
-              *reinterpret_cast<uint16_t*>(so) = (uint16_t)sc;
-            else
-              *so = (uint8_t)sc;
-          }
+        }
+        if (i < 2) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s.tfree);
+        }
+        if (!any) continue;
+        if (args.mode == 0) {
+          if (valid) store_codes<FMT>(args, row, t.n_tile * (BN / 2) + 32 * at, h, hg);
         } else {
-          uint32_t v[32];
-          if (any) {
-            tmem_ld32(tacc + c, v);
-            tmem_ld_wait_regs(v);
-          }
-          if (i < 2) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s.tfree);
-          }
-          const int col = t.n_tile * BN + c;
-          if (valid && col < args.N) {
-            float f[32];
-#pragma unroll
-            for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[j]) * scale;
-            store_row(args, row, col, args.N - col, f);
-          }
+          const int col = t.n_tile * BN + (args.f32 ? 32 : 64) * at;
+          if (col < args.N)
+            store_run(args, lane, w, (int64_t)t.a_row + quarter * 32, t.rows - quarter * 32, col, args.N - col);
         }
       }
     }
@@ -513,6 +572,40 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 }  // namespace a4
+
+a4::Args gemm_a4_args(const GemmA4Desc& d) {
+  a4::Args a;
+  a.offsets = d.offsets;
+  a.slot_expert = d.slot_expert;
+  a.E = d.E;
+  a.shared = d.B_shared != nullptr;
+  a.R = d.R;
+  a.T = d.T;
+  a.K = d.K;
+  a.N = d.N;
+  a.mode = d.mode;
+  a.I = d.I;
+  a.f32 = d.f32;
+  a.n_tiles = d.mode == 0 ? d.I / (a4::BN / 2) : (int)cdiv(d.N, a4::BN);
+  a.a_rows = (int)d.a_rows;
+  a.b_rows = (int)d.b_rows;
+  a.a_scales = static_cast<const uint8_t*>(d.As);
+  a.b_scales = static_cast<const uint8_t*>(d.Bs);
+  a.bs_scales = static_cast<const uint8_t*>(d.Bs_shared);
+  a.a_g = d.Ag;
+  a.b_g = d.Bg;
+  a.bs_g = d.Bg_shared;
+  a.ldo = d.ldo;
+  const uintptr_t mis = reinterpret_cast<uintptr_t>(d.out) | (uintptr_t)(d.ldo * (d.f32 ? 4 : 2));
+  a.vec = mis % 32 == 0 ? 32 : mis % 16 == 0 ? 16 : 0;
+  a.out = d.out;
+  a.out_scales = static_cast<uint8_t*>(d.out_scales);
+  a.out_g = d.out_g;
+  a.row_weight = d.row_weight;
+  a.status = d.status;
+  a.wait_limit = 4000000000LL;  // about two seconds of SM clock
+  return a;
+}
 
 cudaError_t launch_gemm_a4(const GemmA4Desc& d, cudaStream_t stream, std::string* err) {
   cudaError_t e = tma_encoder_ready();
@@ -554,39 +647,8 @@ cudaError_t launch_gemm_a4(const GemmA4Desc& d, cudaStream_t stream, std::string
     *err = "cuTensorMapEncodeTiled rejected a 4-bit GEMM operand";
     return cudaErrorInvalidValue;
   }
-  a4::Args a;
-  a.offsets = d.offsets;
-  a.slot_expert = d.slot_expert;
-  a.E = d.E;
-  a.shared = d.B_shared != nullptr;
-  a.R = d.R;
-  a.T = d.T;
-  a.K = d.K;
-  a.N = d.N;
-  a.mode = d.mode;
-  a.I = d.I;
-  a.f32 = d.f32;
-  a.n_tiles = d.mode == 0 ? d.I / (a4::BN / 2) : (int)cdiv(d.N, a4::BN);
-  a.a_rows = (int)d.a_rows;
-  a.b_rows = (int)d.b_rows;
-  a.a_scales = static_cast<const uint8_t*>(d.As);
-  a.b_scales = static_cast<const uint8_t*>(d.Bs);
-  a.bs_scales = static_cast<const uint8_t*>(d.Bs_shared);
-  a.a_g = d.Ag;
-  a.b_g = d.Bg;
-  a.bs_g = d.Bg_shared;
-  a.ldo = d.ldo;
-  const uintptr_t mis = reinterpret_cast<uintptr_t>(d.out) | (uintptr_t)(d.ldo * (d.f32 ? 4 : 2));
-  a.vec = mis % 32 == 0 ? 32 : mis % 16 == 0 ? 16 : 0;
-  a.out = d.out;
-  a.out_scales = static_cast<uint8_t*>(d.out_scales);
-  a.out_g = d.out_g;
-  a.row_weight = d.row_weight;
-  a.status = d.status;
-  a.wait_limit = 4000000000LL;  // about two seconds of SM clock
-  // rows of scales that are whole 16-byte pieces are loaded as such, others byte by byte
-  const bool vec = d.K / (d.format == fp4::kNv ? fp4::kBlock<fp4::kNv> : fp4::kBlock<fp4::kMx>) % 16 == 0;
-  kernels[(d.format == fp4::kNv ? 0 : 2) + (vec ? 0 : 1)]<<<num_sms(), a4::THREADS, a4::SMEM_BYTES, stream>>>(tA, tA32,
+  const a4::Args a = gemm_a4_args(d);
+  kernels[(d.format == fp4::kNv ? 0 : 2) + (a4::scales_vec(d) ? 0 : 1)]<<<num_sms(), a4::THREADS, a4::SMEM_BYTES, stream>>>(tA, tA32,
                                                                                                              tB, tBs, a);
   return cudaGetLastError();
 }
