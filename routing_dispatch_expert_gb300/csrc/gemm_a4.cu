@@ -96,50 +96,65 @@ struct Shared {
 using grp::wait_or_abort;
 
 // One lane of a converged warp, the same one on every call.
-__device__ __forceinline__ bool elect_one() {
+__device__ __forceinline__ uint32_t elect_one() {
   uint32_t p;
   asm volatile(
       "{\n\t.reg .pred e;\n\t"
       "elect.sync _|e, 0xffffffff;\n\t"
       "selp.u32 %0, 1, 0, e;\n\t}"
       : "=r"(p));
-  return p != 0;
+  return p;
 }
 
-// D (+)= A * B^T with block scales in TMEM; K = 64 elements.
+// The instructions of the MMA thread are issued by one lane (`one`) of a warp that walks its loop together: their
+// operands are then computed once for the warp, in uniform registers. In a branch that one lane had taken alone,
+// each operand went through vector registers first.
+
+// D (+)= A * B^T with block scales in TMEM; K = 64 elements. a, b: the low words of the operands' descriptors.
 template <int FMT>
-__device__ __forceinline__ void umma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
-                                         uint32_t accumulate) {
+__device__ __forceinline__ void umma_fp4(uint32_t one, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t sfa,
+                                         uint32_t sfb, uint32_t accumulate) {
+  // high word: stride 1024 bytes between groups of 8 rows, version 1, 128-byte swizzle (sw128_kmajor_desc)
+  constexpr uint32_t kHigh = (1024u >> 4) | 1u << 14 | 2u << 29;
   if (FMT == fp4::kNv)
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+        "mov.b64 da, {%1, %8};\n\tmov.b64 db, {%2, %8};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], da, db, %3, [%4], [%5], p;\n\t}" ::"r"(
             d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        "r"(a), "r"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(one), "r"(kHigh)
         : "memory");
   else
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+        "mov.b64 da, {%1, %8};\n\tmov.b64 db, {%2, %8};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], da, db, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(one), "r"(kHigh)
         : "memory");
 }
+__device__ __forceinline__ uint32_t operand_desc(uint32_t saddr) { return saddr >> 4 | 1u << 16; }
 
-// 512 bytes of scales [32][16] from shared memory to 4 TMEM columns, once for each lane quarter.
-__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+// 512 bytes of scales [32][16] (no swizzle, groups of 8 lines 128 bytes apart) from shared memory to 4 TMEM columns,
+// once for each lane quarter.
+__device__ __forceinline__ void copy_scales(uint32_t one, uint32_t taddr, uint32_t desc) {
+  constexpr uint32_t kHigh = (128u >> 4) | 1u << 14;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t.reg .b64 ds;\n\t"
+      "setp.ne.b32 q, %2, 0;\n\tmov.b64 ds, {%1, %3};\n\t"
+      "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], ds;\n\t}" ::"r"(taddr),
+      "r"(desc), "r"(one), "r"(kHigh)
+      : "memory");
 }
+__device__ __forceinline__ uint32_t scales_desc(uint32_t saddr) { return saddr >> 4 | (128u >> 4) << 16; }
 
-// Descriptor of 32 lines of 16 bytes, no swizzle: groups of 8 lines 128 bytes apart.
-__device__ __forceinline__ uint64_t scales_desc(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
-  d |= (uint64_t)(128u >> 4) << 16;
-  d |= (uint64_t)(128u >> 4) << 32;
-  d |= (uint64_t)1u << 46;
-  return d;
+__device__ __forceinline__ void commit(uint32_t one, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(one)
+      : "memory");
 }
 
 // Instruction descriptor: e2m1 operands, both K-major, fp32 accumulators; scales e4m3 (NVFP4) or e8m0.
@@ -170,32 +185,35 @@ __device__ __forceinline__ uint4 load_scales(const uint8_t* p, int left) {
 // The scales' copies and the MMAs of one K block: codes at a (A) and b (B), scales of its words at sf. Copies and
 // MMAs of one thread run in order: the copies wait for the MMAs that read the columns they write.
 template <int FMT>
-__device__ __forceinline__ void issue_k_block(uint32_t tmem, uint32_t d, uint32_t a, uint32_t b, uint32_t sf, bool first) {
+__device__ __forceinline__ void issue_k_block(uint32_t one, uint32_t tmem, uint32_t d, uint32_t a, uint32_t b, uint32_t sf,
+                                              bool first) {
   constexpr uint32_t IDESC = idesc_fp4<FMT>(BM, BN);
+  const uint32_t da = operand_desc(a), db = operand_desc(b), ds = scales_desc(sf);
 #pragma unroll
   for (int i = 0; i < kWords<FMT>; ++i) {
-    copy_scales(tmem + SFA_COL + 4 * i, scales_desc(sf + 1536 * i));
-    copy_scales(tmem + SFB_COL + 8 * i, scales_desc(sf + 1536 * i + 512));
-    copy_scales(tmem + SFB_COL + 8 * i + 4, scales_desc(sf + 1536 * i + 1024));
+    copy_scales(one, tmem + SFA_COL + 4 * i, ds + 96 * i);
+    copy_scales(one, tmem + SFB_COL + 8 * i, ds + 96 * i + 32);
+    copy_scales(one, tmem + SFB_COL + 8 * i + 4, ds + 96 * i + 64);
   }
 #pragma unroll
   for (int kk = 0; kk < BK / 64; ++kk) {
     const int w = FMT == fp4::kNv ? kk : kk / 2;               // word of the scales
     const uint32_t id = FMT == fp4::kNv ? 0u : 2u * (kk & 1);  // bytes of it: all four, or a half
-    umma_fp4<FMT>(d, sw128_kmajor_desc(a + kk * 32), sw128_kmajor_desc(b + kk * 32), IDESC | id << 4 | id << 29,
-                        tmem + SFA_COL + 4 * w, tmem + SFB_COL + 8 * w, !(first && kk == 0));
+    umma_fp4<FMT>(one, d, da + 2 * kk, db + 2 * kk, IDESC | id << 4 | id << 29, tmem + SFA_COL + 4 * w,
+                  tmem + SFB_COL + 8 * w, !(first && kk == 0));
   }
 }
 
 // Scale producers: three warps a slot, one for each 128-row block (A, the first and the second of B), and two such
 // groups in turn. Lanes 2 i and 2 i + 1 hold the two 16-byte halves of the 32-byte sector of rows l, l + 32, l + 64,
 // l + 96: whole sectors from L2, and one 16-byte line of shared memory for each word of the slot. A group issues the
-// loads of its next slot as soon as it has stored this one, and they land while the other group's slot is used.
+// loads of its next slot as soon as it has stored this one, and they land while the other group's slot is used (each
+// group has a slot of its own: it never waits for one more than a phase ahead, which a parity could not tell).
 // Tiles first, first + step, ...
 template <int FMT, bool VEC>
 __device__ __forceinline__ void scale_producer(const Args& args, const grp::Table& tb, int warp, int lane, uint32_t slots,
-                                               int first, int step, uint64_t* sempty,
-                                               uint64_t* sfull, volatile int* abort_flag, int* status) {
+                                               int first, int step, uint64_t* sempty, uint64_t* sfull,
+                                               volatile int* abort_flag, int* status) {
   static_assert(SLOTS == 2 && SCALE_WARPS == 6, "a group of three warps for each slot");
   const int G = args.E + args.shared;
   const int total = tb.gtile[G] * args.n_tiles;
@@ -245,20 +263,6 @@ __device__ __forceinline__ void scale_producer(const Args& args, const grp::Tabl
   }
 }
 
-// H in fp32 of 32 gate columns (TMEM address g) and the matching 32 up columns (u) of this lane's row.
-__device__ __forceinline__ void swiglu(uint32_t g, uint32_t u, float scale, float (&h)[32]) {
-#pragma unroll
-  for (int j0 = 0; j0 < 32; j0 += 16) {
-    uint32_t gate[16], up[16];
-    tmem_ld16(g + j0, gate);
-    tmem_ld16(u + j0, up);
-    tmem_ld_wait_regs(gate);
-    tmem_ld_wait_regs(up);
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-      h[j0 + j] = grp::silu(__uint_as_float(gate[j]) * scale) * (__uint_as_float(up[j]) * scale);
-  }
-}
 // H of a row quantised and stored: 16 bytes of codes and the scale bytes of their blocks.
 template <int FMT>
 __device__ __forceinline__ void store_codes(const Args& args, int64_t row, int col, const float (&h)[32],
@@ -444,10 +448,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (long long i = first; i < issued; ++i)
       grp::drain_wait(&s.full[i % STAGES], (uint32_t)((i / STAGES) & 1), args.wait_limit);
   } else if (warp == 1) {
-    // ---------------- MMA issuer. The whole warp walks the loop and one lane issues: with operands in uniform
-    // registers an instruction takes a few cycles to issue; from a branch that one lane alone had taken, each
-    // descriptor went through vector registers first, about 48 cycles for each of the 16 of a K block.
-    const bool leader = elect_one();
+    // ---------------- MMA issuer: the whole warp walks the loop, one lane issues
+    const uint32_t leader = elect_one();
     int stage = 0, slot = 0, n = 0;  // n: tiles of this CTA so far
     uint32_t phase = 0, sphase = 0;
     bool ok = true;
@@ -470,12 +472,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t b = a + A_BYTES;
         const uint32_t sf = slots + slot * SLOT_BYTES + in_slot * kWords<FMT> * 3 * 512;
         const bool slot_done = in_slot == kSlotBlocks<FMT> - 1 || kb + 1 == kblocks;
-        if (leader) {
-          issue_k_block<FMT>(tmem_base, d, a, b, sf, kb == 0);
-          if (slot_done) umma_commit(&s.sempty[slot]);
-          umma_commit(&s.empty[stage]);
-          if (kb + 1 == kblocks) umma_commit(&s.tfull[n & 1]);
-        }
+        issue_k_block<FMT>(leader, tmem_base, d, a, b, sf, kb == 0);
+        if (slot_done) commit(leader, &s.sempty[slot]);
+        commit(leader, &s.empty[stage]);
+        if (kb + 1 == kblocks) commit(leader, &s.tfull[n & 1]);
         if (slot_done && ++slot == SLOTS) {
           slot = 0;
           sphase ^= 1;
@@ -523,27 +523,19 @@ __global__ void __launch_bounds__(THREADS, 1)
       // with the tile before.
       for (int i = half; i < chunks; i += 2) {
         const int at = n & 1 ? i : chunks - 1 - i;
-        float h[32];
-        uint32_t w[32];
+        uint32_t w[32], u[32];  // 64 columns; mode 0: gate and up; fp32 rows: 32
         if (any) {
           if (args.mode == 0) {
-            swiglu(tacc + 32 * at, tacc + BN / 2 + 32 * at, scale, h);
+            tmem_ld32(tacc + 32 * at, w);
+            tmem_ld32(tacc + BN / 2 + 32 * at, u);
           } else if (args.f32) {
             tmem_ld32(tacc + 32 * at, w);
-            tmem_ld_wait_regs(w);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(__uint_as_float(w[j]) * scale);
           } else {
-#pragma unroll
-            for (int c = 0; c < 64; c += 32) {
-              uint32_t v[32];
-              tmem_ld32(tacc + 64 * at + c, v);
-              tmem_ld_wait_regs(v);
-#pragma unroll
-              for (int j = 0; j < 16; ++j)
-                w[c / 2 + j] = pack_bf16x2(__uint_as_float(v[2 * j]) * scale, __uint_as_float(v[2 * j + 1]) * scale);
-            }
+            tmem_ld32(tacc + 64 * at, w);
+            tmem_ld32(tacc + 64 * at + 32, u);
           }
+          tmem_ld_wait_regs(w);
+          if (args.mode == 0 || !args.f32) tmem_ld_wait_regs(u);
         }
         if (i < 2) {
           tc_fence_before();
@@ -552,12 +544,28 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         if (!any) continue;
         if (args.mode == 0) {
+          float h[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            h[j] = grp::silu(__uint_as_float(w[j]) * scale) * (__uint_as_float(u[j]) * scale);
           if (valid) store_codes<FMT>(args, row, t.n_tile * (BN / 2) + 32 * at, h, hg);
-        } else {
-          const int col = t.n_tile * BN + (args.f32 ? 32 : 64) * at;
-          if (col < args.N)
-            store_run(args, lane, w, (int64_t)t.a_row + quarter * 32, t.rows - quarter * 32, col, args.N - col);
+          continue;
         }
+        if (args.f32) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(__uint_as_float(w[j]) * scale);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            w[j] = pack_bf16x2(__uint_as_float(w[2 * j]) * scale, __uint_as_float(w[2 * j + 1]) * scale);
+          }
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            w[16 + j] = pack_bf16x2(__uint_as_float(u[2 * j]) * scale, __uint_as_float(u[2 * j + 1]) * scale);
+        }
+        const int col = t.n_tile * BN + (args.f32 ? 32 : 64) * at;
+        if (col < args.N)
+          store_run(args, lane, w, (int64_t)t.a_row + quarter * 32, t.rows - quarter * 32, col, args.N - col);
       }
     }
   }
