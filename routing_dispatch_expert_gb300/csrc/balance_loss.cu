@@ -84,6 +84,19 @@ __device__ __forceinline__ int seq_of(const int32_t* offsets, int S, int T, int 
   return lo;
 }
 
+// The same for a whole warp and one token: the lanes look at 32 sequences at a time, one load instead of a chain of
+// log2 S (offsets ascend, so the sequences that begin at or before t are the first ones).
+__device__ __forceinline__ int seq_of_warp(const int32_t* offsets, int S, int T, int t) {
+  if (!offsets) return 0;
+  if (S > 1024) return seq_of(offsets, S, T, t);
+  int n = 0;
+  for (int s0 = 0; s0 < S; s0 += 32) {
+    const int s = s0 + (threadIdx.x & 31);
+    n += __popc(__ballot_sync(0xffffffffu, s < S && seq_begin(offsets, s, S, T) <= t));
+  }
+  return max(n - 1, 0);
+}
+
 // This lane's experts of a token, 4 (sub + L j) + i (j < EPL / 4, i < 4), as they lie in memory: nothing is done
 // with them until values(), so that the loads of a token are in flight while another one is worked on.
 template <bool BF16, int L, int EPL>
@@ -224,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, EPL > 8 ? 1 : 2) forward_kernel(cons
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % L;
   const int b0 = blockIdx.x * a.per_block, b1 = min(a.T, b0 + a.per_block);
   if (!SINGLE) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  for (int s = SINGLE ? 0 : seq_of(a.offsets, a.S, a.T, b0); s < a.S; ++s) {
+  for (int s = SINGLE ? 0 : seq_of_warp(a.offsets, a.S, a.T, b0); s < a.S; ++s) {
     const int begin = seq_begin(a.offsets, s, a.S, a.T);
     if (!SINGLE && begin >= b1) break;
     const int lo = max(begin, b0), hi = min(seq_begin(a.offsets, s + 1, a.S, a.T), b1);
