@@ -237,10 +237,13 @@ __global__ void __launch_bounds__(kThreads, EPL > 8 ? 1 : 2) forward_kernel(cons
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % L;
   const int b0 = blockIdx.x * a.per_block, b1 = min(a.T, b0 + a.per_block);
   if (!SINGLE) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  for (int s = SINGLE ? 0 : seq_of_warp(a.offsets, a.S, a.T, b0); s < a.S; ++s) {
+  for (int s = SINGLE ? 0 : seq_of_warp(a.offsets, a.S, a.T, b0), after; s < a.S; s = after) {
     const int begin = seq_begin(a.offsets, s, a.S, a.T);
     if (!SINGLE && begin >= b1) break;
     const int lo = max(begin, b0), hi = min(seq_begin(a.offsets, s + 1, a.S, a.T), b1);
+    after = s + 1;
+    // the next sequence with a token, past those that are empty
+    if (!SINGLE && hi < b1) after = max(after, seq_of_warp(a.offsets, a.S, a.T, max(hi, b0)));
     if (!SINGLE && lo >= hi) continue;
     float acc[EPL], none[1];
     Row<BF16, L, EPL> cur;
@@ -489,16 +492,16 @@ cudaError_t with_shape(int E, F&& f) {
   return f(integral_constant<int, 32>{}, integral_constant<int, 32>{});
 }
 
-// Tokens of a block: at least four rounds of its warps, at most what fills the SMs with two blocks each.
-// A batch of one block's four rounds is one block: its results need no second kernel.
-int tokens_per_block(int T, int E) {
-  const int least = 4 * kWarps * (32 / lanes_of(E));
+// Tokens of a block: at least four rounds of its warps (fewer where the sequences are short: a block works on one
+// after the other, about 3 us each), at most what fills the SMs with two blocks each.
+int tokens_per_block(int T, int E, int S) {
+  const int64_t least = std::min<int64_t>(4 * kWarps * (32 / lanes_of(E)), std::max<int64_t>(1, cdiv(4 * (int64_t)T, S)));
   return (int)std::max<int64_t>(least, cdiv(T, 2 * kNumSMsHint));
 }
 
 }  // namespace bl
 
-int64_t balance_loss_entries(int T, int E, int S) { return cdiv(T, bl::tokens_per_block(T, E)) + S; }
+int64_t balance_loss_entries(int T, int E, int S) { return cdiv(T, bl::tokens_per_block(T, E, S)) + S; }
 
 cudaError_t launch_balance_loss(const BalanceLossDesc& d, int* launches, cudaStream_t stream) {
   bl::Args a;
@@ -510,7 +513,7 @@ cudaError_t launch_balance_loss(const BalanceLossDesc& d, int* launches, cudaStr
   a.E = d.E;
   a.k = d.k;
   a.S = d.S;
-  a.per_block = bl::tokens_per_block(d.T, d.E);
+  a.per_block = bl::tokens_per_block(d.T, d.E, d.S);
   a.alpha = d.alpha;
   const int64_t entries = balance_loss_entries(d.T, d.E, d.S);
   a.psum = static_cast<float*>(d.scratch);
@@ -520,7 +523,7 @@ cudaError_t launch_balance_loss(const BalanceLossDesc& d, int* launches, cudaStr
   a.counts = d.counts;
   a.mean = d.mean;
   a.tokens = d.tokens;
-  const bool single = d.T <= a.per_block;
+  const bool single = d.T <= a.per_block && d.S <= 4;  // one block, one sequence after the other
   const unsigned blocks = single ? 1u : (unsigned)cdiv(d.T, a.per_block);
   cudaError_t e = bl::with_shape(d.E, [&](auto Lc, auto Ec) {
     constexpr int L = decltype(Lc)::value, EPL = decltype(Ec)::value;

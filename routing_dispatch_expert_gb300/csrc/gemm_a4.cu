@@ -70,7 +70,7 @@ struct Args {
   const float* b_g;
   const float* bs_g;
   int64_t ldo;
-  int vec;  // bytes that every output row is aligned to: 32, 16 or less
+  int aligned;  // output rows start on 16 bytes
   void* out;
   uint8_t* out_scales;
   const float* out_g;
@@ -210,7 +210,7 @@ __device__ __forceinline__ void issue_k_block(uint32_t one, uint32_t tmem, uint3
 // loads of its next slot as soon as it has stored this one, and they land while the other group's slot is used (each
 // group has a slot of its own: it never waits for one more than a phase ahead, which a parity could not tell).
 // Tiles first, first + step, ...
-template <int FMT, bool VEC>
+template <int FMT, bool VEC, bool SWIGLU>
 __device__ __forceinline__ void scale_producer(const Args& args, const grp::Table& tb, int warp, int lane, uint32_t slots,
                                                int first, int step, uint64_t* sempty, uint64_t* sfull,
                                                volatile int* abort_flag, int* status) {
@@ -230,8 +230,8 @@ __device__ __forceinline__ void scale_producer(const Args& args, const grp::Tabl
     const grp::Tile t = grp::decode(tb, G, args.n_tiles, tile, BM);
     const bool routed = t.g < args.E;
     const int64_t z = routed ? (args.slot_expert ? args.slot_expert[t.g] : t.g) : 0;
-    const int n0 = args.mode == 0 ? t.n_tile * (BN / 2) : t.n_tile * BN;
-    const int r0 = block == 0 ? t.a_row : block == 1 ? n0 : args.mode == 0 ? args.I + n0 : n0 + BN / 2;
+    const int n0 = SWIGLU ? t.n_tile * (BN / 2) : t.n_tile * BN;
+    const int r0 = block == 0 ? t.a_row : block == 1 ? n0 : SWIGLU ? args.I + n0 : n0 + BN / 2;
     const int rows = block == 0 ? args.a_rows : args.b_rows;
     const uint8_t* base = block == 0 ? args.a_scales
                       : (routed ? args.b_scales : args.bs_scales) + z * args.b_rows * (int64_t)pitch;
@@ -296,44 +296,42 @@ inline bool scales_vec(const GemmA4Desc& d) {
 // One 128-byte run (64 bf16 or 32 fp32 columns) of each of a warp's 32 rows to the output: lane = row, w = its run. A
 // lane that stored its own row would touch 32 lines an instruction, and the stores would hold up the scales' way
 // through the same unit. So four lanes exchange their rows' 32-byte quarters first, and an instruction stores 8
-// whole lines; rows that are not 16-byte aligned are exchanged over all 32 lanes and stored element by element, one
-// line an instruction. `rows`, `cols`: how many of them exist.
-__device__ __forceinline__ void store_run(const Args& a, int lane, uint32_t (&w)[32], int64_t row0, int rows, int col,
-                                          int cols) {
-  const int elem = a.f32 ? 4 : 2;
-  char* out = static_cast<char*>(a.out) + (row0 * a.ldo + col) * elem;
-  const int64_t pitch = a.ldo * elem;
-  const int n = cols * elem;  // bytes of the run
-  if (a.vec >= 16 && n >= 128) {
-    // after the step over lanes that differ in bit b, words 8 p .. hold quarter (p with that bit the lane's) of the
-    // row with that bit p's
+// whole lines. `out`: the run of the first row; rows are 16-byte aligned; `rows` of them exist.
+template <bool WIDE>
+__device__ __forceinline__ void store_lines(char* out, int64_t pitch, int lane, uint32_t (&w)[32], int rows) {
+  // after the step over lanes that differ in bit b, words 8 p .. hold quarter (p with that bit the lane's) of the row
+  // with that bit p's
 #pragma unroll
-    for (int b = 1; b < 4; b *= 2) {
-      const bool up = lane & b;
+  for (int b = 1; b < 4; b *= 2) {
+    const bool up = lane & b;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        if ((i >> 3) & b) continue;
-        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? w[i] : w[i + 8 * b], b);
-        if (up)
-          w[i] = got;
-        else
-          w[i + 8 * b] = got;
-      }
+    for (int i = 0; i < 32; ++i) {
+      if ((i >> 3) & b) continue;
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? w[i] : w[i + 8 * b], b);
+      if (up)
+        w[i] = got;
+      else
+        w[i + 8 * b] = got;
     }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int r = (lane & ~3) + j;
-      if (r >= rows) continue;
-      char* o = out + r * pitch + 32 * (lane & 3);
-      if (a.vec >= 32) {
-        st_global_v8(o, w + 8 * j);
-      } else {
-        reinterpret_cast<uint4*>(o)[0] = make_uint4(w[8 * j], w[8 * j + 1], w[8 * j + 2], w[8 * j + 3]);
-        reinterpret_cast<uint4*>(o)[1] = make_uint4(w[8 * j + 4], w[8 * j + 5], w[8 * j + 6], w[8 * j + 7]);
-      }
-    }
-    return;
   }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int r = (lane & ~3) + j;
+    if (r >= rows) continue;
+    char* o = out + r * pitch + 32 * (lane & 3);
+    if (WIDE) {
+      st_global_v8(o, w + 8 * j);
+    } else {
+      reinterpret_cast<uint4*>(o)[0] = make_uint4(w[8 * j], w[8 * j + 1], w[8 * j + 2], w[8 * j + 3]);
+      reinterpret_cast<uint4*>(o)[1] = make_uint4(w[8 * j + 4], w[8 * j + 5], w[8 * j + 6], w[8 * j + 7]);
+    }
+  }
+}
+
+// The same for rows of any alignment, and runs of which `n` bytes exist: exchanged over all 32 lanes and stored
+// element by element, one line an instruction.
+__device__ __forceinline__ void store_elements(char* out, int64_t pitch, int lane, uint32_t (&w)[32], int rows, int n,
+                                               bool f32) {
 #pragma unroll
   for (int b = 16; b > 0; b /= 2) {
     const bool up = lane & b;
@@ -352,7 +350,7 @@ __device__ __forceinline__ void store_run(const Args& a, int lane, uint32_t (&w)
   for (int r = 0; r < 32; ++r) {
     if (r >= rows) continue;
     char* o = out + r * pitch + at;
-    if (a.f32) {
+    if (f32) {
       if (at < n) *reinterpret_cast<uint32_t*>(o) = w[r];
     } else {
       if (at < n) reinterpret_cast<uint16_t*>(o)[0] = (uint16_t)w[r];
@@ -361,7 +359,11 @@ __device__ __forceinline__ void store_run(const Args& a, int lane, uint32_t (&w)
   }
 }
 
-template <int FMT, bool VEC>
+// What a kernel writes: H in 4 bits; bf16 rows that start on 32 bytes and have whole runs; any rows. A kernel for each,
+// because the roles of a CTA run different code at the same time and share the instruction caches.
+enum { kCodes, kLines, kAny };
+
+template <int FMT, bool VEC, int OUT>
 __global__ void __launch_bounds__(THREADS, 1)
     gemm_a4_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA32,
                    const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmBs, const Args args) {
@@ -418,8 +420,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       const grp::Tile t = grp::decode(s.tb, G, args.n_tiles, tile, BM);
       const CUtensorMap* mb = t.g < args.E ? &tmB : &tmBs;
       const int z = t.g < args.E ? (args.slot_expert ? args.slot_expert[t.g] : t.g) : 0;
-      const int n0 = args.mode == 0 ? t.n_tile * (BN / 2) : t.n_tile * BN;
-      const int n1 = args.mode == 0 ? args.I + n0 : n0 + BN / 2;
+      const int n0 = OUT == kCodes ? t.n_tile * (BN / 2) : t.n_tile * BN;
+      const int n1 = OUT == kCodes ? args.I + n0 : n0 + BN / 2;
       const int boxes = (t.rows + 31) / 32;
       const uint32_t a_bytes = boxes == 4 ? A_BYTES : boxes * (A_BYTES / 4);
       for (int kb = 0; kb < kblocks; ++kb) {
@@ -492,7 +494,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     __syncwarp();
   } else if (warp >= SCALE_WARP0 && warp < EPI_WARP0) {
-    scale_producer<FMT, VEC>(args, s.tb, warp, lane, slots, blockIdx.x, gridDim.x, s.sempty, s.sfull, &s.abort_flag,
+    scale_producer<FMT, VEC, OUT == kCodes>(args, s.tb, warp, lane, slots, blockIdx.x, gridDim.x, s.sempty, s.sfull, &s.abort_flag,
                              status);
   } else if (warp >= EPI_WARP0) {
     // ---------------- epilogue
@@ -500,8 +502,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int r = quarter * 32 + lane;
     const uint32_t tq = tmem_base + ((uint32_t)(quarter * 32) << 16);
     const float ag = args.a_g ? *args.a_g : 1.0f;
-    const fp4::Scale hg(args.mode == 0 ? args.out_g : nullptr);
-    const int chunks = args.mode == 0 || !args.f32 ? 4 : 8;  // 32 columns of H, runs of 64 bf16 or 32 fp32 columns
+    const fp4::Scale hg(OUT == kCodes ? args.out_g : nullptr);
+    const bool f32 = OUT == kAny && args.f32;
+    const int chunks = f32 ? 8 : 4;  // 32 columns of H, runs of 64 bf16 or 32 fp32 columns
     int n = 0;
     for (int tile = blockIdx.x; tile < total; tile += gridDim.x, ++n) {
       const grp::Tile t = grp::decode(s.tb, G, args.n_tiles, tile, BM);
@@ -523,19 +526,12 @@ __global__ void __launch_bounds__(THREADS, 1)
       // with the tile before.
       for (int i = half; i < chunks; i += 2) {
         const int at = n & 1 ? i : chunks - 1 - i;
-        uint32_t w[32], u[32];  // 64 columns; mode 0: gate and up; fp32 rows: 32
+        uint32_t w[32], u[32];  // 64 columns; codes: gate and up; fp32 rows: 32
         if (any) {
-          if (args.mode == 0) {
-            tmem_ld32(tacc + 32 * at, w);
-            tmem_ld32(tacc + BN / 2 + 32 * at, u);
-          } else if (args.f32) {
-            tmem_ld32(tacc + 32 * at, w);
-          } else {
-            tmem_ld32(tacc + 64 * at, w);
-            tmem_ld32(tacc + 64 * at + 32, u);
-          }
+          tmem_ld32(tacc + (f32 || OUT == kCodes ? 32 : 64) * at, w);
+          if (!f32) tmem_ld32(tacc + (OUT == kCodes ? BN / 2 + 32 * at : 64 * at + 32), u);
           tmem_ld_wait_regs(w);
-          if (args.mode == 0 || !args.f32) tmem_ld_wait_regs(u);
+          if (!f32) tmem_ld_wait_regs(u);
         }
         if (i < 2) {
           tc_fence_before();
@@ -543,7 +539,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (lane == 0) mbar_arrive(&s.tfree);
         }
         if (!any) continue;
-        if (args.mode == 0) {
+        if (OUT == kCodes) {
           float h[32];
 #pragma unroll
           for (int j = 0; j < 32; ++j)
@@ -551,21 +547,27 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (valid) store_codes<FMT>(args, row, t.n_tile * (BN / 2) + 32 * at, h, hg);
           continue;
         }
-        if (args.f32) {
+        if (f32) {
 #pragma unroll
           for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(__uint_as_float(w[j]) * scale);
         } else {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
+          for (int j = 0; j < 16; ++j)
             w[j] = pack_bf16x2(__uint_as_float(w[2 * j]) * scale, __uint_as_float(w[2 * j + 1]) * scale);
-          }
 #pragma unroll
           for (int j = 0; j < 16; ++j)
             w[16 + j] = pack_bf16x2(__uint_as_float(u[2 * j]) * scale, __uint_as_float(u[2 * j + 1]) * scale);
         }
-        const int col = t.n_tile * BN + (args.f32 ? 32 : 64) * at;
-        if (col < args.N)
-          store_run(args, lane, w, (int64_t)t.a_row + quarter * 32, t.rows - quarter * 32, col, args.N - col);
+        const int col = t.n_tile * BN + (f32 ? 32 : 64) * at, elem = f32 ? 4 : 2;
+        char* out = static_cast<char*>(args.out) + (((int64_t)t.a_row + quarter * 32) * args.ldo + col) * elem;
+        const int rows = t.rows - quarter * 32, n = (args.N - col) * elem;  // rows and bytes of the run that exist
+        if (OUT == kLines) {
+          if (n > 0) store_lines<true>(out, args.ldo * elem, lane, w, rows);
+        } else if (args.aligned && n >= 128) {
+          store_lines<false>(out, args.ldo * elem, lane, w, rows);
+        } else if (n > 0) {
+          store_elements(out, args.ldo * elem, lane, w, rows, n, f32);
+        }
       }
     }
   }
@@ -580,6 +582,12 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 }  // namespace a4
+
+// bytes (32, 16 or fewer: 0) that every output row is aligned to
+int row_alignment(const GemmA4Desc& d) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(d.out) | (uintptr_t)(d.ldo * (d.f32 ? 4 : 2));
+  return at % 32 == 0 ? 32 : at % 16 == 0 ? 16 : 0;
+}
 
 a4::Args gemm_a4_args(const GemmA4Desc& d) {
   a4::Args a;
@@ -604,8 +612,7 @@ a4::Args gemm_a4_args(const GemmA4Desc& d) {
   a.b_g = d.Bg;
   a.bs_g = d.Bg_shared;
   a.ldo = d.ldo;
-  const uintptr_t mis = reinterpret_cast<uintptr_t>(d.out) | (uintptr_t)(d.ldo * (d.f32 ? 4 : 2));
-  a.vec = mis % 32 == 0 ? 32 : mis % 16 == 0 ? 16 : 0;
+  a.aligned = row_alignment(d) >= 16;
   a.out = d.out;
   a.out_scales = static_cast<uint8_t*>(d.out_scales);
   a.out_g = d.out_g;
@@ -621,9 +628,14 @@ cudaError_t launch_gemm_a4(const GemmA4Desc& d, cudaStream_t stream, std::string
     *err = "cuTensorMapEncodeTiled is not available from the driver";
     return e;
   }
-  using Kernel = decltype(&a4::gemm_a4_kernel<fp4::kNv, true>);
-  static const Kernel kernels[4] = {a4::gemm_a4_kernel<fp4::kNv, true>, a4::gemm_a4_kernel<fp4::kNv, false>,
-                                    a4::gemm_a4_kernel<fp4::kMx, true>, a4::gemm_a4_kernel<fp4::kMx, false>};
+  using namespace a4;
+  using Kernel = decltype(&gemm_a4_kernel<fp4::kNv, true, kCodes>);
+  // [format][scales in 16-byte pieces][output]
+  static const Kernel kernels[2][2][3] = {
+      {{gemm_a4_kernel<fp4::kNv, false, kCodes>, gemm_a4_kernel<fp4::kNv, false, kLines>, gemm_a4_kernel<fp4::kNv, false, kAny>},
+       {gemm_a4_kernel<fp4::kNv, true, kCodes>, gemm_a4_kernel<fp4::kNv, true, kLines>, gemm_a4_kernel<fp4::kNv, true, kAny>}},
+      {{gemm_a4_kernel<fp4::kMx, false, kCodes>, gemm_a4_kernel<fp4::kMx, false, kLines>, gemm_a4_kernel<fp4::kMx, false, kAny>},
+       {gemm_a4_kernel<fp4::kMx, true, kCodes>, gemm_a4_kernel<fp4::kMx, true, kLines>, gemm_a4_kernel<fp4::kMx, true, kAny>}}};
   // the dynamic shared-memory opt-in is a per-device function attribute
   static PerDevice<bool> attr;
   bool attr_set = false;
@@ -631,9 +643,10 @@ cudaError_t launch_gemm_a4(const GemmA4Desc& d, cudaStream_t stream, std::string
       attr,
       [](bool& v) {
         cudaError_t r = cudaSuccess;
-        for (Kernel k : kernels)
-          if (r == cudaSuccess)
-            r = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, a4::SMEM_BYTES);
+        for (const auto& by_scales : kernels)
+          for (const auto& by_output : by_scales)
+            for (Kernel k : by_output)
+              if (r == cudaSuccess) r = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
         v = r == cudaSuccess;
         return r;
       },
@@ -655,9 +668,9 @@ cudaError_t launch_gemm_a4(const GemmA4Desc& d, cudaStream_t stream, std::string
     *err = "cuTensorMapEncodeTiled rejected a 4-bit GEMM operand";
     return cudaErrorInvalidValue;
   }
-  const a4::Args a = gemm_a4_args(d);
-  kernels[(d.format == fp4::kNv ? 0 : 2) + (a4::scales_vec(d) ? 0 : 1)]<<<num_sms(), a4::THREADS, a4::SMEM_BYTES, stream>>>(tA, tA32,
-                                                                                                             tB, tBs, a);
+  const int out = d.mode == 0 ? kCodes : !d.f32 && d.N % 64 == 0 && row_alignment(d) == 32 ? kLines : kAny;
+  kernels[d.format == fp4::kNv ? 0 : 1][scales_vec(d)][out]<<<num_sms(), THREADS, SMEM_BYTES, stream>>>(
+      tA, tA32, tB, tBs, gemm_a4_args(d));
   return cudaGetLastError();
 }
 
