@@ -11,6 +11,11 @@
 // w = 1 / (e^c + e^(c - l)), c = min(m, 0): the sigmoid times e^-c, so that a row whose sigmoids all
 // underflow keeps its ratios. A row of nothing but -inf has no probabilities: its p are 0.
 //
+// One GB300, 65536 tokens x 256 experts, k 8, 24 sequences, fp32 logits: forward 22.5 us (3.1 TB/s: 67 MB of logits at
+// a copy's rate are 10 us; about 163 instructions a token and warp, and 5 us of the second kernel), backward 24.0 us
+// (5.6 TB/s of 6.8); bf16 logits 20.5 and 19.0 us. 512 tokens x 8 experts: 3.4 and 2.6 us, launch and memory latency.
+// Two rows in flight a warp instead of one, and three blocks an SM, changed nothing or spilled.
+//
 // Both directions read the logits once from HBM. A token is held by L lanes (L = E / 4 rounded up to a
 // power of two, at most 32; each lane groups of 4 consecutive experts), and the sums over tokens are
 // kept in registers while the tokens stream by; they are joined over the block in a fixed order, then

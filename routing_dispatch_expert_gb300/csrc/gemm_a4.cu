@@ -7,7 +7,8 @@
 //
 // A and B are e2m1 codes, two a byte, row-major along K, with a scale byte for 16 (NVFP4, e4m3) or 32
 // (MXFP4, e8m0) elements; the tensor core multiplies codes and scales itself and accumulates in fp32, so
-// nothing is expanded: a K block of 256 elements is one 128-byte swizzled row of shared memory.
+// nothing is expanded: a K block of 256 elements is one 128-byte swizzled row of shared memory. The fp32
+// product is rounded once, to the output; H is quantised from it without a bf16 step between.
 //
 //   * tiles of 128 rows x 256 columns (mode 0: 128 gate and the 128 matching up columns), persistent,
 //     one CTA per SM: a 4-stage ring of 48 KB for the codes (TMA), a 2-slot ring of 12 KB for the scales.
@@ -15,14 +16,26 @@
 //     of a step in lane r % 32 of column r / 32, repeated in the four lane quarters; `tcgen05.cp
 //     .32x128b.warpx4` copies 512 bytes of shared memory [32 lanes][4 columns][4 bytes] there. The scales
 //     stay row-major in HBM (the layout of the quantised weights, a plain copy of a checkpoint): six
-//     warps load 32-byte sectors of the rows and store them transposed, a 16-byte line per step.
+//     warps load 32-byte sectors of the rows and store them transposed, a 16-byte line per step. (16 bytes
+//     a row from each of four warps: 307 us where this takes 208, 8192 x 14336 x 4096 NVFP4.)
 //   * TMEM: two accumulators of 256 columns do not leave room for the scales, so they share 48: columns
 //     [0, 256) and [208, 464), scales in [464, 512). The epilogue reads the shared columns of a tile
-//     first and hands them over; the next tile's MMAs then run beside the rest of the epilogue.
-//   * eight epilogue warps, two per TMEM lane quarter, 32 columns at a time; in mode 0 a lane holds whole
-//     quantisation blocks of its row, so H is quantised in registers.
+//     first and hands them over; the next tile's MMAs then run beside the rest of the epilogue. (Two
+//     whole accumulators of 192 columns do without that wait, but a K block takes as long for fewer
+//     columns: 207 us where this takes 189.)
+//   * eight epilogue warps, two per TMEM lane quarter; in mode 0 a lane holds whole quantisation blocks
+//     of its row, so H is quantised in registers.
 //   * a tile of at most 96 rows loads only the 32-row boxes that hold rows (a few rows an expert: the
 //     weights are the traffic); the rest of the tile keeps stale codes, whose products are not stored.
+//
+// What bounds it (GB300, 2.07 GHz). Few rows a group: HBM; the experts of a 256-token step, 153 of 256 active, h
+// 7168, I 2048: 0.86 ms, 6.6 TB/s of 6.8 measured for a copy. Many rows: 8192 x 14336 x 4096 189 us (NVFP4, 5.1
+// PFLOP/s) and 169 us (MXFP4, 5.7), 8192 x 14336 x 16384 654 us (5.9): a K block takes 512 cycles of MMA and about
+// 600 with the scales' copies in the same queue, but 700 - 1000 while an epilogue stores (an SM sends L2 one
+// request a cycle: 384 of a K block for the codes, 96 for the scales, and 2048 a tile for its output), and a tile
+// boundary costs 1500 - 2000 (the accumulators' shared columns), which a short K feels most: 16384 x 7168 x 2048
+// 116 us (4.2 PFLOP/s). CTA pairs (tcgen05.mma.cta_group::2, 256 x 256 and 256 x 192) halve the codes' requests,
+// but each cta_group::2 scale copy holds the queue for about 40 cycles instead of 11: 225 - 265 us.
 #include <cuda.h>
 
 #include "common.cuh"
@@ -359,8 +372,8 @@ __device__ __forceinline__ void store_elements(char* out, int64_t pitch, int lan
   }
 }
 
-// What a kernel writes: H in 4 bits; bf16 rows that start on 32 bytes and have whole runs; any rows. A kernel for each,
-// because the roles of a CTA run different code at the same time and share the instruction caches.
+// What a kernel writes: H in 4 bits; bf16 rows that start on 32 bytes and have whole runs; any rows. A kernel for each:
+// in one for all three the epilogue's registers spilled.
 enum { kCodes, kLines, kAny };
 
 template <int FMT, bool VEC, int OUT>
