@@ -306,7 +306,8 @@ def _fp4_format(fmt):
 
 def _fp4_matrix(q, s, fmt, name):
     """(rows, cols) of a 4-bit matrix."""
-    _need(q, name + " codes", _u8, (None, None))
+    if not (isinstance(q, torch.Tensor) and q.dim() == 2 and _like(q, _u8, q.shape)):
+        _need(q, name + " codes", _u8, (None, None))
     rows, half = q.shape
     cols = 2 * half
     if not _like(s, _u8, (rows, cols // FP4_BLOCK[fmt])):
@@ -328,17 +329,21 @@ def quantize_fp4(x: torch.Tensor, fmt: str = "nvfp4", g: torch.Tensor | None = N
     bits: (codes uint8 [rows, cols/2], scales uint8 [rows, cols/16] for 'nvfp4', [rows, cols/32] for 'mxfp4').
     g: fp32 [1], the NVFP4 scale of the matrix (moe_quantize_fp4 in include/moe.h), None = 1."""
     f = _fp4_format(fmt)
-    _need(x, "x", tuple(ELEMENT_TYPES), (None, None), contiguous=False)
+    if not (isinstance(x, torch.Tensor) and x.dim() == 2 and x.is_cuda and x.dtype in ELEMENT_TYPES):
+        _need(x, "x", tuple(ELEMENT_TYPES), (None, None), contiguous=False)
     rows, cols = x.shape
     ldx, one = x.stride()
     if one != 1 and cols > 1:
         raise ValueError("the elements of a row of x must be contiguous")
+    n = cols // FP4_BLOCK[fmt]
     if q is None:
         q = torch.empty(rows, cols // 2, dtype=_u8, device=x.device)
+    elif not _like(q, _u8, (rows, cols // 2)):
+        _need(q, "q", _u8, (rows, cols // 2))
     if s is None:
-        s = torch.empty(rows, cols // FP4_BLOCK[fmt], dtype=_u8, device=x.device)
-    if not (_like(q, _u8, (rows, cols // 2)) and _like(s, _u8, (rows, cols // FP4_BLOCK[fmt]))):
-        raise ValueError(f"q and s must be contiguous uint8 CUDA tensors, those of a 4-bit matrix {(rows, cols)}")
+        s = torch.empty(rows, n, dtype=_u8, device=x.device)
+    elif not _like(s, _u8, (rows, n)):
+        _need(s, "s", _u8, (rows, n))
     _check((_lib or load()).moe_quantize_fp4(x.data_ptr(), ELEMENT_TYPES[x.dtype], rows, cols, ldx if rows > 1 else cols,
                                              f, _fp4_scale(g, "g"), q.data_ptr(), s.data_ptr(),
                                              _raw_stream(_current_device())))
@@ -352,7 +357,8 @@ def dequantize_fp4(q: torch.Tensor, s: torch.Tensor, fmt: str = "nvfp4", g: torc
     rows, cols = _fp4_matrix(q, s, fmt, "4-bit")
     if y is None:
         y = torch.empty(rows, cols, dtype=dtype, device=q.device)
-    _need(y, "y", tuple(ELEMENT_TYPES), (rows, cols))
+    if y.dtype not in ELEMENT_TYPES or not _like(y, y.dtype, (rows, cols)):
+        _need(y, "y", tuple(ELEMENT_TYPES), (rows, cols))
     _check((_lib or load()).moe_dequantize_fp4(q.data_ptr(), s.data_ptr(), rows, cols, f, _fp4_scale(g, "g"),
                                                ELEMENT_TYPES[y.dtype], y.data_ptr(), _raw_stream(_current_device())))
     return y
@@ -371,12 +377,14 @@ def matmul_fp4(aq, a_s, bq, b_s, fmt: str = "nvfp4", ga=None, gb=None, dtype=tor
     ldy = N
     if y is None:
         y = torch.empty(M, N, dtype=dtype, device=aq.device)
+        if dtype is not torch.bfloat16 and dtype is not _f32:
+            raise ValueError(f"y must be bf16 or fp32, not {dtype}")
     else:
+        _need(y, "y", (torch.bfloat16, _f32), (M, N), contiguous=False)
         if M > 1:
             ldy = y.stride(0)
         if N > 1 and y.stride(1) != 1:
             raise ValueError("the elements of a row of y must be contiguous")
-    _need(y, "y", (torch.bfloat16, torch.float32), (M, N), contiguous=False)
     if status is not None:
         _need(status, "status", _i32, (1,))
     _check((_lib or load()).moe_matmul_fp4(aq.data_ptr(), a_s.data_ptr(), _fp4_scale(ga, "ga"), bq.data_ptr(),
@@ -399,24 +407,30 @@ def _act(act: Fp4Activations | None):
     return None if act is None else ctypes.byref(act.struct)
 
 
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
 def dispatch_fp4(cfg, act: Fp4Activations | None, x, topk_idx, topk_w, counts, offsets, inv_pos, row_token, row_weight,
                  xq, xs, ws):
     """moe_dispatch_fp4: dispatch with the rows quantised to the 4 bits of cfg's weights."""
-    _check(load().moe_dispatch_fp4(ctypes.byref(cfg), _act(act), _ptr(x), _ptr(topk_idx), _ptr(topk_w), _ptr(counts),
-                                   _ptr(offsets), _ptr(inv_pos), _ptr(row_token), _ptr(row_weight), _ptr(xq), _ptr(xs),
-                                   _ptr(ws), ws.numel(), _stream()))
+    _check((_lib or load()).moe_dispatch_fp4(ctypes.byref(cfg), _act(act), _address(x), _address(topk_idx),
+                                             _address(topk_w), _address(counts), _address(offsets), _address(inv_pos),
+                                             _address(row_token), _address(row_weight), _address(xq), _address(xs),
+                                             _address(ws), ws.numel(), _raw_stream(_current_device())))
 
 
 def expert_ffn_fp4(cfg, weights: Weights, act: Fp4Activations | None, xq, xs, offsets, row_weight, yd, ws):
     """moe_expert_ffn_fp4: the experts on 4-bit rows."""
-    _check(load().moe_expert_ffn_fp4(ctypes.byref(cfg), ctypes.byref(weights.struct), _act(act), _ptr(xq), _ptr(xs),
-                                     _ptr(offsets), _ptr(row_weight), _ptr(yd), _ptr(ws), ws.numel(), _stream()))
+    _check((_lib or load()).moe_expert_ffn_fp4(ctypes.byref(cfg), ctypes.byref(weights.struct), _act(act), _address(xq),
+                                               _address(xs), _address(offsets), _address(row_weight), _address(yd),
+                                               _address(ws), ws.numel(), _raw_stream(_current_device())))
 
 
 def forward_fp4(cfg, x, weights: Weights, act: Fp4Activations | None, y, ws):
     """moe_forward_fp4: the whole layer with 4-bit rows and 4-bit weights (dtype 'nvfp4' or 'mxfp4')."""
-    _check(load().moe_forward_fp4(ctypes.byref(cfg), _ptr(x), ctypes.byref(weights.struct), _act(act), _ptr(y),
-                                  _ptr(ws), ws.numel(), _stream()))
+    _check((_lib or load()).moe_forward_fp4(ctypes.byref(cfg), _address(x), ctypes.byref(weights.struct), _act(act),
+                                            _address(y), _address(ws), ws.numel(), _raw_stream(_current_device())))
 
 
 def balance_loss_workspace(cfg: MoeConfig, n_seq: int = 1, device="cuda") -> torch.Tensor:
@@ -431,11 +445,13 @@ def _balance_inputs(cfg, logits, seq_offsets, token_mask):
         _need(logits, "logits", (_f32, torch.bfloat16), (cfg.T, cfg.E))
     mask = offsets = None
     if token_mask is not None:
-        _need(token_mask, "token_mask", (_u8, torch.bool), (cfg.T,))
+        if not (_like(token_mask, _u8, (cfg.T,)) or _like(token_mask, torch.bool, (cfg.T,))):
+            _need(token_mask, "token_mask", (_u8, torch.bool), (cfg.T,))
         mask = token_mask.data_ptr()
     n_seq = 1
     if seq_offsets is not None:
-        _need(seq_offsets, "seq_offsets", _i32, (None,))
+        if not (isinstance(seq_offsets, torch.Tensor) and _like(seq_offsets, _i32, (seq_offsets.numel(),))):
+            _need(seq_offsets, "seq_offsets", _i32, (None,))
         n_seq = seq_offsets.shape[0] - 1
         if n_seq < 1:
             raise ValueError("seq_offsets must hold the begin of each sequence and the end of the last")
