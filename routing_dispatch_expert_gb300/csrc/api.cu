@@ -640,6 +640,7 @@ int do_expert_ffn_fp4(const moe_config* c, const moe_weights* w, const Fp4Rows& 
   g.out_g = nullptr;
   g.ldo = c->h;
   g.row_weight = row_weight;
+  g.after_gemm = true;
   e = moe::launch_gemm_a4(g, stream, &err);
   if (e != cudaSuccess) return err.empty() ? cuda_fail(e, "4-bit down GEMM launch") : cuda_fail(e, err.c_str());
   counted(2);

@@ -38,6 +38,8 @@
 // but each cta_group::2 scale copy holds the queue for about 40 cycles instead of 11: 225 - 265 us.
 #include <cuda.h>
 
+#include <algorithm>
+
 #include "common.cuh"
 #include "fp4_impl.cuh"
 #include "gemm_common.cuh"
@@ -415,6 +417,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     tmem_alloc(&s.tmem_slot, 512);
     tmem_relinquish();
   }
+  // the kernel behind this one in the stream may set itself up now; this one waits here for the one before it
+  // (launch_gemm_a4 says which), after its own set-up, which reads offsets that were there before that one began
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -682,9 +688,22 @@ cudaError_t launch_gemm_a4(const GemmA4Desc& d, cudaStream_t stream, std::string
     return cudaErrorInvalidValue;
   }
   const int out = d.mode == 0 ? kCodes : !d.f32 && d.N % 64 == 0 && row_alignment(d) == 32 ? kLines : kAny;
-  kernels[d.format == fp4::kNv ? 0 : 1][scales_vec(d)][out]<<<num_sms(), THREADS, SMEM_BYTES, stream>>>(
-      tA, tA32, tB, tBs, gemm_a4_args(d));
-  return cudaGetLastError();
+  // at most one CTA a tile: the groups' whole tiles, and one short tile each
+  const int64_t rows = d.offsets ? (int64_t)d.R + (d.B_shared ? d.T : 0) : d.T;
+  const int64_t groups = d.offsets ? std::min<int64_t>(d.E + (d.B_shared ? 1 : 0), rows) : 1;
+  const Args args = gemm_a4_args(d);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(num_sms(), (rows / BM + groups) * args.n_tiles));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = SMEM_BYTES;
+  cfg.stream = stream;
+  cfg.attrs = pdl;
+  cfg.numAttrs = d.after_gemm ? 1 : 0;
+  e = cudaLaunchKernelEx(&cfg, kernels[d.format == fp4::kNv ? 0 : 1][scales_vec(d)][out], tA, tA32, tB, tBs, args);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace moe

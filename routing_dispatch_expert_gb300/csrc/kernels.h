@@ -230,6 +230,9 @@ struct GemmA4Desc {
   int64_t ldo;               // elements
   const float* row_weight = nullptr;
   int* status;               // nullptr: a wait that gives up is not recorded
+  // the launch before this one in the stream is a launch_gemm_a4 that itself waited for all work before it: this
+  // kernel sets itself up beside that one's end
+  bool after_gemm = false;
 };
 cudaError_t launch_gemm_a4(const GemmA4Desc& d, cudaStream_t stream, std::string* err);
 
