@@ -16,8 +16,9 @@
 //     of a step in lane r % 32 of column r / 32, repeated in the four lane quarters; `tcgen05.cp
 //     .32x128b.warpx4` copies 512 bytes of shared memory [32 lanes][4 columns][4 bytes] there. The scales
 //     stay row-major in HBM (the layout of the quantised weights, a plain copy of a checkpoint): six
-//     warps load 32-byte sectors of the rows and store them transposed, a 16-byte line per step. (16 bytes
-//     a row from each of four warps: 307 us where this takes 208, 8192 x 14336 x 4096 NVFP4.)
+//     warps load 32-byte sectors of the rows, one or two at once, and store them transposed, a 16-byte line
+//     per step. (16 bytes a row from each of four warps: 307 us where sectors took 208, 8192 x 14336 x 4096
+//     NVFP4.)
 //   * TMEM: two accumulators of 256 columns do not leave room for the scales, so they share 48: columns
 //     [0, 256) and [208, 464), scales in [464, 512). The epilogue reads the shared columns of a tile
 //     first and hands them over; the next tile's MMAs then run beside the rest of the epilogue. (Two
@@ -29,12 +30,12 @@
 //     weights are the traffic); the rest of the tile keeps stale codes, whose products are not stored.
 //
 // What bounds it (GB300, 2.07 GHz). Few rows a group: HBM; the experts of a 256-token step, 153 of 256 active, h
-// 7168, I 2048: 0.86 ms, 6.6 TB/s of 6.8 measured for a copy. Many rows: 8192 x 14336 x 4096 189 us (NVFP4, 5.1
-// PFLOP/s) and 169 us (MXFP4, 5.7), 8192 x 14336 x 16384 654 us (5.9): a K block takes 512 cycles of MMA and about
+// 7168, I 2048: 0.81 ms, 6.9 TB/s (6.8 measured for a copy). Many rows: 8192 x 14336 x 4096 178 us (NVFP4, 5.4
+// PFLOP/s) and 165 us (MXFP4, 5.8): a K block takes 512 cycles of MMA and about
 // 600 with the scales' copies in the same queue, but 700 - 1000 while an epilogue stores (an SM sends L2 one
 // request a cycle: 384 of a K block for the codes, 96 for the scales, and 2048 a tile for its output), and a tile
 // boundary costs 1500 - 2000 (the accumulators' shared columns), which a short K feels most: 16384 x 7168 x 2048
-// 116 us (4.2 PFLOP/s). CTA pairs (tcgen05.mma.cta_group::2, 256 x 256 and 256 x 192) halve the codes' requests,
+// 105 us (4.6 PFLOP/s). With nothing stored these take 166 and 91 us, with no scales loaded 164 and 97. CTA pairs (tcgen05.mma.cta_group::2, 256 x 256 and 256 x 192) halve the codes' requests,
 // but each cta_group::2 scale copy holds the queue for about 40 cycles instead of 11: 225 - 265 us.
 #include <cuda.h>
 
@@ -86,6 +87,7 @@ struct Args {
   const float* bs_g;
   int64_t ldo;
   int aligned;  // output rows start on 16 bytes
+  int scales32;  // all scales' addresses are on 32 bytes
   void* out;
   uint8_t* out_scales;
   const float* out_g;
@@ -183,17 +185,30 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, ui
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-// 16 scale bytes of a row at p, of which the row has `left` (more, fewer or none): the rest are 0.
+// 32 scale bytes of a row at p, of which the row has `left` (more, fewer or none): the rest are 0. `whole`: rows are
+// whole 32-byte sectors; with VEC alone they are whole 16-byte halves.
 template <bool VEC>
-__device__ __forceinline__ uint4 load_scales(const uint8_t* p, int left) {
-  if constexpr (VEC) {
-    return left > 0 ? *reinterpret_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0);
-  } else {
-    uint32_t w[4] = {0, 0, 0, 0};
+__device__ __forceinline__ void load_scales(uint32_t (&w)[8], const uint8_t* p, int left, bool whole) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
+  for (int i = 0; i < 8; ++i) w[i] = 0;
+  if constexpr (VEC) {
+    if (whole) {
+      if (left > 0)
+        asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                     : "l"(p));
+      return;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (left <= 16 * h) continue;
+      const uint4 v = reinterpret_cast<const uint4*>(p)[h];
+      w[4 * h] = v.x, w[4 * h + 1] = v.y, w[4 * h + 2] = v.z, w[4 * h + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
       if (i < left) w[i / 4] |= (uint32_t)p[i] << (8 * (i % 4));
-    return make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
@@ -219,28 +234,36 @@ __device__ __forceinline__ void issue_k_block(uint32_t one, uint32_t tmem, uint3
   }
 }
 
-// Scale producers: three warps a slot, one for each 128-row block (A, the first and the second of B), and two such
-// groups in turn. Lanes 2 i and 2 i + 1 hold the two 16-byte halves of the 32-byte sector of rows l, l + 32, l + 64,
-// l + 96: whole sectors from L2, and one 16-byte line of shared memory for each word of the slot. A group issues the
-// loads of its next slot as soon as it has stored this one, and they land while the other group's slot is used (each
-// group has a slot of its own: it never waits for one more than a phase ahead, which a parity could not tell).
-// Tiles first, first + step, ...
+// Scale producers: six warps, two for each 128-row block (A, the first and the second of B). A lane stores a 16-byte
+// line for each word of a slot, of rows l, l + 32, l + 64 and l + 96.
+//
+// NVFP4: both warps of a block fill every slot, 16 of its lines each. Even lanes load a slot's sector of their rows
+// and odd lanes the next slot's, so that a row is asked for once in two slots (8192 x 14336 x 4096: 178 us; with a
+// sector at a time, as below, 191).
+// MXFP4, with half as many scales: each warp of a block has a slot of its own and loads a sector of all rows for it
+// (8192 x 14336 x 4096 and 16384 x 7168 x 2048: 165 and 97 us; two sectors at once, which is a tile's whole row in the
+// second, 166 and 100). Rows that are loaded byte by byte go the first way, for fewer rows an instruction.
+//
+// The next loads are issued once the last sector is stored, a slot's use ahead of the first wait for room. No warp
+// waits for a slot more than a phase ahead, which a parity could not tell. Tiles first, first + step, ...
+template <int FMT, bool VEC>
+constexpr int kPiece = FMT == fp4::kNv || !VEC ? 2 : 1;  // sectors of a row loaded at once, and warps that fill a slot's block
 template <int FMT, bool VEC, bool SWIGLU>
 __device__ __forceinline__ void scale_producer(const Args& args, const grp::Table& tb, int warp, int lane, uint32_t slots,
                                                int first, int step, uint64_t* sempty, uint64_t* sfull,
                                                volatile int* abort_flag, int* status) {
-  static_assert(SLOTS == 2 && SCALE_WARPS == 6, "a group of three warps for each slot");
+  constexpr int PIECE = kPiece<FMT, VEC>;
+  static_assert(SLOTS == 2 && SCALE_WARPS == 6 && SLOT_WORDS == 8, "two warps a block, a sector a slot");
   const int G = args.E + args.shared;
   const int total = tb.gtile[G] * args.n_tiles;
   const int kblocks = (args.K + BK - 1) / BK;
-  const int slot = (warp - SCALE_WARP0) / 3, block = (warp - SCALE_WARP0) % 3;
-  const int line = lane >> 1, part = lane & 1;  // and line + 16
+  const int block = (warp - SCALE_WARP0) >> 1, member = (warp - SCALE_WARP0) & 1;
+  const int line = PIECE == 1 ? lane : 16 * member + lane / 2, q = PIECE == 1 ? 0 : lane % 2;
   const int pitch = args.K / fp4::kBlock<FMT>;
+  const bool whole = pitch % 32 == 0 && args.scales32;
   const int per_tile = (kblocks + kSlotBlocks<FMT> - 1) / kSlotBlocks<FMT>;
-  const uint32_t dst = slots + slot * SLOT_BYTES + (uint32_t)((4 * part * 3 + block) * 512 + 16 * line);
-  uint32_t phase = 0;
-  // fill number i of this CTA is slot i % 2: this group's fills are those of its parity
-  int fill = 0;
+  const uint32_t dst = slots + (uint32_t)(block * 512 + 16 * line);
+  int fill = 0;  // fill number i of this CTA is slot i % 2
   for (int tile = first; tile < total; tile += step) {
     const grp::Tile t = grp::decode(tb, G, args.n_tiles, tile, BM);
     const bool routed = t.g < args.E;
@@ -250,30 +273,34 @@ __device__ __forceinline__ void scale_producer(const Args& args, const grp::Tabl
     const int rows = block == 0 ? args.a_rows : args.b_rows;
     const uint8_t* base = block == 0 ? args.a_scales
                       : (routed ? args.b_scales : args.bs_scales) + z * args.b_rows * (int64_t)pitch;
-    const uint8_t* p[8];
+    const uint8_t* p[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)  // rows past the end take the last one's scales: they are not stored
-      p[i] = base + min(r0 + line + 16 * (i & 1) + 32 * (i >> 1), rows - 1) * (int64_t)pitch + 16 * part;
-    for (int j = 0; j < per_tile; ++j, ++fill) {
-      if ((fill & 1) != slot) continue;
-      uint4 v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        v[i] = load_scales<VEC>(p[i] + j * (4 * SLOT_WORDS), pitch - j * (4 * SLOT_WORDS) - 16 * part);
-      const int got = wait_or_abort(&sempty[slot], phase ^ 1, abort_flag, status, args.wait_limit);
-      if (!__all_sync(0xffffffffu, got)) return;
-      phase ^= 1;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t at = dst + 256 * h;
-        sts128(at, v[h].x, v[2 + h].x, v[4 + h].x, v[6 + h].x);
-        sts128(at + 1536, v[h].y, v[2 + h].y, v[4 + h].y, v[6 + h].y);
-        sts128(at + 2 * 1536, v[h].z, v[2 + h].z, v[4 + h].z, v[6 + h].z);
-        sts128(at + 3 * 1536, v[h].w, v[2 + h].w, v[4 + h].w, v[6 + h].w);
+    for (int j = 0; j < 4; ++j)  // rows past the end take the last one's scales: they are not stored
+      p[j] = base + min(r0 + line + 32 * j, rows - 1) * (int64_t)pitch + 32 * q;
+    for (int f = 0; f < per_tile; f += PIECE) {
+      if (PIECE == 1 && (fill & 1) != member) {
+        ++fill;
+        continue;
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sfull[slot]);
+      uint32_t v[4][8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) load_scales<VEC>(v[j], p[j] + 32 * f, pitch - 32 * (f + q), whole);
+#pragma unroll
+      for (int o = 0; o < PIECE; ++o) {
+        if (f + o >= per_tile) break;
+        const int slot = fill & 1;
+        const int got = wait_or_abort(&sempty[slot], (uint32_t)(fill >> 1 & 1) ^ 1, abort_flag, status, args.wait_limit);
+        if (!__all_sync(0xffffffffu, got)) return;
+        ++fill;
+        if (q == o) {
+#pragma unroll
+          for (int w = 0; w < 8; ++w)
+            sts128(dst + slot * SLOT_BYTES + 1536 * w, v[0][w], v[1][w], v[2][w], v[3][w]);
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sfull[slot]);
+      }
     }
   }
 }
@@ -398,7 +425,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         mbar_init(&s.empty[i], 1);
       }
       for (int i = 0; i < SLOTS; ++i) {
-        mbar_init(&s.sfull[i], SCALE_WARPS / 2);
+        mbar_init(&s.sfull[i], 3 * kPiece<FMT, VEC>);
         mbar_init(&s.sempty[i], 1);
       }
       mbar_init(&s.tfull[0], 1);
@@ -630,6 +657,8 @@ a4::Args gemm_a4_args(const GemmA4Desc& d) {
   a.a_g = d.Ag;
   a.b_g = d.Bg;
   a.bs_g = d.Bg_shared;
+  a.scales32 = ((reinterpret_cast<uintptr_t>(d.As) | reinterpret_cast<uintptr_t>(d.Bs) |
+                 reinterpret_cast<uintptr_t>(d.Bs_shared)) & 31) == 0;
   a.ldo = d.ldo;
   a.aligned = row_alignment(d) >= 16;
   a.out = d.out;
