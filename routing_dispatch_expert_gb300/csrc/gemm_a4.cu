@@ -23,20 +23,25 @@
 //     [0, 256) and [208, 464), scales in [464, 512). The epilogue reads the shared columns of a tile
 //     first and hands them over; the next tile's MMAs then run beside the rest of the epilogue. (Two
 //     whole accumulators of 192 columns do without that wait, but a K block takes as long for fewer
-//     columns: 207 us where this takes 189.)
+//     columns: 207 us where this took 189.)
+//   * few tiles: of 64 columns each (mode 0: 32 + 32), in a ring of 8 stages of 24 KB, so that more SMs load the
+//     weights. (A cluster of 2 - 8 CTAs that shares a tile's K and adds its sums through distributed shared memory
+//     gained only past K = 4096, and cost 2 us otherwise: 1 x 4096 x 14336 25 -> 16 us, 1 x 7168 x 2048 7.2 -> 9.1.)
 //   * eight epilogue warps, two per TMEM lane quarter; in mode 0 a lane holds whole quantisation blocks
 //     of its row, so H is quantised in registers.
 //   * a tile of at most 96 rows loads only the 32-row boxes that hold rows (a few rows an expert: the
 //     weights are the traffic); the rest of the tile keeps stale codes, whose products are not stored.
 //
 // What bounds it (GB300, 2.07 GHz). Few rows a group: HBM; the experts of a 256-token step, 153 of 256 active, h
-// 7168, I 2048: 0.81 ms, 6.9 TB/s (6.8 measured for a copy). Many rows: 8192 x 14336 x 4096 178 us (NVFP4, 5.4
-// PFLOP/s) and 165 us (MXFP4, 5.8): a K block takes 512 cycles of MMA and about
-// 600 with the scales' copies in the same queue, but 700 - 1000 while an epilogue stores (an SM sends L2 one
-// request a cycle: 384 of a K block for the codes, 96 for the scales, and 2048 a tile for its output), and a tile
-// boundary costs 1500 - 2000 (the accumulators' shared columns), which a short K feels most: 16384 x 7168 x 2048
-// 105 us (4.6 PFLOP/s). With nothing stored these take 166 and 91 us, with no scales loaded 164 and 97. CTA pairs (tcgen05.mma.cta_group::2, 256 x 256 and 256 x 192) halve the codes' requests,
-// but each cta_group::2 scale copy holds the queue for about 40 cycles instead of 11: 225 - 265 us.
+// 7168, I 2048: 0.81 - 0.83 ms, 6.8 TB/s (a copy: 6.8). Many rows: 8192 x 14336 x 4096 178 us (NVFP4, 5.4 PFLOP/s)
+// and 165 us (MXFP4, 5.8): a K block takes 512 cycles of MMA and about 600 with the scales' copies in the same
+// queue, but 700 - 1000 while an epilogue stores: an SM sends L2 one request a cycle, 384 of a K block for the codes,
+// 96 for the scales, and 2048 a tile for its output. A short K feels the last most: 16384 x 7168 x 2048 105 us (4.6
+// PFLOP/s). Without the stores the two NVFP4 products would take 166 and 91 us, without half of B's codes 177 and 112
+// when they took 190 and 116. The wait at a tile boundary hides behind those requests (a first K block in two
+// halves, the one without shared columns before the wait: no change). CTA pairs (tcgen05.mma.cta_group::2, 256 x 256
+// and 256 x 192) halve the codes' requests, but each cta_group::2 scale copy holds the queue for about 40 cycles
+// instead of 11: 225 - 265 us. A single token: launch, set-up and 8 K blocks in a row, 6.2 us for 7168 x 2048.
 #include <cuda.h>
 
 #include <algorithm>
@@ -50,12 +55,18 @@ namespace moe {
 namespace a4 {
 
 constexpr int BM = 128;
-constexpr int BN = 256;
-constexpr int BK = 256;  // elements of a K block: 128 bytes of codes
-constexpr int STAGES = 4;
+constexpr int BN = 256;        // columns of a wide tile
+constexpr int BN_NARROW = 64;  // of a narrow one
+constexpr int BK = 256;        // elements of a K block: 128 bytes of codes
 constexpr int A_BYTES = BM * BK / 2;
-constexpr int B_BYTES = BN * BK / 2;
-constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+template <int NB>
+constexpr int kBBytes = NB * BK / 2;
+template <int NB>
+constexpr int kStageBytes = A_BYTES + kBBytes<NB>;
+constexpr int RING_BYTES = 4 * kStageBytes<BN>;
+template <int NB>
+constexpr int kStages = RING_BYTES / kStageBytes<NB>;  // 4 or 8
+constexpr int MAX_STAGES = kStages<BN_NARROW>;
 constexpr int SLOTS = 2;                 // ring of scales
 constexpr int SLOT_WORDS = 8;            // 4-byte words of scales of a row in a slot: a 32-byte sector
 constexpr int SLOT_BYTES = SLOT_WORDS * (BM + BN) * 4;
@@ -72,7 +83,7 @@ constexpr int ACC1 = 208;    // column of the second accumulator
 constexpr int SFA_COL = 464;
 constexpr int SFB_COL = 480;
 
-constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + SLOTS * SLOT_BYTES + 1024;
+constexpr int SMEM_BYTES = RING_BYTES + SLOTS * SLOT_BYTES + 1024;
 
 struct Args {
   const int32_t* offsets;
@@ -97,8 +108,8 @@ struct Args {
 };
 
 struct Shared {
-  uint64_t full[STAGES];
-  uint64_t empty[STAGES];
+  uint64_t full[MAX_STAGES];
+  uint64_t empty[MAX_STAGES];
   uint64_t sfull[SLOTS];
   uint64_t sempty[SLOTS];
   uint64_t tfull[2];
@@ -214,16 +225,16 @@ __device__ __forceinline__ void load_scales(uint32_t (&w)[8], const uint8_t* p, 
 
 // The scales' copies and the MMAs of one K block: codes at a (A) and b (B), scales of its words at sf. Copies and
 // MMAs of one thread run in order: the copies wait for the MMAs that read the columns they write.
-template <int FMT>
+template <int FMT, int NB>
 __device__ __forceinline__ void issue_k_block(uint32_t one, uint32_t tmem, uint32_t d, uint32_t a, uint32_t b, uint32_t sf,
                                               bool first) {
-  constexpr uint32_t IDESC = idesc_fp4<FMT>(BM, BN);
+  constexpr uint32_t IDESC = idesc_fp4<FMT>(BM, NB);
   const uint32_t da = operand_desc(a), db = operand_desc(b), ds = scales_desc(sf);
 #pragma unroll
   for (int i = 0; i < kWords<FMT>; ++i) {
     copy_scales(one, tmem + SFA_COL + 4 * i, ds + 96 * i);
     copy_scales(one, tmem + SFB_COL + 8 * i, ds + 96 * i + 32);
-    copy_scales(one, tmem + SFB_COL + 8 * i + 4, ds + 96 * i + 64);
+    if (NB > 128) copy_scales(one, tmem + SFB_COL + 8 * i + 4, ds + 96 * i + 64);
   }
 #pragma unroll
   for (int kk = 0; kk < BK / 64; ++kk) {
@@ -248,7 +259,7 @@ __device__ __forceinline__ void issue_k_block(uint32_t one, uint32_t tmem, uint3
 // waits for a slot more than a phase ahead, which a parity could not tell. Tiles first, first + step, ...
 template <int FMT, bool VEC>
 constexpr int kPiece = FMT == fp4::kNv || !VEC ? 2 : 1;  // sectors of a row loaded at once, and warps that fill a slot's block
-template <int FMT, bool VEC, bool SWIGLU>
+template <int FMT, bool VEC, bool SWIGLU, int NB>
 __device__ __forceinline__ void scale_producer(const Args& args, const grp::Table& tb, int warp, int lane, uint32_t slots,
                                                int first, int step, uint64_t* sempty, uint64_t* sfull,
                                                volatile int* abort_flag, int* status) {
@@ -258,6 +269,7 @@ __device__ __forceinline__ void scale_producer(const Args& args, const grp::Tabl
   const int total = tb.gtile[G] * args.n_tiles;
   const int kblocks = (args.K + BK - 1) / BK;
   const int block = (warp - SCALE_WARP0) >> 1, member = (warp - SCALE_WARP0) & 1;
+  if (NB <= 128 && block == 2) return;
   const int line = PIECE == 1 ? lane : 16 * member + lane / 2, q = PIECE == 1 ? 0 : lane % 2;
   const int pitch = args.K / fp4::kBlock<FMT>;
   const bool whole = pitch % 32 == 0 && args.scales32;
@@ -268,15 +280,20 @@ __device__ __forceinline__ void scale_producer(const Args& args, const grp::Tabl
     const grp::Tile t = grp::decode(tb, G, args.n_tiles, tile, BM);
     const bool routed = t.g < args.E;
     const int64_t z = routed ? (args.slot_expert ? args.slot_expert[t.g] : t.g) : 0;
-    const int n0 = SWIGLU ? t.n_tile * (BN / 2) : t.n_tile * BN;
-    const int r0 = block == 0 ? t.a_row : block == 1 ? n0 : SWIGLU ? args.I + n0 : n0 + BN / 2;
+    const int n0 = SWIGLU ? t.n_tile * (NB / 2) : t.n_tile * NB;
+    const int n1 = SWIGLU ? args.I + n0 : n0 + NB / 2;
+    const int r0 = block == 0 ? t.a_row : block == 1 ? n0 : n1;
     const int rows = block == 0 ? args.a_rows : args.b_rows;
     const uint8_t* base = block == 0 ? args.a_scales
                       : (routed ? args.b_scales : args.bs_scales) + z * args.b_rows * (int64_t)pitch;
     const uint8_t* p[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)  // rows past the end take the last one's scales: they are not stored
-      p[j] = base + min(r0 + line + 32 * j, rows - 1) * (int64_t)pitch + 32 * q;
+    for (int j = 0; j < 4; ++j) {
+      // a narrow tile has two rows of B a line; the other words hold them again, and are not used
+      const int r = NB == 64 && block == 1 ? (j & 1 ? n1 : n0) : r0 + 32 * j;
+      // rows past the end take the last one's scales: they are not stored
+      p[j] = base + min(r + line, rows - 1) * (int64_t)pitch + 32 * q;
+    }
     for (int f = 0; f < per_tile; f += PIECE) {
       if (PIECE == 1 && (fill & 1) != member) {
         ++fill;
@@ -405,10 +422,11 @@ __device__ __forceinline__ void store_elements(char* out, int64_t pitch, int lan
 // in one for all three the epilogue's registers spilled.
 enum { kCodes, kLines, kAny };
 
-template <int FMT, bool VEC, int OUT>
+template <int FMT, bool VEC, int OUT, int NB>
 __global__ void __launch_bounds__(THREADS, 1)
     gemm_a4_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA32,
                    const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmBs, const Args args) {
+  constexpr int STAGES = kStages<NB>, B_BYTES = kBBytes<NB>, STAGE_BYTES = kStageBytes<NB>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared s;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -425,7 +443,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         mbar_init(&s.empty[i], 1);
       }
       for (int i = 0; i < SLOTS; ++i) {
-        mbar_init(&s.sfull[i], 3 * kPiece<FMT, VEC>);
+        mbar_init(&s.sfull[i], (NB > 128 ? 3 : 2) * kPiece<FMT, VEC>);
         mbar_init(&s.sempty[i], 1);
       }
       mbar_init(&s.tfull[0], 1);
@@ -454,7 +472,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t tmem_base = s.tmem_slot;
   const int total = s.tb.gtile[G] * args.n_tiles;
   const int kblocks = (args.K + BK - 1) / BK;
-  const uint32_t slots = smem_u32(smem) + STAGES * STAGE_BYTES;
+  const uint32_t slots = smem_u32(smem) + RING_BYTES;
 
   if (warp == 0 && lane == 0) {
     // ---------------- TMA producer
@@ -466,8 +484,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       const grp::Tile t = grp::decode(s.tb, G, args.n_tiles, tile, BM);
       const CUtensorMap* mb = t.g < args.E ? &tmB : &tmBs;
       const int z = t.g < args.E ? (args.slot_expert ? args.slot_expert[t.g] : t.g) : 0;
-      const int n0 = OUT == kCodes ? t.n_tile * (BN / 2) : t.n_tile * BN;
-      const int n1 = OUT == kCodes ? args.I + n0 : n0 + BN / 2;
+      const int n0 = OUT == kCodes ? t.n_tile * (NB / 2) : t.n_tile * NB;
+      const int n1 = OUT == kCodes ? args.I + n0 : n0 + NB / 2;
       const int boxes = (t.rows + 31) / 32;
       const uint32_t a_bytes = boxes == 4 ? A_BYTES : boxes * (A_BYTES / 4);
       for (int kb = 0; kb < kblocks; ++kb) {
@@ -484,7 +502,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int i = 0; i < boxes; ++i)
             tma_load_2d(a + i * (A_BYTES / 4), &tmA32, &s.full[stage], kb * (BK / 2), t.a_row + 32 * i);
         tma_load_3d(b, mb, &s.full[stage], kb * (BK / 2), n0, z);
-        tma_load_3d(b + B_BYTES / 2, mb, &s.full[stage], kb * (BK / 2), n1, z);
+        if (OUT == kCodes) tma_load_3d(b + B_BYTES / 2, mb, &s.full[stage], kb * (BK / 2), n1, z);
         ++issued;
         if (++stage == STAGES) {
           stage = 0;
@@ -520,7 +538,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t b = a + A_BYTES;
         const uint32_t sf = slots + slot * SLOT_BYTES + in_slot * kWords<FMT> * 3 * 512;
         const bool slot_done = in_slot == kSlotBlocks<FMT> - 1 || kb + 1 == kblocks;
-        issue_k_block<FMT>(leader, tmem_base, d, a, b, sf, kb == 0);
+        issue_k_block<FMT, NB>(leader, tmem_base, d, a, b, sf, kb == 0);
         if (slot_done) commit(leader, &s.sempty[slot]);
         commit(leader, &s.empty[stage]);
         if (kb + 1 == kblocks) commit(leader, &s.tfull[n & 1]);
@@ -540,8 +558,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     __syncwarp();
   } else if (warp >= SCALE_WARP0 && warp < EPI_WARP0) {
-    scale_producer<FMT, VEC, OUT == kCodes>(args, s.tb, warp, lane, slots, blockIdx.x, gridDim.x, s.sempty, s.sfull, &s.abort_flag,
-                             status);
+    scale_producer<FMT, VEC, OUT == kCodes, NB>(args, s.tb, warp, lane, slots, blockIdx.x, gridDim.x, s.sempty, s.sfull,
+                                                &s.abort_flag, status);
   } else if (warp >= EPI_WARP0) {
     // ---------------- epilogue
     const int quarter = warp & 3, half = (warp - EPI_WARP0) >> 2;
@@ -550,7 +568,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const float ag = args.a_g ? *args.a_g : 1.0f;
     const fp4::Scale hg(OUT == kCodes ? args.out_g : nullptr);
     const bool f32 = OUT == kAny && args.f32;
-    const int chunks = f32 ? 8 : 4;  // 32 columns of H, runs of 64 bf16 or 32 fp32 columns
+    const int chunks = NB / (f32 ? 32 : 64);  // 32 columns of H, runs of 64 bf16 or 32 fp32 columns
     int n = 0;
     for (int tile = blockIdx.x; tile < total; tile += gridDim.x, ++n) {
       const grp::Tile t = grp::decode(s.tb, G, args.n_tiles, tile, BM);
@@ -570,12 +588,17 @@ __global__ void __launch_bounds__(THREADS, 1)
       // 48 of the second), alternate ones for the two warps of a quarter: the shared columns lie in the first position
       // (of 64 columns) or the first two (of 32). A warp that reads none of them still says here that it is done
       // with the tile before.
+      if (half >= chunks) {  // a narrow tile has nothing for this warp
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.tfree);
+      }
       for (int i = half; i < chunks; i += 2) {
         const int at = n & 1 ? i : chunks - 1 - i;
         uint32_t w[32], u[32];  // 64 columns; codes: gate and up; fp32 rows: 32
         if (any) {
           tmem_ld32(tacc + (f32 || OUT == kCodes ? 32 : 64) * at, w);
-          if (!f32) tmem_ld32(tacc + (OUT == kCodes ? BN / 2 + 32 * at : 64 * at + 32), u);
+          if (!f32) tmem_ld32(tacc + (OUT == kCodes ? NB / 2 + 32 * at : 64 * at + 32), u);
           tmem_ld_wait_regs(w);
           if (!f32) tmem_ld_wait_regs(u);
         }
@@ -590,7 +613,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j)
             h[j] = grp::silu(__uint_as_float(w[j]) * scale) * (__uint_as_float(u[j]) * scale);
-          if (valid) store_codes<FMT>(args, row, t.n_tile * (BN / 2) + 32 * at, h, hg);
+          if (valid) store_codes<FMT>(args, row, t.n_tile * (NB / 2) + 32 * at, h, hg);
           continue;
         }
         if (f32) {
@@ -604,7 +627,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int j = 0; j < 16; ++j)
             w[16 + j] = pack_bf16x2(__uint_as_float(u[2 * j]) * scale, __uint_as_float(u[2 * j + 1]) * scale);
         }
-        const int col = t.n_tile * BN + (f32 ? 32 : 64) * at, elem = f32 ? 4 : 2;
+        const int col = t.n_tile * NB + (f32 ? 32 : 64) * at, elem = f32 ? 4 : 2;
         char* out = static_cast<char*>(args.out) + (((int64_t)t.a_row + quarter * 32) * args.ldo + col) * elem;
         const int rows = t.rows - quarter * 32, n = (args.N - col) * elem;  // rows and bytes of the run that exist
         if (OUT == kLines) {
@@ -635,7 +658,7 @@ int row_alignment(const GemmA4Desc& d) {
   return at % 32 == 0 ? 32 : at % 16 == 0 ? 16 : 0;
 }
 
-a4::Args gemm_a4_args(const GemmA4Desc& d) {
+a4::Args gemm_a4_args(const GemmA4Desc& d, int columns) {
   a4::Args a;
   a.offsets = d.offsets;
   a.slot_expert = d.slot_expert;
@@ -648,7 +671,7 @@ a4::Args gemm_a4_args(const GemmA4Desc& d) {
   a.mode = d.mode;
   a.I = d.I;
   a.f32 = d.f32;
-  a.n_tiles = d.mode == 0 ? d.I / (a4::BN / 2) : (int)cdiv(d.N, a4::BN);
+  a.n_tiles = d.mode == 0 ? d.I / (columns / 2) : (int)cdiv(d.N, columns);
   a.a_rows = (int)d.a_rows;
   a.b_rows = (int)d.b_rows;
   a.a_scales = static_cast<const uint8_t*>(d.As);
@@ -677,13 +700,16 @@ cudaError_t launch_gemm_a4(const GemmA4Desc& d, cudaStream_t stream, std::string
     return e;
   }
   using namespace a4;
-  using Kernel = decltype(&gemm_a4_kernel<fp4::kNv, true, kCodes>);
-  // [format][scales in 16-byte pieces][output]
-  static const Kernel kernels[2][2][3] = {
-      {{gemm_a4_kernel<fp4::kNv, false, kCodes>, gemm_a4_kernel<fp4::kNv, false, kLines>, gemm_a4_kernel<fp4::kNv, false, kAny>},
-       {gemm_a4_kernel<fp4::kNv, true, kCodes>, gemm_a4_kernel<fp4::kNv, true, kLines>, gemm_a4_kernel<fp4::kNv, true, kAny>}},
-      {{gemm_a4_kernel<fp4::kMx, false, kCodes>, gemm_a4_kernel<fp4::kMx, false, kLines>, gemm_a4_kernel<fp4::kMx, false, kAny>},
-       {gemm_a4_kernel<fp4::kMx, true, kCodes>, gemm_a4_kernel<fp4::kMx, true, kLines>, gemm_a4_kernel<fp4::kMx, true, kAny>}}};
+  using Kernel = decltype(&gemm_a4_kernel<fp4::kNv, true, kCodes, BN>);
+  // [narrow][format][scales in 16-byte pieces][output]
+#define MOE_A4_OUTPUTS(FMT, VEC, NB) \
+  {gemm_a4_kernel<FMT, VEC, kCodes, NB>, gemm_a4_kernel<FMT, VEC, kLines, NB>, gemm_a4_kernel<FMT, VEC, kAny, NB>}
+#define MOE_A4_FORMATS(NB)                                                      \
+  {{MOE_A4_OUTPUTS(fp4::kNv, false, NB), MOE_A4_OUTPUTS(fp4::kNv, true, NB)},   \
+   {MOE_A4_OUTPUTS(fp4::kMx, false, NB), MOE_A4_OUTPUTS(fp4::kMx, true, NB)}}
+  static const Kernel kernels[2][2][2][3] = {MOE_A4_FORMATS(BN), MOE_A4_FORMATS(BN_NARROW)};
+#undef MOE_A4_FORMATS
+#undef MOE_A4_OUTPUTS
   // the dynamic shared-memory opt-in is a per-device function attribute
   static PerDevice<bool> attr;
   bool attr_set = false;
@@ -691,10 +717,9 @@ cudaError_t launch_gemm_a4(const GemmA4Desc& d, cudaStream_t stream, std::string
       attr,
       [](bool& v) {
         cudaError_t r = cudaSuccess;
-        for (const auto& by_scales : kernels)
-          for (const auto& by_output : by_scales)
-            for (Kernel k : by_output)
-              if (r == cudaSuccess) r = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+        const Kernel* all = &kernels[0][0][0][0];
+        for (size_t i = 0; i < sizeof(kernels) / sizeof(Kernel) && r == cudaSuccess; ++i)
+          r = cudaFuncSetAttribute(all[i], cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
         v = r == cudaSuccess;
         return r;
       },
@@ -703,35 +728,42 @@ cudaError_t launch_gemm_a4(const GemmA4Desc& d, cudaStream_t stream, std::string
     *err = "cudaFuncSetAttribute failed";
     return e;
   }
+  // row tiles: the groups' whole ones, and one short one each
+  const int64_t rows = d.offsets ? (int64_t)d.R + (d.B_shared ? d.T : 0) : d.T;
+  const int64_t groups = d.offsets ? std::min<int64_t>(d.E + (d.B_shared ? 1 : 0), rows) : 1;
+  const int64_t row_tiles = rows / BM + groups;
+  // Narrow tiles where all of them run at once. 128 x 7168 x 2048, 28 wide tiles: 5.9 us, wide 7.6 (NVFP4); 128 x 4096 x
+  // 7168, 16: 10.4 and 15.1; 64 rows on 8 experts, h 512, I 256: 8.7 and 10.8. 128 x 14336 x 4096, 56: 12.9 and 11.8.
+  const int64_t wide_tiles = row_tiles * (d.mode == 0 ? d.I / (BN / 2) : cdiv(d.N, BN));
+  const bool narrow = wide_tiles * (BN / BN_NARROW) <= num_sms();
+  const int columns = narrow ? BN_NARROW : BN;
+  const Args args = gemm_a4_args(d, columns);
   CUtensorMap tA, tA32, tB, tBs;
+  const int b_box = d.mode == 0 ? columns / 2 : columns;
   const CUtensorMapDataType U8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   // an encode costs a small call about a microsecond: a map that no tile uses is a copy of another
   bool ok = tma_encode_2d(&tA32, d.A, U8, 1, d.a_rows, d.K / 2, a4::BM / 4) &&
-            tma_encode_3d(&tB, d.B, U8, 1, d.n_experts, d.b_rows, d.K / 2, a4::BN / 2);
+            tma_encode_3d(&tB, d.B, U8, 1, d.n_experts, d.b_rows, d.K / 2, b_box);
   tA = tA32;
   tBs = tB;
   if (d.a_rows > a4::BM - 32) ok = ok && tma_encode_2d(&tA, d.A, U8, 1, d.a_rows, d.K / 2, a4::BM);
-  if (d.B_shared) ok = ok && tma_encode_3d(&tBs, d.B_shared, U8, 1, 1, d.b_rows, d.K / 2, a4::BN / 2);
+  if (d.B_shared) ok = ok && tma_encode_3d(&tBs, d.B_shared, U8, 1, 1, d.b_rows, d.K / 2, b_box);
   if (!ok) {
     *err = "cuTensorMapEncodeTiled rejected a 4-bit GEMM operand";
     return cudaErrorInvalidValue;
   }
   const int out = d.mode == 0 ? kCodes : !d.f32 && d.N % 64 == 0 && row_alignment(d) == 32 ? kLines : kAny;
-  // at most one CTA a tile: the groups' whole tiles, and one short tile each
-  const int64_t rows = d.offsets ? (int64_t)d.R + (d.B_shared ? d.T : 0) : d.T;
-  const int64_t groups = d.offsets ? std::min<int64_t>(d.E + (d.B_shared ? 1 : 0), rows) : 1;
-  const Args args = gemm_a4_args(d);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute pdl[1];
   pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   pdl[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3((unsigned)std::min<int64_t>(num_sms(), (rows / BM + groups) * args.n_tiles));
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(num_sms(), row_tiles * args.n_tiles));
   cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = SMEM_BYTES;
   cfg.stream = stream;
   cfg.attrs = pdl;
   cfg.numAttrs = d.after_gemm ? 1 : 0;
-  e = cudaLaunchKernelEx(&cfg, kernels[d.format == fp4::kNv ? 0 : 1][scales_vec(d)][out], tA, tA32, tB, tBs, args);
+  e = cudaLaunchKernelEx(&cfg, kernels[narrow][d.format == fp4::kNv ? 0 : 1][scales_vec(d)][out], tA, tA32, tB, tBs, args);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

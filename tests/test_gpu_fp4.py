@@ -171,6 +171,38 @@ def test_matmul_scales_reach_their_rows(fmt):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M,N,K", [(1, 10001, 96), (33, 9985, 544), (130, 5130, 800), (640, 2304, 2080)])
+def test_matmul_with_more_tiles_than_run_narrow(fmt, M, N, K):
+    """Products whose 64-column tiles would not all run at once: 256-column tiles, with one and several row tiles."""
+    aq, a_s, ga, a = operand(M, K, fmt, 1)
+    bq, b_s, gb, b = operand(N, K, fmt, 2, 0.02)
+    ref, mag = a @ b.T, a.abs() @ b.abs().T
+    for dtype in (torch.bfloat16, torch.float32):
+        y = rde.matmul_fp4(aq, a_s, bq, b_s, fmt, ga, gb, dtype=dtype)
+        assert (y.double() - ref).abs().sub(product_tolerance(ref, mag, K, dtype)).amax() <= 0
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M,N,K", [(140, 300, 4608), (140, 5000, 4608), (256, 4864, 1024)])
+def test_matmul_scales_of_long_rows(fmt, M, N, K):
+    """As above in narrow and wide tiles, with several fills of the scales' ring: a scale of another row, block or fill
+    is off by a factor of two at least."""
+    n = plain.BLOCK[fmt]
+    gen = rng(12)
+
+    def one(rows):
+        x = torch.sign(torch.randn(rows, K, generator=gen, device="cuda")) * 4
+        e = torch.randint(-3, 4, (rows, K // n), generator=gen, device="cuda")
+        return rde.quantize_fp4(x * torch.exp2(e.float()).repeat_interleave(n, 1), fmt)
+
+    (aq, a_s), (bq, b_s) = one(M), one(N)
+    a, b = plain.values(aq, a_s, fmt), plain.values(bq, b_s, fmt)
+    y = rde.matmul_fp4(aq, a_s, bq, b_s, fmt, dtype=torch.float32)
+    ref, mag = a @ b.T, a.abs() @ b.abs().T
+    assert (y.double() - ref).abs().sub(product_tolerance(ref, mag, K, torch.float32)).amax() <= 0
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 def test_matmul_writes_nothing_else(fmt):
     """Rows of an output with gaps: the gaps, and the rows before and after, keep what they held."""
     M, N, K = 130, 70, 160
