@@ -163,9 +163,11 @@ __device__ __forceinline__ float lanes_sum(float v) {
 // l becomes w, and 1 / sum w is returned: the probabilities are w times it. With DERIV d becomes 1 - sigmoid(l).
 // The exponent is one fused multiply-add, fma(l, log2 e, -c log2 e): its own rounding is |x| 2^-24 for an exponent
 // x, that of c log2 e is the same for the whole row and cancels; ex2.approx and rcp.approx add 2 ulp and 1. In all
-// below 2e-6 down to probabilities of 1e-8 of the largest. Rows near the type's lowest value, where c log2 e would
-// overflow, are shifted first. A row of nothing but -inf has a sum of 0 and no probabilities; a NaN makes its
-// whole row NaN.
+// below 2e-6 down to probabilities of 1e-8 of the largest. The rounding that cancels is up to c 2^-25 in the exponent:
+// harmless for c of 1e6 (a factor of 2^0.05 in every w), but past 1e9, where rows masked with a large negative number
+// are, it would take every w to 0 or infinity. So the row is shifted first where c is large: l - c is exact or off by
+// 2^-24 of the difference. A row of nothing but -inf has a sum of 0 and no probabilities; a NaN makes its whole row NaN.
+constexpr float kShift = 1048576.0f;
 template <bool SIGMOID, bool DERIV, int L, int EPL>
 __device__ __forceinline__ float weights(float (&l)[EPL], float (&d)[DERIV ? EPL : 1]) {
   float m = l[0];
@@ -175,7 +177,7 @@ __device__ __forceinline__ float weights(float (&l)[EPL], float (&d)[DERIV ? EPL
   float c = m == -INFINITY ? 0.f : m;
   if (SIGMOID) c = fminf(c, 0.f);
   float ec = 0.f;
-  if (fabsf(c) > 1e30f) {
+  if (fabsf(c) > kShift) {
 #pragma unroll
     for (int i = 0; i < EPL; ++i) l[i] -= c;
     c = 0.f;  // and e^c is 0
