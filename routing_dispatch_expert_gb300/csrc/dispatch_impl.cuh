@@ -133,8 +133,9 @@ __device__ __forceinline__ void gather_fp4_item(const uint4* __restrict__ x, con
     if (c0 + 32 * u >= hv) break;
     float by, f[8];
     v[u].values(f);
-    const uint32_t scale = fp4::block_scale<FMT>(fp4::block_amax<FMT>(v[u].amax()), g, by);
-    const uint32_t q = fp4::codes8<FMT>(f, by);
+    const uint32_t amax = fp4::block_amax<FMT>(v[u].amax());
+    const uint32_t scale = fp4::block_scale<FMT>(amax, g, by);
+    const uint32_t q = fp4::codes8<FMT>(f, by, amax);
     for (int j = 0; j <= k; ++j) {
       int r;
       if (j < k) {

@@ -42,8 +42,10 @@ __device__ __forceinline__ float e8m0_value(uint32_t code) {
 // RN(a / b) for many a with one b, r = RN(1 / b): the product a r is corrected twice by its residual. After the
 // first correction it is a faithful quotient, and one more of a faithful quotient with a correctly rounded
 // reciprocal gives the rounded one (P. Markstein, IBM Journal of Research and Development 34, 1990). Held for
-// ordinary b only, where no residual underflows; others take the division itself.
+// ordinary b only, where no residual underflows, and for |a| below 1e18, where no quotient overflows (a quotient of
+// infinity would be corrected to a NaN); others take the division itself.
 __device__ __forceinline__ bool ordinary(float b) { return b > 1e-20f && b < 1e20f; }
+constexpr uint32_t kOrdinaryMax = 0x5D5E0B6Bu;  // the bits of 1e18
 // The residual is taken as q b - a and its product subtracted, which keeps the sign of a zero.
 __device__ __forceinline__ float2 quotient(float2 a, float2 b, float2 r) {
   const float2 na = __fmul2_rn(a, make_float2(-1.f, -1.f)), nr = make_float2(-r.x, -r.y);
@@ -73,7 +75,7 @@ __device__ __forceinline__ uint32_t block_scale(uint32_t amax_bits, const Scale&
       return 0x7F;
     }
     const float amax = __uint_as_float(amax_bits);
-    const float t = ordinary(sc.d) && amax < 1e30f
+    const float t = ordinary(sc.d) && amax_bits < kOrdinaryMax
                         ? quotient(make_float2(amax, 0.f), make_float2(sc.d, sc.d), make_float2(sc.r, sc.r)).x
                         : __fdiv_rn(amax, sc.d);
     const uint32_t code = __nv_cvt_float_to_fp8(t, __NV_SATFINITE, __NV_E4M3);
@@ -100,9 +102,10 @@ __device__ __forceinline__ uint32_t pack8(const float* y) {
 // Codes of 8 elements (element 2i in the low nibble of byte i). MXFP4: x times a power of two is exact.
 // NVFP4: the code of RN(x / step); quotients that are exactly the midpoint of two codes are common (a step is a few
 // bits times g, and g is usually made of one of the elements), so the product with a reciprocal alone, 2 ulp off,
-// would not do. The quotient by correction takes 6 instructions for two elements.
+// would not do. The quotient by correction takes 6 instructions for two elements. A block whose scale saturates (numbers
+// past 6 * 448 g) has quotients of any size. amax_bits: the block's largest magnitude.
 template <int FMT>
-__device__ __forceinline__ uint32_t codes8(const float* x, float by) {
+__device__ __forceinline__ uint32_t codes8(const float* x, float by, uint32_t amax_bits) {
   if (by == 0.f) return 0;
   float y[8];
   if (FMT == kMx) {
@@ -110,7 +113,7 @@ __device__ __forceinline__ uint32_t codes8(const float* x, float by) {
     for (int i = 0; i < 8; ++i) y[i] = x[i] * by;
     return pack8(y);
   }
-  if (ordinary(by)) {  // then |x| is at most about 2^12 times 1e20
+  if (ordinary(by) && amax_bits < kOrdinaryMax) {
     const float r = __frcp_rn(by);
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {

@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const void* __restri
 #pragma unroll
     for (int w = 0; w < W; ++w) {
       x8[i][w].values(v);
-      c[w] = codes8<FMT>(v, by);
+      c[w] = codes8<FMT>(v, by, m);
     }
     if (W == 2) {
       reinterpret_cast<uint2*>(q)[u] = make_uint2(c[0], c[W - 1]);

@@ -336,7 +336,7 @@ __device__ __forceinline__ void store_codes(const Args& args, int64_t row, int c
     float by;
     sc |= fp4::block_scale<FMT>(m, hg, by) << (8 * b);
 #pragma unroll
-    for (int j = 0; j < kBlk / 8; ++j) q[kBlk / 8 * b + j] = fp4::codes8<FMT>(h + kBlk * b + 8 * j, by);
+    for (int j = 0; j < kBlk / 8; ++j) q[kBlk / 8 * b + j] = fp4::codes8<FMT>(h + kBlk * b + 8 * j, by, m);
   }
   *reinterpret_cast<uint4*>(static_cast<uint8_t*>(args.out) + (row * args.ldo + col) / 2) =
       make_uint4(q[0], q[1], q[2], q[3]);
