@@ -629,13 +629,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         const int col = t.n_tile * NB + (f32 ? 32 : 64) * at, elem = f32 ? 4 : 2;
         char* out = static_cast<char*>(args.out) + (((int64_t)t.a_row + quarter * 32) * args.ldo + col) * elem;
-        const int rows = t.rows - quarter * 32, n = (args.N - col) * elem;  // rows and bytes of the run that exist
+        // rows, and bytes of the 128-byte run, that exist (N may be close to 2^31: not in bytes)
+        const int rows = t.rows - quarter * 32, run = min(args.N - col, 128 / elem) * elem;
         if (OUT == kLines) {
-          if (n > 0) store_lines<true>(out, args.ldo * elem, lane, w, rows);
-        } else if (args.aligned && n >= 128) {
+          if (run > 0) store_lines<true>(out, args.ldo * elem, lane, w, rows);
+        } else if (args.aligned && run == 128) {
           store_lines<false>(out, args.ldo * elem, lane, w, rows);
-        } else if (n > 0) {
-          store_elements(out, args.ldo * elem, lane, w, rows, n, f32);
+        } else if (run > 0) {
+          store_elements(out, args.ldo * elem, lane, w, rows, run, f32);
         }
       }
     }

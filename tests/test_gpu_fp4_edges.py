@@ -26,3 +26,18 @@ def test_quantize_numbers_far_past_the_scale(dtype, g):
     rq, rs = plain.quantize(x, "nvfp4", float(gt))
     assert torch.equal(s, rs)
     assert torch.equal(q, rq)
+
+
+def test_matmul_with_more_than_2_29_columns():
+    """Every column of a product whose rows are longer than 2^31 bytes is written (11 GB of operands and output)."""
+    N, K = (1 << 29) + 256, 32
+    aq = torch.full((1, K // 2), 0x22, dtype=torch.uint8, device="cuda")  # ones
+    bq = torch.full((N, K // 2), 0x22, dtype=torch.uint8, device="cuda")
+    bq[0], bq[12345], bq[-1] = 0x44, 0x33, 0x55  # 2, 1.5 and 3
+    one = lambda n: torch.full((n, 1), 127, dtype=torch.uint8, device="cuda")  # noqa: E731
+    y = torch.full((1, N), float("nan"), device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    rde.matmul_fp4(aq, one(1), bq, one(N), "mxfp4", y=y, status=status)
+    assert int(status) == 0
+    assert (float(y[0, 0]), float(y[0, 12345]), float(y[0, -1])) == (64.0, 48.0, 96.0)
+    assert int((y != 32).sum()) == 3
