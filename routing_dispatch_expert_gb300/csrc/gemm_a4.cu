@@ -48,6 +48,7 @@
 
 #include "common.cuh"
 #include "fp4_impl.cuh"
+#include "gemm_a4_host.h"
 #include "gemm_common.cuh"
 #include "kernels.h"
 
@@ -729,14 +730,14 @@ cudaError_t launch_gemm_a4(const GemmA4Desc& d, cudaStream_t stream, std::string
     *err = "cudaFuncSetAttribute failed";
     return e;
   }
-  // row tiles: the groups' whole ones, and one short one each
   const int64_t rows = d.offsets ? (int64_t)d.R + (d.B_shared ? d.T : 0) : d.T;
   const int64_t groups = d.offsets ? std::min<int64_t>(d.E + (d.B_shared ? 1 : 0), rows) : 1;
-  const int64_t row_tiles = rows / BM + groups;
-  // Narrow tiles where all of them run at once. 128 x 7168 x 2048, 28 wide tiles: 5.9 us, wide 7.6 (NVFP4); 128 x 4096 x
-  // 7168, 16: 10.4 and 15.1; 64 rows on 8 experts, h 512, I 256: 8.7 and 10.8. 128 x 14336 x 4096, 56: 12.9 and 11.8.
+  const int64_t row_tiles = row_tiles_at_most(rows, groups, BM);
+  // Narrow tiles where all of them run at once. NVFP4, narrow and wide: 128 x 7168 x 2048, 28 wide tiles: 5.7 us and
+  // 7.4; 256 x 4096 x 7168, 32: 10.7 and 15.2; 256 x 4864 x 4096, 38: 7.7 and 10.3; 64 rows on 8 experts, h 512, I 256:
+  // 8.7 and 10.8. 128 x 14336 x 4096, 56: 12.9 and 11.8.
   const int64_t wide_tiles = row_tiles * (d.mode == 0 ? d.I / (BN / 2) : cdiv(d.N, BN));
-  const bool narrow = wide_tiles * (BN / BN_NARROW) <= num_sms();
+  const bool narrow = narrow_tiles(wide_tiles, BN / BN_NARROW, num_sms());
   const int columns = narrow ? BN_NARROW : BN;
   const Args args = gemm_a4_args(d, columns);
   CUtensorMap tA, tA32, tB, tBs;

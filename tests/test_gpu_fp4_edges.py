@@ -4,7 +4,7 @@ import torch
 
 import plain_fp4 as plain
 import routing_dispatch_expert_gb300 as rde
-from test_gpu_fp4 import built, rng  # noqa: F401
+from test_gpu_fp4 import FORMATS, built, operand, product_tolerance, rng  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -41,3 +41,16 @@ def test_matmul_with_more_than_2_29_columns():
     assert int(status) == 0
     assert (float(y[0, 0]), float(y[0, 12345]), float(y[0, -1])) == (64.0, 48.0, 96.0)
     assert int((y != 32).sum()) == 3
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M,N,K", [(128, 7168, 512), (128, 9728, 256), (128, 9729, 256), (256, 4864, 288), (256, 4865, 288),
+                                   (384, 3200, 256), (127, 9728, 256), (129, 4864, 256)])
+def test_matmul_of_whole_row_tiles(fmt, M, N, K):
+    """Whole 128-row tiles on both sides of where all narrow tiles run at once."""
+    aq, a_s, ga, a = operand(M, K, fmt, 1)
+    bq, b_s, gb, b = operand(N, K, fmt, 2, 0.02)
+    ref, mag = a @ b.T, a.abs() @ b.abs().T
+    for dtype in (torch.bfloat16, torch.float32):
+        y = rde.matmul_fp4(aq, a_s, bq, b_s, fmt, ga, gb, dtype=dtype)
+        assert (y.double() - ref).abs().sub(product_tolerance(ref, mag, K, dtype)).amax() <= 0
