@@ -739,6 +739,7 @@ MOE_EXPORT int moe_dispatch(const moe_config* cfg, const void* x, const int32_t*
                             moe_stream_t stream) {
   int rc = check_config(cfg);
   if (rc) return rc;
+  if ((rc = refuse_mxfp4(cfg))) return rc;
   Layout L = make_layout(cfg);
   if ((rc = check_ws(ws, ws_bytes, L))) return rc;
   REQUIRE_PTR(x, "x");
@@ -1358,6 +1359,7 @@ MOE_EXPORT int moe_dispatch_noalloc(const moe_config* cfg, const void* x, const 
                                     moe_stream_t stream) {
   int rc = check_config(cfg);
   if (rc) return rc;
+  if ((rc = refuse_mxfp4(cfg))) return rc;
   const size_t need = moe::dispatch_scratch_ints(cfg->T, cfg->E) + cfg->E;
   if (need > kNoAllocHistInts)
     return fail(MOE_ERR_UNSUPPORTED, "moe_dispatch_noalloc: (ceil(T / 512) + 1) * E = " + std::to_string(need) +

@@ -1,0 +1,19 @@
+"""Refusals of the 4-bit and balance-loss entry points that test_fp4_balance_host.py does not cover. No GPU: each call
+returns before any CUDA call."""
+import ctypes
+
+import pytest
+
+from routing_dispatch_expert_gb300 import moe
+from test_fp4_balance_host import P, _cfg, _says, lib  # noqa: F401
+
+
+@pytest.mark.parametrize("shared", [0, 256])
+def test_mxfp4_layers_have_no_bf16_dispatch(lib, shared):  # noqa: F811
+    """Rows in bf16 serve no MXFP4 entry point, and are four times what a caller with 4-bit rows has room for."""
+    c = ctypes.byref(_cfg(dtype="mxfp4", I_shared=shared))
+    big = ctypes.c_size_t(1 << 40)
+    assert lib.moe_dispatch(c, P, P, P, P, P, P, P, P, P, None, P, big, None) == moe.MOE_ERR_UNSUPPORTED
+    assert _says(lib, "_fp4 entry points")
+    assert lib.moe_dispatch_noalloc(c, P, P, P, P, P, P, P, P, P, None, None) == moe.MOE_ERR_UNSUPPORTED
+    assert _says(lib, "_fp4 entry points")
