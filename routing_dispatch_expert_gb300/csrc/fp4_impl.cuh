@@ -128,15 +128,24 @@ __device__ __forceinline__ uint32_t codes8(const float* x, float by, uint32_t am
   return pack8(y);
 }
 
-// Fp32 values of the 8 codes of a word, times a factor that rounds once (the codes and their block scale
-// have 7 significant bits together: their product is exact).
+// f g for a result that is rounded again, to 16 bits: rounded to odd (of the two fp32 numbers around a product that
+// is none, the one whose last bit is set), so that the second rounding gives what one alone would.
+__device__ __forceinline__ float product_to_odd(float f, float g) {
+  const float low = __fmul_rd(f, g);
+  return __float_as_uint(low) & 1 ? low : __fmul_ru(f, g);
+}
+
+// Fp32 values of the 8 codes of a word, times the matrix scale (the codes and their block scale have 7 significant bits
+// together: their product is exact). ODD: for a 16-bit result.
+template <bool ODD>
 __device__ __forceinline__ void values8(uint32_t codes, float scale, float g, float* v) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)((codes >> (8 * i)) & 0xFF), __NV_E2M1);
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-    v[2 * i] = __fmul_rn(__fmul_rn(f.x, scale), g);
-    v[2 * i + 1] = __fmul_rn(__fmul_rn(f.y, scale), g);
+    const float x = __fmul_rn(f.x, scale), y = __fmul_rn(f.y, scale);
+    v[2 * i] = ODD ? product_to_odd(x, g) : __fmul_rn(x, g);
+    v[2 * i + 1] = ODD ? product_to_odd(y, g) : __fmul_rn(y, g);
   }
 }
 

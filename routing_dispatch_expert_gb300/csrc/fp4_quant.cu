@@ -87,7 +87,8 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const uint32_t* __
     const uint32_t u = u0 + i * kThreads;
     if (u >= units) return;
     float v[8];
-    values8(c[i], FMT == kNv ? e4m3_value(b[i]) : e8m0_value(b[i]), gs, v);
+    // MXFP4 values are exact in fp32: no matrix scale
+    values8<FMT == kNv && TYPE != MOE_TYPE_F32>(c[i], FMT == kNv ? e4m3_value(b[i]) : e8m0_value(b[i]), gs, v);
     if (TYPE == MOE_TYPE_F32) {
       float* o = static_cast<float*>(y) + 8 * (int64_t)u;
       if (WIDE) {

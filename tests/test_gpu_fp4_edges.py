@@ -54,3 +54,33 @@ def test_matmul_of_whole_row_tiles(fmt, M, N, K):
     for dtype in (torch.bfloat16, torch.float32):
         y = rde.matmul_fp4(aq, a_s, bq, b_s, fmt, ga, gb, dtype=dtype)
         assert (y.double() - ref).abs().sub(product_tolerance(ref, mag, K, dtype)).amax() <= 0
+
+
+def rounded(v, dtype):
+    """fp64 numbers rounded once, to nearest even, to a 16-bit type."""
+    bits, least, most = {torch.bfloat16: (8, -133, torch.finfo(torch.bfloat16).max),
+                         torch.float16: (11, -24, 65504.0)}[dtype]
+    e = torch.frexp(v)[1] - bits  # the last bit of v's binade
+    step = torch.pow(2.0, e.clamp(min=least).double())
+    r = torch.round(v / step) * step
+    return torch.where(r.abs() > most, torch.copysign(torch.full_like(r, float("inf")), r), r)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_dequantize_rounds_once(dtype):
+    """code * scale * g for every code and scale, and matrix scales g for which rounding to fp32 first gives another
+    16-bit number (found here by trying), and very small and large ones."""
+    code = torch.arange(16, dtype=torch.uint8)
+    q = (code.repeat(2)[::2] | code.repeat(2)[1::2] << 4).repeat(127, 1)  # a row: codes 0 .. 15 twice
+    s = torch.arange(127, dtype=torch.uint8).unsqueeze(1).repeat(1, 2)
+    unit = plain.values(q, s, "nvfp4", 1.0)
+    gen = torch.Generator().manual_seed(4)
+    tried = torch.rand(400000, generator=gen) + 0.5
+    parts = torch.unique(torch.frexp(unit)[0].abs())  # the same up to a power of two
+    v = tried.double().unsqueeze(1) * parts
+    differ = tried[(v.float().to(dtype).double() != rounded(v, dtype)).any(1)].tolist()
+    assert len(differ) > 5
+    smallest = [float(torch.tensor(v)) for v in (3e-5, 1e-9, 1.37e-36, 5e-38, 3e-39, 2.7e-41, 1.1e30)]
+    for g in differ[:40] + smallest:
+        got = rde.dequantize_fp4(q.cuda(), s.cuda(), "nvfp4", torch.tensor([g], device="cuda"), dtype=dtype)
+        assert torch.equal(got.cpu().double(), rounded(unit * g, dtype)), g
