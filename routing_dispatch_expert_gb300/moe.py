@@ -459,10 +459,8 @@ def _balance_inputs(cfg, logits, seq_offsets, token_mask):
     return n_seq, ELEMENT_TYPES[logits.dtype], offsets, mask
 
 
-def balance_loss(cfg, logits, topk_idx, alpha: float, seq_offsets=None, token_mask=None, ws=None) -> dict:
-    """The router's load-balance loss (moe_balance_loss in include/moe.h) of logits [T, E] (fp32 or bf16) and the
-    chosen experts topk_idx [T, k]: loss [S], counts [S, E], mean_prob [S, E] and tokens [S] of S sequences
-    (seq_offsets int32 [S + 1]; None: one of all tokens). token_mask [T]: 0 = padding. ws: balance_loss_workspace."""
+def _balance_loss(logits, cfg, topk_idx, alpha, seq_offsets, token_mask, ws):
+    """(loss, counts, mean_prob, tokens)."""
     S, kind, offsets, mask = _balance_inputs(cfg, logits, seq_offsets, token_mask)
     if not _like(topk_idx, _i32, (cfg.T, cfg.k)):
         _need(topk_idx, "topk_idx", _i32, (cfg.T, cfg.k))
@@ -479,13 +477,50 @@ def balance_loss(cfg, logits, topk_idx, alpha: float, seq_offsets=None, token_ma
                                              mask, alpha, loss.data_ptr(), counts.data_ptr(), mean.data_ptr(),
                                              tokens.data_ptr(), ws.data_ptr(), ws.numel(),
                                              _raw_stream(_current_device())))
+    return loss, counts, mean, tokens
+
+
+class _BalanceLoss(torch.autograd.Function):
+    """The loss as a node of autograd, whose gradient is moe_balance_loss_backward."""
+
+    @staticmethod
+    def forward(ctx, logits, cfg, topk_idx, alpha, seq_offsets, token_mask, ws):
+        loss, counts, mean, tokens = _balance_loss(logits, cfg, topk_idx, alpha, seq_offsets, token_mask, ws)
+        ctx.mark_non_differentiable(counts, mean, tokens)
+        ctx.save_for_backward(logits, counts, tokens, seq_offsets, token_mask)
+        ctx.cfg, ctx.alpha = cfg, alpha
+        return loss, counts, mean, tokens
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dloss, *_):
+        logits, counts, tokens, seq_offsets, token_mask = ctx.saved_tensors
+        if not dloss.is_contiguous() or dloss.data_ptr() % 16:  # an expanded sum's gradient, a slice of another tensor
+            dloss = dloss.clone(memory_format=torch.contiguous_format)
+        d = balance_loss_backward(ctx.cfg, logits, counts, tokens, ctx.alpha, dloss, seq_offsets, token_mask)
+        return d, None, None, None, None, None, None
+
+
+def balance_loss(cfg, logits, topk_idx, alpha: float, seq_offsets=None, token_mask=None, ws=None) -> dict:
+    """The router's load-balance loss (moe_balance_loss in include/moe.h) of logits [T, E] (fp32 or bf16) and the
+    chosen experts topk_idx [T, k]: loss [S], counts [S, E], mean_prob [S, E] and tokens [S] of S sequences
+    (seq_offsets int32 [S + 1]; None: one of all tokens). token_mask [T]: 0 = padding. ws: balance_loss_workspace.
+
+    The loss is differentiable once with respect to logits that require a gradient, by balance_loss_backward; counts,
+    mean_prob and tokens carry no gradient. (As for any operation: a backward pass that is captured into a CUDA graph
+    must not share leaves with an eager graph that is still alive.)"""
+    run = _balance_loss
+    if getattr(logits, "requires_grad", False) and torch.is_grad_enabled():
+        run = _BalanceLoss.apply
+    loss, counts, mean, tokens = run(logits, cfg, topk_idx, alpha, seq_offsets, token_mask, ws)
     return {"loss": loss, "counts": counts, "mean_prob": mean, "tokens": tokens}
 
 
 def balance_loss_backward(cfg, logits, counts, tokens, alpha: float, dloss, seq_offsets=None, token_mask=None,
                           dlogits=None) -> torch.Tensor:
     """Gradient of balance_loss with respect to logits (of their dtype), from its counts and tokens and the
-    gradients dloss [S] of its losses."""
+    gradients dloss [S] of its losses: what backward() of the loss calls, for use without autograd. The gradient is
+    not itself differentiable."""
     S, kind, offsets, mask = _balance_inputs(cfg, logits, seq_offsets, token_mask)
     if not (_like(counts, _i32, (S, cfg.E)) and _like(tokens, _i32, (S,)) and _like(dloss, _f32, (S,))):
         _need(counts, "counts", _i32, (S, cfg.E))

@@ -3,6 +3,7 @@ returns before any CUDA call."""
 import ctypes
 
 import pytest
+import torch
 
 from routing_dispatch_expert_gb300 import moe
 from test_fp4_balance_host import P, _cfg, _says, lib  # noqa: F401
@@ -17,3 +18,11 @@ def test_mxfp4_layers_have_no_bf16_dispatch(lib, shared):  # noqa: F811
     assert _says(lib, "_fp4 entry points")
     assert lib.moe_dispatch_noalloc(c, P, P, P, P, P, P, P, P, P, None, None) == moe.MOE_ERR_UNSUPPORTED
     assert _says(lib, "_fp4 entry points")
+
+
+def test_balance_loss_refuses_what_is_no_cuda_tensor():
+    """With and without a gradient, and things that are no tensors at all."""
+    idx = torch.zeros(4, 2, dtype=torch.int32)
+    for logits in (torch.zeros(4, 8, requires_grad=True), torch.zeros(4, 8), [[0.0] * 8] * 4, None):
+        with pytest.raises(ValueError, match="logits must be a CUDA tensor"):
+            moe.balance_loss(_cfg(T=4), logits, idx, 0.1)
