@@ -363,11 +363,16 @@ int moe_dequantize_fp4(const void* q, const void* s, int64_t rows, int64_t cols,
  *   aq, as   A [M, K];  bq, bs  B [N, K];  ga, gb  their matrix scales [1] or NULL (MOE_FP4_NV)
  *   y        [M, N] out with ldy >= N elements from row to row, MOE_TYPE_BF16 or MOE_TYPE_F32
  *   status   device int32 that MOE_STATUS_WAIT_TIMEOUT is added to if a wait gives up (y is then not
- *            valid), or NULL
+ *            valid); NULL: the library's own word, see moe_matmul_fp4_status
  * M >= 0 and N >= 1 are any numbers below 2^31 - 256, K is a multiple of 32. Errors: MOE_ERR_INVALID, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA. */
 int moe_matmul_fp4(const void* aq, const void* as, const float* ga, const void* bq, const void* bs, const float* gb,
                    int64_t M, int64_t N, int64_t K, int32_t format, int32_t y_type, void* y, int64_t ldy,
                    int32_t* status, moe_stream_t stream);
+
+/* Status of the products without a status word of their own: waits for `stream`, then reads the MOE_STATUS_* bits
+ * that moe_matmul_fp4 calls with status NULL on the current device have set since the last read, and clears them.
+ * Returns MOE_OK if no bit was set, MOE_ERR_DEVICE if some were; errors: MOE_ERR_INVALID, MOE_ERR_CUDA. */
+int moe_matmul_fp4_status(int32_t* status, moe_stream_t stream);
 
 /* The layer with 4-bit rows as well as 4-bit weights: the tensor cores multiply the codes, nothing is
  * expanded. cfg->dtype is MOE_DTYPE_NVFP4 (weights of moe_quantize_weights_nvfp4) or MOE_DTYPE_MXFP4 (weights
@@ -446,8 +451,9 @@ int moe_device_status(const moe_config* cfg, void* ws, int32_t* status, moe_stre
 /* Failure-detection self-test (no fault, no trap, no endless loop): one thread waits, through the
  * bounded wait that every pipeline wait of the grouped GEMMs uses, on an mbarrier that nothing ever
  * completes. After limit_cycles SM clocks (1 .. 4e9) the wait gives up and records
- * MOE_STATUS_WAIT_TIMEOUT in the status word of ws, which moe_device_status then reports; the kernel
- * returns and the context stays usable. Asynchronous on `stream`.
+ * MOE_STATUS_WAIT_TIMEOUT in the status word of ws, which moe_device_status then reports (ws NULL: in
+ * the word that moe_matmul_fp4_status reports); the kernel returns and the context stays usable.
+ * Asynchronous on `stream`.
  * Errors: MOE_ERR_INVALID, MOE_ERR_WORKSPACE, MOE_ERR_CUDA. */
 int moe_selftest_wait_timeout(const moe_config* cfg, void* ws, size_t ws_bytes, int64_t limit_cycles,
                               moe_stream_t stream);

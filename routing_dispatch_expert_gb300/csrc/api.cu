@@ -1274,9 +1274,15 @@ MOE_EXPORT int moe_selftest_wait_timeout(const moe_config* cfg, void* ws, size_t
   int rc = check_config(cfg);
   if (rc) return rc;
   Layout L = make_layout(cfg);
-  if ((rc = check_ws(ws, ws_bytes, L))) return rc;
+  if (ws && (rc = check_ws(ws, ws_bytes, L))) return rc;
   if (limit_cycles < 1 || limit_cycles > 4000000000LL) return fail(MOE_ERR_INVALID, "limit_cycles must lie in [1, 4e9]");
-  cudaError_t e = moe::launch_wait_timeout_selftest(status_ptr(ws, L.l), (long long)limit_cycles, (cudaStream_t)stream);
+  int* word = nullptr;
+  cudaError_t e = cudaSuccess;
+  if (ws)
+    word = status_ptr(ws, L.l);
+  else
+    e = moe::gemm_a4_default_status(&word);
+  if (e == cudaSuccess) e = moe::launch_wait_timeout_selftest(word, (long long)limit_cycles, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "self-test launch");
   counted(1);
   return MOE_OK;
@@ -1296,13 +1302,10 @@ MOE_EXPORT int moe_balance(const moe_config* cfg, const void* ws, moe_balance_st
   return MOE_OK;
 }
 
-MOE_EXPORT int moe_device_status(const moe_config* cfg, void* ws, int32_t* status, moe_stream_t stream) {
-  int rc = check_config(cfg);
-  if (rc) return rc;
-  if (!ws || !status) return fail(MOE_ERR_INVALID, "ws and status must not be NULL");
-  Layout L = make_layout(cfg);
-  int* p = status_ptr(ws, L.l);
-  cudaStream_t s = (cudaStream_t)stream;
+namespace {
+
+// the status word at p, once `s` has come this far; cleared behind the read
+int read_status(int* p, int32_t* status, cudaStream_t s) {
   int v = 0;
   cudaError_t e = cudaMemcpyAsync(&v, p, sizeof(int), cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = cudaMemsetAsync(p, 0, sizeof(int), s);
@@ -1311,6 +1314,24 @@ MOE_EXPORT int moe_device_status(const moe_config* cfg, void* ws, int32_t* statu
   *status = v;
   if (v) return fail(MOE_ERR_DEVICE, "device status bits set: " + std::to_string(v));
   return MOE_OK;
+}
+
+}  // namespace
+
+MOE_EXPORT int moe_device_status(const moe_config* cfg, void* ws, int32_t* status, moe_stream_t stream) {
+  int rc = check_config(cfg);
+  if (rc) return rc;
+  if (!ws || !status) return fail(MOE_ERR_INVALID, "ws and status must not be NULL");
+  Layout L = make_layout(cfg);
+  return read_status(status_ptr(ws, L.l), status, (cudaStream_t)stream);
+}
+
+MOE_EXPORT int moe_matmul_fp4_status(int32_t* status, moe_stream_t stream) {
+  if (!status) return fail(MOE_ERR_INVALID, "status must not be NULL");
+  int* word = nullptr;
+  cudaError_t e = moe::gemm_a4_default_status(&word);
+  if (e != cudaSuccess) return cuda_fail(e, "address of the status word");
+  return read_status(word, status, (cudaStream_t)stream);
 }
 
 // ------------------------------------------------------------------------------------------

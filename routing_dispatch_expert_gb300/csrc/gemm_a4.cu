@@ -118,11 +118,13 @@ struct Shared {
   uint64_t mma_done;
   uint32_t tmem_slot;
   volatile int abort_flag;
-  int unreported;
   grp::Table tb;
 };
 
 using grp::wait_or_abort;
+
+// where a launch without a status word records a wait that gave up (moe_matmul_fp4_status)
+__device__ int default_status;
 
 // One lane of a converged warp, the same one on every call.
 __device__ __forceinline__ uint32_t elect_one() {
@@ -434,7 +436,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   // the same in all lanes, and known to be: the roles' addresses and counters stay in uniform registers
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int G = args.E + args.shared;
-  int* status = args.status ? args.status : &s.unreported;
+  int* status = args.status ? args.status : &default_status;
 
   if (warp == 0) {
     grp::build_table(s.tb, args.offsets, args.E, args.shared, args.R, args.T, BM, lane);
@@ -653,6 +655,19 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 }  // namespace a4
+
+cudaError_t gemm_a4_default_status(int** word) {
+  static PerDevice<int*> addr;
+  return per_device<int*>(
+      addr,
+      [](int*& p) {
+        void* v = nullptr;
+        const cudaError_t r = cudaGetSymbolAddress(&v, a4::default_status);
+        p = static_cast<int*>(v);
+        return r;
+      },
+      word);
+}
 
 // bytes (32, 16 or fewer: 0) that every output row is aligned to
 int row_alignment(const GemmA4Desc& d) {

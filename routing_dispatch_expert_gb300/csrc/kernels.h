@@ -229,12 +229,14 @@ struct GemmA4Desc {
   const float* out_g = nullptr;  // mode 0: [1] scale of H or nullptr
   int64_t ldo;               // elements
   const float* row_weight = nullptr;
-  int* status;               // nullptr: a wait that gives up is not recorded
+  int* status;               // nullptr: gemm_a4_default_status()
   // the launch before this one in the stream is a launch_gemm_a4 that itself waited for all work before it: this
   // kernel sets itself up beside that one's end
   bool after_gemm = false;
 };
 cudaError_t launch_gemm_a4(const GemmA4Desc& d, cudaStream_t stream, std::string* err);
+// device address, on the current device, of the status word of launches without one of their own
+cudaError_t gemm_a4_default_status(int** word);
 
 // The router's balance loss (balance_loss.cu). scratch: balance_loss_entries() * (2 E + 1) words.
 int64_t balance_loss_entries(int T, int E, int S);

@@ -99,6 +99,7 @@ def load():
                 "moe_quantize_fp4": [vp, i32, i64, i64, i64, i32, vp, vp, vp, vp],
                 "moe_dequantize_fp4": [vp, vp, i64, i64, i32, vp, i32, vp, vp],
                 "moe_matmul_fp4": [vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, i32, vp, i64, vp, vp],
+                "moe_matmul_fp4_status": [ctypes.POINTER(ctypes.c_int32), vp],
                 "moe_dispatch_fp4": [cfgp, actp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
                 "moe_expert_ffn_fp4": [cfgp, wp, actp, vp, vp, vp, vp, vp, vp, sz, vp],
                 "moe_forward_fp4": [cfgp, vp, wp, actp, vp, vp, sz, vp],
@@ -368,7 +369,7 @@ def matmul_fp4(aq, a_s, bq, b_s, fmt: str = "nvfp4", ga=None, gb=None, dtype=tor
                status=None) -> torch.Tensor:
     """y [M, N] = A B^T of 4-bit matrices A [M, K] and B [N, K] (codes, scales, NVFP4 matrix scales fp32 [1] or
     None = 1), fp32 accumulation, rounded once to bf16 or fp32. y may have strided rows. status: int32 [1] that
-    MOE_STATUS_WAIT_TIMEOUT is added to if a wait of the kernel gives up."""
+    MOE_STATUS_WAIT_TIMEOUT is added to if a wait of the kernel gives up; None: matmul_fp4_status() reports it."""
     f = _fp4_format(fmt)
     M, K = _fp4_matrix(aq, a_s, fmt, "A")
     N, kb = _fp4_matrix(bq, b_s, fmt, "B")
@@ -392,6 +393,16 @@ def matmul_fp4(aq, a_s, bq, b_s, fmt: str = "nvfp4", ga=None, gb=None, dtype=tor
                                            y.data_ptr(), ldy, None if status is None else status.data_ptr(),
                                            _raw_stream(_current_device())))
     return y
+
+
+def matmul_fp4_status() -> int:
+    """MOE_STATUS_* bits of the matmul_fp4 calls without a status of their own since the last read, once the current
+    stream has come this far; 0: every wait ended. Reading clears them."""
+    v = ctypes.c_int32()
+    rc = load().moe_matmul_fp4_status(ctypes.byref(v), _stream())
+    if rc not in (MOE_OK, MOE_ERR_DEVICE):
+        _check(rc)
+    return v.value
 
 
 class Fp4Activations:
@@ -551,8 +562,9 @@ def device_status(cfg, ws) -> int:
 
 def selftest_wait_timeout(cfg, ws, limit_cycles: int) -> None:
     """Enqueue the failure-detection self-test (moe_selftest_wait_timeout): a bounded wait that nothing
-    completes records MOE_STATUS_WAIT_TIMEOUT in the workspace's status word."""
-    _check(load().moe_selftest_wait_timeout(ctypes.byref(cfg), _ptr(ws), ws.numel() * ws.element_size(),
+    completes records MOE_STATUS_WAIT_TIMEOUT in the workspace's status word (ws None: in the word of
+    matmul_fp4_status)."""
+    _check(load().moe_selftest_wait_timeout(ctypes.byref(cfg), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
                                             int(limit_cycles), _stream()))
 
 

@@ -26,3 +26,12 @@ def test_balance_loss_refuses_what_is_no_cuda_tensor():
     for logits in (torch.zeros(4, 8, requires_grad=True), torch.zeros(4, 8), [[0.0] * 8] * 4, None):
         with pytest.raises(ValueError, match="logits must be a CUDA tensor"):
             moe.balance_loss(_cfg(T=4), logits, idx, 0.1)
+
+
+def test_status_calls_check_their_arguments(lib):  # noqa: F811
+    assert lib.moe_matmul_fp4_status(None, None) == moe.MOE_ERR_INVALID
+    assert _says(lib, "status")
+    c = ctypes.byref(_cfg())
+    assert lib.moe_selftest_wait_timeout(c, None, 0, 0, None) == moe.MOE_ERR_INVALID  # the limit, not ws
+    assert _says(lib, "limit_cycles")
+    assert lib.moe_selftest_wait_timeout(c, P, 16, 1000, None) == moe.MOE_ERR_WORKSPACE

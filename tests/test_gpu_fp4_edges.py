@@ -84,3 +84,16 @@ def test_dequantize_rounds_once(dtype):
     for g in differ[:40] + smallest:
         got = rde.dequantize_fp4(q.cuda(), s.cuda(), "nvfp4", torch.tensor([g], device="cuda"), dtype=dtype)
         assert torch.equal(got.cpu().double(), rounded(unit * g, dtype)), g
+
+
+def test_a_wait_that_gives_up_is_reported_without_a_status_word():
+    """The word that products without one record in: read and cleared, and untouched by products that end well."""
+    aq, a_s, ga, _ = operand(40, 256, "nvfp4", 1)
+    rde.matmul_fp4_status()
+    y = rde.matmul_fp4(aq, a_s, aq, a_s, "nvfp4", ga, ga)
+    assert rde.matmul_fp4_status() == 0
+    cfg = rde.make_config(T=8, h=256, E=8, k=2, I=256, dtype="nvfp4")
+    rde.selftest_wait_timeout(cfg, None, 1_000_000)  # about half a millisecond of SM clock
+    assert torch.equal(rde.matmul_fp4(aq, a_s, aq, a_s, "nvfp4", ga, ga), y)
+    assert rde.matmul_fp4_status() == rde.moe.MOE_STATUS_WAIT_TIMEOUT
+    assert rde.matmul_fp4_status() == 0
