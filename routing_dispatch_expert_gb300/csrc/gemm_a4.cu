@@ -706,7 +706,7 @@ a4::Args gemm_a4_args(const GemmA4Desc& d, int columns) {
   a.out_g = d.out_g;
   a.row_weight = d.row_weight;
   a.status = d.status;
-  a.wait_limit = 4000000000LL;  // about two seconds of SM clock
+  a.wait_limit = a4::wait_limit(cdiv(d.K, a4::BK));
   return a;
 }
 

@@ -3,6 +3,7 @@
 
 #include <cstdio>
 #include <cstdlib>
+#include <initializer_list>
 
 using namespace moe::a4;
 
@@ -27,6 +28,9 @@ int main() {
   expect(narrow(127, 7168) && narrow(128, 7168) && !narrow(129, 7168), "128 x 7168");
   expect(narrow(128, 9728) && !narrow(128, 9729), "128 rows on either side of 152 SMs");
   expect(narrow(256, 4864) && !narrow(256, 4865) && !narrow(257, 4864), "256 rows");
+  // a tile of the longest K takes up to 1 us (2100 clocks) for each of its 2^23 blocks
+  for (int64_t blocks : {int64_t(1), int64_t(28), int64_t(1) << 20, int64_t(1) << 23})
+    expect(wait_limit(blocks) >= 4000000000LL && wait_limit(blocks) >= 2 * 2100 * blocks, "the wait of a long tile");
   std::printf("ok\n");
   return 0;
 }

@@ -97,3 +97,22 @@ def test_a_wait_that_gives_up_is_reported_without_a_status_word():
     assert torch.equal(rde.matmul_fp4(aq, a_s, aq, a_s, "nvfp4", ga, ga), y)
     assert rde.matmul_fp4_status() == rde.moe.MOE_STATUS_WAIT_TIMEOUT
     assert rde.matmul_fp4_status() == 0
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_matmul_of_very_long_rows(fmt):
+    """2^25 + 32 elements a row, 131073 K blocks: whole numbers at both ends and at the seams, so that sums are exact."""
+    K, M, N = (1 << 25) + 32, 3, 70
+    one = 0x38 if fmt == "nvfp4" else 127
+    scales = lambda n: torch.full((n, K // plain.BLOCK[fmt]), one, dtype=torch.uint8, device="cuda")  # noqa: E731
+    aq = torch.zeros(M, K // 2, dtype=torch.uint8, device="cuda")
+    bq = torch.zeros(N, K // 2, dtype=torch.uint8, device="cuda")
+    bq[:] = 0x24  # 2, 1, 2, 1 ..
+    at = [0, 127, 128, 1 << 16, (1 << 24) - 1, K // 2 - 16, K // 2 - 1]  # bytes: elements 2 i and 2 i + 1
+    for m in range(M):
+        for i in at[:len(at) - m]:
+            aq[m, i] = 0x42  # 1, 2
+    y = rde.matmul_fp4(aq, scales(M), bq, scales(N), fmt, dtype=torch.float32)
+    assert rde.matmul_fp4_status() == 0
+    for m in range(M):
+        assert (y[m] == 4.0 * (len(at) - m)).all()
