@@ -364,7 +364,8 @@ int moe_dequantize_fp4(const void* q, const void* s, int64_t rows, int64_t cols,
  *   y        [M, N] out with ldy >= N elements from row to row, MOE_TYPE_BF16 or MOE_TYPE_F32
  *   status   device int32 that MOE_STATUS_WAIT_TIMEOUT is added to if a wait gives up (y is then not
  *            valid); NULL: the library's own word, see moe_matmul_fp4_status
- * M >= 0 and N >= 1 are any numbers below 2^31 - 256, K is a multiple of 32. Errors: MOE_ERR_INVALID, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA. */
+ * M >= 0 and N >= 1 are any numbers up to 2^31 - 257, K a multiple of 32 up to there; no more than about 2^31 tiles of
+ * 128 x 256. Errors: MOE_ERR_INVALID, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA. */
 int moe_matmul_fp4(const void* aq, const void* as, const float* ga, const void* bq, const void* bs, const float* gb,
                    int64_t M, int64_t N, int64_t K, int32_t format, int32_t y_type, void* y, int64_t ldy,
                    int32_t* status, moe_stream_t stream);
@@ -425,7 +426,8 @@ int moe_forward_fp4(const moe_config* cfg, const void* x, const moe_weights* wei
  *   token_mask   [T] bytes, 0 = padding, left out whatever its logits hold; NULL: no padding
  *   loss [n_seq] fp32, counts [n_seq, E] int32, mean_prob [n_seq, E] fp32, tokens [n_seq] int32 (n) out
  *   ws           moe_balance_loss_workspace_size() bytes; its contents do not matter
- * Deterministic; at most two launches. Errors: MOE_ERR_INVALID, MOE_ERR_WORKSPACE, MOE_ERR_CUDA. */
+ * Deterministic; at most two launches; n_seq at most 2^24. Errors: MOE_ERR_INVALID, MOE_ERR_UNSUPPORTED,
+ * MOE_ERR_WORKSPACE, MOE_ERR_CUDA. */
 int moe_balance_loss_workspace_size(const moe_config* cfg, int32_t n_seq, size_t* bytes);
 int moe_balance_loss(const moe_config* cfg, const void* logits, int32_t logits_type, const int32_t* topk_idx,
                      const int32_t* seq_offsets, int32_t n_seq, const uint8_t* token_mask, float alpha, float* loss,
@@ -434,7 +436,7 @@ int moe_balance_loss(const moe_config* cfg, const void* logits, int32_t logits_t
 
 /* Its gradient: dlogits [T, E] of logits_type = sum_s dloss[s] * d loss[s] / d logits, from the counts and
  * tokens that moe_balance_loss returned. dloss [n_seq] fp32. Rows of padding, and of tokens in no sequence, are
- * 0. One launch. Errors: MOE_ERR_INVALID, MOE_ERR_CUDA. */
+ * 0. One launch. Errors: MOE_ERR_INVALID, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA. */
 int moe_balance_loss_backward(const moe_config* cfg, const void* logits, int32_t logits_type, const int32_t* counts,
                               const int32_t* tokens, const int32_t* seq_offsets, int32_t n_seq,
                               const uint8_t* token_mask, float alpha, const float* dloss, void* dlogits,

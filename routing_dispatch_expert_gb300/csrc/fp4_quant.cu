@@ -3,8 +3,9 @@
 // One pass over the rows: a lane holds 8 or 16 consecutive elements, so a warp's loads and stores are
 // contiguous; a block of 16 or 32 elements is 1 to 4 lanes, which share its largest magnitude by shuffles.
 // Bound by HBM, but for 16-bit rows to NVFP4, whose quotients make about 100 instructions of 8 elements.
-// 16384 x 7168 on one GB300 (bytes in and out over the time; a copy moves 6788 GB/s): bf16 to MXFP4 45.6 us
-// (6.5 TB/s), to NVFP4 56 us (5.3); fp32 to either 77 - 80 us (6.7 - 6.9); back to fp32 82 us (6.5), to bf16 48 us (6.2).
+// 16384 x 7168 on one GB300 (bytes in and out over the time; a copy moves 6788 GB/s): bf16 to MXFP4 43 - 46 us
+// (6.5 - 6.9 TB/s), to NVFP4 54 - 56 us (5.3 - 5.6); fp32 to either 74 - 80 us (6.7 - 7.1); back to fp32 80 - 82 us (6.5),
+// to bf16 45 - 48 us (6.2 - 6.7).
 #include <type_traits>
 
 #include "common.cuh"
