@@ -32,7 +32,7 @@
 //   * a tile of at most 96 rows loads only the 32-row boxes that hold rows (a few rows an expert: the
 //     weights are the traffic); the rest of the tile keeps stale codes, whose products are not stored.
 //
-// What bounds it (GB300, 2.07 GHz). Few rows a group: HBM; the experts of a 256-token step, 153 of 256 active, h
+// What bounds it (GB300, 2.07 GHz). Few rows a group: HBM; the experts of a 256-token step, 226 of 256 active, h
 // 7168, I 2048: 0.82 - 0.83 ms, 6.8 TB/s (a copy: 6.8). Many rows: 8192 x 14336 x 4096 185 us out of HBM and 175 - 178
 // out of L2 (NVFP4, 5.2 and 5.5 PFLOP/s), 169 and 162 - 165 us (MXFP4); fp32 output 227 and 214 us out of L2. The
 // comparisons of variants, here and below, are with inputs in L2. A K block takes 512 cycles of MMA and about 600 with
