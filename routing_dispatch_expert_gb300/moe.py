@@ -177,7 +177,8 @@ class Placement:
 class Weights:
     """Device tensors of one layer and their C struct. bf16 expert weights for dtype 'bf16'; for
     'fp8' pass e4m3 codes (torch.uint8) and fp32 128x128 scales (see quantize_weights_fp8); for
-    'nvfp4' pass codes, e4m3 block scales and fp32 matrix scales (see quantize_weights_nvfp4)."""
+    'nvfp4' pass codes, e4m3 block scales and fp32 matrix scales (see quantize_weights_nvfp4); for 'mxfp4'
+    codes and e8m0 block scales (see quantize_fp4), without matrix scales."""
 
     def __init__(self, w_router, bias=None, w_gu=None, w_d=None, w_gu_shared=None, w_d_shared=None, s_gu=None,
                  s_d=None, s_gu_shared=None, s_d_shared=None, g_gu=None, g_d=None, g_gu_shared=None,
@@ -272,9 +273,10 @@ def quantize_weights_nvfp4(w: torch.Tensor):
     return q, s, g
 
 
-# The small calls of a decode or training step are bound by the host, so the entry points below test their tensors
-# in one expression (_is, _like) and look for the words of a refusal only when that fails, take the stream's handle
-# without making a Stream object, and pass addresses as plain ints: 24 -> 8.5 us for a quantise call on this host.
+# The small calls of a decode or training step are bound by the host, so the entry points below that check their tensors
+# do so in one expression (_like) and look for the words of a refusal (_need) only when that fails, take the stream's
+# handle without making a Stream object, and pass addresses as plain ints: 24 -> 8.5 us for a quantise call. The steps of
+# the 4-bit layer take addresses as they are, like those of the other layers.
 _current_device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _u8, _i32, _f32 = torch.uint8, torch.int32, torch.float32
