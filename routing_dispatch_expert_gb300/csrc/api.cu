@@ -1174,6 +1174,322 @@ MOE_EXPORT int moe_balance_loss_backward(const moe_config* cfg, const void* logi
 }
 
 // ------------------------------------------------------------------------------------------
+// Around the experts: the norm in front, rows sorted by expert and back, and the gradients
+// ------------------------------------------------------------------------------------------
+namespace {
+
+bool known_type(int32_t t) { return t == MOE_TYPE_F32 || t == MOE_TYPE_BF16 || t == MOE_TYPE_F16; }
+
+int check_norm(int64_t rows, int64_t cols, int32_t type, int32_t total_type, int32_t weight_type, float eps) {
+  if (rows < 0 || cols < 1) return fail(MOE_ERR_INVALID, "rows must be >= 0 and cols positive");
+  if (!known_type(type)) return fail(MOE_ERR_INVALID, "unknown element type");
+  if (total_type != type && total_type != MOE_TYPE_F32)
+    return fail(MOE_ERR_INVALID, "the residual must be of the rows' type or fp32");
+  if (weight_type != type && weight_type != MOE_TYPE_F32)
+    return fail(MOE_ERR_INVALID, "weight must be of the rows' type or fp32");
+  if (!(eps >= 0.f)) return fail(MOE_ERR_INVALID, "eps must be >= 0");
+  if (cols > moe::kNormMaxCols) return fail(MOE_ERR_UNSUPPORTED, "cols > 16384");
+  if (rows > INT32_MAX) return fail(MOE_ERR_UNSUPPORTED, "rows exceed int32");
+  return MOE_OK;
+}
+
+#define REQUIRE_ALIGNED(p, name)                                                                          \
+  do {                                                                                                    \
+    if (!aligned16(p)) return fail(MOE_ERR_INVALID, std::string(name) + " must be 16-byte aligned");      \
+  } while (0)
+
+}  // namespace
+
+MOE_EXPORT int moe_rms_norm(const void* x, int32_t x_type, int64_t rows, int64_t cols, int64_t ldx,
+                            const void* residual, int32_t residual_type, int64_t ldr, const void* weight,
+                            int32_t weight_type, float eps, void* y, void* total, void* q, float* s,
+                            moe_stream_t stream) {
+  int rc = check_norm(rows, cols, x_type, residual ? residual_type : x_type, weight ? weight_type : x_type, eps);
+  if (rc) return rc;
+  if (rows == 0) return MOE_OK;
+  if (!q != !s) return fail(MOE_ERR_INVALID, "q and s go together");
+  if (!y && !q) return fail(MOE_ERR_INVALID, "neither y nor q is wanted");
+  if (total && !residual) return fail(MOE_ERR_INVALID, "total is x without a residual");
+  if (rows > 1 && (ldx < cols || (residual && ldr < cols))) return fail(MOE_ERR_INVALID, "ldx and ldr must be at least cols");
+  REQUIRE_PTR(x, "x");
+  REQUIRE_ALIGNED(residual, "residual");
+  REQUIRE_ALIGNED(weight, "weight");
+  REQUIRE_ALIGNED(y, "y");
+  REQUIRE_ALIGNED(total, "total");
+  REQUIRE_ALIGNED(q, "q");
+  REQUIRE_ALIGNED(s, "s");
+  moe::RmsNormDesc d;
+  d.x = x;
+  d.residual = residual;
+  d.weight = weight;
+  d.y = y;
+  d.total = total;
+  d.q = q;
+  d.s = s;
+  d.rows = rows;
+  d.ldx = ldx;
+  d.ldr = ldr;
+  d.cols = (int)cols;
+  d.type = x_type;
+  d.residual_type = residual_type;
+  d.weight_type = weight_type;
+  d.eps = eps;
+  cudaError_t e = moe::launch_rms_norm(d, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "norm launch");
+  counted(1);
+  return MOE_OK;
+}
+
+MOE_EXPORT int moe_rms_norm_backward_workspace_size(int64_t rows, int64_t cols, size_t* bytes) {
+  int rc = check_norm(rows, cols, MOE_TYPE_F32, MOE_TYPE_F32, MOE_TYPE_F32, 0.f);
+  if (rc) return rc;
+  if (!bytes) return fail(MOE_ERR_INVALID, "bytes is NULL");
+  *bytes = align256(sizeof(float) * (size_t)moe::rms_norm_backward_blocks(rows, (int)cols) * cols);
+  return MOE_OK;
+}
+
+MOE_EXPORT int moe_rms_norm_backward(const void* dy, int32_t y_type, int64_t rows, int64_t cols, const void* total,
+                                     int32_t total_type, int64_t ldt, const void* dtotal, const void* weight,
+                                     int32_t weight_type, float eps, void* dx, void* dresidual, void* dweight, void* ws,
+                                     size_t ws_bytes, moe_stream_t stream) {
+  int rc = check_norm(rows, cols, y_type, total_type, weight || dweight ? weight_type : y_type, eps);
+  if (rc) return rc;
+  REQUIRE_ALIGNED(dweight, "dweight");
+  if (rows == 0) {
+    if (!dweight) return MOE_OK;
+    cudaError_t e = cudaMemsetAsync(dweight, 0, (size_t)cols * (weight_type == MOE_TYPE_F32 ? 4 : 2), (cudaStream_t)stream);
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e, "clearing the weight's gradient of no rows");
+  }
+  if (!dx && !dresidual && !dweight) return fail(MOE_ERR_INVALID, "no gradient is wanted");
+  if (rows > 1 && ldt < cols) return fail(MOE_ERR_INVALID, "ldt must be at least cols");
+  REQUIRE_PTR(dy, "dy");
+  REQUIRE_PTR(total, "total");
+  REQUIRE_ALIGNED(dtotal, "dtotal");
+  REQUIRE_ALIGNED(weight, "weight");
+  REQUIRE_ALIGNED(dx, "dx");
+  REQUIRE_ALIGNED(dresidual, "dresidual");
+  if (dweight) {
+    REQUIRE_PTR(ws, "ws");
+    size_t need = 0;
+    moe_rms_norm_backward_workspace_size(rows, cols, &need);
+    if (ws_bytes < need) return fail(MOE_ERR_WORKSPACE, "workspace of the norm's gradient too small");
+  }
+  moe::RmsNormBackwardDesc d;
+  d.dy = dy;
+  d.total = total;
+  d.dtotal = dtotal;
+  d.weight = weight;
+  d.dx = dx;
+  d.dresidual = dresidual;
+  d.dweight = dweight;
+  d.ws = ws;
+  d.rows = rows;
+  d.ldt = ldt;
+  d.cols = (int)cols;
+  d.type = y_type;
+  d.total_type = total_type;
+  d.weight_type = weight_type;
+  d.eps = eps;
+  int launches = 0;
+  cudaError_t e = moe::launch_rms_norm_backward(d, &launches, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "norm gradient launch");
+  counted(launches);
+  return MOE_OK;
+}
+
+namespace {
+
+// the counts and offsets of the rows are those of the layer's experts (slots)
+size_t sort_bytes(const moe_config* c) {
+  return align256(sizeof(int32_t) * (size_t)moe::sort_blocks((int64_t)c->T * c->k) * c->E);
+}
+
+int check_rows(const moe_config* cfg, int64_t cols) {
+  int rc = check_config(cfg);
+  if (rc) return rc;
+  if (cols < 1) return fail(MOE_ERR_INVALID, "cols must be positive");
+  if (cols >= (1 << 28)) return fail(MOE_ERR_UNSUPPORTED, "cols >= 2^28");
+  return MOE_OK;
+}
+
+}  // namespace
+
+MOE_EXPORT int moe_sort_tokens_workspace_size(const moe_config* cfg, size_t* bytes) {
+  int rc = check_config(cfg);
+  if (rc) return rc;
+  if (!bytes) return fail(MOE_ERR_INVALID, "bytes is NULL");
+  *bytes = sort_bytes(cfg);
+  return MOE_OK;
+}
+
+MOE_EXPORT int moe_sort_tokens(const moe_config* cfg, const int32_t* topk_idx, const float* topk_w, int32_t* counts,
+                               int32_t* offsets, int32_t* inv_pos, int32_t* row_token, float* row_weight, void* ws,
+                               size_t ws_bytes, moe_stream_t stream) {
+  int rc = check_config(cfg);
+  if (rc) return rc;
+  if (!topk_w != !row_weight) return fail(MOE_ERR_INVALID, "topk_w and row_weight go together");
+  REQUIRE_PTR(counts, "counts");
+  REQUIRE_PTR(offsets, "offsets");
+  if (cfg->T > 0) {
+    REQUIRE_PTR(topk_idx, "topk_idx");
+    REQUIRE_PTR(inv_pos, "inv_pos");
+    REQUIRE_PTR(row_token, "row_token");
+    REQUIRE_ALIGNED(topk_w, "topk_w");
+    REQUIRE_ALIGNED(row_weight, "row_weight");
+    REQUIRE_PTR(ws, "ws");
+    if (ws_bytes < sort_bytes(cfg)) return fail(MOE_ERR_WORKSPACE, "workspace of the sort too small");
+  }
+  moe::SortDesc d;
+  d.topk_idx = topk_idx;
+  d.topk_w = topk_w;
+  d.counts = counts;
+  d.offsets = offsets;
+  d.inv_pos = inv_pos;
+  d.row_token = row_token;
+  d.row_weight = row_weight;
+  d.scratch = static_cast<int32_t*>(ws);
+  d.T = cfg->T;
+  d.E = cfg->E;
+  d.k = cfg->k;
+  d.capacity = capacity_of(cfg);
+  if (const moe_placement* p = cfg->placement) {
+    d.n_slots = p->n_slots;
+    d.max_replicas = p->max_replicas;
+    d.slot_expert = p->slot_expert;
+    d.slot_replica = p->slot_replica;
+    d.replicas = p->replicas;
+    d.replica_slot = p->replica_slot;
+  }
+  int launches = 0;
+  cudaError_t e = moe::launch_sort_tokens(d, &launches, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "sort launch");
+  counted(launches);
+  return MOE_OK;
+}
+
+MOE_EXPORT int moe_permute(const moe_config* cfg, const void* x, int32_t element_bytes, int64_t cols, int64_t ldx,
+                           const float* x_scales, const int32_t* inv_pos, const int32_t* offsets, void* xd,
+                           float* xd_scales, moe_stream_t stream) {
+  int rc = check_rows(cfg, cols);
+  if (rc) return rc;
+  if (element_bytes != 1 && element_bytes != 2 && element_bytes != 4)
+    return fail(MOE_ERR_INVALID, "elements must have 1, 2 or 4 bytes");
+  if (!x_scales != !xd_scales) return fail(MOE_ERR_INVALID, "x_scales and xd_scales go together");
+  if (cfg->T == 0) return MOE_OK;
+  if (cfg->T > 1 && ldx < cols) return fail(MOE_ERR_INVALID, "ldx must be at least cols");
+  REQUIRE_PTR(x, "x");
+  REQUIRE_PTR(inv_pos, "inv_pos");
+  REQUIRE_PTR(offsets, "offsets");
+  REQUIRE_PTR(xd, "xd");
+  REQUIRE_ALIGNED(x_scales, "x_scales");
+  REQUIRE_ALIGNED(xd_scales, "xd_scales");
+  moe::PermuteDesc d;
+  d.x = x;
+  d.x_scales = x_scales;
+  d.inv_pos = inv_pos;
+  d.held = offsets + n_groups(cfg);
+  d.xd = xd;
+  d.xd_scales = xd_scales;
+  d.ldx = ldx;
+  d.T = cfg->T;
+  d.k = cfg->k;
+  d.cols = (int)cols;
+  d.element_bytes = element_bytes;
+  cudaError_t e = moe::launch_permute(d, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "permute launch");
+  counted(1);
+  return MOE_OK;
+}
+
+MOE_EXPORT int moe_unpermute(const moe_config* cfg, const void* yd, int32_t type, int64_t cols, const int32_t* inv_pos,
+                             const float* weights, const void* base, void* y, moe_stream_t stream) {
+  int rc = check_rows(cfg, cols);
+  if (rc) return rc;
+  if (!known_type(type)) return fail(MOE_ERR_INVALID, "unknown element type");
+  if (cfg->T == 0) return MOE_OK;
+  REQUIRE_PTR(yd, "yd");
+  REQUIRE_PTR(inv_pos, "inv_pos");
+  REQUIRE_PTR(y, "y");
+  REQUIRE_ALIGNED(weights, "weights");
+  REQUIRE_ALIGNED(base, "base");
+  moe::UnpermuteDesc d;
+  d.yd = yd;
+  d.base = base;
+  d.weights = weights;
+  d.inv_pos = inv_pos;
+  d.y = y;
+  d.T = cfg->T;
+  d.k = cfg->k;
+  d.cols = (int)cols;
+  d.type = type;
+  cudaError_t e = moe::launch_unpermute(d, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "unpermute launch");
+  counted(1);
+  return MOE_OK;
+}
+
+MOE_EXPORT int moe_unpermute_backward(const moe_config* cfg, const void* dy, const void* yd, int32_t type, int64_t cols,
+                                      const int32_t* inv_pos, const int32_t* offsets, const float* weights, void* dyd,
+                                      float* dweights, moe_stream_t stream) {
+  int rc = check_rows(cfg, cols);
+  if (rc) return rc;
+  if (!known_type(type)) return fail(MOE_ERR_INVALID, "unknown element type");
+  if (cfg->T == 0) return MOE_OK;
+  REQUIRE_PTR(dy, "dy");
+  if (dweights) REQUIRE_PTR(yd, "yd");
+  REQUIRE_PTR(inv_pos, "inv_pos");
+  REQUIRE_PTR(offsets, "offsets");
+  REQUIRE_PTR(dyd, "dyd");
+  REQUIRE_ALIGNED(weights, "weights");
+  REQUIRE_ALIGNED(dweights, "dweights");
+  moe::UnpermuteBackwardDesc d;
+  d.dy = dy;
+  d.yd = yd;
+  d.weights = weights;
+  d.inv_pos = inv_pos;
+  d.held = offsets + n_groups(cfg);
+  d.dyd = dyd;
+  d.dweights = dweights;
+  d.T = cfg->T;
+  d.k = cfg->k;
+  d.cols = (int)cols;
+  d.type = type;
+  cudaError_t e = moe::launch_unpermute_backward(d, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "unpermute gradient launch");
+  counted(1);
+  return MOE_OK;
+}
+
+MOE_EXPORT int moe_route_backward(const moe_config* cfg, const void* logits, int32_t logits_type,
+                                  const int32_t* topk_idx, const float* dtopk_w, void* dlogits, moe_stream_t stream) {
+  int rc = check_config(cfg);
+  if (rc) return rc;
+  if (logits_type != MOE_TYPE_F32 && logits_type != MOE_TYPE_BF16)
+    return fail(MOE_ERR_INVALID, "logits must be fp32 or bf16");
+  if (cfg->T == 0) return MOE_OK;
+  REQUIRE_PTR(logits, "logits");
+  REQUIRE_PTR(topk_idx, "topk_idx");
+  REQUIRE_PTR(dtopk_w, "dtopk_w");
+  REQUIRE_PTR(dlogits, "dlogits");
+  moe::RouteBackwardDesc d;
+  d.logits = logits;
+  d.topk_idx = topk_idx;
+  d.dtopk_w = dtopk_w;
+  d.dlogits = dlogits;
+  d.T = cfg->T;
+  d.E = cfg->E;
+  d.k = cfg->k;
+  d.sigmoid = cfg->score == MOE_SCORE_SIGMOID;
+  d.renorm = cfg->renormalize;
+  d.bf16 = logits_type == MOE_TYPE_BF16;
+  d.routed_scale = cfg->routed_scale;
+  cudaError_t e = moe::launch_route_backward(d, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "routing gradient launch");
+  counted(1);
+  return MOE_OK;
+}
+
+// ------------------------------------------------------------------------------------------
 // CUDA graph of the whole layer
 // ------------------------------------------------------------------------------------------
 struct moe_graph_s {

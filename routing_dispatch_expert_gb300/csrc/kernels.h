@@ -269,6 +269,101 @@ struct BalanceLossBackwardDesc {
 };
 cudaError_t launch_balance_loss_backward(const BalanceLossBackwardDesc& d, cudaStream_t stream);
 
+// RMS norm of x + residual and its gradient (rms_norm.cu). cols <= kNormMaxCols; types MOE_TYPE_*.
+constexpr int kNormMaxCols = 16384;
+struct RmsNormDesc {
+  const void* x;         // [rows, cols], ldx apart
+  const void* residual;  // [rows, cols], ldr apart, or nullptr
+  const void* weight;    // [cols] or nullptr: ones
+  void* y;               // [rows, cols] of `type` or nullptr
+  void* total;           // [rows, cols] of residual_type or nullptr
+  void* q;               // [rows, cols] e4m3 or nullptr
+  float* s;              // [rows, ceil(cols / 128)] with q
+  int64_t rows, ldx, ldr;
+  int cols, type, residual_type, weight_type;
+  float eps;
+};
+cudaError_t launch_rms_norm(const RmsNormDesc& d, cudaStream_t stream);
+int rms_norm_backward_blocks(int64_t rows, int cols);  // sums of the weight's gradient: [blocks, cols] fp32 in ws
+struct RmsNormBackwardDesc {
+  const void* dy;      // [rows, cols]
+  const void* total;   // [rows, cols], ldt apart
+  const void* dtotal;  // [rows, cols] of total_type or nullptr
+  const void* weight;  // [cols] or nullptr
+  void* dx;            // [rows, cols] of `type` or nullptr
+  void* dresidual;     // [rows, cols] of total_type or nullptr
+  void* dweight;       // [cols] of weight_type or nullptr
+  void* ws;
+  int64_t rows, ldt;
+  int cols, type, total_type, weight_type;
+  float eps;
+};
+cudaError_t launch_rms_norm_backward(const RmsNormBackwardDesc& d, int* launches, cudaStream_t stream);
+
+// Assignments sorted by expert, and rows there and back (permute.cu).
+int sort_blocks(int64_t n);  // of n assignments; scratch: sort_blocks(n) * E ints
+struct SortDesc {
+  const int32_t* topk_idx;
+  const float* topk_w;  // or nullptr
+  int32_t* counts;
+  int32_t* offsets;
+  int32_t* inv_pos;
+  int32_t* row_token;
+  float* row_weight;  // or nullptr
+  int32_t* scratch;
+  int T, E, k, capacity;
+  int n_slots = 0;
+  int max_replicas = 0;
+  const int32_t* slot_expert = nullptr;
+  const int32_t* slot_replica = nullptr;
+  const int32_t* replicas = nullptr;
+  const int32_t* replica_slot = nullptr;
+};
+cudaError_t launch_sort_tokens(const SortDesc& d, int* launches, cudaStream_t stream);
+struct PermuteDesc {
+  const void* x;         // [T, cols], ldx elements apart
+  const float* x_scales; // [T, ceil(cols / 128)] with xd_scales
+  const int32_t* inv_pos;
+  const int32_t* held;   // rows that hold an assignment
+  void* xd;              // [T k, cols]
+  float* xd_scales;      // [T k, ceil(cols / 128)] or nullptr
+  int64_t ldx;
+  int T, k, cols, element_bytes;
+};
+cudaError_t launch_permute(const PermuteDesc& d, cudaStream_t stream);
+struct UnpermuteDesc {
+  const void* yd;        // [T k, cols]
+  const void* base;      // [T, cols] or nullptr
+  const float* weights;  // [T, k] or nullptr: ones
+  const int32_t* inv_pos;
+  void* y;               // [T, cols]
+  int T, k, cols, type;
+};
+cudaError_t launch_unpermute(const UnpermuteDesc& d, cudaStream_t stream);
+struct UnpermuteBackwardDesc {
+  const void* dy;        // [T, cols]
+  const void* yd;        // [T k, cols]; read with dweights
+  const float* weights;  // [T, k] or nullptr: ones
+  const int32_t* inv_pos;
+  const int32_t* held;
+  void* dyd;             // [T k, cols]
+  float* dweights;       // [T, k] or nullptr
+  int T, k, cols, type;
+};
+cudaError_t launch_unpermute_backward(const UnpermuteBackwardDesc& d, cudaStream_t stream);
+
+// Gradient of the route weights with respect to the logits (route_backward.cu).
+struct RouteBackwardDesc {
+  const void* logits;  // [T, E]
+  const int32_t* topk_idx;
+  const float* dtopk_w;  // [T, k]
+  void* dlogits;         // [T, E]
+  int T, E, k;
+  int sigmoid, renorm, bf16;
+  float routed_scale;
+};
+cudaError_t launch_route_backward(const RouteBackwardDesc& d, cudaStream_t stream);
+
 // Step 4: combine.
 cudaError_t launch_combine(const void* yd, const int32_t* inv_pos, void* y, int T, int h, int k, int shared,
                            cudaStream_t stream);

@@ -1,0 +1,534 @@
+// Tokens sorted by expert and back: the sort of the assignments, the rows copied into its order, the rows added up in token
+// order with the route weights, and the gradient of that.
+//
+// The sort is a stable counting sort of the T k assignments (token, then slot) by expert: an assignment's rank is the number
+// of earlier ones to its expert, its row the expert's offset plus that (under a placement: round robin over the expert's
+// replicas). Whole numbers only, so the order of the atomics does not show. An index outside [0, E) is no assignment; ranks
+// at and past the capacity have no row.
+//   count_kernel  assignments of each block of kItems to each expert
+//   rank_kernel   a block's ranks: the counts of the blocks before it, of the warps before a warp, and within a warp the
+//                 lanes before a lane that hold the same expert; the offsets are made again by every block
+// A batch of one block takes the second kernel alone, which then counts its own.
+//
+// Rows are copied as words, token by token: the row is read once and written to each of its places. Everything here is bound
+// by HBM once there are enough tokens.
+#include <algorithm>
+#include <type_traits>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "rows.cuh"
+
+namespace moe {
+namespace pm {
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+
+struct SortArgs {
+  const int32_t* idx;
+  const float* weight;  // or nullptr
+  int32_t* hist;        // [blocks][E]
+  int32_t* counts;
+  int32_t* offsets;
+  int32_t* inv_pos;
+  int32_t* row_token;
+  float* row_weight;  // or nullptr
+  int64_t n;          // T k
+  int64_t per_block;  // a multiple of kThreads
+  int E, k, cap, blocks;
+  int n_slots, max_replicas;  // 0: one slot an expert
+  const int32_t* slot_expert;
+  const int32_t* slot_replica;
+  const int32_t* replicas;
+  const int32_t* replica_slot;
+};
+
+__global__ void __launch_bounds__(kThreads) count_kernel(const SortArgs a) {
+  extern __shared__ int32_t hist[];
+  for (int e = threadIdx.x; e < a.E; e += kThreads) hist[e] = 0;
+  __syncthreads();
+  const int64_t lo = blockIdx.x * a.per_block, hi = min(a.n, lo + a.per_block);
+  for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) {
+    const int e = a.idx[i];
+    if (e >= 0 && e < a.E) atomicAdd(&hist[e], 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.E; e += kThreads) a.hist[(int64_t)blockIdx.x * a.E + e] = hist[e];
+}
+
+// exclusive prefix of v over the block's threads, and the total
+__device__ __forceinline__ int block_prefix(int v, int* warp_sums, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += u;
+  }
+  __syncthreads();
+  if (lane == 31) warp_sums[warp] = incl;
+  __syncthreads();
+  int before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += warp_sums[w];
+    total += warp_sums[w];
+  }
+  return before + incl - v;
+}
+
+// Shared memory: per warp a count of each expert [kWarps][E]; of the assignments before this block [E]; of all, and then the
+// kept ones [E]; the offset of each group [max(E, n_slots) + 1].
+__global__ void __launch_bounds__(kThreads) rank_kernel(const SortArgs a) {
+  extern __shared__ int32_t sh[];
+  __shared__ int warp_sums[kWarps];
+  const int E = a.E, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int32_t* cnt = sh;
+  int32_t* base = cnt + kWarps * E;
+  int32_t* all = base + E;
+  int32_t* offset = all + E;
+  for (int e = threadIdx.x; e < kWarps * E + 2 * E; e += kThreads) sh[e] = 0;
+  __syncthreads();
+  const bool single = a.blocks == 1;
+  const int64_t lo = blockIdx.x * a.per_block, hi = min(a.n, lo + a.per_block);
+  if (single) {
+    for (int64_t i = threadIdx.x; i < a.n; i += kThreads) {
+      const int e = a.idx[i];
+      if (e >= 0 && e < E) atomicAdd(&all[e], 1);
+    }
+  } else {
+    const int mine = (int)blockIdx.x * E, every = a.blocks * E;
+    for (int i = threadIdx.x; i < every; i += kThreads) {
+      const int c = a.hist[i], e = i % E;
+      if (c) {
+        atomicAdd(&all[e], c);
+        if (i < mine) atomicAdd(&base[e], c);
+      }
+    }
+  }
+  __syncthreads();
+  const int groups = a.n_slots ? a.n_slots : E;
+  int run = 0;
+  for (int g0 = 0; g0 < groups; g0 += kThreads) {
+    const int g = g0 + threadIdx.x;
+    int c = 0;
+    if (g < groups) {
+      if (a.n_slots) {  // rows of replica i of an expert with r of them: ranks i, i + r, .. below what it keeps
+        const int e = a.slot_expert[g], i = a.slot_replica[g], r = a.replicas[e], kept = min(all[e], a.cap);
+        c = kept > i ? (kept - i + r - 1) / r : 0;
+      } else {
+        c = min(all[g], a.cap);
+      }
+    }
+    int total;
+    const int at = run + block_prefix(c, warp_sums, total);
+    if (g < groups) {
+      offset[g] = at;
+      if (blockIdx.x == 0) {
+        a.counts[g] = c;
+        a.offsets[g] = at;
+      }
+    }
+    run += total;
+  }
+  const int held = run;  // rows
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.offsets[groups] = held;
+  __syncthreads();
+  for (int64_t c0 = lo; c0 < hi; c0 += 4 * kThreads) {  // 128 assignments a warp at a time
+    int e4[4], rank[4];
+    const int64_t at = c0 + warp * 128 + lane;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t i = at + 32 * j;
+      const int e = i < hi ? a.idx[i] : -1;
+      e4[j] = e >= 0 && e < E ? e : -1;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int e = e4[j];
+      const uint32_t peers = __match_any_sync(0xffffffffu, e), before = peers & ((1u << lane) - 1u);
+      int32_t* c = cnt + warp * E + max(e, 0);
+      const int had = *c;
+      __syncwarp();
+      if (e >= 0 && !before) *c = had + __popc(peers);
+      __syncwarp();
+      rank[j] = had + __popc(before);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += kThreads) {  // a warp's counts become those before it
+      int n = base[e];
+      for (int w = 0; w < kWarps; ++w) {
+        const int c = cnt[w * E + e];
+        cnt[w * E + e] = n;
+        n += c;
+      }
+      base[e] = n;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t i = at + 32 * j;
+      if (i >= hi) continue;
+      const int e = e4[j];
+      int row = -1;
+      if (e >= 0) {
+        const int r = rank[j] + cnt[warp * E + e];
+        if (r < a.cap) {
+          if (a.n_slots) {
+            const int n = a.replicas[e];
+            row = offset[a.replica_slot[(int64_t)e * a.max_replicas + r % n]] + r / n;
+          } else {
+            row = offset[e] + r;
+          }
+          a.row_token[row] = (int32_t)(i / a.k);
+          if (a.row_weight) a.row_weight[row] = a.weight[i];
+        }
+      }
+      a.inv_pos[i] = row;
+    }
+    if (c0 + 4 * kThreads < hi) {
+      __syncthreads();
+      for (int e = threadIdx.x; e < kWarps * E; e += kThreads) cnt[e] = 0;
+      __syncthreads();
+    }
+  }
+  for (int64_t r = max(lo, (int64_t)held) + threadIdx.x; r < hi; r += kThreads) {  // rows that hold nothing
+    a.row_token[r] = -1;
+    if (a.row_weight) a.row_weight[r] = 0.f;
+  }
+}
+
+// ------------------------------------------------------------------------------------------
+// rows into the sorted order
+// ------------------------------------------------------------------------------------------
+struct CopyPlane {
+  const void* src;  // [T], ld words from row to row
+  void* dst;        // [T k], contiguous
+  int64_t ld;
+  int words;        // of a row
+  int pieces;       // of a row: a warp's work
+};
+
+constexpr int kDepth = 4;  // words of a lane in a piece
+
+template <class Word>
+__device__ __forceinline__ void copy_item(const CopyPlane& p, const int32_t* inv_pos, int64_t T, int k, int64_t held,
+                                          int64_t item, int lane) {
+  const int64_t t = item / p.pieces;
+  const int c0 = (int)(item - t * p.pieces) * 32 * kDepth + lane;
+  Word v[kDepth];
+  if (t >= T) {  // a row that holds nothing
+    Word* dst = static_cast<Word*>(p.dst) + (held + (t - T)) * p.words;
+#pragma unroll
+    for (int u = 0; u < kDepth; ++u)
+      if (c0 + 32 * u < p.words) dst[c0 + 32 * u] = Word{};
+    return;
+  }
+  const Word* src = static_cast<const Word*>(p.src) + t * p.ld;
+#pragma unroll
+  for (int u = 0; u < kDepth; ++u)
+    if (c0 + 32 * u < p.words) v[u] = src[c0 + 32 * u];
+  const int mine = lane < k ? inv_pos[t * k + lane] : -1;
+  for (int j = 0; j < k; ++j) {
+    const int r = __shfl_sync(0xffffffffu, mine, j);
+    if (r < 0) continue;
+    Word* dst = static_cast<Word*>(p.dst) + (int64_t)r * p.words;
+#pragma unroll
+    for (int u = 0; u < kDepth; ++u)
+      if (c0 + 32 * u < p.words) dst[c0 + 32 * u] = v[u];
+  }
+}
+
+template <class Word>
+__global__ void __launch_bounds__(256) permute_kernel(const CopyPlane p, const CopyPlane scales, const int32_t* inv_pos,
+                                                      const int32_t* held_at, int64_t T, int k) {
+  const int lane = threadIdx.x & 31;
+  const int64_t warps = ((int64_t)gridDim.x * blockDim.x) >> 5;
+  const int64_t held = *held_at, rows = T + (T * k - held);  // token rows, then those that hold nothing
+  const int64_t items = rows * p.pieces, more = scales.words ? rows * scales.pieces : 0;
+  for (int64_t it = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; it < items + more; it += warps) {
+    if (it < items)
+      copy_item<Word>(p, inv_pos, T, k, held, it, lane);
+    else
+      copy_item<uint32_t>(scales, inv_pos, T, k, held, it - items, lane);
+  }
+}
+
+// ------------------------------------------------------------------------------------------
+// rows back in token order
+// ------------------------------------------------------------------------------------------
+constexpr int kBatch = 8;  // rows of a token in flight
+
+struct AddArgs {
+  const void* yd;
+  const void* base;      // or nullptr
+  const float* weights;  // [T, k] or nullptr
+  const int32_t* inv_pos;
+  void* y;
+  int64_t T;
+  int cols, chunks, k;
+};
+
+// A warp a chunk of a token's row: fp32, the base first and then the slots in order.
+template <int TYPE, int MAP>
+__global__ void __launch_bounds__(256) unpermute_kernel(const AddArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int64_t warps = ((int64_t)gridDim.x * blockDim.x) >> 5, items = a.T * a.chunks;
+  for (int64_t it = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; it < items; it += warps) {
+    const int64_t t = it / a.chunks;
+    const int c0 = (int)(it - t * a.chunks) * rows::kChunk;
+    const int mine = lane < a.k ? a.inv_pos[t * a.k + lane] : -1;
+    const float weight = a.weights && lane < a.k ? a.weights[t * a.k + lane] : 1.f;
+    const int64_t pitch = (int64_t)a.cols * rows::kSize<TYPE>;
+    float sum[8], f[8];
+    rows::Chunk<TYPE, MAP> b, v[kBatch];
+    if (a.base)
+      b.load(static_cast<const char*>(a.base) + t * pitch, c0, a.cols, lane);
+    else
+      b.clear();
+    for (int j0 = 0; j0 < a.k; j0 += kBatch) {
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int r = __shfl_sync(0xffffffffu, mine, min(j0 + j, 31));
+        if (j0 + j < a.k && r >= 0) v[j].load(static_cast<const char*>(a.yd) + r * pitch, c0, a.cols, lane);
+      }
+      if (j0 == 0) b.values(sum);
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int r = __shfl_sync(0xffffffffu, mine, min(j0 + j, 31));
+        const float w = __shfl_sync(0xffffffffu, weight, min(j0 + j, 31));
+        if (j0 + j >= a.k || r < 0) continue;
+        v[j].values(f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i] = fmaf(w, f[i], sum[i]);
+      }
+    }
+    rows::store<TYPE, MAP>(static_cast<char*>(a.y) + t * pitch, c0, a.cols, lane, sum);
+  }
+}
+
+struct SpreadArgs {
+  const void* dy;
+  const void* yd;        // or nullptr: no gradient of the weights
+  const float* weights;  // [T, k] or nullptr
+  const int32_t* inv_pos;
+  const int32_t* held_at;
+  void* dyd;
+  float* dweights;  // [T, k] or nullptr
+  int64_t T;
+  int cols, chunks, k;
+};
+
+// A block of W warps a token: its row of dy to its k rows of dyd, and their products with yd's rows, summed over the lanes
+// and then the warps. The blocks past the tokens clear the rows that hold nothing.
+template <int TYPE, int MAP>
+__global__ void __launch_bounds__(256) spread_kernel(const SpreadArgs a) {
+  __shared__ float part[8][kBatch];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
+  const int64_t pitch = (int64_t)a.cols * rows::kSize<TYPE>;
+  float f[8], g[8];
+  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+    const int mine = lane < a.k ? a.inv_pos[t * a.k + lane] : -1;
+    const float weight = a.weights && lane < a.k ? a.weights[t * a.k + lane] : 1.f;
+    for (int j0 = 0; j0 < a.k; j0 += kBatch) {
+      float dot[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) dot[j] = 0.f;
+      for (int c = warp; c < a.chunks; c += W) {
+        const int c0 = c * rows::kChunk;
+        rows::Chunk<TYPE, MAP> dy, v[kBatch];
+        dy.load(static_cast<const char*>(a.dy) + t * pitch, c0, a.cols, lane);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          const int r = __shfl_sync(0xffffffffu, mine, min(j0 + j, 31));
+          if (a.yd && j0 + j < a.k && r >= 0) v[j].load(static_cast<const char*>(a.yd) + r * pitch, c0, a.cols, lane);
+        }
+        dy.values(g);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          const int r = __shfl_sync(0xffffffffu, mine, min(j0 + j, 31));
+          const float w = __shfl_sync(0xffffffffu, weight, min(j0 + j, 31));
+          if (j0 + j >= a.k || r < 0) continue;
+          if (a.yd) {
+            v[j].values(f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dot[j] = fmaf(g[i], f[i], dot[j]);
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[i] = w * g[i];
+          rows::store<TYPE, MAP>(static_cast<char*>(a.dyd) + r * pitch, c0, a.cols, lane, f);
+        }
+      }
+      if (!a.dweights) continue;
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], o);
+        if (lane == j) part[warp][j] = dot[j];
+      }
+      __syncthreads();
+      if (threadIdx.x < kBatch && j0 + threadIdx.x < a.k) {
+        float sum = 0.f;
+        for (int w = 0; w < W; ++w) sum += part[w][threadIdx.x];
+        a.dweights[t * a.k + j0 + threadIdx.x] = sum;
+      }
+      __syncthreads();
+    }
+  }
+  const int64_t held = *a.held_at;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = 0.f;
+  for (int64_t r = held + blockIdx.x; r < a.T * a.k; r += gridDim.x)
+    for (int c = warp; c < a.chunks; c += W)
+      rows::store<TYPE, MAP>(static_cast<char*>(a.dyd) + r * pitch, c * rows::kChunk, a.cols, lane, f);
+}
+
+// The word that rows of `bytes` bytes, `ld` bytes apart, are copied by: the widest that every row begins on.
+template <class F>
+cudaError_t with_word(int64_t bytes, int64_t ld, F&& f) {
+  if (bytes % 16 == 0 && ld % 16 == 0) return f(uint4{});
+  if (bytes % 4 == 0 && ld % 4 == 0) return f(uint32_t{});
+  if (bytes % 2 == 0 && ld % 2 == 0) return f(uint16_t{});
+  return f(uint8_t{});
+}
+
+template <class F>
+cudaError_t with_rows(int type, int64_t cols, F&& f) {
+  const bool aligned = rows::aligned_rows(type, cols, 2);
+  using std::integral_constant;
+  if (type == MOE_TYPE_F32)
+    return aligned ? f(integral_constant<int, MOE_TYPE_F32>{}, integral_constant<int, rows::kMap4>{})
+                   : f(integral_constant<int, MOE_TYPE_F32>{}, integral_constant<int, rows::kMap1>{});
+  if (type == MOE_TYPE_BF16)
+    return aligned ? f(integral_constant<int, MOE_TYPE_BF16>{}, integral_constant<int, rows::kMap8>{})
+                   : f(integral_constant<int, MOE_TYPE_BF16>{}, integral_constant<int, rows::kMap1>{});
+  return aligned ? f(integral_constant<int, MOE_TYPE_F16>{}, integral_constant<int, rows::kMap8>{})
+                 : f(integral_constant<int, MOE_TYPE_F16>{}, integral_constant<int, rows::kMap1>{});
+}
+
+constexpr int64_t kItems = 4 * kThreads;  // assignments of a block of the sort, at least
+constexpr int kMaxBlocks = 128;           // every block reads every block's counts
+int64_t per_block(int64_t n) {
+  return std::max<int64_t>(kItems, cdiv(cdiv(n, kMaxBlocks), kItems) * kItems);
+}
+
+}  // namespace pm
+
+int sort_blocks(int64_t n) { return (int)cdiv(n, pm::per_block(n)); }
+
+cudaError_t launch_sort_tokens(const SortDesc& d, int* launches, cudaStream_t stream) {
+  pm::SortArgs a;
+  a.idx = d.topk_idx;
+  a.weight = d.topk_w;
+  a.hist = d.scratch;
+  a.counts = d.counts;
+  a.offsets = d.offsets;
+  a.inv_pos = d.inv_pos;
+  a.row_token = d.row_token;
+  a.row_weight = d.row_weight;
+  a.n = (int64_t)d.T * d.k;
+  a.per_block = pm::per_block(a.n);
+  a.E = d.E;
+  a.k = d.k;
+  a.cap = d.capacity > 0 ? d.capacity : 0x7fffffff;
+  a.blocks = sort_blocks(a.n);
+  a.n_slots = d.n_slots;
+  a.max_replicas = d.max_replicas;
+  a.slot_expert = d.slot_expert;
+  a.slot_replica = d.slot_replica;
+  a.replicas = d.replicas;
+  a.replica_slot = d.replica_slot;
+  *launches = 0;
+  if (d.T == 0) {
+    const int groups = d.n_slots ? d.n_slots : d.E;
+    cudaError_t e = cudaMemsetAsync(d.counts, 0, sizeof(int32_t) * groups, stream);
+    if (e == cudaSuccess) e = cudaMemsetAsync(d.offsets, 0, sizeof(int32_t) * (groups + 1), stream);
+    return e;
+  }
+  const size_t smem = sizeof(int32_t) * ((size_t)(pm::kWarps + 2) * d.E + std::max(d.E, d.n_slots));
+  static PerDevice<bool> attr;  // up to 1024 experts and slots need more than the default
+  bool set = false;
+  cudaError_t e = per_device<bool>(
+      attr,
+      [](bool& v) {
+        const cudaError_t r = cudaFuncSetAttribute(pm::rank_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (int)(sizeof(int32_t) * (pm::kWarps + 3) * 1024));
+        v = r == cudaSuccess;
+        return r;
+      },
+      &set);
+  if (e != cudaSuccess) return e;
+  if (a.blocks > 1) {
+    pm::count_kernel<<<a.blocks, pm::kThreads, sizeof(int32_t) * d.E, stream>>>(a);
+    ++*launches;
+  }
+  pm::rank_kernel<<<a.blocks, pm::kThreads, smem, stream>>>(a);
+  ++*launches;
+  return cudaGetLastError();
+}
+
+cudaError_t launch_permute(const PermuteDesc& d, cudaStream_t stream) {
+  const int64_t bytes = (int64_t)d.cols * d.element_bytes, ld = d.T > 1 ? d.ldx * d.element_bytes : bytes;
+  return pm::with_word(bytes, ld, [&](auto word) {
+    using Word = decltype(word);
+    pm::CopyPlane p, s{};
+    p.src = d.x;
+    p.dst = d.xd;
+    p.ld = ld / (int64_t)sizeof(Word);
+    p.words = (int)(bytes / (int64_t)sizeof(Word));
+    p.pieces = (int)cdiv(p.words, 32 * pm::kDepth);
+    if (d.xd_scales) {
+      s.src = d.x_scales;
+      s.dst = d.xd_scales;
+      s.ld = s.words = (int)cdiv(d.cols, 128);
+      s.pieces = (int)cdiv(s.words, 32 * pm::kDepth);
+    }
+    const int64_t items = (int64_t)d.T * (p.pieces + (d.xd_scales ? s.pieces : 0));
+    const unsigned blocks = (unsigned)std::min<int64_t>(cdiv(items, 8), (int64_t)num_sms() * 16);
+    pm::permute_kernel<Word><<<blocks, 256, 0, stream>>>(p, s, d.inv_pos, d.held, d.T, d.k);
+    return cudaGetLastError();
+  });
+}
+
+cudaError_t launch_unpermute(const UnpermuteDesc& d, cudaStream_t stream) {
+  pm::AddArgs a;
+  a.yd = d.yd;
+  a.base = d.base;
+  a.weights = d.weights;
+  a.inv_pos = d.inv_pos;
+  a.y = d.y;
+  a.T = d.T;
+  a.cols = d.cols;
+  a.chunks = (int)cdiv(d.cols, rows::kChunk);
+  a.k = d.k;
+  const unsigned blocks = (unsigned)std::min<int64_t>(cdiv(a.T * a.chunks, 8), (int64_t)num_sms() * 16);
+  return pm::with_rows(d.type, d.cols, [&](auto T, auto M) {
+    pm::unpermute_kernel<decltype(T)::value, decltype(M)::value><<<blocks, 256, 0, stream>>>(a);
+    return cudaGetLastError();
+  });
+}
+
+cudaError_t launch_unpermute_backward(const UnpermuteBackwardDesc& d, cudaStream_t stream) {
+  pm::SpreadArgs a;
+  a.dy = d.dy;
+  a.yd = d.dweights ? d.yd : nullptr;
+  a.weights = d.weights;
+  a.inv_pos = d.inv_pos;
+  a.held_at = d.held;
+  a.dyd = d.dyd;
+  a.dweights = d.dweights;
+  a.T = d.T;
+  a.cols = d.cols;
+  a.chunks = (int)cdiv(d.cols, rows::kChunk);
+  a.k = d.k;
+  const int W = std::min(8, a.chunks);
+  const unsigned blocks = (unsigned)std::min<int64_t>(a.T, (int64_t)num_sms() * 64 / W);
+  return pm::with_rows(d.type, d.cols, [&](auto T, auto M) {
+    pm::spread_kernel<decltype(T)::value, decltype(M)::value><<<blocks, 32 * W, 0, stream>>>(a);
+    return cudaGetLastError();
+  });
+}
+
+}  // namespace moe

@@ -1,0 +1,437 @@
+// Root-mean-square norm of the sum of a row and its residual, with an output in 8 bits, and its gradient.
+//
+//   t = x + r,  n = t * rstd,  rstd = 1 / sqrt(mean(t^2) + eps),  y = n * w
+//   scale of 128 columns = amax |y| / 448 (at least 2^-126; 1 where all are 0), code = e4m3(RN(y / scale))
+//   with g = dy * w:  dt = rstd * (g - n * mean(g n)) + (the gradient that reaches t from elsewhere),  dw = sum_rows dy n
+//
+// Everything is fp32: the sum is normalised and quantised before it is rounded for the residual stream, and each output is
+// rounded once. The gradient is that of the norm of the t it is given; rstd is made again from t, which it reads anyway,
+// instead of being stored.
+//
+// Both are bound by HBM: a row is read once and held in registers between its reduction and its outputs.
+#include "common.cuh"
+#include "fp4_impl.cuh"
+#include "kernels.h"
+#include "rows.cuh"
+
+namespace moe {
+namespace rn {
+
+using rows::Chunk;
+using rows::kChunk;
+using rows::kMap1;
+using rows::kMap4;
+using rows::kMap8;
+
+constexpr int kNone = -1;
+
+struct Args {
+  const void* x;
+  const void* r;
+  const void* w;
+  void* y;
+  void* total;
+  uint8_t* q;
+  float* s;
+  int64_t rows, ldx, ldr;
+  int cols, w_f32;
+  float eps;
+};
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// A chunk of the weight; ones where there is none.
+template <int TYPE, int MAP>
+__device__ __forceinline__ void load_weight(const void* w, int w_f32, int c0, int cols, int lane, float (&f)[8]) {
+  if (!w) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = 1.f;
+  } else if (w_f32) {
+    Chunk<MOE_TYPE_F32, MAP> c;
+    c.load(w, c0, cols, lane);
+    c.values(f);
+  } else {
+    Chunk<TYPE, MAP> c;
+    c.load(w, c0, cols, lane);
+    c.values(f);
+  }
+}
+
+// Codes and scales of a chunk: two blocks of 128 columns. The largest magnitude is taken over the bits, under which a NaN is
+// larger than every number: a block that holds an infinity or a NaN stands for NaN throughout.
+template <int MAP>
+__device__ __forceinline__ void quantize(const Args& a, int64_t row, int c0, int lane, const float (&y)[8]) {
+  uint32_t m[2] = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int h = MAP == kMap8 ? 0 : i / 4;
+    m[h] = max(m[h], __float_as_uint(y[i]) & 0x7FFFFFFFu);
+  }
+  if (MAP == kMap8) {
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) m[0] = max(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
+  } else {
+    m[0] = __reduce_max_sync(0xffffffffu, m[0]);
+    m[1] = __reduce_max_sync(0xffffffffu, m[1]);
+  }
+  const int nb = (a.cols + 127) / 128;
+  float v[8];
+#pragma unroll
+  for (int h = 0; h < (MAP == kMap8 ? 1 : 2); ++h) {
+    constexpr int kN = MAP == kMap8 ? 8 : 4;
+    float scale = 1.f;
+    if (m[h]) scale = m[h] > fp4::kInfBits ? __uint_as_float(m[h]) : fmaxf(__fdiv_rn(__uint_as_float(m[h]), 448.0f), 1.1754944e-38f);
+    if (fp4::ordinary(scale) && m[h] < fp4::kOrdinaryMax) {
+      const float r = __frcp_rn(scale);
+#pragma unroll
+      for (int i = 0; i < kN; i += 2) {
+        const float2 u = fp4::quotient(make_float2(y[4 * h + i], y[4 * h + i + 1]), make_float2(scale, scale), make_float2(r, r));
+        v[4 * h + i] = u.x, v[4 * h + i + 1] = u.y;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kN; ++i) v[4 * h + i] = __fdiv_rn(y[4 * h + i], scale);
+    }
+    const int b = c0 / 128 + (MAP == kMap8 ? lane / 16 : h);
+    if ((MAP == kMap8 ? lane % 16 : lane) == 0 && b < nb) a.s[row * nb + b] = scale;
+  }
+  uint32_t code[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) code[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i], v[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+  uint8_t* q = a.q + row * a.cols + c0;
+  if (MAP == kMap8 && c0 + 8 * lane + 8 <= a.cols) {
+    *reinterpret_cast<uint2*>(q + 8 * lane) = make_uint2(code[0] | code[1] << 16, code[2] | code[3] << 16);
+    return;
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (MAP == kMap4 && c0 + 128 * h + 4 * lane + 4 <= a.cols) {
+      *reinterpret_cast<uint32_t*>(q + 128 * h + 4 * lane) = code[2 * h] | code[2 * h + 1] << 16;
+      continue;
+    }
+#pragma unroll
+    for (int i = 4 * h; i < 4 * h + 4; ++i) {
+      const int c = rows::column<MAP>(lane, i);
+      if (c0 + c < a.cols) q[c] = (uint8_t)(code[i / 2] >> (8 * (i & 1)));
+    }
+  }
+}
+
+// blockDim.x / 32 warps a row, warp w with chunks w, w + W, ..; blockDim.y rows a block.
+template <int XT, int RT, int MAP, bool FP8, int CPW>
+__global__ void __launch_bounds__(1024) norm_kernel(const Args a) {
+  __shared__ float part[32];
+  constexpr int kRT = RT == kNone ? XT : RT;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
+  const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  const bool in = row < a.rows;
+  float t[CPW][8], w[CPW][8];
+  if (in) {
+    Chunk<XT, MAP> x[CPW];
+    Chunk<kRT, MAP> r[CPW];
+    const char* xr = static_cast<const char*>(a.x) + row * a.ldx * rows::kSize<XT>;
+    const char* rr = RT == kNone ? nullptr : static_cast<const char*>(a.r) + row * a.ldr * rows::kSize<kRT>;
+#pragma unroll
+    for (int j = 0; j < CPW; ++j) {
+      const int c0 = (warp + j * W) * kChunk;
+      x[j].load(xr, c0, a.cols, lane);
+      if (RT != kNone) r[j].load(rr, c0, a.cols, lane);
+    }
+#pragma unroll
+    for (int j = 0; j < CPW; ++j) load_weight<XT, MAP>(a.w, a.w_f32, (warp + j * W) * kChunk, a.cols, lane, w[j]);
+#pragma unroll
+    for (int j = 0; j < CPW; ++j) {
+      x[j].values(t[j]);
+      if (RT != kNone) {
+        float f[8];
+        r[j].values(f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[j][i] += f[i];
+      }
+    }
+  }
+  float ss = 0.f;
+  if (in) {
+#pragma unroll
+    for (int j = 0; j < CPW; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = fmaf(t[j][i], t[j][i], ss);
+  }
+  ss = warp_sum(ss);
+  if (W > 1) {
+    if (lane == 0) part[warp] = ss;
+    __syncthreads();
+    ss = warp_sum(lane < W ? part[lane] : 0.f);
+  }
+  if (!in) return;
+  const float rstd = __frsqrt_rn(__fdiv_rn(ss, (float)a.cols) + a.eps);
+#pragma unroll
+  for (int j = 0; j < CPW; ++j) {
+    const int c0 = (warp + j * W) * kChunk;
+    if (c0 >= a.cols) break;
+    if (RT != kNone && a.total)
+      rows::store<kRT, MAP>(static_cast<char*>(a.total) + row * a.cols * rows::kSize<kRT>, c0, a.cols, lane, t[j]);
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = t[j][i] * rstd * w[j][i];
+    if (a.y) rows::store<XT, MAP>(static_cast<char*>(a.y) + row * a.cols * rows::kSize<XT>, c0, a.cols, lane, y);
+    if (FP8) quantize<MAP>(a, row, c0, lane, y);
+  }
+}
+
+struct BackArgs {
+  const void* dy;
+  const void* t;
+  const void* dt;
+  const void* w;
+  void* dx;
+  void* dr;
+  float* part;   // [blocks][cols] or nullptr: no gradient of the weight
+  int64_t rows, ldt;
+  int cols, w_f32;
+  float eps;
+};
+
+constexpr int kGroups = 8;  // rows of a block at a time, where a warp holds a row
+
+// Persistent: a thread has the same columns in every row, so it keeps the weight and the weight's gradient of them in
+// registers. GROUPS rows at a time where one warp holds a row, else one.
+template <int TYPE, int TT, int MAP, int CPW, int GROUPS, int THREADS>
+__global__ void __launch_bounds__(THREADS) back_kernel(const BackArgs a) {
+  __shared__ float2 part[2][32];
+  __shared__ float dw_part[GROUPS > 1 ? GROUPS : 1][GROUPS > 1 ? kChunk : 1];
+  const int lane = threadIdx.x & 31, warp = GROUPS > 1 ? 0 : threadIdx.x >> 5, W = GROUPS > 1 ? 1 : blockDim.x >> 5;
+  const int group = GROUPS > 1 ? threadIdx.x >> 5 : 0;
+  float w[CPW][8], dw[CPW][8];
+#pragma unroll
+  for (int j = 0; j < CPW; ++j) {
+    load_weight<TYPE, MAP>(a.w, a.w_f32, (warp + j * W) * kChunk, a.cols, lane, w[j]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dw[j][i] = 0.f;
+  }
+  constexpr bool kAhead = TYPE != MOE_TYPE_F32 && TT != MOE_TYPE_F32 && MAP != kMap1 && THREADS <= 512;
+  struct Row {
+    Chunk<TYPE, MAP> dy[CPW];
+    Chunk<TT, MAP> t[CPW], dt[CPW];
+  };
+  auto fetch = [&](Row& r, int64_t row) {
+    const char* dyr = static_cast<const char*>(a.dy) + row * a.cols * rows::kSize<TYPE>;
+    const char* tr = static_cast<const char*>(a.t) + row * a.ldt * rows::kSize<TT>;
+    const char* dtr = static_cast<const char*>(a.dt) + row * a.cols * rows::kSize<TT>;
+#pragma unroll
+    for (int j = 0; j < CPW; ++j) {
+      const int c0 = (warp + j * W) * kChunk;
+      r.dy[j].load(dyr, c0, a.cols, lane);
+      r.t[j].load(tr, c0, a.cols, lane);
+      if (a.dt)
+        r.dt[j].load(dtr, c0, a.cols, lane);
+      else
+        r.dt[j].clear();
+    }
+  };
+  const int64_t step = (int64_t)gridDim.x * GROUPS;
+  int64_t row = (int64_t)blockIdx.x * GROUPS + group;
+  Row cur, next;
+  if (kAhead && row < a.rows) fetch(next, row);
+  for (int turn = 0; row < a.rows; row += step, turn ^= 1) {
+    if (kAhead) {
+      cur = next;
+      if (row + step < a.rows) fetch(next, row + step);
+    } else {
+      fetch(cur, row);
+    }
+    float ss = 0.f, gt = 0.f;
+#pragma unroll
+    for (int j = 0; j < CPW; ++j) {
+      float g[8], v[8];
+      cur.dy[j].values(g);
+      cur.t[j].values(v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        ss = fmaf(v[i], v[i], ss);
+        gt = fmaf(g[i] * w[j][i], v[i], gt);
+      }
+    }
+    ss = warp_sum(ss);
+    gt = warp_sum(gt);
+    if (W > 1) {  // one barrier a row: the next row's sums go to the other half
+      if (lane == 0) part[turn][warp] = make_float2(ss, gt);
+      __syncthreads();
+      const float2 p = lane < W ? part[turn][lane] : make_float2(0.f, 0.f);
+      ss = warp_sum(p.x);
+      gt = warp_sum(p.y);
+    }
+    const float rstd = __frsqrt_rn(__fdiv_rn(ss, (float)a.cols) + a.eps);
+    const float dot = __fdiv_rn(gt, (float)a.cols) * rstd;  // mean(g n)
+#pragma unroll
+    for (int j = 0; j < CPW; ++j) {
+      const int c0 = (warp + j * W) * kChunk;
+      if (c0 >= a.cols) break;
+      float g[8], v[8], d[8];
+      cur.dy[j].values(g);
+      cur.t[j].values(v);
+      cur.dt[j].values(d);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float n = v[i] * rstd;
+        dw[j][i] = fmaf(g[i], n, dw[j][i]);
+        d[i] = fmaf(rstd, fmaf(-n, dot, g[i] * w[j][i]), d[i]);
+      }
+      if (a.dx) rows::store<TYPE, MAP>(static_cast<char*>(a.dx) + row * a.cols * rows::kSize<TYPE>, c0, a.cols, lane, d);
+      if (a.dr) rows::store<TT, MAP>(static_cast<char*>(a.dr) + row * a.cols * rows::kSize<TT>, c0, a.cols, lane, d);
+    }
+  }
+  if (!a.part) return;
+  if (GROUPS > 1) {  // the block's rows, in order
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dw_part[group][rows::column<MAP>(lane, i)] = dw[0][i];
+    __syncthreads();
+    for (int c = threadIdx.x; c < a.cols; c += 32 * GROUPS) {
+      float sum = 0.f;
+#pragma unroll
+      for (int k = 0; k < GROUPS; ++k) sum += dw_part[k][c];
+      a.part[(int64_t)blockIdx.x * a.cols + c] = sum;
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < CPW; ++j)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = (warp + j * W) * kChunk + rows::column<MAP>(lane, i);
+      if (c < a.cols) a.part[(int64_t)blockIdx.x * a.cols + c] = dw[j][i];
+    }
+}
+
+// The weight's gradient from the blocks' sums, in block order: 32 columns a block, 32 warps over the sums.
+__global__ void __launch_bounds__(1024) dweight_kernel(const float* part, int n, int cols, int type, void* dw) {
+  __shared__ float sums[32][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+  float sum = 0.f;
+  if (c < cols)
+    for (int b = warp; b < n; b += 32) sum += part[(int64_t)b * cols + c];
+  sums[warp][lane] = sum;
+  __syncthreads();
+  sum = warp_sum(sums[lane][warp]);
+  if (lane == 0 && blockIdx.x * 32 + warp < cols) {
+    const int at = blockIdx.x * 32 + warp;
+    if (type == MOE_TYPE_F32)
+      rows::store_bits<MOE_TYPE_F32>(dw, at, rows::bits_of<MOE_TYPE_F32>(sum));
+    else if (type == MOE_TYPE_BF16)
+      rows::store_bits<MOE_TYPE_BF16>(dw, at, rows::bits_of<MOE_TYPE_BF16>(sum));
+    else
+      rows::store_bits<MOE_TYPE_F16>(dw, at, rows::bits_of<MOE_TYPE_F16>(sum));
+  }
+}
+
+template <int V>
+using Int = std::integral_constant<int, V>;
+
+// f(type, the other type, map) of rows of `type` beside rows of `other` (kNone, the same, or fp32)
+template <class F>
+cudaError_t with_types(int type, int other, bool aligned, F&& f) {
+  auto mapped = [&](auto T, auto O) {
+    constexpr int kAligned = decltype(T)::value == MOE_TYPE_F32 ? kMap4 : kMap8;
+    return aligned ? f(T, O, Int<kAligned>{}) : f(T, O, Int<kMap1>{});
+  };
+  auto beside = [&](auto T) {
+    if (other == kNone) return mapped(T, Int<kNone>{});
+    if (other == MOE_TYPE_F32) return mapped(T, Int<MOE_TYPE_F32>{});
+    return mapped(T, T);
+  };
+  if (type == MOE_TYPE_F32) return beside(Int<MOE_TYPE_F32>{});
+  if (type == MOE_TYPE_BF16) return beside(Int<MOE_TYPE_BF16>{});
+  return beside(Int<MOE_TYPE_F16>{});
+}
+
+}  // namespace rn
+
+cudaError_t launch_rms_norm(const RmsNormDesc& d, cudaStream_t stream) {
+  rn::Args a;
+  a.x = d.x;
+  a.r = d.residual;
+  a.w = d.weight;
+  a.y = d.y;
+  a.total = d.total;
+  a.q = static_cast<uint8_t*>(d.q);
+  a.s = d.s;
+  a.rows = d.rows;
+  a.ldx = d.ldx;
+  a.ldr = d.ldr;
+  a.cols = d.cols;
+  a.w_f32 = d.weight_type == MOE_TYPE_F32;
+  a.eps = d.eps;
+  const bool aligned = rows::aligned_rows(d.type, d.ldx, d.rows) && rows::aligned_rows(d.type, d.cols, d.rows) &&
+                       (!d.residual || rows::aligned_rows(d.type, d.ldr, d.rows));
+  const int chunks = (int)cdiv(d.cols, rows::kChunk);
+  const int cpw = chunks > 8 ? 2 : 1;
+  const int W = (int)cdiv(chunks, cpw), G = W == 1 ? 8 : 1;
+  const dim3 block(32 * W, G);
+  const unsigned grid = (unsigned)cdiv(d.rows, G);
+  return rn::with_types(d.type, d.residual ? d.residual_type : rn::kNone, aligned, [&](auto T, auto R, auto M) {
+    constexpr int kT = decltype(T)::value, kR = decltype(R)::value, kM = decltype(M)::value;
+    auto go = [&](auto kernel) {
+      kernel<<<grid, block, 0, stream>>>(a);
+      return cudaGetLastError();
+    };
+    if (d.q) return cpw == 2 ? go(rn::norm_kernel<kT, kR, kM, true, 2>) : go(rn::norm_kernel<kT, kR, kM, true, 1>);
+    return cpw == 2 ? go(rn::norm_kernel<kT, kR, kM, false, 2>) : go(rn::norm_kernel<kT, kR, kM, false, 1>);
+  });
+}
+
+namespace rn {
+
+// Warps of a row and blocks of the gradient's kernel: 1024 threads an SM, each at least one row.
+int back_warps(int cols) {
+  const int chunks = (int)cdiv(cols, rows::kChunk);
+  return chunks > 8 ? (int)cdiv(chunks, 2) : chunks;
+}
+
+}  // namespace rn
+
+int rms_norm_backward_blocks(int64_t rows, int cols) {
+  const int W = rn::back_warps(cols), G = W == 1 ? rn::kGroups : 1;
+  const int per_sm = std::max(1, 32 / (W * G));
+  return (int)std::max<int64_t>(1, std::min<int64_t>(cdiv(rows, G), (int64_t)kNumSMsHint * per_sm));
+}
+
+cudaError_t launch_rms_norm_backward(const RmsNormBackwardDesc& d, int* launches, cudaStream_t stream) {
+  rn::BackArgs a;
+  a.dy = d.dy;
+  a.t = d.total;
+  a.dt = d.dtotal;
+  a.w = d.weight;
+  a.dx = d.dx;
+  a.dr = d.dresidual;
+  a.part = d.dweight ? static_cast<float*>(d.ws) : nullptr;
+  a.rows = d.rows;
+  a.ldt = d.ldt;
+  a.cols = d.cols;
+  a.w_f32 = d.weight_type == MOE_TYPE_F32;
+  a.eps = d.eps;
+  const bool aligned = rows::aligned_rows(d.type, d.ldt, d.rows) && rows::aligned_rows(d.type, d.cols, d.rows);
+  const int W = rn::back_warps(d.cols);
+  const int grid = rms_norm_backward_blocks(d.rows, d.cols);
+  *launches = d.dweight ? 2 : 1;
+  cudaError_t e = rn::with_types(d.type, d.total_type, aligned, [&](auto T, auto R, auto M) {
+    constexpr int kT = decltype(T)::value, kM = decltype(M)::value;
+    constexpr int kR = decltype(R)::value == rn::kNone ? kT : decltype(R)::value;
+    auto go = [&](auto kernel, int threads) {
+      kernel<<<grid, threads, 0, stream>>>(a);
+      return cudaGetLastError();
+    };
+    if (W == 1) return go(rn::back_kernel<kT, kR, kM, 1, rn::kGroups, 32 * rn::kGroups>, 32 * rn::kGroups);
+    if (d.cols <= 8 * rows::kChunk) return go(rn::back_kernel<kT, kR, kM, 1, 1, 256>, 32 * W);
+    if (W <= 16) return go(rn::back_kernel<kT, kR, kM, 2, 1, 512>, 32 * W);
+    return go(rn::back_kernel<kT, kR, kM, 2, 1, 1024>, 32 * W);
+  });
+  if (e != cudaSuccess || !d.dweight) return e;
+  rn::dweight_kernel<<<(unsigned)cdiv(d.cols, 32), 1024, 0, stream>>>(a.part, grid, d.cols, d.weight_type, d.dweight);
+  return cudaGetLastError();
+}
+
+}  // namespace moe

@@ -1,0 +1,159 @@
+// Rows of fp32, bf16 or fp16 numbers as the kernels of the norm (rms_norm.cu) and of the row permutation (permute.cu)
+// read and write them: a warp takes 256 consecutive columns (a chunk) at a time, a lane 8 of them, held as fp32.
+//
+// Which 8 depends on how the rows lie in memory (MAP):
+//   kMap8  rows that begin on 16 bytes, 16-bit numbers: columns 8 lane .. 8 lane + 7, one 16-byte access
+//   kMap4  the same for fp32: columns 4 lane .. + 3 and 128 + 4 lane .. + 3, so that both accesses are whole lines
+//   kMap1  rows that begin anywhere: columns lane + 32 i, one number an access. A warp's access is then 64 or 128
+//          consecutive bytes; with 8 consecutive numbers a lane it would be 32 pieces of four lines.
+// Every chunk is 256 columns in all of them, so a lane's columns are the same in every row, and the blocks of 128 columns
+// that share an 8-bit scale are half a chunk.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace moe {
+namespace rows {
+
+constexpr int kMap8 = 0, kMap4 = 1, kMap1 = 2;
+constexpr int kChunk = 256;
+
+template <int TYPE>
+constexpr int kSize = TYPE == MOE_TYPE_F32 ? 4 : 2;
+
+// Column of a lane's i-th number within the chunk.
+template <int MAP>
+__device__ __forceinline__ int column(int lane, int i) {
+  return MAP == kMap8 ? 8 * lane + i : MAP == kMap4 ? 128 * (i / 4) + 4 * lane + i % 4 : 32 * i + lane;
+}
+
+template <int TYPE>
+__device__ __forceinline__ float value(uint32_t bits) {
+  if (TYPE == MOE_TYPE_F32) return __uint_as_float(bits);
+  if (TYPE == MOE_TYPE_BF16) return __uint_as_float(bits << 16);
+  return __half2float(__ushort_as_half((unsigned short)bits));
+}
+template <int TYPE>
+__device__ __forceinline__ uint32_t bits_of(float v) {  // rounded to nearest even
+  if (TYPE == MOE_TYPE_F32) return __float_as_uint(v);
+  if (TYPE == MOE_TYPE_BF16) return __bfloat16_as_ushort(__float2bfloat16_rn(v));
+  return __half_as_ushort(__float2half_rn(v));
+}
+template <int TYPE>
+__device__ __forceinline__ uint32_t load_bits(const void* p, int64_t at) {
+  if (TYPE == MOE_TYPE_F32) return static_cast<const uint32_t*>(p)[at];
+  return static_cast<const uint16_t*>(p)[at];
+}
+template <int TYPE>
+__device__ __forceinline__ void store_bits(void* p, int64_t at, uint32_t v) {
+  if (TYPE == MOE_TYPE_F32)
+    static_cast<uint32_t*>(p)[at] = v;
+  else
+    static_cast<uint16_t*>(p)[at] = (uint16_t)v;
+}
+
+template <int TYPE>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if (TYPE == MOE_TYPE_BF16) return pack_bf16x2(lo, hi);
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <int TYPE>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if (TYPE == MOE_TYPE_BF16) return make_float2(bf16_lo(w), bf16_hi(w));
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+// A lane's 8 numbers of a chunk as they lie in memory: nothing is done with them until values(), so the loads of several
+// chunks and tensors are in flight together. c0: first column of the chunk; columns at and past cols are 0.
+template <int TYPE, int MAP>
+struct Chunk {
+  static constexpr bool kWide = TYPE == MOE_TYPE_F32;
+  uint32_t w[MAP == kMap1 || kWide ? 8 : 4];
+
+  __device__ __forceinline__ void load(const void* row, int c0, int cols, int lane) {
+    if constexpr (MAP == kMap1) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int c = c0 + column<MAP>(lane, i);
+        w[i] = c < cols ? load_bits<TYPE>(row, c) : 0u;
+      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < (kWide ? 2 : 1); ++h) {
+        const int c = c0 + column<MAP>(lane, 4 * h);
+        constexpr int kN = kWide ? 4 : 8;
+        if (c + kN <= cols) {
+          const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const char*>(row) + (int64_t)c * kSize<TYPE>);
+          w[4 * h] = v.x, w[4 * h + 1] = v.y, w[4 * h + 2] = v.z, w[4 * h + 3] = v.w;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if constexpr (kWide)
+              w[4 * h + i] = c + i < cols ? load_bits<TYPE>(row, c + i) : 0u;
+            else
+              w[i] = (c + 2 * i < cols ? load_bits<TYPE>(row, c + 2 * i) : 0u) |
+                     (c + 2 * i + 1 < cols ? load_bits<TYPE>(row, c + 2 * i + 1) << 16 : 0u);
+          }
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < (MAP == kMap1 || kWide ? 8 : 4); ++i) w[i] = 0u;
+  }
+  __device__ __forceinline__ void values(float (&f)[8]) const {
+    if constexpr (MAP == kMap1 || kWide) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = value<TYPE>(w[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 v = unpack2<TYPE>(w[i]);
+        f[2 * i] = v.x, f[2 * i + 1] = v.y;
+      }
+    }
+  }
+};
+
+// A lane's 8 numbers to a row, each rounded once; columns at and past cols are left alone.
+template <int TYPE, int MAP>
+__device__ __forceinline__ void store(void* row, int c0, int cols, int lane, const float (&f)[8]) {
+  constexpr bool kWide = TYPE == MOE_TYPE_F32;
+  if constexpr (MAP == kMap1) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = c0 + column<MAP>(lane, i);
+      if (c < cols) store_bits<TYPE>(row, c, bits_of<TYPE>(f[i]));
+    }
+  } else {
+#pragma unroll
+    for (int h = 0; h < (kWide ? 2 : 1); ++h) {
+      const int c = c0 + column<MAP>(lane, 4 * h);
+      constexpr int kN = kWide ? 4 : 8;
+      if (c + kN <= cols) {
+        uint4 v;
+        if constexpr (kWide)
+          v = make_uint4(__float_as_uint(f[4 * h]), __float_as_uint(f[4 * h + 1]), __float_as_uint(f[4 * h + 2]),
+                         __float_as_uint(f[4 * h + 3]));
+        else
+          v = make_uint4(pack2<TYPE>(f[0], f[1]), pack2<TYPE>(f[2], f[3]), pack2<TYPE>(f[4], f[5]), pack2<TYPE>(f[6], f[7]));
+        *reinterpret_cast<uint4*>(static_cast<char*>(row) + (int64_t)c * kSize<TYPE>) = v;
+      } else {
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+          if (c + i < cols) store_bits<TYPE>(row, c + i, bits_of<TYPE>(f[4 * h + i]));
+      }
+    }
+  }
+}
+
+// Whether rows of this type that lie ld numbers apart all begin on 16 bytes (the base does).
+inline bool aligned_rows(int type, int64_t ld, int64_t rows) { return rows <= 1 || ld % (type == MOE_TYPE_F32 ? 4 : 8) == 0; }
+inline int map_of(int type, bool aligned) { return !aligned ? kMap1 : type == MOE_TYPE_F32 ? kMap4 : kMap8; }
+
+}  // namespace rows
+}  // namespace moe

@@ -106,6 +106,16 @@ def load():
                 "moe_balance_loss_workspace_size": [cfgp, i32, ctypes.POINTER(sz)],
                 "moe_balance_loss": [cfgp, vp, i32, vp, vp, i32, vp, ctypes.c_float, vp, vp, vp, vp, vp, sz, vp],
                 "moe_balance_loss_backward": [cfgp, vp, i32, vp, vp, vp, i32, vp, ctypes.c_float, vp, vp, vp],
+                "moe_rms_norm": [vp, i32, i64, i64, i64, vp, i32, i64, vp, i32, ctypes.c_float, vp, vp, vp, vp, vp],
+                "moe_rms_norm_backward_workspace_size": [i64, i64, ctypes.POINTER(sz)],
+                "moe_rms_norm_backward": [vp, i32, i64, i64, vp, i32, i64, vp, vp, i32, ctypes.c_float, vp, vp, vp, vp, sz,
+                                          vp],
+                "moe_sort_tokens_workspace_size": [cfgp, ctypes.POINTER(sz)],
+                "moe_sort_tokens": [cfgp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
+                "moe_permute": [cfgp, vp, i32, i64, i64, vp, vp, vp, vp, vp, vp],
+                "moe_unpermute": [cfgp, vp, i32, i64, vp, vp, vp, vp, vp],
+                "moe_unpermute_backward": [cfgp, vp, vp, i32, i64, vp, vp, vp, vp, vp, vp],
+                "moe_route_backward": [cfgp, vp, i32, vp, vp, vp, vp],
             }
             for name, args in sig.items():
                 f = getattr(L, name)
@@ -546,6 +556,373 @@ def balance_loss_backward(cfg, logits, counts, tokens, alpha: float, dloss, seq_
     _check((_lib or load()).moe_balance_loss_backward(ctypes.byref(cfg), logits.data_ptr(), kind, counts.data_ptr(),
                                                       tokens.data_ptr(), offsets, S, mask, alpha, dloss.data_ptr(),
                                                       dlogits.data_ptr(), _raw_stream(_current_device())))
+    return dlogits
+
+
+# ------------------------------------------------------------------------------------------
+# around the experts: the norm in front, rows sorted by expert and back, and the gradients
+# ------------------------------------------------------------------------------------------
+def _here(*tensors):
+    """Raw handle of the current stream; the tensors have to be on its device."""
+    dev = _current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"a tensor is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+    return _raw_stream(dev)
+
+
+def _gradient(t):
+    """A gradient that autograd hands over, as the library reads it: contiguous, on 16 bytes."""
+    if t.is_contiguous() and t.data_ptr() % 16 == 0:
+        return t
+    return t.clone(memory_format=torch.contiguous_format)
+
+
+def _wants_gradient(*tensors):
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
+def _row_matrix(t, name, dtypes, shape=(None, None)):
+    """(rows, cols, elements from row to row) of a matrix whose rows may be strided."""
+    if not (isinstance(t, torch.Tensor) and t.dim() == 2 and t.is_cuda and t.dtype in dtypes
+            and (shape[0] is None or t.shape == shape)):
+        _need(t, name, tuple(dtypes), shape, contiguous=False)
+    rows, cols = t.shape
+    ld, one = t.stride()
+    if one != 1 and cols > 1:
+        raise ValueError(f"the elements of a row of {name} must be contiguous")
+    return rows, cols, ld if rows > 1 else cols
+
+
+def _norm_weight(weight, dtype, cols):
+    """(address, type) of the norm's weight."""
+    if weight is None:
+        return None, ELEMENT_TYPES[dtype]
+    if not (_like(weight, dtype, (cols,)) or _like(weight, _f32, (cols,))):
+        _need(weight, "weight", (dtype, _f32), (cols,))
+    return weight.data_ptr(), ELEMENT_TYPES[weight.dtype]
+
+
+def _rms_norm(x, weight, residual, eps, fp8, with_y):
+    """(y, total, q, s), None where not wanted."""
+    rows, cols, ldx = _row_matrix(x, "x", ELEMENT_TYPES)
+    dtype = x.dtype
+    w, w_type = _norm_weight(weight, dtype, cols)
+    y = total = q = s = None
+    r = r_type = ldr = 0
+    if residual is not None:
+        _, _, ldr = _row_matrix(residual, "residual", (dtype, _f32), (rows, cols))
+        r, r_type = residual.data_ptr(), ELEMENT_TYPES[residual.dtype]
+        total = torch.empty(rows, cols, dtype=residual.dtype, device=x.device)
+    if with_y:
+        y = torch.empty(rows, cols, dtype=dtype, device=x.device)
+    if fp8:
+        q = torch.empty(rows, cols, dtype=_u8, device=x.device)
+        s = torch.empty(rows, (cols + 127) // 128, dtype=_f32, device=x.device)
+    _check((_lib or load()).moe_rms_norm(x.data_ptr(), ELEMENT_TYPES[dtype], rows, cols, ldx, r or None, r_type, ldr, w,
+                                         w_type, eps, _address(y), _address(total), _address(q), _address(s),
+                                         _here(x, weight, residual)))
+    return y, total, q, s
+
+
+class _RmsNorm(torch.autograd.Function):
+    """The norm as a node of autograd, whose gradient is moe_rms_norm_backward."""
+
+    @staticmethod
+    def forward(ctx, x, weight, residual, eps, fp8, with_y):
+        y, total, q, s = _rms_norm(x, weight, residual, eps, fp8, with_y)
+        ctx.set_materialize_grads(False)
+        ctx.mark_non_differentiable(*(t for t in (q, s) if t is not None))
+        ctx.save_for_backward(x if total is None else total, weight)
+        ctx.eps, ctx.types = eps, (x.dtype, None if residual is None else residual.dtype)
+        return y, total, q, s
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy, dtotal, *_):
+        total, weight = ctx.saved_tensors
+        kind, other = ctx.types
+        if dy is None:  # only the total was used: it is the sum
+            return (None if dtotal is None else dtotal.to(kind), None, dtotal, None, None, None)
+        dx, dresidual, dweight = rms_norm_backward(_gradient(dy), total, weight, ctx.eps,
+                                                   None if dtotal is None else _gradient(dtotal),
+                                                   weight_gradient=ctx.needs_input_grad[1])
+        return dx, dweight, None if other is None else dresidual, None, None, None
+
+
+def rms_norm(x, weight=None, residual=None, eps: float = 1e-6):
+    """Root-mean-square norm (moe_rms_norm in include/moe.h) of x [rows, cols] (fp32, bf16 or fp16; the rows may be
+    strided), or of x + residual (of x's type or fp32), times weight [cols] (x's type or fp32; None: ones): y of x's type,
+    and with a residual (y, total), total = x + residual of the residual's type.
+
+    Differentiable once with respect to x, residual and weight. (As for any operation: a backward pass that is captured
+    into a CUDA graph must not share leaves with an eager graph that is still alive.)"""
+    run = _RmsNorm.apply if _wants_gradient(x, weight, residual) else _rms_norm
+    y, total, _, _ = run(x, weight, residual, eps, False, True)
+    return y if residual is None else (y, total)
+
+
+def rms_norm_fp8(x, weight=None, residual=None, eps: float = 1e-6, with_y: bool = False) -> dict:
+    """rms_norm with an output in 8 bits: q uint8 [rows, cols] (e4m3 codes) and s fp32 [rows, ceil(cols / 128)], the rows of
+    an FP8 layer; total with a residual, and y of x's type with_y (for a router). y and total are differentiable, codes and
+    scales are not."""
+    run = _RmsNorm.apply if _wants_gradient(x, weight, residual) else _rms_norm
+    out = dict(zip(("y", "total", "q", "s"), run(x, weight, residual, eps, True, with_y)))
+    return {name: t for name, t in out.items() if t is not None}
+
+
+def rms_norm_backward(dy, total, weight=None, eps: float = 1e-6, dtotal=None, weight_gradient: bool = True, ws=None):
+    """Gradient of rms_norm (moe_rms_norm_backward): (dx of dy's type, dresidual of total's type, dweight of weight's type or
+    None) from dy, the total that was normalised (x without a residual) and the gradient dtotal that reaches the total
+    from elsewhere. dresidual is dx itself where the types are the same. ws: rms_norm_backward_workspace."""
+    rows, cols = dy.shape if isinstance(dy, torch.Tensor) and dy.dim() == 2 else (None, None)
+    if rows is None or dy.dtype not in ELEMENT_TYPES or not _like(dy, dy.dtype, (rows, cols)):
+        _need(dy, "dy", tuple(ELEMENT_TYPES), (None, None))
+    kind = dy.dtype
+    _, _, ldt = _row_matrix(total, "total", (kind, _f32), (rows, cols))
+    if dtotal is not None and not _like(dtotal, total.dtype, (rows, cols)):
+        _need(dtotal, "dtotal", total.dtype, (rows, cols))
+    w, w_type = _norm_weight(weight, kind, cols)
+    dx = torch.empty_like(dy)
+    dresidual, dweight = dx, None
+    if total.dtype is not kind:
+        dresidual = torch.empty(rows, cols, dtype=total.dtype, device=dy.device)
+    if weight is not None and weight_gradient:
+        dweight = torch.empty_like(weight)
+        if ws is None:
+            ws = rms_norm_backward_workspace(rows, cols, dy.device)
+        elif not _like(ws, _u8, (ws.numel(),)):
+            _need(ws, "ws", _u8, (None,))
+    _check((_lib or load()).moe_rms_norm_backward(
+        dy.data_ptr(), ELEMENT_TYPES[kind], rows, cols, total.data_ptr(), ELEMENT_TYPES[total.dtype], ldt,
+        _address(dtotal), w, w_type, eps, dx.data_ptr(), None if dresidual is dx else dresidual.data_ptr(),
+        _address(dweight), _address(ws), 0 if ws is None else ws.numel(), _here(dy, total, dtotal, weight, ws)))
+    return dx, dresidual, dweight
+
+
+def rms_norm_backward_workspace(rows: int, cols: int, device="cuda") -> torch.Tensor:
+    n = ctypes.c_size_t()
+    _check((_lib or load()).moe_rms_norm_backward_workspace_size(rows, cols, ctypes.byref(n)))
+    return torch.empty(n.value, dtype=_u8, device=device)
+
+
+def sort_tokens_workspace(cfg: MoeConfig, device="cuda") -> torch.Tensor:
+    n = ctypes.c_size_t()
+    _check((_lib or load()).moe_sort_tokens_workspace_size(ctypes.byref(cfg), ctypes.byref(n)))
+    return torch.empty(n.value, dtype=_u8, device=device)
+
+
+def _groups(cfg):
+    return cfg.placement.contents.n_slots if cfg.placement else cfg.E
+
+
+def sort_tokens(cfg, topk_idx, topk_w=None, ws=None) -> dict:
+    """The assignments of topk_idx int32 [T, k] sorted by expert (moe_sort_tokens): counts, offsets, inv_pos [T, k], row_token
+    [T k], and row_weight [T k] with topk_w fp32 [T, k]. Entries outside [0, E) are no assignment. ws:
+    sort_tokens_workspace."""
+    T, k = cfg.T, cfg.k
+    if not _like(topk_idx, _i32, (T, k)):
+        _need(topk_idx, "topk_idx", _i32, (T, k))
+    if topk_w is not None and not _like(topk_w, _f32, (T, k)):
+        _need(topk_w, "topk_w", _f32, (T, k))
+    dev, n = topk_idx.device, _groups(cfg)
+    if ws is None:
+        ws = sort_tokens_workspace(cfg, dev)
+    elif not _like(ws, _u8, (ws.numel(),)):
+        _need(ws, "ws", _u8, (None,))
+    out = {"counts": torch.empty(n, dtype=_i32, device=dev), "offsets": torch.empty(n + 1, dtype=_i32, device=dev),
+           "inv_pos": torch.empty(T, k, dtype=_i32, device=dev), "row_token": torch.empty(T * k, dtype=_i32, device=dev)}
+    if topk_w is not None:
+        out["row_weight"] = torch.empty(T * k, dtype=_f32, device=dev)
+    _check((_lib or load()).moe_sort_tokens(
+        ctypes.byref(cfg), topk_idx.data_ptr(), _address(topk_w), out["counts"].data_ptr(), out["offsets"].data_ptr(),
+        out["inv_pos"].data_ptr(), out["row_token"].data_ptr(), _address(out.get("row_weight")), ws.data_ptr(),
+        ws.numel(), _here(topk_idx, topk_w, ws)))
+    return out
+
+
+def _positions(cfg, inv_pos, offsets=None):
+    if not _like(inv_pos, _i32, (cfg.T, cfg.k)):
+        _need(inv_pos, "inv_pos", _i32, (cfg.T, cfg.k))
+    if offsets is not None and not _like(offsets, _i32, (_groups(cfg) + 1,)):
+        _need(offsets, "offsets", _i32, (_groups(cfg) + 1,))
+
+
+def _route_weights_of(cfg, weights):
+    """Address of the route weights, or None."""
+    if weights is None:
+        return None
+    if not _like(weights, _f32, (cfg.T, cfg.k)):
+        _need(weights, "weights", _f32, (cfg.T, cfg.k))
+    return weights.data_ptr()
+
+
+def _permute(x, cfg, inv_pos, offsets, scales):
+    _positions(cfg, inv_pos, offsets)
+    _, cols, ldx = _row_matrix(x, "x", tuple(ELEMENT_TYPES) if scales is None else (_u8,), (cfg.T, x.shape[-1]))
+    xd = torch.empty(cfg.T * cfg.k, cols, dtype=x.dtype, device=x.device)
+    xd_scales = None
+    if scales is not None:
+        n = (cols + 127) // 128
+        if not _like(scales, _f32, (cfg.T, n)):
+            _need(scales, "scales", _f32, (cfg.T, n))
+        xd_scales = torch.empty(cfg.T * cfg.k, n, dtype=_f32, device=x.device)
+    _check((_lib or load()).moe_permute(ctypes.byref(cfg), x.data_ptr(), x.element_size(), cols, ldx, _address(scales),
+                                        inv_pos.data_ptr(), offsets.data_ptr(), xd.data_ptr(), _address(xd_scales),
+                                        _here(x, scales, inv_pos, offsets)))
+    return xd if scales is None else (xd, xd_scales)
+
+
+class _Permute(torch.autograd.Function):
+    """Rows sorted by expert as a node of autograd, whose gradient is moe_unpermute without weights."""
+
+    @staticmethod
+    def forward(ctx, x, cfg, inv_pos, offsets):
+        ctx.cfg = cfg
+        ctx.save_for_backward(inv_pos)
+        return _permute(x, cfg, inv_pos, offsets, None)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dxd):
+        return _unpermute(_gradient(dxd), None, None, ctx.cfg, ctx.saved_tensors[0]), None, None, None
+
+
+def permute(cfg, x, inv_pos, offsets, scales=None):
+    """Rows of x [T, cols] (fp32, bf16 or fp16; the rows may be strided) into expert order (moe_permute): xd [T k, cols], with
+    inv_pos and offsets of sort_tokens. Rows past the last one held are zero. With scales fp32 [T, ceil(cols / 128)], x
+    holds e4m3 codes (uint8) and (xd, xd_scales) are returned. Differentiable once with respect to x (not 8-bit)."""
+    if scales is None and _wants_gradient(x):
+        return _Permute.apply(x, cfg, inv_pos, offsets)
+    return _permute(x, cfg, inv_pos, offsets, scales)
+
+
+def _expert_rows(cfg, yd):
+    """Columns of the expert-major rows."""
+    if not (isinstance(yd, torch.Tensor) and yd.dim() == 2 and yd.dtype in ELEMENT_TYPES
+            and _like(yd, yd.dtype, (cfg.T * cfg.k, yd.shape[1]))):
+        _need(yd, "yd", tuple(ELEMENT_TYPES), (cfg.T * cfg.k, None))
+    return yd.shape[1]
+
+
+def _unpermute(yd, weights, base, cfg, inv_pos):
+    _positions(cfg, inv_pos)
+    cols = _expert_rows(cfg, yd)
+    w = _route_weights_of(cfg, weights)
+    if base is not None and not _like(base, yd.dtype, (cfg.T, cols)):
+        _need(base, "base", yd.dtype, (cfg.T, cols))
+    y = torch.empty(cfg.T, cols, dtype=yd.dtype, device=yd.device)
+    _check((_lib or load()).moe_unpermute(ctypes.byref(cfg), yd.data_ptr(), ELEMENT_TYPES[yd.dtype], cols,
+                                          inv_pos.data_ptr(), w, _address(base), y.data_ptr(),
+                                          _here(yd, inv_pos, weights, base)))
+    return y
+
+
+class _Unpermute(torch.autograd.Function):
+    """Rows back in token order as a node of autograd, whose gradient is moe_unpermute_backward."""
+
+    @staticmethod
+    def forward(ctx, yd, weights, base, cfg, inv_pos, offsets):
+        ctx.cfg = cfg
+        ctx.save_for_backward(yd if weights is not None and weights.requires_grad else None, weights, inv_pos, offsets)
+        return _unpermute(yd, weights, base, cfg, inv_pos)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        yd, weights, inv_pos, offsets = ctx.saved_tensors
+        dyd = dw = None
+        if ctx.needs_input_grad[0] or ctx.needs_input_grad[1]:
+            dyd, dw = unpermute_backward(ctx.cfg, _gradient(dy), yd, inv_pos, offsets, weights)
+        return dyd, dw, dy if ctx.needs_input_grad[2] else None, None, None, None
+
+
+def unpermute(cfg, yd, inv_pos, weights=None, base=None, offsets=None):
+    """Rows yd [T k, cols] (fp32, bf16 or fp16) back in token order, added up (moe_unpermute): y[t] = base[t] + sum over the
+    slots of weights[t, j] yd[inv_pos[t, j]]; weights fp32 [T, k] (None: ones), base [T, cols] of yd's type or None.
+    Differentiable once with respect to yd, weights and base; that takes the offsets of sort_tokens too."""
+    if _wants_gradient(yd, weights, base):
+        if offsets is None:
+            raise ValueError("the gradient of unpermute needs offsets")
+        _positions(cfg, inv_pos, offsets)
+        return _Unpermute.apply(yd, weights, base, cfg, inv_pos, offsets)
+    return _unpermute(yd, weights, base, cfg, inv_pos)
+
+
+def unpermute_backward(cfg, dy, yd, inv_pos, offsets, weights=None):
+    """Gradient of unpermute (moe_unpermute_backward): (dyd [T k, cols] of dy's type, zero in the rows past the last one held;
+    dweights fp32 [T, k], None where yd is None) from dy [T, cols]."""
+    _positions(cfg, inv_pos, offsets)
+    if not (isinstance(dy, torch.Tensor) and dy.dim() == 2 and dy.dtype in ELEMENT_TYPES
+            and _like(dy, dy.dtype, (cfg.T, dy.shape[1]))):
+        _need(dy, "dy", tuple(ELEMENT_TYPES), (cfg.T, None))
+    cols, kind = dy.shape[1], dy.dtype
+    if yd is not None and not _like(yd, kind, (cfg.T * cfg.k, cols)):
+        _need(yd, "yd", kind, (cfg.T * cfg.k, cols))
+    w = _route_weights_of(cfg, weights)
+    dyd = torch.empty(cfg.T * cfg.k, cols, dtype=kind, device=dy.device)
+    dw = None if yd is None else torch.empty(cfg.T, cfg.k, dtype=_f32, device=dy.device)
+    _check((_lib or load()).moe_unpermute_backward(ctypes.byref(cfg), dy.data_ptr(), _address(yd), ELEMENT_TYPES[kind], cols,
+                                                   inv_pos.data_ptr(), offsets.data_ptr(), w, dyd.data_ptr(),
+                                                   _address(dw), _here(dy, yd, inv_pos, offsets, weights)))
+    return dyd, dw
+
+
+def _route_weights(logits, cfg, bias):
+    """(topk_idx, topk_w)."""
+    if not _like(logits, _f32, (cfg.T, cfg.E)):
+        _need(logits, "logits", _f32, (cfg.T, cfg.E))
+    if bias is not None and not _like(bias, _f32, (cfg.E,)):
+        _need(bias, "bias", _f32, (cfg.E,))
+    idx = torch.empty(cfg.T, cfg.k, dtype=_i32, device=logits.device)
+    w = torch.empty(cfg.T, cfg.k, dtype=_f32, device=logits.device)
+    struct = MoeWeightsStruct(bias=_address(bias))
+    _check((_lib or load()).moe_route(ctypes.byref(cfg), None, ctypes.byref(struct), logits.data_ptr(), MOE_LOGITS_GIVEN,
+                                      idx.data_ptr(), w.data_ptr(), None, 0, _here(logits, bias)))
+    return idx, w
+
+
+class _RouteWeights(torch.autograd.Function):
+    """The route weights as a node of autograd, whose gradient is moe_route_backward."""
+
+    @staticmethod
+    def forward(ctx, logits, cfg, bias):
+        idx, w = _route_weights(logits, cfg, bias)
+        ctx.cfg = cfg
+        ctx.mark_non_differentiable(idx)
+        ctx.save_for_backward(logits, idx)
+        return idx, w
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, _, dw):
+        logits, idx = ctx.saved_tensors
+        return route_backward(ctx.cfg, logits, idx, _gradient(dw)), None, None
+
+
+def route_weights(cfg, logits, bias=None):
+    """(topk_idx int32 [T, k], topk_w fp32 [T, k]) of the router's logits fp32 [T, E] (moe_route with the logits given; bias
+    fp32 [E], sigmoid scoring only). The weights are differentiable once with respect to the logits, by route_backward; the
+    selection and its bias carry no gradient."""
+    run = _RouteWeights.apply if _wants_gradient(logits) else _route_weights
+    return run(logits, cfg, bias)
+
+
+def route_backward(cfg, logits, topk_idx, dtopk_w, dlogits=None) -> torch.Tensor:
+    """Gradient of the route weights with respect to the logits [T, E] (fp32 or bf16), of their dtype
+    (moe_route_backward), from the chosen experts topk_idx int32 [T, k] and the weights' gradient dtopk_w fp32 [T, k]."""
+    if not (_like(logits, _f32, (cfg.T, cfg.E)) or _like(logits, torch.bfloat16, (cfg.T, cfg.E))):
+        _need(logits, "logits", (_f32, torch.bfloat16), (cfg.T, cfg.E))
+    if not (_like(topk_idx, _i32, (cfg.T, cfg.k)) and _like(dtopk_w, _f32, (cfg.T, cfg.k))):
+        _need(topk_idx, "topk_idx", _i32, (cfg.T, cfg.k))
+        _need(dtopk_w, "dtopk_w", _f32, (cfg.T, cfg.k))
+    if dlogits is None:
+        dlogits = torch.empty_like(logits)
+    elif not _like(dlogits, logits.dtype, (cfg.T, cfg.E)):
+        _need(dlogits, "dlogits", logits.dtype, (cfg.T, cfg.E))
+    _check((_lib or load()).moe_route_backward(ctypes.byref(cfg), logits.data_ptr(), ELEMENT_TYPES[logits.dtype],
+                                               topk_idx.data_ptr(), dtopk_w.data_ptr(), dlogits.data_ptr(),
+                                               _here(logits, topk_idx, dtopk_w, dlogits)))
     return dlogits
 
 
