@@ -48,6 +48,7 @@ __global__ void __launch_bounds__(kThreads) count_kernel(const SortArgs a) {
   extern __shared__ int32_t hist[];
   for (int e = threadIdx.x; e < a.E; e += kThreads) hist[e] = 0;
   __syncthreads();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t lo = blockIdx.x * a.per_block, hi = min(a.n, lo + a.per_block);
   for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) {
     const int e = a.idx[i];
@@ -79,8 +80,9 @@ __device__ __forceinline__ int block_prefix(int v, int* warp_sums, int& total) {
   return before + incl - v;
 }
 
-// Shared memory: per warp a count of each expert [kWarps][E]; of the assignments before this block [E]; of all, and then the
-// kept ones [E]; the offset of each group [max(E, n_slots) + 1].
+// Shared memory: per warp a count of each expert, then the ranks before the warp's [kWarps][E]; for each expert the ranks
+// before this round's [E] and the assignments in all [E]; the offset of each group [max(E, n_slots)].
+constexpr int kEach = 4;  // assignments of a lane in a round
 __global__ void __launch_bounds__(kThreads) rank_kernel(const SortArgs a) {
   extern __shared__ int32_t sh[];
   __shared__ int warp_sums[kWarps];
@@ -89,65 +91,23 @@ __global__ void __launch_bounds__(kThreads) rank_kernel(const SortArgs a) {
   int32_t* base = cnt + kWarps * E;
   int32_t* all = base + E;
   int32_t* offset = all + E;
-  for (int e = threadIdx.x; e < kWarps * E + 2 * E; e += kThreads) sh[e] = 0;
-  __syncthreads();
-  const bool single = a.blocks == 1;
   const int64_t lo = blockIdx.x * a.per_block, hi = min(a.n, lo + a.per_block);
-  if (single) {
-    for (int64_t i = threadIdx.x; i < a.n; i += kThreads) {
-      const int e = a.idx[i];
-      if (e >= 0 && e < E) atomicAdd(&all[e], 1);
-    }
-  } else {
-    const int mine = (int)blockIdx.x * E, every = a.blocks * E;
-    for (int i = threadIdx.x; i < every; i += kThreads) {
-      const int c = a.hist[i], e = i % E;
-      if (c) {
-        atomicAdd(&all[e], c);
-        if (i < mine) atomicAdd(&base[e], c);
-      }
-    }
-  }
-  __syncthreads();
-  const int groups = a.n_slots ? a.n_slots : E;
-  int run = 0;
-  for (int g0 = 0; g0 < groups; g0 += kThreads) {
-    const int g = g0 + threadIdx.x;
-    int c = 0;
-    if (g < groups) {
-      if (a.n_slots) {  // rows of replica i of an expert with r of them: ranks i, i + r, .. below what it keeps
-        const int e = a.slot_expert[g], i = a.slot_replica[g], r = a.replicas[e], kept = min(all[e], a.cap);
-        c = kept > i ? (kept - i + r - 1) / r : 0;
-      } else {
-        c = min(all[g], a.cap);
-      }
-    }
-    int total;
-    const int at = run + block_prefix(c, warp_sums, total);
-    if (g < groups) {
-      offset[g] = at;
-      if (blockIdx.x == 0) {
-        a.counts[g] = c;
-        a.offsets[g] = at;
-      }
-    }
-    run += total;
-  }
-  const int held = run;  // rows
-  if (blockIdx.x == 0 && threadIdx.x == 0) a.offsets[groups] = held;
-  __syncthreads();
-  for (int64_t c0 = lo; c0 < hi; c0 += 4 * kThreads) {  // 128 assignments a warp at a time
-    int e4[4], rank[4];
-    const int64_t at = c0 + warp * 128 + lane;
+  int held = 0;
+  for (int64_t c0 = lo; c0 < hi; c0 += kEach * kThreads) {
+    const int64_t at = c0 + warp * 32 * kEach + lane;
+    int mine[kEach], rank[kEach];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < kEach; ++j) {
       const int64_t i = at + 32 * j;
       const int e = i < hi ? a.idx[i] : -1;
-      e4[j] = e >= 0 && e < E ? e : -1;
+      mine[j] = e >= 0 && e < E ? e : -1;
     }
+    if (c0 > lo) __syncthreads();
+    for (int e = threadIdx.x; e < kWarps * E; e += kThreads) cnt[e] = 0;
+    __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int e = e4[j];
+    for (int j = 0; j < kEach; ++j) {  // the first lane of an expert counts for all of its lanes
+      const int e = mine[j];
       const uint32_t peers = __match_any_sync(0xffffffffu, e), before = peers & ((1u << lane) - 1u);
       int32_t* c = cnt + warp * E + max(e, 0);
       const int had = *c;
@@ -156,22 +116,70 @@ __global__ void __launch_bounds__(kThreads) rank_kernel(const SortArgs a) {
       __syncwarp();
       rank[j] = had + __popc(before);
     }
+    if (c0 == lo && a.blocks > 1) {  // the other blocks' counts: kThreads / E of them at a time, or one
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      for (int e = threadIdx.x; e < 2 * E; e += kThreads) base[e] = 0;
+      __syncthreads();
+      const int side = max(1, kThreads / E);
+      for (int e = threadIdx.x % (side * E); e < side * E; e += kThreads) {
+        if (threadIdx.x >= side * E) break;
+        int total = 0, earlier = 0;
+        const int32_t* h = a.hist + e % E;
+#pragma unroll 8
+        for (int b = e / E; b < a.blocks; b += side) {
+          const int c = h[(int64_t)b * E];
+          total += c;
+          if (b < (int)blockIdx.x) earlier += c;
+        }
+        if (total) atomicAdd(&all[e % E], total);
+        if (earlier) atomicAdd(&base[e % E], earlier);
+      }
+    }
     __syncthreads();
-    for (int e = threadIdx.x; e < E; e += kThreads) {  // a warp's counts become those before it
-      int n = base[e];
+    for (int e = threadIdx.x; e < E; e += kThreads) {
+      int n = c0 == lo && a.blocks == 1 ? 0 : base[e];
+#pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const int c = cnt[w * E + e];
         cnt[w * E + e] = n;
         n += c;
       }
       base[e] = n;
+      if (a.blocks == 1) all[e] = n;  // of all once this is the last round, which it is: a batch of one block has one
+    }
+    if (c0 == lo) {
+      __syncthreads();
+      const int groups = a.n_slots ? a.n_slots : E;
+      for (int g0 = 0; g0 < groups; g0 += kThreads) {
+        const int g = g0 + threadIdx.x;
+        int c = 0;
+        if (g < groups) {
+          if (a.n_slots) {  // rows of replica i of an expert with r of them: ranks i, i + r, .. below what it keeps
+            const int e = a.slot_expert[g], i = a.slot_replica[g], r = a.replicas[e], kept = min(all[e], a.cap);
+            c = kept > i ? (kept - i + r - 1) / r : 0;
+          } else {
+            c = min(all[g], a.cap);
+          }
+        }
+        int total;
+        const int first = held + block_prefix(c, warp_sums, total);
+        if (g < groups) {
+          offset[g] = first;
+          if (blockIdx.x == 0) {
+            a.counts[g] = c;
+            a.offsets[g] = first;
+          }
+        }
+        held += total;
+      }
+      if (blockIdx.x == 0 && threadIdx.x == 0) a.offsets[groups] = held;
     }
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < kEach; ++j) {
       const int64_t i = at + 32 * j;
       if (i >= hi) continue;
-      const int e = e4[j];
+      const int e = mine[j];
       int row = -1;
       if (e >= 0) {
         const int r = rank[j] + cnt[warp * E + e];
@@ -187,11 +195,6 @@ __global__ void __launch_bounds__(kThreads) rank_kernel(const SortArgs a) {
         }
       }
       a.inv_pos[i] = row;
-    }
-    if (c0 + 4 * kThreads < hi) {
-      __syncthreads();
-      for (int e = threadIdx.x; e < kWarps * E; e += kThreads) cnt[e] = 0;
-      __syncthreads();
     }
   }
   for (int64_t r = max(lo, (int64_t)held) + threadIdx.x; r < hi; r += kThreads) {  // rows that hold nothing
@@ -261,6 +264,20 @@ __global__ void __launch_bounds__(256) permute_kernel(const CopyPlane p, const C
 // ------------------------------------------------------------------------------------------
 constexpr int kBatch = 8;  // rows of a token in flight
 
+// Rows and weights of a token's slots j0 .. j0 + 7 in every lane; -1 past the last slot.
+__device__ __forceinline__ void slots(const int32_t* inv_pos, const float* weights, int64_t t, int k, int j0,
+                                      int (&row)[kBatch], float (&w)[kBatch]) {
+  const int lane = threadIdx.x & 31;
+  const bool in = lane < kBatch && j0 + lane < k;
+  const int r = in ? inv_pos[t * k + j0 + lane] : -1;
+  const float v = in && weights ? weights[t * k + j0 + lane] : 1.f;
+#pragma unroll
+  for (int j = 0; j < kBatch; ++j) {
+    row[j] = __shfl_sync(0xffffffffu, r, j);
+    w[j] = __shfl_sync(0xffffffffu, v, j);
+  }
+}
+
 struct AddArgs {
   const void* yd;
   const void* base;      // or nullptr
@@ -269,43 +286,49 @@ struct AddArgs {
   void* y;
   int64_t T;
   int cols, chunks, k;
+  int piece, pieces;  // chunks of a warp's work, and those works of a row
 };
 
-// A warp a chunk of a token's row: fp32, the base first and then the slots in order.
+// A warp a piece of a token's row: fp32, the base first and then the slots in order. All rows of a chunk are loaded before any
+// is added.
 template <int TYPE, int MAP>
-__global__ void __launch_bounds__(256) unpermute_kernel(const AddArgs a) {
+__global__ void __launch_bounds__(256, TYPE != MOE_TYPE_F32 && MAP != rows::kMap1 ? 3 : 2) unpermute_kernel(const AddArgs a) {
   const int lane = threadIdx.x & 31;
-  const int64_t warps = ((int64_t)gridDim.x * blockDim.x) >> 5, items = a.T * a.chunks;
+  const int64_t warps = ((int64_t)gridDim.x * blockDim.x) >> 5, items = a.T * a.pieces;
+  const int64_t pitch = (int64_t)a.cols * rows::kSize<TYPE>;
   for (int64_t it = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; it < items; it += warps) {
-    const int64_t t = it / a.chunks;
-    const int c0 = (int)(it - t * a.chunks) * rows::kChunk;
-    const int mine = lane < a.k ? a.inv_pos[t * a.k + lane] : -1;
-    const float weight = a.weights && lane < a.k ? a.weights[t * a.k + lane] : 1.f;
-    const int64_t pitch = (int64_t)a.cols * rows::kSize<TYPE>;
-    float sum[8], f[8];
-    rows::Chunk<TYPE, MAP> b, v[kBatch];
-    if (a.base)
-      b.load(static_cast<const char*>(a.base) + t * pitch, c0, a.cols, lane);
-    else
-      b.clear();
-    for (int j0 = 0; j0 < a.k; j0 += kBatch) {
+    const int64_t t = it / a.pieces;
+    const int first = (int)(it - t * a.pieces) * a.piece, last = min(a.chunks, first + a.piece);
+    int row[kBatch];
+    float w[kBatch];
+    slots(a.inv_pos, a.weights, t, a.k, 0, row, w);
+    for (int c = first; c < last; ++c) {
+      const int c0 = c * rows::kChunk;
+      float sum[8];
+      for (int j0 = 0; j0 < a.k; j0 += kBatch) {
+        if (a.k > kBatch) slots(a.inv_pos, a.weights, t, a.k, j0, row, w);
+        rows::Chunk<TYPE, MAP> b, v[kBatch];
+        if (j0 == 0) {
+          if (a.base)
+            b.load(static_cast<const char*>(a.base) + t * pitch, c0, a.cols, lane);
+          else
+            b.clear();
+        }
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const int r = __shfl_sync(0xffffffffu, mine, min(j0 + j, 31));
-        if (j0 + j < a.k && r >= 0) v[j].load(static_cast<const char*>(a.yd) + r * pitch, c0, a.cols, lane);
+        for (int j = 0; j < kBatch; ++j)
+          if (row[j] >= 0) v[j].load(static_cast<const char*>(a.yd) + row[j] * pitch, c0, a.cols, lane);
+        if (j0 == 0) b.values(sum);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          if (row[j] < 0) continue;
+          float f[8];
+          v[j].values(f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sum[i] = fmaf(w[j], f[i], sum[i]);
+        }
       }
-      if (j0 == 0) b.values(sum);
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const int r = __shfl_sync(0xffffffffu, mine, min(j0 + j, 31));
-        const float w = __shfl_sync(0xffffffffu, weight, min(j0 + j, 31));
-        if (j0 + j >= a.k || r < 0) continue;
-        v[j].values(f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum[i] = fmaf(w, f[i], sum[i]);
-      }
+      rows::store<TYPE, MAP>(static_cast<char*>(a.y) + t * pitch, c0, a.cols, lane, sum);
     }
-    rows::store<TYPE, MAP>(static_cast<char*>(a.y) + t * pitch, c0, a.cols, lane, sum);
   }
 }
 
@@ -322,43 +345,42 @@ struct SpreadArgs {
 };
 
 // A block of W warps a token: its row of dy to its k rows of dyd, and their products with yd's rows, summed over the lanes
-// and then the warps. The blocks past the tokens clear the rows that hold nothing.
+// and then the warps. At the end the blocks clear the rows that hold nothing.
 template <int TYPE, int MAP>
-__global__ void __launch_bounds__(256) spread_kernel(const SpreadArgs a) {
+__global__ void __launch_bounds__(256, TYPE != MOE_TYPE_F32 && MAP != rows::kMap1 ? 3 : 2) spread_kernel(const SpreadArgs a) {
   __shared__ float part[8][kBatch];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
   const int64_t pitch = (int64_t)a.cols * rows::kSize<TYPE>;
-  float f[8], g[8];
+  float f[8];
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-    const int mine = lane < a.k ? a.inv_pos[t * a.k + lane] : -1;
-    const float weight = a.weights && lane < a.k ? a.weights[t * a.k + lane] : 1.f;
     for (int j0 = 0; j0 < a.k; j0 += kBatch) {
-      float dot[kBatch];
+      int row[kBatch];
+      float w[kBatch], dot[kBatch];
+      slots(a.inv_pos, a.weights, t, a.k, j0, row, w);
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) dot[j] = 0.f;
       for (int c = warp; c < a.chunks; c += W) {
         const int c0 = c * rows::kChunk;
         rows::Chunk<TYPE, MAP> dy, v[kBatch];
         dy.load(static_cast<const char*>(a.dy) + t * pitch, c0, a.cols, lane);
+        if (a.yd) {
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-          const int r = __shfl_sync(0xffffffffu, mine, min(j0 + j, 31));
-          if (a.yd && j0 + j < a.k && r >= 0) v[j].load(static_cast<const char*>(a.yd) + r * pitch, c0, a.cols, lane);
+          for (int j = 0; j < kBatch; ++j)
+            if (row[j] >= 0) v[j].load(static_cast<const char*>(a.yd) + row[j] * pitch, c0, a.cols, lane);
         }
+        float g[8];
         dy.values(g);
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
-          const int r = __shfl_sync(0xffffffffu, mine, min(j0 + j, 31));
-          const float w = __shfl_sync(0xffffffffu, weight, min(j0 + j, 31));
-          if (j0 + j >= a.k || r < 0) continue;
+          if (row[j] < 0) continue;
           if (a.yd) {
             v[j].values(f);
 #pragma unroll
             for (int i = 0; i < 8; ++i) dot[j] = fmaf(g[i], f[i], dot[j]);
           }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) f[i] = w * g[i];
-          rows::store<TYPE, MAP>(static_cast<char*>(a.dyd) + r * pitch, c0, a.cols, lane, f);
+          for (int i = 0; i < 8; ++i) f[i] = w[j] * g[i];
+          rows::store<TYPE, MAP>(static_cast<char*>(a.dyd) + row[j] * pitch, c0, a.cols, lane, f);
         }
       }
       if (!a.dweights) continue;
@@ -371,7 +393,7 @@ __global__ void __launch_bounds__(256) spread_kernel(const SpreadArgs a) {
       __syncthreads();
       if (threadIdx.x < kBatch && j0 + threadIdx.x < a.k) {
         float sum = 0.f;
-        for (int w = 0; w < W; ++w) sum += part[w][threadIdx.x];
+        for (int i = 0; i < W; ++i) sum += part[i][threadIdx.x];
         a.dweights[t * a.k + j0 + threadIdx.x] = sum;
       }
       __syncthreads();
@@ -396,7 +418,7 @@ cudaError_t with_word(int64_t bytes, int64_t ld, F&& f) {
 
 template <class F>
 cudaError_t with_rows(int type, int64_t cols, F&& f) {
-  const bool aligned = rows::aligned_rows(type, cols, 2);
+  const bool aligned = rows::whole(type, cols);
   using std::integral_constant;
   if (type == MOE_TYPE_F32)
     return aligned ? f(integral_constant<int, MOE_TYPE_F32>{}, integral_constant<int, rows::kMap4>{})
@@ -408,7 +430,7 @@ cudaError_t with_rows(int type, int64_t cols, F&& f) {
                  : f(integral_constant<int, MOE_TYPE_F16>{}, integral_constant<int, rows::kMap1>{});
 }
 
-constexpr int64_t kItems = 4 * kThreads;  // assignments of a block of the sort, at least
+constexpr int64_t kItems = kEach * kThreads;  // assignments of a block of the sort, at least
 constexpr int kMaxBlocks = 128;           // every block reads every block's counts
 int64_t per_block(int64_t n) {
   return std::max<int64_t>(kItems, cdiv(cdiv(n, kMaxBlocks), kItems) * kItems);
@@ -464,9 +486,18 @@ cudaError_t launch_sort_tokens(const SortDesc& d, int* launches, cudaStream_t st
     pm::count_kernel<<<a.blocks, pm::kThreads, sizeof(int32_t) * d.E, stream>>>(a);
     ++*launches;
   }
-  pm::rank_kernel<<<a.blocks, pm::kThreads, smem, stream>>>(a);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute early;  // beside the counts' end: it ranks its own assignments before it waits for them
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)a.blocks);
+  cfg.blockDim = dim3(pm::kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &early;
+  cfg.numAttrs = a.blocks > 1 ? 1 : 0;
   ++*launches;
-  return cudaGetLastError();
+  return cudaLaunchKernelEx(&cfg, pm::rank_kernel, a);
 }
 
 cudaError_t launch_permute(const PermuteDesc& d, cudaStream_t stream) {
@@ -503,7 +534,12 @@ cudaError_t launch_unpermute(const UnpermuteDesc& d, cudaStream_t stream) {
   a.cols = d.cols;
   a.chunks = (int)cdiv(d.cols, rows::kChunk);
   a.k = d.k;
-  const unsigned blocks = (unsigned)std::min<int64_t>(cdiv(a.T * a.chunks, 8), (int64_t)num_sms() * 16);
+  // a warp's work: up to 16 chunks of a row, fewer where there would be less than 32 works an SM (7168 columns of 16384
+  // tokens: 339 us with 14 chunks, 343 with 7 or 4, 480 with one, whose rows' numbers are then looked up for every chunk)
+  const int64_t pieces = std::max<int64_t>(cdiv(a.chunks, 16), std::min<int64_t>(a.chunks, cdiv(32 * num_sms(), a.T)));
+  a.piece = (int)cdiv(a.chunks, pieces);
+  a.pieces = (int)cdiv(a.chunks, a.piece);
+  const unsigned blocks = (unsigned)std::min<int64_t>(cdiv(a.T * a.pieces, 8), (int64_t)num_sms() * 16);
   return pm::with_rows(d.type, d.cols, [&](auto T, auto M) {
     pm::unpermute_kernel<decltype(T)::value, decltype(M)::value><<<blocks, 256, 0, stream>>>(a);
     return cudaGetLastError();
@@ -523,7 +559,10 @@ cudaError_t launch_unpermute_backward(const UnpermuteBackwardDesc& d, cudaStream
   a.cols = d.cols;
   a.chunks = (int)cdiv(d.cols, rows::kChunk);
   a.k = d.k;
-  const int W = std::min(8, a.chunks);
+  // warps of a token: four, up to eight where few tokens would leave SMs idle (16384 tokens of 7168 columns: 600 us with four
+  // or two, 637 with eight: every token ends in a barrier and a sum over the warps)
+  const int64_t most = std::min<int64_t>(8, std::max<int64_t>(4, cdiv(24 * num_sms(), a.T)));
+  const int W = (int)cdiv(a.chunks, cdiv(a.chunks, most));
   const unsigned blocks = (unsigned)std::min<int64_t>(a.T, (int64_t)num_sms() * 64 / W);
   return pm::with_rows(d.type, d.cols, [&](auto T, auto M) {
     pm::spread_kernel<decltype(T)::value, decltype(M)::value><<<blocks, 32 * W, 0, stream>>>(a);

@@ -9,8 +9,12 @@
 // instead of being stored.
 //
 // Both are bound by HBM: a row is read once and held in registers between its reduction and its outputs.
+#include <cuda_fp8.h>
+
+#include <algorithm>
+#include <type_traits>
+
 #include "common.cuh"
-#include "fp4_impl.cuh"
 #include "kernels.h"
 #include "rows.cuh"
 
@@ -24,6 +28,7 @@ using rows::kMap4;
 using rows::kMap8;
 
 constexpr int kNone = -1;
+constexpr uint32_t kInfBits = 0x7F800000u;
 
 struct Args {
   const void* x;
@@ -84,18 +89,10 @@ __device__ __forceinline__ void quantize(const Args& a, int64_t row, int c0, int
   for (int h = 0; h < (MAP == kMap8 ? 1 : 2); ++h) {
     constexpr int kN = MAP == kMap8 ? 8 : 4;
     float scale = 1.f;
-    if (m[h]) scale = m[h] > fp4::kInfBits ? __uint_as_float(m[h]) : fmaxf(__fdiv_rn(__uint_as_float(m[h]), 448.0f), 1.1754944e-38f);
-    if (fp4::ordinary(scale) && m[h] < fp4::kOrdinaryMax) {
-      const float r = __frcp_rn(scale);
+    if (m[h]) scale = m[h] > kInfBits ? __uint_as_float(m[h]) : fmaxf(__fdiv_rn(__uint_as_float(m[h]), 448.0f), 1.1754944e-38f);
+    const float by = __frcp_rn(scale);
 #pragma unroll
-      for (int i = 0; i < kN; i += 2) {
-        const float2 u = fp4::quotient(make_float2(y[4 * h + i], y[4 * h + i + 1]), make_float2(scale, scale), make_float2(r, r));
-        v[4 * h + i] = u.x, v[4 * h + i + 1] = u.y;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < kN; ++i) v[4 * h + i] = __fdiv_rn(y[4 * h + i], scale);
-    }
+    for (int i = 0; i < kN; ++i) v[4 * h + i] = y[4 * h + i] * by;
     const int b = c0 / 128 + (MAP == kMap8 ? lane / 16 : h);
     if ((MAP == kMap8 ? lane % 16 : lane) == 0 && b < nb) a.s[row * nb + b] = scale;
   }
@@ -103,18 +100,17 @@ __device__ __forceinline__ void quantize(const Args& a, int64_t row, int c0, int
 #pragma unroll
   for (int i = 0; i < 4; ++i) code[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i], v[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
   uint8_t* q = a.q + row * a.cols + c0;
-  if (MAP == kMap8 && c0 + 8 * lane + 8 <= a.cols) {
-    *reinterpret_cast<uint2*>(q + 8 * lane) = make_uint2(code[0] | code[1] << 16, code[2] | code[3] << 16);
-    return;
-  }
+  if constexpr (MAP == kMap8) {
+    if (c0 + 8 * lane < a.cols)
+      *reinterpret_cast<uint2*>(q + 8 * lane) = make_uint2(code[0] | code[1] << 16, code[2] | code[3] << 16);
+  } else if constexpr (MAP == kMap4) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    if (MAP == kMap4 && c0 + 128 * h + 4 * lane + 4 <= a.cols) {
-      *reinterpret_cast<uint32_t*>(q + 128 * h + 4 * lane) = code[2 * h] | code[2 * h + 1] << 16;
-      continue;
-    }
+    for (int h = 0; h < 2; ++h)
+      if (c0 + 128 * h + 4 * lane < a.cols)
+        *reinterpret_cast<uint32_t*>(q + 128 * h + 4 * lane) = code[2 * h] | code[2 * h + 1] << 16;
+  } else {
 #pragma unroll
-    for (int i = 4 * h; i < 4 * h + 4; ++i) {
+    for (int i = 0; i < 8; ++i) {
       const int c = rows::column<MAP>(lane, i);
       if (c0 + c < a.cols) q[c] = (uint8_t)(code[i / 2] >> (8 * (i & 1)));
     }
@@ -122,14 +118,14 @@ __device__ __forceinline__ void quantize(const Args& a, int64_t row, int c0, int
 }
 
 // blockDim.x / 32 warps a row, warp w with chunks w, w + W, ..; blockDim.y rows a block.
-template <int XT, int RT, int MAP, bool FP8, int CPW>
-__global__ void __launch_bounds__(1024) norm_kernel(const Args a) {
+template <int XT, int RT, int MAP, bool FP8, int CPW, int THREADS, int BLOCKS>
+__global__ void __launch_bounds__(THREADS, BLOCKS) norm_kernel(const Args a) {
   __shared__ float part[32];
   constexpr int kRT = RT == kNone ? XT : RT;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
   const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   const bool in = row < a.rows;
-  float t[CPW][8], w[CPW][8];
+  float t[CPW][8];
   if (in) {
     Chunk<XT, MAP> x[CPW];
     Chunk<kRT, MAP> r[CPW];
@@ -141,8 +137,6 @@ __global__ void __launch_bounds__(1024) norm_kernel(const Args a) {
       x[j].load(xr, c0, a.cols, lane);
       if (RT != kNone) r[j].load(rr, c0, a.cols, lane);
     }
-#pragma unroll
-    for (int j = 0; j < CPW; ++j) load_weight<XT, MAP>(a.w, a.w_f32, (warp + j * W) * kChunk, a.cols, lane, w[j]);
 #pragma unroll
     for (int j = 0; j < CPW; ++j) {
       x[j].values(t[j]);
@@ -175,9 +169,10 @@ __global__ void __launch_bounds__(1024) norm_kernel(const Args a) {
     if (c0 >= a.cols) break;
     if (RT != kNone && a.total)
       rows::store<kRT, MAP>(static_cast<char*>(a.total) + row * a.cols * rows::kSize<kRT>, c0, a.cols, lane, t[j]);
-    float y[8];
+    float y[8], w[8];
+    load_weight<XT, MAP>(a.w, a.w_f32, c0, a.cols, lane, w);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = t[j][i] * rstd * w[j][i];
+    for (int i = 0; i < 8; ++i) y[i] = t[j][i] * rstd * w[i];
     if (a.y) rows::store<XT, MAP>(static_cast<char*>(a.y) + row * a.cols * rows::kSize<XT>, c0, a.cols, lane, y);
     if (FP8) quantize<MAP>(a, row, c0, lane, y);
   }
@@ -198,12 +193,40 @@ struct BackArgs {
 
 constexpr int kGroups = 8;  // rows of a block at a time, where a warp holds a row
 
+// 16 bytes of global memory into shared memory, zeros where there is nothing to read: complete once the group they are
+// committed in is waited for. A thread reads back what it copied itself, so no barrier is needed.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A thread's numbers of the rows to come: stages of dy, t and dt, each kWords 16-byte words a chunk. Word w of a stage lies
+// at w * threads + thread, so a warp's words are consecutive.
+template <int TYPE, int TT, int CPW>
+struct Ring {
+  static constexpr int kDy = TYPE == MOE_TYPE_F32 ? 2 : 1, kT = TT == MOE_TYPE_F32 ? 2 : 1;
+  static constexpr int kWords = CPW * (kDy + 2 * kT);
+  static constexpr int bytes(int threads, int stages) { return 16 * kWords * threads * stages; }
+};
+
+// Rows in flight a thread: two, or one where two would not fit (wide fp32 rows).
+template <int TYPE, int TT, int CPW, int THREADS>
+constexpr int kStages = Ring<TYPE, TT, CPW>::bytes(THREADS, 2) <= 200 * 1024 ? 2 : 1;
+
 // Persistent: a thread has the same columns in every row, so it keeps the weight and the weight's gradient of them in
-// registers. GROUPS rows at a time where one warp holds a row, else one.
+// registers, and copies its own numbers of later rows into shared memory while it works on this one. GROUPS rows at a time
+// where one warp holds a row, else one. Rows that are not whole 16 bytes are loaded as they are needed.
 template <int TYPE, int TT, int MAP, int CPW, int GROUPS, int THREADS>
-__global__ void __launch_bounds__(THREADS) back_kernel(const BackArgs a) {
+__global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 4 : THREADS == 512 ? 2 : 1) back_kernel(const BackArgs a) {
+  extern __shared__ uint4 ring[];
   __shared__ float2 part[2][32];
   __shared__ float dw_part[GROUPS > 1 ? GROUPS : 1][GROUPS > 1 ? kChunk : 1];
+  using R = Ring<TYPE, TT, CPW>;
+  constexpr int S = kStages<TYPE, TT, CPW, THREADS>;
   const int lane = threadIdx.x & 31, warp = GROUPS > 1 ? 0 : threadIdx.x >> 5, W = GROUPS > 1 ? 1 : blockDim.x >> 5;
   const int group = GROUPS > 1 ? threadIdx.x >> 5 : 0;
   float w[CPW][8], dw[CPW][8];
@@ -213,43 +236,61 @@ __global__ void __launch_bounds__(THREADS) back_kernel(const BackArgs a) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[j][i] = 0.f;
   }
-  constexpr bool kAhead = TYPE != MOE_TYPE_F32 && TT != MOE_TYPE_F32 && MAP != kMap1 && THREADS <= 512;
-  struct Row {
-    Chunk<TYPE, MAP> dy[CPW];
-    Chunk<TT, MAP> t[CPW], dt[CPW];
-  };
-  auto fetch = [&](Row& r, int64_t row) {
-    const char* dyr = static_cast<const char*>(a.dy) + row * a.cols * rows::kSize<TYPE>;
-    const char* tr = static_cast<const char*>(a.t) + row * a.ldt * rows::kSize<TT>;
-    const char* dtr = static_cast<const char*>(a.dt) + row * a.cols * rows::kSize<TT>;
+  // numbers of a chunk: from the ring, or straight from the row
+  auto numbers = [&](auto type, int slot, int word, const void* row, int j, float (&f)[8]) {
+    constexpr int kType = decltype(type)::value, kN = kType == MOE_TYPE_F32 ? 2 : 1;
+    Chunk<kType, MAP> c;
+    if constexpr (MAP == kMap1) {
+      c.load(row, (warp + j * W) * kChunk, a.cols, lane);
+    } else {
 #pragma unroll
-    for (int j = 0; j < CPW; ++j) {
-      const int c0 = (warp + j * W) * kChunk;
-      r.dy[j].load(dyr, c0, a.cols, lane);
-      r.t[j].load(tr, c0, a.cols, lane);
-      if (a.dt)
-        r.dt[j].load(dtr, c0, a.cols, lane);
-      else
-        r.dt[j].clear();
+      for (int n = 0; n < kN; ++n) {
+        const uint4 v = ring[(slot * R::kWords + word + j * kN + n) * blockDim.x + threadIdx.x];
+        c.w[4 * n] = v.x, c.w[4 * n + 1] = v.y, c.w[4 * n + 2] = v.z, c.w[4 * n + 3] = v.w;
+      }
+    }
+    c.values(f);
+  };
+  auto copy = [&](auto type, int slot, int word, const char* row) {
+    constexpr int kType = decltype(type)::value, kN = kType == MOE_TYPE_F32 ? 2 : 1;
+#pragma unroll
+    for (int j = 0; j < CPW; ++j)
+#pragma unroll
+      for (int n = 0; n < kN; ++n) {
+        const int c = (warp + j * W) * kChunk + rows::column<MAP>(lane, 4 * n);
+        const bool there = c < a.cols;
+        copy16(smem_u32(&ring[(slot * R::kWords + word + j * kN + n) * blockDim.x + threadIdx.x]),
+               row + (there ? (int64_t)c * rows::kSize<kType> : 0), there);
+      }
+  };
+  using Dy = std::integral_constant<int, TYPE>;
+  using T = std::integral_constant<int, TT>;
+  constexpr int kAtT = CPW * R::kDy, kAtDt = kAtT + CPW * R::kT;
+  auto dy_row = [&](int64_t row) { return static_cast<const char*>(a.dy) + row * a.cols * rows::kSize<TYPE>; };
+  auto t_row = [&](int64_t row) { return static_cast<const char*>(a.t) + row * a.ldt * rows::kSize<TT>; };
+  auto dt_row = [&](int64_t row) { return static_cast<const char*>(a.dt) + row * a.cols * rows::kSize<TT>; };
+  auto fetch = [&](int slot, int64_t row) {
+    if constexpr (MAP != kMap1) {
+      if (row < a.rows) {
+        copy(Dy{}, slot, 0, dy_row(row));
+        copy(T{}, slot, kAtT, t_row(row));
+        if (a.dt) copy(T{}, slot, kAtDt, dt_row(row));
+      }
+      copies_commit();
     }
   };
   const int64_t step = (int64_t)gridDim.x * GROUPS;
   int64_t row = (int64_t)blockIdx.x * GROUPS + group;
-  Row cur, next;
-  if (kAhead && row < a.rows) fetch(next, row);
-  for (int turn = 0; row < a.rows; row += step, turn ^= 1) {
-    if (kAhead) {
-      cur = next;
-      if (row + step < a.rows) fetch(next, row + step);
-    } else {
-      fetch(cur, row);
-    }
+#pragma unroll
+  for (int s = 0; s < S; ++s) fetch(s, row + s * step);
+  for (int turn = 0, slot = 0; row < a.rows; row += step, turn ^= 1, slot = slot + 1 == S ? 0 : slot + 1) {
+    if constexpr (MAP != kMap1) copies_wait<S - 1>();
     float ss = 0.f, gt = 0.f;
 #pragma unroll
     for (int j = 0; j < CPW; ++j) {
       float g[8], v[8];
-      cur.dy[j].values(g);
-      cur.t[j].values(v);
+      numbers(Dy{}, slot, 0, dy_row(row), j, g);
+      numbers(T{}, slot, kAtT, t_row(row), j, v);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         ss = fmaf(v[i], v[i], ss);
@@ -272,9 +313,14 @@ __global__ void __launch_bounds__(THREADS) back_kernel(const BackArgs a) {
       const int c0 = (warp + j * W) * kChunk;
       if (c0 >= a.cols) break;
       float g[8], v[8], d[8];
-      cur.dy[j].values(g);
-      cur.t[j].values(v);
-      cur.dt[j].values(d);
+      numbers(Dy{}, slot, 0, dy_row(row), j, g);
+      numbers(T{}, slot, kAtT, t_row(row), j, v);
+      if (a.dt) {
+        numbers(T{}, slot, kAtDt, dt_row(row), j, d);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[i] = 0.f;
+      }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float n = v[i] * rstd;
@@ -284,7 +330,9 @@ __global__ void __launch_bounds__(THREADS) back_kernel(const BackArgs a) {
       if (a.dx) rows::store<TYPE, MAP>(static_cast<char*>(a.dx) + row * a.cols * rows::kSize<TYPE>, c0, a.cols, lane, d);
       if (a.dr) rows::store<TT, MAP>(static_cast<char*>(a.dr) + row * a.cols * rows::kSize<TT>, c0, a.cols, lane, d);
     }
+    fetch(slot, row + S * step);
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (!a.part) return;
   if (GROUPS > 1) {  // the block's rows, in order
 #pragma unroll
@@ -311,6 +359,7 @@ __global__ void __launch_bounds__(THREADS) back_kernel(const BackArgs a) {
 __global__ void __launch_bounds__(1024) dweight_kernel(const float* part, int n, int cols, int type, void* dw) {
   __shared__ float sums[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // it is launched beside the other kernel's end
   float sum = 0.f;
   if (c < cols)
     for (int b = warp; b < n; b += 32) sum += part[(int64_t)b * cols + c];
@@ -365,8 +414,8 @@ cudaError_t launch_rms_norm(const RmsNormDesc& d, cudaStream_t stream) {
   a.cols = d.cols;
   a.w_f32 = d.weight_type == MOE_TYPE_F32;
   a.eps = d.eps;
-  const bool aligned = rows::aligned_rows(d.type, d.ldx, d.rows) && rows::aligned_rows(d.type, d.cols, d.rows) &&
-                       (!d.residual || rows::aligned_rows(d.type, d.ldr, d.rows));
+  const bool aligned = rows::whole(d.type, d.cols) && (d.rows == 1 || rows::whole(d.type, d.ldx)) &&
+                       (d.rows == 1 || !d.residual || rows::whole(d.type, d.ldr));
   const int chunks = (int)cdiv(d.cols, rows::kChunk);
   const int cpw = chunks > 8 ? 2 : 1;
   const int W = (int)cdiv(chunks, cpw), G = W == 1 ? 8 : 1;
@@ -378,14 +427,17 @@ cudaError_t launch_rms_norm(const RmsNormDesc& d, cudaStream_t stream) {
       kernel<<<grid, block, 0, stream>>>(a);
       return cudaGetLastError();
     };
-    if (d.q) return cpw == 2 ? go(rn::norm_kernel<kT, kR, kM, true, 2>) : go(rn::norm_kernel<kT, kR, kM, true, 1>);
-    return cpw == 2 ? go(rn::norm_kernel<kT, kR, kM, false, 2>) : go(rn::norm_kernel<kT, kR, kM, false, 1>);
+    auto sized = [&](auto Q) {
+      constexpr bool kQ = decltype(Q)::value != 0;
+      if (cpw == 2) return W <= 16 ? go(rn::norm_kernel<kT, kR, kM, kQ, 2, 512, 3>) : go(rn::norm_kernel<kT, kR, kM, kQ, 2, 1024, 1>);
+      return W <= 8 ? go(rn::norm_kernel<kT, kR, kM, kQ, 1, 256, 4>) : go(rn::norm_kernel<kT, kR, kM, kQ, 1, 1024, 1>);
+    };
+    return d.q ? sized(rn::Int<1>{}) : sized(rn::Int<0>{});
   });
 }
 
 namespace rn {
 
-// Warps of a row and blocks of the gradient's kernel: 1024 threads an SM, each at least one row.
 int back_warps(int cols) {
   const int chunks = (int)cdiv(cols, rows::kChunk);
   return chunks > 8 ? (int)cdiv(chunks, 2) : chunks;
@@ -393,9 +445,11 @@ int back_warps(int cols) {
 
 }  // namespace rn
 
+// Blocks of the gradient's kernel, at most: as many as run at once (fewer where shared memory holds fewer), each at least
+// one row.
 int rms_norm_backward_blocks(int64_t rows, int cols) {
   const int W = rn::back_warps(cols), G = W == 1 ? rn::kGroups : 1;
-  const int per_sm = std::max(1, 32 / (W * G));
+  const int per_sm = W * G <= 8 ? 32 / (W * G) : W <= 16 ? 2 : 1;
   return (int)std::max<int64_t>(1, std::min<int64_t>(cdiv(rows, G), (int64_t)kNumSMsHint * per_sm));
 }
 
@@ -413,25 +467,52 @@ cudaError_t launch_rms_norm_backward(const RmsNormBackwardDesc& d, int* launches
   a.cols = d.cols;
   a.w_f32 = d.weight_type == MOE_TYPE_F32;
   a.eps = d.eps;
-  const bool aligned = rows::aligned_rows(d.type, d.ldt, d.rows) && rows::aligned_rows(d.type, d.cols, d.rows);
+  const bool aligned = rows::whole(d.type, d.cols) && (d.rows == 1 || rows::whole(d.type, d.ldt));
   const int W = rn::back_warps(d.cols);
-  const int grid = rms_norm_backward_blocks(d.rows, d.cols);
+  int grid = rms_norm_backward_blocks(d.rows, d.cols);
   *launches = d.dweight ? 2 : 1;
   cudaError_t e = rn::with_types(d.type, d.total_type, aligned, [&](auto T, auto R, auto M) {
     constexpr int kT = decltype(T)::value, kM = decltype(M)::value;
     constexpr int kR = decltype(R)::value == rn::kNone ? kT : decltype(R)::value;
-    auto go = [&](auto kernel, int threads) {
-      kernel<<<grid, threads, 0, stream>>>(a);
+    auto go = [&](auto C, auto G, auto N, int threads) {
+      constexpr int kC = decltype(C)::value, kN = decltype(N)::value;
+      constexpr int kS = rn::kStages<kT, kR, kC, kN>;
+      auto kernel = rn::back_kernel<kT, kR, kM, kC, decltype(G)::value, kN>;
+      using Ring = rn::Ring<kT, kR, kC>;
+      static PerDevice<bool> attr;  // one for each kernel
+      bool set = false;
+      cudaError_t r = per_device<bool>(
+          attr,
+          [&](bool& v) {
+            const cudaError_t x =
+                cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Ring::bytes(kN, kS));
+            v = x == cudaSuccess;
+            return x;
+          },
+          &set);
+      if (r != cudaSuccess) return r;
+      const int smem = kM == rows::kMap1 ? 0 : Ring::bytes(threads, kS);
+      const int fit = std::max(1, 220 * 1024 / std::max(1, smem + 1024));  // blocks an SM
+      grid = (int)std::min<int64_t>(grid, (int64_t)kNumSMsHint * fit);
+      kernel<<<grid, threads, smem, stream>>>(a);
       return cudaGetLastError();
     };
-    if (W == 1) return go(rn::back_kernel<kT, kR, kM, 1, rn::kGroups, 32 * rn::kGroups>, 32 * rn::kGroups);
-    if (d.cols <= 8 * rows::kChunk) return go(rn::back_kernel<kT, kR, kM, 1, 1, 256>, 32 * W);
-    if (W <= 16) return go(rn::back_kernel<kT, kR, kM, 2, 1, 512>, 32 * W);
-    return go(rn::back_kernel<kT, kR, kM, 2, 1, 1024>, 32 * W);
+    if (W == 1) return go(rn::Int<1>{}, rn::Int<rn::kGroups>{}, rn::Int<32 * rn::kGroups>{}, 32 * rn::kGroups);
+    if (d.cols <= 8 * rows::kChunk) return go(rn::Int<1>{}, rn::Int<1>{}, rn::Int<256>{}, 32 * W);
+    if (W <= 16) return go(rn::Int<2>{}, rn::Int<1>{}, rn::Int<512>{}, 32 * W);
+    return go(rn::Int<2>{}, rn::Int<1>{}, rn::Int<1024>{}, 32 * W);
   });
   if (e != cudaSuccess || !d.dweight) return e;
-  rn::dweight_kernel<<<(unsigned)cdiv(d.cols, 32), 1024, 0, stream>>>(a.part, grid, d.cols, d.weight_type, d.dweight);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)cdiv(d.cols, 32));
+  cfg.blockDim = dim3(1024);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, rn::dweight_kernel, (const float*)a.part, grid, d.cols, d.weight_type, d.dweight);
 }
 
 }  // namespace moe

@@ -2,9 +2,9 @@
 // read and write them: a warp takes 256 consecutive columns (a chunk) at a time, a lane 8 of them, held as fp32.
 //
 // Which 8 depends on how the rows lie in memory (MAP):
-//   kMap8  rows that begin on 16 bytes, 16-bit numbers: columns 8 lane .. 8 lane + 7, one 16-byte access
+//   kMap8  rows that are whole 16 bytes and begin on 16, 16-bit numbers: columns 8 lane .. 8 lane + 7, one 16-byte access
 //   kMap4  the same for fp32: columns 4 lane .. + 3 and 128 + 4 lane .. + 3, so that both accesses are whole lines
-//   kMap1  rows that begin anywhere: columns lane + 32 i, one number an access. A warp's access is then 64 or 128
+//   kMap1  rows of any width that begin anywhere: columns lane + 32 i, one number an access. A warp's access is then 64 or 128
 //          consecutive bytes; with 8 consecutive numbers a lane it would be 32 pieces of four lines.
 // Every chunk is 256 columns in all of them, so a lane's columns are the same in every row, and the blocks of 128 columns
 // that share an 8-bit scale are half a chunk.
@@ -84,20 +84,9 @@ struct Chunk {
 #pragma unroll
       for (int h = 0; h < (kWide ? 2 : 1); ++h) {
         const int c = c0 + column<MAP>(lane, 4 * h);
-        constexpr int kN = kWide ? 4 : 8;
-        if (c + kN <= cols) {
-          const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const char*>(row) + (int64_t)c * kSize<TYPE>);
-          w[4 * h] = v.x, w[4 * h + 1] = v.y, w[4 * h + 2] = v.z, w[4 * h + 3] = v.w;
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if constexpr (kWide)
-              w[4 * h + i] = c + i < cols ? load_bits<TYPE>(row, c + i) : 0u;
-            else
-              w[i] = (c + 2 * i < cols ? load_bits<TYPE>(row, c + 2 * i) : 0u) |
-                     (c + 2 * i + 1 < cols ? load_bits<TYPE>(row, c + 2 * i + 1) << 16 : 0u);
-          }
-        }
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (c < cols) v = *reinterpret_cast<const uint4*>(static_cast<const char*>(row) + (int64_t)c * kSize<TYPE>);
+        w[4 * h] = v.x, w[4 * h + 1] = v.y, w[4 * h + 2] = v.z, w[4 * h + 3] = v.w;
       }
     }
   }
@@ -133,27 +122,19 @@ __device__ __forceinline__ void store(void* row, int c0, int cols, int lane, con
 #pragma unroll
     for (int h = 0; h < (kWide ? 2 : 1); ++h) {
       const int c = c0 + column<MAP>(lane, 4 * h);
-      constexpr int kN = kWide ? 4 : 8;
-      if (c + kN <= cols) {
-        uint4 v;
-        if constexpr (kWide)
-          v = make_uint4(__float_as_uint(f[4 * h]), __float_as_uint(f[4 * h + 1]), __float_as_uint(f[4 * h + 2]),
-                         __float_as_uint(f[4 * h + 3]));
-        else
-          v = make_uint4(pack2<TYPE>(f[0], f[1]), pack2<TYPE>(f[2], f[3]), pack2<TYPE>(f[4], f[5]), pack2<TYPE>(f[6], f[7]));
-        *reinterpret_cast<uint4*>(static_cast<char*>(row) + (int64_t)c * kSize<TYPE>) = v;
-      } else {
-#pragma unroll
-        for (int i = 0; i < kN; ++i)
-          if (c + i < cols) store_bits<TYPE>(row, c + i, bits_of<TYPE>(f[4 * h + i]));
-      }
+      uint4 v;
+      if constexpr (kWide)
+        v = make_uint4(__float_as_uint(f[4 * h]), __float_as_uint(f[4 * h + 1]), __float_as_uint(f[4 * h + 2]),
+                       __float_as_uint(f[4 * h + 3]));
+      else
+        v = make_uint4(pack2<TYPE>(f[0], f[1]), pack2<TYPE>(f[2], f[3]), pack2<TYPE>(f[4], f[5]), pack2<TYPE>(f[6], f[7]));
+      if (c < cols) *reinterpret_cast<uint4*>(static_cast<char*>(row) + (int64_t)c * kSize<TYPE>) = v;
     }
   }
 }
 
-// Whether rows of this type that lie ld numbers apart all begin on 16 bytes (the base does).
-inline bool aligned_rows(int type, int64_t ld, int64_t rows) { return rows <= 1 || ld % (type == MOE_TYPE_F32 ? 4 : 8) == 0; }
-inline int map_of(int type, bool aligned) { return !aligned ? kMap1 : type == MOE_TYPE_F32 ? kMap4 : kMap8; }
+// Whether a row length or distance of n numbers of this type is whole 16 bytes.
+inline bool whole(int type, int64_t n) { return n % (type == MOE_TYPE_F32 ? 4 : 8) == 0; }
 
 }  // namespace rows
 }  // namespace moe
