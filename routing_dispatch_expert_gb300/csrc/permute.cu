@@ -19,6 +19,9 @@
 #include "kernels.h"
 #include "rows.cuh"
 
+#ifndef PM_DEEP
+#define PM_DEEP 16
+#endif
 namespace moe {
 namespace pm {
 
@@ -84,7 +87,7 @@ __device__ __forceinline__ int block_prefix(int v, int* warp_sums, int& total) {
 // before this round's [E] and the assignments in all [E]; the offset of each group [max(E, n_slots)].
 constexpr int kEach = 4;  // assignments of a lane in a round
 __global__ void __launch_bounds__(kThreads) rank_kernel(const SortArgs a) {
-  extern __shared__ int32_t sh[];
+  extern __shared__ __align__(16) int32_t sh[];
   __shared__ int warp_sums[kWarps];
   const int E = a.E, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int32_t* cnt = sh;
@@ -96,15 +99,19 @@ __global__ void __launch_bounds__(kThreads) rank_kernel(const SortArgs a) {
   for (int64_t c0 = lo; c0 < hi; c0 += kEach * kThreads) {
     const int64_t at = c0 + warp * 32 * kEach + lane;
     int mine[kEach], rank[kEach];
+    float weight[kEach];
 #pragma unroll
     for (int j = 0; j < kEach; ++j) {
       const int64_t i = at + 32 * j;
-      const int e = i < hi ? a.idx[i] : -1;
-      mine[j] = e >= 0 && e < E ? e : -1;
+      mine[j] = i < hi ? a.idx[i] : -1;
+      weight[j] = a.row_weight && i < hi ? a.weight[i] : 0.f;
     }
     if (c0 > lo) __syncthreads();
-    for (int e = threadIdx.x; e < kWarps * E; e += kThreads) cnt[e] = 0;
+    for (int e = threadIdx.x; e < kWarps / 4 * E; e += kThreads) reinterpret_cast<int4*>(cnt)[e] = make_int4(0, 0, 0, 0);
     __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kEach; ++j)
+      if (mine[j] < 0 || mine[j] >= E) mine[j] = -1;
 #pragma unroll
     for (int j = 0; j < kEach; ++j) {  // the first lane of an expert counts for all of its lanes
       const int e = mine[j];
@@ -125,7 +132,7 @@ __global__ void __launch_bounds__(kThreads) rank_kernel(const SortArgs a) {
         if (threadIdx.x >= side * E) break;
         int total = 0, earlier = 0;
         const int32_t* h = a.hist + e % E;
-#pragma unroll 8
+#pragma unroll 16
         for (int b = e / E; b < a.blocks; b += side) {
           const int c = h[(int64_t)b * E];
           total += c;
@@ -137,12 +144,13 @@ __global__ void __launch_bounds__(kThreads) rank_kernel(const SortArgs a) {
     }
     __syncthreads();
     for (int e = threadIdx.x; e < E; e += kThreads) {
-      int n = c0 == lo && a.blocks == 1 ? 0 : base[e];
+      int n = c0 == lo && a.blocks == 1 ? 0 : base[e], c[kWarps];
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) c[w] = cnt[w * E + e];
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const int c = cnt[w * E + e];
         cnt[w * E + e] = n;
-        n += c;
+        n += c[w];
       }
       base[e] = n;
       if (a.blocks == 1) all[e] = n;  // of all once this is the last round, which it is: a batch of one block has one
@@ -190,8 +198,8 @@ __global__ void __launch_bounds__(kThreads) rank_kernel(const SortArgs a) {
           } else {
             row = offset[e] + r;
           }
-          a.row_token[row] = (int32_t)(i / a.k);
-          if (a.row_weight) a.row_weight[row] = a.weight[i];
+          a.row_token[row] = (int)i / a.k;
+          if (a.row_weight) a.row_weight[row] = weight[j];
         }
       }
       a.inv_pos[i] = row;
@@ -210,41 +218,40 @@ struct CopyPlane {
   const void* src;  // [T], ld words from row to row
   void* dst;        // [T k], contiguous
   int64_t ld;
-  int words;        // of a row
-  int pieces;       // of a row: a warp's work
+  int words;          // of a row
+  int piece, pieces;  // words of a warp's work, a multiple of 32, and those works of a row
 };
 
-constexpr int kDepth = 4;  // words of a lane in a piece
-
-template <class Word>
+// Words of a lane in a piece, at most: 8 where there are enough pieces for every SM, else 4.
+template <class Word, int DEPTH>
 __device__ __forceinline__ void copy_item(const CopyPlane& p, const int32_t* inv_pos, int64_t T, int k, int64_t held,
                                           int64_t item, int lane) {
   const int64_t t = item / p.pieces;
-  const int c0 = (int)(item - t * p.pieces) * 32 * kDepth + lane;
-  Word v[kDepth];
+  const int first = (int)(item - t * p.pieces) * p.piece, end = min(p.words, first + p.piece), c0 = first + lane;
+  Word v[DEPTH];
   if (t >= T) {  // a row that holds nothing
     Word* dst = static_cast<Word*>(p.dst) + (held + (t - T)) * p.words;
 #pragma unroll
-    for (int u = 0; u < kDepth; ++u)
-      if (c0 + 32 * u < p.words) dst[c0 + 32 * u] = Word{};
+    for (int u = 0; u < DEPTH; ++u)
+      if (c0 + 32 * u < end) dst[c0 + 32 * u] = Word{};
     return;
   }
   const Word* src = static_cast<const Word*>(p.src) + t * p.ld;
 #pragma unroll
-  for (int u = 0; u < kDepth; ++u)
-    if (c0 + 32 * u < p.words) v[u] = src[c0 + 32 * u];
+  for (int u = 0; u < DEPTH; ++u)
+    if (c0 + 32 * u < end) v[u] = src[c0 + 32 * u];
   const int mine = lane < k ? inv_pos[t * k + lane] : -1;
   for (int j = 0; j < k; ++j) {
     const int r = __shfl_sync(0xffffffffu, mine, j);
     if (r < 0) continue;
     Word* dst = static_cast<Word*>(p.dst) + (int64_t)r * p.words;
 #pragma unroll
-    for (int u = 0; u < kDepth; ++u)
-      if (c0 + 32 * u < p.words) dst[c0 + 32 * u] = v[u];
+    for (int u = 0; u < DEPTH; ++u)
+      if (c0 + 32 * u < end) dst[c0 + 32 * u] = v[u];
   }
 }
 
-template <class Word>
+template <class Word, int DEPTH>
 __global__ void __launch_bounds__(256) permute_kernel(const CopyPlane p, const CopyPlane scales, const int32_t* inv_pos,
                                                       const int32_t* held_at, int64_t T, int k) {
   const int lane = threadIdx.x & 31;
@@ -253,9 +260,9 @@ __global__ void __launch_bounds__(256) permute_kernel(const CopyPlane p, const C
   const int64_t items = rows * p.pieces, more = scales.words ? rows * scales.pieces : 0;
   for (int64_t it = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; it < items + more; it += warps) {
     if (it < items)
-      copy_item<Word>(p, inv_pos, T, k, held, it, lane);
+      copy_item<Word, DEPTH>(p, inv_pos, T, k, held, it, lane);
     else
-      copy_item<uint32_t>(scales, inv_pos, T, k, held, it - items, lane);
+      copy_item<uint32_t, DEPTH>(scales, inv_pos, T, k, held, it - items, lane);
   }
 }
 
@@ -509,16 +516,25 @@ cudaError_t launch_permute(const PermuteDesc& d, cudaStream_t stream) {
     p.dst = d.xd;
     p.ld = ld / (int64_t)sizeof(Word);
     p.words = (int)(bytes / (int64_t)sizeof(Word));
-    p.pieces = (int)cdiv(p.words, 32 * pm::kDepth);
+    const bool deep = d.T * cdiv(p.words, 256) >= (int64_t)num_sms() * 64;
+    const auto cut = [&](pm::CopyPlane& q) {  // even pieces of whole steps of 32 words
+      const int steps = (int)cdiv(q.words, 32);
+      q.piece = 32 * (int)cdiv(steps, cdiv(steps, deep ? PM_DEEP : 4));
+      q.pieces = (int)cdiv(q.words, q.piece);
+    };
+    cut(p);
     if (d.xd_scales) {
       s.src = d.x_scales;
       s.dst = d.xd_scales;
       s.ld = s.words = (int)cdiv(d.cols, 128);
-      s.pieces = (int)cdiv(s.words, 32 * pm::kDepth);
+      cut(s);
     }
     const int64_t items = (int64_t)d.T * (p.pieces + (d.xd_scales ? s.pieces : 0));
     const unsigned blocks = (unsigned)std::min<int64_t>(cdiv(items, 8), (int64_t)num_sms() * 16);
-    pm::permute_kernel<Word><<<blocks, 256, 0, stream>>>(p, s, d.inv_pos, d.held, d.T, d.k);
+    if (deep)
+      pm::permute_kernel<Word, PM_DEEP><<<blocks, 256, 0, stream>>>(p, s, d.inv_pos, d.held, d.T, d.k);
+    else
+      pm::permute_kernel<Word, 4><<<blocks, 256, 0, stream>>>(p, s, d.inv_pos, d.held, d.T, d.k);
     return cudaGetLastError();
   });
 }

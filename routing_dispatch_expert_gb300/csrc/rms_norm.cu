@@ -193,17 +193,6 @@ struct BackArgs {
 
 constexpr int kGroups = 8;  // rows of a block at a time, where a warp holds a row
 
-// 16 bytes of global memory into shared memory, zeros where there is nothing to read: complete once the group they are
-// committed in is waited for. A thread reads back what it copied itself, so no barrier is needed.
-__device__ __forceinline__ void copy16(uint32_t to, const void* from, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // A thread's numbers of the rows to come: stages of dy, t and dt, each kWords 16-byte words a chunk. Word w of a stage lies
 // at w * threads + thread, so a warp's words are consecutive.
 template <int TYPE, int TT, int CPW>
@@ -259,7 +248,7 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 4 : THREADS == 512 ?
       for (int n = 0; n < kN; ++n) {
         const int c = (warp + j * W) * kChunk + rows::column<MAP>(lane, 4 * n);
         const bool there = c < a.cols;
-        copy16(smem_u32(&ring[(slot * R::kWords + word + j * kN + n) * blockDim.x + threadIdx.x]),
+        rows::copy16(smem_u32(&ring[(slot * R::kWords + word + j * kN + n) * blockDim.x + threadIdx.x]),
                row + (there ? (int64_t)c * rows::kSize<kType> : 0), there);
       }
   };
@@ -276,7 +265,7 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 4 : THREADS == 512 ?
         copy(T{}, slot, kAtT, t_row(row));
         if (a.dt) copy(T{}, slot, kAtDt, dt_row(row));
       }
-      copies_commit();
+      rows::copies_commit();
     }
   };
   const int64_t step = (int64_t)gridDim.x * GROUPS;
@@ -284,7 +273,7 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 4 : THREADS == 512 ?
 #pragma unroll
   for (int s = 0; s < S; ++s) fetch(s, row + s * step);
   for (int turn = 0, slot = 0; row < a.rows; row += step, turn ^= 1, slot = slot + 1 == S ? 0 : slot + 1) {
-    if constexpr (MAP != kMap1) copies_wait<S - 1>();
+    if constexpr (MAP != kMap1) rows::copies_wait<S - 1>();
     float ss = 0.f, gt = 0.f;
 #pragma unroll
     for (int j = 0; j < CPW; ++j) {

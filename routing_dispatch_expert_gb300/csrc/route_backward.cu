@@ -11,9 +11,7 @@
 // fp32. Sigmoids are taken with e^min(l) factored out of their sum, so that a token whose sigmoids all underflow keeps their
 // ratios; a token whose chosen logits are all -inf has no weights and a gradient of 0.
 //
-// A token is held by L lanes, at least k of them: lane j works on slot j, and all of them write the row, zeros or the dense
-// part first and the chosen experts' numbers over it (the group's lanes in order: a barrier of the warp lies between). Bound by the
-// bytes of dlogits (and of the logits, for a softmax over all).
+// Bound by the bytes of dlogits (and of the logits, for a softmax over all).
 #include <algorithm>
 #include <type_traits>
 
@@ -21,6 +19,9 @@
 #include "kernels.h"
 #include "rows.cuh"
 
+#ifndef RB_G
+#define RB_G 64
+#endif
 namespace moe {
 namespace rb {
 
@@ -49,9 +50,85 @@ __device__ __forceinline__ float lanes_max(float v) {
   return v;
 }
 
-// EPL: numbers of a lane, 4 (sub + L j) + i
-template <int TYPE, bool SIGMOID, bool DENSE, int L, int EPL>
-__global__ void __launch_bounds__(kThreads) kernel(const Args a) {
+// One slot of a token: its expert (-1: none), the gradient of its weight, and its logit.
+template <int TYPE>
+__device__ __forceinline__ void load_slot(const Args& a, int64_t t, int j, int& e, float& g, float& l) {
+  e = -1;
+  g = 0.f;
+  l = -INFINITY;
+  if (t >= a.T || j >= a.k) return;
+  const int c = a.idx[t * a.k + j];
+  if (c < 0 || c >= a.E) return;
+  e = c;
+  g = a.dw[t * a.k + j];
+  l = rows::value<TYPE>(rows::load_bits<TYPE>(a.logits, t * a.E + e));
+}
+
+// The gradients of the slots that chose this lane's expert, and how many they are: an expert chosen twice gets both, and each
+// of its slots writes the same sum.
+template <int L>
+__device__ __forceinline__ void same_expert(int k, int e, float g, float& all, float& n) {
+  all = n = 0.f;
+  for (int j = 0; j < k; ++j) {
+    const int ej = __shfl_sync(0xffffffffu, e, j, L);
+    const float gj = __shfl_sync(0xffffffffu, g, j, L);
+    if (ej == e) {
+      all += gj;
+      n += 1.f;
+    }
+  }
+}
+
+// Weights of the chosen experts alone: L lanes a token (k rounded up to a power of two), lane j slot j. The rows of a warp's
+// tokens lie one after the other and are zeroed as one; the slots then write over that, behind a barrier of the warp.
+template <int TYPE, bool SIGMOID, int L>
+__global__ void __launch_bounds__(kThreads) chosen_kernel(const Args a) {
+  constexpr int kPer = 32 / L;  // tokens of a warp
+  const int lane = threadIdx.x & 31, sub = lane % L;
+  const int64_t warps = ((int64_t)gridDim.x * kThreads) >> 5;
+  const int64_t bytes = (int64_t)kPer * a.E * rows::kSize<TYPE>;  // of a warp's rows
+  for (int64_t t0 = (((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5) * kPer; t0 < a.T; t0 += warps * kPer) {
+    const int64_t t = t0 + lane / L;
+    int e;
+    float g, l;
+    load_slot<TYPE>(a, t, sub, e, g, l);
+    char* out = static_cast<char*>(a.dlogits) + t0 * a.E * rows::kSize<TYPE>;
+    if ((bytes & 15) == 0 && t0 + kPer <= a.T) {
+      for (int64_t b = 16 * lane; b < bytes; b += 512) *reinterpret_cast<uint4*>(out + b) = make_uint4(0u, 0u, 0u, 0u);
+    } else {
+      const int64_t n = min((int64_t)kPer, a.T - t0) * a.E;
+      for (int64_t i = lane; i < n; i += 32) rows::store_bits<TYPE>(out, i, 0u);
+    }
+    float u, slope = 1.f, all, n;
+    if (!SIGMOID) {
+      float m = lanes_max<L>(l);
+      if (m == -INFINITY) m = 0.f;
+      u = expf(l - m);
+    } else {
+      // sigmoid(l) e^-c = 1 / (e^c + e^(c - l)) with c = min(max l, 0)
+      float c = 0.f;
+      if (a.renorm) {
+        const float m = lanes_max<L>(l);
+        c = m == -INFINITY ? 0.f : fminf(m, 0.f);
+      }
+      u = e < 0 ? 0.f : __fdividef(1.0f, expf(c) + expf(c - l));
+      slope = __fdividef(1.0f, 1.0f + expf(l));
+    }
+    same_expert<L>(a.k, e, g, all, n);
+    if (a.renorm) {  // a softmax over the chosen, or sigmoids divided by their sum
+      const float z = lanes_sum<L>(u);
+      u = z == 0.f ? 0.f : __fdiv_rn(u, z);
+      all -= n * lanes_sum<L>(g * u);
+    }
+    __syncwarp();
+    if (e >= 0) rows::store_bits<TYPE>(a.dlogits, t * a.E + e, rows::bits_of<TYPE>(a.scale * u * slope * all));
+  }
+}
+
+// A softmax over all experts: L lanes a token, at least k, a lane the experts 4 (sub + L j) + i, EPL of them; all of them write
+// the dense part -c p sum_j g_j p_{e_j}, then lane j slot j over that.
+template <int TYPE, int L, int EPL>
+__global__ void __launch_bounds__(kThreads) dense_kernel(const Args a) {
   constexpr int kPer = 32 / L;  // tokens of a warp
   const int lane = threadIdx.x & 31, sub = lane % L;
   const int64_t warps = ((int64_t)gridDim.x * kThreads) >> 5;
@@ -59,81 +136,50 @@ __global__ void __launch_bounds__(kThreads) kernel(const Args a) {
   for (int64_t t0 = (((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5) * kPer; t0 < a.T; t0 += warps * kPer) {
     const int64_t t = t0 + lane / L;
     const bool in = t < a.T;
-    int e = -1;
-    float g = 0.f, l = -INFINITY;
-    if (in && sub < a.k) {
-      e = a.idx[t * a.k + sub];
-      g = a.dw[t * a.k + sub];
-      if (e < 0 || e >= a.E) {
-        e = -1;
-        g = 0.f;
+    int e;
+    float g, l;
+    load_slot<TYPE>(a, t, sub, e, g, l);
+    float p[EPL], m = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < EPL / 4; ++j) {
+      const int at = 4 * (sub + L * j);
+      if (vec && in && at < a.E) {
+        if constexpr (TYPE == MOE_TYPE_F32) {
+          const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.logits) + t * a.E + at);
+          p[4 * j] = v.x, p[4 * j + 1] = v.y, p[4 * j + 2] = v.z, p[4 * j + 3] = v.w;
+        } else {
+          const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.logits) + t * a.E + at);
+          p[4 * j] = bf16_lo(v.x), p[4 * j + 1] = bf16_hi(v.x), p[4 * j + 2] = bf16_lo(v.y), p[4 * j + 3] = bf16_hi(v.y);
+        }
       } else {
-        l = rows::value<TYPE>(rows::load_bits<TYPE>(a.logits, t * a.E + e));
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          p[4 * j + i] = in && at + i < a.E ? rows::value<TYPE>(rows::load_bits<TYPE>(a.logits, t * a.E + at + i)) : -INFINITY;
       }
     }
-    float p[DENSE ? EPL : 1], m = -INFINITY, u, slope = 1.f;
-    if (DENSE) {
 #pragma unroll
-      for (int j = 0; j < EPL; ++j) {
-        const int at = 4 * (sub + L * (j / 4)) + j % 4;
-        p[j] = in && at < a.E ? rows::value<TYPE>(rows::load_bits<TYPE>(a.logits, t * a.E + at)) : -INFINITY;
-        m = fmaxf(m, p[j]);
-      }
-      m = lanes_max<L>(m);
-      if (m == -INFINITY) m = 0.f;
-      float z = 0.f;
+    for (int j = 0; j < EPL; ++j) m = fmaxf(m, p[j]);
+    m = lanes_max<L>(m);
+    if (m == -INFINITY) m = 0.f;
+    float z = 0.f, all, n;
 #pragma unroll
-      for (int j = 0; j < EPL; ++j) {
-        p[j] = expf(p[j] - m);
-        z += p[j];
-      }
-      z = lanes_sum<L>(z);
-      const float r = z == 0.f ? 0.f : __fdiv_rn(1.0f, z);
-#pragma unroll
-      for (int j = 0; j < EPL; ++j) p[j] *= r;
-      u = expf(l - m) * r;
-    } else if (!SIGMOID) {
-      m = lanes_max<L>(l);
-      if (m == -INFINITY) m = 0.f;
-      u = expf(l - m);
-      const float z = lanes_sum<L>(u);
-      u = z == 0.f ? 0.f : __fdiv_rn(u, z);
-    } else {
-      // sigmoid(l) e^-c = 1 / (e^c + e^(c - l)) with c = min(max l, 0)
-      float c = 0.f;
-      if (a.renorm) {
-        m = lanes_max<L>(l);
-        c = m == -INFINITY ? 0.f : fminf(m, 0.f);
-      }
-      u = __fdiv_rn(1.0f, expf(c) + expf(c - l));
-      if (e < 0) u = 0.f;
-      slope = __fdiv_rn(1.0f, 1.0f + expf(l));
-      if (a.renorm) {
-        const float z = lanes_sum<L>(u);
-        u = z == 0.f ? 0.f : __fdiv_rn(u, z);
-      }
+    for (int j = 0; j < EPL; ++j) {
+      p[j] = expf(p[j] - m);
+      z += p[j];
     }
-    const bool centred = DENSE || !SIGMOID || a.renorm;
-    const float dot = centred ? lanes_sum<L>(e >= 0 ? g * u : 0.f) : 0.f;
-    // an expert chosen twice: every slot of it writes the same sum
-    float all = 0.f, n = 0.f;
-    for (int j = 0; j < a.k; ++j) {
-      const int ej = __shfl_sync(0xffffffffu, e, j, L);
-      const float gj = __shfl_sync(0xffffffffu, g, j, L);
-      if (ej == e) {
-        all += gj;
-        n += 1.f;
-      }
-    }
-    if (DENSE) n = 1.f;
-    const float d = a.scale * u * slope * (all - n * dot);
+    z = lanes_sum<L>(z);
+    const float r = z == 0.f ? 0.f : __fdiv_rn(1.0f, z);
+    const float u = expf(l - m) * r;
+    const float dot = lanes_sum<L>(g * u);
+    same_expert<L>(a.k, e, g, all, n);
     if (in) {
+      const float by = -a.scale * r * dot;
 #pragma unroll
       for (int j = 0; j < EPL / 4; ++j) {
         const int at = 4 * (sub + L * j);
         float o[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = DENSE ? -a.scale * p[DENSE ? 4 * j + i : 0] * dot : 0.f;
+        for (int i = 0; i < 4; ++i) o[i] = by * p[4 * j + i];
         if (vec && at < a.E) {
           if (TYPE == MOE_TYPE_F32)
             *reinterpret_cast<float4*>(static_cast<float*>(a.dlogits) + t * a.E + at) = make_float4(o[0], o[1], o[2], o[3]);
@@ -148,7 +194,7 @@ __global__ void __launch_bounds__(kThreads) kernel(const Args a) {
       }
     }
     __syncwarp();
-    if (e >= 0) rows::store_bits<TYPE>(a.dlogits, t * a.E + e, rows::bits_of<TYPE>(d));
+    if (e >= 0) rows::store_bits<TYPE>(a.dlogits, t * a.E + e, rows::bits_of<TYPE>(a.scale * u * (all - dot)));
   }
 }
 
@@ -179,21 +225,30 @@ cudaError_t launch_route_backward(const RouteBackwardDesc& d, cudaStream_t strea
   a.k = d.k;
   a.renorm = d.renorm;
   a.scale = d.routed_scale;
-  const bool dense = !d.sigmoid && !d.renorm;
-  return rb::with_shape(d.E, d.k, [&](auto Lc, auto Ec) {
-    constexpr int L = decltype(Lc)::value, EPL = decltype(Ec)::value;
-    const int64_t blocks = std::min<int64_t>(cdiv(d.T, (rb::kThreads / 32) * (32 / L)), (int64_t)num_sms() * 8);
-    auto go = [&](auto kernel) {
-      kernel<<<(unsigned)blocks, rb::kThreads, 0, stream>>>(a);
-      return cudaGetLastError();
+  auto go = [&](auto kernel, int per_warp) {
+    const int64_t blocks = std::min<int64_t>(cdiv(d.T, (rb::kThreads / 32) * per_warp), (int64_t)num_sms() * RB_G);
+    kernel<<<(unsigned)blocks, rb::kThreads, 0, stream>>>(a);
+    return cudaGetLastError();
+  };
+  auto typed = [&](auto T) {
+    constexpr int kT = decltype(T)::value;
+    if (!d.sigmoid && !d.renorm)
+      return rb::with_shape(d.E, d.k, [&](auto Lc, auto Ec) {
+        constexpr int L = decltype(Lc)::value;
+        return go(rb::dense_kernel<kT, L, decltype(Ec)::value>, 32 / L);
+      });
+    auto chosen = [&](auto Lc) {
+      constexpr int L = decltype(Lc)::value;
+      return d.sigmoid ? go(rb::chosen_kernel<kT, true, L>, 32 / L) : go(rb::chosen_kernel<kT, false, L>, 32 / L);
     };
-    auto typed = [&](auto T) {
-      constexpr int kT = decltype(T)::value;
-      if (d.sigmoid) return go(rb::kernel<kT, true, false, L, EPL>);
-      return dense ? go(rb::kernel<kT, false, true, L, EPL>) : go(rb::kernel<kT, false, false, L, EPL>);
-    };
-    return d.bf16 ? typed(std::integral_constant<int, MOE_TYPE_BF16>{}) : typed(std::integral_constant<int, MOE_TYPE_F32>{});
-  });
+    using std::integral_constant;
+    if (d.k <= 2) return chosen(integral_constant<int, 2>{});
+    if (d.k <= 4) return chosen(integral_constant<int, 4>{});
+    if (d.k <= 8) return chosen(integral_constant<int, 8>{});
+    if (d.k <= 16) return chosen(integral_constant<int, 16>{});
+    return chosen(integral_constant<int, 32>{});
+  };
+  return d.bf16 ? typed(std::integral_constant<int, MOE_TYPE_BF16>{}) : typed(std::integral_constant<int, MOE_TYPE_F32>{});
 }
 
 }  // namespace moe

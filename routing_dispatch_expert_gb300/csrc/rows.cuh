@@ -133,6 +133,17 @@ __device__ __forceinline__ void store(void* row, int c0, int cols, int lane, con
   }
 }
 
+// 16 bytes of global memory into shared memory, zeros where there is nothing to read: complete once the group they are
+// committed in is waited for. A thread reads back what it copied itself, so no barrier is needed.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // Whether a row length or distance of n numbers of this type is whole 16 bytes.
 inline bool whole(int type, int64_t n) { return n % (type == MOE_TYPE_F32 ? 4 : 8) == 0; }
 
