@@ -1,5 +1,4 @@
-// Tokens sorted by expert and back: the sort of the assignments, the rows copied into its order, the rows added up in token
-// order with the route weights, and the gradient of that.
+// Tokens sorted by expert: the sort of the assignments, and the rows copied into its order. (The way back is in unpermute.cu.)
 //
 // The sort is a stable counting sort of the T k assignments (token, then slot) by expert: an assignment's rank is the number
 // of earlier ones to its expert, its row the expert's offset plus that (under a placement: round robin over the expert's
@@ -17,11 +16,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
-#include "rows.cuh"
 
-#ifndef PM_DEEP
-#define PM_DEEP 16
-#endif
 namespace moe {
 namespace pm {
 
@@ -222,7 +217,10 @@ struct CopyPlane {
   int piece, pieces;  // words of a warp's work, a multiple of 32, and those works of a row
 };
 
-// Words of a lane in a piece, at most: 8 where there are enough pieces for every SM, else 4.
+// Words of a lane in a piece, at most: 16 where there are enough pieces for every SM, else 4 (16384 rows of 7168 bytes to
+// eight places each: 165 us with the whole row in a piece, 169 with 8, 172 with 4).
+constexpr int kDeep = 16;
+
 template <class Word, int DEPTH>
 __device__ __forceinline__ void copy_item(const CopyPlane& p, const int32_t* inv_pos, int64_t T, int k, int64_t held,
                                           int64_t item, int lane) {
@@ -266,154 +264,6 @@ __global__ void __launch_bounds__(256) permute_kernel(const CopyPlane p, const C
   }
 }
 
-// ------------------------------------------------------------------------------------------
-// rows back in token order
-// ------------------------------------------------------------------------------------------
-constexpr int kBatch = 8;  // rows of a token in flight
-
-// Rows and weights of a token's slots j0 .. j0 + 7 in every lane; -1 past the last slot.
-__device__ __forceinline__ void slots(const int32_t* inv_pos, const float* weights, int64_t t, int k, int j0,
-                                      int (&row)[kBatch], float (&w)[kBatch]) {
-  const int lane = threadIdx.x & 31;
-  const bool in = lane < kBatch && j0 + lane < k;
-  const int r = in ? inv_pos[t * k + j0 + lane] : -1;
-  const float v = in && weights ? weights[t * k + j0 + lane] : 1.f;
-#pragma unroll
-  for (int j = 0; j < kBatch; ++j) {
-    row[j] = __shfl_sync(0xffffffffu, r, j);
-    w[j] = __shfl_sync(0xffffffffu, v, j);
-  }
-}
-
-struct AddArgs {
-  const void* yd;
-  const void* base;      // or nullptr
-  const float* weights;  // [T, k] or nullptr
-  const int32_t* inv_pos;
-  void* y;
-  int64_t T;
-  int cols, chunks, k;
-  int piece, pieces;  // chunks of a warp's work, and those works of a row
-};
-
-// A warp a piece of a token's row: fp32, the base first and then the slots in order. All rows of a chunk are loaded before any
-// is added.
-template <int TYPE, int MAP>
-__global__ void __launch_bounds__(256, TYPE != MOE_TYPE_F32 && MAP != rows::kMap1 ? 3 : 2) unpermute_kernel(const AddArgs a) {
-  const int lane = threadIdx.x & 31;
-  const int64_t warps = ((int64_t)gridDim.x * blockDim.x) >> 5, items = a.T * a.pieces;
-  const int64_t pitch = (int64_t)a.cols * rows::kSize<TYPE>;
-  for (int64_t it = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; it < items; it += warps) {
-    const int64_t t = it / a.pieces;
-    const int first = (int)(it - t * a.pieces) * a.piece, last = min(a.chunks, first + a.piece);
-    int row[kBatch];
-    float w[kBatch];
-    slots(a.inv_pos, a.weights, t, a.k, 0, row, w);
-    for (int c = first; c < last; ++c) {
-      const int c0 = c * rows::kChunk;
-      float sum[8];
-      for (int j0 = 0; j0 < a.k; j0 += kBatch) {
-        if (a.k > kBatch) slots(a.inv_pos, a.weights, t, a.k, j0, row, w);
-        rows::Chunk<TYPE, MAP> b, v[kBatch];
-        if (j0 == 0) {
-          if (a.base)
-            b.load(static_cast<const char*>(a.base) + t * pitch, c0, a.cols, lane);
-          else
-            b.clear();
-        }
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j)
-          if (row[j] >= 0) v[j].load(static_cast<const char*>(a.yd) + row[j] * pitch, c0, a.cols, lane);
-        if (j0 == 0) b.values(sum);
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-          if (row[j] < 0) continue;
-          float f[8];
-          v[j].values(f);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) sum[i] = fmaf(w[j], f[i], sum[i]);
-        }
-      }
-      rows::store<TYPE, MAP>(static_cast<char*>(a.y) + t * pitch, c0, a.cols, lane, sum);
-    }
-  }
-}
-
-struct SpreadArgs {
-  const void* dy;
-  const void* yd;        // or nullptr: no gradient of the weights
-  const float* weights;  // [T, k] or nullptr
-  const int32_t* inv_pos;
-  const int32_t* held_at;
-  void* dyd;
-  float* dweights;  // [T, k] or nullptr
-  int64_t T;
-  int cols, chunks, k;
-};
-
-// A block of W warps a token: its row of dy to its k rows of dyd, and their products with yd's rows, summed over the lanes
-// and then the warps. At the end the blocks clear the rows that hold nothing.
-template <int TYPE, int MAP>
-__global__ void __launch_bounds__(256, TYPE != MOE_TYPE_F32 && MAP != rows::kMap1 ? 3 : 2) spread_kernel(const SpreadArgs a) {
-  __shared__ float part[8][kBatch];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
-  const int64_t pitch = (int64_t)a.cols * rows::kSize<TYPE>;
-  float f[8];
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-    for (int j0 = 0; j0 < a.k; j0 += kBatch) {
-      int row[kBatch];
-      float w[kBatch], dot[kBatch];
-      slots(a.inv_pos, a.weights, t, a.k, j0, row, w);
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) dot[j] = 0.f;
-      for (int c = warp; c < a.chunks; c += W) {
-        const int c0 = c * rows::kChunk;
-        rows::Chunk<TYPE, MAP> dy, v[kBatch];
-        dy.load(static_cast<const char*>(a.dy) + t * pitch, c0, a.cols, lane);
-        if (a.yd) {
-#pragma unroll
-          for (int j = 0; j < kBatch; ++j)
-            if (row[j] >= 0) v[j].load(static_cast<const char*>(a.yd) + row[j] * pitch, c0, a.cols, lane);
-        }
-        float g[8];
-        dy.values(g);
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-          if (row[j] < 0) continue;
-          if (a.yd) {
-            v[j].values(f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) dot[j] = fmaf(g[i], f[i], dot[j]);
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) f[i] = w[j] * g[i];
-          rows::store<TYPE, MAP>(static_cast<char*>(a.dyd) + row[j] * pitch, c0, a.cols, lane, f);
-        }
-      }
-      if (!a.dweights) continue;
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], o);
-        if (lane == j) part[warp][j] = dot[j];
-      }
-      __syncthreads();
-      if (threadIdx.x < kBatch && j0 + threadIdx.x < a.k) {
-        float sum = 0.f;
-        for (int i = 0; i < W; ++i) sum += part[i][threadIdx.x];
-        a.dweights[t * a.k + j0 + threadIdx.x] = sum;
-      }
-      __syncthreads();
-    }
-  }
-  const int64_t held = *a.held_at;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = 0.f;
-  for (int64_t r = held + blockIdx.x; r < a.T * a.k; r += gridDim.x)
-    for (int c = warp; c < a.chunks; c += W)
-      rows::store<TYPE, MAP>(static_cast<char*>(a.dyd) + r * pitch, c * rows::kChunk, a.cols, lane, f);
-}
-
 // The word that rows of `bytes` bytes, `ld` bytes apart, are copied by: the widest that every row begins on.
 template <class F>
 cudaError_t with_word(int64_t bytes, int64_t ld, F&& f) {
@@ -421,20 +271,6 @@ cudaError_t with_word(int64_t bytes, int64_t ld, F&& f) {
   if (bytes % 4 == 0 && ld % 4 == 0) return f(uint32_t{});
   if (bytes % 2 == 0 && ld % 2 == 0) return f(uint16_t{});
   return f(uint8_t{});
-}
-
-template <class F>
-cudaError_t with_rows(int type, int64_t cols, F&& f) {
-  const bool aligned = rows::whole(type, cols);
-  using std::integral_constant;
-  if (type == MOE_TYPE_F32)
-    return aligned ? f(integral_constant<int, MOE_TYPE_F32>{}, integral_constant<int, rows::kMap4>{})
-                   : f(integral_constant<int, MOE_TYPE_F32>{}, integral_constant<int, rows::kMap1>{});
-  if (type == MOE_TYPE_BF16)
-    return aligned ? f(integral_constant<int, MOE_TYPE_BF16>{}, integral_constant<int, rows::kMap8>{})
-                   : f(integral_constant<int, MOE_TYPE_BF16>{}, integral_constant<int, rows::kMap1>{});
-  return aligned ? f(integral_constant<int, MOE_TYPE_F16>{}, integral_constant<int, rows::kMap8>{})
-                 : f(integral_constant<int, MOE_TYPE_F16>{}, integral_constant<int, rows::kMap1>{});
 }
 
 constexpr int64_t kItems = kEach * kThreads;  // assignments of a block of the sort, at least
@@ -519,7 +355,7 @@ cudaError_t launch_permute(const PermuteDesc& d, cudaStream_t stream) {
     const bool deep = d.T * cdiv(p.words, 256) >= (int64_t)num_sms() * 64;
     const auto cut = [&](pm::CopyPlane& q) {  // even pieces of whole steps of 32 words
       const int steps = (int)cdiv(q.words, 32);
-      q.piece = 32 * (int)cdiv(steps, cdiv(steps, deep ? PM_DEEP : 4));
+      q.piece = 32 * (int)cdiv(steps, cdiv(steps, deep ? pm::kDeep : 4));
       q.pieces = (int)cdiv(q.words, q.piece);
     };
     cut(p);
@@ -532,56 +368,9 @@ cudaError_t launch_permute(const PermuteDesc& d, cudaStream_t stream) {
     const int64_t items = (int64_t)d.T * (p.pieces + (d.xd_scales ? s.pieces : 0));
     const unsigned blocks = (unsigned)std::min<int64_t>(cdiv(items, 8), (int64_t)num_sms() * 16);
     if (deep)
-      pm::permute_kernel<Word, PM_DEEP><<<blocks, 256, 0, stream>>>(p, s, d.inv_pos, d.held, d.T, d.k);
+      pm::permute_kernel<Word, pm::kDeep><<<blocks, 256, 0, stream>>>(p, s, d.inv_pos, d.held, d.T, d.k);
     else
       pm::permute_kernel<Word, 4><<<blocks, 256, 0, stream>>>(p, s, d.inv_pos, d.held, d.T, d.k);
-    return cudaGetLastError();
-  });
-}
-
-cudaError_t launch_unpermute(const UnpermuteDesc& d, cudaStream_t stream) {
-  pm::AddArgs a;
-  a.yd = d.yd;
-  a.base = d.base;
-  a.weights = d.weights;
-  a.inv_pos = d.inv_pos;
-  a.y = d.y;
-  a.T = d.T;
-  a.cols = d.cols;
-  a.chunks = (int)cdiv(d.cols, rows::kChunk);
-  a.k = d.k;
-  // a warp's work: up to 16 chunks of a row, fewer where there would be less than 32 works an SM (7168 columns of 16384
-  // tokens: 339 us with 14 chunks, 343 with 7 or 4, 480 with one, whose rows' numbers are then looked up for every chunk)
-  const int64_t pieces = std::max<int64_t>(cdiv(a.chunks, 16), std::min<int64_t>(a.chunks, cdiv(32 * num_sms(), a.T)));
-  a.piece = (int)cdiv(a.chunks, pieces);
-  a.pieces = (int)cdiv(a.chunks, a.piece);
-  const unsigned blocks = (unsigned)std::min<int64_t>(cdiv(a.T * a.pieces, 8), (int64_t)num_sms() * 16);
-  return pm::with_rows(d.type, d.cols, [&](auto T, auto M) {
-    pm::unpermute_kernel<decltype(T)::value, decltype(M)::value><<<blocks, 256, 0, stream>>>(a);
-    return cudaGetLastError();
-  });
-}
-
-cudaError_t launch_unpermute_backward(const UnpermuteBackwardDesc& d, cudaStream_t stream) {
-  pm::SpreadArgs a;
-  a.dy = d.dy;
-  a.yd = d.dweights ? d.yd : nullptr;
-  a.weights = d.weights;
-  a.inv_pos = d.inv_pos;
-  a.held_at = d.held;
-  a.dyd = d.dyd;
-  a.dweights = d.dweights;
-  a.T = d.T;
-  a.cols = d.cols;
-  a.chunks = (int)cdiv(d.cols, rows::kChunk);
-  a.k = d.k;
-  // warps of a token: four, up to eight where few tokens would leave SMs idle (16384 tokens of 7168 columns: 600 us with four
-  // or two, 637 with eight: every token ends in a barrier and a sum over the warps)
-  const int64_t most = std::min<int64_t>(8, std::max<int64_t>(4, cdiv(24 * num_sms(), a.T)));
-  const int W = (int)cdiv(a.chunks, cdiv(a.chunks, most));
-  const unsigned blocks = (unsigned)std::min<int64_t>(a.T, (int64_t)num_sms() * 64 / W);
-  return pm::with_rows(d.type, d.cols, [&](auto T, auto M) {
-    pm::spread_kernel<decltype(T)::value, decltype(M)::value><<<blocks, 32 * W, 0, stream>>>(a);
     return cudaGetLastError();
   });
 }

@@ -43,9 +43,10 @@ struct Args {
   float eps;
 };
 
-__device__ __forceinline__ float warp_sum(float v) {
+template <int LANES = 32>
+__device__ __forceinline__ float lanes_sum(float v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
@@ -68,8 +69,8 @@ __device__ __forceinline__ void load_weight(const void* w, int w_f32, int c0, in
 
 // Codes and scales of a chunk: two blocks of 128 columns. The largest magnitude is taken over the bits, under which a NaN is
 // larger than every number: a block that holds an infinity or a NaN stands for NaN throughout.
-template <int MAP>
-__device__ __forceinline__ void quantize(const Args& a, int64_t row, int c0, int lane, const float (&y)[8]) {
+template <int MAP, int LANES>
+__device__ __forceinline__ void quantize(const Args& a, int64_t row, int c0, int cols, int lane, const float (&y)[8]) {
   uint32_t m[2] = {0u, 0u};
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -78,7 +79,7 @@ __device__ __forceinline__ void quantize(const Args& a, int64_t row, int c0, int
   }
   if (MAP == kMap8) {
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) m[0] = max(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
+    for (int o = (LANES < 16 ? LANES : 16) / 2; o > 0; o >>= 1) m[0] = max(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
   } else {
     m[0] = __reduce_max_sync(0xffffffffu, m[0]);
     m[1] = __reduce_max_sync(0xffffffffu, m[1]);
@@ -94,39 +95,40 @@ __device__ __forceinline__ void quantize(const Args& a, int64_t row, int c0, int
 #pragma unroll
     for (int i = 0; i < kN; ++i) v[4 * h + i] = y[4 * h + i] * by;
     const int b = c0 / 128 + (MAP == kMap8 ? lane / 16 : h);
-    if ((MAP == kMap8 ? lane % 16 : lane) == 0 && b < nb) a.s[row * nb + b] = scale;
+    if ((MAP == kMap8 ? lane % 16 : lane) == 0 && b < nb && cols > 0) a.s[row * nb + b] = scale;
   }
   uint32_t code[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) code[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i], v[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
   uint8_t* q = a.q + row * a.cols + c0;
   if constexpr (MAP == kMap8) {
-    if (c0 + 8 * lane < a.cols)
+    if (c0 + 8 * lane < cols)
       *reinterpret_cast<uint2*>(q + 8 * lane) = make_uint2(code[0] | code[1] << 16, code[2] | code[3] << 16);
   } else if constexpr (MAP == kMap4) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      if (c0 + 128 * h + 4 * lane < a.cols)
+      if (c0 + 128 * h + 4 * lane < cols)
         *reinterpret_cast<uint32_t*>(q + 128 * h + 4 * lane) = code[2 * h] | code[2 * h + 1] << 16;
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int c = rows::column<MAP>(lane, i);
-      if (c0 + c < a.cols) q[c] = (uint8_t)(code[i / 2] >> (8 * (i & 1)));
+      if (c0 + c < cols) q[c] = (uint8_t)(code[i / 2] >> (8 * (i & 1)));
     }
   }
 }
 
-// blockDim.x / 32 warps a row, warp w with chunks w, w + W, ..; blockDim.y rows a block.
-template <int XT, int RT, int MAP, bool FP8, int CPW, int THREADS, int BLOCKS>
+// blockDim.x / 32 warps a row, warp w with chunks w, w + W, ..; blockDim.y rows a block. With LANES < 32 a warp has 32 / LANES
+// narrow rows.
+template <int XT, int RT, int MAP, bool FP8, int CPW, int LANES, int THREADS, int BLOCKS>
 __global__ void __launch_bounds__(THREADS, BLOCKS) norm_kernel(const Args a) {
   __shared__ float part[32];
   constexpr int kRT = RT == kNone ? XT : RT;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
-  const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-  const bool in = row < a.rows;
+  const int lane = (threadIdx.x & 31) % LANES, warp = threadIdx.x >> 5, W = LANES == 32 ? blockDim.x >> 5 : 1;
+  const int64_t row = ((int64_t)blockIdx.x * blockDim.y + threadIdx.y) * (32 / LANES) + (threadIdx.x & 31) / LANES;
+  const int cols = row < a.rows ? a.cols : 0;
   float t[CPW][8];
-  if (in) {
+  {
     Chunk<XT, MAP> x[CPW];
     Chunk<kRT, MAP> r[CPW];
     const char* xr = static_cast<const char*>(a.x) + row * a.ldx * rows::kSize<XT>;
@@ -134,8 +136,8 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_kernel(const Args a) {
 #pragma unroll
     for (int j = 0; j < CPW; ++j) {
       const int c0 = (warp + j * W) * kChunk;
-      x[j].load(xr, c0, a.cols, lane);
-      if (RT != kNone) r[j].load(rr, c0, a.cols, lane);
+      x[j].load(xr, c0, cols, lane);
+      if (RT != kNone) r[j].load(rr, c0, cols, lane);
     }
 #pragma unroll
     for (int j = 0; j < CPW; ++j) {
@@ -149,32 +151,29 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_kernel(const Args a) {
     }
   }
   float ss = 0.f;
-  if (in) {
 #pragma unroll
-    for (int j = 0; j < CPW; ++j)
+  for (int j = 0; j < CPW; ++j)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(t[j][i], t[j][i], ss);
-  }
-  ss = warp_sum(ss);
+    for (int i = 0; i < 8; ++i) ss = fmaf(t[j][i], t[j][i], ss);
+  ss = lanes_sum<LANES>(ss);
   if (W > 1) {
     if (lane == 0) part[warp] = ss;
     __syncthreads();
-    ss = warp_sum(lane < W ? part[lane] : 0.f);
+    ss = lanes_sum(lane < W ? part[lane] : 0.f);
   }
-  if (!in) return;
   const float rstd = __frsqrt_rn(__fdiv_rn(ss, (float)a.cols) + a.eps);
 #pragma unroll
   for (int j = 0; j < CPW; ++j) {
     const int c0 = (warp + j * W) * kChunk;
-    if (c0 >= a.cols) break;
+    if (LANES == 32 && c0 >= cols) break;
     if (RT != kNone && a.total)
-      rows::store<kRT, MAP>(static_cast<char*>(a.total) + row * a.cols * rows::kSize<kRT>, c0, a.cols, lane, t[j]);
+      rows::store<kRT, MAP>(static_cast<char*>(a.total) + row * a.cols * rows::kSize<kRT>, c0, cols, lane, t[j]);
     float y[8], w[8];
     load_weight<XT, MAP>(a.w, a.w_f32, c0, a.cols, lane, w);
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = t[j][i] * rstd * w[i];
-    if (a.y) rows::store<XT, MAP>(static_cast<char*>(a.y) + row * a.cols * rows::kSize<XT>, c0, a.cols, lane, y);
-    if (FP8) quantize<MAP>(a, row, c0, lane, y);
+    if (a.y) rows::store<XT, MAP>(static_cast<char*>(a.y) + row * a.cols * rows::kSize<XT>, c0, cols, lane, y);
+    if (FP8) quantize<MAP, LANES>(a, row, c0, cols, lane, y);
   }
 }
 
@@ -189,12 +188,13 @@ struct BackArgs {
   int64_t rows, ldt;
   int cols, w_f32;
   float eps;
+  int stage, stages;  // rows that are not whole 16 bytes: words of a stage, and stages
 };
 
-constexpr int kGroups = 8;  // rows of a block at a time, where a warp holds a row
+constexpr int kGroups = 8;  // warps with rows of their own in a block, where a warp holds one row or several
 
 // A thread's numbers of the rows to come: stages of dy, t and dt, each kWords 16-byte words a chunk. Word w of a stage lies
-// at w * threads + thread, so a warp's words are consecutive.
+// at w * threads + thread, so a warp's words are consecutive. A thread reads back what it copied itself: no barrier.
 template <int TYPE, int TT, int CPW>
 struct Ring {
   static constexpr int kDy = TYPE == MOE_TYPE_F32 ? 2 : 1, kT = TT == MOE_TYPE_F32 ? 2 : 1;
@@ -202,21 +202,28 @@ struct Ring {
   static constexpr int bytes(int threads, int stages) { return 16 * kWords * threads * stages; }
 };
 
+constexpr int kMaxRing = 216 * 1024;  // bytes of a block's stages, at most
+
 // Rows in flight a thread: two, or one where two would not fit (wide fp32 rows).
 template <int TYPE, int TT, int CPW, int THREADS>
-constexpr int kStages = Ring<TYPE, TT, CPW>::bytes(THREADS, 2) <= 200 * 1024 ? 2 : 1;
+constexpr int kStages = Ring<TYPE, TT, CPW>::bytes(THREADS, 2) <= kMaxRing ? 2 : 1;
+
+// Rows that are not whole 16 bytes: a row's warps copy it as the 16-byte words that cover it, and read their numbers out of
+// those behind a barrier. Its first word may begin in the row before, its last one is copied up to the row's end.
+__host__ __device__ __forceinline__ int covering(int cols, int size) { return (cols * size + 15 + 15) / 16; }  // words, at most
 
 // Persistent: a thread has the same columns in every row, so it keeps the weight and the weight's gradient of them in
-// registers, and copies its own numbers of later rows into shared memory while it works on this one. GROUPS rows at a time
-// where one warp holds a row, else one. Rows that are not whole 16 bytes are loaded as they are needed.
-template <int TYPE, int TT, int MAP, int CPW, int GROUPS, int THREADS>
+// registers, while later rows are copied into shared memory. One row at a time by all warps of a block, or, with GROUPS > 1, a
+// row by each warp, or 32 / LANES narrow ones.
+template <int TYPE, int TT, int MAP, int CPW, int LANES, int GROUPS, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 4 : THREADS == 512 ? 2 : 1) back_kernel(const BackArgs a) {
   extern __shared__ uint4 ring[];
   __shared__ float2 part[2][32];
   __shared__ float dw_part[GROUPS > 1 ? GROUPS : 1][GROUPS > 1 ? kChunk : 1];
   using R = Ring<TYPE, TT, CPW>;
   constexpr int S = kStages<TYPE, TT, CPW, THREADS>;
-  const int lane = threadIdx.x & 31, warp = GROUPS > 1 ? 0 : threadIdx.x >> 5, W = GROUPS > 1 ? 1 : blockDim.x >> 5;
+  const int lane = (threadIdx.x & 31) % LANES, warp = GROUPS > 1 ? 0 : threadIdx.x >> 5;
+  const int W = GROUPS > 1 ? 1 : blockDim.x >> 5;
   const int group = GROUPS > 1 ? threadIdx.x >> 5 : 0;
   float w[CPW][8], dw[CPW][8];
 #pragma unroll
@@ -225,87 +232,123 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 4 : THREADS == 512 ?
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[j][i] = 0.f;
   }
-  // numbers of a chunk: from the ring, or straight from the row
-  auto numbers = [&](auto type, int slot, int word, const void* row, int j, float (&f)[8]) {
-    constexpr int kType = decltype(type)::value, kN = kType == MOE_TYPE_F32 ? 2 : 1;
+  using Dy = std::integral_constant<int, TYPE>;
+  using T = std::integral_constant<int, TT>;
+  const char* const from[3] = {static_cast<const char*>(a.dy), static_cast<const char*>(a.t), static_cast<const char*>(a.dt)};
+  const int64_t pitch[3] = {(int64_t)a.cols * rows::kSize<TYPE>, a.ldt * rows::kSize<TT>, (int64_t)a.cols * rows::kSize<TT>};
+  // first word of dy, t and dt in a stage
+  const int words[3] = {0, MAP == kMap1 ? covering(a.cols, rows::kSize<TYPE>) : CPW * R::kDy,
+                        MAP == kMap1 ? covering(a.cols, rows::kSize<TYPE>) + covering(a.cols, rows::kSize<TT>)
+                                     : CPW * (R::kDy + R::kT)};
+  uint4* const mine = MAP == kMap1 ? ring + (int64_t)group * a.stages * a.stage : ring;  // of this warp's rows
+  auto copy = [&](auto type, int which, int slot, int64_t row) {
+    constexpr int kType = decltype(type)::value;
+    const char* p = from[which] + row * pitch[which];
+    if constexpr (MAP == kMap1) {
+      const int off = (int)(reinterpret_cast<uintptr_t>(p) & 15), end = off + a.cols * rows::kSize<kType>;
+      for (int b = 16 * (GROUPS > 1 ? threadIdx.x & 31 : threadIdx.x); b < end; b += 16 * 32 * W)
+        rows::copy16(smem_u32(mine + slot * a.stage + words[which]) + b, p - off + b, min(16, end - b));
+    } else {
+      constexpr bool kHalves = kType != MOE_TYPE_F32 && MAP == kMap4;  // 8 bytes and 8 bytes of one word
+      constexpr int kN = kType == MOE_TYPE_F32 ? 2 : 1;
+#pragma unroll
+      for (int j = 0; j < CPW; ++j)
+#pragma unroll
+        for (int n = 0; n < (kHalves ? 2 : kN); ++n) {
+          const int c = (warp + j * W) * kChunk + rows::column<MAP>(lane, 4 * n);
+          const bool there = c < a.cols && (LANES == 32 || row < a.rows);
+          const char* src = there ? p + (int64_t)c * rows::kSize<kType> : from[which];
+          const int word = (slot * R::kWords + words[which] + j * kN + (kHalves ? 0 : n)) * blockDim.x + threadIdx.x;
+          if constexpr (kHalves)
+            rows::copy8(smem_u32(ring + word) + 8 * n, src, there ? 8 : 0);
+          else
+            rows::copy16(smem_u32(ring + word), src, there ? 16 : 0);
+        }
+    }
+  };
+  auto numbers = [&](auto type, int which, int slot, int64_t row, int j, float (&f)[8]) {
+    constexpr int kType = decltype(type)::value;
     Chunk<kType, MAP> c;
     if constexpr (MAP == kMap1) {
-      c.load(row, (warp + j * W) * kChunk, a.cols, lane);
+      const int off = (int)(reinterpret_cast<uintptr_t>(from[which] + row * pitch[which]) & 15);
+      c.load(reinterpret_cast<const char*>(mine + slot * a.stage + words[which]) + off, (warp + j * W) * kChunk, a.cols, lane);
     } else {
+      constexpr int kN = kType == MOE_TYPE_F32 ? 2 : 1;
 #pragma unroll
       for (int n = 0; n < kN; ++n) {
-        const uint4 v = ring[(slot * R::kWords + word + j * kN + n) * blockDim.x + threadIdx.x];
+        const uint4 v = ring[(slot * R::kWords + words[which] + j * kN + n) * blockDim.x + threadIdx.x];
         c.w[4 * n] = v.x, c.w[4 * n + 1] = v.y, c.w[4 * n + 2] = v.z, c.w[4 * n + 3] = v.w;
       }
     }
     c.values(f);
   };
-  auto copy = [&](auto type, int slot, int word, const char* row) {
-    constexpr int kType = decltype(type)::value, kN = kType == MOE_TYPE_F32 ? 2 : 1;
-#pragma unroll
-    for (int j = 0; j < CPW; ++j)
-#pragma unroll
-      for (int n = 0; n < kN; ++n) {
-        const int c = (warp + j * W) * kChunk + rows::column<MAP>(lane, 4 * n);
-        const bool there = c < a.cols;
-        rows::copy16(smem_u32(&ring[(slot * R::kWords + word + j * kN + n) * blockDim.x + threadIdx.x]),
-               row + (there ? (int64_t)c * rows::kSize<kType> : 0), there);
-      }
-  };
-  using Dy = std::integral_constant<int, TYPE>;
-  using T = std::integral_constant<int, TT>;
-  constexpr int kAtT = CPW * R::kDy, kAtDt = kAtT + CPW * R::kT;
-  auto dy_row = [&](int64_t row) { return static_cast<const char*>(a.dy) + row * a.cols * rows::kSize<TYPE>; };
-  auto t_row = [&](int64_t row) { return static_cast<const char*>(a.t) + row * a.ldt * rows::kSize<TT>; };
-  auto dt_row = [&](int64_t row) { return static_cast<const char*>(a.dt) + row * a.cols * rows::kSize<TT>; };
-  auto fetch = [&](int slot, int64_t row) {
-    if constexpr (MAP != kMap1) {
-      if (row < a.rows) {
-        copy(Dy{}, slot, 0, dy_row(row));
-        copy(T{}, slot, kAtT, t_row(row));
-        if (a.dt) copy(T{}, slot, kAtDt, dt_row(row));
-      }
-      rows::copies_commit();
+  constexpr int kRows = 32 / LANES;  // of a warp
+  const int64_t step = (int64_t)gridDim.x * GROUPS * kRows;
+  int64_t first = ((int64_t)blockIdx.x * GROUPS + group) * kRows;  // the warp's
+  auto fetch = [&](int slot, int64_t at) {
+    if (at < a.rows) {
+      const int64_t row = at + (threadIdx.x & 31) / LANES;
+      copy(Dy{}, 0, slot, row);
+      copy(T{}, 1, slot, row);
+      if (a.dt) copy(T{}, 2, slot, row);
     }
+    rows::copies_commit();
   };
-  const int64_t step = (int64_t)gridDim.x * GROUPS;
-  int64_t row = (int64_t)blockIdx.x * GROUPS + group;
-#pragma unroll
-  for (int s = 0; s < S; ++s) fetch(s, row + s * step);
-  for (int turn = 0, slot = 0; row < a.rows; row += step, turn ^= 1, slot = slot + 1 == S ? 0 : slot + 1) {
-    if constexpr (MAP != kMap1) rows::copies_wait<S - 1>();
+  auto meet = [&]() {  // the warps of a row
+    if (GROUPS > 1)
+      __syncwarp();
+    else
+      __syncthreads();
+  };
+  const int stages = MAP == kMap1 ? a.stages : S;
+  if (MAP != kMap1 || stages == 2) fetch(0, first);
+  if (MAP != kMap1 && S == 2) fetch(1, first + step);
+  for (int turn = 0, slot = 0; first < a.rows; first += step, turn ^= 1, slot = slot + 1 == stages ? 0 : slot + 1) {
+    if constexpr (MAP == kMap1) {
+      if (stages == 1) {
+        meet();  // the row before has been read
+        fetch(0, first);
+      }
+      rows::copies_wait<0>();
+      meet();  // this row has come, and the one before has been read
+      if (stages == 2) fetch(slot ^ 1, first + step);
+    } else {
+      rows::copies_wait<S - 1>();
+    }
+    const int64_t row = first + (threadIdx.x & 31) / LANES;
+    const int cols = LANES == 32 || row < a.rows ? a.cols : 0;
     float ss = 0.f, gt = 0.f;
 #pragma unroll
     for (int j = 0; j < CPW; ++j) {
       float g[8], v[8];
-      numbers(Dy{}, slot, 0, dy_row(row), j, g);
-      numbers(T{}, slot, kAtT, t_row(row), j, v);
+      numbers(Dy{}, 0, slot, row, j, g);
+      numbers(T{}, 1, slot, row, j, v);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         ss = fmaf(v[i], v[i], ss);
         gt = fmaf(g[i] * w[j][i], v[i], gt);
       }
     }
-    ss = warp_sum(ss);
-    gt = warp_sum(gt);
+    ss = lanes_sum<LANES>(ss);
+    gt = lanes_sum<LANES>(gt);
     if (W > 1) {  // one barrier a row: the next row's sums go to the other half
       if (lane == 0) part[turn][warp] = make_float2(ss, gt);
       __syncthreads();
       const float2 p = lane < W ? part[turn][lane] : make_float2(0.f, 0.f);
-      ss = warp_sum(p.x);
-      gt = warp_sum(p.y);
+      ss = lanes_sum(p.x);
+      gt = lanes_sum(p.y);
     }
     const float rstd = __frsqrt_rn(__fdiv_rn(ss, (float)a.cols) + a.eps);
     const float dot = __fdiv_rn(gt, (float)a.cols) * rstd;  // mean(g n)
 #pragma unroll
     for (int j = 0; j < CPW; ++j) {
       const int c0 = (warp + j * W) * kChunk;
-      if (c0 >= a.cols) break;
+      if (LANES == 32 && c0 >= cols) break;
       float g[8], v[8], d[8];
-      numbers(Dy{}, slot, 0, dy_row(row), j, g);
-      numbers(T{}, slot, kAtT, t_row(row), j, v);
+      numbers(Dy{}, 0, slot, row, j, g);
+      numbers(T{}, 1, slot, row, j, v);
       if (a.dt) {
-        numbers(T{}, slot, kAtDt, dt_row(row), j, d);
+        numbers(T{}, 2, slot, row, j, d);
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) d[i] = 0.f;
@@ -313,19 +356,23 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 4 : THREADS == 512 ?
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float n = v[i] * rstd;
-        dw[j][i] = fmaf(g[i], n, dw[j][i]);
+        if (LANES == 32 || cols) dw[j][i] = fmaf(g[i], n, dw[j][i]);
         d[i] = fmaf(rstd, fmaf(-n, dot, g[i] * w[j][i]), d[i]);
       }
-      if (a.dx) rows::store<TYPE, MAP>(static_cast<char*>(a.dx) + row * a.cols * rows::kSize<TYPE>, c0, a.cols, lane, d);
-      if (a.dr) rows::store<TT, MAP>(static_cast<char*>(a.dr) + row * a.cols * rows::kSize<TT>, c0, a.cols, lane, d);
+      if (a.dx) rows::store<TYPE, MAP>(static_cast<char*>(a.dx) + row * a.cols * rows::kSize<TYPE>, c0, cols, lane, d);
+      if (a.dr) rows::store<TT, MAP>(static_cast<char*>(a.dr) + row * a.cols * rows::kSize<TT>, c0, cols, lane, d);
     }
-    fetch(slot, row + S * step);
+    if constexpr (MAP != kMap1) fetch(slot, first + S * step);
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (!a.part) return;
-  if (GROUPS > 1) {  // the block's rows, in order
+  if constexpr (GROUPS > 1) {  // a warp's rows, then the block's warps, in order
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dw_part[group][rows::column<MAP>(lane, i)] = dw[0][i];
+    for (int i = 0; i < 8; ++i) {
+#pragma unroll
+      for (int o = LANES; o < 32; o <<= 1) dw[0][i] += __shfl_xor_sync(0xffffffffu, dw[0][i], o);
+      if ((threadIdx.x & 31) < LANES) dw_part[group][rows::column<MAP>(lane, i)] = dw[0][i];
+    }
     __syncthreads();
     for (int c = threadIdx.x; c < a.cols; c += 32 * GROUPS) {
       float sum = 0.f;
@@ -333,15 +380,15 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 4 : THREADS == 512 ?
       for (int k = 0; k < GROUPS; ++k) sum += dw_part[k][c];
       a.part[(int64_t)blockIdx.x * a.cols + c] = sum;
     }
-    return;
+  } else {
+#pragma unroll
+    for (int j = 0; j < CPW; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int c = (warp + j * W) * kChunk + rows::column<MAP>(lane, i);
+        if (c < a.cols) a.part[(int64_t)blockIdx.x * a.cols + c] = dw[j][i];
+      }
   }
-#pragma unroll
-  for (int j = 0; j < CPW; ++j)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = (warp + j * W) * kChunk + rows::column<MAP>(lane, i);
-      if (c < a.cols) a.part[(int64_t)blockIdx.x * a.cols + c] = dw[j][i];
-    }
 }
 
 // The weight's gradient from the blocks' sums, in block order: 32 columns a block, 32 warps over the sums.
@@ -354,7 +401,7 @@ __global__ void __launch_bounds__(1024) dweight_kernel(const float* part, int n,
     for (int b = warp; b < n; b += 32) sum += part[(int64_t)b * cols + c];
   sums[warp][lane] = sum;
   __syncthreads();
-  sum = warp_sum(sums[lane][warp]);
+  sum = lanes_sum(sums[lane][warp]);
   if (lane == 0 && blockIdx.x * 32 + warp < cols) {
     const int at = blockIdx.x * 32 + warp;
     if (type == MOE_TYPE_F32)
@@ -369,12 +416,19 @@ __global__ void __launch_bounds__(1024) dweight_kernel(const float* part, int n,
 template <int V>
 using Int = std::integral_constant<int, V>;
 
-// f(type, the other type, map) of rows of `type` beside rows of `other` (kNone, the same, or fp32)
+// Lanes of a row: narrow rows of whole 8 columns share a warp.
+int narrow_lanes(int cols) { return cols % 8 ? 32 : cols <= 32 ? 4 : cols <= 64 ? 8 : cols <= 128 ? 16 : 32; }
+
+// f(type, the other type, map, lanes of a row) of rows of `type` beside rows of `other` (kNone, the same, or fp32)
 template <class F>
-cudaError_t with_types(int type, int other, bool aligned, F&& f) {
+cudaError_t with_types(int type, int other, bool aligned, int lanes, F&& f) {
   auto mapped = [&](auto T, auto O) {
-    constexpr int kAligned = decltype(T)::value == MOE_TYPE_F32 ? kMap4 : kMap8;
-    return aligned ? f(T, O, Int<kAligned>{}) : f(T, O, Int<kMap1>{});
+    constexpr int kAligned = decltype(T)::value == MOE_TYPE_F32 || decltype(O)::value == MOE_TYPE_F32 ? kMap4 : kMap8;
+    if (!aligned) return f(T, O, Int<kMap1>{}, Int<32>{});
+    if (lanes == 4) return f(T, O, Int<kMap8>{}, Int<4>{});
+    if (lanes == 8) return f(T, O, Int<kMap8>{}, Int<8>{});
+    if (lanes == 16) return f(T, O, Int<kMap8>{}, Int<16>{});
+    return f(T, O, Int<kAligned>{}, Int<32>{});
   };
   auto beside = [&](auto T) {
     if (other == kNone) return mapped(T, Int<kNone>{});
@@ -408,18 +462,20 @@ cudaError_t launch_rms_norm(const RmsNormDesc& d, cudaStream_t stream) {
   const int chunks = (int)cdiv(d.cols, rows::kChunk);
   const int cpw = chunks > 8 ? 2 : 1;
   const int W = (int)cdiv(chunks, cpw), G = W == 1 ? 8 : 1;
-  const dim3 block(32 * W, G);
-  const unsigned grid = (unsigned)cdiv(d.rows, G);
-  return rn::with_types(d.type, d.residual ? d.residual_type : rn::kNone, aligned, [&](auto T, auto R, auto M) {
-    constexpr int kT = decltype(T)::value, kR = decltype(R)::value, kM = decltype(M)::value;
+  const int lanes = aligned ? rn::narrow_lanes(d.cols) : 32;
+  return rn::with_types(d.type, d.residual ? d.residual_type : rn::kNone, aligned, lanes, [&](auto T, auto R, auto M, auto L) {
+    constexpr int kT = decltype(T)::value, kR = decltype(R)::value, kM = decltype(M)::value, kL = decltype(L)::value;
     auto go = [&](auto kernel) {
-      kernel<<<grid, block, 0, stream>>>(a);
+      kernel<<<(unsigned)cdiv(d.rows, G * (32 / kL)), dim3(32 * W, G), 0, stream>>>(a);
       return cudaGetLastError();
     };
     auto sized = [&](auto Q) {
       constexpr bool kQ = decltype(Q)::value != 0;
-      if (cpw == 2) return W <= 16 ? go(rn::norm_kernel<kT, kR, kM, kQ, 2, 512, 3>) : go(rn::norm_kernel<kT, kR, kM, kQ, 2, 1024, 1>);
-      return W <= 8 ? go(rn::norm_kernel<kT, kR, kM, kQ, 1, 256, 4>) : go(rn::norm_kernel<kT, kR, kM, kQ, 1, 1024, 1>);
+      if constexpr (kL == 32) {
+        if (cpw == 2)
+          return W <= 16 ? go(rn::norm_kernel<kT, kR, kM, kQ, 2, 32, 512, 3>) : go(rn::norm_kernel<kT, kR, kM, kQ, 2, 32, 1024, 1>);
+      }
+      return go(rn::norm_kernel<kT, kR, kM, kQ, 1, kL, 256, 4>);
     };
     return d.q ? sized(rn::Int<1>{}) : sized(rn::Int<0>{});
   });
@@ -460,36 +516,45 @@ cudaError_t launch_rms_norm_backward(const RmsNormBackwardDesc& d, int* launches
   const int W = rn::back_warps(d.cols);
   int grid = rms_norm_backward_blocks(d.rows, d.cols);
   *launches = d.dweight ? 2 : 1;
-  cudaError_t e = rn::with_types(d.type, d.total_type, aligned, [&](auto T, auto R, auto M) {
-    constexpr int kT = decltype(T)::value, kM = decltype(M)::value;
+  auto fit = [&](int smem) {  // blocks an SM's shared memory holds, each with 10 KB of its own at most
+    grid = (int)std::min<int64_t>(grid, (int64_t)kNumSMsHint * std::max(1, 226 * 1024 / (smem + (W == 1 ? 10 : 2) * 1024)));
+  };
+  const int lanes = aligned ? rn::narrow_lanes(d.cols) : 32;
+  cudaError_t e = rn::with_types(d.type, d.total_type, aligned, lanes, [&](auto T, auto R, auto M, auto L) {
+    constexpr int kT = decltype(T)::value, kM = decltype(M)::value, kL = decltype(L)::value;
     constexpr int kR = decltype(R)::value == rn::kNone ? kT : decltype(R)::value;
     auto go = [&](auto C, auto G, auto N, int threads) {
-      constexpr int kC = decltype(C)::value, kN = decltype(N)::value;
-      constexpr int kS = rn::kStages<kT, kR, kC, kN>;
-      auto kernel = rn::back_kernel<kT, kR, kM, kC, decltype(G)::value, kN>;
-      using Ring = rn::Ring<kT, kR, kC>;
+      constexpr int kC = decltype(C)::value, kN = decltype(N)::value, kG = decltype(G)::value;
+      auto kernel = rn::back_kernel<kT, kR, kM, kC, kL, kG, kN>;
       static PerDevice<bool> attr;  // one for each kernel
       bool set = false;
       cudaError_t r = per_device<bool>(
           attr,
           [&](bool& v) {
-            const cudaError_t x =
-                cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Ring::bytes(kN, kS));
+            const cudaError_t x = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, rn::kMaxRing);
             v = x == cudaSuccess;
             return x;
           },
           &set);
       if (r != cudaSuccess) return r;
-      const int smem = kM == rows::kMap1 ? 0 : Ring::bytes(threads, kS);
-      const int fit = std::max(1, 220 * 1024 / std::max(1, smem + 1024));  // blocks an SM
-      grid = (int)std::min<int64_t>(grid, (int64_t)kNumSMsHint * fit);
+      int smem = rn::Ring<kT, kR, kC>::bytes(threads, rn::kStages<kT, kR, kC, kN>);
+      if (kM == rows::kMap1) {
+        a.stage = rn::covering(d.cols, rows::kSize<kT>) + (d.dtotal ? 2 : 1) * rn::covering(d.cols, rows::kSize<kR>);
+        a.stages = 2 * kG * a.stage * 16 <= rn::kMaxRing ? 2 : 1;
+        smem = a.stages * kG * a.stage * 16;
+      }
+      fit(smem);
+      grid = (int)std::min<int64_t>(grid, cdiv(d.rows, kG * (32 / kL)));
       kernel<<<grid, threads, smem, stream>>>(a);
       return cudaGetLastError();
     };
     if (W == 1) return go(rn::Int<1>{}, rn::Int<rn::kGroups>{}, rn::Int<32 * rn::kGroups>{}, 32 * rn::kGroups);
-    if (d.cols <= 8 * rows::kChunk) return go(rn::Int<1>{}, rn::Int<1>{}, rn::Int<256>{}, 32 * W);
-    if (W <= 16) return go(rn::Int<2>{}, rn::Int<1>{}, rn::Int<512>{}, 32 * W);
-    return go(rn::Int<2>{}, rn::Int<1>{}, rn::Int<1024>{}, 32 * W);
+    if constexpr (kL == 32) {
+      if (d.cols <= 8 * rows::kChunk) return go(rn::Int<1>{}, rn::Int<1>{}, rn::Int<256>{}, 32 * W);
+      if (W <= 16) return go(rn::Int<2>{}, rn::Int<1>{}, rn::Int<512>{}, 32 * W);
+      return go(rn::Int<2>{}, rn::Int<1>{}, rn::Int<1024>{}, 32 * W);
+    }
+    return cudaErrorInvalidValue;  // narrow rows have one warp
   });
   if (e != cudaSuccess || !d.dweight) return e;
   cudaLaunchConfig_t cfg = {};

@@ -3,7 +3,8 @@
 //
 // Which 8 depends on how the rows lie in memory (MAP):
 //   kMap8  rows that are whole 16 bytes and begin on 16, 16-bit numbers: columns 8 lane .. 8 lane + 7, one 16-byte access
-//   kMap4  the same for fp32: columns 4 lane .. + 3 and 128 + 4 lane .. + 3, so that both accesses are whole lines
+//   kMap4  the same for fp32: columns 4 lane .. + 3 and 128 + 4 lane .. + 3, so that both accesses are whole lines; 16-bit rows
+//          beside fp32 ones take two 8-byte accesses for it
 //   kMap1  rows of any width that begin anywhere: columns lane + 32 i, one number an access. A warp's access is then 64 or 128
 //          consecutive bytes; with 8 consecutive numbers a lane it would be 32 pieces of four lines.
 // Every chunk is 256 columns in all of them, so a lane's columns are the same in every row, and the blocks of 128 columns
@@ -82,11 +83,18 @@ struct Chunk {
       }
     } else {
 #pragma unroll
-      for (int h = 0; h < (kWide ? 2 : 1); ++h) {
+      for (int h = 0; h < (kWide || MAP == kMap4 ? 2 : 1); ++h) {
         const int c = c0 + column<MAP>(lane, 4 * h);
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (c < cols) v = *reinterpret_cast<const uint4*>(static_cast<const char*>(row) + (int64_t)c * kSize<TYPE>);
-        w[4 * h] = v.x, w[4 * h + 1] = v.y, w[4 * h + 2] = v.z, w[4 * h + 3] = v.w;
+        const char* p = static_cast<const char*>(row) + (int64_t)c * kSize<TYPE>;
+        if constexpr (!kWide && MAP == kMap4) {
+          uint2 v = make_uint2(0u, 0u);
+          if (c < cols) v = *reinterpret_cast<const uint2*>(p);
+          w[2 * h] = v.x, w[2 * h + 1] = v.y;
+        } else {
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (c < cols) v = *reinterpret_cast<const uint4*>(p);
+          w[4 * h] = v.x, w[4 * h + 1] = v.y, w[4 * h + 2] = v.z, w[4 * h + 3] = v.w;
+        }
       }
     }
   }
@@ -120,28 +128,35 @@ __device__ __forceinline__ void store(void* row, int c0, int cols, int lane, con
     }
   } else {
 #pragma unroll
-    for (int h = 0; h < (kWide ? 2 : 1); ++h) {
+    for (int h = 0; h < (kWide || MAP == kMap4 ? 2 : 1); ++h) {
       const int c = c0 + column<MAP>(lane, 4 * h);
-      uint4 v;
+      char* p = static_cast<char*>(row) + (int64_t)c * kSize<TYPE>;
+      if (c >= cols) continue;
+      const float* g = f + 4 * h;
       if constexpr (kWide)
-        v = make_uint4(__float_as_uint(f[4 * h]), __float_as_uint(f[4 * h + 1]), __float_as_uint(f[4 * h + 2]),
-                       __float_as_uint(f[4 * h + 3]));
+        *reinterpret_cast<float4*>(p) = make_float4(g[0], g[1], g[2], g[3]);
+      else if constexpr (MAP == kMap4)
+        *reinterpret_cast<uint2*>(p) = make_uint2(pack2<TYPE>(g[0], g[1]), pack2<TYPE>(g[2], g[3]));
       else
-        v = make_uint4(pack2<TYPE>(f[0], f[1]), pack2<TYPE>(f[2], f[3]), pack2<TYPE>(f[4], f[5]), pack2<TYPE>(f[6], f[7]));
-      if (c < cols) *reinterpret_cast<uint4*>(static_cast<char*>(row) + (int64_t)c * kSize<TYPE>) = v;
+        *reinterpret_cast<uint4*>(p) = make_uint4(pack2<TYPE>(f[0], f[1]), pack2<TYPE>(f[2], f[3]),
+                                                  pack2<TYPE>(f[4], f[5]), pack2<TYPE>(f[6], f[7]));
     }
   }
 }
 
-// 16 bytes of global memory into shared memory, zeros where there is nothing to read: complete once the group they are
-// committed in is waited for. A thread reads back what it copied itself, so no barrier is needed.
-__device__ __forceinline__ void copy16(uint32_t to, const void* from, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
+// The first n of 16 bytes of global memory into shared memory, zeros behind them: complete once the group they are committed
+// in is waited for.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, int n) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(n) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void copy8(uint32_t to, const void* from, int n) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(from), "r"(n) : "memory");
 }
 
 // Whether a row length or distance of n numbers of this type is whole 16 bytes.

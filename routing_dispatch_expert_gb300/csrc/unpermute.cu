@@ -1,0 +1,271 @@
+// Rows back from expert order to token order, added up with the route weights, and the gradient of that.
+//
+//   y[t] = base[t] + sum_j w[t, j] yd[p[t, j]]                      in slot order, fp32, rounded once
+//   dyd[p[t, j]] = w[t, j] dy[t],   dw[t, j] = <yd[p[t, j]], dy[t]>  fp32
+//
+// Both go token by token, so that the k uses of a token's row meet; the k rows elsewhere are read (and written) once. Bound by
+// HBM: the rows of a chunk are all loaded before any is worked on.
+#include <algorithm>
+#include <type_traits>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "rows.cuh"
+
+namespace moe {
+namespace un {
+
+using std::integral_constant;
+
+// Rows and weights of the slots j0 .. j0 + KB - 1 of token t, in each of its LANES lanes; -1 past the last slot.
+template <int KB, int LANES>
+__device__ __forceinline__ void slots(const int32_t* inv_pos, const float* weights, int64_t t, int64_t T, int k, int j0,
+                                      int (&row)[KB], float (&w)[KB]) {
+  if constexpr (LANES == 32) {
+    const int lane = threadIdx.x & 31;
+    const bool in = lane < KB && j0 + lane < k;
+    const int r = in ? inv_pos[t * k + j0 + lane] : -1;
+    const float v = in && weights ? weights[t * k + j0 + lane] : 1.f;
+#pragma unroll
+    for (int j = 0; j < KB; ++j) {
+      row[j] = __shfl_sync(0xffffffffu, r, j);
+      w[j] = __shfl_sync(0xffffffffu, v, j);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < KB; ++j) {
+      const bool in = t < T && j0 + j < k;
+      row[j] = in ? inv_pos[t * k + j0 + j] : -1;
+      w[j] = in && weights ? weights[t * k + j0 + j] : 1.f;
+    }
+  }
+}
+
+// Blocks of 256 threads an SM holds: the registers of KB rows in flight.
+template <int TYPE, int MAP, int KB>
+constexpr int kBlocks = MAP == rows::kMap1 || (TYPE == MOE_TYPE_F32 && KB == 8) ? 2 : KB == 8 || TYPE == MOE_TYPE_F32 ? 3 : 4;
+
+struct AddArgs {
+  const void* yd;
+  const void* base;      // or nullptr
+  const float* weights;  // [T, k] or nullptr
+  const int32_t* inv_pos;
+  void* y;
+  int64_t T;
+  int cols, chunks, k;
+  int piece, pieces;  // chunks of a warp's work, and those works of a row
+};
+
+// A warp a piece of a token's row, or LANES lanes a whole narrow row: fp32, the base first and then the slots in order. KB: slots at
+// a time, a power of two at or above k, at most 8.
+template <int TYPE, int MAP, int KB, int LANES>
+__global__ void __launch_bounds__(256, (kBlocks<TYPE, MAP, KB>)) unpermute_kernel(const AddArgs a) {
+  constexpr int kTokens = 32 / LANES;
+  const int lane = threadIdx.x & 31, sub = lane % LANES;
+  const int64_t warps = ((int64_t)gridDim.x * blockDim.x) >> 5;
+  const int64_t items = LANES == 32 ? a.T * a.pieces : cdiv(a.T, kTokens);
+  const int64_t pitch = (int64_t)a.cols * rows::kSize<TYPE>;
+  for (int64_t it = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; it < items; it += warps) {
+    const int64_t t = LANES == 32 ? it / a.pieces : it * kTokens + lane / LANES;
+    const int first = LANES == 32 ? (int)(it - t * a.pieces) * a.piece : 0;
+    const int last = LANES == 32 ? min(a.chunks, first + a.piece) : 1;
+    const int cols = t < a.T ? a.cols : 0;
+    int row[KB];
+    float w[KB];
+    slots<KB, LANES>(a.inv_pos, a.weights, t, a.T, a.k, 0, row, w);
+    for (int c = first; c < last; ++c) {
+      const int c0 = c * rows::kChunk;
+      float sum[8];
+      for (int j0 = 0; j0 < a.k; j0 += KB) {
+        if (KB == 8 && a.k > KB) slots<KB, LANES>(a.inv_pos, a.weights, t, a.T, a.k, j0, row, w);
+        rows::Chunk<TYPE, MAP> b, v[KB];
+        if (j0 == 0) {
+          if (a.base)
+            b.load(static_cast<const char*>(a.base) + t * pitch, c0, cols, sub);
+          else
+            b.clear();
+        }
+#pragma unroll
+        for (int j = 0; j < KB; ++j)
+          if (row[j] >= 0) v[j].load(static_cast<const char*>(a.yd) + row[j] * pitch, c0, cols, sub);
+        if (j0 == 0) b.values(sum);
+#pragma unroll
+        for (int j = 0; j < KB; ++j) {
+          if (row[j] < 0) continue;
+          float f[8];
+          v[j].values(f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sum[i] = fmaf(w[j], f[i], sum[i]);
+        }
+        if (KB < 8) break;  // k is at most KB
+      }
+      rows::store<TYPE, MAP>(static_cast<char*>(a.y) + t * pitch, c0, cols, sub, sum);
+    }
+  }
+}
+
+struct SpreadArgs {
+  const void* dy;
+  const void* yd;        // or nullptr: no gradient of the weights
+  const float* weights;  // [T, k] or nullptr
+  const int32_t* inv_pos;
+  const int32_t* held_at;
+  void* dyd;
+  float* dweights;  // [T, k] or nullptr
+  int64_t T;
+  int cols, chunks, k;
+};
+
+// A group of W warps a token (blockDim.x / 32, blockDim.y groups a block where W is 1), or LANES lanes a narrow row: its row of dy to
+// its k rows of dyd, and their products with yd's rows, summed over the lanes and then the warps. At the end the warps clear
+// the rows that hold nothing.
+template <int TYPE, int MAP, int KB, int LANES>
+__global__ void __launch_bounds__(256, (kBlocks<TYPE, MAP, KB>)) spread_kernel(const SpreadArgs a) {
+  constexpr int kTokens = 32 / LANES;
+  __shared__ float part[8][KB];
+  const int lane = threadIdx.x & 31, sub = lane % LANES, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
+  const int64_t pitch = (int64_t)a.cols * rows::kSize<TYPE>;
+  const int64_t group = (int64_t)blockIdx.x * blockDim.y + threadIdx.y, groups = (int64_t)gridDim.x * blockDim.y;
+  float f[8];
+  for (int64_t g0 = group * kTokens; g0 < a.T; g0 += groups * kTokens) {
+    const int64_t t = g0 + lane / LANES;
+    const int cols = t < a.T ? a.cols : 0;
+    for (int j0 = 0; j0 < a.k; j0 += KB) {
+      int row[KB];
+      float w[KB], dot[KB];
+      slots<KB, LANES>(a.inv_pos, a.weights, t, a.T, a.k, j0, row, w);
+#pragma unroll
+      for (int j = 0; j < KB; ++j) dot[j] = 0.f;
+      for (int c = warp; c < a.chunks; c += W) {
+        const int c0 = c * rows::kChunk;
+        rows::Chunk<TYPE, MAP> dy, v[KB];
+        dy.load(static_cast<const char*>(a.dy) + t * pitch, c0, cols, sub);
+        if (a.yd) {
+#pragma unroll
+          for (int j = 0; j < KB; ++j)
+            if (row[j] >= 0) v[j].load(static_cast<const char*>(a.yd) + row[j] * pitch, c0, cols, sub);
+        }
+        float g[8];
+        dy.values(g);
+#pragma unroll
+        for (int j = 0; j < KB; ++j) {
+          if (row[j] < 0) continue;
+          if (a.yd) {
+            v[j].values(f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dot[j] = fmaf(g[i], f[i], dot[j]);
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[i] = w[j] * g[i];
+          rows::store<TYPE, MAP>(static_cast<char*>(a.dyd) + row[j] * pitch, c0, cols, sub, f);
+        }
+      }
+      if (!a.dweights) continue;
+      float mine = 0.f;
+#pragma unroll
+      for (int j = 0; j < KB; ++j) {
+#pragma unroll
+        for (int o = LANES / 2; o > 0; o >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], o);
+        if (sub == j) mine = dot[j];
+      }
+      if (W == 1) {
+        if (t < a.T && sub < KB && j0 + sub < a.k) a.dweights[t * a.k + j0 + sub] = mine;
+        continue;
+      }
+      if (lane < KB) part[warp][lane] = mine;
+      __syncthreads();
+      if (threadIdx.x < KB && j0 + threadIdx.x < a.k) {
+        float sum = 0.f;
+        for (int i = 0; i < W; ++i) sum += part[i][threadIdx.x];
+        a.dweights[t * a.k + j0 + threadIdx.x] = sum;
+      }
+      __syncthreads();
+    }
+  }
+  const int64_t held = *a.held_at;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = 0.f;
+  for (int64_t r = held + group; r < a.T * a.k; r += groups)
+    for (int c = warp; c < a.chunks; c += W)
+      rows::store<TYPE, MAP>(static_cast<char*>(a.dyd) + r * pitch, c * rows::kChunk, a.cols, lane, f);
+}
+
+// f(type, map, slots at a time, lanes of a row). Rows of up to 64 and 128 columns of whole 16 bytes take 8 and 16 lanes.
+template <class F>
+cudaError_t with_rows(int type, int64_t cols, int k, F&& f) {
+  const bool whole = rows::whole(type, cols);
+  auto typed = [&](auto T) {
+    constexpr int kT = decltype(T)::value;
+    constexpr int kAligned = kT == MOE_TYPE_F32 ? rows::kMap4 : rows::kMap8;
+    using One = integral_constant<int, rows::kMap1>;
+    using Whole = integral_constant<int, kAligned>;
+    using Eight = integral_constant<int, rows::kMap8>;  // narrow rows: 8 columns a lane whatever the type
+    integral_constant<int, 2> two;
+    integral_constant<int, 4> four;
+    integral_constant<int, 8> eight;
+    integral_constant<int, 16> sixteen;
+    integral_constant<int, 32> all;
+    if (!whole) return k <= 2 ? f(T, One{}, two, all) : f(T, One{}, eight, all);
+    if (cols <= 64 && cols % 8 == 0) return k <= 2 ? f(T, Eight{}, two, eight) : f(T, Eight{}, eight, eight);
+    if (cols <= 128 && cols % 8 == 0) return k <= 2 ? f(T, Eight{}, two, sixteen) : f(T, Eight{}, eight, sixteen);
+    return k <= 2 ? f(T, Whole{}, two, all) : k <= 4 ? f(T, Whole{}, four, all) : f(T, Whole{}, eight, all);
+  };
+  if (type == MOE_TYPE_F32) return typed(integral_constant<int, MOE_TYPE_F32>{});
+  if (type == MOE_TYPE_BF16) return typed(integral_constant<int, MOE_TYPE_BF16>{});
+  return typed(integral_constant<int, MOE_TYPE_F16>{});
+}
+
+}  // namespace un
+
+cudaError_t launch_unpermute(const UnpermuteDesc& d, cudaStream_t stream) {
+  un::AddArgs a;
+  a.yd = d.yd;
+  a.base = d.base;
+  a.weights = d.weights;
+  a.inv_pos = d.inv_pos;
+  a.y = d.y;
+  a.T = d.T;
+  a.cols = d.cols;
+  a.chunks = (int)cdiv(d.cols, rows::kChunk);
+  a.k = d.k;
+  // a warp's work: up to 16 chunks of a row, fewer where there would be less than 32 works an SM (7168 columns of 16384
+  // tokens: 339 us with 14 chunks, 343 with 7 or 4, 480 with one, whose rows' numbers are then looked up for every chunk)
+  const int64_t pieces = std::max<int64_t>(cdiv(a.chunks, 16), std::min<int64_t>(a.chunks, cdiv(32 * num_sms(), a.T)));
+  a.piece = (int)cdiv(a.chunks, pieces);
+  a.pieces = (int)cdiv(a.chunks, a.piece);
+  return un::with_rows(d.type, d.cols, d.k, [&](auto T, auto M, auto K, auto L) {
+    constexpr int kL = decltype(L)::value;
+    const int64_t items = kL == 32 ? a.T * a.pieces : cdiv(a.T, 32 / kL);
+    const unsigned blocks = (unsigned)std::min<int64_t>(cdiv(items, 8), (int64_t)num_sms() * 16);
+    un::unpermute_kernel<decltype(T)::value, decltype(M)::value, decltype(K)::value, kL><<<blocks, 256, 0, stream>>>(a);
+    return cudaGetLastError();
+  });
+}
+
+cudaError_t launch_unpermute_backward(const UnpermuteBackwardDesc& d, cudaStream_t stream) {
+  un::SpreadArgs a;
+  a.dy = d.dy;
+  a.yd = d.dweights ? d.yd : nullptr;
+  a.weights = d.weights;
+  a.inv_pos = d.inv_pos;
+  a.held_at = d.held;
+  a.dyd = d.dyd;
+  a.dweights = d.dweights;
+  a.T = d.T;
+  a.cols = d.cols;
+  a.chunks = (int)cdiv(d.cols, rows::kChunk);
+  a.k = d.k;
+  // warps of a token: four, up to eight where few tokens would leave SMs idle (16384 tokens of 7168 columns: 600 us with four
+  // or two, 637 with eight: every token ends in a barrier and a sum over the warps)
+  const int64_t most = std::min<int64_t>(8, std::max<int64_t>(4, cdiv(24 * num_sms(), a.T)));
+  const int W = (int)cdiv(a.chunks, cdiv(a.chunks, most)), G = W == 1 ? 8 : 1;
+  return un::with_rows(d.type, d.cols, d.k, [&](auto T, auto M, auto K, auto L) {
+    constexpr int kL = decltype(L)::value;
+    const unsigned blocks = (unsigned)std::min<int64_t>(cdiv(a.T, G * (32 / kL)), (int64_t)num_sms() * 64 / (W * G));
+    un::spread_kernel<decltype(T)::value, decltype(M)::value, decltype(K)::value, kL>
+        <<<blocks, dim3(32 * W, G), 0, stream>>>(a);
+    return cudaGetLastError();
+  });
+}
+
+}  // namespace moe

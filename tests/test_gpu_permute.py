@@ -122,7 +122,7 @@ def test_sort_agrees_with_dispatch():
 # rows
 # ------------------------------------------------------------------------------------------
 SHAPES = [(1, 4, 1), (77, 8, 2), (300, 33, 8), (130, 40, 17), (20, 64, 32)]
-WIDTHS = [1, 2, 3, 8, 33, 64, 255, 256, 1003, 4096, 4104]
+WIDTHS = [1, 2, 3, 8, 24, 33, 64, 72, 128, 255, 256, 1003, 4096, 4104]
 
 
 def sorted_batch(T, E, k, pad=0.15, factor=1.25):

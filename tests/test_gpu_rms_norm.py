@@ -17,7 +17,7 @@ from routing_dispatch_expert_gb300 import build as pkg_build
 pytestmark = pytest.mark.gpu
 F32, BF16, F16 = torch.float32, torch.bfloat16, torch.float16
 EPS = 1e-5
-COLS = [1, 7, 8, 64, 129, 255, 256, 257, 1000, 2048, 2049, 2304, 4101, 7168, 8192, 8200, 16383, 16384]
+COLS = [1, 7, 8, 24, 40, 64, 72, 128, 129, 136, 255, 256, 257, 1000, 2048, 2049, 2304, 4101, 7168, 8192, 8200, 16383, 16384]
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -168,7 +168,8 @@ def test_gradient(cols, kind):
 
 def test_gradient_of_many_rows():
     gen = torch.Generator(device="cuda").manual_seed(5)
-    for n, cols, kind in ((20001, 64, F32), (70000, 8, BF16), (5003, 520, F16), (3000, 7168, BF16)):
+    for n, cols, kind in ((20001, 64, F32), (70000, 8, BF16), (70001, 33, BF16), (30011, 128, F16), (5003, 520, F16), (3000, 7168, BF16),
+                          (2001, 4101, F32), (2001, 2051, BF16)):
         dy, t, w = rows(gen, n, cols, kind), rows(gen, n, cols, kind), torch.randn(cols, generator=gen, device="cuda")
         got = rde.rms_norm_backward(dy, t, w, EPS)
         check_gradient(dy, t, w, None, got)
