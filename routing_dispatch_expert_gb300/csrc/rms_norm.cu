@@ -202,7 +202,7 @@ struct Ring {
   static constexpr int bytes(int threads, int stages) { return 16 * kWords * threads * stages; }
 };
 
-constexpr int kMaxRing = 216 * 1024;  // bytes of a block's stages, at most
+constexpr int kMaxRing = 208 * 1024;  // bytes of a block's stages, at most
 
 // Rows in flight a thread: two, or one where two would not fit (wide fp32 rows).
 template <int TYPE, int TT, int CPW, int THREADS>
@@ -216,7 +216,7 @@ __host__ __device__ __forceinline__ int covering(int cols, int size) { return (c
 // registers, while later rows are copied into shared memory. One row at a time by all warps of a block, or, with GROUPS > 1, a
 // row by each warp, or 32 / LANES narrow ones.
 template <int TYPE, int TT, int MAP, int CPW, int LANES, int GROUPS, int THREADS>
-__global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 4 : THREADS == 512 ? 2 : 1) back_kernel(const BackArgs a) {
+__global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 4 : THREADS <= 512 ? 2 : 1) back_kernel(const BackArgs a) {
   extern __shared__ uint4 ring[];
   __shared__ float2 part[2][32];
   __shared__ float dw_part[GROUPS > 1 ? GROUPS : 1][GROUPS > 1 ? kChunk : 1];
@@ -397,8 +397,10 @@ __global__ void __launch_bounds__(1024) dweight_kernel(const float* part, int n,
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // it is launched beside the other kernel's end
   float sum = 0.f;
-  if (c < cols)
+  if (c < cols) {
+#pragma unroll 8
     for (int b = warp; b < n; b += 32) sum += part[(int64_t)b * cols + c];
+  }
   sums[warp][lane] = sum;
   __syncthreads();
   sum = lanes_sum(sums[lane][warp]);
@@ -483,10 +485,9 @@ cudaError_t launch_rms_norm(const RmsNormDesc& d, cudaStream_t stream) {
 
 namespace rn {
 
-int back_warps(int cols) {
-  const int chunks = (int)cdiv(cols, rows::kChunk);
-  return chunks > 8 ? (int)cdiv(chunks, 2) : chunks;
-}
+// Chunks of a warp, and warps of a row (2048 columns: 83 us with two chunks, 88 with one; 512 columns: 63 and 53).
+int back_chunks(int cols) { return cols > 4 * rows::kChunk ? 2 : 1; }
+int back_warps(int cols) { return (int)cdiv(cdiv(cols, rows::kChunk), back_chunks(cols)); }
 
 }  // namespace rn
 
@@ -548,9 +549,11 @@ cudaError_t launch_rms_norm_backward(const RmsNormBackwardDesc& d, int* launches
       kernel<<<grid, threads, smem, stream>>>(a);
       return cudaGetLastError();
     };
-    if (W == 1) return go(rn::Int<1>{}, rn::Int<rn::kGroups>{}, rn::Int<32 * rn::kGroups>{}, 32 * rn::kGroups);
+    if (d.cols <= rows::kChunk) return go(rn::Int<1>{}, rn::Int<rn::kGroups>{}, rn::Int<32 * rn::kGroups>{}, 32 * rn::kGroups);
     if constexpr (kL == 32) {
-      if (d.cols <= 8 * rows::kChunk) return go(rn::Int<1>{}, rn::Int<1>{}, rn::Int<256>{}, 32 * W);
+      if (rn::back_chunks(d.cols) == 1) return go(rn::Int<1>{}, rn::Int<1>{}, rn::Int<256>{}, 32 * W);
+      if (W <= 8) return go(rn::Int<2>{}, rn::Int<1>{}, rn::Int<256>{}, 32 * W);
+      if (W <= 14) return go(rn::Int<2>{}, rn::Int<1>{}, rn::Int<448>{}, 32 * W);
       if (W <= 16) return go(rn::Int<2>{}, rn::Int<1>{}, rn::Int<512>{}, 32 * W);
       return go(rn::Int<2>{}, rn::Int<1>{}, rn::Int<1024>{}, 32 * W);
     }

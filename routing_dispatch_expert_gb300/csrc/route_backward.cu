@@ -19,13 +19,21 @@
 #include "kernels.h"
 #include "rows.cuh"
 
-#ifndef RB_G
-#define RB_G 64
-#endif
 namespace moe {
 namespace rb {
 
 constexpr int kThreads = 256;
+constexpr int kMaxE = 1024;
+constexpr float kLog2e = 1.4426950408889634f;
+
+// 2 ulp. A probability e^(l - m) is taken as 2^(log2(e) (l - m)): the product's rounding is |x| 2^-24 of an exponent x, that is
+// below 2e-6 of a probability of 1e-8, and less of larger ones.
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float exponential(float x) { return ex2(x * kLog2e); }
 
 struct Args {
   const void* logits;
@@ -50,24 +58,28 @@ __device__ __forceinline__ float lanes_max(float v) {
   return v;
 }
 
-// One slot of a token: its expert (-1: none), the gradient of its weight, and its logit.
+// One slot of a token: its expert (-1: none) and the gradient of its weight (asked for together), then its logit.
+__device__ __forceinline__ void ask_slot(const Args& a, int64_t t, int j, int& e, float& g) {
+  const bool in = t < a.T && j < a.k;
+  e = in ? a.idx[t * a.k + j] : -1;
+  g = in ? a.dw[t * a.k + j] : 0.f;
+}
 template <int TYPE>
-__device__ __forceinline__ void load_slot(const Args& a, int64_t t, int j, int& e, float& g, float& l) {
+__device__ __forceinline__ float slot_logit(const Args& a, int64_t t, int& e, float& g) {
+  if (e >= 0 && e < a.E) return rows::value<TYPE>(rows::load_bits<TYPE>(a.logits, t * a.E + e));
   e = -1;
   g = 0.f;
-  l = -INFINITY;
-  if (t >= a.T || j >= a.k) return;
-  const int c = a.idx[t * a.k + j];
-  if (c < 0 || c >= a.E) return;
-  e = c;
-  g = a.dw[t * a.k + j];
-  l = rows::value<TYPE>(rows::load_bits<TYPE>(a.logits, t * a.E + e));
+  return -INFINITY;
 }
 
 // The gradients of the slots that chose this lane's expert, and how many they are: an expert chosen twice gets both, and each
 // of its slots writes the same sum.
 template <int L>
 __device__ __forceinline__ void same_expert(int k, int e, float g, float& all, float& n) {
+  all = g;
+  n = 1.f;
+  const uint32_t peers = __match_any_sync(0xffffffffu, e < 0 ? -1 : e + (int)((threadIdx.x & 31) / L) * kMaxE);
+  if (!__any_sync(0xffffffffu, e >= 0 && __popc(peers) > 1)) return;
   all = n = 0.f;
   for (int j = 0; j < k; ++j) {
     const int ej = __shfl_sync(0xffffffffu, e, j, L);
@@ -90,8 +102,8 @@ __global__ void __launch_bounds__(kThreads) chosen_kernel(const Args a) {
   for (int64_t t0 = (((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5) * kPer; t0 < a.T; t0 += warps * kPer) {
     const int64_t t = t0 + lane / L;
     int e;
-    float g, l;
-    load_slot<TYPE>(a, t, sub, e, g, l);
+    float g;
+    ask_slot(a, t, sub, e, g);
     char* out = static_cast<char*>(a.dlogits) + t0 * a.E * rows::kSize<TYPE>;
     if ((bytes & 15) == 0 && t0 + kPer <= a.T) {
       for (int64_t b = 16 * lane; b < bytes; b += 512) *reinterpret_cast<uint4*>(out + b) = make_uint4(0u, 0u, 0u, 0u);
@@ -99,11 +111,12 @@ __global__ void __launch_bounds__(kThreads) chosen_kernel(const Args a) {
       const int64_t n = min((int64_t)kPer, a.T - t0) * a.E;
       for (int64_t i = lane; i < n; i += 32) rows::store_bits<TYPE>(out, i, 0u);
     }
+    const float l = slot_logit<TYPE>(a, t, e, g);
     float u, slope = 1.f, all, n;
     if (!SIGMOID) {
       float m = lanes_max<L>(l);
       if (m == -INFINITY) m = 0.f;
-      u = expf(l - m);
+      u = exponential(l - m);
     } else {
       // sigmoid(l) e^-c = 1 / (e^c + e^(c - l)) with c = min(max l, 0)
       float c = 0.f;
@@ -111,8 +124,8 @@ __global__ void __launch_bounds__(kThreads) chosen_kernel(const Args a) {
         const float m = lanes_max<L>(l);
         c = m == -INFINITY ? 0.f : fminf(m, 0.f);
       }
-      u = e < 0 ? 0.f : __fdividef(1.0f, expf(c) + expf(c - l));
-      slope = __fdividef(1.0f, 1.0f + expf(l));
+      u = e < 0 ? 0.f : __fdividef(1.0f, exponential(c) + exponential(c - l));
+      slope = __fdividef(1.0f, 1.0f + exponential(l));
     }
     same_expert<L>(a.k, e, g, all, n);
     if (a.renorm) {  // a softmax over the chosen, or sigmoids divided by their sum
@@ -137,9 +150,8 @@ __global__ void __launch_bounds__(kThreads) dense_kernel(const Args a) {
     const int64_t t = t0 + lane / L;
     const bool in = t < a.T;
     int e;
-    float g, l;
-    load_slot<TYPE>(a, t, sub, e, g, l);
-    float p[EPL], m = -INFINITY;
+    float g, p[EPL], m = -INFINITY;
+    ask_slot(a, t, sub, e, g);
 #pragma unroll
     for (int j = 0; j < EPL / 4; ++j) {
       const int at = 4 * (sub + L * j);
@@ -157,6 +169,7 @@ __global__ void __launch_bounds__(kThreads) dense_kernel(const Args a) {
           p[4 * j + i] = in && at + i < a.E ? rows::value<TYPE>(rows::load_bits<TYPE>(a.logits, t * a.E + at + i)) : -INFINITY;
       }
     }
+    const float l = slot_logit<TYPE>(a, t, e, g);
 #pragma unroll
     for (int j = 0; j < EPL; ++j) m = fmaxf(m, p[j]);
     m = lanes_max<L>(m);
@@ -164,12 +177,12 @@ __global__ void __launch_bounds__(kThreads) dense_kernel(const Args a) {
     float z = 0.f, all, n;
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
-      p[j] = expf(p[j] - m);
+      p[j] = exponential(p[j] - m);
       z += p[j];
     }
     z = lanes_sum<L>(z);
     const float r = z == 0.f ? 0.f : __fdiv_rn(1.0f, z);
-    const float u = expf(l - m) * r;
+    const float u = exponential(l - m) * r;
     const float dot = lanes_sum<L>(g * u);
     same_expert<L>(a.k, e, g, all, n);
     if (in) {
@@ -226,7 +239,7 @@ cudaError_t launch_route_backward(const RouteBackwardDesc& d, cudaStream_t strea
   a.renorm = d.renorm;
   a.scale = d.routed_scale;
   auto go = [&](auto kernel, int per_warp) {
-    const int64_t blocks = std::min<int64_t>(cdiv(d.T, (rb::kThreads / 32) * per_warp), (int64_t)num_sms() * RB_G);
+    const int64_t blocks = std::min<int64_t>(cdiv(d.T, (rb::kThreads / 32) * per_warp), (int64_t)num_sms() * 64);
     kernel<<<(unsigned)blocks, rb::kThreads, 0, stream>>>(a);
     return cudaGetLastError();
   };
