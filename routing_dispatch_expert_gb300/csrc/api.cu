@@ -1301,7 +1301,8 @@ namespace {
 
 // the counts and offsets of the rows are those of the layer's experts (slots)
 size_t sort_bytes(const moe_config* c) {
-  return align256(sizeof(int32_t) * (size_t)moe::sort_blocks((int64_t)c->T * c->k) * c->E);
+  const int blocks = moe::sort_blocks((int64_t)c->T * c->k);
+  return blocks > 1 ? align256(sizeof(int32_t) * (size_t)blocks * c->E) : 0;  // one block counts for itself
 }
 
 int check_rows(const moe_config* cfg, int64_t cols) {
@@ -1336,7 +1337,7 @@ MOE_EXPORT int moe_sort_tokens(const moe_config* cfg, const int32_t* topk_idx, c
     REQUIRE_PTR(row_token, "row_token");
     REQUIRE_ALIGNED(topk_w, "topk_w");
     REQUIRE_ALIGNED(row_weight, "row_weight");
-    REQUIRE_PTR(ws, "ws");
+    if (sort_bytes(cfg) > 0) REQUIRE_PTR(ws, "ws");
     if (ws_bytes < sort_bytes(cfg)) return fail(MOE_ERR_WORKSPACE, "workspace of the sort too small");
   }
   moe::SortDesc d;

@@ -91,6 +91,7 @@ __global__ void __launch_bounds__(kThreads) rank_kernel(const SortArgs a) {
   int32_t* offset = all + E;
   const int64_t lo = blockIdx.x * a.per_block, hi = min(a.n, lo + a.per_block);
   int held = 0;
+  const int bits = 32 - __clz(E);  // of 0 .. E
   for (int64_t c0 = lo; c0 < hi; c0 += kEach * kThreads) {
     const int64_t at = c0 + warp * 32 * kEach + lane;
     int mine[kEach], rank[kEach];
@@ -110,7 +111,13 @@ __global__ void __launch_bounds__(kThreads) rank_kernel(const SortArgs a) {
 #pragma unroll
     for (int j = 0; j < kEach; ++j) {  // the first lane of an expert counts for all of its lanes
       const int e = mine[j];
-      const uint32_t peers = __match_any_sync(0xffffffffu, e), before = peers & ((1u << lane) - 1u);
+      uint32_t peers = 0xffffffffu;  // the lanes that hold the same expert: bit by bit
+      for (int b = 0; b < bits; ++b) {
+        const bool set = (unsigned)(e < 0 ? E : e) >> b & 1u;
+        const uint32_t with = __ballot_sync(0xffffffffu, set);
+        peers &= set ? with : ~with;
+      }
+      const uint32_t before = peers & ((1u << lane) - 1u);
       int32_t* c = cnt + warp * E + max(e, 0);
       const int had = *c;
       __syncwarp();

@@ -495,8 +495,9 @@ int back_warps(int cols) { return (int)cdiv(cdiv(cols, rows::kChunk), back_chunk
 // one row.
 int rms_norm_backward_blocks(int64_t rows, int cols) {
   const int W = rn::back_warps(cols), G = W == 1 ? rn::kGroups : 1;
-  const int per_sm = W * G <= 8 ? 32 / (W * G) : W <= 16 ? 2 : 1;
-  return (int)std::max<int64_t>(1, std::min<int64_t>(cdiv(rows, G), (int64_t)kNumSMsHint * per_sm));
+  const int per_sm = W * G <= 8 ? 32 / (W * G) : W <= 14 ? 28 / W : W <= 16 ? 2 : 1;
+  const int64_t few = cdiv(cdiv(rows, G), (int64_t)kNumSMsHint * 4);  // so that a block has several rows to add up
+  return (int)std::max<int64_t>(1, std::min<int64_t>(cdiv(rows, G), kNumSMsHint * std::min<int64_t>(per_sm, few)));
 }
 
 cudaError_t launch_rms_norm_backward(const RmsNormBackwardDesc& d, int* launches, cudaStream_t stream) {
@@ -551,6 +552,10 @@ cudaError_t launch_rms_norm_backward(const RmsNormBackwardDesc& d, int* launches
     };
     if (d.cols <= rows::kChunk) return go(rn::Int<1>{}, rn::Int<rn::kGroups>{}, rn::Int<32 * rn::kGroups>{}, 32 * rn::kGroups);
     if constexpr (kL == 32) {
+      // odd rows so wide that an SM holds one block of them: one chunk a warp, for twice the warps
+      if (kM == rows::kMap1 && d.cols > 4 * rows::kChunk && d.cols <= 32 * rows::kChunk &&
+          2 * (rn::covering(d.cols, rows::kSize<kT>) + (d.dtotal ? 2 : 1) * rn::covering(d.cols, rows::kSize<kR>)) * 16 > 110 * 1024)
+        return go(rn::Int<1>{}, rn::Int<1>{}, rn::Int<1024>{}, 32 * (int)cdiv(d.cols, rows::kChunk));
       if (rn::back_chunks(d.cols) == 1) return go(rn::Int<1>{}, rn::Int<1>{}, rn::Int<256>{}, 32 * W);
       if (W <= 8) return go(rn::Int<2>{}, rn::Int<1>{}, rn::Int<256>{}, 32 * W);
       if (W <= 14) return go(rn::Int<2>{}, rn::Int<1>{}, rn::Int<448>{}, 32 * W);

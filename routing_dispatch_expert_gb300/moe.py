@@ -7,6 +7,7 @@ There is no fallback: if the library is not built, loading it raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -578,8 +579,9 @@ def _gradient(t):
     return t.clone(memory_format=torch.contiguous_format)
 
 
-def _wants_gradient(*tensors):
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+def _wants_gradient(a, b=None, c=None):
+    return (getattr(a, "requires_grad", False) or getattr(b, "requires_grad", False)
+            or getattr(c, "requires_grad", False)) and torch.is_grad_enabled()
 
 
 def _row_matrix(t, name, dtypes, shape=(None, None)):
@@ -700,16 +702,25 @@ def rms_norm_backward(dy, total, weight=None, eps: float = 1e-6, dtotal=None, we
     return dx, dresidual, dweight
 
 
-def rms_norm_backward_workspace(rows: int, cols: int, device="cuda") -> torch.Tensor:
+@functools.lru_cache(maxsize=256)
+def _rms_norm_backward_bytes(rows, cols):
     n = ctypes.c_size_t()
     _check((_lib or load()).moe_rms_norm_backward_workspace_size(rows, cols, ctypes.byref(n)))
-    return torch.empty(n.value, dtype=_u8, device=device)
+    return n.value
+
+
+def rms_norm_backward_workspace(rows: int, cols: int, device="cuda") -> torch.Tensor:
+    return torch.empty(_rms_norm_backward_bytes(rows, cols), dtype=_u8, device=device)
+
+
+def _sort_tokens_bytes(cfg):
+    n = ctypes.c_size_t()
+    _check((_lib or load()).moe_sort_tokens_workspace_size(ctypes.byref(cfg), ctypes.byref(n)))
+    return n.value
 
 
 def sort_tokens_workspace(cfg: MoeConfig, device="cuda") -> torch.Tensor:
-    n = ctypes.c_size_t()
-    _check((_lib or load()).moe_sort_tokens_workspace_size(ctypes.byref(cfg), ctypes.byref(n)))
-    return torch.empty(n.value, dtype=_u8, device=device)
+    return torch.empty(_sort_tokens_bytes(cfg), dtype=_u8, device=device)
 
 
 def _groups(cfg):
@@ -727,17 +738,19 @@ def sort_tokens(cfg, topk_idx, topk_w=None, ws=None) -> dict:
         _need(topk_w, "topk_w", _f32, (T, k))
     dev, n = topk_idx.device, _groups(cfg)
     if ws is None:
-        ws = sort_tokens_workspace(cfg, dev)
+        size = _sort_tokens_bytes(cfg)
+        if size:
+            ws = torch.empty(size, dtype=_u8, device=dev)
     elif not _like(ws, _u8, (ws.numel(),)):
         _need(ws, "ws", _u8, (None,))
     out = {"counts": torch.empty(n, dtype=_i32, device=dev), "offsets": torch.empty(n + 1, dtype=_i32, device=dev),
-           "inv_pos": torch.empty(T, k, dtype=_i32, device=dev), "row_token": torch.empty(T * k, dtype=_i32, device=dev)}
+           "inv_pos": torch.empty_like(topk_idx), "row_token": torch.empty(T * k, dtype=_i32, device=dev)}
     if topk_w is not None:
         out["row_weight"] = torch.empty(T * k, dtype=_f32, device=dev)
     _check((_lib or load()).moe_sort_tokens(
         ctypes.byref(cfg), topk_idx.data_ptr(), _address(topk_w), out["counts"].data_ptr(), out["offsets"].data_ptr(),
-        out["inv_pos"].data_ptr(), out["row_token"].data_ptr(), _address(out.get("row_weight")), ws.data_ptr(),
-        ws.numel(), _here(topk_idx, topk_w, ws)))
+        out["inv_pos"].data_ptr(), out["row_token"].data_ptr(), _address(out.get("row_weight")), _address(ws),
+        0 if ws is None else ws.numel(), _here(topk_idx, topk_w, ws)))
     return out
 
 

@@ -243,7 +243,7 @@ def test_no_tokens_and_refusals():
         with pytest.raises(ValueError, match=text):
             call()
     with pytest.raises(rde.MoeError, match="too small"):
-        rde.sort_tokens(cfg, s["inv_pos"], ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        rde.sort_tokens(config(3000, 4, 2), choices(3000, 4, 2), ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(rde.MoeError, match="16-byte aligned"):
         rde.permute(config(1, 4, 2), torch.zeros(17, device="cuda")[1:].view(1, 16), s["inv_pos"][:1].clone(), s["offsets"])
 

@@ -70,7 +70,7 @@ def test_norm_gradient_refusals(lib, change, code, text):
 ])
 def test_sort_refusals(lib, change, code, text):
     a = {**dict(idx=P, w=P, counts=P, off=P, inv=P, tok=P, rw=P, ws=P, bytes=BIG), **change}
-    _refused(lib, lib.moe_sort_tokens(ctypes.byref(_cfg()), a["idx"], a["w"], a["counts"], a["off"], a["inv"], a["tok"],
+    _refused(lib, lib.moe_sort_tokens(ctypes.byref(_cfg(T=5000)), a["idx"], a["w"], a["counts"], a["off"], a["inv"], a["tok"],
                                       a["rw"], a["ws"], a["bytes"], None), code, text)
 
 
@@ -130,7 +130,7 @@ def test_workspaces(lib):
     for T, E, k in ((1, 8, 2), (70000, 256, 8), (1 << 20, 1024, 8)):  # a count of each expert for each block of assignments
         assert lib.moe_sort_tokens_workspace_size(ctypes.byref(_cfg(T=T, E=E, k=k)), ctypes.byref(n)) == 0
         blocks = -(-T * k // max(2048, -(-T * k // 128 // 2048) * 2048))
-        assert 4 * blocks * E <= n.value <= 4 * 129 * E
+        assert (n.value == 0) if blocks == 1 else 4 * blocks * E <= n.value <= 4 * 129 * E
     for rows, cols in ((0, 5), (1, 16384), (100000, 7168), (100000, 3)):
         assert lib.moe_rms_norm_backward_workspace_size(rows, cols, ctypes.byref(n)) == 0
         assert n.value >= 4 * cols and n.value <= 4 * 152 * 32 * cols + 256
