@@ -563,12 +563,18 @@ def balance_loss_backward(cfg, logits, counts, tokens, alpha: float, dloss, seq_
 # ------------------------------------------------------------------------------------------
 # around the experts: the norm in front, rows sorted by expert and back, and the gradients
 # ------------------------------------------------------------------------------------------
-def _here(*tensors):
+# As above, the calls below look at their tensors in as few steps as they can and find the words of a refusal only after
+# one failed; outputs are made like an input where there is one of their shape (two thirds of the time of a call on small
+# tensors is three allocations and a launch).
+_empty, _empty_like = torch.empty, torch.empty_like
+
+
+def _here(a, b=None, c=None, d=None, e=None):
     """Raw handle of the current stream; the tensors have to be on its device."""
     dev = _current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"a tensor is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+    if (a.get_device() != dev or (b is not None and b.get_device() != dev) or (c is not None and c.get_device() != dev)
+            or (d is not None and d.get_device() != dev) or (e is not None and e.get_device() != dev)):
+        raise ValueError(f"tensors must be on the current device, cuda:{dev}")
     return _raw_stream(dev)
 
 
@@ -585,15 +591,14 @@ def _wants_gradient(a, b=None, c=None):
 
 
 def _row_matrix(t, name, dtypes, shape=(None, None)):
-    """(rows, cols, elements from row to row) of a matrix whose rows may be strided."""
+    """Elements from row to row of a matrix whose rows may be strided."""
     if not (isinstance(t, torch.Tensor) and t.dim() == 2 and t.is_cuda and t.dtype in dtypes
             and (shape[0] is None or t.shape == shape)):
         _need(t, name, tuple(dtypes), shape, contiguous=False)
-    rows, cols = t.shape
     ld, one = t.stride()
-    if one != 1 and cols > 1:
+    if one != 1 and t.shape[1] > 1:
         raise ValueError(f"the elements of a row of {name} must be contiguous")
-    return rows, cols, ld if rows > 1 else cols
+    return ld if t.shape[0] > 1 else t.shape[1]
 
 
 def _norm_weight(weight, dtype, cols):
@@ -607,23 +612,29 @@ def _norm_weight(weight, dtype, cols):
 
 def _rms_norm(x, weight, residual, eps, fp8, with_y):
     """(y, total, q, s), None where not wanted."""
-    rows, cols, ldx = _row_matrix(x, "x", ELEMENT_TYPES)
-    dtype = x.dtype
+    ldx = _row_matrix(x, "x", ELEMENT_TYPES)
+    shape, dtype = x.shape, x.dtype
+    rows, cols = shape
     w, w_type = _norm_weight(weight, dtype, cols)
-    y = total = q = s = None
-    r = r_type = ldr = 0
+    y = total = q = s = r = to = None
+    r_type = ldr = 0
     if residual is not None:
-        _, _, ldr = _row_matrix(residual, "residual", (dtype, _f32), (rows, cols))
-        r, r_type = residual.data_ptr(), ELEMENT_TYPES[residual.dtype]
-        total = torch.empty(rows, cols, dtype=residual.dtype, device=x.device)
+        if not (_like(residual, dtype, shape) or _like(residual, _f32, shape)):
+            ldr = _row_matrix(residual, "residual", (dtype, _f32), shape)
+            total = _empty(rows, cols, dtype=residual.dtype, device=x.device)
+        else:
+            ldr, total = cols, _empty_like(residual)
+        r, r_type, to = residual.data_ptr(), ELEMENT_TYPES[residual.dtype], total.data_ptr()
     if with_y:
-        y = torch.empty(rows, cols, dtype=dtype, device=x.device)
+        y = _empty_like(x) if ldx == cols else _empty(rows, cols, dtype=dtype, device=x.device)
     if fp8:
-        q = torch.empty(rows, cols, dtype=_u8, device=x.device)
-        s = torch.empty(rows, (cols + 127) // 128, dtype=_f32, device=x.device)
-    _check((_lib or load()).moe_rms_norm(x.data_ptr(), ELEMENT_TYPES[dtype], rows, cols, ldx, r or None, r_type, ldr, w,
-                                         w_type, eps, _address(y), _address(total), _address(q), _address(s),
-                                         _here(x, weight, residual)))
+        q = _empty(rows, cols, dtype=_u8, device=x.device)
+        s = _empty(rows, (cols + 127) // 128, dtype=_f32, device=x.device)
+    rc = (_lib or load()).moe_rms_norm(x.data_ptr(), ELEMENT_TYPES[dtype], rows, cols, ldx, r, r_type, ldr, w, w_type, eps,
+                                       y.data_ptr() if with_y else None, to, q.data_ptr() if fp8 else None,
+                                       s.data_ptr() if fp8 else None, _here(x, weight, residual))
+    if rc:
+        _check(rc)
     return y, total, q, s
 
 
@@ -677,28 +688,33 @@ def rms_norm_backward(dy, total, weight=None, eps: float = 1e-6, dtotal=None, we
     """Gradient of rms_norm (moe_rms_norm_backward): (dx of dy's type, dresidual of total's type, dweight of weight's type or
     None) from dy, the total that was normalised (x without a residual) and the gradient dtotal that reaches the total
     from elsewhere. dresidual is dx itself where the types are the same. ws: rms_norm_backward_workspace."""
-    rows, cols = dy.shape if isinstance(dy, torch.Tensor) and dy.dim() == 2 else (None, None)
-    if rows is None or dy.dtype not in ELEMENT_TYPES or not _like(dy, dy.dtype, (rows, cols)):
+    if not (isinstance(dy, torch.Tensor) and dy.dim() == 2 and dy.dtype in ELEMENT_TYPES and dy.is_cuda
+            and dy.is_contiguous()):
         _need(dy, "dy", tuple(ELEMENT_TYPES), (None, None))
-    kind = dy.dtype
-    _, _, ldt = _row_matrix(total, "total", (kind, _f32), (rows, cols))
-    if dtotal is not None and not _like(dtotal, total.dtype, (rows, cols)):
-        _need(dtotal, "dtotal", total.dtype, (rows, cols))
+    shape, kind = dy.shape, dy.dtype
+    rows, cols = shape
+    ldt = _row_matrix(total, "total", (kind, _f32), shape)
+    of = total.dtype
+    if dtotal is not None and not _like(dtotal, of, shape):
+        _need(dtotal, "dtotal", of, shape)
     w, w_type = _norm_weight(weight, kind, cols)
-    dx = torch.empty_like(dy)
+    dx = _empty_like(dy)
     dresidual, dweight = dx, None
-    if total.dtype is not kind:
-        dresidual = torch.empty(rows, cols, dtype=total.dtype, device=dy.device)
+    if of is not kind:
+        dresidual = _empty(rows, cols, dtype=of, device=dy.device)
     if weight is not None and weight_gradient:
-        dweight = torch.empty_like(weight)
+        dweight = _empty_like(weight)
         if ws is None:
             ws = rms_norm_backward_workspace(rows, cols, dy.device)
         elif not _like(ws, _u8, (ws.numel(),)):
             _need(ws, "ws", _u8, (None,))
-    _check((_lib or load()).moe_rms_norm_backward(
-        dy.data_ptr(), ELEMENT_TYPES[kind], rows, cols, total.data_ptr(), ELEMENT_TYPES[total.dtype], ldt,
-        _address(dtotal), w, w_type, eps, dx.data_ptr(), None if dresidual is dx else dresidual.data_ptr(),
-        _address(dweight), _address(ws), 0 if ws is None else ws.numel(), _here(dy, total, dtotal, weight, ws)))
+    rc = (_lib or load()).moe_rms_norm_backward(
+        dy.data_ptr(), ELEMENT_TYPES[kind], rows, cols, total.data_ptr(), ELEMENT_TYPES[of], ldt,
+        None if dtotal is None else dtotal.data_ptr(), w, w_type, eps, dx.data_ptr(),
+        None if dresidual is dx else dresidual.data_ptr(), None if dweight is None else dweight.data_ptr(),
+        None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), _here(dy, total, dtotal, weight, ws))
+    if rc:
+        _check(rc)
     return dx, dresidual, dweight
 
 
@@ -732,57 +748,72 @@ def sort_tokens(cfg, topk_idx, topk_w=None, ws=None) -> dict:
     [T k], and row_weight [T k] with topk_w fp32 [T, k]. Entries outside [0, E) are no assignment. ws:
     sort_tokens_workspace."""
     T, k = cfg.T, cfg.k
-    if not _like(topk_idx, _i32, (T, k)):
-        _need(topk_idx, "topk_idx", _i32, (T, k))
-    if topk_w is not None and not _like(topk_w, _f32, (T, k)):
-        _need(topk_w, "topk_w", _f32, (T, k))
+    shape = (T, k)
+    if not _like(topk_idx, _i32, shape):
+        _need(topk_idx, "topk_idx", _i32, shape)
+    if topk_w is not None and not _like(topk_w, _f32, shape):
+        _need(topk_w, "topk_w", _f32, shape)
     dev, n = topk_idx.device, _groups(cfg)
     if ws is None:
         size = _sort_tokens_bytes(cfg)
         if size:
-            ws = torch.empty(size, dtype=_u8, device=dev)
+            ws = _empty(size, dtype=_u8, device=dev)
     elif not _like(ws, _u8, (ws.numel(),)):
         _need(ws, "ws", _u8, (None,))
-    out = {"counts": torch.empty(n, dtype=_i32, device=dev), "offsets": torch.empty(n + 1, dtype=_i32, device=dev),
-           "inv_pos": torch.empty_like(topk_idx), "row_token": torch.empty(T * k, dtype=_i32, device=dev)}
+    counts, offsets = _empty(n, dtype=_i32, device=dev), _empty(n + 1, dtype=_i32, device=dev)
+    inv_pos, row_token = _empty_like(topk_idx), _empty(T * k, dtype=_i32, device=dev)
+    out = {"counts": counts, "offsets": offsets, "inv_pos": inv_pos, "row_token": row_token}
+    w = row_weight = None
     if topk_w is not None:
-        out["row_weight"] = torch.empty(T * k, dtype=_f32, device=dev)
-    _check((_lib or load()).moe_sort_tokens(
-        ctypes.byref(cfg), topk_idx.data_ptr(), _address(topk_w), out["counts"].data_ptr(), out["offsets"].data_ptr(),
-        out["inv_pos"].data_ptr(), out["row_token"].data_ptr(), _address(out.get("row_weight")), _address(ws),
-        0 if ws is None else ws.numel(), _here(topk_idx, topk_w, ws)))
+        out["row_weight"] = row_weight = _empty(T * k, dtype=_f32, device=dev)
+        w, row_weight = topk_w.data_ptr(), row_weight.data_ptr()
+    rc = (_lib or load()).moe_sort_tokens(
+        ctypes.byref(cfg), topk_idx.data_ptr(), w, counts.data_ptr(), offsets.data_ptr(), inv_pos.data_ptr(),
+        row_token.data_ptr(), row_weight, None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
+        _here(topk_idx, topk_w, ws))
+    if rc:
+        _check(rc)
     return out
 
 
-def _positions(cfg, inv_pos, offsets=None):
-    if not _like(inv_pos, _i32, (cfg.T, cfg.k)):
-        _need(inv_pos, "inv_pos", _i32, (cfg.T, cfg.k))
+def _positions(cfg, shape, inv_pos, offsets=None):
+    if not _like(inv_pos, _i32, shape):
+        _need(inv_pos, "inv_pos", _i32, shape)
     if offsets is not None and not _like(offsets, _i32, (_groups(cfg) + 1,)):
         _need(offsets, "offsets", _i32, (_groups(cfg) + 1,))
 
 
-def _route_weights_of(cfg, weights):
+def _route_weights_of(weights, shape):
     """Address of the route weights, or None."""
     if weights is None:
         return None
-    if not _like(weights, _f32, (cfg.T, cfg.k)):
-        _need(weights, "weights", _f32, (cfg.T, cfg.k))
+    if not _like(weights, _f32, shape):
+        _need(weights, "weights", _f32, shape)
     return weights.data_ptr()
 
 
+_COPIED = (torch.bfloat16, _f32, torch.float16, _u8)
+
+
 def _permute(x, cfg, inv_pos, offsets, scales):
-    _positions(cfg, inv_pos, offsets)
-    _, cols, ldx = _row_matrix(x, "x", tuple(ELEMENT_TYPES) if scales is None else (_u8,), (cfg.T, x.shape[-1]))
-    xd = torch.empty(cfg.T * cfg.k, cols, dtype=x.dtype, device=x.device)
-    xd_scales = None
+    T, k = cfg.T, cfg.k
+    _positions(cfg, (T, k), inv_pos, offsets)
+    ldx = _row_matrix(x, "x", _COPIED if scales is None else (_u8,))
+    rows, cols = x.shape
+    if rows != T:
+        _need(x, "x", x.dtype, (T, cols), contiguous=False)
+    xd = _empty(T * k, cols, dtype=x.dtype, device=x.device)
+    xd_scales = of = to = None
     if scales is not None:
         n = (cols + 127) // 128
-        if not _like(scales, _f32, (cfg.T, n)):
-            _need(scales, "scales", _f32, (cfg.T, n))
-        xd_scales = torch.empty(cfg.T * cfg.k, n, dtype=_f32, device=x.device)
-    _check((_lib or load()).moe_permute(ctypes.byref(cfg), x.data_ptr(), x.element_size(), cols, ldx, _address(scales),
-                                        inv_pos.data_ptr(), offsets.data_ptr(), xd.data_ptr(), _address(xd_scales),
-                                        _here(x, scales, inv_pos, offsets)))
+        if not _like(scales, _f32, (T, n)):
+            _need(scales, "scales", _f32, (T, n))
+        xd_scales = _empty(T * k, n, dtype=_f32, device=x.device)
+        of, to = scales.data_ptr(), xd_scales.data_ptr()
+    rc = (_lib or load()).moe_permute(ctypes.byref(cfg), x.data_ptr(), x.element_size(), cols, ldx, of, inv_pos.data_ptr(),
+                                      offsets.data_ptr(), xd.data_ptr(), to, _here(x, inv_pos, offsets, scales))
+    if rc:
+        _check(rc)
     return xd if scales is None else (xd, xd_scales)
 
 
@@ -802,7 +833,7 @@ class _Permute(torch.autograd.Function):
 
 
 def permute(cfg, x, inv_pos, offsets, scales=None):
-    """Rows of x [T, cols] (fp32, bf16 or fp16; the rows may be strided) into expert order (moe_permute): xd [T k, cols], with
+    """Rows of x [T, cols] (fp32, bf16, fp16 or uint8; the rows may be strided) into expert order (moe_permute): xd [T k, cols], with
     inv_pos and offsets of sort_tokens. Rows past the last one held are zero. With scales fp32 [T, ceil(cols / 128)], x
     holds e4m3 codes (uint8) and (xd, xd_scales) are returned. Differentiable once with respect to x (not 8-bit)."""
     if scales is None and _wants_gradient(x):
@@ -810,24 +841,26 @@ def permute(cfg, x, inv_pos, offsets, scales=None):
     return _permute(x, cfg, inv_pos, offsets, scales)
 
 
-def _expert_rows(cfg, yd):
-    """Columns of the expert-major rows."""
-    if not (isinstance(yd, torch.Tensor) and yd.dim() == 2 and yd.dtype in ELEMENT_TYPES
-            and _like(yd, yd.dtype, (cfg.T * cfg.k, yd.shape[1]))):
-        _need(yd, "yd", tuple(ELEMENT_TYPES), (cfg.T * cfg.k, None))
-    return yd.shape[1]
-
-
 def _unpermute(yd, weights, base, cfg, inv_pos):
-    _positions(cfg, inv_pos)
-    cols = _expert_rows(cfg, yd)
-    w = _route_weights_of(cfg, weights)
-    if base is not None and not _like(base, yd.dtype, (cfg.T, cols)):
-        _need(base, "base", yd.dtype, (cfg.T, cols))
-    y = torch.empty(cfg.T, cols, dtype=yd.dtype, device=yd.device)
-    _check((_lib or load()).moe_unpermute(ctypes.byref(cfg), yd.data_ptr(), ELEMENT_TYPES[yd.dtype], cols,
-                                          inv_pos.data_ptr(), w, _address(base), y.data_ptr(),
-                                          _here(yd, inv_pos, weights, base)))
+    T, k = cfg.T, cfg.k
+    shape = (T, k)
+    _positions(cfg, shape, inv_pos)
+    w = _route_weights_of(weights, shape)
+    if not (isinstance(yd, torch.Tensor) and yd.dim() == 2 and yd.dtype in ELEMENT_TYPES and yd.is_cuda
+            and yd.is_contiguous() and yd.shape[0] == T * k):
+        _need(yd, "yd", tuple(ELEMENT_TYPES), (T * k, None))
+    dtype, cols = yd.dtype, yd.shape[1]
+    b = None
+    if base is None:
+        y = _empty(T, cols, dtype=dtype, device=yd.device)
+    else:
+        if not _like(base, dtype, (T, cols)):
+            _need(base, "base", dtype, (T, cols))
+        y, b = _empty_like(base), base.data_ptr()
+    rc = (_lib or load()).moe_unpermute(ctypes.byref(cfg), yd.data_ptr(), ELEMENT_TYPES[dtype], cols, inv_pos.data_ptr(), w, b,
+                                        y.data_ptr(), _here(yd, inv_pos, weights, base))
+    if rc:
+        _check(rc)
     return y
 
 
@@ -857,7 +890,7 @@ def unpermute(cfg, yd, inv_pos, weights=None, base=None, offsets=None):
     if _wants_gradient(yd, weights, base):
         if offsets is None:
             raise ValueError("the gradient of unpermute needs offsets")
-        _positions(cfg, inv_pos, offsets)
+        _positions(cfg, (cfg.T, cfg.k), inv_pos, offsets)
         return _Unpermute.apply(yd, weights, base, cfg, inv_pos, offsets)
     return _unpermute(yd, weights, base, cfg, inv_pos)
 
@@ -865,19 +898,27 @@ def unpermute(cfg, yd, inv_pos, weights=None, base=None, offsets=None):
 def unpermute_backward(cfg, dy, yd, inv_pos, offsets, weights=None):
     """Gradient of unpermute (moe_unpermute_backward): (dyd [T k, cols] of dy's type, zero in the rows past the last one held;
     dweights fp32 [T, k], None where yd is None) from dy [T, cols]."""
-    _positions(cfg, inv_pos, offsets)
-    if not (isinstance(dy, torch.Tensor) and dy.dim() == 2 and dy.dtype in ELEMENT_TYPES
-            and _like(dy, dy.dtype, (cfg.T, dy.shape[1]))):
-        _need(dy, "dy", tuple(ELEMENT_TYPES), (cfg.T, None))
+    T, k = cfg.T, cfg.k
+    shape = (T, k)
+    _positions(cfg, shape, inv_pos, offsets)
+    w = _route_weights_of(weights, shape)
+    if not (isinstance(dy, torch.Tensor) and dy.dim() == 2 and dy.dtype in ELEMENT_TYPES and dy.is_cuda
+            and dy.is_contiguous() and dy.shape[0] == T):
+        _need(dy, "dy", tuple(ELEMENT_TYPES), (T, None))
     cols, kind = dy.shape[1], dy.dtype
-    if yd is not None and not _like(yd, kind, (cfg.T * cfg.k, cols)):
-        _need(yd, "yd", kind, (cfg.T * cfg.k, cols))
-    w = _route_weights_of(cfg, weights)
-    dyd = torch.empty(cfg.T * cfg.k, cols, dtype=kind, device=dy.device)
-    dw = None if yd is None else torch.empty(cfg.T, cfg.k, dtype=_f32, device=dy.device)
-    _check((_lib or load()).moe_unpermute_backward(ctypes.byref(cfg), dy.data_ptr(), _address(yd), ELEMENT_TYPES[kind], cols,
-                                                   inv_pos.data_ptr(), offsets.data_ptr(), w, dyd.data_ptr(),
-                                                   _address(dw), _here(dy, yd, inv_pos, offsets, weights)))
+    dw = of = to = None
+    if yd is None:
+        dyd = _empty(T * k, cols, dtype=kind, device=dy.device)
+    else:
+        if not _like(yd, kind, (T * k, cols)):
+            _need(yd, "yd", kind, (T * k, cols))
+        dyd, dw = _empty_like(yd), _empty(T, k, dtype=_f32, device=dy.device)
+        of, to = yd.data_ptr(), dw.data_ptr()
+    rc = (_lib or load()).moe_unpermute_backward(ctypes.byref(cfg), dy.data_ptr(), of, ELEMENT_TYPES[kind], cols,
+                                                 inv_pos.data_ptr(), offsets.data_ptr(), w, dyd.data_ptr(), to,
+                                                 _here(dy, yd, inv_pos, offsets, weights))
+    if rc:
+        _check(rc)
     return dyd, dw
 
 
@@ -924,18 +965,21 @@ def route_weights(cfg, logits, bias=None):
 def route_backward(cfg, logits, topk_idx, dtopk_w, dlogits=None) -> torch.Tensor:
     """Gradient of the route weights with respect to the logits [T, E] (fp32 or bf16), of their dtype
     (moe_route_backward), from the chosen experts topk_idx int32 [T, k] and the weights' gradient dtopk_w fp32 [T, k]."""
-    if not (_like(logits, _f32, (cfg.T, cfg.E)) or _like(logits, torch.bfloat16, (cfg.T, cfg.E))):
-        _need(logits, "logits", (_f32, torch.bfloat16), (cfg.T, cfg.E))
-    if not (_like(topk_idx, _i32, (cfg.T, cfg.k)) and _like(dtopk_w, _f32, (cfg.T, cfg.k))):
-        _need(topk_idx, "topk_idx", _i32, (cfg.T, cfg.k))
-        _need(dtopk_w, "dtopk_w", _f32, (cfg.T, cfg.k))
+    T, E, k = cfg.T, cfg.E, cfg.k
+    if not (_like(logits, _f32, (T, E)) or _like(logits, torch.bfloat16, (T, E))):
+        _need(logits, "logits", (_f32, torch.bfloat16), (T, E))
+    if not (_like(topk_idx, _i32, (T, k)) and _like(dtopk_w, _f32, (T, k))):
+        _need(topk_idx, "topk_idx", _i32, (T, k))
+        _need(dtopk_w, "dtopk_w", _f32, (T, k))
     if dlogits is None:
-        dlogits = torch.empty_like(logits)
-    elif not _like(dlogits, logits.dtype, (cfg.T, cfg.E)):
-        _need(dlogits, "dlogits", logits.dtype, (cfg.T, cfg.E))
-    _check((_lib or load()).moe_route_backward(ctypes.byref(cfg), logits.data_ptr(), ELEMENT_TYPES[logits.dtype],
-                                               topk_idx.data_ptr(), dtopk_w.data_ptr(), dlogits.data_ptr(),
-                                               _here(logits, topk_idx, dtopk_w, dlogits)))
+        dlogits = _empty_like(logits)
+    elif not _like(dlogits, logits.dtype, (T, E)):
+        _need(dlogits, "dlogits", logits.dtype, (T, E))
+    rc = (_lib or load()).moe_route_backward(ctypes.byref(cfg), logits.data_ptr(), ELEMENT_TYPES[logits.dtype],
+                                             topk_idx.data_ptr(), dtopk_w.data_ptr(), dlogits.data_ptr(),
+                                             _here(logits, topk_idx, dtopk_w, dlogits))
+    if rc:
+        _check(rc)
     return dlogits
 
 
