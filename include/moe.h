@@ -450,15 +450,16 @@ int moe_balance_loss_backward(const moe_config* cfg, const void* logits, int32_t
  * and written 16 bytes at a time, others number by number. Sums, statistics and gradients are fp32; every output is
  * rounded once.
  *
- * moe_rms_norm: total = x + residual, y = total * weight / sqrt(mean(total^2) + eps).
+ * moe_rms_norm: total = x + residual, y = total * weight / sqrt(mean(total^2) + eps). The squares are added in fp32: rows of
+ * numbers past 1e18 in size overflow it and come out as 0, as in fp32 arithmetic anywhere.
  *   x         [rows, cols] of x_type, ldx elements from row to row
  *   residual  [rows, cols] of residual_type (x_type or MOE_TYPE_F32), ldr apart; NULL: total is x, and `total` is not written
  *   weight    [cols] of weight_type (x_type or MOE_TYPE_F32); NULL: ones
  *   y         [rows, cols] of x_type out, or NULL
  *   total     [rows, cols] of residual_type out, or NULL. It is the unrounded total that is normalised and quantised.
  *   q, s      [rows, cols] e4m3 codes and [rows, ceil(cols / 128)] scales of y out, or both NULL: scale = amax / 448 of 128
- *             columns, at least 2^-126 (1 where all are zero), code = e4m3(RN(y / scale)). A block that holds an infinity or
- *             a NaN stands for NaN. The form of the FP8 layer's rows (moe_dispatch), of y before it is rounded.
+ *             columns, at least 2^-126 (1 where all are zero), code = e4m3(RN(y * RN(1 / scale))). A block that holds an
+ *             infinity or a NaN stands for NaN. The form of the FP8 layer's rows (moe_dispatch), of y before it is rounded.
  * Outputs are contiguous. total may be residual, or y or total x, where those are contiguous; outputs overlap nothing else.
  * 1 <= cols <= 16384; eps >= 0. One launch. Errors: MOE_ERR_INVALID, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA. */
 int moe_rms_norm(const void* x, int32_t x_type, int64_t rows, int64_t cols, int64_t ldx, const void* residual,
@@ -512,7 +513,7 @@ int moe_permute(const moe_config* cfg, const void* x, int32_t element_bytes, int
  *   yd         [T*k, cols] of type;  base [T, cols] of type, or NULL (it may be y)
  *   weights    [T, k] fp32, or NULL: ones
  *   y          [T, cols] of type out
- * Rows and weights of slots at -1 are not read. (yd of moe_expert_ffn holds its rows' weights already: that takes NULL, or a
+ * Rows and weights of slots at -1 (or outside the rows) are not read. (yd of moe_expert_ffn holds its rows' weights already: that takes NULL, or a
  * row_weight of ones.) cols < 2^28. One launch. Errors: as moe_permute. */
 int moe_unpermute(const moe_config* cfg, const void* yd, int32_t type, int64_t cols, const int32_t* inv_pos,
                   const float* weights, const void* base, void* y, moe_stream_t stream);
@@ -529,8 +530,8 @@ int moe_unpermute_backward(const moe_config* cfg, const void* dy, const void* yd
 /* Gradient of moe_route's weights with respect to its logits (cfg: T, E, k, score, renormalize, routed_scale; the
  * selection and its bias carry none): dlogits [T, E] of logits_type (MOE_TYPE_F32 or MOE_TYPE_BF16) from logits [T, E],
  * topk_idx [T, k] and dtopk_w [T, k] fp32. Entries of topk_idx outside [0, E) are left out; an expert that a token names
- * twice gets the sum of both. A row whose (chosen) logits are all -inf has a gradient of 0. Every number of dlogits is
- * written. One launch. Errors: MOE_ERR_INVALID, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA. */
+ * twice gets the sum of both. A token without assignments (padding), or whose (chosen) logits are all -inf, has a gradient
+ * of 0, whatever its row holds. Every number of dlogits is written. One launch. Errors: MOE_ERR_INVALID, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA. */
 int moe_route_backward(const moe_config* cfg, const void* logits, int32_t logits_type, const int32_t* topk_idx,
                        const float* dtopk_w, void* dlogits, moe_stream_t stream);
 

@@ -248,7 +248,7 @@ __device__ __forceinline__ void copy_item(const CopyPlane& p, const int32_t* inv
   const int mine = lane < k ? inv_pos[t * k + lane] : -1;
   for (int j = 0; j < k; ++j) {
     const int r = __shfl_sync(0xffffffffu, mine, j);
-    if (r < 0) continue;
+    if (r < 0 || r >= T * k) continue;
     Word* dst = static_cast<Word*>(p.dst) + (int64_t)r * p.words;
 #pragma unroll
     for (int u = 0; u < DEPTH; ++u)
@@ -261,7 +261,8 @@ __global__ void __launch_bounds__(256) permute_kernel(const CopyPlane p, const C
                                                       const int32_t* held_at, int64_t T, int k) {
   const int lane = threadIdx.x & 31;
   const int64_t warps = ((int64_t)gridDim.x * blockDim.x) >> 5;
-  const int64_t held = *held_at, rows = T + (T * k - held);  // token rows, then those that hold nothing
+  const int64_t held = min(max((int64_t)*held_at, (int64_t)0), T * k);
+  const int64_t rows = T + (T * k - held);  // token rows, then those that hold nothing
   const int64_t items = rows * p.pieces, more = scales.words ? rows * scales.pieces : 0;
   for (int64_t it = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; it < items + more; it += warps) {
     if (it < items)

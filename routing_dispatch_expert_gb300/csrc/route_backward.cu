@@ -183,6 +183,9 @@ __global__ void __launch_bounds__(kThreads) dense_kernel(const Args a) {
     z = lanes_sum<L>(z);
     const float r = z == 0.f ? 0.f : __fdiv_rn(1.0f, z);
     const float u = exponential(l - m) * r;
+    // a token without choices, padding say, has no gradient whatever its logits hold
+    const uint32_t own = L == 32 ? 0xffffffffu : ((1u << (L & 31)) - 1u) << (lane - sub);
+    const bool none = (__ballot_sync(0xffffffffu, e >= 0) & own) == 0u;
     const float dot = lanes_sum<L>(g * u);
     same_expert<L>(a.k, e, g, all, n);
     if (in) {
@@ -192,7 +195,7 @@ __global__ void __launch_bounds__(kThreads) dense_kernel(const Args a) {
         const int at = 4 * (sub + L * j);
         float o[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = by * p[4 * j + i];
+        for (int i = 0; i < 4; ++i) o[i] = none ? 0.f : by * p[4 * j + i];
         if (vec && at < a.E) {
           if (TYPE == MOE_TYPE_F32)
             *reinterpret_cast<float4*>(static_cast<float*>(a.dlogits) + t * a.E + at) = make_float4(o[0], o[1], o[2], o[3]);

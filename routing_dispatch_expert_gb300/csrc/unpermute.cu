@@ -17,14 +17,16 @@ namespace un {
 
 using std::integral_constant;
 
-// Rows and weights of the slots j0 .. j0 + KB - 1 of token t, in each of its LANES lanes; -1 past the last slot.
+// Rows and weights of the slots j0 .. j0 + KB - 1 of token t, in each of its LANES lanes; -1 past the last slot, and for
+// positions outside the T k rows.
 template <int KB, int LANES>
 __device__ __forceinline__ void slots(const int32_t* inv_pos, const float* weights, int64_t t, int64_t T, int k, int j0,
                                       int (&row)[KB], float (&w)[KB]) {
   if constexpr (LANES == 32) {
     const int lane = threadIdx.x & 31;
     const bool in = lane < KB && j0 + lane < k;
-    const int r = in ? inv_pos[t * k + j0 + lane] : -1;
+    int r = in ? inv_pos[t * k + j0 + lane] : -1;
+    if (r >= T * k) r = -1;
     const float v = in && weights ? weights[t * k + j0 + lane] : 1.f;
 #pragma unroll
     for (int j = 0; j < KB; ++j) {
@@ -36,6 +38,7 @@ __device__ __forceinline__ void slots(const int32_t* inv_pos, const float* weigh
     for (int j = 0; j < KB; ++j) {
       const bool in = t < T && j0 + j < k;
       row[j] = in ? inv_pos[t * k + j0 + j] : -1;
+      if (row[j] >= T * k) row[j] = -1;
       w[j] = in && weights ? weights[t * k + j0 + j] : 1.f;
     }
   }
@@ -182,7 +185,7 @@ __global__ void __launch_bounds__(256, (kBlocks<TYPE, MAP, KB>)) spread_kernel(c
       __syncthreads();
     }
   }
-  const int64_t held = *a.held_at;
+  const int64_t held = max(*a.held_at, 0);
 #pragma unroll
   for (int i = 0; i < 8; ++i) f[i] = 0.f;
   for (int64_t r = held + group; r < a.T * a.k; r += groups)

@@ -216,6 +216,21 @@ def test_far_rows():
     close(dw, want.expand(T, k), 160 * U32 * want, "dweights")
 
 
+def test_positions_outside_the_rows_are_left_out():
+    """The kernels look at every position before they use it."""
+    cfg, s = sorted_batch(40, 4, 2, pad=0.0, factor=0.0)
+    inv = s["inv_pos"].clone()
+    inv[3, 0], inv[7, 1], inv[9, 0] = 80, 2 ** 31 - 1, -2 ** 31
+    clean = torch.where((inv < 0) | (inv >= 80), -1, inv).int()
+    for cols in (24, 100, 333, 512):
+        x, yd, w = torch.randn(40, cols, device="cuda"), torch.randn(80, cols, device="cuda"), torch.rand(40, 2, device="cuda")
+        rows = clean[clean >= 0].long()
+        assert torch.equal(rde.permute(cfg, x, inv, s["offsets"])[rows], rde.permute(cfg, x, clean, s["offsets"])[rows])
+        assert torch.equal(rde.unpermute(cfg, yd, inv, w), rde.unpermute(cfg, yd, clean, w))
+        a, b = (rde.unpermute_backward(cfg, x, yd, i, s["offsets"], w) for i in (inv, clean))
+        assert torch.equal(a[0][rows], b[0][rows]) and torch.equal(a[1], b[1])
+
+
 def test_no_tokens_and_refusals():
     cfg = config(0, 4, 2)
     idx = torch.empty(0, 2, dtype=torch.int32, device="cuda")

@@ -75,11 +75,7 @@ def test_rows_without_choices_and_masked_experts(score, renorm):
     z[5] -= 300                    # sigmoids that all underflow
     z[6] += 300
     got = rde.route_backward(config(T, E, k, score, renorm), z, idx, dw)
-    assert (got[3] == 0).all()
-    if score == "softmax" and not renorm:
-        assert torch.isfinite(got[torch.tensor([0, 1, 3, 4, 5, 6, 7])]).all()
-    else:
-        assert torch.isfinite(got).all() and (got[2] == 0).all()
+    assert torch.isfinite(got).all() and (got[2] == 0).all() and (got[3] == 0).all()
     assert (got[1, 4:] == 0).all()
     if renorm:  # a shift of all logits leaves a softmax, and sigmoids that are e^l, as they are
         ref = torch.softmax(z[5, idx[5].long()].double(), 0)

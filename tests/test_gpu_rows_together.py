@@ -209,9 +209,10 @@ def test_captured_training_step():
     assert same(got, want)
 
 
-def test_in_place():
+@pytest.mark.parametrize("cols", [64, 1000, 1003, 4101])
+def test_in_place(cols):
     """Through the C entry points: total written over the residual, y over x; dx over dy; y of unpermute over its base."""
-    cfg, x, r, w, idx, tw, z, dy = inputs(13)
+    cfg, x, r, w, idx, tw, z, dy = inputs(13, cols=cols)
     lib, n, c = rde.load(), x.shape[0], x.shape[1]
     y, total = rde.rms_norm(x, w, r)
     dx, _, dw = rde.rms_norm_backward(dy, total, w, dtotal=r)
