@@ -108,16 +108,22 @@ __global__ void __launch_bounds__(kThreads) rank_kernel(const SortArgs a) {
 #pragma unroll
     for (int j = 0; j < kEach; ++j)
       if (mine[j] < 0 || mine[j] >= E) mine[j] = -1;
+    const bool some = c0 + warp * 32 * kEach < hi;  // of the whole warp
+    uint32_t same[kEach];  // the lanes that hold the same expert, bit by bit of its number
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) same[j] = 0xffffffffu;
+    for (int b = 0; some && b < bits; ++b)
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) {
+        const bool set = (unsigned)(mine[j] < 0 ? E : mine[j]) >> b & 1u;
+        const uint32_t with = __ballot_sync(0xffffffffu, set);
+        same[j] &= set ? with : ~with;
+      }
 #pragma unroll
     for (int j = 0; j < kEach; ++j) {  // the first lane of an expert counts for all of its lanes
+      if (!some) break;
       const int e = mine[j];
-      uint32_t peers = 0xffffffffu;  // the lanes that hold the same expert: bit by bit
-      for (int b = 0; b < bits; ++b) {
-        const bool set = (unsigned)(e < 0 ? E : e) >> b & 1u;
-        const uint32_t with = __ballot_sync(0xffffffffu, set);
-        peers &= set ? with : ~with;
-      }
-      const uint32_t before = peers & ((1u << lane) - 1u);
+      const uint32_t peers = same[j], before = peers & ((1u << lane) - 1u);
       int32_t* c = cnt + warp * E + max(e, 0);
       const int had = *c;
       __syncwarp();
@@ -224,8 +230,8 @@ struct CopyPlane {
   int piece, pieces;  // words of a warp's work, a multiple of 32, and those works of a row
 };
 
-// Words of a lane in a piece, at most: 16 where there are enough pieces for every SM, else 4 (16384 rows of 7168 bytes to
-// eight places each: 165 us with the whole row in a piece, 169 with 8, 172 with 4).
+// Words of a lane in a piece, at most: 16 where there are enough pieces for every SM, else 4; one for short rows (16384 rows
+// of 7168 bytes to eight places each: 165 us with the whole row in a piece, 169 with 8, 172 with 4).
 constexpr int kDeep = 16;
 
 template <class Word, int DEPTH>
@@ -253,6 +259,29 @@ __device__ __forceinline__ void copy_item(const CopyPlane& p, const int32_t* inv
 #pragma unroll
     for (int u = 0; u < DEPTH; ++u)
       if (c0 + 32 * u < end) dst[c0 + 32 * u] = v[u];
+  }
+}
+
+// Rows of at most LANES words: 32 / LANES of them a warp, a lane one word of each of its row's places.
+template <class Word, int LANES>
+__global__ void __launch_bounds__(256) permute_short_kernel(const CopyPlane p, const int32_t* inv_pos, const int32_t* held_at,
+                                                            int64_t T, int k) {
+  const int sub = threadIdx.x % LANES;
+  const int64_t groups = (int64_t)gridDim.x * blockDim.x / LANES;
+  const int64_t held = min(max((int64_t)*held_at, (int64_t)0), T * k), rows = T + (T * k - held);
+  if (sub >= p.words) return;
+  Word* const dst = static_cast<Word*>(p.dst) + sub;
+  for (int64_t t = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / LANES; t < rows; t += groups) {
+    if (t >= T) {
+      dst[(held + (t - T)) * p.words] = Word{};
+      continue;
+    }
+    const Word v = static_cast<const Word*>(p.src)[t * p.ld + sub];
+#pragma unroll 8
+    for (int j = 0; j < k; ++j) {
+      const int r = inv_pos[t * k + j];
+      if (r >= 0 && r < T * k) dst[(int64_t)r * p.words] = v;
+    }
   }
 }
 
@@ -360,10 +389,19 @@ cudaError_t launch_permute(const PermuteDesc& d, cudaStream_t stream) {
     p.dst = d.xd;
     p.ld = ld / (int64_t)sizeof(Word);
     p.words = (int)(bytes / (int64_t)sizeof(Word));
-    const bool deep = d.T * cdiv(p.words, 256) >= (int64_t)num_sms() * 64;
+    const int64_t sms = num_sms();
+    if (p.words <= 16 && !d.xd_scales) {
+      const int lanes = p.words <= 4 ? 4 : p.words <= 8 ? 8 : 16;
+      const unsigned blocks = (unsigned)std::min<int64_t>(cdiv((int64_t)d.T * lanes, 256), sms * 32);
+      auto kernel = lanes == 4 ? pm::permute_short_kernel<Word, 4>
+                               : lanes == 8 ? pm::permute_short_kernel<Word, 8> : pm::permute_short_kernel<Word, 16>;
+      kernel<<<blocks, 256, 0, stream>>>(p, d.inv_pos, d.held, d.T, d.k);
+      return cudaGetLastError();
+    }
+    const bool deep = p.words > 128 && d.T * cdiv(p.words, 512) >= sms * 32;
     const auto cut = [&](pm::CopyPlane& q) {  // even pieces of whole steps of 32 words
       const int steps = (int)cdiv(q.words, 32);
-      q.piece = 32 * (int)cdiv(steps, cdiv(steps, deep ? pm::kDeep : 4));
+      q.piece = 32 * (int)cdiv(steps, cdiv(steps, deep ? pm::kDeep : p.words <= 32 ? 1 : 4));
       q.pieces = (int)cdiv(q.words, q.piece);
     };
     cut(p);
@@ -374,8 +412,10 @@ cudaError_t launch_permute(const PermuteDesc& d, cudaStream_t stream) {
       cut(s);
     }
     const int64_t items = (int64_t)d.T * (p.pieces + (d.xd_scales ? s.pieces : 0));
-    const unsigned blocks = (unsigned)std::min<int64_t>(cdiv(items, 8), (int64_t)num_sms() * 16);
-    if (deep)
+    const unsigned blocks = (unsigned)std::min<int64_t>(cdiv(items, 8), sms * 16);
+    if (p.words <= 32)
+      pm::permute_kernel<Word, 1><<<blocks, 256, 0, stream>>>(p, s, d.inv_pos, d.held, d.T, d.k);
+    else if (deep)
       pm::permute_kernel<Word, pm::kDeep><<<blocks, 256, 0, stream>>>(p, s, d.inv_pos, d.held, d.T, d.k);
     else
       pm::permute_kernel<Word, 4><<<blocks, 256, 0, stream>>>(p, s, d.inv_pos, d.held, d.T, d.k);
