@@ -11,7 +11,10 @@
 // fp32. Sigmoids are taken with e^min(l) factored out of their sum, so that a token whose sigmoids all underflow keeps their
 // ratios; a token whose chosen logits are all -inf has no weights and a gradient of 0.
 //
-// Bound by the bytes of dlogits (and of the logits, for a softmax over all).
+// One GB300: 65536 tokens x 256 experts, k 8, fp32: chosen experts alone 20.6 us. Its bytes, dlogits and the 8 logits a token, are
+// 11 us at a copy's rate, but the logits come in pieces of 64 bytes: 46 MB are read and 67 written, 17 us. Softmax over all
+// 24.6 us (5.5 TB/s of 6.78), bf16 23.9: latency, a token's loads and sums in a row. 4096 x 8: 2.4 us, launch. Four tokens a warp
+// instead of one for the chosen experts: 33 -> 20 us; all loads of a token asked for together: 30 -> 24.6 us (softmax).
 #include <algorithm>
 #include <type_traits>
 

@@ -3,8 +3,12 @@
 //   y[t] = base[t] + sum_j w[t, j] yd[p[t, j]]                      in slot order, fp32, rounded once
 //   dyd[p[t, j]] = w[t, j] dy[t],   dw[t, j] = <yd[p[t, j]], dy[t]>  fp32
 //
-// Both go token by token, so that the k uses of a token's row meet; the k rows elsewhere are read (and written) once. Bound by
-// HBM: the rows of a chunk are all loaded before any is worked on.
+// Both go token by token, so that the k uses of a token's row meet; the k rows elsewhere are read (and written) once. The rows of a
+// chunk are all loaded before any is worked on, and a token's positions are looked up once for many chunks.
+//
+// Bound by HBM. One GB300, k 8 (a copy's rate is 6.78 TB/s): 16384 x 7168 bf16 with weights and base 345 us, 6.8 TB/s, the
+// gradient with the weights' 601 us, 6.6; 8192 x 7168 fp32 331 and 589 us; 65536 x 64 bf16 20 and 28 us (4.4 and 5.4 TB/s); odd
+// 16-bit rows 8192 x 7167 257 and 416 us (4.6 and 4.8: 64 bytes an access); 64 x 512, k 2 2.4 us, launch.
 #include <algorithm>
 #include <type_traits>
 
