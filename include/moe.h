@@ -450,17 +450,21 @@ int moe_balance_loss_backward(const moe_config* cfg, const void* logits, int32_t
  * and written 16 bytes at a time, others number by number. Sums, statistics and gradients are fp32; every output is
  * rounded once.
  *
- * moe_rms_norm: total = x + residual, y = total * weight / sqrt(mean(total^2) + eps). The squares are added in fp32: rows of
- * numbers past 1e18 in size overflow it and come out as 0, as in fp32 arithmetic anywhere.
+ * moe_rms_norm: total = x + residual, y = total * weight / sqrt(mean(total^2) + eps). The squares are added in fp32:
+ * rows of numbers past 1e18 in size overflow it and come out as 0, and a row of zeros with eps 0 as NaN, as in fp32
+ * arithmetic anywhere.
  *   x         [rows, cols] of x_type, ldx elements from row to row
- *   residual  [rows, cols] of residual_type (x_type or MOE_TYPE_F32), ldr apart; NULL: total is x, and `total` is not written
+ *   residual  [rows, cols] of residual_type (x_type or MOE_TYPE_F32), ldr apart; NULL: total is x, and
+ *             `total` is not written
  *   weight    [cols] of weight_type (x_type or MOE_TYPE_F32); NULL: ones
  *   y         [rows, cols] of x_type out, or NULL
  *   total     [rows, cols] of residual_type out, or NULL. It is the unrounded total that is normalised and quantised.
- *   q, s      [rows, cols] e4m3 codes and [rows, ceil(cols / 128)] scales of y out, or both NULL: scale = amax / 448 of 128
- *             columns, at least 2^-126 (1 where all are zero), code = e4m3(RN(y * RN(1 / scale))). A block that holds an
- *             infinity or a NaN stands for NaN. The form of the FP8 layer's rows (moe_dispatch), of y before it is rounded.
- * Outputs are contiguous. total may be residual, or y or total x, where those are contiguous; outputs overlap nothing else.
+ *   q, s      [rows, cols] e4m3 codes and [rows, ceil(cols / 128)] scales of y out, or both NULL: scale = amax / 448 of
+ *             128 columns, at least 2^-126 (1 where all are zero), code = e4m3(RN(y * RN(1 / scale))). A block that
+ *             holds an infinity or a NaN stands for NaN. The form of the FP8 layer's rows (moe_dispatch), of y before
+ *             it is rounded.
+ * Outputs are contiguous. total may be residual, or y or total x, where those are contiguous; outputs overlap nothing
+ * else.
  * 1 <= cols <= 16384; eps >= 0. One launch. Errors: MOE_ERR_INVALID, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA. */
 int moe_rms_norm(const void* x, int32_t x_type, int64_t rows, int64_t cols, int64_t ldx, const void* residual,
                  int32_t residual_type, int64_t ldr, const void* weight, int32_t weight_type, float eps, void* y,
@@ -469,8 +473,8 @@ int moe_rms_norm(const void* x, int32_t x_type, int64_t rows, int64_t cols, int6
 /* Its gradient, from the total that was normalised (x where there was no residual):
  *   dy         [rows, cols] of y_type;  total [rows, cols] of total_type (y_type or MOE_TYPE_F32), ldt apart
  *   dtotal     [rows, cols] of total_type: the gradient that reaches the total from elsewhere, added; or NULL
- *   dx         [rows, cols] of y_type out, dresidual [rows, cols] of total_type out: the gradient of the total, which is
- *              that of x and of the residual; either may be NULL
+ *   dx         [rows, cols] of y_type out, dresidual [rows, cols] of total_type out: the gradient of the total, which
+ *              is that of x and of the residual; either may be NULL
  *   dweight    [cols] of weight_type out, or NULL. The rows are added in an order that rows and cols fix.
  *   ws         moe_rms_norm_backward_workspace_size() bytes, with dweight (else NULL)
  * dx or dresidual may be dy, total (if contiguous) or dtotal where their types are the same; otherwise outputs overlap
@@ -491,7 +495,8 @@ int moe_rms_norm_backward(const void* dy, int32_t y_type, int64_t rows, int64_t 
  *   row_token, row_weight      [T*k] out: token and weight of each row; -1 and 0 for the rows past the last one held
  *              (offsets[E], or offsets[n_slots])
  *   ws         moe_sort_tokens_workspace_size() bytes (0 where one launch does it: NULL); its contents do not matter
- * One launch for T*k <= 2048, else two. Errors: MOE_ERR_INVALID, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_CUDA. */
+ * One launch for T*k <= 2048, else two. Errors: MOE_ERR_INVALID, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE,
+ * MOE_ERR_CUDA. */
 int moe_sort_tokens_workspace_size(const moe_config* cfg, size_t* bytes);
 int moe_sort_tokens(const moe_config* cfg, const int32_t* topk_idx, const float* topk_w, int32_t* counts,
                     int32_t* offsets, int32_t* inv_pos, int32_t* row_token, float* row_weight, void* ws, size_t ws_bytes,
@@ -501,10 +506,11 @@ int moe_sort_tokens(const moe_config* cfg, const int32_t* topk_idx, const float*
  *   x          [T, cols] of elements of element_bytes (1, 2 or 4), ldx elements from row to row
  *   inv_pos, offsets   from moe_sort_tokens or moe_dispatch with the same cfg
  *   xd         [T*k, cols] out, contiguous
- *   x_scales, xd_scales  [T, ceil(cols / 128)] and [T*k, ceil(cols / 128)] fp32: the scales of 8-bit rows, moved with them;
- *              or both NULL
- * cols < 2^28. Its gradient is moe_unpermute without weights. One launch. Errors: MOE_ERR_INVALID, MOE_ERR_UNSUPPORTED,
- * MOE_ERR_CUDA. */
+ *   x_scales, xd_scales  [T, ceil(cols / 128)] and [T*k, ceil(cols / 128)] fp32: the scales of 8-bit rows, moved with
+ *              them; or both NULL
+ * The rows are the T*k routed ones: a layer with a shared expert wants its T rows behind them. xd and xd_scales overlap
+ * no input. cols < 2^28. Its gradient is moe_unpermute without weights. One launch. Errors: MOE_ERR_INVALID,
+ * MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA. */
 int moe_permute(const moe_config* cfg, const void* x, int32_t element_bytes, int64_t cols, int64_t ldx,
                 const float* x_scales, const int32_t* inv_pos, const int32_t* offsets, void* xd, float* xd_scales,
                 moe_stream_t stream);
@@ -513,15 +519,16 @@ int moe_permute(const moe_config* cfg, const void* x, int32_t element_bytes, int
  *   yd         [T*k, cols] of type;  base [T, cols] of type, or NULL (it may be y)
  *   weights    [T, k] fp32, or NULL: ones
  *   y          [T, cols] of type out
- * Rows and weights of slots at -1 (or outside the rows) are not read. (yd of moe_expert_ffn holds its rows' weights already: that takes NULL, or a
- * row_weight of ones.) cols < 2^28. One launch. Errors: as moe_permute. */
+ * Rows and weights of slots at -1 (or outside the rows) are not read. (yd of moe_expert_ffn holds its rows' weights
+ * already: that takes NULL, or a row_weight of ones.) y overlaps no input but base. cols < 2^28. One launch. Errors: as
+ * moe_permute. */
 int moe_unpermute(const moe_config* cfg, const void* yd, int32_t type, int64_t cols, const int32_t* inv_pos,
                   const float* weights, const void* base, void* y, moe_stream_t stream);
 
 /* Its gradient: dyd[inv_pos[t, j]] = weights[t, j] dy[t], zero in the rows past the last one held, and
  * dweights[t, j] = sum_c yd[inv_pos[t, j], c] dy[t, c], 0 for slots at -1. (That of base is dy.)
  *   dy [T, cols] of type; yd [T*k, cols] of type (read with dweights only); weights as above;
- *   dyd [T*k, cols] of type out; dweights [T, k] fp32 out, or NULL
+ *   dyd [T*k, cols] of type out; dweights [T, k] fp32 out, or NULL; they overlap no input
  * One launch. Errors: as moe_permute. */
 int moe_unpermute_backward(const moe_config* cfg, const void* dy, const void* yd, int32_t type, int64_t cols,
                            const int32_t* inv_pos, const int32_t* offsets, const float* weights, void* dyd,
@@ -529,9 +536,10 @@ int moe_unpermute_backward(const moe_config* cfg, const void* dy, const void* yd
 
 /* Gradient of moe_route's weights with respect to its logits (cfg: T, E, k, score, renormalize, routed_scale; the
  * selection and its bias carry none): dlogits [T, E] of logits_type (MOE_TYPE_F32 or MOE_TYPE_BF16) from logits [T, E],
- * topk_idx [T, k] and dtopk_w [T, k] fp32. Entries of topk_idx outside [0, E) are left out; an expert that a token names
- * twice gets the sum of both. A token without assignments (padding), or whose (chosen) logits are all -inf, has a gradient
- * of 0, whatever its row holds. Every number of dlogits is written. One launch. Errors: MOE_ERR_INVALID, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA. */
+ * topk_idx [T, k] and dtopk_w [T, k] fp32. Entries of topk_idx outside [0, E) are left out; an expert that a token
+ * names twice gets the sum of both. A token without assignments (padding), or whose (chosen) logits are all -inf, has a
+ * gradient of 0, whatever its row holds. Every number of dlogits is written. One launch. Errors: MOE_ERR_INVALID,
+ * MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA. */
 int moe_route_backward(const moe_config* cfg, const void* logits, int32_t logits_type, const int32_t* topk_idx,
                        const float* dtopk_w, void* dlogits, moe_stream_t stream);
 

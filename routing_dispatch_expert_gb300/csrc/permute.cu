@@ -1,22 +1,24 @@
-// Tokens sorted by expert: the sort of the assignments, and the rows copied into its order. (The way back is in unpermute.cu.)
+// Tokens sorted by expert: the sort of the assignments, and the rows copied into its order. (The way back is in
+// unpermute.cu.)
 //
-// The sort is a stable counting sort of the T k assignments (token, then slot) by expert: an assignment's rank is the number
-// of earlier ones to its expert, its row the expert's offset plus that (under a placement: round robin over the expert's
-// replicas). Whole numbers only, so the order of the atomics does not show. An index outside [0, E) is no assignment; ranks
-// at and past the capacity have no row.
+// The sort is a stable counting sort of the T k assignments (token, then slot) by expert: an assignment's rank is the
+// number of earlier ones to its expert, its row the expert's offset plus that (under a placement: round robin over the
+// expert's replicas). Whole numbers only, so the order of the atomics does not show. An index outside [0, E) is no
+// assignment; ranks at and past the capacity have no row.
 //   count_kernel  assignments of each block of kItems to each expert
-//   rank_kernel   a block's ranks: the counts of the blocks before it, of the warps before a warp, and within a warp the
-//                 lanes before a lane that hold the same expert; the offsets are made again by every block
+//   rank_kernel   a block's ranks: the counts of the blocks before it, of the warps before a warp, and within a warp
+//                 the lanes before a lane that hold the same expert; the offsets are made again by every block
 // A batch of one block takes the second kernel alone, which then counts its own.
 //
 // Rows are copied as words, token by token: the row is read once and written to each of its places.
 //
-// One GB300: the sort of T k assignments is bound by latency, a few dependent steps a block: 256 x 8 to 256 experts 5.8 us, one
-// launch; 16384 x 8 8.7 us, 65536 x 8 14.2 us (with 1024 experts 16384 x 8 13.4 us: the blocks' counts). A block adds up the
-// others' counts itself instead of a third launch; reading them one after the other with atomics took 11.8 us for 16384 x 8.
-// The copies are bound by HBM: 16384 rows to eight places each, 7168 bytes and scales 164 us (6.6 TB/s, a copy's rate is 6.78),
-// 14336 bytes 315 us (6.7), 65536 rows of 128 bytes 13.5 us (5.6); odd 16-bit rows of 1003 59 us (5.0: 64 bytes an access).
-// Bulk copies out of shared memory, a place each, were slower: 186 us instead of 171 for the rows of 7168 bytes.
+// One GB300: the sort of T k assignments is bound by latency, a few dependent steps a block: 256 x 8 to 256 experts 5.8
+// us, one launch; 16384 x 8 8.7 us, 65536 x 8 14.2 us (with 1024 experts 16384 x 8 13.4 us: the blocks' counts). A
+// block adds up the others' counts itself instead of a third launch; reading them one after the other with atomics took
+// 11.8 us for 16384 x 8. The copies are bound by HBM: 16384 rows to eight places each, 7168 bytes and scales 164 us
+// (6.6 TB/s, a copy's rate is 6.78), 14336 bytes 315 us (6.7), 65536 rows of 128 bytes 13.5 us (5.6); odd 16-bit rows of
+// 1003 59 us (5.0: 64 bytes an access). Bulk copies out of shared memory, a place each, were slower: 186 us instead of 171 for the rows of 7168
+// bytes.
 #include <algorithm>
 #include <type_traits>
 
@@ -84,8 +86,8 @@ __device__ __forceinline__ int block_prefix(int v, int* warp_sums, int& total) {
   return before + incl - v;
 }
 
-// Shared memory: per warp a count of each expert, then the ranks before the warp's [kWarps][E]; for each expert the ranks
-// before this round's [E] and the assignments in all [E]; the offset of each group [max(E, n_slots)].
+// Shared memory: per warp a count of each expert, then the ranks before the warp's [kWarps][E]; for each expert the
+// ranks before this round's [E] and the assignments in all [E]; the offset of each group [max(E, n_slots)].
 constexpr int kEach = 4;  // assignments of a lane in a round
 __global__ void __launch_bounds__(kThreads) rank_kernel(const SortArgs a) {
   extern __shared__ __align__(16) int32_t sh[];
@@ -236,8 +238,8 @@ struct CopyPlane {
   int piece, pieces;  // words of a warp's work, a multiple of 32, and those works of a row
 };
 
-// Words of a lane in a piece, at most: 16 where there are enough pieces for every SM, else 4; one for short rows (16384 rows
-// of 7168 bytes to eight places each: 165 us with the whole row in a piece, 169 with 8, 172 with 4).
+// Words of a lane in a piece, at most: 16 where there are enough pieces for every SM, else 4; one for short rows (16384
+// rows of 7168 bytes to eight places each: 165 us with the whole row in a piece, 169 with 8, 172 with 4).
 constexpr int kDeep = 16;
 
 template <class Word, int DEPTH>
@@ -396,7 +398,7 @@ cudaError_t launch_permute(const PermuteDesc& d, cudaStream_t stream) {
     p.ld = ld / (int64_t)sizeof(Word);
     p.words = (int)(bytes / (int64_t)sizeof(Word));
     const int64_t sms = num_sms();
-    if (p.words <= 16 && !d.xd_scales) {
+    if (p.words <= 16 && !d.xd_scales) {  // 65536 rows of 8 words: 13.5 us, with a warp a row 22.9
       const int lanes = p.words <= 4 ? 4 : p.words <= 8 ? 8 : 16;
       const unsigned blocks = (unsigned)std::min<int64_t>(cdiv((int64_t)d.T * lanes, 256), sms * 32);
       auto kernel = lanes == 4 ? pm::permute_short_kernel<Word, 4>

@@ -2,23 +2,24 @@
 //
 //   t = x + r,  n = t * rstd,  rstd = 1 / sqrt(mean(t^2) + eps),  y = n * w
 //   scale of 128 columns = amax |y| / 448 (at least 2^-126; 1 where all are 0), code = e4m3(RN(y RN(1 / scale)))
-//   with g = dy * w:  dt = rstd * (g - n * mean(g n)) + (the gradient that reaches t from elsewhere),  dw = sum_rows dy n
+//   with g = dy * w:  dt = rstd * (g - n * mean(g n)) + (the gradient that reaches t from elsewhere)
+//                     dw = sum over the rows of dy * n
 //
-// Everything is fp32: the sum is normalised and quantised before it is rounded for the residual stream, and each output is
-// rounded once. The gradient is that of the norm of the t it is given; rstd is made again from t, which it reads anyway,
-// instead of being stored.
+// Everything is fp32: the sum is normalised and quantised before it is rounded for the residual stream, and each output
+// is rounded once. The gradient is that of the norm of the t it is given; rstd is made again from t, which it reads
+// anyway, instead of being stored.
 //
-// Both are bound by HBM: a row is read once and held on the SM between its reduction and its outputs. One GB300, out of HBM (a
-// copy's rate is 6.78 TB/s), x and residual of one type, the gradient with the residual stream's:
+// Both are bound by HBM: a row is read once and held on the SM between its reduction and its outputs. One GB300, out of
+// HBM (a copy's rate is 6.78 TB/s), x and residual of one type, the gradient with the residual stream's:
 //   16384 x 7168 bf16 to bf16 and e4m3 162 us, 6.5 TB/s        its gradient 143 us, 6.6 TB/s
 //   8192 x 7168 fp32                   137 us, 6.9 TB/s                     138 us, 6.8 TB/s
 //   8192 x 7167 bf16 / fp32            101, 4.6 / 138 us, 6.8               139, 3.4 / 161 us, 5.8
 //   65536 x 512 bf16 / 65536 x 64      41, 6.6 / 6.6 us, 5.1                53, 5.0 / 11.6 us, 2.9
 //   one row of 4096                    2.7 us, launch                       5.5 us, two launches
-// Odd 16-bit rows are bound by their number-by-number accesses, narrow ones of the gradient by a barrier a row and its sums.
-// Forward: three blocks of 448 threads an SM for 7168 columns, so that one block's loads run beside another's sums; that takes
-// 42 registers, with the weight loaded behind the reduction (two blocks: 192 us). Backward: one round of blocks, rows copied
-// ahead into shared memory (rows held in registers instead, one block an SM: 167 us; two, spilling: 226).
+// Odd 16-bit rows are bound by their number-by-number accesses, narrow ones of the gradient by a barrier a row and its
+// sums. Forward: three blocks of 448 threads an SM for 7168 columns, so that one block's loads run beside another's
+// sums; that takes 42 registers, with the weight loaded behind the reduction (two blocks: 192 us). Backward: one round of blocks, rows
+// copied ahead into shared memory (rows held in registers instead, one block an SM: 167 us; two, spilling: 226).
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -77,10 +78,10 @@ __device__ __forceinline__ void load_weight(const void* w, int w_f32, int c0, in
   }
 }
 
-// Codes and scales of a chunk: two blocks of 128 columns. The codes are made with the reciprocal, 1.5 ulp of fp32 off the
-// quotient: that moves a code only where y / scale is that close to a midpoint, which unlike for rows of few bits is rare here,
-// and takes one instruction instead of eight. The largest magnitude is taken over the bits, under which a NaN is
-// larger than every number: a block that holds an infinity or a NaN stands for NaN throughout.
+// Codes and scales of a chunk: two blocks of 128 columns. The codes are made with the reciprocal, 1.5 ulp of fp32 off
+// the quotient: that moves a code only where y / scale is that close to a midpoint, which unlike for rows of few bits
+// is rare here, and takes one instruction instead of eight. The largest magnitude is taken over the bits, under which a
+// NaN is larger than every number: a block that holds an infinity or a NaN stands for NaN throughout.
 template <int MAP, int LANES>
 __device__ __forceinline__ void quantize(const Args& a, int64_t row, int c0, int cols, int lane, const float (&y)[8]) {
   uint32_t m[2] = {0u, 0u};
@@ -130,8 +131,8 @@ __device__ __forceinline__ void quantize(const Args& a, int64_t row, int c0, int
   }
 }
 
-// blockDim.x / 32 warps a row, warp w with chunks w, w + W, ..; blockDim.y rows a block. With LANES < 32 a warp has 32 / LANES
-// narrow rows.
+// blockDim.x / 32 warps a row, warp w with chunks w, w + W, ..; blockDim.y rows a block. With LANES < 32 a warp
+// has 32 / LANES narrow rows.
 template <int XT, int RT, int MAP, bool FP8, int CPW, int LANES, int THREADS, int BLOCKS>
 __global__ void __launch_bounds__(THREADS, BLOCKS) norm_kernel(const Args a) {
   __shared__ float part[32];
@@ -205,8 +206,9 @@ struct BackArgs {
 
 constexpr int kGroups = 8;  // warps with rows of their own in a block, where a warp holds one row or several
 
-// A thread's numbers of the rows to come: stages of dy, t and dt, each kWords 16-byte words a chunk. Word w of a stage lies
-// at w * threads + thread, so a warp's words are consecutive. A thread reads back what it copied itself: no barrier.
+// A thread's numbers of the rows to come: stages of dy, t and dt, each kWords 16-byte words a chunk. Word w of a stage
+// lies at w * threads + thread, so a warp's words are consecutive. A thread reads back what it copied itself: no
+// barrier.
 template <int TYPE, int TT, int CPW>
 struct Ring {
   static constexpr int kDy = TYPE == MOE_TYPE_F32 ? 2 : 1, kT = TT == MOE_TYPE_F32 ? 2 : 1;
@@ -220,13 +222,14 @@ constexpr int kMaxRing = 208 * 1024;  // bytes of a block's stages, at most
 template <int TYPE, int TT, int CPW, int THREADS>
 constexpr int kStages = Ring<TYPE, TT, CPW>::bytes(THREADS, 2) <= kMaxRing ? 2 : 1;
 
-// Rows that are not whole 16 bytes: a row's warps copy it as the 16-byte words that cover it, and read their numbers out of
-// those behind a barrier. Its first word may begin in the row before, its last one is copied up to the row's end.
+// Rows that are not whole 16 bytes: a row's warps copy it as the 16-byte words that cover it, and read their numbers
+// out of those behind a barrier. Its first word may begin in the row before, its last one is copied up to the row's
+// end.
 __host__ __device__ __forceinline__ int covering(int cols, int size) { return (cols * size + 15 + 15) / 16; }  // words, at most
 
 // Persistent: a thread has the same columns in every row, so it keeps the weight and the weight's gradient of them in
-// registers, while later rows are copied into shared memory. One row at a time by all warps of a block, or, with GROUPS > 1, a
-// row by each warp, or 32 / LANES narrow ones.
+// registers, while later rows are copied into shared memory. One row at a time by all warps of a block, or, with GROUPS
+// > 1, a row by each warp, or 32 / LANES narrow ones.
 template <int TYPE, int TT, int MAP, int CPW, int LANES, int GROUPS, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 4 : THREADS <= 512 ? 2 : 1) back_kernel(const BackArgs a) {
   extern __shared__ uint4 ring[];
@@ -430,7 +433,7 @@ __global__ void __launch_bounds__(1024) dweight_kernel(const float* part, int n,
 template <int V>
 using Int = std::integral_constant<int, V>;
 
-// Lanes of a row: narrow rows of whole 8 columns share a warp.
+// Lanes of a row: narrow rows of whole 8 columns share a warp (65536 x 64 bf16 6.6 us, with a warp a row 16.7).
 int narrow_lanes(int cols) { return cols % 8 ? 32 : cols <= 32 ? 4 : cols <= 64 ? 8 : cols <= 128 ? 16 : 32; }
 
 // f(type, the other type, map, lanes of a row) of rows of `type` beside rows of `other` (kNone, the same, or fp32)
@@ -474,7 +477,9 @@ cudaError_t launch_rms_norm(const RmsNormDesc& d, cudaStream_t stream) {
   const bool aligned = rows::whole(d.type, d.cols) && (d.rows == 1 || rows::whole(d.type, d.ldx)) &&
                        (d.rows == 1 || !d.residual || rows::whole(d.type, d.ldr));
   const int chunks = (int)cdiv(d.cols, rows::kChunk);
-  const int cpw = chunks > 8 ? 2 : 1;
+  // two chunks a warp wherever there are two (65536 x 384 bf16 31 us, with one 36; 32768 x 2048 with codes 91 and 97;
+  // 32768 x 512 fp32 with codes 44.8 and 44.1); eight rows a block where a warp holds one or several
+  const int cpw = chunks > 1 ? 2 : 1;
   const int W = (int)cdiv(chunks, cpw), G = W == 1 ? 8 : 1;
   const int lanes = aligned ? rn::narrow_lanes(d.cols) : 32;
   return rn::with_types(d.type, d.residual ? d.residual_type : rn::kNone, aligned, lanes, [&](auto T, auto R, auto M, auto L) {
@@ -503,12 +508,14 @@ int back_warps(int cols) { return (int)cdiv(cdiv(cols, rows::kChunk), back_chunk
 
 }  // namespace rn
 
-// Blocks of the gradient's kernel, at most: as many as run at once (fewer where shared memory holds fewer), each at least
-// one row.
+// Blocks of the gradient's kernel, at most: as many as run at once (fewer where shared memory holds fewer), each at
+// least one row.
 int rms_norm_backward_blocks(int64_t rows, int cols) {
   const int W = rn::back_warps(cols), G = W == 1 ? rn::kGroups : 1;
   const int per_sm = W * G <= 8 ? 32 / (W * G) : W <= 14 ? 28 / W : W <= 16 ? 2 : 1;
-  const int64_t few = cdiv(cdiv(rows, G), (int64_t)kNumSMsHint * 4);  // so that a block has several rows to add up
+  // a block of few rows has little to add up: four at least for another block an SM (1000 x 4096 bf16 14.2 us, without
+  // 16.4)
+  const int64_t few = cdiv(cdiv(rows, G), (int64_t)kNumSMsHint * 4);
   return (int)std::max<int64_t>(1, std::min<int64_t>(cdiv(rows, G), kNumSMsHint * std::min<int64_t>(per_sm, few)));
 }
 
@@ -564,7 +571,8 @@ cudaError_t launch_rms_norm_backward(const RmsNormBackwardDesc& d, int* launches
     };
     if (d.cols <= rows::kChunk) return go(rn::Int<1>{}, rn::Int<rn::kGroups>{}, rn::Int<32 * rn::kGroups>{}, 32 * rn::kGroups);
     if constexpr (kL == 32) {
-      // odd rows so wide that an SM holds one block of them: one chunk a warp, for twice the warps
+      // odd rows so wide that an SM holds one block of them: one chunk a warp, for twice the warps (8192 x 7167 fp32
+      // 161 us, with two chunks 201)
       if (kM == rows::kMap1 && d.cols > 4 * rows::kChunk && d.cols <= 32 * rows::kChunk &&
           2 * (rn::covering(d.cols, rows::kSize<kT>) + (d.dtotal ? 2 : 1) * rn::covering(d.cols, rows::kSize<kR>)) * 16 > 110 * 1024)
         return go(rn::Int<1>{}, rn::Int<1>{}, rn::Int<1024>{}, 32 * (int)cdiv(d.cols, rows::kChunk));

@@ -5,16 +5,17 @@
 //   softmax, renorm.  w_j = c u_j, u = softmax of the chosen ones:  dl_{e_j} = c u_j (g_j - sum_i g_i u_i)
 //   sigmoid           w_j = c s_j, s = sigmoid(l_{e_j}):            dl_{e_j} = c s_j (1 - s_j) g_j
 //   sigmoid, renorm.  w_j = c u_j, u_j = s_j / sum_i s_i:           dl_{e_j} = c u_j (1 - s_j) (g_j - sum_i g_i u_i)
-// G_e adds the g_j of the slots that chose e (an expert chosen twice gets both); 0 where nothing is said. The selection and
-// its bias carry no gradient. Slots whose index lies outside [0, E) are left out.
+// G_e adds the g_j of the slots that chose e (an expert chosen twice gets both); 0 where nothing is said. The selection
+// and its bias carry no gradient. Slots whose index lies outside [0, E) are left out.
 //
-// fp32. Sigmoids are taken with e^min(l) factored out of their sum, so that a token whose sigmoids all underflow keeps their
-// ratios; a token whose chosen logits are all -inf has no weights and a gradient of 0.
+// fp32. Sigmoids are taken with e^min(l) factored out of their sum, so that a token whose sigmoids all underflow keeps
+// their ratios; a token whose chosen logits are all -inf has no weights and a gradient of 0.
 //
-// One GB300: 65536 tokens x 256 experts, k 8, fp32: chosen experts alone 20.6 us. Its bytes, dlogits and the 8 logits a token, are
-// 11 us at a copy's rate, but the logits come in pieces of 64 bytes: 46 MB are read and 67 written, 17 us. Softmax over all
-// 24.6 us (5.5 TB/s of 6.78), bf16 23.9: latency, a token's loads and sums in a row. 4096 x 8: 2.4 us, launch. Four tokens a warp
-// instead of one for the chosen experts: 33 -> 20 us; all loads of a token asked for together: 30 -> 24.6 us (softmax).
+// One GB300: 65536 tokens x 256 experts, k 8, fp32: chosen experts alone 20.6 us. Its bytes, dlogits and the 8 logits a
+// token, are 11 us at a copy's rate, but the logits come in pieces of 64 bytes: 46 MB are read and 67 written, 17 us.
+// Softmax over all 24.6 us (5.5 TB/s of 6.78), bf16 23.9: latency, a token's loads and sums in a row. 4096 x 8: 2.4 us,
+// launch. Four tokens a warp instead of one for the chosen experts: 33 -> 20 us; all loads of a token asked for together:
+// 30 -> 24.6 us (softmax).
 #include <algorithm>
 #include <type_traits>
 
@@ -29,8 +30,8 @@ constexpr int kThreads = 256;
 constexpr int kMaxE = 1024;
 constexpr float kLog2e = 1.4426950408889634f;
 
-// 2 ulp. A probability e^(l - m) is taken as 2^(log2(e) (l - m)): the product's rounding is |x| 2^-24 of an exponent x, that is
-// below 2e-6 of a probability of 1e-8, and less of larger ones.
+// 2 ulp. A probability e^(l - m) is taken as 2^(log2(e) (l - m)): the product's rounding is |x| 2^-24 of an exponent x,
+// that is below 2e-6 of a probability of 1e-8, and less of larger ones.
 __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -75,8 +76,8 @@ __device__ __forceinline__ float slot_logit(const Args& a, int64_t t, int& e, fl
   return -INFINITY;
 }
 
-// The gradients of the slots that chose this lane's expert, and how many they are: an expert chosen twice gets both, and each
-// of its slots writes the same sum.
+// The gradients of the slots that chose this lane's expert, and how many they are: an expert chosen twice gets both,
+// and each of its slots writes the same sum.
 template <int L>
 __device__ __forceinline__ void same_expert(int k, int e, float g, float& all, float& n) {
   all = g;
@@ -94,8 +95,9 @@ __device__ __forceinline__ void same_expert(int k, int e, float g, float& all, f
   }
 }
 
-// Weights of the chosen experts alone: L lanes a token (k rounded up to a power of two), lane j slot j. The rows of a warp's
-// tokens lie one after the other and are zeroed as one; the slots then write over that, behind a barrier of the warp.
+// Weights of the chosen experts alone: L lanes a token (k rounded up to a power of two), lane j slot j. The rows of a
+// warp's tokens lie one after the other and are zeroed as one; the slots then write over that, behind a barrier of the
+// warp.
 template <int TYPE, bool SIGMOID, int L>
 __global__ void __launch_bounds__(kThreads) chosen_kernel(const Args a) {
   constexpr int kPer = 32 / L;  // tokens of a warp
@@ -141,8 +143,8 @@ __global__ void __launch_bounds__(kThreads) chosen_kernel(const Args a) {
   }
 }
 
-// A softmax over all experts: L lanes a token, at least k, a lane the experts 4 (sub + L j) + i, EPL of them; all of them write
-// the dense part -c p sum_j g_j p_{e_j}, then lane j slot j over that.
+// A softmax over all experts: L lanes a token, at least k, a lane the experts 4 (sub + L j) + i, EPL of them; all of
+// them write the dense part -c p sum_j g_j p_{e_j}, then lane j slot j over that.
 template <int TYPE, int L, int EPL>
 __global__ void __launch_bounds__(kThreads) dense_kernel(const Args a) {
   constexpr int kPer = 32 / L;  // tokens of a warp

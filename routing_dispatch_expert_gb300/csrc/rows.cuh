@@ -2,13 +2,14 @@
 // read and write them: a warp takes 256 consecutive columns (a chunk) at a time, a lane 8 of them, held as fp32.
 //
 // Which 8 depends on how the rows lie in memory (MAP):
-//   kMap8  rows that are whole 16 bytes and begin on 16, 16-bit numbers: columns 8 lane .. 8 lane + 7, one 16-byte access
-//   kMap4  the same for fp32: columns 4 lane .. + 3 and 128 + 4 lane .. + 3, so that both accesses are whole lines; 16-bit rows
-//          beside fp32 ones take two 8-byte accesses for it
-//   kMap1  rows of any width that begin anywhere: columns lane + 32 i, one number an access. A warp's access is then 64 or 128
-//          consecutive bytes; with 8 consecutive numbers a lane it would be 32 pieces of four lines.
-// Every chunk is 256 columns in all of them, so a lane's columns are the same in every row, and the blocks of 128 columns
-// that share an 8-bit scale are half a chunk.
+//   kMap8  rows that are whole 16 bytes and begin on 16, 16-bit numbers: columns 8 lane .. 8 lane + 7, one 16-byte
+//          access
+//   kMap4  the same for fp32: columns 4 lane .. + 3 and 128 + 4 lane .. + 3, so that both accesses are whole lines;
+//          16-bit rows beside fp32 ones take two 8-byte accesses for it
+//   kMap1  rows of any width that begin anywhere: columns lane + 32 i, one number an access. A warp's access is then 64
+//          or 128 consecutive bytes; with 8 consecutive numbers a lane it would be 32 pieces of four lines.
+// Every chunk is 256 columns in all of them, so a lane's columns are the same in every row, and the blocks of 128
+// columns that share an 8-bit scale are half a chunk.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -67,8 +68,8 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
   return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
-// A lane's 8 numbers of a chunk as they lie in memory: nothing is done with them until values(), so the loads of several
-// chunks and tensors are in flight together. c0: first column of the chunk; columns at and past cols are 0.
+// A lane's 8 numbers of a chunk as they lie in memory: nothing is done with them until values(), so the loads of
+// several chunks and tensors are in flight together. c0: first column of the chunk; columns at and past cols are 0.
 template <int TYPE, int MAP>
 struct Chunk {
   static constexpr bool kWide = TYPE == MOE_TYPE_F32;
@@ -144,8 +145,8 @@ __device__ __forceinline__ void store(void* row, int c0, int cols, int lane, con
   }
 }
 
-// The first n of 16 bytes of global memory into shared memory, zeros behind them: complete once the group they are committed
-// in is waited for.
+// The first n of 16 bytes of global memory into shared memory, zeros behind them: complete once the group they are
+// committed in is waited for.
 __device__ __forceinline__ void copy16(uint32_t to, const void* from, int n) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(n) : "memory");
 }

@@ -3,12 +3,13 @@
 //   y[t] = base[t] + sum_j w[t, j] yd[p[t, j]]                      in slot order, fp32, rounded once
 //   dyd[p[t, j]] = w[t, j] dy[t],   dw[t, j] = <yd[p[t, j]], dy[t]>  fp32
 //
-// Both go token by token, so that the k uses of a token's row meet; the k rows elsewhere are read (and written) once. The rows of a
-// chunk are all loaded before any is worked on, and a token's positions are looked up once for many chunks.
+// Both go token by token, so that the k uses of a token's row meet; the k rows elsewhere are read (and written) once.
+// The rows of a chunk are all loaded before any is worked on, and a token's positions are looked up once for many
+// chunks.
 //
-// Bound by HBM. One GB300, k 8 (a copy's rate is 6.78 TB/s): 16384 x 7168 bf16 with weights and base 345 us, 6.8 TB/s, the
-// gradient with the weights' 601 us, 6.6; 8192 x 7168 fp32 331 and 589 us; 65536 x 64 bf16 20 and 28 us (4.4 and 5.4 TB/s); odd
-// 16-bit rows 8192 x 7167 257 and 416 us (4.6 and 4.8: 64 bytes an access); 64 x 512, k 2 2.4 us, launch.
+// Bound by HBM. One GB300, k 8 (a copy's rate is 6.78 TB/s): 16384 x 7168 bf16 with weights and base 345 us, 6.8 TB/s,
+// the gradient with the weights' 601 us, 6.6; 8192 x 7168 fp32 331 and 589 us; 65536 x 64 bf16 20 and 28 us (4.4 and
+// 5.4 TB/s); odd 16-bit rows 8192 x 7167 257 and 416 us (4.6 and 4.8: 64 bytes an access); 64 x 512, k 2 2.4 us, launch.
 #include <algorithm>
 #include <type_traits>
 
@@ -21,8 +22,8 @@ namespace un {
 
 using std::integral_constant;
 
-// Rows and weights of the slots j0 .. j0 + KB - 1 of token t, in each of its LANES lanes; -1 past the last slot, and for
-// positions outside the T k rows.
+// Rows and weights of the slots j0 .. j0 + KB - 1 of token t, in each of its LANES lanes; -1 past the last slot, and
+// for positions outside the T k rows.
 template <int KB, int LANES>
 __device__ __forceinline__ void slots(const int32_t* inv_pos, const float* weights, int64_t t, int64_t T, int k, int j0,
                                       int (&row)[KB], float (&w)[KB]) {
@@ -63,8 +64,8 @@ struct AddArgs {
   int piece, pieces;  // chunks of a warp's work, and those works of a row
 };
 
-// A warp a piece of a token's row, or LANES lanes a whole narrow row: fp32, the base first and then the slots in order. KB: slots at
-// a time, a power of two at or above k, at most 8.
+// A warp a piece of a token's row, or LANES lanes a whole narrow row: fp32, the base first and then the slots in order.
+// KB: slots at a time, a power of two at or above k, at most 8.
 template <int TYPE, int MAP, int KB, int LANES>
 __global__ void __launch_bounds__(256, (kBlocks<TYPE, MAP, KB>)) unpermute_kernel(const AddArgs a) {
   constexpr int kTokens = 32 / LANES;
@@ -123,9 +124,9 @@ struct SpreadArgs {
   int cols, chunks, k;
 };
 
-// A group of W warps a token (blockDim.x / 32, blockDim.y groups a block where W is 1), or LANES lanes a narrow row: its row of dy to
-// its k rows of dyd, and their products with yd's rows, summed over the lanes and then the warps. At the end the warps clear
-// the rows that hold nothing.
+// A group of W warps a token (blockDim.x / 32, blockDim.y groups a block where W is 1), or LANES lanes a narrow row:
+// its row of dy to its k rows of dyd, and their products with yd's rows, summed over the lanes and then the warps. At
+// the end the warps clear the rows that hold nothing.
 template <int TYPE, int MAP, int KB, int LANES>
 __global__ void __launch_bounds__(256, (kBlocks<TYPE, MAP, KB>)) spread_kernel(const SpreadArgs a) {
   constexpr int kTokens = 32 / LANES;
@@ -197,7 +198,9 @@ __global__ void __launch_bounds__(256, (kBlocks<TYPE, MAP, KB>)) spread_kernel(c
       rows::store<TYPE, MAP>(static_cast<char*>(a.dyd) + r * pitch, c * rows::kChunk, a.cols, lane, f);
 }
 
-// f(type, map, slots at a time, lanes of a row). Rows of up to 64 and 128 columns of whole 16 bytes take 8 and 16 lanes.
+// f(type, map, slots at a time, lanes of a row). Rows of up to 64 and 128 columns of whole 16 bytes take 8 and 16 lanes
+// (65536 x 64 bf16 20 us, with a warp a row 45); two or four slots leave registers for more blocks (65536 x 512, k 2:
+// 52 us, with eight 58).
 template <class F>
 cudaError_t with_rows(int type, int64_t cols, int k, F&& f) {
   const bool whole = rows::whole(type, cols);
@@ -236,7 +239,8 @@ cudaError_t launch_unpermute(const UnpermuteDesc& d, cudaStream_t stream) {
   a.chunks = (int)cdiv(d.cols, rows::kChunk);
   a.k = d.k;
   // a warp's work: up to 16 chunks of a row, fewer where there would be less than 32 works an SM (7168 columns of 16384
-  // tokens: 339 us with 14 chunks, 343 with 7 or 4, 480 with one, whose rows' numbers are then looked up for every chunk)
+  // tokens: 339 us with 14 chunks, 343 with 7 or 4, 480 with one, whose rows' numbers are then looked up for every
+  // chunk)
   const int64_t pieces = std::max<int64_t>(cdiv(a.chunks, 16), std::min<int64_t>(a.chunks, cdiv(32 * num_sms(), a.T)));
   a.piece = (int)cdiv(a.chunks, pieces);
   a.pieces = (int)cdiv(a.chunks, a.piece);
@@ -262,8 +266,8 @@ cudaError_t launch_unpermute_backward(const UnpermuteBackwardDesc& d, cudaStream
   a.cols = d.cols;
   a.chunks = (int)cdiv(d.cols, rows::kChunk);
   a.k = d.k;
-  // warps of a token: four, up to eight where few tokens would leave SMs idle (16384 tokens of 7168 columns: 600 us with four
-  // or two, 637 with eight: every token ends in a barrier and a sum over the warps)
+  // warps of a token: four, up to eight where few tokens would leave SMs idle (16384 tokens of 7168 columns: 600 us
+  // with four or two, 637 with eight: every token ends in a barrier and a sum over the warps)
   const int64_t most = std::min<int64_t>(8, std::max<int64_t>(4, cdiv(24 * num_sms(), a.T)));
   const int W = (int)cdiv(a.chunks, cdiv(a.chunks, most)), G = W == 1 ? 8 : 1;
   return un::with_rows(d.type, d.cols, d.k, [&](auto T, auto M, auto K, auto L) {
