@@ -17,13 +17,15 @@
 // block adds up the others' counts itself instead of a third launch; reading them one after the other with atomics took
 // 11.8 us for 16384 x 8. The copies are bound by HBM: 16384 rows to eight places each, 7168 bytes and scales 164 us
 // (6.6 TB/s, a copy's rate is 6.78), 14336 bytes 315 us (6.7), 65536 rows of 128 bytes 13.5 us (5.6); odd 16-bit rows of
-// 1003 59 us (5.0: 64 bytes an access). Bulk copies out of shared memory, a place each, were slower: 186 us instead of 171 for the rows of 7168
-// bytes.
+// 1003 59 us (5.0: 64 bytes an access). Slower: bulk copies out of shared memory, a place each (186 us instead of 171 for the
+// rows of 7168 bytes); odd rows by the 16-byte words of their places, shifted (65536 x 511 bf16 with the sort 196 us
+// instead of 135: the parts of words at a row's ends; only rows of kilobytes gain, 215 to 195 for 8192 x 7167).
 #include <algorithm>
 #include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
+#include "rows.cuh"
 
 namespace moe {
 namespace pm {
@@ -238,8 +240,10 @@ struct CopyPlane {
   int piece, pieces;  // words of a warp's work, a multiple of 32, and those works of a row
 };
 
-// Words of a lane in a piece, at most: 16 where there are enough pieces for every SM, else 4; one for short rows (16384
-// rows of 7168 bytes to eight places each: 165 us with the whole row in a piece, 169 with 8, 172 with 4).
+// Words of a lane in a piece, at most: 16 where there are enough pieces for every SM, else 4 (16384 rows of 7168 bytes to
+// eight places each: 165 us with the whole row in a piece, 169 with 8, 172 with 4). A kernel for every few numbers of
+// words, since each is an instruction for every place (65536 rows of 129 codes of 8 bits, with scales and sort: 59.8 us,
+// with room for 16 words 90).
 constexpr int kDeep = 16;
 
 template <class Word, int DEPTH>
@@ -270,27 +274,37 @@ __device__ __forceinline__ void copy_item(const CopyPlane& p, const int32_t* inv
   }
 }
 
-// Rows of at most LANES words: 32 / LANES of them a warp, a lane one word of each of its row's places.
-template <class Word, int LANES>
-__global__ void __launch_bounds__(256) permute_short_kernel(const CopyPlane p, const int32_t* inv_pos, const int32_t* held_at,
-                                                            int64_t T, int k) {
+// Rows of at most N LANES words: 32 / LANES of them a warp, a lane N words of each of its row's places, and one of the
+// row's scales, of which there are at most LANES.
+template <class Word, int LANES, int N>
+__global__ void __launch_bounds__(256) permute_short_kernel(const CopyPlane p, const CopyPlane scales, const int32_t* inv_pos,
+                                                            const int32_t* held_at, int64_t T, int k) {
   const int sub = threadIdx.x % LANES;
-  const int64_t groups = (int64_t)gridDim.x * blockDim.x / LANES;
-  const int64_t held = min(max((int64_t)*held_at, (int64_t)0), T * k), rows = T + (T * k - held);
-  if (sub >= p.words) return;
-  Word* const dst = static_cast<Word*>(p.dst) + sub;
-  for (int64_t t = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / LANES; t < rows; t += groups) {
-    if (t >= T) {
-      dst[(held + (t - T)) * p.words] = Word{};
-      continue;
-    }
-    const Word v = static_cast<const Word*>(p.src)[t * p.ld + sub];
+  const int64_t thread = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, threads = (int64_t)gridDim.x * blockDim.x;
+  const int64_t held = min(max((int64_t)*held_at, (int64_t)0), T * k);
+  const bool scaled = sub < scales.words;
+  for (int64_t t = thread / LANES; t < T; t += threads / LANES) {
+    const Word* const src = static_cast<const Word*>(p.src) + t * p.ld;
+    Word v[N];
+    uint32_t scale = 0;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+      if (sub + LANES * n < p.words) v[n] = src[sub + LANES * n];
+    if (scaled) scale = static_cast<const uint32_t*>(scales.src)[t * scales.words + sub];
 #pragma unroll 8
     for (int j = 0; j < k; ++j) {
       const int r = inv_pos[t * k + j];
-      if (r >= 0 && r < T * k) dst[(int64_t)r * p.words] = v;
+      if (r < 0 || r >= T * k) continue;
+      Word* const dst = static_cast<Word*>(p.dst) + (int64_t)r * p.words;
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+        if (sub + LANES * n < p.words) dst[sub + LANES * n] = v[n];
+      if (scaled) static_cast<uint32_t*>(scales.dst)[(int64_t)r * scales.words + sub] = scale;
     }
   }
+  const int64_t bytes = (int64_t)p.words * sizeof(Word);
+  rows::clear<sizeof(Word) < 4 ? sizeof(Word) : 4>(p.dst, held * bytes, T * k * bytes, thread, threads);
+  if (scales.words) rows::clear<4>(scales.dst, 4 * held * scales.words, 4 * T * k * scales.words, thread, threads);
 }
 
 template <class Word, int DEPTH>
@@ -398,36 +412,47 @@ cudaError_t launch_permute(const PermuteDesc& d, cudaStream_t stream) {
     p.ld = ld / (int64_t)sizeof(Word);
     p.words = (int)(bytes / (int64_t)sizeof(Word));
     const int64_t sms = num_sms();
-    if (p.words <= 16 && !d.xd_scales) {  // 65536 rows of 8 words: 13.5 us, with a warp a row 22.9
-      const int lanes = p.words <= 4 ? 4 : p.words <= 8 ? 8 : 16;
-      const unsigned blocks = (unsigned)std::min<int64_t>(cdiv((int64_t)d.T * lanes, 256), sms * 32);
-      auto kernel = lanes == 4 ? pm::permute_short_kernel<Word, 4>
-                               : lanes == 8 ? pm::permute_short_kernel<Word, 8> : pm::permute_short_kernel<Word, 16>;
-      kernel<<<blocks, 256, 0, stream>>>(p, d.inv_pos, d.held, d.T, d.k);
-      return cudaGetLastError();
-    }
-    const bool deep = p.words > 128 && d.T * cdiv(p.words, 512) >= sms * 32;
-    const auto cut = [&](pm::CopyPlane& q) {  // even pieces of whole steps of 32 words
-      const int steps = (int)cdiv(q.words, 32);
-      q.piece = 32 * (int)cdiv(steps, cdiv(steps, deep ? pm::kDeep : p.words <= 32 ? 1 : 4));
-      q.pieces = (int)cdiv(q.words, q.piece);
-    };
-    cut(p);
     if (d.xd_scales) {
       s.src = d.x_scales;
       s.dst = d.xd_scales;
       s.ld = s.words = (int)cdiv(d.cols, 128);
-      cut(s);
     }
+    // Rows of few words share a warp: 65536 rows of 8 words of 16 bytes 13.5 us, with a warp a row 22.9; with their sort
+    // (14 us), 33 numbers of 16 bits 28.6 and 33.4 us, 33 codes of 8 bits and their scales 28.3 and 48.2 us.
+    if (p.words <= 64) {
+      const int lanes = p.words <= 4 ? 4 : p.words <= 8 ? 8 : 16;
+      const unsigned blocks = (unsigned)std::min<int64_t>(cdiv((int64_t)d.T * lanes, 256), sms * 32);
+      auto kernel = lanes == 4    ? pm::permute_short_kernel<Word, 4, 1>
+                    : lanes == 8  ? pm::permute_short_kernel<Word, 8, 1>
+                    : p.words <= 16 ? pm::permute_short_kernel<Word, 16, 1>
+                    : p.words <= 32 ? pm::permute_short_kernel<Word, 16, 2>
+                    : p.words <= 48 ? pm::permute_short_kernel<Word, 16, 3> : pm::permute_short_kernel<Word, 16, 4>;
+      kernel<<<blocks, 256, 0, stream>>>(p, s, d.inv_pos, d.held, d.T, d.k);
+      return cudaGetLastError();
+    }
+    // words of a lane in a piece, at most: a long row's in one piece where there are enough pieces for every SM
+    const bool enough = d.T * cdiv(p.words, 32 * pm::kDeep) >= sms * 32;
+    const int steps = (int)cdiv(p.words, 32), most = enough ? pm::kDeep : 4;
+    const int step = (int)cdiv(steps, cdiv(steps, most));  // of a piece: even ones
+    const auto cut = [&](pm::CopyPlane& q) {
+      q.piece = 32 * step;
+      q.pieces = (int)cdiv(q.words, q.piece);
+    };
+    cut(p);
+    if (s.words) cut(s);
     const int64_t items = (int64_t)d.T * (p.pieces + (d.xd_scales ? s.pieces : 0));
     const unsigned blocks = (unsigned)std::min<int64_t>(cdiv(items, 8), sms * 16);
-    if (p.words <= 32)
-      pm::permute_kernel<Word, 1><<<blocks, 256, 0, stream>>>(p, s, d.inv_pos, d.held, d.T, d.k);
-    else if (deep)
-      pm::permute_kernel<Word, pm::kDeep><<<blocks, 256, 0, stream>>>(p, s, d.inv_pos, d.held, d.T, d.k);
-    else
-      pm::permute_kernel<Word, 4><<<blocks, 256, 0, stream>>>(p, s, d.inv_pos, d.held, d.T, d.k);
-    return cudaGetLastError();
+    const auto go = [&](auto kernel) {
+      kernel<<<blocks, 256, 0, stream>>>(p, s, d.inv_pos, d.held, d.T, d.k);
+      return cudaGetLastError();
+    };
+    if (step <= 1) return go(pm::permute_kernel<Word, 1>);
+    if (step <= 2) return go(pm::permute_kernel<Word, 2>);
+    if (step <= 4) return go(pm::permute_kernel<Word, 4>);
+    if (step <= 6) return go(pm::permute_kernel<Word, 6>);
+    if (step <= 9) return go(pm::permute_kernel<Word, 9>);
+    if (step <= 12) return go(pm::permute_kernel<Word, 12>);
+    return go(pm::permute_kernel<Word, pm::kDeep>);
   });
 }
 

@@ -15,11 +15,14 @@
 //   8192 x 7168 fp32                   137 us, 6.9 TB/s                     138 us, 6.8 TB/s
 //   8192 x 7167 bf16 / fp32            101, 4.6 / 138 us, 6.8               139, 3.4 / 161 us, 5.8
 //   65536 x 512 bf16 / 65536 x 64      41, 6.6 / 6.6 us, 5.1                53, 5.0 / 11.6 us, 2.9
+//   65536 x 511 bf16 / 65536 x 33      53, 5.0 / 6.5 us, 2.7               87, 3.1 / 14.7 us, 1.2
 //   one row of 4096                    2.7 us, launch                       5.5 us, two launches
 // Odd 16-bit rows are bound by their number-by-number accesses, narrow ones of the gradient by a barrier a row and its
 // sums. Forward: three blocks of 448 threads an SM for 7168 columns, so that one block's loads run beside another's
-// sums; that takes 42 registers, with the weight loaded behind the reduction (two blocks: 192 us). Backward: one round of blocks, rows
-// copied ahead into shared memory (rows held in registers instead, one block an SM: 167 us; two, spilling: 226).
+// sums; that takes 42 registers, with the weight loaded behind the reduction (two blocks: 192 us). Backward: one
+// round of blocks, rows copied ahead into shared memory (rows held in registers instead, one block an SM: 167 us; two,
+// spilling: 226). Rows of up to 128 columns share a warp (65536 x 64 bf16 6.6 us, with a warp a row 16.7; 65536 x 33 6.5
+// and 18.8, its gradient 14.7 and 39).
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -62,17 +65,17 @@ __device__ __forceinline__ float lanes_sum(float v) {
 }
 
 // A chunk of the weight; ones where there is none.
-template <int TYPE, int MAP>
+template <int TYPE, int MAP, int LANES>
 __device__ __forceinline__ void load_weight(const void* w, int w_f32, int c0, int cols, int lane, float (&f)[8]) {
   if (!w) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = 1.f;
   } else if (w_f32) {
-    Chunk<MOE_TYPE_F32, MAP> c;
+    Chunk<MOE_TYPE_F32, MAP, LANES> c;
     c.load(w, c0, cols, lane);
     c.values(f);
   } else {
-    Chunk<TYPE, MAP> c;
+    Chunk<TYPE, MAP, LANES> c;
     c.load(w, c0, cols, lane);
     c.values(f);
   }
@@ -84,13 +87,14 @@ __device__ __forceinline__ void load_weight(const void* w, int w_f32, int c0, in
 // NaN is larger than every number: a block that holds an infinity or a NaN stands for NaN throughout.
 template <int MAP, int LANES>
 __device__ __forceinline__ void quantize(const Args& a, int64_t row, int c0, int cols, int lane, const float (&y)[8]) {
+  constexpr bool kOne = MAP == kMap8 || LANES < 32;  // a lane's columns lie in one block
   uint32_t m[2] = {0u, 0u};
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int h = MAP == kMap8 ? 0 : i / 4;
+    const int h = kOne ? 0 : i / 4;
     m[h] = max(m[h], __float_as_uint(y[i]) & 0x7FFFFFFFu);
   }
-  if (MAP == kMap8) {
+  if (kOne) {
 #pragma unroll
     for (int o = (LANES < 16 ? LANES : 16) / 2; o > 0; o >>= 1) m[0] = max(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
   } else {
@@ -100,15 +104,15 @@ __device__ __forceinline__ void quantize(const Args& a, int64_t row, int c0, int
   const int nb = (a.cols + 127) / 128;
   float v[8];
 #pragma unroll
-  for (int h = 0; h < (MAP == kMap8 ? 1 : 2); ++h) {
-    constexpr int kN = MAP == kMap8 ? 8 : 4;
+  for (int h = 0; h < (kOne ? 1 : 2); ++h) {
+    constexpr int kN = kOne ? 8 : 4;
     float scale = 1.f;
     if (m[h]) scale = m[h] > kInfBits ? __uint_as_float(m[h]) : fmaxf(__fdiv_rn(__uint_as_float(m[h]), 448.0f), 1.1754944e-38f);
     const float by = __frcp_rn(scale);
 #pragma unroll
     for (int i = 0; i < kN; ++i) v[4 * h + i] = y[4 * h + i] * by;
-    const int b = c0 / 128 + (MAP == kMap8 ? lane / 16 : h);
-    if ((MAP == kMap8 ? lane % 16 : lane) == 0 && b < nb && cols > 0) a.s[row * nb + b] = scale;
+    const int b = c0 / 128 + (kOne ? lane / 16 : h);
+    if ((kOne ? lane % 16 : lane) == 0 && b < nb && cols > 0) a.s[row * nb + b] = scale;
   }
   uint32_t code[4];
 #pragma unroll
@@ -125,7 +129,7 @@ __device__ __forceinline__ void quantize(const Args& a, int64_t row, int c0, int
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int c = rows::column<MAP>(lane, i);
+      const int c = rows::column<MAP, LANES>(lane, i);
       if (c0 + c < cols) q[c] = (uint8_t)(code[i / 2] >> (8 * (i & 1)));
     }
   }
@@ -142,8 +146,8 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_kernel(const Args a) {
   const int cols = row < a.rows ? a.cols : 0;
   float t[CPW][8];
   {
-    Chunk<XT, MAP> x[CPW];
-    Chunk<kRT, MAP> r[CPW];
+    Chunk<XT, MAP, LANES> x[CPW];
+    Chunk<kRT, MAP, LANES> r[CPW];
     const char* xr = static_cast<const char*>(a.x) + row * a.ldx * rows::kSize<XT>;
     const char* rr = RT == kNone ? nullptr : static_cast<const char*>(a.r) + row * a.ldr * rows::kSize<kRT>;
 #pragma unroll
@@ -180,12 +184,12 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_kernel(const Args a) {
     const int c0 = (warp + j * W) * kChunk;
     if (LANES == 32 && c0 >= cols) break;
     if (RT != kNone && a.total)
-      rows::store<kRT, MAP>(static_cast<char*>(a.total) + row * a.cols * rows::kSize<kRT>, c0, cols, lane, t[j]);
+      rows::store<kRT, MAP, LANES>(static_cast<char*>(a.total) + row * a.cols * rows::kSize<kRT>, c0, cols, lane, t[j]);
     float y[8], w[8];
-    load_weight<XT, MAP>(a.w, a.w_f32, c0, a.cols, lane, w);
+    load_weight<XT, MAP, LANES>(a.w, a.w_f32, c0, a.cols, lane, w);
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = t[j][i] * rstd * w[i];
-    if (a.y) rows::store<XT, MAP>(static_cast<char*>(a.y) + row * a.cols * rows::kSize<XT>, c0, cols, lane, y);
+    if (a.y) rows::store<XT, MAP, LANES>(static_cast<char*>(a.y) + row * a.cols * rows::kSize<XT>, c0, cols, lane, y);
     if (FP8) quantize<MAP, LANES>(a, row, c0, cols, lane, y);
   }
 }
@@ -222,8 +226,8 @@ constexpr int kMaxRing = 208 * 1024;  // bytes of a block's stages, at most
 template <int TYPE, int TT, int CPW, int THREADS>
 constexpr int kStages = Ring<TYPE, TT, CPW>::bytes(THREADS, 2) <= kMaxRing ? 2 : 1;
 
-// Rows that are not whole 16 bytes: a row's warps copy it as the 16-byte words that cover it, and read their numbers
-// out of those behind a barrier. Its first word may begin in the row before, its last one is copied up to the row's
+// Rows that are not whole 16 bytes: a row's warps (or its lanes) copy it as the 16-byte words that cover it, and read
+// their numbers out of those behind a barrier. Its first word may begin in the row before, its last one is copied up to the row's
 // end.
 __host__ __device__ __forceinline__ int covering(int cols, int size) { return (cols * size + 15 + 15) / 16; }  // words, at most
 
@@ -243,7 +247,7 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 4 : THREADS <= 512 ?
   float w[CPW][8], dw[CPW][8];
 #pragma unroll
   for (int j = 0; j < CPW; ++j) {
-    load_weight<TYPE, MAP>(a.w, a.w_f32, (warp + j * W) * kChunk, a.cols, lane, w[j]);
+    load_weight<TYPE, MAP, LANES>(a.w, a.w_f32, (warp + j * W) * kChunk, a.cols, lane, w[j]);
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[j][i] = 0.f;
   }
@@ -255,13 +259,15 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 4 : THREADS <= 512 ?
   const int words[3] = {0, MAP == kMap1 ? covering(a.cols, rows::kSize<TYPE>) : CPW * R::kDy,
                         MAP == kMap1 ? covering(a.cols, rows::kSize<TYPE>) + covering(a.cols, rows::kSize<TT>)
                                      : CPW * (R::kDy + R::kT)};
-  uint4* const mine = MAP == kMap1 ? ring + (int64_t)group * a.stages * a.stage : ring;  // of this warp's rows
+  constexpr int kRows = 32 / LANES;  // of a warp
+  const int sub = (threadIdx.x & 31) / LANES;  // the lane's row of those
+  uint4* const mine = MAP == kMap1 ? ring + (group * kRows + sub) * a.stages * a.stage : ring;  // of this row
   auto copy = [&](auto type, int which, int slot, int64_t row) {
     constexpr int kType = decltype(type)::value;
     const char* p = from[which] + row * pitch[which];
     if constexpr (MAP == kMap1) {
       const int off = (int)(reinterpret_cast<uintptr_t>(p) & 15), end = off + a.cols * rows::kSize<kType>;
-      for (int b = 16 * (GROUPS > 1 ? threadIdx.x & 31 : threadIdx.x); b < end; b += 16 * 32 * W)
+      for (int b = 16 * (GROUPS > 1 ? lane : threadIdx.x); b < end; b += 16 * LANES * W)
         rows::copy16(smem_u32(mine + slot * a.stage + words[which]) + b, p - off + b, min(16, end - b));
     } else {
       constexpr bool kHalves = kType != MOE_TYPE_F32 && MAP == kMap4;  // 8 bytes and 8 bytes of one word
@@ -283,7 +289,7 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 4 : THREADS <= 512 ?
   };
   auto numbers = [&](auto type, int which, int slot, int64_t row, int j, float (&f)[8]) {
     constexpr int kType = decltype(type)::value;
-    Chunk<kType, MAP> c;
+    Chunk<kType, MAP, LANES> c;
     if constexpr (MAP == kMap1) {
       const int off = (int)(reinterpret_cast<uintptr_t>(from[which] + row * pitch[which]) & 15);
       c.load(reinterpret_cast<const char*>(mine + slot * a.stage + words[which]) + off, (warp + j * W) * kChunk, a.cols, lane);
@@ -297,15 +303,16 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 4 : THREADS <= 512 ?
     }
     c.values(f);
   };
-  constexpr int kRows = 32 / LANES;  // of a warp
   const int64_t step = (int64_t)gridDim.x * GROUPS * kRows;
   int64_t first = ((int64_t)blockIdx.x * GROUPS + group) * kRows;  // the warp's
   auto fetch = [&](int slot, int64_t at) {
     if (at < a.rows) {
-      const int64_t row = at + (threadIdx.x & 31) / LANES;
-      copy(Dy{}, 0, slot, row);
-      copy(T{}, 1, slot, row);
-      if (a.dt) copy(T{}, 2, slot, row);
+      const int64_t row = at + sub;
+      if (MAP != kMap1 || LANES == 32 || row < a.rows) {
+        copy(Dy{}, 0, slot, row);
+        copy(T{}, 1, slot, row);
+        if (a.dt) copy(T{}, 2, slot, row);
+      }
     }
     rows::copies_commit();
   };
@@ -330,7 +337,7 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 4 : THREADS <= 512 ?
     } else {
       rows::copies_wait<S - 1>();
     }
-    const int64_t row = first + (threadIdx.x & 31) / LANES;
+    const int64_t row = first + sub;
     const int cols = LANES == 32 || row < a.rows ? a.cols : 0;
     float ss = 0.f, gt = 0.f;
 #pragma unroll
@@ -374,8 +381,8 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 4 : THREADS <= 512 ?
         if (LANES == 32 || cols) dw[j][i] = fmaf(g[i], n, dw[j][i]);
         d[i] = fmaf(rstd, fmaf(-n, dot, g[i] * w[j][i]), d[i]);
       }
-      if (a.dx) rows::store<TYPE, MAP>(static_cast<char*>(a.dx) + row * a.cols * rows::kSize<TYPE>, c0, cols, lane, d);
-      if (a.dr) rows::store<TT, MAP>(static_cast<char*>(a.dr) + row * a.cols * rows::kSize<TT>, c0, cols, lane, d);
+      if (a.dx) rows::store<TYPE, MAP, LANES>(static_cast<char*>(a.dx) + row * a.cols * rows::kSize<TYPE>, c0, cols, lane, d);
+      if (a.dr) rows::store<TT, MAP, LANES>(static_cast<char*>(a.dr) + row * a.cols * rows::kSize<TT>, c0, cols, lane, d);
     }
     if constexpr (MAP != kMap1) fetch(slot, first + S * step);
   }
@@ -386,7 +393,7 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 4 : THREADS <= 512 ?
     for (int i = 0; i < 8; ++i) {
 #pragma unroll
       for (int o = LANES; o < 32; o <<= 1) dw[0][i] += __shfl_xor_sync(0xffffffffu, dw[0][i], o);
-      if ((threadIdx.x & 31) < LANES) dw_part[group][rows::column<MAP>(lane, i)] = dw[0][i];
+      if ((threadIdx.x & 31) < LANES) dw_part[group][rows::column<MAP, LANES>(lane, i)] = dw[0][i];
     }
     __syncthreads();
     for (int c = threadIdx.x; c < a.cols; c += 32 * GROUPS) {
@@ -433,15 +440,20 @@ __global__ void __launch_bounds__(1024) dweight_kernel(const float* part, int n,
 template <int V>
 using Int = std::integral_constant<int, V>;
 
-// Lanes of a row: narrow rows of whole 8 columns share a warp (65536 x 64 bf16 6.6 us, with a warp a row 16.7).
-int narrow_lanes(int cols) { return cols % 8 ? 32 : cols <= 32 ? 4 : cols <= 64 ? 8 : cols <= 128 ? 16 : 32; }
+// Narrow rows take an access of 8 columns a lane where they are whole ones, else number by number.
+bool by_words(int cols) { return cols > 128 || cols % 8 == 0; }
 
 // f(type, the other type, map, lanes of a row) of rows of `type` beside rows of `other` (kNone, the same, or fp32)
 template <class F>
 cudaError_t with_types(int type, int other, bool aligned, int lanes, F&& f) {
   auto mapped = [&](auto T, auto O) {
     constexpr int kAligned = decltype(T)::value == MOE_TYPE_F32 || decltype(O)::value == MOE_TYPE_F32 ? kMap4 : kMap8;
-    if (!aligned) return f(T, O, Int<kMap1>{}, Int<32>{});
+    if (!aligned) {
+      if (lanes == 4) return f(T, O, Int<kMap1>{}, Int<4>{});
+      if (lanes == 8) return f(T, O, Int<kMap1>{}, Int<8>{});
+      if (lanes == 16) return f(T, O, Int<kMap1>{}, Int<16>{});
+      return f(T, O, Int<kMap1>{}, Int<32>{});
+    }
     if (lanes == 4) return f(T, O, Int<kMap8>{}, Int<4>{});
     if (lanes == 8) return f(T, O, Int<kMap8>{}, Int<8>{});
     if (lanes == 16) return f(T, O, Int<kMap8>{}, Int<16>{});
@@ -475,13 +487,13 @@ cudaError_t launch_rms_norm(const RmsNormDesc& d, cudaStream_t stream) {
   a.w_f32 = d.weight_type == MOE_TYPE_F32;
   a.eps = d.eps;
   const bool aligned = rows::whole(d.type, d.cols) && (d.rows == 1 || rows::whole(d.type, d.ldx)) &&
-                       (d.rows == 1 || !d.residual || rows::whole(d.type, d.ldr));
+                       (d.rows == 1 || !d.residual || rows::whole(d.type, d.ldr)) && rn::by_words(d.cols);
   const int chunks = (int)cdiv(d.cols, rows::kChunk);
   // two chunks a warp wherever there are two (65536 x 384 bf16 31 us, with one 36; 32768 x 2048 with codes 91 and 97;
   // 32768 x 512 fp32 with codes 44.8 and 44.1); eight rows a block where a warp holds one or several
   const int cpw = chunks > 1 ? 2 : 1;
   const int W = (int)cdiv(chunks, cpw), G = W == 1 ? 8 : 1;
-  const int lanes = aligned ? rn::narrow_lanes(d.cols) : 32;
+  const int lanes = rows::lanes_of(d.cols);
   return rn::with_types(d.type, d.residual ? d.residual_type : rn::kNone, aligned, lanes, [&](auto T, auto R, auto M, auto L) {
     constexpr int kT = decltype(T)::value, kR = decltype(R)::value, kM = decltype(M)::value, kL = decltype(L)::value;
     auto go = [&](auto kernel) {
@@ -533,14 +545,14 @@ cudaError_t launch_rms_norm_backward(const RmsNormBackwardDesc& d, int* launches
   a.cols = d.cols;
   a.w_f32 = d.weight_type == MOE_TYPE_F32;
   a.eps = d.eps;
-  const bool aligned = rows::whole(d.type, d.cols) && (d.rows == 1 || rows::whole(d.type, d.ldt));
+  const bool aligned = rows::whole(d.type, d.cols) && (d.rows == 1 || rows::whole(d.type, d.ldt)) && rn::by_words(d.cols);
   const int W = rn::back_warps(d.cols);
   int grid = rms_norm_backward_blocks(d.rows, d.cols);
   *launches = d.dweight ? 2 : 1;
   auto fit = [&](int smem) {  // blocks an SM's shared memory holds, each with 10 KB of its own at most
     grid = (int)std::min<int64_t>(grid, (int64_t)kNumSMsHint * std::max(1, 226 * 1024 / (smem + (W == 1 ? 10 : 2) * 1024)));
   };
-  const int lanes = aligned ? rn::narrow_lanes(d.cols) : 32;
+  const int lanes = rows::lanes_of(d.cols);
   cudaError_t e = rn::with_types(d.type, d.total_type, aligned, lanes, [&](auto T, auto R, auto M, auto L) {
     constexpr int kT = decltype(T)::value, kM = decltype(M)::value, kL = decltype(L)::value;
     constexpr int kR = decltype(R)::value == rn::kNone ? kT : decltype(R)::value;
@@ -561,8 +573,9 @@ cudaError_t launch_rms_norm_backward(const RmsNormBackwardDesc& d, int* launches
       int smem = rn::Ring<kT, kR, kC>::bytes(threads, rn::kStages<kT, kR, kC, kN>);
       if (kM == rows::kMap1) {
         a.stage = rn::covering(d.cols, rows::kSize<kT>) + (d.dtotal ? 2 : 1) * rn::covering(d.cols, rows::kSize<kR>);
-        a.stages = 2 * kG * a.stage * 16 <= rn::kMaxRing ? 2 : 1;
-        smem = a.stages * kG * a.stage * 16;
+        const int held = kG * (32 / kL);  // rows of a block
+        a.stages = 2 * held * a.stage * 16 <= rn::kMaxRing ? 2 : 1;
+        smem = a.stages * held * a.stage * 16;
       }
       fit(smem);
       grid = (int)std::min<int64_t>(grid, cdiv(d.rows, kG * (32 / kL)));

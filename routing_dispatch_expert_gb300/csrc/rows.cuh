@@ -7,12 +7,15 @@
 //   kMap4  the same for fp32: columns 4 lane .. + 3 and 128 + 4 lane .. + 3, so that both accesses are whole lines;
 //          16-bit rows beside fp32 ones take two 8-byte accesses for it
 //   kMap1  rows of any width that begin anywhere: columns lane + 32 i, one number an access. A warp's access is then 64
-//          or 128 consecutive bytes; with 8 consecutive numbers a lane it would be 32 pieces of four lines.
+//          or 128 consecutive bytes; with 8 consecutive numbers a lane it would be 32 pieces of four lines. Of narrow
+//          rows that share a warp, LANES lanes each, columns lane + LANES i.
 // Every chunk is 256 columns in all of them, so a lane's columns are the same in every row, and the blocks of 128
 // columns that share an 8-bit scale are half a chunk.
 #pragma once
 
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 
@@ -26,9 +29,9 @@ template <int TYPE>
 constexpr int kSize = TYPE == MOE_TYPE_F32 ? 4 : 2;
 
 // Column of a lane's i-th number within the chunk.
-template <int MAP>
+template <int MAP, int LANES = 32>
 __device__ __forceinline__ int column(int lane, int i) {
-  return MAP == kMap8 ? 8 * lane + i : MAP == kMap4 ? 128 * (i / 4) + 4 * lane + i % 4 : 32 * i + lane;
+  return MAP == kMap8 ? 8 * lane + i : MAP == kMap4 ? 128 * (i / 4) + 4 * lane + i % 4 : LANES * i + lane;
 }
 
 template <int TYPE>
@@ -70,7 +73,7 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
 
 // A lane's 8 numbers of a chunk as they lie in memory: nothing is done with them until values(), so the loads of
 // several chunks and tensors are in flight together. c0: first column of the chunk; columns at and past cols are 0.
-template <int TYPE, int MAP>
+template <int TYPE, int MAP, int LANES = 32>
 struct Chunk {
   static constexpr bool kWide = TYPE == MOE_TYPE_F32;
   uint32_t w[MAP == kMap1 || kWide ? 8 : 4];
@@ -79,7 +82,7 @@ struct Chunk {
     if constexpr (MAP == kMap1) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int c = c0 + column<MAP>(lane, i);
+        const int c = c0 + column<MAP, LANES>(lane, i);
         w[i] = c < cols ? load_bits<TYPE>(row, c) : 0u;
       }
     } else {
@@ -118,13 +121,13 @@ struct Chunk {
 };
 
 // A lane's 8 numbers to a row, each rounded once; columns at and past cols are left alone.
-template <int TYPE, int MAP>
+template <int TYPE, int MAP, int LANES = 32>
 __device__ __forceinline__ void store(void* row, int c0, int cols, int lane, const float (&f)[8]) {
   constexpr bool kWide = TYPE == MOE_TYPE_F32;
   if constexpr (MAP == kMap1) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int c = c0 + column<MAP>(lane, i);
+      const int c = c0 + column<MAP, LANES>(lane, i);
       if (c < cols) store_bits<TYPE>(row, c, bits_of<TYPE>(f[i]));
     }
   } else {
@@ -160,8 +163,22 @@ __device__ __forceinline__ void copy8(uint32_t to, const void* from, int n) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(from), "r"(n) : "memory");
 }
 
+// Zeros from byte `from` of base, which is on 16 bytes, up to byte `to`, by this thread of so many. Both are whole elements.
+template <int SIZE>
+__device__ __forceinline__ void clear(void* base, int64_t from, int64_t to, int64_t thread, int64_t threads) {
+  using Part = typename std::conditional<SIZE == 4, uint32_t, typename std::conditional<SIZE == 2, uint16_t, uint8_t>::type>::type;
+  char* const p = static_cast<char*>(base);
+  const int64_t lo = min((from + 15) & ~(int64_t)15, to), hi = max(to & ~(int64_t)15, lo);
+  for (int64_t i = from + SIZE * thread; i < lo; i += SIZE * threads) *reinterpret_cast<Part*>(p + i) = 0;
+  for (int64_t i = lo + 16 * thread; i < hi; i += 16 * threads) *reinterpret_cast<uint4*>(p + i) = make_uint4(0u, 0u, 0u, 0u);
+  for (int64_t i = hi + SIZE * thread; i < to; i += SIZE * threads) *reinterpret_cast<Part*>(p + i) = 0;
+}
+
 // Whether a row length or distance of n numbers of this type is whole 16 bytes.
 inline bool whole(int type, int64_t n) { return n % (type == MOE_TYPE_F32 ? 4 : 8) == 0; }
+
+// Lanes of a row, 8 columns each: narrow rows share a warp.
+inline int lanes_of(int64_t cols) { return cols <= 32 ? 4 : cols <= 64 ? 8 : cols <= 128 ? 16 : 32; }
 
 }  // namespace rows
 }  // namespace moe

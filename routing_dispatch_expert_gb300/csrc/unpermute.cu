@@ -9,7 +9,7 @@
 //
 // Bound by HBM. One GB300, k 8 (a copy's rate is 6.78 TB/s): 16384 x 7168 bf16 with weights and base 345 us, 6.8 TB/s,
 // the gradient with the weights' 601 us, 6.6; 8192 x 7168 fp32 331 and 589 us; 65536 x 64 bf16 20 and 28 us (4.4 and
-// 5.4 TB/s); odd 16-bit rows 8192 x 7167 257 and 416 us (4.6 and 4.8: 64 bytes an access); 64 x 512, k 2 2.4 us, launch.
+// 5.4 TB/s), 65536 x 33 22.5 and 40 us (instructions: a number an access); odd 16-bit rows 8192 x 7167 257 and 416 us (4.6 and 4.8: 64 bytes an access); 64 x 512, k 2 2.4 us, launch.
 #include <algorithm>
 #include <type_traits>
 
@@ -49,9 +49,13 @@ __device__ __forceinline__ void slots(const int32_t* inv_pos, const float* weigh
   }
 }
 
-// Blocks of 256 threads an SM holds: the registers of KB rows in flight.
+// Blocks of 256 threads an SM holds: the registers of KB rows in flight. Rows number by number take a register a number
+// (65536 x 511 bf16, the gradient: two slots 80 us with four blocks, 98 with three; four slots 142 with three, 163 with
+// four, which spill; eight slots 272 with two, 652 with three).
 template <int TYPE, int MAP, int KB>
-constexpr int kBlocks = MAP == rows::kMap1 || (TYPE == MOE_TYPE_F32 && KB == 8) ? 2 : KB == 8 || TYPE == MOE_TYPE_F32 ? 3 : 4;
+constexpr int kBlocks = MAP == rows::kMap1 ? (KB == 8 ? 2 : KB == 4 ? 3 : 4)
+                        : TYPE == MOE_TYPE_F32 ? (KB == 8 ? 2 : 3)
+                                               : (KB == 8 ? 3 : 4);
 
 struct AddArgs {
   const void* yd;
@@ -86,7 +90,7 @@ __global__ void __launch_bounds__(256, (kBlocks<TYPE, MAP, KB>)) unpermute_kerne
       float sum[8];
       for (int j0 = 0; j0 < a.k; j0 += KB) {
         if (KB == 8 && a.k > KB) slots<KB, LANES>(a.inv_pos, a.weights, t, a.T, a.k, j0, row, w);
-        rows::Chunk<TYPE, MAP> b, v[KB];
+        rows::Chunk<TYPE, MAP, LANES> b, v[KB];
         if (j0 == 0) {
           if (a.base)
             b.load(static_cast<const char*>(a.base) + t * pitch, c0, cols, sub);
@@ -107,7 +111,7 @@ __global__ void __launch_bounds__(256, (kBlocks<TYPE, MAP, KB>)) unpermute_kerne
         }
         if (KB < 8) break;  // k is at most KB
       }
-      rows::store<TYPE, MAP>(static_cast<char*>(a.y) + t * pitch, c0, cols, sub, sum);
+      rows::store<TYPE, MAP, LANES>(static_cast<char*>(a.y) + t * pitch, c0, cols, sub, sum);
     }
   }
 }
@@ -126,7 +130,7 @@ struct SpreadArgs {
 
 // A group of W warps a token (blockDim.x / 32, blockDim.y groups a block where W is 1), or LANES lanes a narrow row:
 // its row of dy to its k rows of dyd, and their products with yd's rows, summed over the lanes and then the warps. At
-// the end the warps clear the rows that hold nothing.
+// the end all threads clear the rows that hold nothing.
 template <int TYPE, int MAP, int KB, int LANES>
 __global__ void __launch_bounds__(256, (kBlocks<TYPE, MAP, KB>)) spread_kernel(const SpreadArgs a) {
   constexpr int kTokens = 32 / LANES;
@@ -134,7 +138,6 @@ __global__ void __launch_bounds__(256, (kBlocks<TYPE, MAP, KB>)) spread_kernel(c
   const int lane = threadIdx.x & 31, sub = lane % LANES, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
   const int64_t pitch = (int64_t)a.cols * rows::kSize<TYPE>;
   const int64_t group = (int64_t)blockIdx.x * blockDim.y + threadIdx.y, groups = (int64_t)gridDim.x * blockDim.y;
-  float f[8];
   for (int64_t g0 = group * kTokens; g0 < a.T; g0 += groups * kTokens) {
     const int64_t t = g0 + lane / LANES;
     const int cols = t < a.T ? a.cols : 0;
@@ -146,7 +149,7 @@ __global__ void __launch_bounds__(256, (kBlocks<TYPE, MAP, KB>)) spread_kernel(c
       for (int j = 0; j < KB; ++j) dot[j] = 0.f;
       for (int c = warp; c < a.chunks; c += W) {
         const int c0 = c * rows::kChunk;
-        rows::Chunk<TYPE, MAP> dy, v[KB];
+        rows::Chunk<TYPE, MAP, LANES> dy, v[KB];
         dy.load(static_cast<const char*>(a.dy) + t * pitch, c0, cols, sub);
         if (a.yd) {
 #pragma unroll
@@ -158,6 +161,7 @@ __global__ void __launch_bounds__(256, (kBlocks<TYPE, MAP, KB>)) spread_kernel(c
 #pragma unroll
         for (int j = 0; j < KB; ++j) {
           if (row[j] < 0) continue;
+          float f[8];
           if (a.yd) {
             v[j].values(f);
 #pragma unroll
@@ -165,7 +169,7 @@ __global__ void __launch_bounds__(256, (kBlocks<TYPE, MAP, KB>)) spread_kernel(c
           }
 #pragma unroll
           for (int i = 0; i < 8; ++i) f[i] = w[j] * g[i];
-          rows::store<TYPE, MAP>(static_cast<char*>(a.dyd) + row[j] * pitch, c0, cols, sub, f);
+          rows::store<TYPE, MAP, LANES>(static_cast<char*>(a.dyd) + row[j] * pitch, c0, cols, sub, f);
         }
       }
       if (!a.dweights) continue;
@@ -174,8 +178,10 @@ __global__ void __launch_bounds__(256, (kBlocks<TYPE, MAP, KB>)) spread_kernel(c
       for (int j = 0; j < KB; ++j) {
 #pragma unroll
         for (int o = LANES / 2; o > 0; o >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], o);
+        if (LANES < KB && sub == j % LANES && t < a.T && j0 + j < a.k) a.dweights[t * a.k + j0 + j] = dot[j];
         if (sub == j) mine = dot[j];
       }
+      if (LANES < KB) continue;  // narrow rows have one warp
       if (W == 1) {
         if (t < a.T && sub < KB && j0 + sub < a.k) a.dweights[t * a.k + j0 + sub] = mine;
         continue;
@@ -190,17 +196,14 @@ __global__ void __launch_bounds__(256, (kBlocks<TYPE, MAP, KB>)) spread_kernel(c
       __syncthreads();
     }
   }
-  const int64_t held = max(*a.held_at, 0);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = 0.f;
-  for (int64_t r = held + group; r < a.T * a.k; r += groups)
-    for (int c = warp; c < a.chunks; c += W)
-      rows::store<TYPE, MAP>(static_cast<char*>(a.dyd) + r * pitch, c * rows::kChunk, a.cols, lane, f);
+  const int64_t held = min(max((int64_t)*a.held_at, (int64_t)0), a.T * a.k), threads = (int64_t)blockDim.x * blockDim.y;
+  rows::clear<rows::kSize<TYPE>>(a.dyd, held * pitch, a.T * a.k * pitch,
+                                 blockIdx.x * threads + threadIdx.y * blockDim.x + threadIdx.x, gridDim.x * threads);
 }
 
-// f(type, map, slots at a time, lanes of a row). Rows of up to 64 and 128 columns of whole 16 bytes take 8 and 16 lanes
-// (65536 x 64 bf16 20 us, with a warp a row 45); two or four slots leave registers for more blocks (65536 x 512, k 2:
-// 52 us, with eight 58).
+// f(type, map, slots at a time, lanes of a row). Rows of up to 128 columns share a warp (65536 x 64 bf16 20 us, with a warp
+// a row 45; 65536 x 33 22.5 and 69); two or four slots leave registers for more blocks (65536 x 512, k 2: 52 us, with eight
+// 58; 65536 x 511, k 4: 92 and 112).
 template <class F>
 cudaError_t with_rows(int type, int64_t cols, int k, F&& f) {
   const bool whole = rows::whole(type, cols);
@@ -212,12 +215,18 @@ cudaError_t with_rows(int type, int64_t cols, int k, F&& f) {
     using Eight = integral_constant<int, rows::kMap8>;  // narrow rows: 8 columns a lane whatever the type
     integral_constant<int, 2> two;
     integral_constant<int, 4> four;
+    const int lanes = rows::lanes_of(cols);
     integral_constant<int, 8> eight;
     integral_constant<int, 16> sixteen;
     integral_constant<int, 32> all;
-    if (!whole) return k <= 2 ? f(T, One{}, two, all) : f(T, One{}, eight, all);
-    if (cols <= 64 && cols % 8 == 0) return k <= 2 ? f(T, Eight{}, two, eight) : f(T, Eight{}, eight, eight);
-    if (cols <= 128 && cols % 8 == 0) return k <= 2 ? f(T, Eight{}, two, sixteen) : f(T, Eight{}, eight, sixteen);
+    if (!whole || (lanes < 32 && cols % 8)) {
+      auto odd = [&](auto L) {
+        return k <= 2 ? f(T, One{}, two, L) : k <= 4 ? f(T, One{}, four, L) : f(T, One{}, eight, L);
+      };
+      return lanes == 4 ? odd(four) : lanes == 8 ? odd(eight) : lanes == 16 ? odd(sixteen) : odd(all);
+    }
+    if (lanes <= 8) return k <= 2 ? f(T, Eight{}, two, eight) : f(T, Eight{}, eight, eight);
+    if (lanes == 16) return k <= 2 ? f(T, Eight{}, two, sixteen) : f(T, Eight{}, eight, sixteen);
     return k <= 2 ? f(T, Whole{}, two, all) : k <= 4 ? f(T, Whole{}, four, all) : f(T, Whole{}, eight, all);
   };
   if (type == MOE_TYPE_F32) return typed(integral_constant<int, MOE_TYPE_F32>{});
