@@ -10,10 +10,10 @@ CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "_build")
 SO = os.path.join(OUT_DIR, "libmoe_gb300.so")
 SOURCES = ["api.cu", "route.cu", "dispatch.cu", "gemm.cu", "gemm_pair.cu", "gemm_fp8.cu", "gemm_fp4.cu", "combine.cu", "eplb.cu", "fused.cu",
-           "fp4_quant.cu", "gemm_a4.cu", "balance_loss.cu", "rms_norm.cu", "permute.cu", "unpermute.cu",
+           "fp4_quant.cu", "gemm_a4.cu", "balance_loss.cu", "rms_norm.cu", "rms_norm_backward.cu", "permute.cu", "unpermute.cu",
            "route_backward.cu"]
 HEADERS = ["common.cuh", "gemm_common.cuh", "kernels.h", "device_state.h", "route_impl.cuh", "dispatch_impl.cuh", "fp4_impl.cuh", "rows.cuh",
-           "gemm_a4_host.h"]
+           "rms_norm.cuh", "gemm_a4_host.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden", "--expt-relaxed-constexpr",
          "-Xptxas", "-warn-spills"]

@@ -269,7 +269,7 @@ struct BalanceLossBackwardDesc {
 };
 cudaError_t launch_balance_loss_backward(const BalanceLossBackwardDesc& d, cudaStream_t stream);
 
-// RMS norm of x + residual and its gradient (rms_norm.cu). cols <= kNormMaxCols; types MOE_TYPE_*.
+// RMS norm of x + residual and its gradient (rms_norm.cu, rms_norm_backward.cu). cols <= kNormMaxCols; types MOE_TYPE_*.
 constexpr int kNormMaxCols = 16384;
 struct RmsNormDesc {
   const void* x;         // [rows, cols], ldx apart

@@ -16,10 +16,10 @@
 // us, one launch; 16384 x 8 8.7 us, 65536 x 8 14.2 us (with 1024 experts 16384 x 8 13.4 us: the blocks' counts). A
 // block adds up the others' counts itself instead of a third launch; reading them one after the other with atomics took
 // 11.8 us for 16384 x 8. The copies are bound by HBM: 16384 rows to eight places each, 7168 bytes and scales 164 us
-// (6.6 TB/s, a copy's rate is 6.78), 14336 bytes 315 us (6.7), 65536 rows of 128 bytes 13.5 us (5.6); odd 16-bit rows of
-// 1003 59 us (5.0: 64 bytes an access). Slower: bulk copies out of shared memory, a place each (186 us instead of 171 for the
-// rows of 7168 bytes); odd rows by the 16-byte words of their places, shifted (65536 x 511 bf16 with the sort 196 us
-// instead of 135: the parts of words at a row's ends; only rows of kilobytes gain, 215 to 195 for 8192 x 7167).
+// (6.6 TB/s, a copy's rate is 6.78), 14336 bytes 315 us (6.7), 65536 rows of 128 bytes 13.5 us (5.6); odd 16-bit rows
+// of 1003 59 us (5.0: 64 bytes an access). Slower: bulk copies out of shared memory, a place each (186 us instead of 171
+// for the rows of 7168 bytes); odd rows by the 16-byte words of their places, shifted (65536 x 511 bf16 with the sort
+// 196 us instead of 135: the parts of words at a row's ends; only rows of kilobytes gain, 215 to 195 for 8192 x 7167).
 #include <algorithm>
 #include <type_traits>
 

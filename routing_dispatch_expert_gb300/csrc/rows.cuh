@@ -1,4 +1,4 @@
-// Rows of fp32, bf16 or fp16 numbers as the kernels of the norm (rms_norm.cu) and of the row permutation (permute.cu)
+// Rows of fp32, bf16 or fp16 numbers as the kernels of the norm (rms_norm.cu, rms_norm_backward.cu) and of the rows' way back (unpermute.cu)
 // read and write them: a warp takes 256 consecutive columns (a chunk) at a time, a lane 8 of them, held as fp32.
 //
 // Which 8 depends on how the rows lie in memory (MAP):
@@ -9,6 +9,8 @@
 //   kMap1  rows of any width that begin anywhere: columns lane + 32 i, one number an access. A warp's access is then 64
 //          or 128 consecutive bytes; with 8 consecutive numbers a lane it would be 32 pieces of four lines. Of narrow
 //          rows that share a warp, LANES lanes each, columns lane + LANES i.
+//   kMap2  rows of an even number of 16-bit numbers, whose begins are as far apart: the same by two numbers an access,
+//          columns 2 lane + 64 i and the next one; fp32 rows beside them take two numbers of 8 bytes
 // Every chunk is 256 columns in all of them, so a lane's columns are the same in every row, and the blocks of 128
 // columns that share an 8-bit scale are half a chunk.
 #pragma once
@@ -22,7 +24,9 @@
 namespace moe {
 namespace rows {
 
-constexpr int kMap8 = 0, kMap4 = 1, kMap1 = 2;
+constexpr int kMap8 = 0, kMap4 = 1, kMap1 = 2, kMap2 = 3;
+template <int MAP>
+constexpr bool kOdd = MAP == kMap1 || MAP == kMap2;  // rows that are not whole 16 bytes
 constexpr int kChunk = 256;
 
 template <int TYPE>
@@ -31,7 +35,10 @@ constexpr int kSize = TYPE == MOE_TYPE_F32 ? 4 : 2;
 // Column of a lane's i-th number within the chunk.
 template <int MAP, int LANES = 32>
 __device__ __forceinline__ int column(int lane, int i) {
-  return MAP == kMap8 ? 8 * lane + i : MAP == kMap4 ? 128 * (i / 4) + 4 * lane + i % 4 : LANES * i + lane;
+  return MAP == kMap8   ? 8 * lane + i
+         : MAP == kMap4 ? 128 * (i / 4) + 4 * lane + i % 4
+         : MAP == kMap2 ? 2 * LANES * (i / 2) + 2 * lane + i % 2
+                        : LANES * i + lane;
 }
 
 template <int TYPE>
@@ -85,6 +92,18 @@ struct Chunk {
         const int c = c0 + column<MAP, LANES>(lane, i);
         w[i] = c < cols ? load_bits<TYPE>(row, c) : 0u;
       }
+    } else if constexpr (MAP == kMap2) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = c0 + column<MAP, LANES>(lane, 2 * i);
+        const char* p = static_cast<const char*>(row) + (int64_t)c * kSize<TYPE>;
+        if constexpr (kWide) {
+          const uint2 v = c < cols ? *reinterpret_cast<const uint2*>(p) : make_uint2(0u, 0u);
+          w[2 * i] = v.x, w[2 * i + 1] = v.y;
+        } else {
+          w[i] = c < cols ? *reinterpret_cast<const uint32_t*>(p) : 0u;
+        }
+      }
     } else {
 #pragma unroll
       for (int h = 0; h < (kWide || MAP == kMap4 ? 2 : 1); ++h) {
@@ -129,6 +148,17 @@ __device__ __forceinline__ void store(void* row, int c0, int cols, int lane, con
     for (int i = 0; i < 8; ++i) {
       const int c = c0 + column<MAP, LANES>(lane, i);
       if (c < cols) store_bits<TYPE>(row, c, bits_of<TYPE>(f[i]));
+    }
+  } else if constexpr (MAP == kMap2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = c0 + column<MAP, LANES>(lane, 2 * i);
+      char* p = static_cast<char*>(row) + (int64_t)c * kSize<TYPE>;
+      if (c >= cols) continue;
+      if constexpr (kWide)
+        *reinterpret_cast<float2*>(p) = make_float2(f[2 * i], f[2 * i + 1]);
+      else
+        *reinterpret_cast<uint32_t*>(p) = pack2<TYPE>(f[2 * i], f[2 * i + 1]);
     }
   } else {
 #pragma unroll

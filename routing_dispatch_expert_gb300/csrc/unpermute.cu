@@ -7,9 +7,11 @@
 // The rows of a chunk are all loaded before any is worked on, and a token's positions are looked up once for many
 // chunks.
 //
-// Bound by HBM. One GB300, k 8 (a copy's rate is 6.78 TB/s): 16384 x 7168 bf16 with weights and base 345 us, 6.8 TB/s,
-// the gradient with the weights' 601 us, 6.6; 8192 x 7168 fp32 331 and 589 us; 65536 x 64 bf16 20 and 28 us (4.4 and
-// 5.4 TB/s), 65536 x 33 22.5 and 40 us (instructions: a number an access); odd 16-bit rows 8192 x 7167 257 and 416 us (4.6 and 4.8: 64 bytes an access); 64 x 512, k 2 2.4 us, launch.
+// Bound by HBM. One GB300, k 8 (a copy's rate is 6.78 TB/s), with weights and base, and the gradient with the weights':
+//   16384 x 7168 bf16 345 us, 6.8 TB/s   601 us, 6.6        8192 x 7168 fp32 331 us   589 us
+//   65536 x 64 bf16    20 us, 4.4         28 us, 5.4        65536 x 33 bf16 22.5 us   40 us
+//   8192 x 7166 bf16  210 us, 5.6        331 us, 6.0        8192 x 7167 bf16 257 us, 4.6   416 us, 4.8
+// 16-bit rows that are not whole 16 bytes are bound by their accesses of one number or two. 64 x 512, k 2: 2.4 us, launch.
 #include <algorithm>
 #include <type_traits>
 
@@ -51,9 +53,11 @@ __device__ __forceinline__ void slots(const int32_t* inv_pos, const float* weigh
 
 // Blocks of 256 threads an SM holds: the registers of KB rows in flight. Rows number by number take a register a number
 // (65536 x 511 bf16, the gradient: two slots 80 us with four blocks, 98 with three; four slots 142 with three, 163 with
-// four, which spill; eight slots 272 with two, 652 with three).
-template <int TYPE, int MAP, int KB>
-constexpr int kBlocks = MAP == rows::kMap1 ? (KB == 8 ? 2 : KB == 4 ? 3 : 4)
+// four, which spill; eight slots 272 with two, 652 with three), by pairs one for two (8192 x 7166: 210 us with two blocks,
+// 259 with three, which spill; the narrow rows of 65536 x 66 33.5 and 28.0).
+template <int TYPE, int MAP, int KB, int LANES = 32>
+constexpr int kBlocks = MAP == rows::kMap2   ? (KB < 8 ? 4 : LANES == 32 ? 2 : 3)
+                        : MAP == rows::kMap1 ? (KB == 8 ? 2 : KB == 4 ? 3 : 4)
                         : TYPE == MOE_TYPE_F32 ? (KB == 8 ? 2 : 3)
                                                : (KB == 8 ? 3 : 4);
 
@@ -71,7 +75,7 @@ struct AddArgs {
 // A warp a piece of a token's row, or LANES lanes a whole narrow row: fp32, the base first and then the slots in order.
 // KB: slots at a time, a power of two at or above k, at most 8.
 template <int TYPE, int MAP, int KB, int LANES>
-__global__ void __launch_bounds__(256, (kBlocks<TYPE, MAP, KB>)) unpermute_kernel(const AddArgs a) {
+__global__ void __launch_bounds__(256, (kBlocks<TYPE, MAP, KB, LANES>)) unpermute_kernel(const AddArgs a) {
   constexpr int kTokens = 32 / LANES;
   const int lane = threadIdx.x & 31, sub = lane % LANES;
   const int64_t warps = ((int64_t)gridDim.x * blockDim.x) >> 5;
@@ -211,6 +215,7 @@ cudaError_t with_rows(int type, int64_t cols, int k, F&& f) {
     constexpr int kT = decltype(T)::value;
     constexpr int kAligned = kT == MOE_TYPE_F32 ? rows::kMap4 : rows::kMap8;
     using One = integral_constant<int, rows::kMap1>;
+    using Two = integral_constant<int, kT == MOE_TYPE_F32 ? rows::kMap1 : rows::kMap2>;
     using Whole = integral_constant<int, kAligned>;
     using Eight = integral_constant<int, rows::kMap8>;  // narrow rows: 8 columns a lane whatever the type
     integral_constant<int, 2> two;
@@ -220,10 +225,11 @@ cudaError_t with_rows(int type, int64_t cols, int k, F&& f) {
     integral_constant<int, 16> sixteen;
     integral_constant<int, 32> all;
     if (!whole || (lanes < 32 && cols % 8)) {
-      auto odd = [&](auto L) {
-        return k <= 2 ? f(T, One{}, two, L) : k <= 4 ? f(T, One{}, four, L) : f(T, One{}, eight, L);
+      auto by = [&](auto M) {
+        auto odd = [&](auto L) { return k <= 2 ? f(T, M, two, L) : k <= 4 ? f(T, M, four, L) : f(T, M, eight, L); };
+        return lanes == 4 ? odd(four) : lanes == 8 ? odd(eight) : lanes == 16 ? odd(sixteen) : odd(all);
       };
-      return lanes == 4 ? odd(four) : lanes == 8 ? odd(eight) : lanes == 16 ? odd(sixteen) : odd(all);
+      return cols % 2 ? by(One{}) : by(Two{});
     }
     if (lanes <= 8) return k <= 2 ? f(T, Eight{}, two, eight) : f(T, Eight{}, eight, eight);
     if (lanes == 16) return k <= 2 ? f(T, Eight{}, two, sixteen) : f(T, Eight{}, eight, sixteen);

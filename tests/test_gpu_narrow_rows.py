@@ -112,3 +112,45 @@ def test_codes_by_expert(cols):
         assert torch.equal(q, torch.where(held, x[token.clamp(min=0)], torch.zeros((), dtype=torch.uint8, device="cuda")))
         assert torch.equal(qs, torch.where(held, scales[token.clamp(min=0)], 0.0))
         assert torch.equal(q, rde.permute(cfg, x, s["inv_pos"], s["offsets"]))
+
+
+EVEN = [130, 250, 258, 1002, 2050, 4102, 16382]
+
+
+@pytest.mark.parametrize("cols", EVEN)
+@pytest.mark.parametrize("kind,other", [(BF16, BF16), (F16, F32)])
+def test_norm_of_even_rows(cols, kind, other):
+    """16-bit rows of an even number of columns that are not whole 16 bytes, whose begins lie an even or an odd number apart."""
+    gen = torch.Generator(device="cuda").manual_seed(cols)
+    for n, more, wkind in itertools.product((1, 2, 35, 311), (0, 2, 3), (None, kind, F32)):
+        if n == 311 and cols > 4102:
+            continue
+        w = None if wkind is None else (1 + 0.3 * torch.randn(cols, generator=gen, device="cuda")).to(wkind)
+        x, r = rows(gen, n, cols + more, kind)[:, :cols], rows(gen, n, cols + more, other, 3.0)[:, :cols]
+        want_y, want_t = plain.norm(x, w, r, EPS)
+        out = rde.rms_norm_fp8(x, w, r, EPS, with_y=True)
+        check_total_and_y(out["y"], out["total"], want_y, want_t, kind, other)
+        check_codes(out["q"], out["s"], want_y, cols)
+        dy, dt = rows(gen, n, cols, kind), rows(gen, n, cols, other) if n % 2 else None
+        check_gradient(dy, r, w, dt, rde.rms_norm_backward(dy, r, w, EPS, dt))
+
+
+@pytest.mark.parametrize("cols", EVEN[:-1])
+@pytest.mark.parametrize("kind", [BF16, F16])
+def test_even_rows_and_back(cols, kind):
+    for T, k in ((1, 1), (67, 2), (130, 4), (300, 8), (35, 11)):
+        cfg = config(T, 16, k, capacity_factor=1.5)
+        s = rde.sort_tokens(cfg, choices(T, 16, k, seed=T, pad=0.2))
+        inv, n_held = s["inv_pos"], int(s["offsets"][-1])
+        gen = torch.Generator(device="cuda").manual_seed(cols)
+        dy, base = (rows(gen, T, cols, kind) for _ in range(2))
+        yd = rows(gen, T * k, cols, kind)
+        yd[n_held:] = float("nan")
+        w = torch.rand(T, k, generator=gen, device="cuda")
+        y, size = plain.unpermute(yd, inv, w, base)
+        close(rde.unpermute(cfg, yd, inv, w, base), y, (k + 2) * U32 * size + HALF[kind] * y.abs() * (1 + 2.0 ** -8) + TINY[kind], "y")
+        dyd, dw, size = plain.unpermute_backward(dy, yd, inv, w)
+        got = rde.unpermute_backward(cfg, dy, yd, inv, s["offsets"], w)
+        close(got[0], dyd, (HALF[kind] + 2 * U32) * dyd.abs() + TINY[kind], "dyd")
+        assert (got[0][n_held:] == 0).all() and (got[1][inv < 0] == 0).all()
+        close(got[1], dw, (8 * (cols // 256 + 1) + 14) * U32 * size, "dweights")
