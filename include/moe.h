@@ -447,7 +447,7 @@ int moe_balance_loss_backward(const moe_config* cfg, const void* logits, int32_t
  * the gradients
  * ------------------------------------------------------------------------------------------
  * Rows are fp32, bf16 or fp16 (MOE_TYPE_*) and of any width unless said otherwise. Rows that begin on 16 bytes are read
- * and written 16 bytes at a time, others number by number. Sums, statistics and gradients are fp32; every output is
+ * and written 16 bytes at a time, others number by number (16-bit ones of an even width two at a time). Sums, statistics and gradients are fp32; every output is
  * rounded once.
  *
  * moe_rms_norm: total = x + residual, y = total * weight / sqrt(mean(total^2) + eps). The squares are added in fp32:
@@ -538,7 +538,7 @@ int moe_unpermute_backward(const moe_config* cfg, const void* dy, const void* yd
  * selection and its bias carry none): dlogits [T, E] of logits_type (MOE_TYPE_F32 or MOE_TYPE_BF16) from logits [T, E],
  * topk_idx [T, k] and dtopk_w [T, k] fp32. Entries of topk_idx outside [0, E) are left out; an expert that a token
  * names twice gets the sum of both. A token without assignments (padding), or whose (chosen) logits are all -inf, has a
- * gradient of 0, whatever its row holds. Every number of dlogits is written. One launch. Errors: MOE_ERR_INVALID,
+ * gradient of 0, whatever its row holds. Every number of dlogits is written; it overlaps no input. One launch. Errors: MOE_ERR_INVALID,
  * MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA. */
 int moe_route_backward(const moe_config* cfg, const void* logits, int32_t logits_type, const int32_t* topk_idx,
                        const float* dtopk_w, void* dlogits, moe_stream_t stream);

@@ -1472,6 +1472,10 @@ MOE_EXPORT int moe_route_backward(const moe_config* cfg, const void* logits, int
   REQUIRE_PTR(topk_idx, "topk_idx");
   REQUIRE_PTR(dtopk_w, "dtopk_w");
   REQUIRE_PTR(dlogits, "dlogits");
+  const size_t bytes = (size_t)cfg->T * cfg->E * (logits_type == MOE_TYPE_F32 ? 4 : 2);
+  const uintptr_t from = reinterpret_cast<uintptr_t>(logits), to = reinterpret_cast<uintptr_t>(dlogits);
+  if (from < to + bytes && to < from + bytes)  // a warp clears its tokens' rows before it reads the chosen logits
+    return fail(MOE_ERR_INVALID, "dlogits overlaps logits");
   moe::RouteBackwardDesc d;
   d.logits = logits;
   d.topk_idx = topk_idx;

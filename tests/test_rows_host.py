@@ -211,3 +211,10 @@ def test_plain_sort_under_a_placement():
     place = {"slot_expert": [0, 1, 0], "slot_replica": [1, 0, 0], "replicas": [2, 1], "replica_slot": None}
     s = plain.sort(idx, 2, placement=place)  # expert 0's rows go round slots 2 and 0
     assert s["counts"] == [1, 1, 2] and s["inv_pos"] == [2, 0, 1, 3]
+
+
+def test_route_gradient_over_its_logits_is_refused(lib):
+    c = ctypes.byref(_cfg())  # 64 x 8 fp32: 2048 bytes
+    for off in (0, 16, 2032, -2032):
+        out = ctypes.c_void_p(0x10000 + off)
+        _refused(lib, lib.moe_route_backward(c, ctypes.c_void_p(0x10000), 0, P, P, out, None), -1, "overlaps")
