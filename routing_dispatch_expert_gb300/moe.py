@@ -585,6 +585,13 @@ def _gradient(t):
     return t.clone(memory_format=torch.contiguous_format)
 
 
+def _kept(cfg):
+    """A copy of a configuration for a backward pass, which the caller may change meanwhile (T, for the next batch)."""
+    copy = MoeConfig.from_buffer_copy(cfg)
+    copy._placement = getattr(cfg, "_placement", None)
+    return copy
+
+
 def _wants_gradient(a, b=None, c=None):
     return (getattr(a, "requires_grad", False) or getattr(b, "requires_grad", False)
             or getattr(c, "requires_grad", False)) and torch.is_grad_enabled()
@@ -822,7 +829,7 @@ class _Permute(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, cfg, inv_pos, offsets):
-        ctx.cfg = cfg
+        ctx.cfg = _kept(cfg)
         ctx.save_for_backward(inv_pos)
         return _permute(x, cfg, inv_pos, offsets, None)
 
@@ -869,7 +876,7 @@ class _Unpermute(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, yd, weights, base, cfg, inv_pos, offsets):
-        ctx.cfg = cfg
+        ctx.cfg = _kept(cfg)
         ctx.save_for_backward(yd if weights is not None and weights.requires_grad else None, weights, inv_pos, offsets)
         return _unpermute(yd, weights, base, cfg, inv_pos)
 
@@ -942,7 +949,7 @@ class _RouteWeights(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, cfg, bias):
         idx, w = _route_weights(logits, cfg, bias)
-        ctx.cfg = cfg
+        ctx.cfg = _kept(cfg)
         ctx.mark_non_differentiable(idx)
         ctx.save_for_backward(logits, idx)
         return idx, w
