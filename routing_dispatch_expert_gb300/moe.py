@@ -564,9 +564,10 @@ def balance_loss_backward(cfg, logits, counts, tokens, alpha: float, dloss, seq_
 # around the experts: the norm in front, rows sorted by expert and back, and the gradients
 # ------------------------------------------------------------------------------------------
 # As above, the calls below look at their tensors in as few steps as they can and find the words of a refusal only after
-# one failed; outputs are made like an input where there is one of their shape (two thirds of the time of a call on small
-# tensors is three allocations and a launch).
-_empty, _empty_like = torch.empty, torch.empty_like
+# one failed. Two thirds of the time of a call on small tensors is three allocations and a launch: outputs are made by the
+# shortest way that torch has to memory of the current device, which is the tensors' (sizes, strides, dtype; 0.85 us each,
+# torch.empty 1.45).
+_new = torch._C._dynamo.guards._empty_strided_cuda
 
 
 def _here(a, b=None, c=None, d=None, e=None):
@@ -628,15 +629,16 @@ def _rms_norm(x, weight, residual, eps, fp8, with_y):
     if residual is not None:
         if not (_like(residual, dtype, shape) or _like(residual, _f32, shape)):
             ldr = _row_matrix(residual, "residual", (dtype, _f32), shape)
-            total = _empty(rows, cols, dtype=residual.dtype, device=x.device)
+            total = _new((rows, cols), (cols, 1), residual.dtype)
         else:
-            ldr, total = cols, _empty_like(residual)
+            ldr, total = cols, _new((rows, cols), (cols, 1), residual.dtype)
         r, r_type, to = residual.data_ptr(), ELEMENT_TYPES[residual.dtype], total.data_ptr()
     if with_y:
-        y = _empty_like(x) if ldx == cols else _empty(rows, cols, dtype=dtype, device=x.device)
+        y = _new((rows, cols), (cols, 1), dtype)
     if fp8:
-        q = _empty(rows, cols, dtype=_u8, device=x.device)
-        s = _empty(rows, (cols + 127) // 128, dtype=_f32, device=x.device)
+        q = _new((rows, cols), (cols, 1), _u8)
+        n = (cols + 127) // 128
+        s = _new((rows, n), (n, 1), _f32)
     rc = (_lib or load()).moe_rms_norm(x.data_ptr(), ELEMENT_TYPES[dtype], rows, cols, ldx, r, r_type, ldr, w, w_type, eps,
                                        y.data_ptr() if with_y else None, to, q.data_ptr() if fp8 else None,
                                        s.data_ptr() if fp8 else None, _here(x, weight, residual))
@@ -705,14 +707,14 @@ def rms_norm_backward(dy, total, weight=None, eps: float = 1e-6, dtotal=None, we
     if dtotal is not None and not _like(dtotal, of, shape):
         _need(dtotal, "dtotal", of, shape)
     w, w_type = _norm_weight(weight, kind, cols)
-    dx = _empty_like(dy)
+    dx = _new((rows, cols), (cols, 1), kind)
     dresidual, dweight = dx, None
     if of is not kind:
-        dresidual = _empty(rows, cols, dtype=of, device=dy.device)
+        dresidual = _new((rows, cols), (cols, 1), of)
     if weight is not None and weight_gradient:
-        dweight = _empty_like(weight)
+        dweight = _new((cols,), (1,), weight.dtype)
         if ws is None:
-            ws = rms_norm_backward_workspace(rows, cols, dy.device)
+            ws = _new((_rms_norm_backward_bytes(rows, cols),), (1,), _u8)
         elif not _like(ws, _u8, (ws.numel(),)):
             _need(ws, "ws", _u8, (None,))
     rc = (_lib or load()).moe_rms_norm_backward(
@@ -736,14 +738,15 @@ def rms_norm_backward_workspace(rows: int, cols: int, device="cuda") -> torch.Te
     return torch.empty(_rms_norm_backward_bytes(rows, cols), dtype=_u8, device=device)
 
 
-def _sort_tokens_bytes(cfg):
+@functools.lru_cache(maxsize=256)
+def _sort_tokens_bytes(T, E, k):
     n = ctypes.c_size_t()
-    _check((_lib or load()).moe_sort_tokens_workspace_size(ctypes.byref(cfg), ctypes.byref(n)))
+    _check((_lib or load()).moe_sort_tokens_workspace_size(ctypes.byref(make_config(T, 256, E, k, 256)), ctypes.byref(n)))
     return n.value
 
 
 def sort_tokens_workspace(cfg: MoeConfig, device="cuda") -> torch.Tensor:
-    return torch.empty(_sort_tokens_bytes(cfg), dtype=_u8, device=device)
+    return torch.empty(_sort_tokens_bytes(cfg.T, cfg.E, cfg.k), dtype=_u8, device=device)
 
 
 def _groups(cfg):
@@ -760,19 +763,19 @@ def sort_tokens(cfg, topk_idx, topk_w=None, ws=None) -> dict:
         _need(topk_idx, "topk_idx", _i32, shape)
     if topk_w is not None and not _like(topk_w, _f32, shape):
         _need(topk_w, "topk_w", _f32, shape)
-    dev, n = topk_idx.device, _groups(cfg)
+    n = _groups(cfg)
     if ws is None:
-        size = _sort_tokens_bytes(cfg)
+        size = _sort_tokens_bytes(T, cfg.E, k)
         if size:
-            ws = _empty(size, dtype=_u8, device=dev)
+            ws = _new((size,), (1,), _u8)
     elif not _like(ws, _u8, (ws.numel(),)):
         _need(ws, "ws", _u8, (None,))
-    counts, offsets = _empty(n, dtype=_i32, device=dev), _empty(n + 1, dtype=_i32, device=dev)
-    inv_pos, row_token = _empty_like(topk_idx), _empty(T * k, dtype=_i32, device=dev)
+    counts, offsets = _new((n,), (1,), _i32), _new((n + 1,), (1,), _i32)
+    inv_pos, row_token = _new(shape, (k, 1), _i32), _new((T * k,), (1,), _i32)
     out = {"counts": counts, "offsets": offsets, "inv_pos": inv_pos, "row_token": row_token}
     w = row_weight = None
     if topk_w is not None:
-        out["row_weight"] = row_weight = _empty(T * k, dtype=_f32, device=dev)
+        out["row_weight"] = row_weight = _new((T * k,), (1,), _f32)
         w, row_weight = topk_w.data_ptr(), row_weight.data_ptr()
     rc = (_lib or load()).moe_sort_tokens(
         ctypes.byref(cfg), topk_idx.data_ptr(), w, counts.data_ptr(), offsets.data_ptr(), inv_pos.data_ptr(),
@@ -809,13 +812,13 @@ def _permute(x, cfg, inv_pos, offsets, scales):
     rows, cols = x.shape
     if rows != T:
         _need(x, "x", x.dtype, (T, cols), contiguous=False)
-    xd = _empty(T * k, cols, dtype=x.dtype, device=x.device)
+    xd = _new((T * k, cols), (cols, 1), x.dtype)
     xd_scales = of = to = None
     if scales is not None:
         n = (cols + 127) // 128
         if not _like(scales, _f32, (T, n)):
             _need(scales, "scales", _f32, (T, n))
-        xd_scales = _empty(T * k, n, dtype=_f32, device=x.device)
+        xd_scales = _new((T * k, n), (n, 1), _f32)
         of, to = scales.data_ptr(), xd_scales.data_ptr()
     rc = (_lib or load()).moe_permute(ctypes.byref(cfg), x.data_ptr(), x.element_size(), cols, ldx, of, inv_pos.data_ptr(),
                                       offsets.data_ptr(), xd.data_ptr(), to, _here(x, inv_pos, offsets, scales))
@@ -859,11 +862,11 @@ def _unpermute(yd, weights, base, cfg, inv_pos):
     dtype, cols = yd.dtype, yd.shape[1]
     b = None
     if base is None:
-        y = _empty(T, cols, dtype=dtype, device=yd.device)
+        y = _new((T, cols), (cols, 1), dtype)
     else:
         if not _like(base, dtype, (T, cols)):
             _need(base, "base", dtype, (T, cols))
-        y, b = _empty_like(base), base.data_ptr()
+        y, b = _new((T, cols), (cols, 1), dtype), base.data_ptr()
     rc = (_lib or load()).moe_unpermute(ctypes.byref(cfg), yd.data_ptr(), ELEMENT_TYPES[dtype], cols, inv_pos.data_ptr(), w, b,
                                         y.data_ptr(), _here(yd, inv_pos, weights, base))
     if rc:
@@ -915,11 +918,11 @@ def unpermute_backward(cfg, dy, yd, inv_pos, offsets, weights=None):
     cols, kind = dy.shape[1], dy.dtype
     dw = of = to = None
     if yd is None:
-        dyd = _empty(T * k, cols, dtype=kind, device=dy.device)
+        dyd = _new((T * k, cols), (cols, 1), kind)
     else:
         if not _like(yd, kind, (T * k, cols)):
             _need(yd, "yd", kind, (T * k, cols))
-        dyd, dw = _empty_like(yd), _empty(T, k, dtype=_f32, device=dy.device)
+        dyd, dw = _new((T * k, cols), (cols, 1), kind), _new(shape, (k, 1), _f32)
         of, to = yd.data_ptr(), dw.data_ptr()
     rc = (_lib or load()).moe_unpermute_backward(ctypes.byref(cfg), dy.data_ptr(), of, ELEMENT_TYPES[kind], cols,
                                                  inv_pos.data_ptr(), offsets.data_ptr(), w, dyd.data_ptr(), to,
@@ -979,7 +982,7 @@ def route_backward(cfg, logits, topk_idx, dtopk_w, dlogits=None) -> torch.Tensor
         _need(topk_idx, "topk_idx", _i32, (T, k))
         _need(dtopk_w, "dtopk_w", _f32, (T, k))
     if dlogits is None:
-        dlogits = _empty_like(logits)
+        dlogits = _new((T, E), (E, 1), logits.dtype)
     elif not _like(dlogits, logits.dtype, (T, E)):
         _need(dlogits, "dlogits", logits.dtype, (T, E))
     rc = (_lib or load()).moe_route_backward(ctypes.byref(cfg), logits.data_ptr(), ELEMENT_TYPES[logits.dtype],
