@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.util
 import os
 import threading
 
@@ -126,8 +127,24 @@ def load():
             L.moe_last_error.restype = ctypes.c_char_p
             L.moe_launch_count.argtypes = []
             L.moe_launch_count.restype = ctypes.c_uint64
+            _load_calls()
             _lib = L
     return _lib
+
+
+_calls = None  # csrc/calls.cpp, once the library is loaded
+
+
+def _load_calls():
+    global _calls
+    path = os.path.join(os.path.dirname(SO_PATH), "_calls.so")
+    if not os.path.exists(path):
+        raise ImportError(f"_calls.so is not built ({path}); run routing_dispatch_expert_gb300.build")
+    spec = importlib.util.spec_from_file_location("_calls", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    module.bind(MoeConfig)
+    _calls = module
 
 
 def _check(rc: int):
@@ -563,11 +580,16 @@ def balance_loss_backward(cfg, logits, counts, tokens, alpha: float, dloss, seq_
 # ------------------------------------------------------------------------------------------
 # around the experts: the norm in front, rows sorted by expert and back, and the gradients
 # ------------------------------------------------------------------------------------------
-# As above, the calls below look at their tensors in as few steps as they can and find the words of a refusal only after
-# one failed. Two thirds of the time of a call on small tensors is three allocations and a launch: outputs are made by the
-# shortest way that torch has to memory of the current device, which is the tensors' (sizes, strides, dtype; 0.85 us each,
-# torch.empty 1.45).
-_new = torch._C._dynamo.guards._empty_strided_cuda
+# On small tensors the calls below are bound by the host, so each is first made as a whole by csrc/calls.cpp. What that
+# does not take (it returns None) goes through the steps here, which find the words of a refusal.
+def _new(shape, dtype):
+    return torch.empty(shape, dtype=dtype, device="cuda")
+
+
+def _native():
+    if _calls is None:
+        load()
+    return _calls
 
 
 def _here(a, b=None, c=None, d=None, e=None):
@@ -620,6 +642,9 @@ def _norm_weight(weight, dtype, cols):
 
 def _rms_norm(x, weight, residual, eps, fp8, with_y):
     """(y, total, q, s), None where not wanted."""
+    out = (_calls or _native()).rms_norm(x, weight, residual, eps, fp8, with_y)
+    if out is not None:
+        return out
     ldx = _row_matrix(x, "x", ELEMENT_TYPES)
     shape, dtype = x.shape, x.dtype
     rows, cols = shape
@@ -629,16 +654,16 @@ def _rms_norm(x, weight, residual, eps, fp8, with_y):
     if residual is not None:
         if not (_like(residual, dtype, shape) or _like(residual, _f32, shape)):
             ldr = _row_matrix(residual, "residual", (dtype, _f32), shape)
-            total = _new((rows, cols), (cols, 1), residual.dtype)
+            total = _new((rows, cols), residual.dtype)
         else:
-            ldr, total = cols, _new((rows, cols), (cols, 1), residual.dtype)
+            ldr, total = cols, _new((rows, cols), residual.dtype)
         r, r_type, to = residual.data_ptr(), ELEMENT_TYPES[residual.dtype], total.data_ptr()
     if with_y:
-        y = _new((rows, cols), (cols, 1), dtype)
+        y = _new((rows, cols), dtype)
     if fp8:
-        q = _new((rows, cols), (cols, 1), _u8)
+        q = _new((rows, cols), _u8)
         n = (cols + 127) // 128
-        s = _new((rows, n), (n, 1), _f32)
+        s = _new((rows, n), _f32)
     rc = (_lib or load()).moe_rms_norm(x.data_ptr(), ELEMENT_TYPES[dtype], rows, cols, ldx, r, r_type, ldr, w, w_type, eps,
                                        y.data_ptr() if with_y else None, to, q.data_ptr() if fp8 else None,
                                        s.data_ptr() if fp8 else None, _here(x, weight, residual))
@@ -697,6 +722,9 @@ def rms_norm_backward(dy, total, weight=None, eps: float = 1e-6, dtotal=None, we
     """Gradient of rms_norm (moe_rms_norm_backward): (dx of dy's type, dresidual of total's type, dweight of weight's type or
     None) from dy, the total that was normalised (x without a residual) and the gradient dtotal that reaches the total
     from elsewhere. dresidual is dx itself where the types are the same. ws: rms_norm_backward_workspace."""
+    out = (_calls or _native()).rms_norm_backward(dy, total, weight, eps, dtotal, weight_gradient, ws)
+    if out is not None:
+        return out
     if not (isinstance(dy, torch.Tensor) and dy.dim() == 2 and dy.dtype in ELEMENT_TYPES and dy.is_cuda
             and dy.is_contiguous()):
         _need(dy, "dy", tuple(ELEMENT_TYPES), (None, None))
@@ -707,14 +735,14 @@ def rms_norm_backward(dy, total, weight=None, eps: float = 1e-6, dtotal=None, we
     if dtotal is not None and not _like(dtotal, of, shape):
         _need(dtotal, "dtotal", of, shape)
     w, w_type = _norm_weight(weight, kind, cols)
-    dx = _new((rows, cols), (cols, 1), kind)
+    dx = _new((rows, cols), kind)
     dresidual, dweight = dx, None
     if of is not kind:
-        dresidual = _new((rows, cols), (cols, 1), of)
+        dresidual = _new((rows, cols), of)
     if weight is not None and weight_gradient:
-        dweight = _new((cols,), (1,), weight.dtype)
+        dweight = _new((cols,), weight.dtype)
         if ws is None:
-            ws = _new((_rms_norm_backward_bytes(rows, cols),), (1,), _u8)
+            ws = _new((_rms_norm_backward_bytes(rows, cols),), _u8)
         elif not _like(ws, _u8, (ws.numel(),)):
             _need(ws, "ws", _u8, (None,))
     rc = (_lib or load()).moe_rms_norm_backward(
@@ -757,6 +785,13 @@ def sort_tokens(cfg, topk_idx, topk_w=None, ws=None) -> dict:
     """The assignments of topk_idx int32 [T, k] sorted by expert (moe_sort_tokens): counts, offsets, inv_pos [T, k], row_token
     [T k], and row_weight [T k] with topk_w fp32 [T, k]. Entries outside [0, E) are no assignment. ws:
     sort_tokens_workspace."""
+    out = (_calls or _native()).sort_tokens(cfg, topk_idx, topk_w, ws)
+    if out is not None:
+        counts, offsets, inv_pos, row_token, row_weight = out
+        out = {"counts": counts, "offsets": offsets, "inv_pos": inv_pos, "row_token": row_token}
+        if row_weight is not None:
+            out["row_weight"] = row_weight
+        return out
     T, k = cfg.T, cfg.k
     shape = (T, k)
     if not _like(topk_idx, _i32, shape):
@@ -767,15 +802,15 @@ def sort_tokens(cfg, topk_idx, topk_w=None, ws=None) -> dict:
     if ws is None:
         size = _sort_tokens_bytes(T, cfg.E, k)
         if size:
-            ws = _new((size,), (1,), _u8)
+            ws = _new((size,), _u8)
     elif not _like(ws, _u8, (ws.numel(),)):
         _need(ws, "ws", _u8, (None,))
-    counts, offsets = _new((n,), (1,), _i32), _new((n + 1,), (1,), _i32)
-    inv_pos, row_token = _new(shape, (k, 1), _i32), _new((T * k,), (1,), _i32)
+    counts, offsets = _new((n,), _i32), _new((n + 1,), _i32)
+    inv_pos, row_token = _new(shape, _i32), _new((T * k,), _i32)
     out = {"counts": counts, "offsets": offsets, "inv_pos": inv_pos, "row_token": row_token}
     w = row_weight = None
     if topk_w is not None:
-        out["row_weight"] = row_weight = _new((T * k,), (1,), _f32)
+        out["row_weight"] = row_weight = _new((T * k,), _f32)
         w, row_weight = topk_w.data_ptr(), row_weight.data_ptr()
     rc = (_lib or load()).moe_sort_tokens(
         ctypes.byref(cfg), topk_idx.data_ptr(), w, counts.data_ptr(), offsets.data_ptr(), inv_pos.data_ptr(),
@@ -806,19 +841,22 @@ _COPIED = (torch.bfloat16, _f32, torch.float16, _u8)
 
 
 def _permute(x, cfg, inv_pos, offsets, scales):
+    out = (_calls or _native()).permute(cfg, x, inv_pos, offsets, scales)
+    if out is not None:
+        return out
     T, k = cfg.T, cfg.k
     _positions(cfg, (T, k), inv_pos, offsets)
     ldx = _row_matrix(x, "x", _COPIED if scales is None else (_u8,))
     rows, cols = x.shape
     if rows != T:
         _need(x, "x", x.dtype, (T, cols), contiguous=False)
-    xd = _new((T * k, cols), (cols, 1), x.dtype)
+    xd = _new((T * k, cols), x.dtype)
     xd_scales = of = to = None
     if scales is not None:
         n = (cols + 127) // 128
         if not _like(scales, _f32, (T, n)):
             _need(scales, "scales", _f32, (T, n))
-        xd_scales = _new((T * k, n), (n, 1), _f32)
+        xd_scales = _new((T * k, n), _f32)
         of, to = scales.data_ptr(), xd_scales.data_ptr()
     rc = (_lib or load()).moe_permute(ctypes.byref(cfg), x.data_ptr(), x.element_size(), cols, ldx, of, inv_pos.data_ptr(),
                                       offsets.data_ptr(), xd.data_ptr(), to, _here(x, inv_pos, offsets, scales))
@@ -852,6 +890,9 @@ def permute(cfg, x, inv_pos, offsets, scales=None):
 
 
 def _unpermute(yd, weights, base, cfg, inv_pos):
+    y = (_calls or _native()).unpermute(cfg, yd, inv_pos, weights, base)
+    if y is not None:
+        return y
     T, k = cfg.T, cfg.k
     shape = (T, k)
     _positions(cfg, shape, inv_pos)
@@ -862,11 +903,11 @@ def _unpermute(yd, weights, base, cfg, inv_pos):
     dtype, cols = yd.dtype, yd.shape[1]
     b = None
     if base is None:
-        y = _new((T, cols), (cols, 1), dtype)
+        y = _new((T, cols), dtype)
     else:
         if not _like(base, dtype, (T, cols)):
             _need(base, "base", dtype, (T, cols))
-        y, b = _new((T, cols), (cols, 1), dtype), base.data_ptr()
+        y, b = _new((T, cols), dtype), base.data_ptr()
     rc = (_lib or load()).moe_unpermute(ctypes.byref(cfg), yd.data_ptr(), ELEMENT_TYPES[dtype], cols, inv_pos.data_ptr(), w, b,
                                         y.data_ptr(), _here(yd, inv_pos, weights, base))
     if rc:
@@ -908,6 +949,9 @@ def unpermute(cfg, yd, inv_pos, weights=None, base=None, offsets=None):
 def unpermute_backward(cfg, dy, yd, inv_pos, offsets, weights=None):
     """Gradient of unpermute (moe_unpermute_backward): (dyd [T k, cols] of dy's type, zero in the rows past the last one held;
     dweights fp32 [T, k], None where yd is None) from dy [T, cols]."""
+    out = (_calls or _native()).unpermute_backward(cfg, dy, yd, inv_pos, offsets, weights)
+    if out is not None:
+        return out
     T, k = cfg.T, cfg.k
     shape = (T, k)
     _positions(cfg, shape, inv_pos, offsets)
@@ -918,11 +962,11 @@ def unpermute_backward(cfg, dy, yd, inv_pos, offsets, weights=None):
     cols, kind = dy.shape[1], dy.dtype
     dw = of = to = None
     if yd is None:
-        dyd = _new((T * k, cols), (cols, 1), kind)
+        dyd = _new((T * k, cols), kind)
     else:
         if not _like(yd, kind, (T * k, cols)):
             _need(yd, "yd", kind, (T * k, cols))
-        dyd, dw = _new((T * k, cols), (cols, 1), kind), _new(shape, (k, 1), _f32)
+        dyd, dw = _new((T * k, cols), kind), _new(shape, _f32)
         of, to = yd.data_ptr(), dw.data_ptr()
     rc = (_lib or load()).moe_unpermute_backward(ctypes.byref(cfg), dy.data_ptr(), of, ELEMENT_TYPES[kind], cols,
                                                  inv_pos.data_ptr(), offsets.data_ptr(), w, dyd.data_ptr(), to,
@@ -975,6 +1019,10 @@ def route_weights(cfg, logits, bias=None):
 def route_backward(cfg, logits, topk_idx, dtopk_w, dlogits=None) -> torch.Tensor:
     """Gradient of the route weights with respect to the logits [T, E] (fp32 or bf16), of their dtype
     (moe_route_backward), from the chosen experts topk_idx int32 [T, k] and the weights' gradient dtopk_w fp32 [T, k]."""
+    if dlogits is None:
+        out = (_calls or _native()).route_backward(cfg, logits, topk_idx, dtopk_w)
+        if out is not None:
+            return out
     T, E, k = cfg.T, cfg.E, cfg.k
     if not (_like(logits, _f32, (T, E)) or _like(logits, torch.bfloat16, (T, E))):
         _need(logits, "logits", (_f32, torch.bfloat16), (T, E))
@@ -982,7 +1030,7 @@ def route_backward(cfg, logits, topk_idx, dtopk_w, dlogits=None) -> torch.Tensor
         _need(topk_idx, "topk_idx", _i32, (T, k))
         _need(dtopk_w, "dtopk_w", _f32, (T, k))
     if dlogits is None:
-        dlogits = _new((T, E), (E, 1), logits.dtype)
+        dlogits = _new((T, E), logits.dtype)
     elif not _like(dlogits, logits.dtype, (T, E)):
         _need(dlogits, "dlogits", logits.dtype, (T, E))
     rc = (_lib or load()).moe_route_backward(ctypes.byref(cfg), logits.data_ptr(), ELEMENT_TYPES[logits.dtype],
