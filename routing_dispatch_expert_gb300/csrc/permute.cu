@@ -5,7 +5,7 @@
 // number of earlier ones to its expert, its row the expert's offset plus that (under a placement: round robin over the
 // expert's replicas). Whole numbers only, so the order of the atomics does not show. An index outside [0, E) is no
 // assignment; ranks at and past the capacity have no row.
-//   count_kernel  assignments of each block of kItems to each expert
+//   count_kernel  assignments of each block to each expert
 //   rank_kernel   a block's ranks: the counts of the blocks before it, of the warps before a warp, and within a warp
 //                 the lanes before a lane that hold the same expert; the offsets are made again by every block
 // A batch of one block takes the second kernel alone, which then counts its own.
@@ -13,13 +13,14 @@
 // Rows are copied as words, token by token: the row is read once and written to each of its places.
 //
 // One GB300: the sort of T k assignments is bound by latency, a few dependent steps a block: 256 x 8 to 256 experts 5.8
-// us, one launch; 16384 x 8 8.7 us, 65536 x 8 14.2 us (with 1024 experts 16384 x 8 13.4 us: the blocks' counts). A
-// block adds up the others' counts itself instead of a third launch; reading them one after the other with atomics took
-// 11.8 us for 16384 x 8. The copies are bound by HBM: 16384 rows to eight places each, 7168 bytes and scales 164 us
-// (6.6 TB/s, a copy's rate is 6.78), 14336 bytes 315 us (6.7), 65536 rows of 128 bytes 13.5 us (5.6); odd 16-bit rows
-// of 1003 59 us (5.0: 64 bytes an access). Slower: bulk copies out of shared memory, a place each (186 us instead of 171
-// for the rows of 7168 bytes); odd rows by the 16-byte words of their places, shifted (65536 x 511 bf16 with the sort
-// 196 us instead of 135: the parts of words at a row's ends; only rows of kilobytes gain, 215 to 195 for 8192 x 7167).
+// us, one launch; 4096 x 8 6.6 us, 16384 x 8 8.7, 65536 x 8 14.2 (with 1024 experts 16384 x 8 13.4 us: the blocks'
+// counts). A block adds up the others' counts itself instead of a third launch; reading them one after the other with
+// atomics took 11.8 us for 16384 x 8. The copies are bound by HBM: 16384 rows to eight places each, 7168 bytes and
+// scales 164 us (6.6 TB/s, a copy's rate is 6.78), 14336 bytes 315 us (6.7), 65536 rows of 128 bytes 13.5 us (5.6); odd
+// 16-bit rows of 1003 59 us (5.0: 64 bytes an access). Slower: bulk copies out of shared memory, a place each (186 us
+// instead of 171 for the rows of 7168 bytes); odd rows by the 16-byte words of their places, shifted (65536 x 511 bf16
+// with the sort 196 us instead of 135: the parts of words at a row's ends; only rows of kilobytes gain, 215 to 195 for
+// 8192 x 7167).
 #include <algorithm>
 #include <type_traits>
 
@@ -90,7 +91,8 @@ __device__ __forceinline__ int block_prefix(int v, int* warp_sums, int& total) {
 
 // Shared memory: per warp a count of each expert, then the ranks before the warp's [kWarps][E]; for each expert the
 // ranks before this round's [E] and the assignments in all [E]; the offset of each group [max(E, n_slots)].
-constexpr int kEach = 4;  // assignments of a lane in a round
+// EACH: assignments of a lane in a round.
+template <int EACH>
 __global__ void __launch_bounds__(kThreads) rank_kernel(const SortArgs a) {
   extern __shared__ __align__(16) int32_t sh[];
   __shared__ int warp_sums[kWarps];
@@ -102,12 +104,12 @@ __global__ void __launch_bounds__(kThreads) rank_kernel(const SortArgs a) {
   const int64_t lo = blockIdx.x * a.per_block, hi = min(a.n, lo + a.per_block);
   int held = 0;
   const int bits = 32 - __clz(E);  // of 0 .. E
-  for (int64_t c0 = lo; c0 < hi; c0 += kEach * kThreads) {
-    const int64_t at = c0 + warp * 32 * kEach + lane;
-    int mine[kEach], rank[kEach];
-    float weight[kEach];
+  for (int64_t c0 = lo; c0 < hi; c0 += EACH * kThreads) {
+    const int64_t at = c0 + warp * 32 * EACH + lane;
+    int mine[EACH], rank[EACH];
+    float weight[EACH];
 #pragma unroll
-    for (int j = 0; j < kEach; ++j) {
+    for (int j = 0; j < EACH; ++j) {
       const int64_t i = at + 32 * j;
       mine[j] = i < hi ? a.idx[i] : -1;
       weight[j] = a.row_weight && i < hi ? a.weight[i] : 0.f;
@@ -116,21 +118,21 @@ __global__ void __launch_bounds__(kThreads) rank_kernel(const SortArgs a) {
     for (int e = threadIdx.x; e < kWarps / 4 * E; e += kThreads) reinterpret_cast<int4*>(cnt)[e] = make_int4(0, 0, 0, 0);
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < kEach; ++j)
+    for (int j = 0; j < EACH; ++j)
       if (mine[j] < 0 || mine[j] >= E) mine[j] = -1;
-    const bool some = c0 + warp * 32 * kEach < hi;  // of the whole warp
-    uint32_t same[kEach];  // the lanes that hold the same expert, bit by bit of its number
+    const bool some = c0 + warp * 32 * EACH < hi;  // of the whole warp
+    uint32_t same[EACH];  // the lanes that hold the same expert, bit by bit of its number
 #pragma unroll
-    for (int j = 0; j < kEach; ++j) same[j] = 0xffffffffu;
+    for (int j = 0; j < EACH; ++j) same[j] = 0xffffffffu;
     for (int b = 0; some && b < bits; ++b)
 #pragma unroll
-      for (int j = 0; j < kEach; ++j) {
+      for (int j = 0; j < EACH; ++j) {
         const bool set = (unsigned)(mine[j] < 0 ? E : mine[j]) >> b & 1u;
         const uint32_t with = __ballot_sync(0xffffffffu, set);
         same[j] &= set ? with : ~with;
       }
 #pragma unroll
-    for (int j = 0; j < kEach; ++j) {  // the first lane of an expert counts for all of its lanes
+    for (int j = 0; j < EACH; ++j) {  // the first lane of an expert counts for all of its lanes
       if (!some) break;
       const int e = mine[j];
       const uint32_t peers = same[j], before = peers & ((1u << lane) - 1u);
@@ -202,7 +204,7 @@ __global__ void __launch_bounds__(kThreads) rank_kernel(const SortArgs a) {
     }
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < kEach; ++j) {
+    for (int j = 0; j < EACH; ++j) {
       const int64_t i = at + 32 * j;
       if (i >= hi) continue;
       const int e = mine[j];
@@ -332,15 +334,22 @@ cudaError_t with_word(int64_t bytes, int64_t ld, F&& f) {
   return f(uint8_t{});
 }
 
-constexpr int64_t kItems = kEach * kThreads;  // assignments of a block of the sort, at least
-constexpr int kMaxBlocks = 128;           // every block reads every block's counts
-int64_t per_block(int64_t n) {
-  return std::max<int64_t>(kItems, cdiv(cdiv(n, kMaxBlocks), kItems) * kItems);
+// Assignments of a lane in a round of the sort. Two make twice the blocks, each of which reads every block's counts: two
+// where those are few, and four where one block then takes all (two and four: 16 x 8 to 256 experts 3.0 and 3.6 us, 4096 x 8
+// 6.6 and 9.2, 8192 x 8 7.2 and 8.1, 16384 x 8 12.0 and 8.7; to 64 experts 16384 x 8 7.3 and 8.7; to 1024 experts 2048 x 8
+// 8.9 and 12.6, 8192 x 8 12.9 and 11.5).
+constexpr int kMaxBlocks = 128;
+int each(int64_t n, int E) {
+  return n <= 2 * kThreads || (n > 4 * kThreads && n <= 2 * kThreads * kMaxBlocks && n * E <= 1 << 24) ? 2 : 4;
+}
+int64_t per_block(int64_t n, int E) {
+  const int64_t items = (int64_t)each(n, E) * kThreads;
+  return std::max<int64_t>(items, cdiv(cdiv(n, kMaxBlocks), items) * items);
 }
 
 }  // namespace pm
 
-int sort_blocks(int64_t n) { return (int)cdiv(n, pm::per_block(n)); }
+int sort_blocks(int64_t n, int E) { return (int)cdiv(n, pm::per_block(n, E)); }
 
 cudaError_t launch_sort_tokens(const SortDesc& d, int* launches, cudaStream_t stream) {
   pm::SortArgs a;
@@ -353,11 +362,11 @@ cudaError_t launch_sort_tokens(const SortDesc& d, int* launches, cudaStream_t st
   a.row_token = d.row_token;
   a.row_weight = d.row_weight;
   a.n = (int64_t)d.T * d.k;
-  a.per_block = pm::per_block(a.n);
+  a.per_block = pm::per_block(a.n, d.E);
   a.E = d.E;
   a.k = d.k;
   a.cap = d.capacity > 0 ? d.capacity : 0x7fffffff;
-  a.blocks = sort_blocks(a.n);
+  a.blocks = sort_blocks(a.n, d.E);
   a.n_slots = d.n_slots;
   a.max_replicas = d.max_replicas;
   a.slot_expert = d.slot_expert;
@@ -377,8 +386,9 @@ cudaError_t launch_sort_tokens(const SortDesc& d, int* launches, cudaStream_t st
   cudaError_t e = per_device<bool>(
       attr,
       [](bool& v) {
-        const cudaError_t r = cudaFuncSetAttribute(pm::rank_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   (int)(sizeof(int32_t) * (pm::kWarps + 3) * 1024));
+        constexpr int kMost = (int)(sizeof(int32_t) * (pm::kWarps + 3) * 1024);
+        cudaError_t r = cudaFuncSetAttribute(pm::rank_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+        if (r == cudaSuccess) r = cudaFuncSetAttribute(pm::rank_kernel<4>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
         v = r == cudaSuccess;
         return r;
       },
@@ -399,7 +409,7 @@ cudaError_t launch_sort_tokens(const SortDesc& d, int* launches, cudaStream_t st
   cfg.attrs = &early;
   cfg.numAttrs = a.blocks > 1 ? 1 : 0;
   ++*launches;
-  return cudaLaunchKernelEx(&cfg, pm::rank_kernel, a);
+  return cudaLaunchKernelEx(&cfg, pm::each(a.n, d.E) == 2 ? pm::rank_kernel<2> : pm::rank_kernel<4>, a);
 }
 
 cudaError_t launch_permute(const PermuteDesc& d, cudaStream_t stream) {
