@@ -460,9 +460,9 @@ int moe_balance_loss_backward(const moe_config* cfg, const void* logits, int32_t
  *   y         [rows, cols] of x_type out, or NULL
  *   total     [rows, cols] of residual_type out, or NULL. It is the unrounded total that is normalised and quantised.
  *   q, s      [rows, cols] e4m3 codes and [rows, ceil(cols / 128)] scales of y out, or both NULL: scale = amax / 448 of
- *             128 columns, at least 2^-126 (1 where all are zero), code = e4m3(RN(y * RN(1 / scale))). A block that
- *             holds an infinity or a NaN stands for NaN. The form of the FP8 layer's rows (moe_dispatch), of y before
- *             it is rounded.
+ *             128 columns, at least 2^-126 (1 where all are zero), code = e4m3(RN(y / scale)). A block that holds an
+ *             infinity or a NaN stands for NaN. Layout, codes and scales are those of the FP8 layer's rows (moe_dispatch,
+ *             which has no least scale), of y before it is rounded.
  * Outputs are contiguous. total may be residual, or y or total x, where those are contiguous; outputs overlap nothing
  * else.
  * 1 <= cols <= 16384; eps >= 0. One launch. Errors: MOE_ERR_INVALID, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA. */

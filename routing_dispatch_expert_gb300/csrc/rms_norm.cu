@@ -2,16 +2,16 @@
 // rms_norm_backward.cu.)
 //
 //   t = x + r,  n = t * rstd,  rstd = 1 / sqrt(mean(t^2) + eps),  y = n * w
-//   scale of 128 columns = amax |y| / 448 (at least 2^-126; 1 where all are 0), code = e4m3(RN(y RN(1 / scale)))
+//   scale of 128 columns = amax |y| / 448 (at least 2^-126; 1 where all are 0), code = e4m3(RN(y / scale))
 //
 // Everything is fp32: the sum is normalised and quantised before it is rounded for the residual stream, and each output
 // is rounded once.
 //
 // Bound by HBM: a row is read once and held on the SM between its reduction and its outputs. One GB300, out of HBM (a
 // copy's rate is 6.78 TB/s), x and residual of one type:
-//   16384 x 7168 bf16 to bf16 and e4m3   162 us, 6.5 TB/s     8192 x 7168 fp32   137 us, 6.9 TB/s
+//   16384 x 7168 bf16 to bf16 and e4m3   163 us, 6.5 TB/s     8192 x 7168 fp32   137 us, 6.9 TB/s
 //   65536 x 512 bf16                      41 us, 6.6          65536 x 64 bf16    6.6 us, 5.1
-//   8192 x 7166 bf16 (with codes)         94 us, 5.0 (99)     65536 x 34 bf16    5.8 us, 3.1
+//   8192 x 7166 bf16 (with codes)         94 us, 5.0 (100)    65536 x 34 bf16    5.8 us, 3.1
 //   8192 x 7167 bf16 (with codes)        101 us, 4.6 (135)    65536 x 33 bf16    6.5 us, 2.7
 //   one row of 4096                      2.7 us, launch
 // 16-bit rows that are not whole 16 bytes are bound by their accesses of one number or two. Three blocks of 448 threads
@@ -42,10 +42,14 @@ struct Args {
   float eps;
 };
 
-// Codes and scales of a chunk: two blocks of 128 columns. The codes are made with the reciprocal, 1.5 ulp of fp32 off
-// the quotient: that moves a code only where y / scale is that close to a midpoint, which unlike for rows of few bits
-// is rare here, and takes one instruction instead of eight. The largest magnitude is taken over the bits, under which a
-// NaN is larger than every number: a block that holds an infinity or a NaN stands for NaN throughout.
+// Codes and scales of a chunk: two blocks of 128 columns. The codes are e4m3(RN(y / scale)), those of the FP8 layer's
+// rows. 1 / scale is taken as by + rest, by rounded down and rest what it lacks, and the quotient as fma(y, by, y * rest):
+// the product by a constant in two parts of Brisebarre and Muller, "Correctly rounded multiplication by arbitrary
+// precision constants" (2008). It is RN(y / scale) unless the quotient lies within 2^-46 of itself from the middle of two
+// fp32 numbers (scales below 2^100; past them rest loses bits). rest is not negative, so zeros keep their sign. 16384 x
+// 7168 to codes 163 us; with a division a number 174; by the rounded reciprocal alone 162, one code in 10^6 another, next
+// to a midpoint. The largest magnitude is taken over the bits, under which a NaN is larger than every number: a block
+// that holds an infinity or a NaN stands for NaN throughout.
 template <int MAP, int LANES>
 __device__ __forceinline__ void quantize(const Args& a, int64_t row, int c0, int cols, int lane, const float (&y)[8]) {
   constexpr bool kOne = MAP == kMap8 || LANES < 32;  // a lane's columns lie in one block
@@ -69,9 +73,10 @@ __device__ __forceinline__ void quantize(const Args& a, int64_t row, int c0, int
     constexpr int kN = kOne ? 8 : 4;
     float scale = 1.f;
     if (m[h]) scale = m[h] > kInfBits ? __uint_as_float(m[h]) : fmaxf(__fdiv_rn(__uint_as_float(m[h]), 448.0f), 1.1754944e-38f);
-    const float by = __frcp_rn(scale);
+    const float by = __frcp_rd(scale), e = fmaf(-by, scale, 1.f);  // 1 / scale = by / (1 - e) = by (1 + e + e^2 + ..)
+    const float rest = by > 0.f ? fmaf(e, e, e) * by : 0.f;         // 0 under an infinite scale
 #pragma unroll
-    for (int i = 0; i < kN; ++i) v[4 * h + i] = y[4 * h + i] * by;
+    for (int i = 0; i < kN; ++i) v[4 * h + i] = fmaf(y[4 * h + i], by, y[4 * h + i] * rest);
     const int b = c0 / 128 + (kOne ? lane / 16 : h);
     if ((kOne ? lane % 16 : lane) == 0 && b < nb && cols > 0) a.s[row * nb + b] = scale;
   }
