@@ -308,6 +308,7 @@ def quantize_weights_nvfp4(w: torch.Tensor):
 _current_device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _u8, _i32, _f32 = torch.uint8, torch.int32, torch.float32
+_forward_ad = torch.autograd.forward_ad
 
 
 def _like(t, dtype, shape):
@@ -327,6 +328,16 @@ def _need(t, name, dtypes, shape, contiguous=True):
         raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
     if contiguous and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+
+
+def _no_tangents(*tensors):
+    """Refuses a tensor with a tangent of forward mode: no call of the library takes a derivative that way, and an output
+    without one would stand for a derivative of zero."""
+    if getattr(_forward_ad, "_current_level", 0) < 0:  # no level is open
+        return
+    for t in tensors:
+        if isinstance(t, torch.Tensor) and _forward_ad.unpack_dual(t).tangent is not None:
+            raise NotImplementedError("there is no forward-mode derivative of this call")
 
 
 def _fp4_format(fmt):
@@ -502,6 +513,7 @@ def _balance_inputs(cfg, logits, seq_offsets, token_mask):
 
 def _balance_loss(logits, cfg, topk_idx, alpha, seq_offsets, token_mask, ws):
     """(loss, counts, mean_prob, tokens)."""
+    _no_tangents(logits)
     S, kind, offsets, mask = _balance_inputs(cfg, logits, seq_offsets, token_mask)
     if not _like(topk_idx, _i32, (cfg.T, cfg.k)):
         _need(topk_idx, "topk_idx", _i32, (cfg.T, cfg.k))
@@ -645,6 +657,7 @@ def _rms_norm(x, weight, residual, eps, fp8, with_y):
     out = (_calls or _native()).rms_norm(x, weight, residual, eps, fp8, with_y)
     if out is not None:
         return out
+    _no_tangents(x, weight, residual)
     ldx = _row_matrix(x, "x", ELEMENT_TYPES)
     shape, dtype = x.shape, x.dtype
     rows, cols = shape
@@ -725,6 +738,7 @@ def rms_norm_backward(dy, total, weight=None, eps: float = 1e-6, dtotal=None, we
     out = (_calls or _native()).rms_norm_backward(dy, total, weight, eps, dtotal, weight_gradient, ws)
     if out is not None:
         return out
+    _no_tangents(dy, total, weight, dtotal)
     if not (isinstance(dy, torch.Tensor) and dy.dim() == 2 and dy.dtype in ELEMENT_TYPES and dy.is_cuda
             and dy.is_contiguous()):
         _need(dy, "dy", tuple(ELEMENT_TYPES), (None, None))
@@ -792,6 +806,7 @@ def sort_tokens(cfg, topk_idx, topk_w=None, ws=None) -> dict:
         if row_weight is not None:
             out["row_weight"] = row_weight
         return out
+    _no_tangents(topk_w)
     T, k = cfg.T, cfg.k
     shape = (T, k)
     if not _like(topk_idx, _i32, shape):
@@ -844,6 +859,7 @@ def _permute(x, cfg, inv_pos, offsets, scales):
     out = (_calls or _native()).permute(cfg, x, inv_pos, offsets, scales)
     if out is not None:
         return out
+    _no_tangents(x, scales)
     T, k = cfg.T, cfg.k
     _positions(cfg, (T, k), inv_pos, offsets)
     ldx = _row_matrix(x, "x", _COPIED if scales is None else (_u8,))
@@ -893,6 +909,7 @@ def _unpermute(yd, weights, base, cfg, inv_pos):
     y = (_calls or _native()).unpermute(cfg, yd, inv_pos, weights, base)
     if y is not None:
         return y
+    _no_tangents(yd, weights, base)
     T, k = cfg.T, cfg.k
     shape = (T, k)
     _positions(cfg, shape, inv_pos)
@@ -952,6 +969,7 @@ def unpermute_backward(cfg, dy, yd, inv_pos, offsets, weights=None):
     out = (_calls or _native()).unpermute_backward(cfg, dy, yd, inv_pos, offsets, weights)
     if out is not None:
         return out
+    _no_tangents(dy, yd, weights)
     T, k = cfg.T, cfg.k
     shape = (T, k)
     _positions(cfg, shape, inv_pos, offsets)
@@ -978,6 +996,7 @@ def unpermute_backward(cfg, dy, yd, inv_pos, offsets, weights=None):
 
 def _route_weights(logits, cfg, bias):
     """(topk_idx, topk_w)."""
+    _no_tangents(logits, bias)
     if not _like(logits, _f32, (cfg.T, cfg.E)):
         _need(logits, "logits", _f32, (cfg.T, cfg.E))
     if bias is not None and not _like(bias, _f32, (cfg.E,)):
@@ -1023,6 +1042,7 @@ def route_backward(cfg, logits, topk_idx, dtopk_w, dlogits=None) -> torch.Tensor
         out = (_calls or _native()).route_backward(cfg, logits, topk_idx, dtopk_w)
         if out is not None:
             return out
+    _no_tangents(logits, dtopk_w)
     T, E, k = cfg.T, cfg.E, cfg.k
     if not (_like(logits, _f32, (T, E)) or _like(logits, torch.bfloat16, (T, E))):
         _need(logits, "logits", (_f32, torch.bfloat16), (T, E))
