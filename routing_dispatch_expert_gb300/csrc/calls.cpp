@@ -41,12 +41,13 @@ int element_type(ScalarType s) {
   return s == kF32 ? MOE_TYPE_F32 : s == ScalarType::BFloat16 ? MOE_TYPE_BF16 : s == ScalarType::Half ? MOE_TYPE_F16 : -1;
 }
 
-// Everything has to be on the current device, and without a tangent of forward mode, of which the outputs would know
-// nothing.
+// Everything has to be on the current device, in memory of its own (a wrapper's tensor has none, nor one whose storage was
+// given up, whatever their addresses) and without a tangent of forward mode, of which the outputs would know nothing.
 struct Here {
   int device = -1;
   bool holds(const Tensor& t) {
     if (!t.is_cuda() || t._fw_grad(0).defined()) return false;
+    if (t.numel() && !(t.has_storage() && t.storage().data())) return false;
     if (device < 0) device = c10::cuda::current_device();
     return t.get_device() == device;
   }

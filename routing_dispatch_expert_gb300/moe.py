@@ -152,8 +152,17 @@ def _check(rc: int):
         raise MoeError(rc, load().moe_last_error().decode())
 
 
+def _memory(t):
+    """Address of a tensor. One without memory of its own (a wrapper's, say) is refused: it has the address of its offset, and
+    without one would be taken for a tensor that was not given."""
+    p = t.data_ptr()
+    if p < 1 << 40 and t.numel() and p <= t.storage_offset() * t.element_size():  # no offset is past 2^40 bytes
+        raise ValueError("a tensor has no memory of its own")
+    return p
+
+
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else ctypes.c_void_p(_memory(t))
 
 
 def _stream():
@@ -215,7 +224,7 @@ class Weights:
                             w_gu_shared=w_gu_shared, s_gu_shared=s_gu_shared, w_d_shared=w_d_shared,
                             s_d_shared=s_d_shared, g_gu=g_gu, g_d=g_d, g_gu_shared=g_gu_shared,
                             g_d_shared=g_d_shared)
-        self.struct = MoeWeightsStruct(**{n: (None if t is None else t.data_ptr()) for n, t in self.tensors.items()})
+        self.struct = MoeWeightsStruct(**{n: _address(t) for n, t in self.tensors.items()})
 
 
 def workspace_size(cfg: MoeConfig) -> int:
@@ -340,6 +349,14 @@ def _no_tangents(*tensors):
             raise NotImplementedError("there is no forward-mode derivative of this call")
 
 
+def _plain(*tensors):
+    """Refuses what a kernel would not see of the tensors among these: a tangent, or that there is no memory."""
+    _no_tangents(*tensors)
+    for t in tensors:
+        if isinstance(t, torch.Tensor):
+            _memory(t)
+
+
 def _fp4_format(fmt):
     if fmt not in FP4_FORMATS:
         raise ValueError(f"unknown 4-bit format {fmt!r}: 'nvfp4' or 'mxfp4'")
@@ -363,7 +380,7 @@ def _fp4_scale(g, name):
         return None
     if not _like(g, _f32, (1,)):
         _need(g, name, _f32, (1,))
-    return g.data_ptr()
+    return _memory(g)
 
 
 def quantize_fp4(x: torch.Tensor, fmt: str = "nvfp4", g: torch.Tensor | None = None, q=None, s=None):
@@ -386,8 +403,8 @@ def quantize_fp4(x: torch.Tensor, fmt: str = "nvfp4", g: torch.Tensor | None = N
         s = torch.empty(rows, n, dtype=_u8, device=x.device)
     elif not _like(s, _u8, (rows, n)):
         _need(s, "s", _u8, (rows, n))
-    _check((_lib or load()).moe_quantize_fp4(x.data_ptr(), ELEMENT_TYPES[x.dtype], rows, cols, ldx if rows > 1 else cols,
-                                             f, _fp4_scale(g, "g"), q.data_ptr(), s.data_ptr(),
+    _check((_lib or load()).moe_quantize_fp4(_memory(x), ELEMENT_TYPES[x.dtype], rows, cols, ldx if rows > 1 else cols,
+                                             f, _fp4_scale(g, "g"), _memory(q), _memory(s),
                                              _raw_stream(_current_device())))
     return q, s
 
@@ -401,8 +418,8 @@ def dequantize_fp4(q: torch.Tensor, s: torch.Tensor, fmt: str = "nvfp4", g: torc
         y = torch.empty(rows, cols, dtype=dtype, device=q.device)
     if y.dtype not in ELEMENT_TYPES or not _like(y, y.dtype, (rows, cols)):
         _need(y, "y", tuple(ELEMENT_TYPES), (rows, cols))
-    _check((_lib or load()).moe_dequantize_fp4(q.data_ptr(), s.data_ptr(), rows, cols, f, _fp4_scale(g, "g"),
-                                               ELEMENT_TYPES[y.dtype], y.data_ptr(), _raw_stream(_current_device())))
+    _check((_lib or load()).moe_dequantize_fp4(_memory(q), _memory(s), rows, cols, f, _fp4_scale(g, "g"),
+                                               ELEMENT_TYPES[y.dtype], _memory(y), _raw_stream(_current_device())))
     return y
 
 
@@ -429,9 +446,9 @@ def matmul_fp4(aq, a_s, bq, b_s, fmt: str = "nvfp4", ga=None, gb=None, dtype=tor
             raise ValueError("the elements of a row of y must be contiguous")
     if status is not None:
         _need(status, "status", _i32, (1,))
-    _check((_lib or load()).moe_matmul_fp4(aq.data_ptr(), a_s.data_ptr(), _fp4_scale(ga, "ga"), bq.data_ptr(),
-                                           b_s.data_ptr(), _fp4_scale(gb, "gb"), M, N, K, f, ELEMENT_TYPES[y.dtype],
-                                           y.data_ptr(), ldy, None if status is None else status.data_ptr(),
+    _check((_lib or load()).moe_matmul_fp4(_memory(aq), _memory(a_s), _fp4_scale(ga, "ga"), _memory(bq),
+                                           _memory(b_s), _fp4_scale(gb, "gb"), M, N, K, f, ELEMENT_TYPES[y.dtype],
+                                           _memory(y), ldy, _address(status),
                                            _raw_stream(_current_device())))
     return y
 
@@ -460,7 +477,7 @@ def _act(act: Fp4Activations | None):
 
 
 def _address(t):
-    return None if t is None else t.data_ptr()
+    return None if t is None else _memory(t)
 
 
 def dispatch_fp4(cfg, act: Fp4Activations | None, x, topk_idx, topk_w, counts, offsets, inv_pos, row_token, row_weight,
@@ -499,7 +516,7 @@ def _balance_inputs(cfg, logits, seq_offsets, token_mask):
     if token_mask is not None:
         if not (_like(token_mask, _u8, (cfg.T,)) or _like(token_mask, torch.bool, (cfg.T,))):
             _need(token_mask, "token_mask", (_u8, torch.bool), (cfg.T,))
-        mask = token_mask.data_ptr()
+        mask = _memory(token_mask)
     n_seq = 1
     if seq_offsets is not None:
         if not (isinstance(seq_offsets, torch.Tensor) and _like(seq_offsets, _i32, (seq_offsets.numel(),))):
@@ -507,7 +524,7 @@ def _balance_inputs(cfg, logits, seq_offsets, token_mask):
         n_seq = seq_offsets.shape[0] - 1
         if n_seq < 1:
             raise ValueError("seq_offsets must hold the begin of each sequence and the end of the last")
-        offsets = seq_offsets.data_ptr()
+        offsets = _memory(seq_offsets)
     return n_seq, ELEMENT_TYPES[logits.dtype], offsets, mask
 
 
@@ -526,9 +543,9 @@ def _balance_loss(logits, cfg, topk_idx, alpha, seq_offsets, token_mask, ws):
     counts = torch.empty(S, cfg.E, dtype=_i32, device=dev)
     mean = torch.empty(S, cfg.E, dtype=_f32, device=dev)
     tokens = torch.empty(S, dtype=_i32, device=dev)
-    _check((_lib or load()).moe_balance_loss(ctypes.byref(cfg), logits.data_ptr(), kind, topk_idx.data_ptr(), offsets, S,
-                                             mask, alpha, loss.data_ptr(), counts.data_ptr(), mean.data_ptr(),
-                                             tokens.data_ptr(), ws.data_ptr(), ws.numel(),
+    _check((_lib or load()).moe_balance_loss(ctypes.byref(cfg), _memory(logits), kind, _memory(topk_idx), offsets, S,
+                                             mask, alpha, loss.data_ptr(), _memory(counts), mean.data_ptr(),
+                                             _memory(tokens), _memory(ws), ws.numel(),
                                              _raw_stream(_current_device())))
     return loss, counts, mean, tokens
 
@@ -583,9 +600,9 @@ def balance_loss_backward(cfg, logits, counts, tokens, alpha: float, dloss, seq_
         dlogits = torch.empty_like(logits)
     else:
         _need(dlogits, "dlogits", logits.dtype, (cfg.T, cfg.E))
-    _check((_lib or load()).moe_balance_loss_backward(ctypes.byref(cfg), logits.data_ptr(), kind, counts.data_ptr(),
-                                                      tokens.data_ptr(), offsets, S, mask, alpha, dloss.data_ptr(),
-                                                      dlogits.data_ptr(), _raw_stream(_current_device())))
+    _check((_lib or load()).moe_balance_loss_backward(ctypes.byref(cfg), _memory(logits), kind, _memory(counts),
+                                                      _memory(tokens), offsets, S, mask, alpha, _memory(dloss),
+                                                      _memory(dlogits), _raw_stream(_current_device())))
     return dlogits
 
 
@@ -657,7 +674,7 @@ def _rms_norm(x, weight, residual, eps, fp8, with_y):
     out = (_calls or _native()).rms_norm(x, weight, residual, eps, fp8, with_y)
     if out is not None:
         return out
-    _no_tangents(x, weight, residual)
+    _plain(x, weight, residual)
     ldx = _row_matrix(x, "x", ELEMENT_TYPES)
     shape, dtype = x.shape, x.dtype
     rows, cols = shape
@@ -738,7 +755,7 @@ def rms_norm_backward(dy, total, weight=None, eps: float = 1e-6, dtotal=None, we
     out = (_calls or _native()).rms_norm_backward(dy, total, weight, eps, dtotal, weight_gradient, ws)
     if out is not None:
         return out
-    _no_tangents(dy, total, weight, dtotal)
+    _plain(dy, total, weight, dtotal, ws)
     if not (isinstance(dy, torch.Tensor) and dy.dim() == 2 and dy.dtype in ELEMENT_TYPES and dy.is_cuda
             and dy.is_contiguous()):
         _need(dy, "dy", tuple(ELEMENT_TYPES), (None, None))
@@ -806,7 +823,7 @@ def sort_tokens(cfg, topk_idx, topk_w=None, ws=None) -> dict:
         if row_weight is not None:
             out["row_weight"] = row_weight
         return out
-    _no_tangents(topk_w)
+    _plain(topk_idx, topk_w, ws)
     T, k = cfg.T, cfg.k
     shape = (T, k)
     if not _like(topk_idx, _i32, shape):
@@ -859,7 +876,7 @@ def _permute(x, cfg, inv_pos, offsets, scales):
     out = (_calls or _native()).permute(cfg, x, inv_pos, offsets, scales)
     if out is not None:
         return out
-    _no_tangents(x, scales)
+    _plain(x, inv_pos, offsets, scales)
     T, k = cfg.T, cfg.k
     _positions(cfg, (T, k), inv_pos, offsets)
     ldx = _row_matrix(x, "x", _COPIED if scales is None else (_u8,))
@@ -909,7 +926,7 @@ def _unpermute(yd, weights, base, cfg, inv_pos):
     y = (_calls or _native()).unpermute(cfg, yd, inv_pos, weights, base)
     if y is not None:
         return y
-    _no_tangents(yd, weights, base)
+    _plain(yd, inv_pos, weights, base)
     T, k = cfg.T, cfg.k
     shape = (T, k)
     _positions(cfg, shape, inv_pos)
@@ -969,7 +986,7 @@ def unpermute_backward(cfg, dy, yd, inv_pos, offsets, weights=None):
     out = (_calls or _native()).unpermute_backward(cfg, dy, yd, inv_pos, offsets, weights)
     if out is not None:
         return out
-    _no_tangents(dy, yd, weights)
+    _plain(dy, yd, inv_pos, offsets, weights)
     T, k = cfg.T, cfg.k
     shape = (T, k)
     _positions(cfg, shape, inv_pos, offsets)
@@ -996,7 +1013,7 @@ def unpermute_backward(cfg, dy, yd, inv_pos, offsets, weights=None):
 
 def _route_weights(logits, cfg, bias):
     """(topk_idx, topk_w)."""
-    _no_tangents(logits, bias)
+    _plain(logits, bias)
     if not _like(logits, _f32, (cfg.T, cfg.E)):
         _need(logits, "logits", _f32, (cfg.T, cfg.E))
     if bias is not None and not _like(bias, _f32, (cfg.E,)):
@@ -1042,7 +1059,7 @@ def route_backward(cfg, logits, topk_idx, dtopk_w, dlogits=None) -> torch.Tensor
         out = (_calls or _native()).route_backward(cfg, logits, topk_idx, dtopk_w)
         if out is not None:
             return out
-    _no_tangents(logits, dtopk_w)
+    _plain(logits, topk_idx, dtopk_w, dlogits)
     T, E, k = cfg.T, cfg.E, cfg.k
     if not (_like(logits, _f32, (T, E)) or _like(logits, torch.bfloat16, (T, E))):
         _need(logits, "logits", (_f32, torch.bfloat16), (T, E))
