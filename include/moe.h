@@ -494,7 +494,8 @@ int moe_rms_norm_backward(const void* dy, int32_t y_type, int64_t rows, int64_t 
  *              assignment, -1 where it has none
  *   row_token, row_weight      [T*k] out: token and weight of each row; -1 and 0 for the rows past the last one held
  *              (offsets[E], or offsets[n_slots])
- *   ws         moe_sort_tokens_workspace_size() bytes (0 where one launch does it: NULL); its contents do not matter
+ *   ws         moe_sort_tokens_workspace_size() bytes (0 where one launch does it: NULL); its contents do not matter. The
+ *              size grows with T*k and E alone and never falls: the largest batch's workspace serves the smaller ones
  * One launch for T*k <= 2048, else two. Errors: MOE_ERR_INVALID, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE,
  * MOE_ERR_CUDA. */
 int moe_sort_tokens_workspace_size(const moe_config* cfg, size_t* bytes);

@@ -1301,7 +1301,7 @@ namespace {
 
 // the counts and offsets of the rows are those of the layer's experts (slots)
 size_t sort_bytes(const moe_config* c) {
-  const int blocks = moe::sort_blocks((int64_t)c->T * c->k, c->E);
+  const int blocks = moe::sort_most_blocks((int64_t)c->T * c->k);
   return blocks > 1 ? align256(sizeof(int32_t) * (size_t)blocks * c->E) : 0;  // one block counts for itself
 }
 

@@ -301,7 +301,8 @@ struct RmsNormBackwardDesc {
 cudaError_t launch_rms_norm_backward(const RmsNormBackwardDesc& d, int* launches, cudaStream_t stream);
 
 // Assignments sorted by expert, and rows there (permute.cu) and back (unpermute.cu).
-int sort_blocks(int64_t n, int E);  // of n assignments; scratch: sort_blocks(n, E) * E ints
+int sort_blocks(int64_t n, int E);  // of n assignments
+int sort_most_blocks(int64_t n);    // of n or fewer, whatever E; scratch: E ints for each, none for one block
 struct SortDesc {
   const int32_t* topk_idx;
   const float* topk_w;  // or nullptr
