@@ -4,7 +4,8 @@
 // experts each 12.5 and 23, the routing gradient 3.9 and 8.7 (the launch alone 2.5).
 //
 // Arguments that are not all as the entry point wants them, and calls that it refuses, return None: the binding in moe.py
-// then goes through them one by one and finds the words. Nothing has been launched in that case.
+// then goes through them one by one and finds the words. Nothing has been launched in that case: an entry point refuses
+// before its first launch. What goes wrong behind that, a launch, raises MoeError at once.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -26,6 +27,7 @@ using at::ScalarType;
 using at::Tensor;
 
 PyTypeObject* config_type = nullptr;  // moe.MoeConfig
+PyObject* error_type = nullptr;       // moe.MoeError
 
 constexpr ScalarType kF32 = ScalarType::Float, kInt = ScalarType::Int, kByte = ScalarType::Byte;
 
@@ -121,13 +123,27 @@ PyObject* tuple_of(const T&... t) {
     if (!(condition)) Py_RETURN_NONE; \
   } while (0)
 
-PyObject* bind(PyObject*, PyObject* type) {
-  if (!PyType_Check(type)) {
-    PyErr_SetString(PyExc_TypeError, "the configuration's class");
+// After a call: goes on where it was made, returns None where it was refused.
+#define MADE(rc)                                                                                     \
+  do {                                                                                               \
+    if ((rc) == MOE_ERR_INVALID || (rc) == MOE_ERR_UNSUPPORTED || (rc) == MOE_ERR_WORKSPACE) Py_RETURN_NONE; \
+    if ((rc) != MOE_OK) return failed(rc);                                                           \
+  } while (0)
+
+PyObject* failed(int rc) {
+  PyObject* error = PyObject_CallFunction(error_type, "is", rc, moe_last_error());
+  if (error) PyErr_SetObject(error_type, error);
+  Py_XDECREF(error);
+  return nullptr;
+}
+
+PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (n != 2 || !PyType_Check(args[0]) || !PyExceptionClass_Check(args[1])) {
+    PyErr_SetString(PyExc_TypeError, "the classes of a configuration and of an error");
     return nullptr;
   }
-  Py_INCREF(type);
-  config_type = reinterpret_cast<PyTypeObject*>(type);
+  config_type = reinterpret_cast<PyTypeObject*>(Py_NewRef(args[0]));
+  error_type = Py_NewRef(args[1]);
   Py_RETURN_NONE;
 }
 
@@ -160,7 +176,7 @@ PyObject* rms_norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
                       w ? element_type(w->scalar_type()) : type, eps, address(y), address(total), address(q),
                       static_cast<float*>(address(s)), here.stream());
   }
-  WANT(rc == MOE_OK);
+  MADE(rc);
   return tuple_of(y, total, q, s);
   END_HANDLE_TH_ERRORS
 }
@@ -198,7 +214,7 @@ PyObject* rms_norm_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
                                w ? element_type(w->scalar_type()) : type, eps, address(dx), address(dr), address(dw), address(ws),
                                ws.defined() ? (size_t)ws.numel() : 0, here.stream());
   }
-  WANT(rc == MOE_OK);
+  MADE(rc);
   PyObject* out = tuple_of(dx, dr, dw);
   if (out && !dr.defined()) {  // the residual's is dx itself
     PyObject* same = PyTuple_GET_ITEM(out, 0);
@@ -240,7 +256,7 @@ PyObject* sort_tokens(PyObject*, PyObject* const* args, Py_ssize_t n) {
                          static_cast<int32_t*>(address(inv)), static_cast<int32_t*>(address(token)),
                          static_cast<float*>(address(weight)), address(ws), ws.defined() ? (size_t)ws.numel() : 0, here.stream());
   }
-  WANT(rc == MOE_OK);
+  MADE(rc);
   return tuple_of(counts, offsets, inv, token, weight);
   END_HANDLE_TH_ERRORS
 }
@@ -270,7 +286,7 @@ PyObject* permute(PyObject*, PyObject* const* args, Py_ssize_t n) {
                      static_cast<const int32_t*>(address(inv)), static_cast<const int32_t*>(address(offsets)), address(xd),
                      static_cast<float*>(address(xs)), here.stream());
   }
-  WANT(rc == MOE_OK);
+  MADE(rc);
   return scales ? tuple_of(xd, xs) : wrapped(xd);
   END_HANDLE_TH_ERRORS
 }
@@ -296,7 +312,7 @@ PyObject* unpermute(PyObject*, PyObject* const* args, Py_ssize_t n) {
     rc = moe_unpermute(&c, address(yd), element_type(kind), cols, static_cast<const int32_t*>(address(inv)),
                        static_cast<const float*>(address(w)), address(base), address(y), here.stream());
   }
-  WANT(rc == MOE_OK);
+  MADE(rc);
   return wrapped(y);
   END_HANDLE_TH_ERRORS
 }
@@ -325,7 +341,7 @@ PyObject* unpermute_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
                                 static_cast<const int32_t*>(address(offsets)), static_cast<const float*>(address(w)), address(dyd),
                                 static_cast<float*>(address(dw)), here.stream());
   }
-  WANT(rc == MOE_OK);
+  MADE(rc);
   return tuple_of(dyd, dw);
   END_HANDLE_TH_ERRORS
 }
@@ -349,13 +365,13 @@ PyObject* route_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
     rc = moe_route_backward(&c, address(z), element_type(kind), static_cast<const int32_t*>(address(idx)),
                             static_cast<const float*>(address(dw)), address(out), here.stream());
   }
-  WANT(rc == MOE_OK);
+  MADE(rc);
   return wrapped(out);
   END_HANDLE_TH_ERRORS
 }
 
 #define CALL(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(name)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {{"bind", bind, METH_O, nullptr}, CALL(rms_norm), CALL(rms_norm_backward), CALL(sort_tokens), CALL(permute),
+PyMethodDef methods[] = {CALL(bind), CALL(rms_norm), CALL(rms_norm_backward), CALL(sort_tokens), CALL(permute),
                          CALL(unpermute), CALL(unpermute_backward), CALL(route_backward), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -143,7 +143,7 @@ def _load_calls():
     spec = importlib.util.spec_from_file_location("_calls", path)
     module = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(module)
-    module.bind(MoeConfig)
+    module.bind(MoeConfig, MoeError)
     _calls = module
 
 
