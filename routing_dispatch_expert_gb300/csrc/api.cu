@@ -26,6 +26,7 @@ int fail(int code, const std::string& msg) {
 
 int cuda_fail(cudaError_t e, const char* what) {
   g_err = std::string(what) + ": " + cudaGetErrorName(e) + " (" + cudaGetErrorString(e) + ")";
+  cudaGetLastError();  // reported here: the next launch's check, the caller's own say, is not to find it
   return MOE_ERR_CUDA;
 }
 

@@ -400,6 +400,8 @@ cudaError_t launch_sort_tokens(const SortDesc& d, int* launches, cudaStream_t st
   if (e != cudaSuccess) return e;
   if (a.blocks > 1) {
     pm::count_kernel<<<a.blocks, pm::kThreads, sizeof(int32_t) * d.E, stream>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
     ++*launches;
   }
   cudaLaunchConfig_t cfg = {};

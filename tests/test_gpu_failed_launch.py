@@ -69,3 +69,19 @@ def test_reported_at_once(monkeypatch, name):
         monkeypatch.undo()
         call()
         stream.synchronize()
+
+
+@pytest.mark.parametrize("name", ["rms_norm", "rms_norm_backward", "sort_tokens", "permute", "unpermute", "unpermute_backward",
+                                  "route_backward"])
+def test_nothing_is_left_behind(name):
+    """The error is the call's alone: the runtime's last error, which the next launch of any other code looks at, is clear."""
+    call, stream = calls()[name], torch.cuda.Stream()
+    rt = ctypes.CDLL(f"libcudart.so.{torch.version.cuda.split('.')[0]}")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        call()
+        stream.synchronize()
+        with ended_capture(stream):
+            with pytest.raises(rde.MoeError):
+                call()
+            assert rt.cudaPeekAtLastError() == 0
