@@ -11,6 +11,7 @@ import functools
 import importlib.util
 import os
 import threading
+import warnings
 
 import torch
 
@@ -132,19 +133,33 @@ def load():
     return _lib
 
 
+class _NoCalls:
+    """In the place of csrc/calls.cpp where it is not built: takes no call, so that each goes through its steps here."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
 _calls = None  # csrc/calls.cpp, once the library is loaded
 
 
 def _load_calls():
+    """The module as it is built for this torch and Python. The library's calls do not need it: those that it makes are made
+    here then, at two to three times the host time."""
     global _calls
-    path = os.path.join(os.path.dirname(SO_PATH), "_calls.so")
-    if not os.path.exists(path):
-        raise ImportError(f"_calls.so is not built ({path}); run routing_dispatch_expert_gb300.build")
-    spec = importlib.util.spec_from_file_location("_calls", path)
-    module = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(module)
-    module.bind(MoeConfig, MoeError)
-    _calls = module
+    from .build import calls_path
+
+    path = calls_path()
+    try:
+        spec = importlib.util.spec_from_file_location("_calls", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.bind(MoeConfig, MoeError)
+        _calls = module
+    except ImportError as e:
+        warnings.warn(f"csrc/calls.cpp is not built for this torch and Python, small calls take longer ({e}); run "
+                      "routing_dispatch_expert_gb300.build")
+        _calls = _NoCalls()
 
 
 def _check(rc: int):
