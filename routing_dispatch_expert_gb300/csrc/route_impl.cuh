@@ -135,6 +135,19 @@ constexpr float kGroupGap = 2e-6f;  // between two group scores (sums of two key
 __device__ __forceinline__ float sigmoid_exact(float l) { return __double2float_rn(1.0 / (1.0 + exp(-(double)l))); }
 __device__ __forceinline__ float sigmoid_fast(float l) { return __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-l))); }
 
+// exp(l - m), with the rounding error of the subtraction carried into the exponential (l - m = dh + dl exactly, e = expf(dh)
+// * (1 + dl)).
+__device__ __forceinline__ float exp_difference(float l, float m) {
+  const float b = -m;
+  const float dh = __fadd_rn(l, b);
+  const float e = expf(dh);
+  if (!(e > 0.f) || isinf(e)) return e;  // 0, inf or NaN: nothing to correct
+  // TwoSum (Knuth): dh + dl == l + b exactly
+  const float bb = __fsub_rn(dh, l);
+  const float dl = __fadd_rn(__fsub_rn(l, __fsub_rn(dh, bb)), __fsub_rn(b, bb));
+  return __fmaf_rn(e, dl, e);  // exp(dh + dl) to first order in dl (|dl| <= 2^-24 |dh|)
+}
+
 // Per-lane constants of the expert slots: group index and validity, the same for every token.
 template <int EPL>
 struct Slots {
@@ -371,9 +384,20 @@ __device__ __forceinline__ void topk_token(const TopkDesc& d, const Slots<EPL>& 
   if (sigmoid) {
     // w_j = s_j * (scale / sum s): s in fp32 (relative error below 4e-7); the k scores summed in slot
     // order by every lane (the same sum on every lane, k - 1 roundings)
-    const float sj = lane < d.k ? sigmoid_fast(sel_l) : 0.f;
+    float sj = lane < d.k ? sigmoid_fast(sel_l) : 0.f;
     float sum = 0.f;
     for (int j = 0; j < d.k; ++j) sum = __fadd_rn(sum, __shfl_sync(0xffffffffu, sj, j));
+    if (d.renorm && sum < 1e-26f) {
+      // Every chosen logit is below -59: its score is e^l (to 2^-85) and may be too small for fp32, all of them 0 below
+      // -88, but their ratios are not. With the largest factored out the sum is 1 and more. (All -inf: no ratios, NaN as
+      // ever.)
+      const float m = warp_max(lane < d.k ? sel_l : -INFINITY);
+      if (m > -INFINITY) {
+        sj = lane < d.k ? exp_difference(sel_l, m) : 0.f;
+        sum = 0.f;
+        for (int j = 0; j < d.k; ++j) sum = __fadd_rn(sum, __shfl_sync(0xffffffffu, sj, j));
+      }
+    }
     const float scale = d.renorm ? __fdiv_rn(d.routed_scale, sum) : d.routed_scale;
     if (lane < d.k) {
       d.topk_idx[(int64_t)t * d.k + lane] = sel_e;
@@ -382,8 +406,7 @@ __device__ __forceinline__ void topk_token(const TopkDesc& d, const Slots<EPL>& 
     return;
   }
   // softmax: e_i = exp(l_i - lmax), with the rounding error of the subtraction carried into the
-  // exponential (l - lmax = dh + dl exactly, e = expf(dh) * (1 + dl)), so e has expf's 2 ulp plus a
-  // few roundings. Renormalised, w_j = e_j / sum_sel e (the normaliser over all experts cancels; k - 1
+  // exponential, so e has expf's 2 ulp plus a few roundings. Renormalised, w_j = e_j / sum_sel e (the normaliser over all experts cancels; k - 1
   // roundings in slot order); otherwise w_j = e_j / z with z = sum over all experts, per lane in slot
   // order and then a butterfly (every lane ends with the same z; EPL + 4 roundings); above 256
   // experts z is summed in fp64 to keep its error small.
@@ -392,16 +415,7 @@ __device__ __forceinline__ void topk_token(const TopkDesc& d, const Slots<EPL>& 
   for (int i = 0; i < EPL; ++i)
     if (sl.valid[i]) lmax = fmaxf(lmax, lv[i]);
   lmax = warp_max(lmax);
-  auto expd = [lmax](float l) {
-    const float b = -lmax;
-    const float dh = __fadd_rn(l, b);
-    const float e = expf(dh);
-    if (!(e > 0.f) || isinf(e)) return e;  // 0, inf or NaN: nothing to correct
-    // TwoSum (Knuth): dh + dl == l + b exactly
-    const float bb = __fsub_rn(dh, l);
-    const float dl = __fadd_rn(__fsub_rn(l, __fsub_rn(dh, bb)), __fsub_rn(b, bb));
-    return __fmaf_rn(e, dl, e);  // exp(dh + dl) to first order in dl (|dl| <= 2^-24 |dh|)
-  };
+  auto expd = [lmax](float l) { return exp_difference(l, lmax); };
   const float e_sel = lane < d.k ? expd(sel_l) : 0.f;
   float w;
   if (d.renorm) {
