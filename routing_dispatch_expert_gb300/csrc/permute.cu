@@ -243,9 +243,11 @@ struct CopyPlane {
 };
 
 // Words of a lane in a piece, at most: 16 where there are enough pieces for every SM, else 4 (16384 rows of 7168 bytes to
-// eight places each: 165 us with the whole row in a piece, 169 with 8, 172 with 4). A kernel for every few numbers of
-// words, since each is an instruction for every place (65536 rows of 129 codes of 8 bits, with scales and sort: 59.8 us,
-// with room for 16 words 90).
+// eight places each: 165 us with the whole row in a piece, 169 with 8, 172 with 4). A kernel for each of 1, 2, 4 and 6
+// words, since each word that a kernel has room for is an instruction for every place: 65536 rows of 129 codes of 8 bits,
+// with scales and sort, 59.8 us, with room for 16 words 90; of 159 numbers of 16 bits, 5 words, 44.4 and 47.2 (wide
+// words, 16384 x 1536 bf16, 70.5 and 69.1). From 7 words on the room costs nothing (16384 x 2304, 9 words: a kernel for 9
+// 105.5 us, for 16 103.5; x 3000, 12 words: 136.2 and 136.6; 65536 x 255, 8 words of 16 bits: 70.7 and 68.9).
 constexpr int kDeep = 16;
 
 template <class Word, int DEPTH>
@@ -466,8 +468,6 @@ cudaError_t launch_permute(const PermuteDesc& d, cudaStream_t stream) {
     if (step <= 2) return go(pm::permute_kernel<Word, 2>);
     if (step <= 4) return go(pm::permute_kernel<Word, 4>);
     if (step <= 6) return go(pm::permute_kernel<Word, 6>);
-    if (step <= 9) return go(pm::permute_kernel<Word, 9>);
-    if (step <= 12) return go(pm::permute_kernel<Word, 12>);
     return go(pm::permute_kernel<Word, pm::kDeep>);
   });
 }
