@@ -447,8 +447,8 @@ int moe_balance_loss_backward(const moe_config* cfg, const void* logits, int32_t
  * the gradients
  * ------------------------------------------------------------------------------------------
  * Rows are fp32, bf16 or fp16 (MOE_TYPE_*) and of any width unless said otherwise. Rows that begin on 16 bytes are read
- * and written 16 bytes at a time, others number by number (16-bit ones of an even width two at a time). Sums, statistics and gradients are fp32; every output is
- * rounded once.
+ * and written 16 bytes at a time, others number by number (16-bit ones of an even width two at a time). Sums, statistics
+ * and gradients are fp32; every output is rounded once.
  *
  * moe_rms_norm: total = x + residual, y = total * weight / sqrt(mean(total^2) + eps). The squares are added in fp32:
  * rows of numbers past 1e18 in size overflow it and come out as 0, and a row of zeros with eps 0 as NaN, as in fp32
@@ -475,7 +475,8 @@ int moe_rms_norm(const void* x, int32_t x_type, int64_t rows, int64_t cols, int6
  *   dtotal     [rows, cols] of total_type: the gradient that reaches the total from elsewhere, added; or NULL
  *   dx         [rows, cols] of y_type out, dresidual [rows, cols] of total_type out: the gradient of the total, which
  *              is that of x and of the residual; either may be NULL
- *   dweight    [cols] of weight_type out, or NULL. The rows are added in an order that rows and cols fix.
+ *   dweight    [cols] of weight_type out, or NULL. The rows are added in a fixed order, that of the same call every time:
+ *              rows, cols, the types, whether there is a dtotal and whether the rows are whole 16 bytes decide it
  *   ws         moe_rms_norm_backward_workspace_size() bytes, with dweight (else NULL)
  * dx or dresidual may be dy, total (if contiguous) or dtotal where their types are the same; otherwise outputs overlap
  * nothing. Two launches with dweight, else one. Errors: as moe_rms_norm, MOE_ERR_WORKSPACE. */
@@ -486,7 +487,8 @@ int moe_rms_norm_backward(const void* dy, int32_t y_type, int64_t rows, int64_t 
                           moe_stream_t stream);
 
 /* The assignments of T tokens to k experts each, sorted by expert (stable: token, then slot). cfg gives T, E, k,
- * capacity_factor and placement; its h, I and dtype do not matter here, nor in the three calls behind this one.
+ * capacity_factor and placement; its h, I and dtype (valid ones) do not matter here, nor in the three calls behind this
+ * one.
  *   topk_idx   [T, k] int32. An entry outside [0, E) is no assignment (a padded token, say). An expert that a token
  *              names twice gets two rows.
  *   topk_w     [T, k] fp32, or NULL (with row_weight)
@@ -539,8 +541,8 @@ int moe_unpermute_backward(const moe_config* cfg, const void* dy, const void* yd
  * selection and its bias carry none): dlogits [T, E] of logits_type (MOE_TYPE_F32 or MOE_TYPE_BF16) from logits [T, E],
  * topk_idx [T, k] and dtopk_w [T, k] fp32. Entries of topk_idx outside [0, E) are left out; an expert that a token
  * names twice gets the sum of both. A token without assignments (padding), or whose (chosen) logits are all -inf, has a
- * gradient of 0, whatever its row holds. Every number of dlogits is written; it overlaps no input. One launch. Errors: MOE_ERR_INVALID,
- * MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA. */
+ * gradient of 0, whatever its row holds. Every number of dlogits is written; it overlaps no input. One launch. Errors:
+ * MOE_ERR_INVALID, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA. */
 int moe_route_backward(const moe_config* cfg, const void* logits, int32_t logits_type, const int32_t* topk_idx,
                        const float* dtopk_w, void* dlogits, moe_stream_t stream);
 

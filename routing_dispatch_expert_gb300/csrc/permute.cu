@@ -353,9 +353,11 @@ int64_t per_block(int64_t n, int E) {
 
 int sort_blocks(int64_t n, int E) { return (int)cdiv(n, pm::per_block(n, E)); }
 
-// The blocks themselves become fewer where a lane takes four assignments instead of two (8192 x 8 to 256 experts 64, 8193 x 8
-// 33), or another round.
-int sort_most_blocks(int64_t n) { return n <= 4 * pm::kThreads ? 1 : (int)std::min<int64_t>(pm::kMaxBlocks, cdiv(n, 2 * pm::kThreads)); }
+// The blocks themselves become fewer where a lane takes four assignments instead of two (8192 x 8 to 256 experts 64,
+// 8193 x 8 33), or another round.
+int sort_most_blocks(int64_t n) {
+  return n <= 4 * pm::kThreads ? 1 : (int)std::min<int64_t>(pm::kMaxBlocks, cdiv(n, 2 * pm::kThreads));
+}
 
 cudaError_t launch_sort_tokens(const SortDesc& d, int* launches, cudaStream_t stream) {
   pm::SortArgs a;

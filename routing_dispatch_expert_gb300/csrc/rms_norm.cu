@@ -14,10 +14,11 @@
 //   8192 x 7166 bf16 (with codes)         94 us, 5.0 (100)    65536 x 34 bf16    5.8 us, 3.1
 //   8192 x 7167 bf16 (with codes)        101 us, 4.6 (135)    65536 x 33 bf16    6.5 us, 2.7
 //   one row of 4096                      2.7 us, launch
+//   16384 x 7168 bf16, fp32 residual     202 us, 7.0 TB/s (240 with codes, 6.4)
 // 16-bit rows that are not whole 16 bytes are bound by their accesses of one number or two. Three blocks of 448 threads
-// an SM for 7168 columns, so that one block's loads run beside another's sums; that takes 42 registers, with the weight
-// loaded behind the reduction (two blocks: 192 us). Rows of up to 128 columns share a warp (65536 x 64 bf16 6.6 us, with
-// a warp a row 16.7; 65536 x 33 6.5 and 18.8).
+// an SM for 7168 columns, so that one block's loads run beside another's sums: 40 registers, for which the weight is
+// loaded behind the reduction and the kernels with codes spill up to 36 bytes (two blocks: 192 us). Rows of up to 128
+// columns share a warp (65536 x 64 bf16 6.6 us, with a warp a row 16.7; 65536 x 33 6.5 and 18.8).
 #include <cuda_fp8.h>
 
 #include <algorithm>

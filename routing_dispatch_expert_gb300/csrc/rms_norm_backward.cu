@@ -6,17 +6,19 @@
 //
 // fp32, each output rounded once. rstd is made again from t, which is read anyway, instead of being stored.
 //
-// Bound by HBM: a row is read once and held on the SM between its sums and its outputs. One GB300, out of HBM (a copy's rate
-// is 6.78 TB/s), with the residual stream's gradient:
+// Bound by HBM: a row is read once and held on the SM between its sums and its outputs. One GB300, out of HBM (a copy's
+// rate is 6.78 TB/s), with the residual stream's gradient:
 //   16384 x 7168 bf16  143 us, 6.6 TB/s     8192 x 7168 fp32  138 us, 6.8 TB/s
 //   65536 x 512 bf16    53 us, 5.0          65536 x 64 bf16   11.6 us, 2.9
 //   8192 x 7166 bf16   104 us, 4.5          65536 x 34 bf16   13 us, 1.4
 //   8192 x 7167 bf16   139 us, 3.4          8192 x 7167 fp32  161 us, 5.8
 //   65536 x 33 bf16   14.7 us, 1.2          one row of 4096   5.5 us, two launches
-// 16-bit rows that are not whole 16 bytes are bound by their accesses of one number or two, in shared memory and to
-// HBM, narrow rows by a barrier a row and its sums. One round of blocks, rows copied ahead into shared memory (rows held
-// in registers instead, one block an SM: 167 us; two, spilling: 226). Rows of up to 128 columns share a warp (65536 x 33
-// 14.7 us, with a warp a row 39).
+// 16-bit rows that are not whole 16 bytes are bound by their accesses of one number or two, in shared memory (dy and t
+// twice) and to HBM. Narrow rows share a warp and wait for no other (65536 x 33 14.7 us, with a warp a row 39); they are
+// bound by instructions, two sums over the lanes a row, odd ones by reads of one number, and by the second launch over up
+// to 608 blocks' sums; whole ones of one 16-bit type spill 120 bytes at the 64 registers that four blocks an SM leave.
+// One round of blocks, rows copied ahead into shared memory (rows held in registers instead, one block an SM: 167 us;
+// two, spilling: 226).
 #include <algorithm>
 
 #include "rms_norm.cuh"
@@ -57,9 +59,11 @@ template <int TYPE, int TT, int CPW, int THREADS>
 constexpr int kStages = Ring<TYPE, TT, CPW>::bytes(THREADS, 2) <= kMaxRing ? 2 : 1;
 
 // Rows that are not whole 16 bytes: a row's warps (or its lanes) copy it as the 16-byte words that cover it, and read
-// their numbers out of those behind a barrier. Its first word may begin in the row before, its last one is copied up to the row's
-// end.
-__host__ __device__ __forceinline__ int covering(int cols, int size) { return (cols * size + 15 + 15) / 16; }  // words, at most
+// their numbers out of those behind a barrier (of the warp, where it has rows of its own). Its first word may begin in
+// the row before, its last one is copied up to the row's end.
+__host__ __device__ __forceinline__ int covering(int cols, int size) {  // words, at most
+  return (cols * size + 15 + 15) / 16;
+}
 
 // Persistent: a thread has the same columns in every row, so it keeps the weight and the weight's gradient of them in
 // registers, while later rows are copied into shared memory. One row at a time by all warps of a block, or, with GROUPS
@@ -267,10 +271,6 @@ __global__ void __launch_bounds__(1024) dweight_kernel(const float* part, int n,
   }
 }
 
-}  // namespace rn
-
-namespace rn {
-
 // Chunks of a warp, and warps of a row (2048 columns: 83 us with two chunks, 88 with one; 512 columns: 63 and 53).
 int back_chunks(int cols) { return cols > 4 * rows::kChunk ? 2 : 1; }
 int back_warps(int cols) { return (int)cdiv(cdiv(cols, rows::kChunk), back_chunks(cols)); }
@@ -278,7 +278,7 @@ int back_warps(int cols) { return (int)cdiv(cdiv(cols, rows::kChunk), back_chunk
 }  // namespace rn
 
 // Blocks of the gradient's kernel, at most: as many as run at once (fewer where shared memory holds fewer), each at
-// least one row.
+// least one row. An SM's registers hold 32 warps of 64 a thread, 28 of the 72 that rows of 9 to 14 warps take.
 int rms_norm_backward_blocks(int64_t rows, int cols) {
   const int W = rn::back_warps(cols), G = W == 1 ? rn::kGroups : 1;
   const int per_sm = W * G <= 8 ? 32 / (W * G) : W <= 14 ? 28 / W : W <= 16 ? 2 : 1;
@@ -349,6 +349,8 @@ cudaError_t launch_rms_norm_backward(const RmsNormBackwardDesc& d, int* launches
         return go(rn::Int<1>{}, rn::Int<1>{}, rn::Int<1024>{}, 32 * (int)cdiv(d.cols, rows::kChunk));
       if (rn::back_chunks(d.cols) == 1) return go(rn::Int<1>{}, rn::Int<1>{}, rn::Int<256>{}, 32 * W);
       if (W <= 8) return go(rn::Int<2>{}, rn::Int<1>{}, rn::Int<256>{}, 32 * W);
+      // up to 14 warps, two blocks an SM have 72 registers a thread instead of 64 (16384 x 7168 bf16 143 us, with the
+      // kernel for 16 warps 149; 8192 x 7166 104.5 and 113.8; 8192 x 4608 55 and 57)
       if (W <= 14) return go(rn::Int<2>{}, rn::Int<1>{}, rn::Int<448>{}, 32 * W);
       if (W <= 16) return go(rn::Int<2>{}, rn::Int<1>{}, rn::Int<512>{}, 32 * W);
       return go(rn::Int<2>{}, rn::Int<1>{}, rn::Int<1024>{}, 32 * W);

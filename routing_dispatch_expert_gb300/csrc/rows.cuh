@@ -1,5 +1,6 @@
-// Rows of fp32, bf16 or fp16 numbers as the kernels of the norm (rms_norm.cu, rms_norm_backward.cu) and of the rows' way back (unpermute.cu)
-// read and write them: a warp takes 256 consecutive columns (a chunk) at a time, a lane 8 of them, held as fp32.
+// Rows of fp32, bf16 or fp16 numbers as the kernels of the norm (rms_norm.cu, rms_norm_backward.cu) and of the rows' way
+// back (unpermute.cu) read and write them: a warp takes 256 consecutive columns (a chunk) at a time, a lane 8 of them,
+// held as fp32.
 //
 // Which 8 depends on how the rows lie in memory (MAP):
 //   kMap8  rows that are whole 16 bytes and begin on 16, 16-bit numbers: columns 8 lane .. 8 lane + 7, one 16-byte
@@ -193,7 +194,8 @@ __device__ __forceinline__ void copy8(uint32_t to, const void* from, int n) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(from), "r"(n) : "memory");
 }
 
-// Zeros from byte `from` of base, which is on 16 bytes, up to byte `to`, by this thread of so many. Both are whole elements.
+// Zeros from byte `from` of base, which is on 16 bytes, up to byte `to`, by this thread of so many. Both are whole
+// elements.
 template <int SIZE>
 __device__ __forceinline__ void clear(void* base, int64_t from, int64_t to, int64_t thread, int64_t threads) {
   using Part = typename std::conditional<SIZE == 4, uint32_t, typename std::conditional<SIZE == 2, uint16_t, uint8_t>::type>::type;

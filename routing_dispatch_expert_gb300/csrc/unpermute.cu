@@ -51,10 +51,11 @@ __device__ __forceinline__ void slots(const int32_t* inv_pos, const float* weigh
   }
 }
 
-// Blocks of 256 threads an SM holds: the registers of KB rows in flight. Rows number by number take a register a number
-// (65536 x 511 bf16, the gradient: two slots 80 us with four blocks, 98 with three; four slots 142 with three, 163 with
-// four, which spill; eight slots 272 with two, 652 with three), by pairs one for two (8192 x 7166: 210 us with two blocks,
-// 259 with three, which spill; the narrow rows of 65536 x 66 33.5 and 28.0).
+// Blocks of 256 threads an SM holds: the registers of KB rows in flight, by the times. Rows number by number take a
+// register a number (65536 x 511 bf16, the gradient: two slots 80 us with four blocks, 98 with three; four slots 142 with
+// three, 163 with four; eight slots 272 with two, 652 with three), by pairs one for two (8192 x 7166: 210 us with two
+// blocks, 259 with three; the narrow rows of 65536 x 66 33.5 and 28.0). A few spilled words do not decide it: eight slots
+// of whole 16-bit rows spill 68 bytes at three blocks and run at a copy's rate.
 template <int TYPE, int MAP, int KB, int LANES = 32>
 constexpr int kBlocks = MAP == rows::kMap2   ? (KB < 8 ? 4 : LANES == 32 ? 2 : 3)
                         : MAP == rows::kMap1 ? (KB == 8 ? 2 : KB == 4 ? 3 : 4)
