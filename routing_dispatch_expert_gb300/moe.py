@@ -830,7 +830,10 @@ def _groups(cfg):
 def sort_tokens(cfg, topk_idx, topk_w=None, ws=None) -> dict:
     """The assignments of topk_idx int32 [T, k] sorted by expert (moe_sort_tokens): counts, offsets, inv_pos [T, k], row_token
     [T k], and row_weight [T k] with topk_w fp32 [T, k]. Entries outside [0, E) are no assignment. ws:
-    sort_tokens_workspace."""
+    sort_tokens_workspace. row_weight carries no gradient: weights that require one are refused (they are applied, and get
+    theirs, in unpermute)."""
+    if getattr(topk_w, "requires_grad", False) and torch.is_grad_enabled():
+        raise ValueError("row_weight carries no gradient: pass topk_w.detach(), and topk_w itself to unpermute")
     out = (_calls or _native()).sort_tokens(cfg, topk_idx, topk_w, ws)
     if out is not None:
         counts, offsets, inv_pos, row_token, row_weight = out

@@ -83,3 +83,24 @@ def test_others_are_taken_in_an_open_level():
             assert torch.equal(moe.rms_norm(d), want)
         assert torch.equal(moe.rms_norm(forward_ad.unpack_dual(d).primal), want)
     assert torch.equal(moe.rms_norm(x), want)
+
+
+def test_sorted_weights_that_require_a_gradient_are_refused():
+    """The sort has no gradient in either mode: its row_weight would cut the router's."""
+    cfg = moe.make_config(T=4, h=256, E=8, k=2, I=256)
+    idx, w = torch.zeros(4, 2, dtype=torch.int32), torch.ones(4, 2, requires_grad=True)
+    with pytest.raises(ValueError, match="row_weight carries no gradient"):
+        moe.sort_tokens(cfg, idx, w)
+    for call in (lambda: moe.sort_tokens(cfg, idx, w.detach()), torch.no_grad()(lambda: moe.sort_tokens(cfg, idx, w))):
+        with pytest.raises(ValueError, match="must be a CUDA tensor"):  # what is wrong with them otherwise
+            call()
+
+
+@pytest.mark.gpu
+def test_sorted_weights_without_a_graph_are_taken():
+    cfg = moe.make_config(T=4, h=256, E=8, k=2, I=256)
+    idx, w = torch.zeros(4, 2, dtype=torch.int32, device="cuda"), torch.rand(4, 2, device="cuda", requires_grad=True)
+    want = w.detach().flatten()
+    assert torch.equal(moe.sort_tokens(cfg, idx, w.detach())["row_weight"], want)
+    with torch.no_grad():
+        assert torch.equal(moe.sort_tokens(cfg, idx, w)["row_weight"], want)
